@@ -1,0 +1,307 @@
+// stage_head.cu -- softmax cross entropy of the last stage over a large
+// vocabulary, and its gradients, without keeping the logits.
+//
+// Forward.  l = x w^T is taken tile by tile; of each (token, vocabulary tile)
+// only the largest logit and the sum of exponentials relative to it leave the
+// product, and a second kernel joins the tiles of a token:
+//   m = max_i m_i,  s = sum_i s_i e^(m_i - m),  lse = m + log s.
+// Backward.  d = weight (softmax - onehot) is recomputed for a piece of the
+// vocabulary at a time, as bf16 in the workspace, and both gradients take
+// their product with it before the next piece:  dx += d w_piece,
+// dw_piece = d^T x.
+#include "stage_product.cuh"
+
+namespace pps {
+namespace {
+
+constexpr float kNegInf = -__builtin_huge_valf();
+
+// The reference point of a sum of exponentials: the largest logit, or 0 where
+// that is infinite (so that inf - inf never appears).
+__device__ __forceinline__ float ref_of(float m) { return isinf(m) ? 0.f : m; }
+
+// Joins (m, s) with (m2, s2): sums of exponentials relative to ref_of(m).
+__device__ __forceinline__ void join_stats(float &m, float &s, float m2, float s2) {
+    const float mm = fmaxf(m, m2), r = ref_of(mm);
+    // an empty part (m = -inf, s = 0) adds nothing
+    const float a = s == 0.f ? 0.f : s * exp2f((ref_of(m) - r) * kLog2e);
+    const float b = s2 == 0.f ? 0.f : s2 * exp2f((ref_of(m2) - r) * kLog2e);
+    m = mm;
+    s = a + b;
+}
+
+__device__ __forceinline__ bool inside(int64_t target, int64_t V) { return target >= 0 && target < V; }
+
+struct StatsEpi {
+    const int64_t *target;
+    int64_t T, V;
+    float2 *part;   // [column tiles][T]: largest logit, sum of exponentials
+    float *picked;  // [T]: the target's logit
+    struct Row {
+        float m, s;
+        int64_t target;
+    };
+    __device__ __forceinline__ void begin(Row &r, int64_t t) const {
+        r.m = kNegInf;
+        r.s = 0.f;
+        r.target = target ? target[t] : -1;
+    }
+    __device__ __forceinline__ void chunk(Row &r, int64_t t, int64_t n, int cnt, const float (&v)[32]) const {
+        float m = kNegInf, s = 0.f;
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+            if (j < cnt) m = fmaxf(m, v[j]);
+        const float ref = ref_of(m);
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+            if (j < cnt) s += exp2f((v[j] - ref) * kLog2e);
+        join_stats(r.m, r.s, m, s);
+        if (r.target >= n && r.target < n + cnt) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+                if (r.target == n + j) picked[t] = v[j];
+        }
+    }
+    __device__ __forceinline__ void end(Row &r, int64_t t, int64_t tile) const {
+        part[tile * T + t] = make_float2(r.m, r.s);
+    }
+};
+
+// d of one piece: columns v0 .. of the vocabulary, as bf16.
+struct GradEpi {
+    const int64_t *target;
+    const float *lse, *weight;
+    int64_t T, V, v0;
+    uint16_t *d;  // [T][ld]
+    int64_t ld;
+    struct Row {
+        float lse, c;
+        int64_t at;  // the target's column counted from the piece's first
+        bool in;
+    };
+    __device__ __forceinline__ void begin(Row &r, int64_t t) const {
+        const int64_t g = target[t];
+        r.in = inside(g, V);
+        r.c = weight ? weight[t] : 1.f;
+        r.lse = lse[t];
+        r.at = g - v0;
+    }
+    __device__ __forceinline__ void chunk(Row &r, int64_t t, int64_t n, int cnt, const float (&v)[32]) const {
+        for (int j = 0; j < cnt; ++j) {
+            float p = 0.f;
+            if (r.in) {
+                p = exp2f((v[j] - r.lse) * kLog2e);
+                if (n + j == r.at) p -= 1.f;
+                p *= r.c;
+            }
+            d[t * ld + n + j] = f32_to_bf16(p);
+        }
+    }
+    __device__ __forceinline__ void end(Row &, int64_t, int64_t) const {}
+};
+
+// dx: pieces add up in 32 bits; the last one writes the result.
+struct DxEpi {
+    float *acc;  // [T][H]
+    uint16_t *dx;
+    const int64_t *target;
+    int64_t H, V, ld;
+    float scale;
+    bool first, last;
+    struct Row {
+        bool in;
+    };
+    __device__ __forceinline__ void begin(Row &r, int64_t t) const { r.in = inside(target[t], V); }
+    __device__ __forceinline__ void chunk(Row &r, int64_t t, int64_t n, int cnt, const float (&v)[32]) const {
+        for (int j = 0; j < cnt; ++j) {
+            float s = v[j];
+            if (!first) s += acc[t * H + n + j];
+            if (last) dx[t * ld + n + j] = r.in ? f32_to_bf16(s * scale) : 0;  // 0, whatever w holds
+            else acc[t * H + n + j] = s;
+        }
+    }
+    __device__ __forceinline__ void end(Row &, int64_t, int64_t) const {}
+};
+
+struct DwEpi {
+    uint16_t *dw16;  // one of the two
+    float *dw32;
+    int64_t ld;
+    float scale;
+    bool add;
+    struct Row {};
+    __device__ __forceinline__ void begin(Row &, int64_t) const {}
+    __device__ __forceinline__ void chunk(Row &, int64_t v_, int64_t n, int cnt, const float (&v)[32]) const {
+        for (int j = 0; j < cnt; ++j) {
+            const int64_t at = v_ * ld + n + j;
+            const float s = v[j] * scale;
+            if (dw16) dw16[at] = f32_to_bf16(s);
+            else dw32[at] = add ? dw32[at] + s : s;
+        }
+    }
+    __device__ __forceinline__ void end(Row &, int64_t, int64_t) const {}
+};
+
+// One block of 32 tokens: 32 lanes along the tiles for each token.
+__global__ void __launch_bounds__(1024) k_head_join(const float2 *part, const float *picked, const int64_t *target,
+                                                    int64_t tiles, int64_t T, int64_t V, float *loss, float *lse) {
+    __shared__ float2 sh[32][33];
+    const int lane = threadIdx.x & 31, row = threadIdx.x >> 5;
+    const int64_t t = (int64_t)blockIdx.x * 32 + lane;
+    float m = kNegInf, s = 0.f;
+    if (t < T)
+        for (int64_t i = row; i < tiles; i += 32) {
+            const float2 p = part[i * T + t];
+            join_stats(m, s, p.x, p.y);
+        }
+    sh[row][lane] = make_float2(m, s);
+    __syncthreads();
+    // token blockIdx*32 + row: its 32 parts across the warp, always in the same order
+    const int64_t u = (int64_t)blockIdx.x * 32 + row;
+    m = sh[lane][row].x;
+    s = sh[lane][row].y;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) join_stats(m, s, __shfl_xor_sync(~0u, m, o), __shfl_xor_sync(~0u, s, o));
+    if (lane == 0 && u < T) {
+        const float l = ref_of(m) + logf(s);
+        if (lse) lse[u] = l;
+        if (loss) loss[u] = inside(target[u], V) ? l - picked[u] : 0.f;
+    }
+}
+
+// A copy of x with aligned rows (ld a multiple of 8 elements) in which the
+// rows that are left out are 0 (target NULL: none is), and so are the columns
+// past H.
+__global__ void __launch_bounds__(256) k_copy_rows(const uint16_t *x, int64_t stride, int64_t T, int64_t H,
+                                                   const int64_t *target, int64_t V, uint16_t *out, int64_t ld) {
+    for (int64_t t = blockIdx.x; t < T; t += gridDim.x) {
+        const bool in = !target || inside(target[t], V);
+        for (int64_t h = threadIdx.x; h < ld; h += blockDim.x) out[t * ld + h] = in && h < H ? x[t * stride + h] : 0;
+    }
+}
+
+// Columns of the vocabulary per piece of the backward pass: d of one piece is
+// at most kPieceBytes.
+constexpr int64_t kPieceBytes = 512ll << 20;
+int64_t piece_of(int64_t T, int64_t V) {
+    const int64_t cols = kPieceBytes / (2 * (T > 0 ? T : 1)) / 256 * 256;
+    const int64_t most = 256 * 1024;
+    int64_t p = cols < 256 ? 256 : cols > most ? most : cols;
+    // equal pieces
+    const int64_t n = ceil_div(V, p);
+    return round_up(ceil_div(V, n), 256);
+}
+
+int check_head(const void *x, int64_t sx, const void *w, int64_t sw, const void *target, int64_t T, int64_t V,
+               int64_t H) {
+    if (T < 0 || V < 1 || H < 1) return PP_ERR_ARG;
+    if (T > PP_STAGE_MAX_ROWS || V > PP_STAGE_MAX_VOCAB || H > PP_STAGE_MAX_WIDTH) return PP_ERR_SIZE;
+    if (!w || ((uintptr_t)w & 1) || sw < H) return PP_ERR_ARG;
+    if (T > 0 && (!x || !target || ((uintptr_t)x & 1) || ((uintptr_t)target & 7) || sx < H)) return PP_ERR_ARG;
+    return PP_OK;
+}
+
+struct ForwardSpace {
+    float2 *part;
+    float *picked;
+    size_t bytes;
+};
+ForwardSpace forward_space(void *ws, int64_t T, int64_t V) {
+    Carve c{static_cast<unsigned char *>(ws)};
+    ForwardSpace s;
+    s.part = c.take<float2>(column_tiles(V) * T);
+    s.picked = c.take<float>(T);
+    s.bytes = c.used;
+    return s;
+}
+
+struct BackwardSpace {
+    uint16_t *x, *d;
+    float *acc;
+    int64_t piece, ldx;
+    size_t bytes;
+};
+BackwardSpace backward_space(void *ws, int64_t T, int64_t V, int64_t H) {
+    Carve c{static_cast<unsigned char *>(ws)};
+    BackwardSpace s;
+    s.piece = piece_of(T, V);
+    s.ldx = round_up(H, 8);
+    s.x = c.take<uint16_t>(T * s.ldx);
+    s.d = c.take<uint16_t>(T * s.piece);
+    s.acc = c.take<float>(T * H);
+    s.bytes = c.used;
+    return s;
+}
+
+}  // namespace
+}  // namespace pps
+
+using namespace pps;
+
+extern "C" size_t pp_stage_head_forward_workspace(const uint16_t *x, int64_t stride_x, const uint16_t *w,
+                                                  int64_t stride_w, int64_t T, int64_t V, int64_t H) {
+    if (T < 1 || V < 1 || H < 1) return 0;
+    return forward_space(nullptr, T, V).bytes;
+}
+
+extern "C" int pp_stage_head_forward(const uint16_t *x, int64_t stride_x, const uint16_t *w, int64_t stride_w,
+                                     const int64_t *target, int64_t T, int64_t V, int64_t H, float *loss,
+                                     float *lse, void *workspace, size_t workspace_bytes, cudaStream_t stream) {
+    const int rc = check_head(x, stride_x, w, stride_w, target, T, V, H);
+    if (rc != PP_OK) return rc;
+    if (T == 0) return PP_OK;
+    if ((!loss && !lse) || ((uintptr_t)loss & 3) || ((uintptr_t)lse & 3)) return PP_ERR_ARG;
+    const ForwardSpace s = forward_space(workspace, T, V);
+    if (!workspace || ((uintptr_t)workspace & (kStageAlign - 1)) || workspace_bytes < s.bytes) return PP_ERR_ARG;
+    const Operand A{x, stride_x, true}, B{w, stride_w, true};
+    const int rp = launch_product(A, B, T, V, H, StatsEpi{target, T, V, s.part, s.picked}, stream);
+    if (rp != PP_OK) return rp;
+    k_head_join<<<(unsigned)ceil_div(T, 32), 1024, 0, stream>>>(s.part, s.picked, target, column_tiles(V), T, V, loss,
+                                                                lse);
+    PPS_CUDA_TRY(cudaGetLastError());
+    return PP_OK;
+}
+
+extern "C" size_t pp_stage_head_backward_workspace(const uint16_t *x, int64_t stride_x, const uint16_t *w,
+                                                   int64_t stride_w, int64_t T, int64_t V, int64_t H) {
+    if (T < 1 || V < 1 || H < 1) return 0;
+    return backward_space(nullptr, T, V, H).bytes;
+}
+
+extern "C" int pp_stage_head_backward(const uint16_t *x, int64_t stride_x, const uint16_t *w, int64_t stride_w,
+                                      const int64_t *target, const float *lse, const float *weight, float scale,
+                                      int64_t T, int64_t V, int64_t H, uint16_t *dx, int64_t stride_dx, void *dw,
+                                      int64_t stride_dw, int dw_float, int dw_add, void *workspace,
+                                      size_t workspace_bytes, cudaStream_t stream) {
+    const int rc = check_head(x, stride_x, w, stride_w, target, T, V, H);
+    if (rc != PP_OK) return rc;
+    if (!dw && (T > 0 && !dx)) return PP_ERR_ARG;
+    if (dw && (stride_dw < H || ((uintptr_t)dw & (dw_float ? 3 : 1)) || (dw_add && !dw_float))) return PP_ERR_ARG;
+    if (T > 0 && (!lse || ((uintptr_t)lse & 3) || ((uintptr_t)weight & 3) || (dx && (stride_dx < H || ((uintptr_t)dx & 1))))) return PP_ERR_ARG;
+    if (T == 0) {  // no token: dw is 0, or what it was
+        if (dw && !dw_add) {
+            const size_t e = dw_float ? 4 : 2;
+            PPS_CUDA_TRY(cudaMemset2DAsync(dw, stride_dw * e, 0, H * e, V, stream));
+        }
+        return PP_OK;
+    }
+    const BackwardSpace s = backward_space(workspace, T, V, H);
+    if (!workspace || ((uintptr_t)workspace & (kStageAlign - 1)) || workspace_bytes < s.bytes) return PP_ERR_ARG;
+    k_copy_rows<<<(unsigned)(T < 65535 ? T : 65535), 256, 0, stream>>>(x, stride_x, T, H, target, V, s.x, s.ldx);
+    PPS_CUDA_TRY(cudaGetLastError());
+    for (int64_t v0 = 0; v0 < V; v0 += s.piece) {
+        const int64_t n = V - v0 < s.piece ? V - v0 : s.piece;
+        int rp = launch_product(Operand{s.x, s.ldx, true}, Operand{w + v0 * stride_w, stride_w, true}, T, n, H,
+                                GradEpi{target, lse, weight, T, V, v0, s.d, s.piece}, stream);
+        if (rp == PP_OK && dx)
+            rp = launch_product(Operand{s.d, s.piece, true}, Operand{w + v0 * stride_w, stride_w, false}, T, H, n,
+                                DxEpi{s.acc, dx, target, H, V, stride_dx, scale, v0 == 0, v0 + n == V}, stream);
+        if (rp == PP_OK && dw)
+            rp = launch_product(Operand{s.d, s.piece, false}, Operand{s.x, s.ldx, false}, n, H, T,
+                                DwEpi{dw_float ? nullptr : (uint16_t *)dw + v0 * stride_dw,
+                                      dw_float ? (float *)dw + v0 * stride_dw : nullptr, stride_dw, scale, dw_add != 0},
+                                stream);
+        if (rp != PP_OK) return rp;
+    }
+    return PP_OK;
+}

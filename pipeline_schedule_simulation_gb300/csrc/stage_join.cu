@@ -1,0 +1,426 @@
+// stage_join.cu -- the norm after a block, its gate, the residual scale and
+// sum, and the norm before the next block, forward and backward.
+//
+// A block of threads holds a whole row in registers, so each input is read
+// once and each output written once: forward moves 8 bytes an element (10 with
+// both checkpoints), backward 10 from checkpoints and 12 from bf16.  Both
+// directions need two sums over the row, one after the other.
+#include "stage_kept.cuh"
+
+namespace pps {
+namespace {
+
+// Sum over the block; every thread gets it.  `sh` holds one value per warp and
+// must not be in use by an earlier call that some thread may still be reading:
+// callers alternate between two.
+template <int NT>
+__device__ __forceinline__ float block_sum(float v, float *sh) {
+#pragma unroll
+    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(~0u, v, o);
+    if (NT == 32) return v;
+    if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = v;
+    __syncthreads();
+    float s = 0.f;
+#pragma unroll
+    for (int i = 0; i < NT / 32; ++i) s += sh[i];
+    return s;
+}
+
+struct Kept {
+    int8_t *q, *e;
+    int64_t sq, se;
+};
+
+struct JoinForward {
+    const uint16_t *x, *f, *w_post, *w_pre, *gate;
+    int64_t sx, sf, sg, rows_per_gate;
+    float alpha, eps;
+    int64_t T;
+    int H;
+    uint16_t *y, *h;
+    int64_t sy, sh;
+    float *rstd_post, *rstd_pre;
+    Kept ky, kf;
+};
+
+// NT threads hold NV vectors of 8 columns each: H <= 8 * NT * NV.
+template <int NT, int NV, bool VEC, bool KEEP>
+__global__ void __launch_bounds__(NT) k_join_forward(const JoinForward a) {
+    __shared__ float sh[2][32];
+    const float inv_h = 1.f / (float)a.H;
+    for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
+        const uint16_t *g = a.gate ? a.gate + (a.rows_per_gate > 0 ? t / a.rows_per_gate : 0) * a.sg : nullptr;
+        float f[NV][8], y[NV][8], ss = 0.f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (i * NT + (int)threadIdx.x) * 8;
+            const int left = a.H - c;
+            load8_bf16<VEC>(a.f + t * a.sf + (left > 0 ? c : 0), left, f[i]);
+            load8_bf16<VEC>(a.x + t * a.sx + (left > 0 ? c : 0), left, y[i]);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) ss += f[i][j] * f[i][j];
+        }
+        const float r1 = rsqrtf(block_sum<NT>(ss, sh[0]) * inv_h + a.eps);
+        if (KEEP) {
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const int c = (i * NT + (int)threadIdx.x) * 8, left = a.H - c;
+                int e;
+                const uint2 b = pack8(f[i], e);
+                if (left > 0) {
+                    store8_bytes<VEC>(a.kf.q + t * a.kf.sq + c, left, b);
+                    if ((threadIdx.x & 7) == 0) a.kf.e[t * a.kf.se + c / kBlock] = (int8_t)e;
+                }
+            }
+        }
+        ss = 0.f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (i * NT + (int)threadIdx.x) * 8, left = a.H - c;
+            float w[8];
+            load8_bf16<VEC>(a.w_post + (left > 0 ? c : 0), left, w);
+            if (g) {
+                float gv[8];
+                load8_bf16<VEC>(g + (left > 0 ? c : 0), left, gv);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) w[j] *= gv[j];
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                y[i][j] = a.alpha * y[i][j] + w[j] * (f[i][j] * r1);
+                ss += y[i][j] * y[i][j];
+            }
+            if (left > 0) store8_bf16<VEC>(a.y + t * a.sy + c, left, y[i]);
+        }
+        const float r2 = rsqrtf(block_sum<NT>(ss, sh[1]) * inv_h + a.eps);
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (i * NT + (int)threadIdx.x) * 8, left = a.H - c;
+            float w[8];
+            load8_bf16<VEC>(a.w_pre + (left > 0 ? c : 0), left, w);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) w[j] *= y[i][j] * r2;
+            if (left > 0) store8_bf16<VEC>(a.h + t * a.sh + c, left, w);
+            if (KEEP) {
+                float yr[8];  // y as the next reader sees it
+#pragma unroll
+                for (int j = 0; j < 8; ++j) yr[j] = bf16_to_f32(f32_to_bf16(y[i][j]));
+                int e;
+                const uint2 b = pack8(yr, e);
+                if (left > 0) {
+                    store8_bytes<VEC>(a.ky.q + t * a.ky.sq + c, left, b);
+                    if ((threadIdx.x & 7) == 0) a.ky.e[t * a.ky.se + c / kBlock] = (int8_t)e;
+                }
+            }
+        }
+        if (threadIdx.x == 0) {
+            a.rstd_post[t] = r1;
+            a.rstd_pre[t] = r2;
+        }
+    }
+}
+
+// Rows are shared out in items: a run of rows of one gate group, so that an
+// item's column sums belong to one gate row.
+struct Items {
+    int64_t rows_per_gate, groups, rows, per_group, count;
+};
+Items items_of(int64_t T, int64_t rows_per_gate) {
+    Items it;
+    it.rows_per_gate = rows_per_gate > 0 && rows_per_gate < T ? rows_per_gate : T;
+    it.groups = ceil_div(T, it.rows_per_gate);
+    const int64_t want = 152 * 2;
+    it.rows = ceil_div(T, want);
+    if (it.rows > it.rows_per_gate) it.rows = it.rows_per_gate;
+    it.per_group = ceil_div(it.rows_per_gate, it.rows);
+    it.count = it.groups * it.per_group;
+    return it;
+}
+
+struct JoinBackward {
+    const uint16_t *dh, *dy, *y, *f, *w_post, *w_pre, *gate;
+    int64_t sdh, sdy, sy, sf, sg;
+    Kept ky, kf;
+    const float *rstd_post, *rstd_pre;
+    float alpha;
+    int64_t T;
+    int H;
+    uint16_t *dx, *df;
+    int64_t sdx, sdf;
+    float *part_pre, *part_post;  // [items][H]: sum dh n2, sum d n1
+    Items it;
+};
+
+template <bool VEC, bool PACKED>
+__device__ __forceinline__ void load_saved(const uint16_t *p, int64_t s, const Kept &k, int64_t t, int c, int left,
+                                           float (&v)[8]) {
+    if (PACKED) {
+        if (left > 0) unpack8(load8_bytes<VEC>(k.q + t * k.sq + c, left), k.e[t * k.se + c / kBlock], v);
+        // past the row's end a block's bytes are 0, and so is a value unless the block is not finite
+        if (left < 8) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (j >= left) v[j] = 0.f;
+        }
+    } else {
+        load8_bf16<VEC>(p + t * s + (left > 0 ? c : 0), left, v);
+    }
+}
+
+template <int NT, int NV, bool VEC, bool PACKED>
+__global__ void __launch_bounds__(NT) k_join_backward(const JoinBackward a) {
+    __shared__ float sh[2][32];
+    const float inv_h = 1.f / (float)a.H;
+    const int64_t group = blockIdx.x / a.it.per_group, part = blockIdx.x % a.it.per_group;
+    const int64_t first = group * a.it.rows_per_gate + part * a.it.rows;
+    int64_t last = min(first + a.it.rows, (group + 1) * a.it.rows_per_gate);
+    last = min(last, a.T);
+    const uint16_t *g = a.gate ? a.gate + group * a.sg : nullptr;
+    float sum_pre[NV][8] = {}, sum_post[NV][8] = {};
+    for (int64_t t = first; t < last; ++t) {
+        const float r1 = a.rstd_post[t], r2 = a.rstd_pre[t];
+        float n2[NV][8], d[NV][8], ss = 0.f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (i * NT + (int)threadIdx.x) * 8, left = a.H - c;
+            float w[8];
+            load8_bf16<VEC>(a.dh + t * a.sdh + (left > 0 ? c : 0), left, d[i]);
+            load_saved<VEC, PACKED>(a.y, a.sy, a.ky, t, c, left, n2[i]);
+            load8_bf16<VEC>(a.w_pre + (left > 0 ? c : 0), left, w);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                n2[i][j] *= r2;
+                sum_pre[i][j] += d[i][j] * n2[i][j];
+                d[i][j] *= w[j];
+                ss += d[i][j] * n2[i][j];
+            }
+        }
+        const float m2 = block_sum<NT>(ss, sh[0]) * inv_h;
+        float n1[NV][8];
+        ss = 0.f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (i * NT + (int)threadIdx.x) * 8, left = a.H - c;
+            float u[8], w[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) d[i][j] = r2 * (d[i][j] - n2[i][j] * m2);
+            if (a.dy) {
+                load8_bf16<VEC>(a.dy + t * a.sdy + (left > 0 ? c : 0), left, u);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) d[i][j] += u[j];
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) u[j] = a.alpha * d[i][j];
+            if (left > 0) store8_bf16<VEC>(a.dx + t * a.sdx + c, left, u);
+            load_saved<VEC, PACKED>(a.f, a.sf, a.kf, t, c, left, n1[i]);
+            load8_bf16<VEC>(a.w_post + (left > 0 ? c : 0), left, w);
+            if (g) {
+                load8_bf16<VEC>(g + (left > 0 ? c : 0), left, u);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) w[j] *= u[j];
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                n1[i][j] *= r1;
+                sum_post[i][j] += d[i][j] * n1[i][j];
+                d[i][j] *= w[j];
+                ss += d[i][j] * n1[i][j];
+            }
+        }
+        const float m1 = block_sum<NT>(ss, sh[1]) * inv_h;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (i * NT + (int)threadIdx.x) * 8, left = a.H - c;
+            float u[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) u[j] = r1 * (d[i][j] - n1[i][j] * m1);
+            if (left > 0) store8_bf16<VEC>(a.df + t * a.sdf + c, left, u);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int c = (i * NT + (int)threadIdx.x) * 8;
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (c + j < a.H) {
+                a.part_pre[blockIdx.x * (int64_t)a.H + c + j] = sum_pre[i][j];
+                a.part_post[blockIdx.x * (int64_t)a.H + c + j] = sum_post[i][j];
+            }
+    }
+}
+
+// Column sums of the items' parts, in a fixed order: blockIdx.y = 0 joins all
+// items (the part of the norm after the block weighted by its group's gate), the
+// others a gate group each.
+__global__ void __launch_bounds__(1024) k_join_columns(const float *part_pre, const float *part_post, Items it, int H,
+                                                       const uint16_t *w_post, const uint16_t *gate, int64_t sg,
+                                                       float *dw_post, float *dw_pre, float *dgate, int64_t sdg) {
+    __shared__ float s0[32][33], s1[32][33];
+    const int lane = threadIdx.x & 31, row = threadIdx.x >> 5;
+    const int h = blockIdx.x * 32 + lane;
+    const bool all = blockIdx.y == 0;
+    for (int64_t g = all ? 0 : blockIdx.y - 1; g < (all ? 1 : it.groups); g += all ? 1 : gridDim.y - 1) {
+        const int64_t from = all ? 0 : g * it.per_group, to = all ? it.count : (g + 1) * it.per_group;
+        float a = 0.f, b = 0.f;
+        if (h < H)
+            for (int64_t i = from + row; i < to; i += 32) {
+                float p = part_post[i * H + h];
+                if (all) {
+                    a += part_pre[i * H + h];
+                    if (gate) p *= bf16_to_f32(gate[i / it.per_group * sg + h]);
+                }
+                b += p;
+            }
+        s0[row][lane] = a;
+        s1[row][lane] = b;
+        __syncthreads();
+        a = s0[lane][row];
+        b = s1[lane][row];
+#pragma unroll
+        for (int o = 16; o; o >>= 1) {
+            a += __shfl_xor_sync(~0u, a, o);
+            b += __shfl_xor_sync(~0u, b, o);
+        }
+        const int hh = blockIdx.x * 32 + row;
+        if (lane == 0 && hh < H) {
+            if (all) {
+                dw_pre[hh] = a;
+                dw_post[hh] = b;
+            } else {
+                dgate[g * sdg + hh] = b * bf16_to_f32(w_post[hh]);
+            }
+        }
+        __syncthreads();
+    }
+}
+
+template <bool VEC, bool KEEP>
+void forward_by_width(const JoinForward &a, unsigned grid, cudaStream_t s) {
+    if (a.H <= 1024) k_join_forward<128, 1, VEC, KEEP><<<grid, 128, 0, s>>>(a);
+    else if (a.H <= 2048) k_join_forward<256, 1, VEC, KEEP><<<grid, 256, 0, s>>>(a);
+    else if (a.H <= 4096) k_join_forward<512, 1, VEC, KEEP><<<grid, 512, 0, s>>>(a);
+    else if (a.H <= 8192) k_join_forward<512, 2, VEC, KEEP><<<grid, 512, 0, s>>>(a);
+    else k_join_forward<1024, 2, VEC, KEEP><<<grid, 1024, 0, s>>>(a);
+}
+
+template <bool VEC, bool PACKED>
+void backward_by_width(const JoinBackward &a, cudaStream_t s) {
+    const unsigned grid = (unsigned)a.it.count;
+    if (a.H <= 1024) k_join_backward<128, 1, VEC, PACKED><<<grid, 128, 0, s>>>(a);
+    else if (a.H <= 2048) k_join_backward<256, 1, VEC, PACKED><<<grid, 256, 0, s>>>(a);
+    else if (a.H <= 4096) k_join_backward<512, 1, VEC, PACKED><<<grid, 512, 0, s>>>(a);
+    else if (a.H <= 8192) k_join_backward<512, 2, VEC, PACKED><<<grid, 512, 0, s>>>(a);
+    else k_join_backward<1024, 2, VEC, PACKED><<<grid, 1024, 0, s>>>(a);
+}
+
+int check_join(int64_t T, int64_t H) {
+    if (T < 0 || H < 1) return PP_ERR_ARG;
+    if (T > PP_STAGE_MAX_ROWS || H > PP_STAGE_MAX_JOIN_WIDTH) return PP_ERR_SIZE;
+    return PP_OK;
+}
+bool bad_rows(const void *p, int64_t stride, int64_t H) { return !p || ((uintptr_t)p & 1) || stride < H; }
+bool bad_kept(const Kept &k, int64_t H) { return !k.q || !k.e || k.sq < H || k.se < ceil_div(H, kBlock); }
+
+struct BackSpace {
+    float *pre, *post;
+    size_t bytes;
+};
+BackSpace back_space(void *ws, const Items &it, int64_t H) {
+    Carve c{static_cast<unsigned char *>(ws)};
+    BackSpace s;
+    s.pre = c.take<float>(it.count * H);
+    s.post = c.take<float>(it.count * H);
+    s.bytes = c.used;
+    return s;
+}
+
+}  // namespace
+}  // namespace pps
+
+using namespace pps;
+
+extern "C" int pp_stage_join_forward(const uint16_t *x, int64_t stride_x, const uint16_t *f, int64_t stride_f,
+                                     const uint16_t *w_post, const uint16_t *w_pre, const uint16_t *gate,
+                                     int64_t stride_gate, int64_t rows_per_gate, float alpha, float eps, int64_t T,
+                                     int64_t H, uint16_t *y, int64_t stride_y, uint16_t *h, int64_t stride_h,
+                                     float *rstd_post, float *rstd_pre, int8_t *y_q, int64_t stride_yq, int8_t *y_e,
+                                     int64_t stride_ye, int8_t *f_q, int64_t stride_fq, int8_t *f_e, int64_t stride_fe,
+                                     cudaStream_t stream) {
+    const int rc = check_join(T, H);
+    if (rc != PP_OK) return rc;
+    if (T == 0) return PP_OK;
+    const bool keep = y_q || y_e || f_q || f_e;
+    JoinForward a{x, f, w_post, w_pre, gate, stride_x, stride_f, stride_gate, rows_per_gate, alpha, eps, T, (int)H,
+                  y, h, stride_y, stride_h, rstd_post, rstd_pre,
+                  Kept{y_q, y_e, stride_yq, stride_ye}, Kept{f_q, f_e, stride_fq, stride_fe}};
+    if (bad_rows(x, stride_x, H) || bad_rows(f, stride_f, H) || bad_rows(w_post, H, H) || bad_rows(w_pre, H, H) ||
+        bad_rows(y, stride_y, H) || bad_rows(h, stride_h, H) || (gate && bad_rows(gate, stride_gate, H)) ||
+        !rstd_post || !rstd_pre || ((uintptr_t)rstd_post & 3) || ((uintptr_t)rstd_pre & 3) || !(eps >= 0.f) ||
+        (keep && (bad_kept(a.ky, H) || bad_kept(a.kf, H))))
+        return PP_ERR_ARG;
+    const bool vec = rows_aligned(x, stride_x, T, 2) && rows_aligned(f, stride_f, T, 2) &&
+                     rows_aligned(w_post, H, 1, 2) && rows_aligned(w_pre, H, 1, 2) && rows_aligned(y, stride_y, T, 2) &&
+                     rows_aligned(h, stride_h, T, 2) && (!gate || rows_aligned(gate, stride_gate, 2, 2)) &&
+                     (!keep || (kept_aligned(y_q, stride_yq, T) && kept_aligned(f_q, stride_fq, T)));
+    const unsigned grid = (unsigned)(T < 152 * 16 ? T : 152 * 16);
+    if (vec) keep ? forward_by_width<true, true>(a, grid, stream) : forward_by_width<true, false>(a, grid, stream);
+    else keep ? forward_by_width<false, true>(a, grid, stream) : forward_by_width<false, false>(a, grid, stream);
+    PPS_CUDA_TRY(cudaGetLastError());
+    return PP_OK;
+}
+
+extern "C" size_t pp_stage_join_backward_workspace(int64_t T, int64_t H, int64_t rows_per_gate) {
+    if (T < 1 || H < 1) return 0;
+    return back_space(nullptr, items_of(T, rows_per_gate), H).bytes;
+}
+
+extern "C" int pp_stage_join_backward(const uint16_t *dh, int64_t stride_dh, const uint16_t *dy, int64_t stride_dy,
+                                      const uint16_t *y, int64_t stride_y, const uint16_t *f, int64_t stride_f,
+                                      const int8_t *y_q, int64_t stride_yq, const int8_t *y_e, int64_t stride_ye,
+                                      const int8_t *f_q, int64_t stride_fq, const int8_t *f_e, int64_t stride_fe,
+                                      const float *rstd_post, const float *rstd_pre, const uint16_t *w_post,
+                                      const uint16_t *w_pre, const uint16_t *gate, int64_t stride_gate,
+                                      int64_t rows_per_gate, float alpha, int64_t T, int64_t H, uint16_t *dx,
+                                      int64_t stride_dx, uint16_t *df, int64_t stride_df, float *dw_post, float *dw_pre,
+                                      float *dgate, int64_t stride_dgate, void *workspace, size_t workspace_bytes,
+                                      cudaStream_t stream) {
+    const int rc = check_join(T, H);
+    if (rc != PP_OK) return rc;
+    if (!dw_post || !dw_pre || ((uintptr_t)dw_post & 3) || ((uintptr_t)dw_pre & 3) || (!gate != !dgate) ||
+        (dgate && (((uintptr_t)dgate & 3) || stride_dgate < H)))
+        return PP_ERR_ARG;
+    if (T == 0) {  // no gate group has a row
+        PPS_CUDA_TRY(cudaMemsetAsync(dw_post, 0, H * 4, stream));
+        PPS_CUDA_TRY(cudaMemsetAsync(dw_pre, 0, H * 4, stream));
+        return PP_OK;
+    }
+    const bool packed = y_q || y_e || f_q || f_e;
+    const Items it = items_of(T, rows_per_gate);
+    const BackSpace s = back_space(workspace, it, H);
+    JoinBackward a{dh, dy, y, f, w_post, w_pre, gate, stride_dh, stride_dy, stride_y, stride_f, stride_gate,
+                   Kept{const_cast<int8_t *>(y_q), const_cast<int8_t *>(y_e), stride_yq, stride_ye},
+                   Kept{const_cast<int8_t *>(f_q), const_cast<int8_t *>(f_e), stride_fq, stride_fe},
+                   rstd_post, rstd_pre, alpha, T, (int)H, dx, df, stride_dx, stride_df, s.pre, s.post, it};
+    if (bad_rows(dh, stride_dh, H) || (dy && bad_rows(dy, stride_dy, H)) || bad_rows(w_post, H, H) ||
+        bad_rows(w_pre, H, H) || (gate && bad_rows(gate, stride_gate, H)) || bad_rows(dx, stride_dx, H) ||
+        bad_rows(df, stride_df, H) || !rstd_post || !rstd_pre || ((uintptr_t)rstd_post & 3) ||
+        ((uintptr_t)rstd_pre & 3))
+        return PP_ERR_ARG;
+    if (packed ? (y || f || bad_kept(a.ky, H) || bad_kept(a.kf, H)) : (bad_rows(y, stride_y, H) || bad_rows(f, stride_f, H)))
+        return PP_ERR_ARG;
+    if (!workspace || ((uintptr_t)workspace & (kStageAlign - 1)) || workspace_bytes < s.bytes) return PP_ERR_ARG;
+    const bool vec = rows_aligned(dh, stride_dh, T, 2) && (!dy || rows_aligned(dy, stride_dy, T, 2)) &&
+                     rows_aligned(w_post, H, 1, 2) && rows_aligned(w_pre, H, 1, 2) &&
+                     (!gate || rows_aligned(gate, stride_gate, 2, 2)) && rows_aligned(dx, stride_dx, T, 2) &&
+                     rows_aligned(df, stride_df, T, 2) &&
+                     (packed ? kept_aligned(y_q, stride_yq, T) && kept_aligned(f_q, stride_fq, T)
+                             : rows_aligned(y, stride_y, T, 2) && rows_aligned(f, stride_f, T, 2));
+    if (vec) packed ? backward_by_width<true, true>(a, stream) : backward_by_width<true, false>(a, stream);
+    else packed ? backward_by_width<false, true>(a, stream) : backward_by_width<false, false>(a, stream);
+    PPS_CUDA_TRY(cudaGetLastError());
+    const dim3 grid((unsigned)ceil_div(H, 32), 1 + (gate ? (unsigned)(it.groups < 1024 ? it.groups : 1024) : 0));
+    k_join_columns<<<grid, 1024, 0, stream>>>(s.pre, s.post, it, (int)H, w_post, gate, stride_gate, dw_post, dw_pre,
+                                              dgate, stride_dgate);
+    PPS_CUDA_TRY(cudaGetLastError());
+    return PP_OK;
+}

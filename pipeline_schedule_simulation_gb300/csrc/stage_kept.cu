@@ -1,0 +1,153 @@
+// stage_kept.cu -- activation checkpoints in 8 bits and the weight gradient
+// taken from them.
+#include "stage_kept.cuh"
+#include "stage_product.cuh"
+
+namespace pps {
+namespace {
+
+// 8 lanes per block of 64 columns, 8 columns each.
+template <bool VEC>
+__global__ void __launch_bounds__(256) k_pack(const uint16_t *x, int64_t stride_x, int64_t T, int64_t H, int8_t *q,
+                                              int64_t stride_q, int8_t *e, int64_t stride_e) {
+    const int64_t nb = (H + kBlock - 1) / kBlock, units = T * nb * 8;
+    const int64_t step = (int64_t)gridDim.x * blockDim.x;
+    // whole warps go on together: pack8 shuffles
+    for (int64_t u = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; u - (threadIdx.x & 31) < units; u += step) {
+        const int64_t t = u / (nb * 8), c = u % (nb * 8) * 8;
+        const int64_t left = u < units ? H - c : 0;
+        float v[8];
+        load8_bf16<VEC>(x + (left > 0 ? t * stride_x + c : 0), left, v);
+        int ex;
+        const uint2 b = pack8(v, ex);
+        if (left > 0) store8_bytes<VEC>(q + t * stride_q + c, left, b);
+        if (u < units && (u & 7) == 0) e[t * stride_e + c / kBlock] = (int8_t)ex;
+    }
+}
+
+template <bool VEC>
+__global__ void __launch_bounds__(256) k_unpack(const int8_t *q, int64_t stride_q, const int8_t *e, int64_t stride_e,
+                                                int64_t T, int64_t H, uint16_t *x, int64_t stride_x) {
+    const int64_t per = (H + 7) / 8, units = T * per;
+    const int64_t step = (int64_t)gridDim.x * blockDim.x;
+    for (int64_t u = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; u < units; u += step) {
+        const int64_t t = u / per, c = u % per * 8;
+        float v[8];
+        unpack8(load8_bytes<VEC>(q + t * stride_q + c, H - c), e[t * stride_e + c / kBlock], v);
+        store8_bf16<VEC>(x + t * stride_x + c, H - c, v);
+    }
+}
+
+unsigned grid_for(int64_t threads) {
+    const int64_t b = ceil_div(threads, 256);
+    return (unsigned)(b < 1 ? 1 : b > 152 * 64 ? 152 * 64 : b);
+}
+
+struct WgradEpi {
+    const float *add;
+    float *dw;
+    int64_t ld_add, ld;
+    struct Row {};
+    __device__ __forceinline__ void begin(Row &, int64_t) const {}
+    __device__ __forceinline__ void chunk(Row &, int64_t m, int64_t n, int cnt, const float (&v)[32]) const {
+        for (int j = 0; j < cnt; ++j) dw[m * ld + n + j] = add ? add[m * ld_add + n + j] + v[j] : v[j];
+    }
+    __device__ __forceinline__ void end(Row &, int64_t, int64_t) const {}
+};
+
+bool bad_kept(const int8_t *q, int64_t sq, const int8_t *e, int64_t se, int64_t H) {
+    return !q || !e || sq < H || se < ceil_div(H, kBlock);
+}
+
+struct WgradSpace {
+    uint16_t *v;  // what the checkpoint stands for, rows of ld
+    int64_t ld;
+    size_t bytes;
+};
+WgradSpace wgrad_space(void *ws, int64_t T, int64_t H) {
+    Carve c{static_cast<unsigned char *>(ws)};
+    WgradSpace s;
+    s.ld = round_up(H, 8);
+    s.v = c.take<uint16_t>(T * s.ld);
+    s.bytes = c.used;
+    return s;
+}
+
+}  // namespace
+
+int launch_unpack(const int8_t *q, int64_t stride_q, const int8_t *e, int64_t stride_e, int64_t T, int64_t H,
+                  uint16_t *x, int64_t stride_x, cudaStream_t stream) {
+    const unsigned grid = grid_for(T * ceil_div(H, 8));
+    if (rows_aligned(x, stride_x, T, 2) && kept_aligned(q, stride_q, T))
+        k_unpack<true><<<grid, 256, 0, stream>>>(q, stride_q, e, stride_e, T, H, x, stride_x);
+    else
+        k_unpack<false><<<grid, 256, 0, stream>>>(q, stride_q, e, stride_e, T, H, x, stride_x);
+    PPS_CUDA_TRY(cudaGetLastError());
+    return PP_OK;
+}
+
+}  // namespace pps
+
+using namespace pps;
+
+static int check_kept(int64_t T, int64_t H) {
+    if (T < 0 || H < 1) return PP_ERR_ARG;
+    if (T > PP_STAGE_MAX_ROWS || H > PP_STAGE_MAX_WIDTH) return PP_ERR_SIZE;
+    return PP_OK;
+}
+
+extern "C" int pp_stage_pack(const uint16_t *x, int64_t stride_x, int64_t T, int64_t H, int8_t *q, int64_t stride_q,
+                             int8_t *e, int64_t stride_e, cudaStream_t stream) {
+    const int rc = check_kept(T, H);
+    if (rc != PP_OK) return rc;
+    if (T == 0) return PP_OK;
+    if (!x || ((uintptr_t)x & 1) || stride_x < H || bad_kept(q, stride_q, e, stride_e, H)) return PP_ERR_ARG;
+    const unsigned grid = grid_for(T * ceil_div(H, kBlock) * 8);
+    if (rows_aligned(x, stride_x, T, 2) && kept_aligned(q, stride_q, T))
+        k_pack<true><<<grid, 256, 0, stream>>>(x, stride_x, T, H, q, stride_q, e, stride_e);
+    else
+        k_pack<false><<<grid, 256, 0, stream>>>(x, stride_x, T, H, q, stride_q, e, stride_e);
+    PPS_CUDA_TRY(cudaGetLastError());
+    return PP_OK;
+}
+
+extern "C" int pp_stage_unpack(const int8_t *q, int64_t stride_q, const int8_t *e, int64_t stride_e, int64_t T,
+                               int64_t H, uint16_t *x, int64_t stride_x, cudaStream_t stream) {
+    const int rc = check_kept(T, H);
+    if (rc != PP_OK) return rc;
+    if (T == 0) return PP_OK;
+    if (!x || ((uintptr_t)x & 1) || stride_x < H || bad_kept(q, stride_q, e, stride_e, H)) return PP_ERR_ARG;
+    return launch_unpack(q, stride_q, e, stride_e, T, H, x, stride_x, stream);
+}
+
+extern "C" size_t pp_stage_weight_grad_workspace(const uint16_t *dy, int64_t stride_dy, int64_t T, int64_t N,
+                                                 int64_t H) {
+    if (T < 1 || N < 1 || H < 1) return 0;
+    return wgrad_space(nullptr, T, H).bytes;
+}
+
+extern "C" int pp_stage_weight_grad(const uint16_t *dy, int64_t stride_dy, const int8_t *q, int64_t stride_q,
+                                    const int8_t *e, int64_t stride_e, int64_t T, int64_t N, int64_t H,
+                                    const float *add, int64_t stride_add, float *dw, int64_t stride_dw,
+                                    void *workspace, size_t workspace_bytes, cudaStream_t stream) {
+    const int rc = check_kept(T, H);
+    if (rc != PP_OK) return rc;
+    if (N < 1) return PP_ERR_ARG;
+    if (N > PP_STAGE_MAX_VOCAB) return PP_ERR_SIZE;
+    if (!dw || ((uintptr_t)dw & 3) || stride_dw < H) return PP_ERR_ARG;
+    if (add && (((uintptr_t)add & 3) || stride_add < H || (add == dw && stride_add != stride_dw))) return PP_ERR_ARG;
+    if (T == 0) {
+        if (!add) PPS_CUDA_TRY(cudaMemset2DAsync(dw, stride_dw * 4, 0, H * 4, N, stream));
+        else if (add != dw)
+            PPS_CUDA_TRY(cudaMemcpy2DAsync(dw, stride_dw * 4, add, stride_add * 4, H * 4, N, cudaMemcpyDeviceToDevice,
+                                           stream));
+        return PP_OK;
+    }
+    if (!dy || ((uintptr_t)dy & 1) || stride_dy < N || bad_kept(q, stride_q, e, stride_e, H)) return PP_ERR_ARG;
+    const WgradSpace s = wgrad_space(workspace, T, H);
+    if (!workspace || ((uintptr_t)workspace & (kStageAlign - 1)) || workspace_bytes < s.bytes) return PP_ERR_ARG;
+    const int ru = launch_unpack(q, stride_q, e, stride_e, T, H, s.v, s.ld, stream);
+    if (ru != PP_OK) return ru;
+    return launch_product(Operand{dy, stride_dy, false}, Operand{s.v, s.ld, false}, N, H, T,
+                          WgradEpi{add, dw, stride_add, stride_dw}, stream);
+}
