@@ -143,6 +143,16 @@ int pp_stage_join_backward(const uint16_t *dh, int64_t stride_dh, const uint16_t
                            float *dw_post, float *dw_pre, float *dgate, int64_t stride_dgate,
                            void *workspace, size_t workspace_bytes, cudaStream_t stream);
 
+/* ---- waits --------------------------------------------------------------
+ * The products' blocks wait for their own copies and matrix instructions with
+ * a limit of two seconds.  A wait that runs out is recorded, its block gives up
+ * (its outputs are then wrong) and the kernel ends.  *first_failure (HOST)
+ * receives the first record since the previous call, 0 if there is none, and
+ * the records are cleared: bit 63 set, the waiting role in bits 32..39 (1
+ * loads, 2 and 3 matrix instructions, 4 results), the block below.
+ * Synchronizes the device.  Errors: PP_ERR_ARG, PP_ERR_CUDA. */
+int pp_stage_wait_failure(uint64_t *first_failure);
+
 #ifdef __cplusplus
 }
 #endif

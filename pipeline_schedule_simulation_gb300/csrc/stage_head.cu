@@ -9,6 +9,8 @@
 // vocabulary at a time, as bf16 in the workspace, and both gradients take
 // their product with it before the next piece:  dx += d w_piece,
 // dw_piece = d^T x.
+#include <algorithm>
+
 #include "stage_product.cuh"
 
 namespace pps {
@@ -41,7 +43,7 @@ struct StatsEpi {
         float m, s;
         int64_t target;
     };
-    __device__ __forceinline__ void begin(Row &r, int64_t t) const {
+    __device__ __forceinline__ void begin(Row &r, int64_t t, int) const {
         r.m = kNegInf;
         r.s = 0.f;
         r.target = target ? target[t] : -1;
@@ -79,7 +81,7 @@ struct GradEpi {
         int64_t at;  // the target's column counted from the piece's first
         bool in;
     };
-    __device__ __forceinline__ void begin(Row &r, int64_t t) const {
+    __device__ __forceinline__ void begin(Row &r, int64_t t, int) const {
         const int64_t g = target[t];
         r.in = inside(g, V);
         r.c = weight ? weight[t] : 1.f;
@@ -87,37 +89,51 @@ struct GradEpi {
         r.at = g - v0;
     }
     __device__ __forceinline__ void chunk(Row &r, int64_t t, int64_t n, int cnt, const float (&v)[32]) const {
-        for (int j = 0; j < cnt; ++j) {
-            float p = 0.f;
-            if (r.in) {
-                p = exp2f((v[j] - r.lse) * kLog2e);
-                if (n + j == r.at) p -= 1.f;
-                p *= r.c;
+        float p[32];
+        if (r.in) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+                p[j] = exp2f((v[j] - r.lse) * kLog2e);
+                if (n + j == r.at) p[j] -= 1.f;
+                p[j] *= r.c;
             }
-            d[t * ld + n + j] = f32_to_bf16(p);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) p[j] = 0.f;
         }
+        store_bf16(d + t * ld + n, cnt, true, p);  // rows of the workspace are aligned
     }
     __device__ __forceinline__ void end(Row &, int64_t, int64_t) const {}
 };
 
 // dx: pieces add up in 32 bits; the last one writes the result.
 struct DxEpi {
-    float *acc;  // [T][H]
+    float *acc;  // [T][ld_acc]
     uint16_t *dx;
     const int64_t *target;
-    int64_t H, V, ld;
+    int64_t V, ld_acc, ld;
     float scale;
-    bool first, last;
+    bool first, last, vec;
     struct Row {
         bool in;
     };
-    __device__ __forceinline__ void begin(Row &r, int64_t t) const { r.in = inside(target[t], V); }
+    __device__ __forceinline__ void begin(Row &r, int64_t t, int) const { r.in = inside(target[t], V); }
     __device__ __forceinline__ void chunk(Row &r, int64_t t, int64_t n, int cnt, const float (&v)[32]) const {
-        for (int j = 0; j < cnt; ++j) {
-            float s = v[j];
-            if (!first) s += acc[t * H + n + j];
-            if (last) dx[t * ld + n + j] = r.in ? f32_to_bf16(s * scale) : 0;  // 0, whatever w holds
-            else acc[t * H + n + j] = s;
+        float s[32];
+        if (first) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) s[j] = v[j];
+        } else {
+            load_f32(acc + t * ld_acc + n, cnt, true, s);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) s[j] += v[j];
+        }
+        if (last) {  // a row that is left out is 0, whatever w holds
+#pragma unroll
+            for (int j = 0; j < 32; ++j) s[j] = r.in ? s[j] * scale : 0.f;
+            store_bf16(dx + t * ld + n, cnt, vec, s);
+        } else {
+            store_f32(acc + t * ld_acc + n, cnt, true, s);
         }
     }
     __device__ __forceinline__ void end(Row &, int64_t, int64_t) const {}
@@ -128,16 +144,21 @@ struct DwEpi {
     float *dw32;
     int64_t ld;
     float scale;
-    bool add;
+    bool add, vec;
     struct Row {};
-    __device__ __forceinline__ void begin(Row &, int64_t) const {}
-    __device__ __forceinline__ void chunk(Row &, int64_t v_, int64_t n, int cnt, const float (&v)[32]) const {
-        for (int j = 0; j < cnt; ++j) {
-            const int64_t at = v_ * ld + n + j;
-            const float s = v[j] * scale;
-            if (dw16) dw16[at] = f32_to_bf16(s);
-            else dw32[at] = add ? dw32[at] + s : s;
+    __device__ __forceinline__ void begin(Row &, int64_t, int) const {}
+    __device__ __forceinline__ void chunk(Row &, int64_t m, int64_t n, int cnt, const float (&v)[32]) const {
+        float s[32];
+        if (dw32 && add) {
+            load_f32(dw32 + m * ld + n, cnt, vec, s);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) s[j] += v[j] * scale;
+        } else {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) s[j] = v[j] * scale;
         }
+        if (dw32) store_f32(dw32 + m * ld + n, cnt, vec, s);
+        else store_bf16(dw16 + m * ld + n, cnt, vec, s);
     }
     __device__ __forceinline__ void end(Row &, int64_t, int64_t) const {}
 };
@@ -169,17 +190,6 @@ __global__ void __launch_bounds__(1024) k_head_join(const float2 *part, const fl
     }
 }
 
-// A copy of x with aligned rows (ld a multiple of 8 elements) in which the
-// rows that are left out are 0 (target NULL: none is), and so are the columns
-// past H.
-__global__ void __launch_bounds__(256) k_copy_rows(const uint16_t *x, int64_t stride, int64_t T, int64_t H,
-                                                   const int64_t *target, int64_t V, uint16_t *out, int64_t ld) {
-    for (int64_t t = blockIdx.x; t < T; t += gridDim.x) {
-        const bool in = !target || inside(target[t], V);
-        for (int64_t h = threadIdx.x; h < ld; h += blockDim.x) out[t * ld + h] = in && h < H ? x[t * stride + h] : 0;
-    }
-}
-
 // Columns of the vocabulary per piece of the backward pass: d of one piece is
 // at most kPieceBytes.
 constexpr int64_t kPieceBytes = 512ll << 20;
@@ -201,14 +211,30 @@ int check_head(const void *x, int64_t sx, const void *w, int64_t sw, const void 
     return PP_OK;
 }
 
+// An operand as the products read it: in place, or as an aligned copy.
+struct Aligned {
+    uint16_t *copy;  // null: in place
+    Operand op;
+};
+Aligned aligned(Carve &c, const uint16_t *p, int64_t stride, int64_t rows, int64_t H, bool always) {
+    if (!always && rows_aligned(p, stride, rows, 2)) return {nullptr, {p, stride}};
+    const int64_t ld = round_up(H, 8);
+    uint16_t *q = c.take<uint16_t>(rows * ld);
+    return {q, {q, ld}};
+}
+
 struct ForwardSpace {
+    Aligned x, w;
     float2 *part;
     float *picked;
     size_t bytes;
 };
-ForwardSpace forward_space(void *ws, int64_t T, int64_t V) {
+ForwardSpace forward_space(void *ws, const uint16_t *x, int64_t sx, const uint16_t *w, int64_t sw, int64_t T,
+                           int64_t V, int64_t H) {
     Carve c{static_cast<unsigned char *>(ws)};
     ForwardSpace s;
+    s.x = aligned(c, x, sx, T, H, false);
+    s.w = aligned(c, w, sw, V, H, false);
     s.part = c.take<float2>(column_tiles(V) * T);
     s.picked = c.take<float>(T);
     s.bytes = c.used;
@@ -216,21 +242,35 @@ ForwardSpace forward_space(void *ws, int64_t T, int64_t V) {
 }
 
 struct BackwardSpace {
-    uint16_t *x, *d;
-    float *acc;
-    int64_t piece, ldx;
+    Aligned x, w;  // x always as a copy, with the rows that are left out at 0
+    uint16_t *d;
+    float *acc, *parts;
+    int64_t piece, ld_acc;
     size_t bytes;
 };
-BackwardSpace backward_space(void *ws, int64_t T, int64_t V, int64_t H) {
+BackwardSpace backward_space(void *ws, const uint16_t *x, int64_t sx, const uint16_t *w, int64_t sw, int64_t T,
+                             int64_t V, int64_t H) {
     Carve c{static_cast<unsigned char *>(ws)};
     BackwardSpace s;
     s.piece = piece_of(T, V);
-    s.ldx = round_up(H, 8);
-    s.x = c.take<uint16_t>(T * s.ldx);
+    s.ld_acc = round_up(H, 32);
+    s.x = aligned(c, x, sx, T, H, true);
+    s.w = aligned(c, w, sw, V, H, false);
     s.d = c.take<uint16_t>(T * s.piece);
-    s.acc = c.take<float>(T * H);
+    s.acc = c.take<float>(s.piece < V ? T * s.ld_acc : 0);
+    int64_t parts = 0;  // the last piece may be shorter than the others
+    for (const int64_t n : {s.piece < V ? s.piece : V, V - (V - 1) / s.piece * s.piece}) {
+        parts = std::max(parts, part_floats(T, H, n));
+        parts = std::max(parts, part_floats(n, H, T));
+    }
+    s.parts = c.take<float>(parts);
     s.bytes = c.used;
     return s;
+}
+
+int copy_if(const Aligned &a, const uint16_t *p, int64_t stride, int64_t rows, int64_t H, const int64_t *target,
+            int64_t V, cudaStream_t stream) {
+    return a.copy ? launch_copy_rows(p, stride, rows, H, target, V, a.copy, a.op.ld, stream) : PP_OK;
 }
 
 }  // namespace
@@ -241,7 +281,7 @@ using namespace pps;
 extern "C" size_t pp_stage_head_forward_workspace(const uint16_t *x, int64_t stride_x, const uint16_t *w,
                                                   int64_t stride_w, int64_t T, int64_t V, int64_t H) {
     if (T < 1 || V < 1 || H < 1) return 0;
-    return forward_space(nullptr, T, V).bytes;
+    return forward_space(nullptr, x, stride_x, w, stride_w, T, V, H).bytes;
 }
 
 extern "C" int pp_stage_head_forward(const uint16_t *x, int64_t stride_x, const uint16_t *w, int64_t stride_w,
@@ -251,10 +291,12 @@ extern "C" int pp_stage_head_forward(const uint16_t *x, int64_t stride_x, const 
     if (rc != PP_OK) return rc;
     if (T == 0) return PP_OK;
     if ((!loss && !lse) || ((uintptr_t)loss & 3) || ((uintptr_t)lse & 3)) return PP_ERR_ARG;
-    const ForwardSpace s = forward_space(workspace, T, V);
+    const ForwardSpace s = forward_space(workspace, x, stride_x, w, stride_w, T, V, H);
     if (!workspace || ((uintptr_t)workspace & (kStageAlign - 1)) || workspace_bytes < s.bytes) return PP_ERR_ARG;
-    const Operand A{x, stride_x, true}, B{w, stride_w, true};
-    const int rp = launch_product(A, B, T, V, H, StatsEpi{target, T, V, s.part, s.picked}, stream);
+    int rp = copy_if(s.x, x, stride_x, T, H, nullptr, 0, stream);
+    if (rp == PP_OK) rp = copy_if(s.w, w, stride_w, V, H, nullptr, 0, stream);
+    if (rp == PP_OK)
+        rp = launch_product<false, false>(s.x.op, s.w.op, T, V, H, StatsEpi{target, T, V, s.part, s.picked}, stream);
     if (rp != PP_OK) return rp;
     k_head_join<<<(unsigned)ceil_div(T, 32), 1024, 0, stream>>>(s.part, s.picked, target, column_tiles(V), T, V, loss,
                                                                 lse);
@@ -265,7 +307,7 @@ extern "C" int pp_stage_head_forward(const uint16_t *x, int64_t stride_x, const 
 extern "C" size_t pp_stage_head_backward_workspace(const uint16_t *x, int64_t stride_x, const uint16_t *w,
                                                    int64_t stride_w, int64_t T, int64_t V, int64_t H) {
     if (T < 1 || V < 1 || H < 1) return 0;
-    return backward_space(nullptr, T, V, H).bytes;
+    return backward_space(nullptr, x, stride_x, w, stride_w, T, V, H).bytes;
 }
 
 extern "C" int pp_stage_head_backward(const uint16_t *x, int64_t stride_x, const uint16_t *w, int64_t stride_w,
@@ -285,23 +327,26 @@ extern "C" int pp_stage_head_backward(const uint16_t *x, int64_t stride_x, const
         }
         return PP_OK;
     }
-    const BackwardSpace s = backward_space(workspace, T, V, H);
+    const BackwardSpace s = backward_space(workspace, x, stride_x, w, stride_w, T, V, H);
     if (!workspace || ((uintptr_t)workspace & (kStageAlign - 1)) || workspace_bytes < s.bytes) return PP_ERR_ARG;
-    k_copy_rows<<<(unsigned)(T < 65535 ? T : 65535), 256, 0, stream>>>(x, stride_x, T, H, target, V, s.x, s.ldx);
-    PPS_CUDA_TRY(cudaGetLastError());
-    for (int64_t v0 = 0; v0 < V; v0 += s.piece) {
+    int rp = copy_if(s.x, x, stride_x, T, H, target, V, stream);
+    if (rp == PP_OK) rp = copy_if(s.w, w, stride_w, V, H, nullptr, 0, stream);
+    const bool vec_dx = dx && rows_aligned(dx, stride_dx, T, 2), vec_dw = dw && rows_aligned(dw, stride_dw, V, dw_float ? 4 : 2);
+    for (int64_t v0 = 0; v0 < V && rp == PP_OK; v0 += s.piece) {
         const int64_t n = V - v0 < s.piece ? V - v0 : s.piece;
-        int rp = launch_product(Operand{s.x, s.ldx, true}, Operand{w + v0 * stride_w, stride_w, true}, T, n, H,
-                                GradEpi{target, lse, weight, T, V, v0, s.d, s.piece}, stream);
+        const Operand wp{s.w.op.p + v0 * s.w.op.ld, s.w.op.ld}, d{s.d, s.piece};
+        rp = launch_product<false, false>(s.x.op, wp, T, n, H, GradEpi{target, lse, weight, T, V, v0, s.d, s.piece},
+                                          stream);
         if (rp == PP_OK && dx)
-            rp = launch_product(Operand{s.d, s.piece, true}, Operand{w + v0 * stride_w, stride_w, false}, T, H, n,
-                                DxEpi{s.acc, dx, target, H, V, stride_dx, scale, v0 == 0, v0 + n == V}, stream);
+            rp = product_in_parts<false, true>(
+                d, wp, T, H, n, DxEpi{s.acc, dx, target, V, s.ld_acc, stride_dx, scale, v0 == 0, v0 + n == V, vec_dx},
+                s.parts, stream);
         if (rp == PP_OK && dw)
-            rp = launch_product(Operand{s.d, s.piece, false}, Operand{s.x, s.ldx, false}, n, H, T,
-                                DwEpi{dw_float ? nullptr : (uint16_t *)dw + v0 * stride_dw,
-                                      dw_float ? (float *)dw + v0 * stride_dw : nullptr, stride_dw, scale, dw_add != 0},
-                                stream);
-        if (rp != PP_OK) return rp;
+            rp = product_in_parts<true, true>(
+                d, s.x.op, n, H, T,
+                DwEpi{dw_float ? nullptr : (uint16_t *)dw + v0 * stride_dw,
+                      dw_float ? (float *)dw + v0 * stride_dw : nullptr, stride_dw, scale, dw_add != 0, vec_dw},
+                s.parts, stream);
     }
-    return PP_OK;
+    return rp;
 }

@@ -47,10 +47,19 @@ struct WgradEpi {
     const float *add;
     float *dw;
     int64_t ld_add, ld;
+    bool vec;
     struct Row {};
-    __device__ __forceinline__ void begin(Row &, int64_t) const {}
+    __device__ __forceinline__ void begin(Row &, int64_t, int) const {}
     __device__ __forceinline__ void chunk(Row &, int64_t m, int64_t n, int cnt, const float (&v)[32]) const {
-        for (int j = 0; j < cnt; ++j) dw[m * ld + n + j] = add ? add[m * ld_add + n + j] + v[j] : v[j];
+        if (add) {
+            float s[32];
+            load_f32(add + m * ld_add + n, cnt, vec, s);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) s[j] += v[j];
+            store_f32(dw + m * ld + n, cnt, vec, s);
+        } else {
+            store_f32(dw + m * ld + n, cnt, vec, v);
+        }
     }
     __device__ __forceinline__ void end(Row &, int64_t, int64_t) const {}
 };
@@ -60,15 +69,21 @@ bool bad_kept(const int8_t *q, int64_t sq, const int8_t *e, int64_t se, int64_t 
 }
 
 struct WgradSpace {
-    uint16_t *v;  // what the checkpoint stands for, rows of ld
-    int64_t ld;
+    uint16_t *v;   // what the checkpoint stands for, rows of ld
+    uint16_t *dy;  // an aligned copy of dy, or null
+    float *parts;
+    int64_t ld, ld_dy;
     size_t bytes;
 };
-WgradSpace wgrad_space(void *ws, int64_t T, int64_t H) {
+WgradSpace wgrad_space(void *ws, const uint16_t *dy, int64_t stride_dy, int64_t T, int64_t N, int64_t H) {
     Carve c{static_cast<unsigned char *>(ws)};
     WgradSpace s;
     s.ld = round_up(H, 8);
     s.v = c.take<uint16_t>(T * s.ld);
+    const bool copy = !rows_aligned(dy, stride_dy, T, 2);
+    s.ld_dy = copy ? round_up(N, 8) : stride_dy;
+    s.dy = copy ? c.take<uint16_t>(T * s.ld_dy) : nullptr;
+    s.parts = c.take<float>(part_floats(N, H, T));
     s.bytes = c.used;
     return s;
 }
@@ -123,7 +138,7 @@ extern "C" int pp_stage_unpack(const int8_t *q, int64_t stride_q, const int8_t *
 extern "C" size_t pp_stage_weight_grad_workspace(const uint16_t *dy, int64_t stride_dy, int64_t T, int64_t N,
                                                  int64_t H) {
     if (T < 1 || N < 1 || H < 1) return 0;
-    return wgrad_space(nullptr, T, H).bytes;
+    return wgrad_space(nullptr, dy, stride_dy, T, N, H).bytes;
 }
 
 extern "C" int pp_stage_weight_grad(const uint16_t *dy, int64_t stride_dy, const int8_t *q, int64_t stride_q,
@@ -144,10 +159,13 @@ extern "C" int pp_stage_weight_grad(const uint16_t *dy, int64_t stride_dy, const
         return PP_OK;
     }
     if (!dy || ((uintptr_t)dy & 1) || stride_dy < N || bad_kept(q, stride_q, e, stride_e, H)) return PP_ERR_ARG;
-    const WgradSpace s = wgrad_space(workspace, T, H);
+    const WgradSpace s = wgrad_space(workspace, dy, stride_dy, T, N, H);
     if (!workspace || ((uintptr_t)workspace & (kStageAlign - 1)) || workspace_bytes < s.bytes) return PP_ERR_ARG;
-    const int ru = launch_unpack(q, stride_q, e, stride_e, T, H, s.v, s.ld, stream);
-    if (ru != PP_OK) return ru;
-    return launch_product(Operand{dy, stride_dy, false}, Operand{s.v, s.ld, false}, N, H, T,
-                          WgradEpi{add, dw, stride_add, stride_dw}, stream);
+    const bool copy = !rows_aligned(dy, stride_dy, T, 2);
+    int rp = launch_unpack(q, stride_q, e, stride_e, T, H, s.v, s.ld, stream);
+    if (rp == PP_OK && copy) rp = launch_copy_rows(dy, stride_dy, T, N, nullptr, 0, s.dy, s.ld_dy, stream);
+    if (rp != PP_OK) return rp;
+    const bool vec = rows_aligned(dw, stride_dw, N, 4) && (!add || rows_aligned(add, stride_add, N, 4));
+    return product_in_parts<true, true>(Operand{copy ? s.dy : dy, s.ld_dy}, Operand{s.v, s.ld}, N, H, T,
+                                        WgradEpi{add, dw, stride_add, stride_dw, vec}, s.parts, stream);
 }

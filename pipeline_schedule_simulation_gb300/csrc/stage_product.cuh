@@ -1,85 +1,358 @@
-// stage_product.cuh -- matrix products of the pipeline-stage operators.
+// stage_product.cuh -- matrix products of the pipeline-stage operators on the
+// tensor cores.
 //
-// C[m][n] = sum_k A(m,k) B(n,k) over bf16 operands, summed in 32 bits, handed
-// to an epilogue row by row instead of being stored:
+// C[m][n] = sum_k A(m,k) B(n,k) over bf16 operands, summed in 32 bits in TMEM,
+// handed to an epilogue row by row instead of being stored:
 //   typename Epi::Row  what a row keeps between its pieces
-//   begin(row, m)      a row m of the tile starts
+//   begin(row, m, part)  a row m of the tile starts (part: which part of K)
 //   chunk(row, m, n, cnt, v)  columns n .. n+cnt-1 (cnt <= 32) of row m
 //   end(row, m, tile)  the row's piece of column tile `tile` is done
 // Each (row, column tile) is handed over by one thread, in column order.
+//
+// One persistent block per SM: a warp loads 64-deep slices of A and B by TMA
+// into a ring, a thread issues the MMAs of a 128 x 256 tile into one of two
+// TMEM accumulators, four warps take the other accumulator through the
+// epilogue.  Operands come K-major or MN-major as they lie in memory; both
+// forms use the 128-byte swizzle.
 #pragma once
 
+#include <atomic>
+
 #include "stage_common.cuh"
+#include "stage_tc.cuh"
 
 namespace pps {
 
-// An operand: element (i, k) at p[i*ld + k] (k_major) or p[k*ld + i].
+// An operand: element (i, k) at p[i*ld + k] (K-major) or p[k*ld + i]
+// (MN-major), with rows aligned to 16 bytes (rows_aligned).
 struct Operand {
     const uint16_t *p;
     int64_t ld;
-    bool k_major;
-    __device__ __forceinline__ uint16_t at(int64_t i, int64_t k) const {
-        return k_major ? p[i * ld + k] : p[k * ld + i];
-    }
 };
 
-constexpr int kTileN = 64;  // columns of one column tile
-
-// One 64 x 64 tile per block, 4 x 4 elements per thread, 16 k at a time.
-template <class Epi>
-__global__ void __launch_bounds__(256) k_product(Operand A, Operand B, int64_t M, int64_t N, int64_t K, Epi epi) {
-    __shared__ float sa[16][65], sb[16][65], sc[64][65];
-    const int64_t mt = (M + 63) / 64, tile = blockIdx.x / mt;
-    const int64_t m0 = blockIdx.x % mt * 64, n0 = tile * kTileN;
-    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-    float acc[4][4] = {};
-    for (int64_t k0 = 0; k0 < K; k0 += 16) {
-        for (int i = threadIdx.x; i < 64 * 16; i += 256) {
-            // consecutive threads follow the operand's contiguous direction
-            const int ra = A.k_major ? i >> 4 : i & 63, ka = A.k_major ? i & 15 : i >> 6;
-            const int rb = B.k_major ? i >> 4 : i & 63, kb = B.k_major ? i & 15 : i >> 6;
-            sa[ka][ra] = m0 + ra < M && k0 + ka < K ? bf16_to_f32(A.at(m0 + ra, k0 + ka)) : 0.f;
-            sb[kb][rb] = n0 + rb < N && k0 + kb < K ? bf16_to_f32(B.at(n0 + rb, k0 + kb)) : 0.f;
-        }
-        __syncthreads();
-#pragma unroll
-        for (int k = 0; k < 16; ++k)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) acc[i][j] += sa[k][ty + 16 * i] * sb[k][tx + 16 * j];
-        __syncthreads();
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) sc[ty + 16 * i][tx + 16 * j] = acc[i][j];
-    __syncthreads();
-    const int64_t m = m0 + threadIdx.x;
-    if (threadIdx.x >= 64 || m >= M) return;
-    typename Epi::Row row;
-    epi.begin(row, m);
-    for (int c = 0; c < kTileN && n0 + c < N; c += 32) {
-        float v[32];
-#pragma unroll
-        for (int j = 0; j < 32; ++j) v[j] = sc[threadIdx.x][c + j];
-        const int64_t left = N - n0 - c;
-        epi.chunk(row, m, n0 + c, left < 32 ? (int)left : 32, v);
-    }
-    epi.end(row, m, tile);
-}
+constexpr int kTileM = 128, kTileN = 256, kTileK = 64;
+constexpr int kStages = 4;
+constexpr int kBytesA = kTileM * kTileK * 2, kBytesB = kTileN * kTileK * 2, kBytesStage = kBytesA + kBytesB;
+constexpr int kProductSmem = kStages * kBytesStage + 1024;
+constexpr int kProductThreads = 256;
 
 inline int64_t column_tiles(int64_t N) { return ceil_div(N, kTileN); }
 
-template <class Epi>
+struct ProductShape {
+    int M, N, K;
+    int mt, nt;    // tiles
+    int group;     // row tiles that a run of blocks takes together
+    int splits;    // parts of K
+    int k_blocks;  // slices of K in each part (the last may have fewer)
+};
+
+// Tile number -> (row tile, column tile): `group` row tiles at a time run
+// through all column tiles, so that their slices of A stay in the L2 cache.
+__device__ __forceinline__ void tile_at(const ProductShape &s, int64_t i, int &m, int &n) {
+    const int64_t per = (int64_t)s.group * s.nt;
+    const int g = (int)(i / per), first = g * s.group;
+    const int rows = min(s.group, s.mt - first), r = (int)(i - g * per);
+    m = first + r % rows;
+    n = r / rows;
+}
+
+template <class Epi, bool A_MN, bool B_MN>
+__global__ void __launch_bounds__(kProductThreads, 1)
+    k_product(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
+              const ProductShape s, const Epi epi) {
+    extern __shared__ unsigned char raw[];
+    __shared__ __align__(8) uint64_t bars[2 * kStages + 5];
+    __shared__ uint32_t tmem_at;
+    __shared__ int stop;
+    const uint32_t ring = (tc::smem_u32(raw) + 1023) & ~1023u;
+    const uint32_t full = tc::smem_u32(bars), empty = full + 8 * kStages;
+    const uint32_t acc_full = empty + 8 * kStages, acc_empty = acc_full + 16, drained = acc_empty + 16;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t tiles = (int64_t)s.mt * s.nt * s.splits;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kStages; ++i) {
+            tc::mbar_init(full + 8 * i, 1);
+            tc::mbar_init(empty + 8 * i, 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            tc::mbar_init(acc_full + 8 * i, 1);
+            tc::mbar_init(acc_empty + 8 * i, 4);
+        }
+        tc::mbar_init(drained, 1);
+        stop = 0;
+        tc::fence_barrier_init();
+        tc::prefetch_map(&map_a);
+        tc::prefetch_map(&map_b);
+    }
+    if (warp == 2) tc::tmem_alloc(tc::smem_u32(&tmem_at), 512);
+    tc::fence_before();
+    __syncthreads();
+    tc::fence_after();
+    const uint32_t tmem = tmem_at;
+    const int all_blocks = (s.K + kTileK - 1) / kTileK;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            int64_t it = 0;
+            bool ok = true;
+            for (int64_t t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
+                const int part = (int)(t % s.splits);
+                int m, n;
+                tile_at(s, t / s.splits, m, n);
+                const int k0 = part * s.k_blocks, k1 = min(k0 + s.k_blocks, all_blocks);
+                for (int k = k0; k < k1; ++k, ++it) {
+                    const int st = (int)(it % kStages);
+                    if (!tc::mbar_wait(empty + 8 * st, (uint32_t)(it / kStages + 1) & 1, &stop, 1)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t bar = full + 8 * st, a = ring + st * kBytesStage, b = a + kBytesA;
+                    tc::mbar_expect(bar, kBytesStage);
+                    if (A_MN) {
+#pragma unroll
+                        for (int i = 0; i < kTileM / 64; ++i)
+                            tc::tma_load(a + i * 8192, &map_a, m * kTileM + i * 64, k * kTileK, bar);
+                    } else {
+                        tc::tma_load(a, &map_a, k * kTileK, m * kTileM, bar);
+                    }
+                    if (B_MN) {
+#pragma unroll
+                        for (int i = 0; i < kTileN / 64; ++i)
+                            tc::tma_load(b + i * 8192, &map_b, n * kTileN + i * 64, k * kTileK, bar);
+                    } else {
+                        tc::tma_load(b, &map_b, k * kTileK, n * kTileN, bar);
+                    }
+                }
+            }
+            // after giving up: the copies still in flight land before the block ends
+            if (!ok)
+                for (int64_t j = it > kStages ? it - kStages : 0; j < it; ++j)
+                    tc::mbar_drain(full + 8 * (int)(j % kStages), (uint32_t)(j / kStages) & 1);
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            constexpr uint32_t idesc = tc::instr_desc(kTileM, kTileN, A_MN, B_MN);
+            // 16 k further: 32 bytes along a K-major row, two groups of 8 k in the MN-major form
+            constexpr uint32_t step_a = A_MN ? 2048 : 32, step_b = B_MN ? 2048 : 32;
+            int64_t it = 0;
+            int j = 0;
+            bool ok = true;
+            for (int64_t t = blockIdx.x; t < tiles && ok; t += gridDim.x, ++j) {
+                const int part = (int)(t % s.splits);
+                const int k0 = part * s.k_blocks, k1 = min(k0 + s.k_blocks, all_blocks);
+                const int buf = j & 1;
+                if (!tc::mbar_wait(acc_empty + 8 * buf, (uint32_t)((j >> 1) + 1) & 1, &stop, 2)) {
+                    ok = false;
+                    break;
+                }
+                tc::fence_after();
+                for (int k = k0; k < k1; ++k, ++it) {
+                    const int st = (int)(it % kStages);
+                    if (!tc::mbar_wait(full + 8 * st, (uint32_t)(it / kStages) & 1, &stop, 3)) {
+                        ok = false;
+                        break;
+                    }
+                    tc::fence_after();
+                    const uint32_t a = ring + st * kBytesStage, b = a + kBytesA;
+#pragma unroll
+                    for (int kk = 0; kk < kTileK / 16; ++kk)
+                        tc::mma(tmem + buf * kTileN, tc::smem_desc(a + kk * step_a, A_MN ? 8192 : 16, 1024),
+                                tc::smem_desc(b + kk * step_b, B_MN ? 8192 : 16, 1024), idesc, k > k0 || kk > 0);
+                    tc::mma_commit(empty + 8 * st);
+                }
+                if (ok) tc::mma_commit(acc_full + 8 * buf);
+            }
+            // the MMAs have finished before TMEM is given back
+            tc::mma_commit(drained);
+            tc::mbar_drain(drained, 0);
+        }
+    } else if (warp >= 4) {
+        const int quarter = warp - 4;
+        int j = 0;
+        for (int64_t t = blockIdx.x; t < tiles; t += gridDim.x, ++j) {
+            const int part = (int)(t % s.splits);
+            int mt, nt;
+            tile_at(s, t / s.splits, mt, nt);
+            const int buf = j & 1;
+            const int64_t m = (int64_t)mt * kTileM + quarter * 32 + lane;
+            const bool live = m < s.M;
+            typename Epi::Row row;
+            if (live) epi.begin(row, m, part);
+            // lanes give up one by one: the warp goes on together
+            const bool ok = tc::mbar_wait(acc_full + 8 * buf, (uint32_t)(j >> 1) & 1, &stop, 4);
+            if (!__all_sync(~0u, ok)) break;
+            tc::fence_after();
+            for (int c = 0; c < kTileN && nt * kTileN + c < s.N; c += 32) {
+                float v[32];
+                tc::tmem_load32(tmem + ((uint32_t)(quarter * 32) << 16) + buf * kTileN + c, v);
+                const int n = nt * kTileN + c, left = s.N - n;
+                if (live) epi.chunk(row, m, n, left < 32 ? left : 32, v);
+            }
+            tc::fence_before();
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(acc_empty + 8 * buf);
+            if (live) epi.end(row, m, nt);
+        }
+    }
+    tc::fence_before();
+    __syncthreads();
+    tc::fence_after();
+    if (warp == 2) tc::tmem_free(tmem, 512);
+}
+
+// ---- host side
+
+// One map of a row-major matrix for boxes of box_rows x box_inner elements.
+int encode_map(CUtensorMap *map, const void *base, int64_t inner, int64_t rows, int64_t ld, int box_inner,
+               int box_rows);
+int sm_count();
+
+// Parts of K that give every SM a tile where there are few tiles: each part
+// has at least 4 slices.
+inline int splits_for(int64_t M, int64_t N, int64_t K) {
+    const int64_t tiles = ceil_div(M, kTileM) * ceil_div(N, kTileN), blocks = ceil_div(K, kTileK);
+    int64_t s = sm_count() / (tiles > 0 ? tiles : 1);
+    if (s > blocks / 4) s = blocks / 4;
+    if (s <= 1) return 1;
+    return (int)ceil_div(blocks, ceil_div(blocks, s));  // no part is empty
+}
+
+template <bool A_MN, bool B_MN, class Epi>
 int launch_product(const Operand &A, const Operand &B, int64_t M, int64_t N, int64_t K, const Epi &epi,
-                   cudaStream_t stream) {
-    if (M <= 0 || N <= 0) return PP_OK;
-    const int64_t blocks = ceil_div(M, 64) * column_tiles(N);
-    if (blocks > 0x7FFFFFFF) return PP_ERR_SIZE;
-    k_product<Epi><<<(unsigned)blocks, 256, 0, stream>>>(A, B, M, N, K, epi);
+                   cudaStream_t stream, int splits = 1) {
+    if (M <= 0 || N <= 0 || K <= 0) return PP_ERR_INTERNAL;
+    CUtensorMap ma, mb;
+    int rc = A_MN ? encode_map(&ma, A.p, M, K, A.ld, 64, kTileK) : encode_map(&ma, A.p, K, M, A.ld, kTileK, kTileM);
+    if (rc == PP_OK)
+        rc = B_MN ? encode_map(&mb, B.p, N, K, B.ld, 64, kTileK) : encode_map(&mb, B.p, K, N, B.ld, kTileK, kTileN);
+    if (rc != PP_OK) return rc;
+    static std::atomic<uint64_t> ready{0};  // devices on which the kernel's shared memory is set
+    int dev = 0;
+    PPS_CUDA_TRY(cudaGetDevice(&dev));
+    if (dev > 63 || !(ready.load(std::memory_order_relaxed) >> dev & 1)) {
+        PPS_CUDA_TRY(cudaFuncSetAttribute(k_product<Epi, A_MN, B_MN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                          kProductSmem));
+        if (dev <= 63) ready.fetch_or(1ull << dev, std::memory_order_relaxed);
+    }
+    ProductShape s;
+    s.M = (int)M, s.N = (int)N, s.K = (int)K;
+    s.mt = (int)ceil_div(M, kTileM), s.nt = (int)ceil_div(N, kTileN);
+    s.splits = splits;
+    s.k_blocks = (int)ceil_div(ceil_div(K, kTileK), splits);
+    s.group = s.mt < 16 ? s.mt : 16;
+    const int64_t tiles = (int64_t)s.mt * s.nt * s.splits, sms = sm_count();
+    k_product<Epi, A_MN, B_MN>
+        <<<(unsigned)(tiles < sms ? tiles : sms), kProductThreads, kProductSmem, stream>>>(ma, mb, s, epi);
     PPS_CUDA_TRY(cudaGetLastError());
     return PP_OK;
 }
+
+// Parts of K: each part's sums apart, [part][M][ld].  Epilogues are local to
+// their translation unit, and so are the kernels and attribute flags made from
+// them.
+namespace {
+struct PartEpi {
+    float *parts;
+    int64_t M, ld;
+    struct Row {
+        float *p;
+    };
+    __device__ __forceinline__ void begin(Row &r, int64_t m, int part) const { r.p = parts + (part * M + m) * ld; }
+    __device__ __forceinline__ void chunk(Row &r, int64_t, int64_t n, int cnt, const float (&v)[32]) const {
+        // ld is a multiple of 32: the columns past the last one are there to be written
+        float4 *p = reinterpret_cast<float4 *>(r.p + n);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) p[j] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+    }
+    __device__ __forceinline__ void end(Row &, int64_t, int64_t) const {}
+};
+}  // namespace
+
+// Adds the parts up, always in the same order, and hands them to the epilogue.
+template <class Epi>
+__global__ void __launch_bounds__(128) k_join_parts(const float *parts, int splits, int64_t M, int64_t N, int64_t ld,
+                                                    const Epi epi) {
+    const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x, per = ld / 32;
+    const int64_t m = i / per, n = i % per * 32;
+    if (m >= M || n >= N) return;
+    float v[32] = {};
+    for (int s = 0; s < splits; ++s) {
+        const float4 *p = reinterpret_cast<const float4 *>(parts + (s * M + m) * ld + n);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float4 q = p[j];
+            v[4 * j] += q.x, v[4 * j + 1] += q.y, v[4 * j + 2] += q.z, v[4 * j + 3] += q.w;
+        }
+    }
+    typename Epi::Row row;
+    epi.begin(row, m, 0);
+    epi.chunk(row, m, n, N - n < 32 ? (int)(N - n) : 32, v);
+    epi.end(row, m, 0);
+}
+
+// Floats of scratch memory that product_in_parts needs.
+inline int64_t part_floats(int64_t M, int64_t N, int64_t K) {
+    const int s = splits_for(M, N, K);
+    return s > 1 ? s * M * round_up(N, 32) : 0;
+}
+
+// A product whose K is shared out where there are too few tiles for the SMs.
+template <bool A_MN, bool B_MN, class Epi>
+int product_in_parts(const Operand &A, const Operand &B, int64_t M, int64_t N, int64_t K, const Epi &epi, float *parts,
+                     cudaStream_t stream) {
+    const int splits = splits_for(M, N, K);
+    if (splits == 1) return launch_product<A_MN, B_MN>(A, B, M, N, K, epi, stream);
+    const int64_t ld = round_up(N, 32);
+    const int rc = launch_product<A_MN, B_MN>(A, B, M, N, K, PartEpi{parts, M, ld}, stream, splits);
+    if (rc != PP_OK) return rc;
+    k_join_parts<Epi><<<(unsigned)ceil_div(M * (ld / 32), 128), 128, 0, stream>>>(parts, splits, M, N, ld, epi);
+    PPS_CUDA_TRY(cudaGetLastError());
+    return PP_OK;
+}
+
+// 32 columns of a row as bf16, or added to / stored as 32-bit floats.
+__device__ __forceinline__ void store_bf16(uint16_t *p, int cnt, bool vec, const float (&v)[32]) {
+    if (vec && cnt == 32) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            reinterpret_cast<uint4 *>(p)[j] =
+                make_uint4(f32_to_bf16x2(v[8 * j], v[8 * j + 1]), f32_to_bf16x2(v[8 * j + 2], v[8 * j + 3]),
+                           f32_to_bf16x2(v[8 * j + 4], v[8 * j + 5]), f32_to_bf16x2(v[8 * j + 6], v[8 * j + 7]));
+    } else {
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+            if (j < cnt) p[j] = f32_to_bf16(v[j]);
+    }
+}
+__device__ __forceinline__ void load_f32(const float *p, int cnt, bool vec, float (&v)[32]) {
+    if (vec && cnt == 32) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float4 q = reinterpret_cast<const float4 *>(p)[j];
+            v[4 * j] = q.x, v[4 * j + 1] = q.y, v[4 * j + 2] = q.z, v[4 * j + 3] = q.w;
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < 32; ++j) v[j] = j < cnt ? p[j] : 0.f;
+    }
+}
+__device__ __forceinline__ void store_f32(float *p, int cnt, bool vec, const float (&v)[32]) {
+    if (vec && cnt == 32) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            reinterpret_cast<float4 *>(p)[j] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+            if (j < cnt) p[j] = v[j];
+    }
+}
+
+// A copy of rows at any stride and alignment into aligned ones (ld a multiple
+// of 8 elements), 0 past column H; with `target`, a row whose target is
+// outside 0..V-1 becomes 0.
+int launch_copy_rows(const uint16_t *x, int64_t stride, int64_t T, int64_t H, const int64_t *target, int64_t V,
+                     uint16_t *out, int64_t ld, cudaStream_t stream);
 
 }  // namespace pps

@@ -27,7 +27,7 @@ from .binding import LIB, PPSchedError, _arg, _check, _ptr, _reach, _stream  # n
 EXPORTS = ("pp_stage_head_forward_workspace", "pp_stage_head_forward", "pp_stage_head_backward_workspace",
            "pp_stage_head_backward", "pp_stage_pack", "pp_stage_unpack", "pp_stage_weight_grad_workspace",
            "pp_stage_weight_grad", "pp_stage_join_forward", "pp_stage_join_backward_workspace",
-           "pp_stage_join_backward")
+           "pp_stage_join_backward", "pp_stage_wait_failure")
 
 #: Columns of a checkpoint that share one exponent.
 BLOCK = 64
@@ -51,6 +51,7 @@ def _declare(lib):
     lib.pp_stage_join_backward_workspace.argtypes = [i64, i64, i64]
     lib.pp_stage_join_backward.argtypes = [*m, *m, *m, *m, *m, *m, *m, *m, vp, vp, vp, vp, *m, i64, f32, i64, i64,
                                            *m, *m, vp, vp, *m, vp, size, vp]
+    lib.pp_stage_wait_failure.argtypes = [vp]
     for name in EXPORTS:
         getattr(lib, name).restype = size if name.endswith("_workspace") else i32
 
@@ -367,3 +368,10 @@ def join_backward(dh, dy, y, f, rstd_post, rstd_pre, w_post, w_pre, gate=None, *
                                           T, H, *_m(dx), *_m(df), _ptr(dw1), _ptr(dw2), *_m(dg), _ptr(ws), ws.numel(),
                                           on.handle), "pp_stage_join_backward")
     return out
+
+
+def wait_failure():
+    """The first wait inside a product that ran out since the previous call (0: none); synchronizes the device."""
+    word = ctypes.c_uint64()
+    _check(LIB.pp_stage_wait_failure(ctypes.byref(word)), "pp_stage_wait_failure")
+    return word.value
