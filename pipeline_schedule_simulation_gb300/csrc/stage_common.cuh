@@ -1,6 +1,7 @@
 // stage_common.cuh -- what the pipeline-stage operators (ppstage.h) share.
 #pragma once
 
+#include <atomic>
 #include <cstddef>
 #include <cstdint>
 
@@ -34,6 +35,21 @@ inline int64_t round_up(int64_t a, int64_t b) { return ceil_div(a, b) * b; }
 // 16 bytes (a single row needs only its base).
 inline bool rows_aligned(const void *p, int64_t stride, int64_t rows, int elem) {
     return ((uintptr_t)p & 15) == 0 && (rows <= 1 || (stride * elem & 15) == 0);
+}
+
+int sm_count();  // of the current device
+
+// Lets a kernel use `bytes` of dynamic shared memory, once per device (`ready`
+// is the kernel's own).
+template <class K>
+int allow_smem(K kernel, int bytes, std::atomic<uint64_t> &ready) {
+    int dev = 0;
+    PPS_CUDA_TRY(cudaGetDevice(&dev));
+    if (dev > 63 || !(ready.load(std::memory_order_relaxed) >> dev & 1)) {
+        PPS_CUDA_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes));
+        if (dev <= 63) ready.fetch_or(1ull << dev, std::memory_order_relaxed);
+    }
+    return PP_OK;
 }
 
 __device__ __forceinline__ float bf16_to_f32(uint16_t b) { return __uint_as_float((uint32_t)b << 16); }

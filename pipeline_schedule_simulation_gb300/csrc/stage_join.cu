@@ -4,8 +4,15 @@
 // A block of threads holds a whole row in registers, so each input is read
 // once and each output written once: forward moves 8 bytes an element (10 with
 // both checkpoints), backward 10 from checkpoints and 12 from bf16.  Both
-// directions need two sums over the row, one after the other.
+// directions need two sums over the row, one after the other, and a block that
+// loads a row, sums and only then loads the next leaves the memory idle while
+// it sums.  So long runs of rows come through a ring in shared memory that
+// bulk copies keep filled, several rows ahead of the arithmetic; few or
+// unaligned rows are loaded directly, by as many blocks as there are rows.
+#include <atomic>
+
 #include "stage_kept.cuh"
+#include "stage_tc.cuh"
 
 namespace pps {
 namespace {
@@ -66,7 +73,7 @@ __global__ void __launch_bounds__(NT) k_join_forward(const JoinForward a) {
             for (int i = 0; i < NV; ++i) {
                 const int c = (i * NT + (int)threadIdx.x) * 8, left = a.H - c;
                 int e;
-                const uint2 b = pack8(f[i], e);
+                const uint2 b = pack8(narrow(f[i]), e);  // f came as bf16: nothing is lost
                 if (left > 0) {
                     store8_bytes<VEC>(a.kf.q + t * a.kf.sq + c, left, b);
                     if ((threadIdx.x & 7) == 0) a.kf.e[t * a.kf.se + c / kBlock] = (int8_t)e;
@@ -102,11 +109,8 @@ __global__ void __launch_bounds__(NT) k_join_forward(const JoinForward a) {
             for (int j = 0; j < 8; ++j) w[j] *= y[i][j] * r2;
             if (left > 0) store8_bf16<VEC>(a.h + t * a.sh + c, left, w);
             if (KEEP) {
-                float yr[8];  // y as the next reader sees it
-#pragma unroll
-                for (int j = 0; j < 8; ++j) yr[j] = bf16_to_f32(f32_to_bf16(y[i][j]));
                 int e;
-                const uint2 b = pack8(yr, e);
+                const uint2 b = pack8(narrow(y[i]), e);  // y as its next reader sees it
                 if (left > 0) {
                     store8_bytes<VEC>(a.ky.q + t * a.ky.sq + c, left, b);
                     if ((threadIdx.x & 7) == 0) a.ky.e[t * a.ky.se + c / kBlock] = (int8_t)e;
@@ -120,16 +124,23 @@ __global__ void __launch_bounds__(NT) k_join_forward(const JoinForward a) {
     }
 }
 
+// Threads of a ring block for this width, two vectors of 8 columns each (one
+// up to 1024 columns); 0 where a row is too wide.
+int ring_threads(int64_t H) { return H <= 2048 ? 128 : H <= 4096 ? 256 : H <= 8192 ? 512 : 0; }
+
 // Rows are shared out in items: a run of rows of one gate group, so that an
 // item's column sums belong to one gate row.
 struct Items {
     int64_t rows_per_gate, groups, rows, per_group, count;
 };
-Items items_of(int64_t T, int64_t rows_per_gate) {
+Items items_of(int64_t T, int64_t H, int64_t rows_per_gate) {
     Items it;
     it.rows_per_gate = rows_per_gate > 0 && rows_per_gate < T ? rows_per_gate : T;
     it.groups = ceil_div(T, it.rows_per_gate);
-    const int64_t want = 152 * 2;
+    // one run of rows for each ring block that is resident, or one for each of
+    // two direct blocks on an SM
+    const int threads = ring_threads(H);
+    const int64_t want = (int64_t)sm_count() * (threads ? 512 / threads : 2);
     it.rows = ceil_div(T, want);
     if (it.rows > it.rows_per_gate) it.rows = it.rows_per_gate;
     it.per_group = ceil_div(it.rows_per_gate, it.rows);
@@ -155,7 +166,7 @@ template <bool VEC, bool PACKED>
 __device__ __forceinline__ void load_saved(const uint16_t *p, int64_t s, const Kept &k, int64_t t, int c, int left,
                                            float (&v)[8]) {
     if (PACKED) {
-        if (left > 0) unpack8(load8_bytes<VEC>(k.q + t * k.sq + c, left), k.e[t * k.se + c / kBlock], v);
+        if (left > 0) unpack8(load8_bytes<VEC>(k.q + t * k.sq + c, left), step_of(k.e[t * k.se + c / kBlock]), v);
         // past the row's end a block's bytes are 0, and so is a value unless the block is not finite
         if (left < 8) {
 #pragma unroll
@@ -249,6 +260,318 @@ __global__ void __launch_bounds__(NT) k_join_backward(const JoinBackward a) {
     }
 }
 
+// ---- rows through a ring
+
+// Shared memory of one block: two mbarriers' worth of header, then the stages.
+constexpr int kRingHeader = 128, kMaxStages = 4;
+
+// The rows that one block takes, first, first + step, ... below last, each as
+// `parts` bulk copies into the ring's next stage.
+struct RowPart {
+    const unsigned char *p;
+    int64_t stride;  // bytes
+    uint32_t bytes, at;
+};
+template <int PARTS>
+struct Ring {
+    uint32_t base, bars, stage_bytes;
+    int stages;
+    RowPart part[PARTS];
+    __device__ __forceinline__ void load(int64_t row, int slot) const {  // one thread
+        const uint32_t bar = bars + 8 * slot, to = base + slot * stage_bytes;
+        tc::mbar_expect(bar, stage_bytes);
+#pragma unroll
+        for (int i = 0; i < PARTS; ++i)
+            if (part[i].bytes) tc::bulk_load(to + part[i].at, part[i].p + row * part[i].stride, part[i].bytes, bar);
+    }
+};
+
+__device__ __forceinline__ Raw8 ring_raw(const unsigned char *stage, uint32_t at, int c) {
+    const uint4 w = *reinterpret_cast<const uint4 *>(stage + at + 2 * c);
+    return Raw8{{w.x, w.y, w.z, w.w}};
+}
+
+template <int NT, int NV, bool KEEP>
+__global__ void __launch_bounds__(NT, 1024 / NT) k_join_forward_ring(const JoinForward a, const int stages) {
+    extern __shared__ __align__(128) unsigned char smem[];
+    __shared__ float sh[2][32];
+    __shared__ int stop;
+    const uint32_t row_bytes = 2u * a.H;
+    Ring<2> ring{tc::smem_u32(smem) + kRingHeader, tc::smem_u32(smem), 2 * row_bytes, stages,
+                 {{(const unsigned char *)a.f, 2 * a.sf, row_bytes, 0}, {(const unsigned char *)a.x, 2 * a.sx, row_bytes, row_bytes}}};
+    const float inv_h = 1.f / (float)a.H;
+    if (threadIdx.x == 0) {
+        stop = 0;
+        for (int i = 0; i < stages; ++i) tc::mbar_init(ring.bars + 8 * i, 1);
+        tc::fence_barrier_init();
+        for (int i = 0; i < stages; ++i)
+            if (blockIdx.x + (int64_t)i * gridDim.x < a.T) ring.load(blockIdx.x + (int64_t)i * gridDim.x, i);
+    }
+    __syncthreads();
+    int slot = 0;
+    uint32_t parity = 0;
+    for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
+        const unsigned char *stage = smem + kRingHeader + slot * ring.stage_bytes;
+        const uint16_t *g = a.gate ? a.gate + (a.rows_per_gate > 0 ? t / a.rows_per_gate : 0) * a.sg : nullptr;
+        // a wait that runs out is recorded; the block then goes through its rows without data
+        tc::mbar_wait(ring.bars + 8 * slot, parity, &stop, 5);
+        Raw8 fr[NV];
+        float y[NV][8], ss = 0.f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (i * NT + (int)threadIdx.x) * 8;
+            fr[i] = Raw8{};
+#pragma unroll
+            for (int j = 0; j < 8; ++j) y[i][j] = 0.f;
+            if (c < a.H) {
+                fr[i] = ring_raw(stage, 0, c);
+                widen(ring_raw(stage, row_bytes, c), y[i]);
+            }
+            float f[8];
+            widen(fr[i], f);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) ss += f[j] * f[j];
+        }
+        const float r1 = rsqrtf(block_sum<NT>(ss, sh[0]) * inv_h + a.eps);
+        // every thread has read the stage
+        if (threadIdx.x == 0 && t + (int64_t)stages * gridDim.x < a.T) {
+            tc::fence_async();
+            ring.load(t + (int64_t)stages * gridDim.x, slot);
+        }
+        if (KEEP) {
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const int c = (i * NT + (int)threadIdx.x) * 8;
+                int e;
+                const uint2 b = pack8(fr[i], e);
+                if (c < a.H) {
+                    *reinterpret_cast<uint2 *>(a.kf.q + t * a.kf.sq + c) = b;
+                    if ((threadIdx.x & 7) == 0) a.kf.e[t * a.kf.se + c / kBlock] = (int8_t)e;
+                }
+            }
+        }
+        ss = 0.f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (i * NT + (int)threadIdx.x) * 8, at = c < a.H ? c : 0;
+            float w[8], f[8];
+            load8_bf16<true>(a.w_post + at, 8, w);
+            if (g) {
+                load8_bf16<true>(g + at, 8, f);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) w[j] *= f[j];
+            }
+            widen(fr[i], f);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                y[i][j] = a.alpha * y[i][j] + w[j] * (f[j] * r1);
+                ss += y[i][j] * y[i][j];
+            }
+            const Raw8 yr = narrow(y[i]);
+            if (c < a.H) store8<true>(a.y + t * a.sy + c, 8, yr);
+            if (KEEP) {
+                int e;
+                const uint2 b = pack8(yr, e);  // y as its next reader sees it
+                if (c < a.H) {
+                    *reinterpret_cast<uint2 *>(a.ky.q + t * a.ky.sq + c) = b;
+                    if ((threadIdx.x & 7) == 0) a.ky.e[t * a.ky.se + c / kBlock] = (int8_t)e;
+                }
+            }
+        }
+        const float r2 = rsqrtf(block_sum<NT>(ss, sh[1]) * inv_h + a.eps);
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (i * NT + (int)threadIdx.x) * 8;
+            if (c < a.H) {
+                float w[8];
+                load8_bf16<true>(a.w_pre + c, 8, w);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) w[j] *= y[i][j] * r2;
+                store8_bf16<true>(a.h + t * a.sh + c, 8, w);
+            }
+        }
+        if (threadIdx.x == 0) {
+            a.rstd_post[t] = r1;
+            a.rstd_pre[t] = r2;
+        }
+        if (++slot == stages) slot = 0, parity ^= 1;
+    }
+}
+
+template <int NT, int NV, bool PACKED>
+__global__ void __launch_bounds__(NT, 512 / NT) k_join_backward_ring(const JoinBackward a, const int stages) {
+    extern __shared__ __align__(128) unsigned char smem[];
+    __shared__ float sh[2][32];
+    __shared__ int stop;
+    const uint32_t wide = 2u * a.H, saved = PACKED ? (uint32_t)a.H : wide, at_dy = wide + 2 * saved;
+    Ring<4> ring{tc::smem_u32(smem) + kRingHeader, tc::smem_u32(smem), at_dy + (a.dy ? wide : 0), stages,
+                 {{(const unsigned char *)a.dh, 2 * a.sdh, wide, 0},
+                  {PACKED ? (const unsigned char *)a.ky.q : (const unsigned char *)a.y, PACKED ? a.ky.sq : 2 * a.sy, saved, wide},
+                  {PACKED ? (const unsigned char *)a.kf.q : (const unsigned char *)a.f, PACKED ? a.kf.sq : 2 * a.sf, saved,
+                   wide + saved},
+                  {(const unsigned char *)a.dy, 2 * a.sdy, a.dy ? wide : 0, at_dy}}};
+    const float inv_h = 1.f / (float)a.H;
+    const int64_t group = blockIdx.x / a.it.per_group, part = blockIdx.x % a.it.per_group;
+    const int64_t first = group * a.it.rows_per_gate + part * a.it.rows;
+    int64_t last = min(first + a.it.rows, (group + 1) * a.it.rows_per_gate);
+    last = min(last, a.T);
+    if (threadIdx.x == 0) {
+        stop = 0;
+        for (int i = 0; i < stages; ++i) tc::mbar_init(ring.bars + 8 * i, 1);
+        tc::fence_barrier_init();
+        for (int i = 0; i < stages; ++i)
+            if (first + i < last) ring.load(first + i, i);
+    }
+    // the weights of this thread's columns stay in registers: the item has one gate row
+    Raw8 w_pre[NV];
+    float gw[NV][8], sum_pre[NV][8] = {}, sum_post[NV][8] = {};
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int c = (i * NT + (int)threadIdx.x) * 8, left = a.H - c, at = left > 0 ? c : 0;
+        w_pre[i] = load8<true>(a.w_pre + at, left);
+        load8_bf16<true>(a.w_post + at, left, gw[i]);
+        if (a.gate) {
+            float u[8];
+            load8_bf16<true>(a.gate + group * a.sg + at, left, u);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) gw[i][j] *= u[j];
+        }
+    }
+    // what is read beside the ring is read a row ahead
+    float r1 = 0.f, r2 = 0.f, next1 = 0.f, next2 = 0.f;
+    int ey[NV] = {}, ef[NV] = {};
+    const auto ahead = [&](int64_t t) {
+        next1 = a.rstd_post[t], next2 = a.rstd_pre[t];
+        if (PACKED) {
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const int c = (i * NT + (int)threadIdx.x) * 8, b = (c < a.H ? c : 0) / kBlock;
+                ey[i] = a.ky.e[t * a.ky.se + b], ef[i] = a.kf.e[t * a.kf.se + b];
+            }
+        }
+    };
+    if (first < last) ahead(first);
+    __syncthreads();
+    int slot = 0;
+    uint32_t parity = 0;
+    for (int64_t t = first; t < last; ++t) {
+        const unsigned char *stage = smem + kRingHeader + slot * ring.stage_bytes;
+        float step_y[NV], step_f[NV];
+        r1 = next1, r2 = next2;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            step_y[i] = PACKED ? step_of(ey[i]) * r2 : r2;
+            step_f[i] = PACKED ? step_of(ef[i]) * r1 : r1;
+        }
+        if (t + 1 < last) ahead(t + 1);
+        tc::mbar_wait(ring.bars + 8 * slot, parity, &stop, 6);
+        const auto norm = [&](uint32_t at, int c, float step, float (&n)[8]) {
+            if (PACKED) {
+                unpack8(*reinterpret_cast<const uint2 *>(stage + at + c), step, n);
+            } else {
+                widen(ring_raw(stage, at, c), n);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) n[j] *= step;
+            }
+        };
+        float n2[NV][8], d[NV][8], ss = 0.f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (i * NT + (int)threadIdx.x) * 8;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) n2[i][j] = d[i][j] = 0.f;
+            if (c < a.H) {
+                float w[8];
+                norm(wide, c, step_y[i], n2[i]);
+                widen(ring_raw(stage, 0, c), d[i]);
+                widen(w_pre[i], w);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    sum_pre[i][j] += d[i][j] * n2[i][j];
+                    d[i][j] *= w[j];
+                    ss += d[i][j] * n2[i][j];
+                }
+            }
+        }
+        const float m2 = block_sum<NT>(ss, sh[0]) * inv_h;
+        float n1[NV][8];
+        ss = 0.f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (i * NT + (int)threadIdx.x) * 8;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) n1[i][j] = 0.f;
+            if (c < a.H) {
+                float u[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) d[i][j] = r2 * (d[i][j] - n2[i][j] * m2);
+                if (a.dy) {
+                    widen(ring_raw(stage, at_dy, c), u);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) d[i][j] += u[j];
+                }
+#pragma unroll
+                for (int j = 0; j < 8; ++j) u[j] = a.alpha * d[i][j];
+                store8_bf16<true>(a.dx + t * a.sdx + c, 8, u);
+                norm(wide + saved, c, step_f[i], n1[i]);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    sum_post[i][j] += d[i][j] * n1[i][j];
+                    d[i][j] *= gw[i][j];
+                    ss += d[i][j] * n1[i][j];
+                }
+            }
+        }
+        const float m1 = block_sum<NT>(ss, sh[1]) * inv_h;
+        // every thread has read the stage
+        if (threadIdx.x == 0 && t + stages < last) {
+            tc::fence_async();
+            ring.load(t + stages, slot);
+        }
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (i * NT + (int)threadIdx.x) * 8;
+            if (c < a.H) {
+                float u[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) u[j] = r1 * (d[i][j] - n1[i][j] * m1);
+                store8_bf16<true>(a.df + t * a.sdf + c, 8, u);
+            }
+        }
+        if (++slot == stages) slot = 0, parity ^= 1;
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int c = (i * NT + (int)threadIdx.x) * 8;
+        if (c < a.H) {
+            float *p = a.part_pre + blockIdx.x * (int64_t)a.H + c, *q = a.part_post + blockIdx.x * (int64_t)a.H + c;
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                reinterpret_cast<float4 *>(p)[j] =
+                    make_float4(sum_pre[i][4 * j], sum_pre[i][4 * j + 1], sum_pre[i][4 * j + 2], sum_pre[i][4 * j + 3]);
+                reinterpret_cast<float4 *>(q)[j] =
+                    make_float4(sum_post[i][4 * j], sum_post[i][4 * j + 1], sum_post[i][4 * j + 2], sum_post[i][4 * j + 3]);
+            }
+        }
+    }
+}
+
+// Blocks on an SM and stages that each has.
+struct RingPlan {
+    int threads, blocks, stages;
+    size_t smem;
+};
+RingPlan ring_plan(int64_t H, int64_t stage_bytes, int threads_on_sm) {
+    RingPlan p{ring_threads(H), 0, 0, 0};
+    if (!p.threads) return p;
+    p.blocks = threads_on_sm / p.threads;
+    const int64_t each = 220 * 1024 / p.blocks - 1024 - kRingHeader;
+    p.stages = (int)(each / stage_bytes < kMaxStages ? each / stage_bytes : kMaxStages);
+    if (p.stages < 2) p.threads = 0;
+    p.smem = kRingHeader + p.stages * stage_bytes;
+    return p;
+}
+
 // Column sums of the items' parts, in a fixed order: blockIdx.y = 0 joins all
 // items (the part of the norm after the block weighted by its group's gate), the
 // others a gate group each.
@@ -313,6 +636,35 @@ void backward_by_width(const JoinBackward &a, cudaStream_t s) {
     else k_join_backward<1024, 2, VEC, PACKED><<<grid, 1024, 0, s>>>(a);
 }
 
+template <class K, class A>
+int launch_ring(K kernel, const A &a, const RingPlan &p, unsigned grid, std::atomic<uint64_t> &ready, cudaStream_t s) {
+    const int rc = allow_smem(kernel, 226 * 1024, ready);
+    if (rc != PP_OK) return rc;
+    kernel<<<grid, p.threads, p.smem, s>>>(a, p.stages);
+    return PP_OK;
+}
+
+template <bool KEEP>
+int forward_ring(const JoinForward &a, const RingPlan &p, cudaStream_t s) {
+    static std::atomic<uint64_t> ready[4];
+    const int64_t most = (int64_t)sm_count() * p.blocks;
+    const unsigned grid = (unsigned)(a.T < most ? a.T : most);
+    if (a.H <= 1024) return launch_ring(k_join_forward_ring<128, 1, KEEP>, a, p, grid, ready[0], s);
+    if (a.H <= 2048) return launch_ring(k_join_forward_ring<128, 2, KEEP>, a, p, grid, ready[1], s);
+    if (a.H <= 4096) return launch_ring(k_join_forward_ring<256, 2, KEEP>, a, p, grid, ready[2], s);
+    return launch_ring(k_join_forward_ring<512, 2, KEEP>, a, p, grid, ready[3], s);
+}
+
+template <bool PACKED>
+int backward_ring(const JoinBackward &a, const RingPlan &p, cudaStream_t s) {
+    static std::atomic<uint64_t> ready[4];
+    const unsigned grid = (unsigned)a.it.count;
+    if (a.H <= 1024) return launch_ring(k_join_backward_ring<128, 1, PACKED>, a, p, grid, ready[0], s);
+    if (a.H <= 2048) return launch_ring(k_join_backward_ring<128, 2, PACKED>, a, p, grid, ready[1], s);
+    if (a.H <= 4096) return launch_ring(k_join_backward_ring<256, 2, PACKED>, a, p, grid, ready[2], s);
+    return launch_ring(k_join_backward_ring<512, 2, PACKED>, a, p, grid, ready[3], s);
+}
+
 int check_join(int64_t T, int64_t H) {
     if (T < 0 || H < 1) return PP_ERR_ARG;
     if (T > PP_STAGE_MAX_ROWS || H > PP_STAGE_MAX_JOIN_WIDTH) return PP_ERR_SIZE;
@@ -362,6 +714,14 @@ extern "C" int pp_stage_join_forward(const uint16_t *x, int64_t stride_x, const 
                      rows_aligned(w_post, H, 1, 2) && rows_aligned(w_pre, H, 1, 2) && rows_aligned(y, stride_y, T, 2) &&
                      rows_aligned(h, stride_h, T, 2) && (!gate || rows_aligned(gate, stride_gate, 2, 2)) &&
                      (!keep || (kept_aligned(y_q, stride_yq, T) && kept_aligned(f_q, stride_fq, T)));
+    // the ring pays from about two rows a block on
+    const RingPlan p = ring_plan(H, 4 * H, 1024);
+    if (vec && p.threads && H % 8 == 0 && T >= 2 * (int64_t)sm_count() * p.blocks) {
+        const int rr = keep ? forward_ring<true>(a, p, stream) : forward_ring<false>(a, p, stream);
+        if (rr != PP_OK) return rr;
+        PPS_CUDA_TRY(cudaGetLastError());
+        return PP_OK;
+    }
     const unsigned grid = (unsigned)(T < 152 * 16 ? T : 152 * 16);
     if (vec) keep ? forward_by_width<true, true>(a, grid, stream) : forward_by_width<true, false>(a, grid, stream);
     else keep ? forward_by_width<false, true>(a, grid, stream) : forward_by_width<false, false>(a, grid, stream);
@@ -371,7 +731,7 @@ extern "C" int pp_stage_join_forward(const uint16_t *x, int64_t stride_x, const 
 
 extern "C" size_t pp_stage_join_backward_workspace(int64_t T, int64_t H, int64_t rows_per_gate) {
     if (T < 1 || H < 1) return 0;
-    return back_space(nullptr, items_of(T, rows_per_gate), H).bytes;
+    return back_space(nullptr, items_of(T, H, rows_per_gate), H).bytes;
 }
 
 extern "C" int pp_stage_join_backward(const uint16_t *dh, int64_t stride_dh, const uint16_t *dy, int64_t stride_dy,
@@ -395,7 +755,7 @@ extern "C" int pp_stage_join_backward(const uint16_t *dh, int64_t stride_dh, con
         return PP_OK;
     }
     const bool packed = y_q || y_e || f_q || f_e;
-    const Items it = items_of(T, rows_per_gate);
+    const Items it = items_of(T, H, rows_per_gate);
     const BackSpace s = back_space(workspace, it, H);
     JoinBackward a{dh, dy, y, f, w_post, w_pre, gate, stride_dh, stride_dy, stride_y, stride_f, stride_gate,
                    Kept{const_cast<int8_t *>(y_q), const_cast<int8_t *>(y_e), stride_yq, stride_ye},
@@ -415,7 +775,14 @@ extern "C" int pp_stage_join_backward(const uint16_t *dh, int64_t stride_dh, con
                      rows_aligned(df, stride_df, T, 2) &&
                      (packed ? kept_aligned(y_q, stride_yq, T) && kept_aligned(f_q, stride_fq, T)
                              : rows_aligned(y, stride_y, T, 2) && rows_aligned(f, stride_f, T, 2));
-    if (vec) packed ? backward_by_width<true, true>(a, stream) : backward_by_width<true, false>(a, stream);
+    const RingPlan p = ring_plan(H, (dy ? 4 : 2) * H + (packed ? 2 : 4) * H, 512);
+    // bulk copies take whole 16 bytes
+    const bool whole = packed ? H % 16 == 0 && rows_aligned(y_q, stride_yq, T, 1) && rows_aligned(f_q, stride_fq, T, 1)
+                              : H % 8 == 0;
+    if (vec && whole && p.threads && it.rows >= 2) {
+        const int rr = packed ? backward_ring<true>(a, p, stream) : backward_ring<false>(a, p, stream);
+        if (rr != PP_OK) return rr;
+    } else if (vec) packed ? backward_by_width<true, true>(a, stream) : backward_by_width<true, false>(a, stream);
     else packed ? backward_by_width<false, true>(a, stream) : backward_by_width<false, false>(a, stream);
     PPS_CUDA_TRY(cudaGetLastError());
     const dim3 grid((unsigned)ceil_div(H, 32), 1 + (gate ? (unsigned)(it.groups < 1024 ? it.groups : 1024) : 0));

@@ -6,41 +6,63 @@
 namespace pps {
 namespace {
 
-// 8 lanes per block of 64 columns, 8 columns each.
-template <bool VEC>
-__global__ void __launch_bounds__(256) k_pack(const uint16_t *x, int64_t stride_x, int64_t T, int64_t H, int8_t *q,
-                                              int64_t stride_q, int8_t *e, int64_t stride_e) {
-    const int64_t nb = (H + kBlock - 1) / kBlock, units = T * nb * 8;
-    const int64_t step = (int64_t)gridDim.x * blockDim.x;
-    // whole warps go on together: pack8 shuffles
-    for (int64_t u = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; u - (threadIdx.x & 31) < units; u += step) {
-        const int64_t t = u / (nb * 8), c = u % (nb * 8) * 8;
-        const int64_t left = u < units ? H - c : 0;
-        float v[8];
-        load8_bf16<VEC>(x + (left > 0 ? t * stride_x + c : 0), left, v);
+// Each thread takes kUnits units of 8 columns, a block of threads apart, and
+// has all their loads in flight at once: the kernels are one pass over memory.
+// Units are counted in 32 bits where that is enough (I), for the division.
+constexpr int kUnits = 4, kThreads = 256;
+constexpr int64_t kManyUnits = 1ll << 31;  // from here on 64 bits
+
+// 8 lanes to a block of 64 columns.
+template <bool VEC, class I>
+__global__ void __launch_bounds__(kThreads) k_pack(const uint16_t *x, int64_t stride_x, int64_t T, int64_t H, int8_t *q,
+                                                   int64_t stride_q, int8_t *e, int64_t stride_e) {
+    const I per = (I)((H + kBlock - 1) / kBlock * 8), units = (I)T * per;
+    const I first = (I)blockIdx.x * (kThreads * kUnits) + threadIdx.x;
+    Raw8 r[kUnits];
+#pragma unroll
+    for (int i = 0; i < kUnits; ++i) {
+        const I u = first + i * kThreads, t = u / per;
+        const int64_t c = (int64_t)(u - t * per) * 8, left = u < units ? H - c : 0;
+        r[i] = load8<VEC>(x + (left > 0 ? (int64_t)t * stride_x + c : 0), left);
+    }
+#pragma unroll
+    for (int i = 0; i < kUnits; ++i) {
+        const I u = first + i * kThreads, t = u / per;
+        const int64_t c = (int64_t)(u - t * per) * 8, left = u < units ? H - c : 0;
         int ex;
-        const uint2 b = pack8(v, ex);
-        if (left > 0) store8_bytes<VEC>(q + t * stride_q + c, left, b);
-        if (u < units && (u & 7) == 0) e[t * stride_e + c / kBlock] = (int8_t)ex;
+        const uint2 b = pack8(r[i], ex);
+        if (left > 0) store8_bytes<VEC>(q + (int64_t)t * stride_q + c, left, b);
+        if (u < units && (u & 7) == 0) e[(int64_t)t * stride_e + c / kBlock] = (int8_t)ex;
     }
 }
 
-template <bool VEC>
-__global__ void __launch_bounds__(256) k_unpack(const int8_t *q, int64_t stride_q, const int8_t *e, int64_t stride_e,
-                                                int64_t T, int64_t H, uint16_t *x, int64_t stride_x) {
-    const int64_t per = (H + 7) / 8, units = T * per;
-    const int64_t step = (int64_t)gridDim.x * blockDim.x;
-    for (int64_t u = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; u < units; u += step) {
-        const int64_t t = u / per, c = u % per * 8;
-        float v[8];
-        unpack8(load8_bytes<VEC>(q + t * stride_q + c, H - c), e[t * stride_e + c / kBlock], v);
-        store8_bf16<VEC>(x + t * stride_x + c, H - c, v);
+template <bool VEC, class I>
+__global__ void __launch_bounds__(kThreads) k_unpack(const int8_t *q, int64_t stride_q, const int8_t *e,
+                                                     int64_t stride_e, int64_t T, int64_t H, uint16_t *x,
+                                                     int64_t stride_x) {
+    const I per = (I)((H + 7) / 8), units = (I)T * per;
+    const I first = (I)blockIdx.x * (kThreads * kUnits) + threadIdx.x;
+    uint2 b[kUnits];
+    int ex[kUnits];
+#pragma unroll
+    for (int i = 0; i < kUnits; ++i) {
+        const I u = first + i * kThreads, t = u / per;
+        const int64_t c = (int64_t)(u - t * per) * 8;
+        if (u < units) {
+            b[i] = load8_bytes<VEC>(q + (int64_t)t * stride_q + c, H - c);
+            ex[i] = e[(int64_t)t * stride_e + c / kBlock];
+        }
     }
-}
-
-unsigned grid_for(int64_t threads) {
-    const int64_t b = ceil_div(threads, 256);
-    return (unsigned)(b < 1 ? 1 : b > 152 * 64 ? 152 * 64 : b);
+#pragma unroll
+    for (int i = 0; i < kUnits; ++i) {
+        const I u = first + i * kThreads, t = u / per;
+        const int64_t c = (int64_t)(u - t * per) * 8;
+        if (u < units) {
+            float v[8];
+            unpack8(b[i], step_of(ex[i]), v);
+            store8_bf16<VEC>(x + (int64_t)t * stride_x + c, H - c, v);
+        }
+    }
 }
 
 struct WgradEpi {
@@ -92,11 +114,13 @@ WgradSpace wgrad_space(void *ws, const uint16_t *dy, int64_t stride_dy, int64_t 
 
 int launch_unpack(const int8_t *q, int64_t stride_q, const int8_t *e, int64_t stride_e, int64_t T, int64_t H,
                   uint16_t *x, int64_t stride_x, cudaStream_t stream) {
-    const unsigned grid = grid_for(T * ceil_div(H, 8));
-    if (rows_aligned(x, stride_x, T, 2) && kept_aligned(q, stride_q, T))
-        k_unpack<true><<<grid, 256, 0, stream>>>(q, stride_q, e, stride_e, T, H, x, stride_x);
-    else
-        k_unpack<false><<<grid, 256, 0, stream>>>(q, stride_q, e, stride_e, T, H, x, stride_x);
+    const int64_t units = T * ceil_div(H, 8), grid = ceil_div(units, kThreads * kUnits);
+    const bool vec = rows_aligned(x, stride_x, T, 2) && kept_aligned(q, stride_q, T);
+    const auto go = [&](auto kernel) {
+        kernel<<<(unsigned)grid, kThreads, 0, stream>>>(q, stride_q, e, stride_e, T, H, x, stride_x);
+    };
+    if (units < kManyUnits) vec ? go(k_unpack<true, uint32_t>) : go(k_unpack<false, uint32_t>);
+    else vec ? go(k_unpack<true, int64_t>) : go(k_unpack<false, int64_t>);
     PPS_CUDA_TRY(cudaGetLastError());
     return PP_OK;
 }
@@ -117,11 +141,13 @@ extern "C" int pp_stage_pack(const uint16_t *x, int64_t stride_x, int64_t T, int
     if (rc != PP_OK) return rc;
     if (T == 0) return PP_OK;
     if (!x || ((uintptr_t)x & 1) || stride_x < H || bad_kept(q, stride_q, e, stride_e, H)) return PP_ERR_ARG;
-    const unsigned grid = grid_for(T * ceil_div(H, kBlock) * 8);
-    if (rows_aligned(x, stride_x, T, 2) && kept_aligned(q, stride_q, T))
-        k_pack<true><<<grid, 256, 0, stream>>>(x, stride_x, T, H, q, stride_q, e, stride_e);
-    else
-        k_pack<false><<<grid, 256, 0, stream>>>(x, stride_x, T, H, q, stride_q, e, stride_e);
+    const int64_t units = T * ceil_div(H, kBlock) * 8, grid = ceil_div(units, kThreads * kUnits);
+    const bool vec = rows_aligned(x, stride_x, T, 2) && kept_aligned(q, stride_q, T);
+    const auto go = [&](auto kernel) {
+        kernel<<<(unsigned)grid, kThreads, 0, stream>>>(x, stride_x, T, H, q, stride_q, e, stride_e);
+    };
+    if (units < kManyUnits) vec ? go(k_pack<true, uint32_t>) : go(k_pack<false, uint32_t>);
+    else vec ? go(k_pack<true, int64_t>) : go(k_pack<false, int64_t>);
     PPS_CUDA_TRY(cudaGetLastError());
     return PP_OK;
 }

@@ -9,6 +9,8 @@
 // number: the backward pass multiplies exactly what was kept.
 #pragma once
 
+#include <cstring>
+
 #include "stage_common.cuh"
 
 namespace pps {
@@ -29,64 +31,100 @@ __device__ __forceinline__ int block_exp(uint32_t amax_bits) {
     return e < kMinExp ? kMinExp : e;
 }
 
-// q of one value given 2^-e (0 for a non-finite block).
-__device__ __forceinline__ int quantize(float x, float inv) {
-    const float r = fminf(fmaxf(rintf(x * inv), -127.f), 127.f);
-    return inv == 0.f ? 0 : (int)r;
+__device__ __forceinline__ float inv_step(int e) { return two_to(-e); }
+__device__ __forceinline__ float step_of(int e) { return e == kNonfinite ? __uint_as_float(0x7FC00000u) : two_to(e); }
+
+// 8 consecutive bf16 elements of a row, two to a word.
+struct Raw8 {
+    uint32_t w[4];
+};
+__device__ __forceinline__ void widen(const Raw8 &r, float (&v)[8]) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[2 * j] = bf16_lo(r.w[j]), v[2 * j + 1] = bf16_hi(r.w[j]);
+}
+__device__ __forceinline__ Raw8 narrow(const float (&v)[8]) {
+    Raw8 r;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) r.w[j] = f32_to_bf16x2(v[2 * j], v[2 * j + 1]);
+    return r;
 }
 
-__device__ __forceinline__ float inv_step(int e) { return e == kNonfinite ? 0.f : two_to(-e); }
-__device__ __forceinline__ float step_of(int e) { return e == kNonfinite ? __uint_as_float(0x7FC00000u) : two_to(e); }
+__device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {  // NaN wins
+    __nv_bfloat162 x, y;
+    memcpy(&x, &a, 4);
+    memcpy(&y, &b, 4);
+    const __nv_bfloat162 m = __hmax2_nan(x, y);
+    uint32_t r;
+    memcpy(&r, &m, 4);
+    return r;
+}
 
 // Packs the 8 consecutive columns that this lane holds; the 8 lanes of an
 // aligned group of 8 hold one block (columns past the row's end are 0).
 // Returns the 8 bytes and the exponent (the same in all 8 lanes).
-__device__ __forceinline__ uint2 pack8(const float (&v)[8], int &e) {
-    uint32_t a = 0;
+__device__ __forceinline__ uint2 pack8(const Raw8 &x, int &e) {
+    uint32_t a = x.w[0] & 0x7FFF7FFFu;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) a = max(a, __float_as_uint(v[j]) & 0x7FFFFFFFu);
+    for (int j = 1; j < 4; ++j) a = max_bf16x2(a, x.w[j] & 0x7FFF7FFFu);
 #pragma unroll
-    for (int o = 4; o; o >>= 1) a = max(a, __shfl_xor_sync(~0u, a, o));
-    e = block_exp(a);
-    const float inv = inv_step(e);
-    uint32_t w[2] = {0, 0};
-#pragma unroll
-    for (int j = 0; j < 8; ++j) w[j >> 2] |= (uint32_t)(quantize(v[j], inv) & 0xFF) << (8 * (j & 3));
-    return make_uint2(w[0], w[1]);
-}
-
-// The 8 values that 8 bytes stand for.
-__device__ __forceinline__ void unpack8(uint2 b, int e, float (&v)[8]) {
-    const float step = step_of(e);
+    for (int o = 4; o; o >>= 1) a = max_bf16x2(a, __shfl_xor_sync(~0u, a, o));
+    e = block_exp(max(a << 16, a & 0xFFFF0000u));
+    // x / 2^e is exact, so that adding 1.5 * 2^23 rounds it to a whole number
+    // (ties to even) that lies in the sum's low bits
+    const float inv = e == kNonfinite ? 0.f : inv_step(e);
+    constexpr float kRound = 12582912.f;
+    uint32_t b[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-        const uint32_t w = j < 4 ? b.x : b.y;
-        v[j] = (float)(int8_t)(w >> (8 * (j & 3))) * step;
+        const float v = j & 1 ? bf16_hi(x.w[j >> 1]) : bf16_lo(x.w[j >> 1]);
+        b[j] = __float_as_uint(fminf(fmaxf(fmaf(v, inv, kRound), kRound - 127.f), kRound + 127.f));
+    }
+    if (e == kNonfinite) return make_uint2(0u, 0u);
+    return make_uint2(__byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410),
+                      __byte_perm(__byte_perm(b[4], b[5], 0x0040), __byte_perm(b[6], b[7], 0x0040), 0x5410));
+}
+
+// The 8 values that 8 bytes stand for, times `step`: a byte with its sign bit
+// flipped becomes the low bits of 2^23, from which 2^23 + 128 is taken.
+__device__ __forceinline__ void unpack8(uint2 b, float step, float (&v)[8]) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const uint32_t w = (j < 4 ? b.x : b.y) ^ 0x80808080u;
+        v[j] = (__uint_as_float(__byte_perm(w, 0x4B000000u, 0x7440 + (j & 3))) - 8388736.f) * step;
     }
 }
 
 // 8 consecutive elements at p, of which `left` exist (all 8 in the vector form).
 template <bool VEC>
-__device__ __forceinline__ void load8_bf16(const uint16_t *p, int64_t left, float (&v)[8]) {
+__device__ __forceinline__ Raw8 load8(const uint16_t *p, int64_t left) {
+    Raw8 r;
     if (VEC && left >= 8) {
         const uint4 w = *reinterpret_cast<const uint4 *>(p);
-        v[0] = bf16_lo(w.x), v[1] = bf16_hi(w.x), v[2] = bf16_lo(w.y), v[3] = bf16_hi(w.y);
-        v[4] = bf16_lo(w.z), v[5] = bf16_hi(w.z), v[6] = bf16_lo(w.w), v[7] = bf16_hi(w.w);
+        r.w[0] = w.x, r.w[1] = w.y, r.w[2] = w.z, r.w[3] = w.w;
     } else {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = j < left ? bf16_to_f32(p[j]) : 0.f;
+        for (int j = 0; j < 4; ++j)
+            r.w[j] = (2 * j < left ? (uint32_t)p[2 * j] : 0u) | (2 * j + 1 < left ? (uint32_t)p[2 * j + 1] : 0u) << 16;
     }
+    return r;
 }
 template <bool VEC>
-__device__ __forceinline__ void store8_bf16(uint16_t *p, int64_t left, const float (&v)[8]) {
+__device__ __forceinline__ void store8(uint16_t *p, int64_t left, const Raw8 &r) {
     if (VEC && left >= 8) {
-        *reinterpret_cast<uint4 *>(p) = make_uint4(f32_to_bf16x2(v[0], v[1]), f32_to_bf16x2(v[2], v[3]),
-                                                   f32_to_bf16x2(v[4], v[5]), f32_to_bf16x2(v[6], v[7]));
+        *reinterpret_cast<uint4 *>(p) = make_uint4(r.w[0], r.w[1], r.w[2], r.w[3]);
     } else {
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-            if (j < left) p[j] = f32_to_bf16(v[j]);
+            if (j < left) p[j] = (uint16_t)(r.w[j >> 1] >> (16 * (j & 1)));
     }
+}
+template <bool VEC>
+__device__ __forceinline__ void load8_bf16(const uint16_t *p, int64_t left, float (&v)[8]) {
+    widen(load8<VEC>(p, left), v);
+}
+template <bool VEC>
+__device__ __forceinline__ void store8_bf16(uint16_t *p, int64_t left, const float (&v)[8]) {
+    store8<VEC>(p, left, narrow(v));
 }
 template <bool VEC>
 __device__ __forceinline__ uint2 load8_bytes(const int8_t *p, int64_t left) {

@@ -16,8 +16,6 @@
 // forms use the 128-byte swizzle.
 #pragma once
 
-#include <atomic>
-
 #include "stage_common.cuh"
 #include "stage_tc.cuh"
 
@@ -206,7 +204,6 @@ __global__ void __launch_bounds__(kProductThreads, 1)
 // One map of a row-major matrix for boxes of box_rows x box_inner elements.
 int encode_map(CUtensorMap *map, const void *base, int64_t inner, int64_t rows, int64_t ld, int box_inner,
                int box_rows);
-int sm_count();
 
 // Parts of K that give every SM a tile where there are few tiles: each part
 // has at least 4 slices.
@@ -227,14 +224,9 @@ int launch_product(const Operand &A, const Operand &B, int64_t M, int64_t N, int
     if (rc == PP_OK)
         rc = B_MN ? encode_map(&mb, B.p, N, K, B.ld, 64, kTileK) : encode_map(&mb, B.p, K, N, B.ld, kTileK, kTileN);
     if (rc != PP_OK) return rc;
-    static std::atomic<uint64_t> ready{0};  // devices on which the kernel's shared memory is set
-    int dev = 0;
-    PPS_CUDA_TRY(cudaGetDevice(&dev));
-    if (dev > 63 || !(ready.load(std::memory_order_relaxed) >> dev & 1)) {
-        PPS_CUDA_TRY(cudaFuncSetAttribute(k_product<Epi, A_MN, B_MN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                          kProductSmem));
-        if (dev <= 63) ready.fetch_or(1ull << dev, std::memory_order_relaxed);
-    }
+    static std::atomic<uint64_t> ready{0};
+    const int ra = allow_smem(k_product<Epi, A_MN, B_MN>, kProductSmem, ready);
+    if (ra != PP_OK) return ra;
     ProductShape s;
     s.M = (int)M, s.N = (int)N, s.K = (int)K;
     s.mt = (int)ceil_div(M, kTileM), s.nt = (int)ceil_div(N, kTileN);

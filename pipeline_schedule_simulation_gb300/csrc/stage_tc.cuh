@@ -90,6 +90,15 @@ __device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap *map, i
         "l"(map), "r"(x), "r"(y), "r"(bar)
         : "memory");
 }
+// `bytes` consecutive bytes (both addresses and the size multiples of 16).
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+                 "l"(src), "r"(bytes), "r"(bar)
+                 : "memory");
+}
+// Reads of shared memory made before this are done before later asynchronous
+// copies write there.
+__device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 __device__ __forceinline__ void prefetch_map(const CUtensorMap *map) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
 }
