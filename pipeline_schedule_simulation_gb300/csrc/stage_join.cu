@@ -24,12 +24,14 @@ template <int NT>
 __device__ __forceinline__ float block_sum(float v, float *sh) {
 #pragma unroll
     for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(~0u, v, o);
-    if (NT == 32) return v;
     if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = v;
     __syncthreads();
     float s = 0.f;
 #pragma unroll
-    for (int i = 0; i < NT / 32; ++i) s += sh[i];
+    for (int i = 0; i < NT / 128; ++i) {
+        const float4 p = reinterpret_cast<const float4 *>(sh)[i];
+        s += (p.x + p.y) + (p.z + p.w);
+    }
     return s;
 }
 
@@ -53,7 +55,7 @@ struct JoinForward {
 // NT threads hold NV vectors of 8 columns each: H <= 8 * NT * NV.
 template <int NT, int NV, bool VEC, bool KEEP>
 __global__ void __launch_bounds__(NT) k_join_forward(const JoinForward a) {
-    __shared__ float sh[2][32];
+    __shared__ __align__(16) float sh[2][32];
     const float inv_h = 1.f / (float)a.H;
     for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
         const uint16_t *g = a.gate ? a.gate + (a.rows_per_gate > 0 ? t / a.rows_per_gate : 0) * a.sg : nullptr;
@@ -180,7 +182,7 @@ __device__ __forceinline__ void load_saved(const uint16_t *p, int64_t s, const K
 
 template <int NT, int NV, bool VEC, bool PACKED>
 __global__ void __launch_bounds__(NT) k_join_backward(const JoinBackward a) {
-    __shared__ float sh[2][32];
+    __shared__ __align__(16) float sh[2][32];
     const float inv_h = 1.f / (float)a.H;
     const int64_t group = blockIdx.x / a.it.per_group, part = blockIdx.x % a.it.per_group;
     const int64_t first = group * a.it.rows_per_gate + part * a.it.rows;
@@ -294,7 +296,7 @@ __device__ __forceinline__ Raw8 ring_raw(const unsigned char *stage, uint32_t at
 template <int NT, int NV, bool KEEP>
 __global__ void __launch_bounds__(NT, 1024 / NT) k_join_forward_ring(const JoinForward a, const int stages) {
     extern __shared__ __align__(128) unsigned char smem[];
-    __shared__ float sh[2][32];
+    __shared__ __align__(16) float sh[2][32];
     __shared__ int stop;
     const uint32_t row_bytes = 2u * a.H;
     Ring<2> ring{tc::smem_u32(smem) + kRingHeader, tc::smem_u32(smem), 2 * row_bytes, stages,
@@ -310,6 +312,10 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_join_forward_ring(const JoinF
     __syncthreads();
     int slot = 0;
     uint32_t parity = 0;
+    const int c0 = (int)threadIdx.x * 8;
+    uint16_t *py = a.y + blockIdx.x * a.sy + c0, *ph = a.h + blockIdx.x * a.sh + c0;
+    int8_t *qf = a.kf.q + blockIdx.x * a.kf.sq + c0, *ef = a.kf.e + blockIdx.x * a.kf.se + c0 / kBlock;
+    int8_t *qy = a.ky.q + blockIdx.x * a.ky.sq + c0, *ey = a.ky.e + blockIdx.x * a.ky.se + c0 / kBlock;
     for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
         const unsigned char *stage = smem + kRingHeader + slot * ring.stage_bytes;
         const uint16_t *g = a.gate ? a.gate + (a.rows_per_gate > 0 ? t / a.rows_per_gate : 0) * a.sg : nullptr;
@@ -345,8 +351,8 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_join_forward_ring(const JoinF
                 int e;
                 const uint2 b = pack8(fr[i], e);
                 if (c < a.H) {
-                    *reinterpret_cast<uint2 *>(a.kf.q + t * a.kf.sq + c) = b;
-                    if ((threadIdx.x & 7) == 0) a.kf.e[t * a.kf.se + c / kBlock] = (int8_t)e;
+                    *reinterpret_cast<uint2 *>(qf + i * NT * 8) = b;
+                    if ((threadIdx.x & 7) == 0) ef[i * NT * 8 / kBlock] = (int8_t)e;
                 }
             }
         }
@@ -368,13 +374,13 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_join_forward_ring(const JoinF
                 ss += y[i][j] * y[i][j];
             }
             const Raw8 yr = narrow(y[i]);
-            if (c < a.H) store8<true>(a.y + t * a.sy + c, 8, yr);
+            if (c < a.H) store8<true>(py + i * NT * 8, 8, yr);
             if (KEEP) {
                 int e;
                 const uint2 b = pack8(yr, e);  // y as its next reader sees it
                 if (c < a.H) {
-                    *reinterpret_cast<uint2 *>(a.ky.q + t * a.ky.sq + c) = b;
-                    if ((threadIdx.x & 7) == 0) a.ky.e[t * a.ky.se + c / kBlock] = (int8_t)e;
+                    *reinterpret_cast<uint2 *>(qy + i * NT * 8) = b;
+                    if ((threadIdx.x & 7) == 0) ey[i * NT * 8 / kBlock] = (int8_t)e;
                 }
             }
         }
@@ -387,12 +393,17 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_join_forward_ring(const JoinF
                 load8_bf16<true>(a.w_pre + c, 8, w);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) w[j] *= y[i][j] * r2;
-                store8_bf16<true>(a.h + t * a.sh + c, 8, w);
+                store8_bf16<true>(ph + i * NT * 8, 8, w);
             }
         }
         if (threadIdx.x == 0) {
             a.rstd_post[t] = r1;
             a.rstd_pre[t] = r2;
+        }
+        py += gridDim.x * a.sy, ph += gridDim.x * a.sh;
+        if (KEEP) {
+            qf += gridDim.x * a.kf.sq, ef += gridDim.x * a.kf.se;
+            qy += gridDim.x * a.ky.sq, ey += gridDim.x * a.ky.se;
         }
         if (++slot == stages) slot = 0, parity ^= 1;
     }
@@ -401,7 +412,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_join_forward_ring(const JoinF
 template <int NT, int NV, bool PACKED>
 __global__ void __launch_bounds__(NT, 512 / NT) k_join_backward_ring(const JoinBackward a, const int stages) {
     extern __shared__ __align__(128) unsigned char smem[];
-    __shared__ float sh[2][32];
+    __shared__ __align__(16) float sh[2][32];
     __shared__ int stop;
     const uint32_t wide = 2u * a.H, saved = PACKED ? (uint32_t)a.H : wide, at_dy = wide + 2 * saved;
     Ring<4> ring{tc::smem_u32(smem) + kRingHeader, tc::smem_u32(smem), at_dy + (a.dy ? wide : 0), stages,
@@ -440,16 +451,18 @@ __global__ void __launch_bounds__(NT, 512 / NT) k_join_backward_ring(const JoinB
     // what is read beside the ring is read a row ahead
     float r1 = 0.f, r2 = 0.f, next1 = 0.f, next2 = 0.f;
     int ey[NV] = {}, ef[NV] = {};
+    const int c0 = (int)threadIdx.x * 8;
+    const int8_t *py = a.ky.e + first * a.ky.se + c0 / kBlock, *pf = a.kf.e + first * a.kf.se + c0 / kBlock;
     const auto ahead = [&](int64_t t) {
         next1 = a.rstd_post[t], next2 = a.rstd_pre[t];
         if (PACKED) {
 #pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                const int c = (i * NT + (int)threadIdx.x) * 8, b = (c < a.H ? c : 0) / kBlock;
-                ey[i] = a.ky.e[t * a.ky.se + b], ef[i] = a.kf.e[t * a.kf.se + b];
-            }
+            for (int i = 0; i < NV; ++i)
+                if (c0 + i * NT * 8 < a.H) ey[i] = py[i * NT * 8 / kBlock], ef[i] = pf[i * NT * 8 / kBlock];
+            py += a.ky.se, pf += a.kf.se;
         }
     };
+    uint16_t *px = a.dx + first * a.sdx + c0, *pd = a.df + first * a.sdf + c0;
     if (first < last) ahead(first);
     __syncthreads();
     int slot = 0;
@@ -493,7 +506,7 @@ __global__ void __launch_bounds__(NT, 512 / NT) k_join_backward_ring(const JoinB
                 }
             }
         }
-        const float m2 = block_sum<NT>(ss, sh[0]) * inv_h;
+        const float m2 = block_sum<NT>(ss, sh[0]) * (inv_h * r2);
         float n1[NV][8];
         ss = 0.f;
 #pragma unroll
@@ -503,16 +516,17 @@ __global__ void __launch_bounds__(NT, 512 / NT) k_join_backward_ring(const JoinB
             for (int j = 0; j < 8; ++j) n1[i][j] = 0.f;
             if (c < a.H) {
                 float u[8];
-#pragma unroll
-                for (int j = 0; j < 8; ++j) d[i][j] = r2 * (d[i][j] - n2[i][j] * m2);
                 if (a.dy) {
                     widen(ring_raw(stage, at_dy, c), u);
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) d[i][j] += u[j];
+                    for (int j = 0; j < 8; ++j) d[i][j] = fmaf(r2, d[i][j], fmaf(-m2, n2[i][j], u[j]));
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) d[i][j] = fmaf(r2, d[i][j], -m2 * n2[i][j]);
                 }
 #pragma unroll
                 for (int j = 0; j < 8; ++j) u[j] = a.alpha * d[i][j];
-                store8_bf16<true>(a.dx + t * a.sdx + c, 8, u);
+                store8_bf16<true>(px + i * NT * 8, 8, u);
                 norm(wide + saved, c, step_f[i], n1[i]);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
@@ -522,7 +536,7 @@ __global__ void __launch_bounds__(NT, 512 / NT) k_join_backward_ring(const JoinB
                 }
             }
         }
-        const float m1 = block_sum<NT>(ss, sh[1]) * inv_h;
+        const float m1 = block_sum<NT>(ss, sh[1]) * (inv_h * r1);
         // every thread has read the stage
         if (threadIdx.x == 0 && t + stages < last) {
             tc::fence_async();
@@ -534,10 +548,11 @@ __global__ void __launch_bounds__(NT, 512 / NT) k_join_backward_ring(const JoinB
             if (c < a.H) {
                 float u[8];
 #pragma unroll
-                for (int j = 0; j < 8; ++j) u[j] = r1 * (d[i][j] - n1[i][j] * m1);
-                store8_bf16<true>(a.df + t * a.sdf + c, 8, u);
+                for (int j = 0; j < 8; ++j) u[j] = fmaf(r1, d[i][j], -m1 * n1[i][j]);
+                store8_bf16<true>(pd + i * NT * 8, 8, u);
             }
         }
+        px += a.sdx, pd += a.sdf;
         if (++slot == stages) slot = 0, parity ^= 1;
     }
 #pragma unroll
@@ -574,43 +589,66 @@ RingPlan ring_plan(int64_t H, int64_t stage_bytes, int threads_on_sm) {
 
 // Column sums of the items' parts, in a fixed order: blockIdx.y = 0 joins all
 // items (the part of the norm after the block weighted by its group's gate), the
-// others a gate group each.
-__global__ void __launch_bounds__(1024) k_join_columns(const float *part_pre, const float *part_post, Items it, int H,
-                                                       const uint16_t *w_post, const uint16_t *gate, int64_t sg,
-                                                       float *dw_post, float *dw_pre, float *dgate, int64_t sdg) {
+// others a gate group each.  8 quads of columns and 32 runs of items a block.
+template <bool VEC>
+__global__ void __launch_bounds__(256) k_join_columns(const float *part_pre, const float *part_post, Items it, int H,
+                                                      const uint16_t *w_post, const uint16_t *gate, int64_t sg,
+                                                      float *dw_post, float *dw_pre, float *dgate, int64_t sdg) {
     __shared__ float s0[32][33], s1[32][33];
-    const int lane = threadIdx.x & 31, row = threadIdx.x >> 5;
-    const int h = blockIdx.x * 32 + lane;
+    const int quad = threadIdx.x & 7, row = threadIdx.x >> 3;
+    const int h = blockIdx.x * 32 + quad * 4;
     const bool all = blockIdx.y == 0;
+    const auto load4 = [&](const float *p, float (&v)[4]) {
+        if (VEC) {
+            const float4 q = *reinterpret_cast<const float4 *>(p);
+            v[0] = q.x, v[1] = q.y, v[2] = q.z, v[3] = q.w;
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[j] = h + j < H ? p[j] : 0.f;
+        }
+    };
     for (int64_t g = all ? 0 : blockIdx.y - 1; g < (all ? 1 : it.groups); g += all ? 1 : gridDim.y - 1) {
         const int64_t from = all ? 0 : g * it.per_group, to = all ? it.count : (g + 1) * it.per_group;
-        float a = 0.f, b = 0.f;
-        if (h < H)
+        float a[4] = {}, b[4] = {};
+        if (h < H) {
+#pragma unroll 4
             for (int64_t i = from + row; i < to; i += 32) {
-                float p = part_post[i * H + h];
+                float p[4];
+                load4(part_post + i * H + h, p);
                 if (all) {
-                    a += part_pre[i * H + h];
-                    if (gate) p *= bf16_to_f32(gate[i / it.per_group * sg + h]);
-                }
-                b += p;
-            }
-        s0[row][lane] = a;
-        s1[row][lane] = b;
-        __syncthreads();
-        a = s0[lane][row];
-        b = s1[lane][row];
+                    float r[4];
+                    load4(part_pre + i * H + h, r);
 #pragma unroll
-        for (int o = 16; o; o >>= 1) {
-            a += __shfl_xor_sync(~0u, a, o);
-            b += __shfl_xor_sync(~0u, b, o);
+                    for (int j = 0; j < 4; ++j) a[j] += r[j];
+                    if (gate) {
+                        const uint16_t *gr = gate + i / it.per_group * sg + h;
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) p[j] *= h + j < H ? bf16_to_f32(gr[j]) : 0.f;
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < 4; ++j) b[j] += p[j];
+            }
         }
-        const int hh = blockIdx.x * 32 + row;
-        if (lane == 0 && hh < H) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) s0[row][quad * 4 + j] = a[j], s1[row][quad * 4 + j] = b[j];
+        __syncthreads();
+        // 8 lanes to a column, 4 runs each
+        const int col = threadIdx.x >> 3, hh = blockIdx.x * 32 + col;
+        float sa = 0.f, sb = 0.f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) sa += s0[quad * 4 + j][col], sb += s1[quad * 4 + j][col];
+#pragma unroll
+        for (int o = 4; o; o >>= 1) {
+            sa += __shfl_xor_sync(~0u, sa, o);
+            sb += __shfl_xor_sync(~0u, sb, o);
+        }
+        if (quad == 0 && hh < H) {
             if (all) {
-                dw_pre[hh] = a;
-                dw_post[hh] = b;
+                dw_pre[hh] = sa;
+                dw_post[hh] = sb;
             } else {
-                dgate[g * sdg + hh] = b * bf16_to_f32(w_post[hh]);
+                dgate[g * sdg + hh] = sb * bf16_to_f32(w_post[hh]);
             }
         }
         __syncthreads();
@@ -786,8 +824,12 @@ extern "C" int pp_stage_join_backward(const uint16_t *dh, int64_t stride_dh, con
     else packed ? backward_by_width<false, true>(a, stream) : backward_by_width<false, false>(a, stream);
     PPS_CUDA_TRY(cudaGetLastError());
     const dim3 grid((unsigned)ceil_div(H, 32), 1 + (gate ? (unsigned)(it.groups < 1024 ? it.groups : 1024) : 0));
-    k_join_columns<<<grid, 1024, 0, stream>>>(s.pre, s.post, it, (int)H, w_post, gate, stride_gate, dw_post, dw_pre,
-                                              dgate, stride_dgate);
+    if (H % 4 == 0)
+        k_join_columns<true><<<grid, 256, 0, stream>>>(s.pre, s.post, it, (int)H, w_post, gate, stride_gate, dw_post,
+                                                       dw_pre, dgate, stride_dgate);
+    else
+        k_join_columns<false><<<grid, 256, 0, stream>>>(s.pre, s.post, it, (int)H, w_post, gate, stride_gate, dw_post,
+                                                        dw_pre, dgate, stride_dgate);
     PPS_CUDA_TRY(cudaGetLastError());
     return PP_OK;
 }

@@ -6,33 +6,38 @@
 namespace pps {
 namespace {
 
-// Each thread takes kUnits units of 8 columns, a block of threads apart, and
-// has all their loads in flight at once: the kernels are one pass over memory.
-// Units are counted in 32 bits where that is enough (I), for the division.
-constexpr int kUnits = 4, kThreads = 256;
+// A thread takes one unit of 8 columns of kRows consecutive rows and has all
+// their loads in flight at once: the kernels are one pass over memory.  A warp
+// is 32 consecutive units of a row, then of the next kRows rows; units are
+// counted in 32 bits where that is enough (I), for the one division.
+constexpr int kRows = 4, kThreads = 256;
 constexpr int64_t kManyUnits = 1ll << 31;  // from here on 64 bits
 
 // 8 lanes to a block of 64 columns.
 template <bool VEC, class I>
 __global__ void __launch_bounds__(kThreads) k_pack(const uint16_t *x, int64_t stride_x, int64_t T, int64_t H, int8_t *q,
                                                    int64_t stride_q, int8_t *e, int64_t stride_e) {
-    const I per = (I)((H + kBlock - 1) / kBlock * 8), units = (I)T * per;
-    const I first = (I)blockIdx.x * (kThreads * kUnits) + threadIdx.x;
-    Raw8 r[kUnits];
+    const I per = (I)((H + kBlock - 1) / kBlock * 8), u = (I)blockIdx.x * kThreads + threadIdx.x, g = u / per;
+    const int64_t t = (int64_t)g * kRows, c = (int64_t)(u - g * per) * 8;
+    // threads past the last unit go on with nothing: whole warps shuffle
+    const int rows = t < T ? (int)(T - t < kRows ? T - t : kRows) : 0;
+    const int left = H - c > 8 ? 8 : (int)(H - c);
+    const uint16_t *px = x + t * stride_x + c;
+    int8_t *pq = q + t * stride_q + c, *pe = e + t * stride_e + c / kBlock;
+    Raw8 r[kRows];
 #pragma unroll
-    for (int i = 0; i < kUnits; ++i) {
-        const I u = first + i * kThreads, t = u / per;
-        const int64_t c = (int64_t)(u - t * per) * 8, left = u < units ? H - c : 0;
-        r[i] = load8<VEC>(x + (left > 0 ? (int64_t)t * stride_x + c : 0), left);
+    for (int i = 0; i < kRows; ++i) {
+        r[i] = Raw8{};
+        if (i < rows && left > 0) r[i] = load8<VEC>(px + i * stride_x, left);
     }
 #pragma unroll
-    for (int i = 0; i < kUnits; ++i) {
-        const I u = first + i * kThreads, t = u / per;
-        const int64_t c = (int64_t)(u - t * per) * 8, left = u < units ? H - c : 0;
+    for (int i = 0; i < kRows; ++i) {
         int ex;
         const uint2 b = pack8(r[i], ex);
-        if (left > 0) store8_bytes<VEC>(q + (int64_t)t * stride_q + c, left, b);
-        if (u < units && (u & 7) == 0) e[(int64_t)t * stride_e + c / kBlock] = (int8_t)ex;
+        if (i < rows) {
+            if (left > 0) store8_bytes<VEC>(pq + i * stride_q, left, b);
+            if ((c & (kBlock - 1)) == 0) pe[i * stride_e] = (int8_t)ex;
+        }
     }
 }
 
@@ -40,29 +45,27 @@ template <bool VEC, class I>
 __global__ void __launch_bounds__(kThreads) k_unpack(const int8_t *q, int64_t stride_q, const int8_t *e,
                                                      int64_t stride_e, int64_t T, int64_t H, uint16_t *x,
                                                      int64_t stride_x) {
-    const I per = (I)((H + 7) / 8), units = (I)T * per;
-    const I first = (I)blockIdx.x * (kThreads * kUnits) + threadIdx.x;
-    uint2 b[kUnits];
-    int ex[kUnits];
+    const I per = (I)((H + 7) / 8), u = (I)blockIdx.x * kThreads + threadIdx.x, g = u / per;
+    const int64_t t = (int64_t)g * kRows, c = (int64_t)(u - g * per) * 8;
+    if (t >= T) return;
+    const int rows = (int)(T - t < kRows ? T - t : kRows), left = H - c > 8 ? 8 : (int)(H - c);
+    const int8_t *pq = q + t * stride_q + c, *pe = e + t * stride_e + c / kBlock;
+    uint16_t *px = x + t * stride_x + c;
+    uint2 b[kRows];
+    int ex[kRows];
 #pragma unroll
-    for (int i = 0; i < kUnits; ++i) {
-        const I u = first + i * kThreads, t = u / per;
-        const int64_t c = (int64_t)(u - t * per) * 8;
-        if (u < units) {
-            b[i] = load8_bytes<VEC>(q + (int64_t)t * stride_q + c, H - c);
-            ex[i] = e[(int64_t)t * stride_e + c / kBlock];
+    for (int i = 0; i < kRows; ++i)
+        if (i < rows) {
+            b[i] = load8_bytes<VEC>(pq + i * stride_q, left);
+            ex[i] = pe[i * stride_e];
         }
-    }
 #pragma unroll
-    for (int i = 0; i < kUnits; ++i) {
-        const I u = first + i * kThreads, t = u / per;
-        const int64_t c = (int64_t)(u - t * per) * 8;
-        if (u < units) {
+    for (int i = 0; i < kRows; ++i)
+        if (i < rows) {
             float v[8];
             unpack8(b[i], step_of(ex[i]), v);
-            store8_bf16<VEC>(x + (int64_t)t * stride_x + c, H - c, v);
+            store8_bf16<VEC>(px + i * stride_x, left, v);
         }
-    }
 }
 
 struct WgradEpi {
@@ -114,7 +117,7 @@ WgradSpace wgrad_space(void *ws, const uint16_t *dy, int64_t stride_dy, int64_t 
 
 int launch_unpack(const int8_t *q, int64_t stride_q, const int8_t *e, int64_t stride_e, int64_t T, int64_t H,
                   uint16_t *x, int64_t stride_x, cudaStream_t stream) {
-    const int64_t units = T * ceil_div(H, 8), grid = ceil_div(units, kThreads * kUnits);
+    const int64_t units = ceil_div(T, kRows) * ceil_div(H, 8), grid = ceil_div(units, kThreads);
     const bool vec = rows_aligned(x, stride_x, T, 2) && kept_aligned(q, stride_q, T);
     const auto go = [&](auto kernel) {
         kernel<<<(unsigned)grid, kThreads, 0, stream>>>(q, stride_q, e, stride_e, T, H, x, stride_x);
@@ -141,7 +144,7 @@ extern "C" int pp_stage_pack(const uint16_t *x, int64_t stride_x, int64_t T, int
     if (rc != PP_OK) return rc;
     if (T == 0) return PP_OK;
     if (!x || ((uintptr_t)x & 1) || stride_x < H || bad_kept(q, stride_q, e, stride_e, H)) return PP_ERR_ARG;
-    const int64_t units = T * ceil_div(H, kBlock) * 8, grid = ceil_div(units, kThreads * kUnits);
+    const int64_t units = ceil_div(T, kRows) * ceil_div(H, kBlock) * 8, grid = ceil_div(units, kThreads);
     const bool vec = rows_aligned(x, stride_x, T, 2) && kept_aligned(q, stride_q, T);
     const auto go = [&](auto kernel) {
         kernel<<<(unsigned)grid, kThreads, 0, stream>>>(x, stride_x, T, H, q, stride_q, e, stride_e);

@@ -73,15 +73,16 @@ __device__ __forceinline__ uint2 pack8(const Raw8 &x, int &e) {
     // (ties to even) that lies in the sum's low bits
     const float inv = e == kNonfinite ? 0.f : inv_step(e);
     constexpr float kRound = 12582912.f;
-    uint32_t b[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        const float v = j & 1 ? bf16_hi(x.w[j >> 1]) : bf16_lo(x.w[j >> 1]);
-        b[j] = __float_as_uint(fminf(fmaxf(fmaf(v, inv, kRound), kRound - 127.f), kRound + 127.f));
-    }
     if (e == kNonfinite) return make_uint2(0u, 0u);
-    return make_uint2(__byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410),
-                      __byte_perm(__byte_perm(b[4], b[5], 0x0040), __byte_perm(b[6], b[7], 0x0040), 0x5410));
+    uint32_t b[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const uint32_t lo = __float_as_uint(fmaf(bf16_lo(x.w[j]), inv, kRound));
+        const uint32_t hi = __float_as_uint(fmaf(bf16_hi(x.w[j]), inv, kRound));
+        // the sums' low 16 bits are the whole numbers: two of them are held to +-127 at once
+        b[j] = __vmins2(__vmaxs2(__byte_perm(lo, hi, 0x5410), 0xFF81FF81u), 0x007F007Fu);
+    }
+    return make_uint2(__byte_perm(b[0], b[1], 0x6420), __byte_perm(b[2], b[3], 0x6420));
 }
 
 // The 8 values that 8 bytes stand for, times `step`: a byte with its sign bit
