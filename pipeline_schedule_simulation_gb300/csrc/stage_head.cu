@@ -227,6 +227,7 @@ struct ForwardSpace {
     Aligned x, w;
     float2 *part;
     float *picked;
+    int64_t tiles;
     size_t bytes;
 };
 ForwardSpace forward_space(void *ws, const uint16_t *x, int64_t sx, const uint16_t *w, int64_t sw, int64_t T,
@@ -235,7 +236,8 @@ ForwardSpace forward_space(void *ws, const uint16_t *x, int64_t sx, const uint16
     ForwardSpace s;
     s.x = aligned(c, x, sx, T, H, false);
     s.w = aligned(c, w, sw, V, H, false);
-    s.part = c.take<float2>(column_tiles(V) * T);
+    s.tiles = plan_product(T, V, H).nt;
+    s.part = c.take<float2>(s.tiles * T);
     s.picked = c.take<float>(T);
     s.bytes = c.used;
     return s;
@@ -298,7 +300,7 @@ extern "C" int pp_stage_head_forward(const uint16_t *x, int64_t stride_x, const 
     if (rp == PP_OK)
         rp = launch_product<false, false>(s.x.op, s.w.op, T, V, H, StatsEpi{target, T, V, s.part, s.picked}, stream);
     if (rp != PP_OK) return rp;
-    k_head_join<<<(unsigned)ceil_div(T, 32), 1024, 0, stream>>>(s.part, s.picked, target, column_tiles(V), T, V, loss,
+    k_head_join<<<(unsigned)ceil_div(T, 32), 1024, 0, stream>>>(s.part, s.picked, target, s.tiles, T, V, loss,
                                                                 lse);
     PPS_CUDA_TRY(cudaGetLastError());
     return PP_OK;

@@ -9,11 +9,17 @@
 //   end(row, m, tile)  the row's piece of column tile `tile` is done
 // Each (row, column tile) is handed over by one thread, in column order.
 //
-// One persistent block per SM: a warp loads 64-deep slices of A and B by TMA
-// into a ring, a thread issues the MMAs of a 128 x 256 tile into one of two
+// Persistent blocks, one to an SM: a warp loads 64-deep slices of A and B by
+// TMA into a ring of six, a thread issues the MMAs of a tile into one of two
 // TMEM accumulators, four warps take the other accumulator through the
 // epilogue.  Operands come K-major or MN-major as they lie in memory; both
 // forms use the 128-byte swizzle.
+//
+// CG = 2: a pair of blocks shares a tile of 256 x 256: each holds half of A
+// and half of B, so that a slice costs each SM 32 KB of loads for 256 x 256 x
+// 64 products of the pair; a lone block needs 48 KB for half of that.
+// CG = 1: a block takes a tile of 128 x 128, with the same loads: for products
+// with so few tiles that more of them are worth more than fast ones.
 #pragma once
 
 #include "stage_common.cuh"
@@ -28,18 +34,16 @@ struct Operand {
     int64_t ld;
 };
 
-constexpr int kTileM = 128, kTileN = 256, kTileK = 64;
-constexpr int kStages = 4;
-constexpr int kBytesA = kTileM * kTileK * 2, kBytesB = kTileN * kTileK * 2, kBytesStage = kBytesA + kBytesB;
+constexpr int kTileK = 64, kHalf = 128;  // a block holds 128 rows of A and 128 of B
+constexpr int kStages = 6;
+constexpr int kBytesHalf = kHalf * kTileK * 2, kBytesStage = 2 * kBytesHalf;
 constexpr int kProductSmem = kStages * kBytesStage + 1024;
 constexpr int kProductThreads = 256;
-
-inline int64_t column_tiles(int64_t N) { return ceil_div(N, kTileN); }
 
 struct ProductShape {
     int M, N, K;
     int mt, nt;    // tiles
-    int group;     // row tiles that a run of blocks takes together
+    int group;     // row tiles that are taken together
     int splits;    // parts of K
     int k_blocks;  // slices of K in each part (the last may have fewer)
 };
@@ -54,10 +58,12 @@ __device__ __forceinline__ void tile_at(const ProductShape &s, int64_t i, int &m
     n = r / rows;
 }
 
-template <class Epi, bool A_MN, bool B_MN>
+template <class Epi, bool A_MN, bool B_MN, int CG>
 __global__ void __launch_bounds__(kProductThreads, 1)
     k_product(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
               const ProductShape s, const Epi epi) {
+    constexpr int kTileN = kHalf * CG;
+    constexpr uint32_t kCols = 2 * kTileN;  // TMEM columns: two accumulators
     extern __shared__ unsigned char raw[];
     __shared__ __align__(8) uint64_t bars[2 * kStages + 5];
     __shared__ uint32_t tmem_at;
@@ -66,7 +72,8 @@ __global__ void __launch_bounds__(kProductThreads, 1)
     const uint32_t full = tc::smem_u32(bars), empty = full + 8 * kStages;
     const uint32_t acc_full = empty + 8 * kStages, acc_empty = acc_full + 16, drained = acc_empty + 16;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int64_t tiles = (int64_t)s.mt * s.nt * s.splits;
+    const uint32_t rank = CG == 2 ? tc::cluster_rank() : 0;
+    const int64_t tiles = (int64_t)s.mt * s.nt * s.splits, first = blockIdx.x / CG, step = gridDim.x / CG;
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < kStages; ++i) {
@@ -75,7 +82,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
         }
         for (int i = 0; i < 2; ++i) {
             tc::mbar_init(acc_full + 8 * i, 1);
-            tc::mbar_init(acc_empty + 8 * i, 4);
+            tc::mbar_init(acc_empty + 8 * i, 4 * CG);
         }
         tc::mbar_init(drained, 1);
         stop = 0;
@@ -83,9 +90,10 @@ __global__ void __launch_bounds__(kProductThreads, 1)
         tc::prefetch_map(&map_a);
         tc::prefetch_map(&map_b);
     }
-    if (warp == 2) tc::tmem_alloc(tc::smem_u32(&tmem_at), 512);
+    if (warp == 2) tc::tmem_alloc<CG>(tc::smem_u32(&tmem_at), kCols);
     tc::fence_before();
     __syncthreads();
+    if (CG == 2) tc::cluster_sync();  // the other block's barriers are ready
     tc::fence_after();
     const uint32_t tmem = tmem_at;
     const int all_blocks = (s.K + kTileK - 1) / kTileK;
@@ -94,10 +102,11 @@ __global__ void __launch_bounds__(kProductThreads, 1)
         if (lane == 0) {
             int64_t it = 0;
             bool ok = true;
-            for (int64_t t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
+            for (int64_t t = first; t < tiles && ok; t += step) {
                 const int part = (int)(t % s.splits);
                 int m, n;
                 tile_at(s, t / s.splits, m, n);
+                const int m0 = (m * CG + (int)rank) * kHalf, n0 = (n * CG + (int)rank) * kHalf;
                 const int k0 = part * s.k_blocks, k1 = min(k0 + s.k_blocks, all_blocks);
                 for (int k = k0; k < k1; ++k, ++it) {
                     const int st = (int)(it % kStages);
@@ -105,38 +114,42 @@ __global__ void __launch_bounds__(kProductThreads, 1)
                         ok = false;
                         break;
                     }
-                    const uint32_t bar = full + 8 * st, a = ring + st * kBytesStage, b = a + kBytesA;
-                    tc::mbar_expect(bar, kBytesStage);
+                    const uint32_t a = ring + st * kBytesStage, b = a + kBytesHalf;
+                    // a pair's loads all count on the first block's barrier
+                    const uint32_t bar = CG == 2 ? tc::in_block(full + 8 * st, 0) : full + 8 * st;
+                    if (rank == 0) tc::mbar_expect(full + 8 * st, CG * kBytesStage);
                     if (A_MN) {
-#pragma unroll
-                        for (int i = 0; i < kTileM / 64; ++i)
-                            tc::tma_load(a + i * 8192, &map_a, m * kTileM + i * 64, k * kTileK, bar);
+                        tc::tma_load<CG>(a, &map_a, m0, k * kTileK, bar);
+                        tc::tma_load<CG>(a + 8192, &map_a, m0 + 64, k * kTileK, bar);
                     } else {
-                        tc::tma_load(a, &map_a, k * kTileK, m * kTileM, bar);
+                        tc::tma_load<CG>(a, &map_a, k * kTileK, m0, bar);
                     }
                     if (B_MN) {
-#pragma unroll
-                        for (int i = 0; i < kTileN / 64; ++i)
-                            tc::tma_load(b + i * 8192, &map_b, n * kTileN + i * 64, k * kTileK, bar);
+                        tc::tma_load<CG>(b, &map_b, n0, k * kTileK, bar);
+                        tc::tma_load<CG>(b + 8192, &map_b, n0 + 64, k * kTileK, bar);
                     } else {
-                        tc::tma_load(b, &map_b, k * kTileK, n * kTileN, bar);
+                        tc::tma_load<CG>(b, &map_b, k * kTileK, n0, bar);
                     }
                 }
             }
             // after giving up: the copies still in flight land before the block ends
-            if (!ok)
-                for (int64_t j = it > kStages ? it - kStages : 0; j < it; ++j)
-                    tc::mbar_drain(full + 8 * (int)(j % kStages), (uint32_t)(j / kStages) & 1);
+            if (!ok) {
+                if (rank == 0)
+                    for (int64_t j = it > kStages ? it - kStages : 0; j < it; ++j)
+                        tc::mbar_drain(full + 8 * (int)(j % kStages), (uint32_t)(j / kStages) & 1);
+                else
+                    tc::let_land();
+            }
         }
     } else if (warp == 1) {
-        if (lane == 0) {
-            constexpr uint32_t idesc = tc::instr_desc(kTileM, kTileN, A_MN, B_MN);
+        if (lane == 0 && rank == 0) {
+            constexpr uint32_t idesc = tc::instr_desc(kHalf * CG, kTileN, A_MN, B_MN);
             // 16 k further: 32 bytes along a K-major row, two groups of 8 k in the MN-major form
             constexpr uint32_t step_a = A_MN ? 2048 : 32, step_b = B_MN ? 2048 : 32;
             int64_t it = 0;
             int j = 0;
             bool ok = true;
-            for (int64_t t = blockIdx.x; t < tiles && ok; t += gridDim.x, ++j) {
+            for (int64_t t = first; t < tiles && ok; t += step, ++j) {
                 const int part = (int)(t % s.splits);
                 const int k0 = part * s.k_blocks, k1 = min(k0 + s.k_blocks, all_blocks);
                 const int buf = j & 1;
@@ -152,28 +165,28 @@ __global__ void __launch_bounds__(kProductThreads, 1)
                         break;
                     }
                     tc::fence_after();
-                    const uint32_t a = ring + st * kBytesStage, b = a + kBytesA;
+                    const uint32_t a = ring + st * kBytesStage, b = a + kBytesHalf;
 #pragma unroll
                     for (int kk = 0; kk < kTileK / 16; ++kk)
-                        tc::mma(tmem + buf * kTileN, tc::smem_desc(a + kk * step_a, A_MN ? 8192 : 16, 1024),
-                                tc::smem_desc(b + kk * step_b, B_MN ? 8192 : 16, 1024), idesc, k > k0 || kk > 0);
-                    tc::mma_commit(empty + 8 * st);
+                        tc::mma<CG>(tmem + buf * kTileN, tc::smem_desc(a + kk * step_a, A_MN ? 8192 : 16, 1024),
+                                    tc::smem_desc(b + kk * step_b, B_MN ? 8192 : 16, 1024), idesc, k > k0 || kk > 0);
+                    tc::mma_commit<CG>(empty + 8 * st);
                 }
-                if (ok) tc::mma_commit(acc_full + 8 * buf);
+                if (ok) tc::mma_commit<CG>(acc_full + 8 * buf);
             }
             // the MMAs have finished before TMEM is given back
-            tc::mma_commit(drained);
+            tc::mma_commit<CG>(drained);
             tc::mbar_drain(drained, 0);
         }
     } else if (warp >= 4) {
         const int quarter = warp - 4;
         int j = 0;
-        for (int64_t t = blockIdx.x; t < tiles; t += gridDim.x, ++j) {
+        for (int64_t t = first; t < tiles; t += step, ++j) {
             const int part = (int)(t % s.splits);
             int mt, nt;
             tile_at(s, t / s.splits, mt, nt);
             const int buf = j & 1;
-            const int64_t m = (int64_t)mt * kTileM + quarter * 32 + lane;
+            const int64_t m = (int64_t)(mt * CG + (int)rank) * kHalf + quarter * 32 + lane;
             const bool live = m < s.M;
             typename Epi::Row row;
             if (live) epi.begin(row, m, part);
@@ -189,14 +202,18 @@ __global__ void __launch_bounds__(kProductThreads, 1)
             }
             tc::fence_before();
             __syncwarp();
-            if (lane == 0) tc::mbar_arrive(acc_empty + 8 * buf);
+            if (lane == 0) {
+                if (CG == 2) tc::mbar_arrive_at(tc::in_block(acc_empty + 8 * buf, 0));
+                else tc::mbar_arrive(acc_empty + 8 * buf);
+            }
             if (live) epi.end(row, m, nt);
         }
     }
     tc::fence_before();
     __syncthreads();
+    if (CG == 2) tc::cluster_sync();  // neither block ends while the other may still signal it
     tc::fence_after();
-    if (warp == 2) tc::tmem_free(tmem, 512);
+    if (warp == 2) tc::tmem_free<CG>(tmem, kCols);
 }
 
 // ---- host side
@@ -205,38 +222,62 @@ __global__ void __launch_bounds__(kProductThreads, 1)
 int encode_map(CUtensorMap *map, const void *base, int64_t inner, int64_t rows, int64_t ld, int box_inner,
                int box_rows);
 
-// Parts of K that give every SM a tile where there are few tiles: each part
-// has at least 4 slices.
-inline int splits_for(int64_t M, int64_t N, int64_t K) {
-    const int64_t tiles = ceil_div(M, kTileM) * ceil_div(N, kTileN), blocks = ceil_div(K, kTileK);
-    int64_t s = sm_count() / (tiles > 0 ? tiles : 1);
+// How a product is cut: pairs of blocks from the point on where lone blocks'
+// tiles would not all fit on the SMs at once, and K in parts where there are
+// still fewer tiles than SMs (each part has at least 4 slices, none is empty).
+struct ProductPlan {
+    int cg, splits;
+    int64_t mt, nt;
+};
+inline ProductPlan plan_product(int64_t M, int64_t N, int64_t K) {
+    const int64_t sms = sm_count(), blocks = ceil_div(K, kTileK);
+    ProductPlan p;
+    p.cg = M > kHalf && ceil_div(M, kHalf) * ceil_div(N, kHalf) > sms ? 2 : 1;
+    p.mt = ceil_div(M, kHalf * p.cg), p.nt = ceil_div(N, kHalf * p.cg);
+    int64_t s = sms / p.cg / (p.mt * p.nt > 0 ? p.mt * p.nt : 1);
     if (s > blocks / 4) s = blocks / 4;
-    if (s <= 1) return 1;
-    return (int)ceil_div(blocks, ceil_div(blocks, s));  // no part is empty
+    p.splits = s <= 1 ? 1 : (int)ceil_div(blocks, ceil_div(blocks, s));
+    return p;
 }
 
+// A product without parts of K, whatever the plan says of them: its column
+// tiles are plan_product()'s.
 template <bool A_MN, bool B_MN, class Epi>
 int launch_product(const Operand &A, const Operand &B, int64_t M, int64_t N, int64_t K, const Epi &epi,
                    cudaStream_t stream, int splits = 1) {
     if (M <= 0 || N <= 0 || K <= 0) return PP_ERR_INTERNAL;
     CUtensorMap ma, mb;
-    int rc = A_MN ? encode_map(&ma, A.p, M, K, A.ld, 64, kTileK) : encode_map(&ma, A.p, K, M, A.ld, kTileK, kTileM);
+    int rc = A_MN ? encode_map(&ma, A.p, M, K, A.ld, 64, kTileK) : encode_map(&ma, A.p, K, M, A.ld, kTileK, kHalf);
     if (rc == PP_OK)
-        rc = B_MN ? encode_map(&mb, B.p, N, K, B.ld, 64, kTileK) : encode_map(&mb, B.p, K, N, B.ld, kTileK, kTileN);
+        rc = B_MN ? encode_map(&mb, B.p, N, K, B.ld, 64, kTileK) : encode_map(&mb, B.p, K, N, B.ld, kTileK, kHalf);
     if (rc != PP_OK) return rc;
-    static std::atomic<uint64_t> ready{0};
-    const int ra = allow_smem(k_product<Epi, A_MN, B_MN>, kProductSmem, ready);
-    if (ra != PP_OK) return ra;
+    const ProductPlan p = plan_product(M, N, K);
     ProductShape s;
     s.M = (int)M, s.N = (int)N, s.K = (int)K;
-    s.mt = (int)ceil_div(M, kTileM), s.nt = (int)ceil_div(N, kTileN);
+    s.mt = (int)p.mt, s.nt = (int)p.nt;
     s.splits = splits;
     s.k_blocks = (int)ceil_div(ceil_div(K, kTileK), splits);
-    s.group = s.mt < 16 ? s.mt : 16;
-    const int64_t tiles = (int64_t)s.mt * s.nt * s.splits, sms = sm_count();
-    k_product<Epi, A_MN, B_MN>
-        <<<(unsigned)(tiles < sms ? tiles : sms), kProductThreads, kProductSmem, stream>>>(ma, mb, s, epi);
-    PPS_CUDA_TRY(cudaGetLastError());
+    s.group = s.mt < 16 / p.cg ? s.mt : 16 / p.cg;
+    const int64_t tiles = p.mt * p.nt * splits, most = sm_count() / p.cg;
+    const unsigned grid = (unsigned)(tiles < most ? tiles : most) * p.cg;
+    static std::atomic<uint64_t> ready[2];
+    if (p.cg == 1) {
+        rc = allow_smem(k_product<Epi, A_MN, B_MN, 1>, kProductSmem, ready[0]);
+        if (rc != PP_OK) return rc;
+        k_product<Epi, A_MN, B_MN, 1><<<grid, kProductThreads, kProductSmem, stream>>>(ma, mb, s, epi);
+        PPS_CUDA_TRY(cudaGetLastError());
+        return PP_OK;
+    }
+    rc = allow_smem(k_product<Epi, A_MN, B_MN, 2>, kProductSmem, ready[1]);
+    if (rc != PP_OK) return rc;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid), cfg.blockDim = dim3(kProductThreads), cfg.dynamicSmemBytes = kProductSmem;
+    cfg.stream = stream;
+    cudaLaunchAttribute pair;
+    pair.id = cudaLaunchAttributeClusterDimension;
+    pair.val.clusterDim.x = 2, pair.val.clusterDim.y = 1, pair.val.clusterDim.z = 1;
+    cfg.attrs = &pair, cfg.numAttrs = 1;
+    PPS_CUDA_TRY(cudaLaunchKernelEx(&cfg, k_product<Epi, A_MN, B_MN, 2>, ma, mb, s, epi));
     return PP_OK;
 }
 
@@ -285,7 +326,7 @@ __global__ void __launch_bounds__(128) k_join_parts(const float *parts, int spli
 
 // Floats of scratch memory that product_in_parts needs.
 inline int64_t part_floats(int64_t M, int64_t N, int64_t K) {
-    const int s = splits_for(M, N, K);
+    const int s = plan_product(M, N, K).splits;
     return s > 1 ? s * M * round_up(N, 32) : 0;
 }
 
@@ -293,7 +334,7 @@ inline int64_t part_floats(int64_t M, int64_t N, int64_t K) {
 template <bool A_MN, bool B_MN, class Epi>
 int product_in_parts(const Operand &A, const Operand &B, int64_t M, int64_t N, int64_t K, const Epi &epi, float *parts,
                      cudaStream_t stream) {
-    const int splits = splits_for(M, N, K);
+    const int splits = plan_product(M, N, K).splits;
     if (splits == 1) return launch_product<A_MN, B_MN>(A, B, M, N, K, epi, stream);
     const int64_t ld = round_up(N, 32);
     const int rc = launch_product<A_MN, B_MN>(A, B, M, N, K, PartEpi{parts, M, ld}, stream, splits);

@@ -34,7 +34,9 @@ def _both(S, x, w, target, scale=1.0, weight=None, **kw):
 
 # one token, ragged edges of every tile, widths that are no multiple of 8, narrow and wide
 SHAPES = [(1, 1, 1), (1, 257, 64), (2, 1000, 8), (5, 100, 1001), (64, 64, 64), (127, 300, 72), (128, 512, 128),
-          (129, 513, 136), (255, 777, 200), (300, 5000, 63), (1000, 1031, 520), (3, 50257, 96), (700, 130, 2048)]
+          (129, 513, 136), (255, 777, 200), (300, 5000, 63), (1000, 1031, 520), (3, 50257, 96), (700, 130, 2048),
+          # enough tiles for pairs of blocks in every product
+          (2100, 2500, 1200), (1537, 3001, 264), (2049, 5001, 531)]
 
 
 @pytest.mark.parametrize("T,V,H", SHAPES)
