@@ -35,6 +35,7 @@ __device__ __forceinline__ void join_stats(float &m, float &s, float m2, float s
 __device__ __forceinline__ bool inside(int64_t target, int64_t V) { return target >= 0 && target < V; }
 
 struct StatsEpi {
+    static constexpr bool kWhole = false;
     const int64_t *target;
     int64_t T, V;
     float2 *part;   // [column tiles][T]: largest logit, sum of exponentials
@@ -71,11 +72,11 @@ struct StatsEpi {
 
 // d of one piece: columns v0 .. of the vocabulary, as bf16.
 struct GradEpi {
+    static constexpr bool kWhole = true;
     const int64_t *target;
     const float *lse, *weight;
     int64_t T, V, v0;
-    uint16_t *d;  // [T][ld]
-    int64_t ld;
+    uint16_t *d;  // in panels of T rows
     struct Row {
         float lse, c;
         int64_t at;  // the target's column counted from the piece's first
@@ -90,24 +91,20 @@ struct GradEpi {
     }
     __device__ __forceinline__ void chunk(Row &r, int64_t t, int64_t n, int cnt, const float (&v)[32]) const {
         float p[32];
-        if (r.in) {
 #pragma unroll
-            for (int j = 0; j < 32; ++j) {
-                p[j] = exp2f((v[j] - r.lse) * kLog2e);
-                if (n + j == r.at) p[j] -= 1.f;
-                p[j] *= r.c;
-            }
-        } else {
-#pragma unroll
-            for (int j = 0; j < 32; ++j) p[j] = 0.f;
+        for (int j = 0; j < 32; ++j) {
+            p[j] = exp2f((v[j] - r.lse) * kLog2e);
+            if (n + j == r.at) p[j] -= 1.f;
+            p[j] = r.in && j < cnt ? p[j] * r.c : 0.f;
         }
-        store_bf16(d + t * ld + n, cnt, true, p);  // rows of the workspace are aligned
+        store_bf16(d + (n >> 6) * (T * 64) + t * 64 + (n & 63), 32, true, p);
     }
     __device__ __forceinline__ void end(Row &, int64_t, int64_t) const {}
 };
 
 // dx: pieces add up in 32 bits; the last one writes the result.
 struct DxEpi {
+    static constexpr bool kWhole = false;
     float *acc;  // [T][ld_acc]
     uint16_t *dx;
     const int64_t *target;
@@ -140,6 +137,7 @@ struct DxEpi {
 };
 
 struct DwEpi {
+    static constexpr bool kWhole = false;
     uint16_t *dw16;  // one of the two
     float *dw32;
     int64_t ld;
@@ -211,16 +209,16 @@ int check_head(const void *x, int64_t sx, const void *w, int64_t sw, const void 
     return PP_OK;
 }
 
-// An operand as the products read it: in place, or as an aligned copy.
+// An operand as the products read it: in place, or as an aligned copy in rows.
 struct Aligned {
     uint16_t *copy;  // null: in place
-    Operand op;
+    Matrix at;
 };
-Aligned aligned(Carve &c, const uint16_t *p, int64_t stride, int64_t rows, int64_t H, bool always) {
-    if (!always && rows_aligned(p, stride, rows, 2)) return {nullptr, {p, stride}};
-    const int64_t ld = round_up(H, 8);
+Aligned aligned(Carve &c, const uint16_t *p, int64_t stride, int64_t rows, int64_t H) {
+    if (rows_aligned(p, stride, rows, 2)) return {nullptr, in_rows(p, stride)};
+    const int64_t ld = round_up(H, 64);
     uint16_t *q = c.take<uint16_t>(rows * ld);
-    return {q, {q, ld}};
+    return {q, in_rows(q, ld)};
 }
 
 struct ForwardSpace {
@@ -234,8 +232,8 @@ ForwardSpace forward_space(void *ws, const uint16_t *x, int64_t sx, const uint16
                            int64_t V, int64_t H) {
     Carve c{static_cast<unsigned char *>(ws)};
     ForwardSpace s;
-    s.x = aligned(c, x, sx, T, H, false);
-    s.w = aligned(c, w, sw, V, H, false);
+    s.x = aligned(c, x, sx, T, H);
+    s.w = aligned(c, w, sw, V, H);
     s.tiles = plan_product(T, V, H).nt;
     s.part = c.take<float2>(s.tiles * T);
     s.picked = c.take<float>(T);
@@ -244,8 +242,8 @@ ForwardSpace forward_space(void *ws, const uint16_t *x, int64_t sx, const uint16
 }
 
 struct BackwardSpace {
-    Aligned x, w;  // x always as a copy, with the rows that are left out at 0
-    uint16_t *d;
+    Aligned w;
+    uint16_t *x, *d;  // in panels: x with the rows that are left out at 0, d of one piece
     float *acc, *parts;
     int64_t piece, ld_acc;
     size_t bytes;
@@ -256,8 +254,8 @@ BackwardSpace backward_space(void *ws, const uint16_t *x, int64_t sx, const uint
     BackwardSpace s;
     s.piece = piece_of(T, V);
     s.ld_acc = round_up(H, 32);
-    s.x = aligned(c, x, sx, T, H, true);
-    s.w = aligned(c, w, sw, V, H, false);
+    s.w = aligned(c, w, sw, V, H);
+    s.x = c.take<uint16_t>(T * round_up(H, 64));
     s.d = c.take<uint16_t>(T * s.piece);
     s.acc = c.take<float>(s.piece < V ? T * s.ld_acc : 0);
     int64_t parts = 0;  // the last piece may be shorter than the others
@@ -270,9 +268,8 @@ BackwardSpace backward_space(void *ws, const uint16_t *x, int64_t sx, const uint
     return s;
 }
 
-int copy_if(const Aligned &a, const uint16_t *p, int64_t stride, int64_t rows, int64_t H, const int64_t *target,
-            int64_t V, cudaStream_t stream) {
-    return a.copy ? launch_copy_rows(p, stride, rows, H, target, V, a.copy, a.op.ld, stream) : PP_OK;
+int copy_if(const Aligned &a, const uint16_t *p, int64_t stride, int64_t rows, int64_t H, cudaStream_t stream) {
+    return a.copy ? launch_copy_rows(p, stride, rows, H, nullptr, 0, a.copy, a.at.ld, 64, stream) : PP_OK;
 }
 
 }  // namespace
@@ -295,10 +292,10 @@ extern "C" int pp_stage_head_forward(const uint16_t *x, int64_t stride_x, const 
     if ((!loss && !lse) || ((uintptr_t)loss & 3) || ((uintptr_t)lse & 3)) return PP_ERR_ARG;
     const ForwardSpace s = forward_space(workspace, x, stride_x, w, stride_w, T, V, H);
     if (!workspace || ((uintptr_t)workspace & (kStageAlign - 1)) || workspace_bytes < s.bytes) return PP_ERR_ARG;
-    int rp = copy_if(s.x, x, stride_x, T, H, nullptr, 0, stream);
-    if (rp == PP_OK) rp = copy_if(s.w, w, stride_w, V, H, nullptr, 0, stream);
+    int rp = copy_if(s.x, x, stride_x, T, H, stream);
+    if (rp == PP_OK) rp = copy_if(s.w, w, stride_w, V, H, stream);
     if (rp == PP_OK)
-        rp = launch_product<false, false>(s.x.op, s.w.op, T, V, H, StatsEpi{target, T, V, s.part, s.picked}, stream);
+        rp = launch_product<kRowsK, kRowsK>(s.x.at, s.w.at, T, V, H, StatsEpi{target, T, V, s.part, s.picked}, stream);
     if (rp != PP_OK) return rp;
     k_head_join<<<(unsigned)ceil_div(T, 32), 1024, 0, stream>>>(s.part, s.picked, target, s.tiles, T, V, loss,
                                                                 lse);
@@ -331,21 +328,24 @@ extern "C" int pp_stage_head_backward(const uint16_t *x, int64_t stride_x, const
     }
     const BackwardSpace s = backward_space(workspace, x, stride_x, w, stride_w, T, V, H);
     if (!workspace || ((uintptr_t)workspace & (kStageAlign - 1)) || workspace_bytes < s.bytes) return PP_ERR_ARG;
-    int rp = copy_if(s.x, x, stride_x, T, H, target, V, stream);
-    if (rp == PP_OK) rp = copy_if(s.w, w, stride_w, V, H, nullptr, 0, stream);
+    int rp = launch_copy_rows(x, stride_x, T, H, target, V, s.x, 64, T * 64, stream);
+    if (rp == PP_OK) rp = copy_if(s.w, w, stride_w, V, H, stream);
     const bool vec_dx = dx && rows_aligned(dx, stride_dx, T, 2), vec_dw = dw && rows_aligned(dw, stride_dw, V, dw_float ? 4 : 2);
+    const Matrix xm = in_panels(s.x, T), d = in_panels(s.d, T);
     for (int64_t v0 = 0; v0 < V && rp == PP_OK; v0 += s.piece) {
         const int64_t n = V - v0 < s.piece ? V - v0 : s.piece;
-        const Operand wp{s.w.op.p + v0 * s.w.op.ld, s.w.op.ld}, d{s.d, s.piece};
-        rp = launch_product<false, false>(s.x.op, wp, T, n, H, GradEpi{target, lse, weight, T, V, v0, s.d, s.piece},
-                                          stream);
-        if (rp == PP_OK && dx)
-            rp = product_in_parts<false, true>(
-                d, wp, T, H, n, DxEpi{s.acc, dx, target, V, s.ld_acc, stride_dx, scale, v0 == 0, v0 + n == V, vec_dx},
-                s.parts, stream);
+        const Matrix wp = in_rows(s.w.at.p + v0 * s.w.at.ld, s.w.at.ld);
+        rp = launch_product<kPanelsK, kRowsK>(xm, wp, T, n, H, GradEpi{target, lse, weight, T, V, v0, s.d}, stream);
+        if (rp == PP_OK && dx) {
+            const DxEpi epi{s.acc, dx, target, V, s.ld_acc, stride_dx, scale, v0 == 0, v0 + n == V, vec_dx};
+            // the copy's rows are whole panels; so are w's own if H is
+            rp = s.w.copy || H % 64 == 0
+                     ? product_in_parts<kPanelsK, kPanelsMN>(d, wp, T, H, n, epi, s.parts, stream)
+                     : product_in_parts<kPanelsK, kRowsMN>(d, wp, T, H, n, epi, s.parts, stream);
+        }
         if (rp == PP_OK && dw)
-            rp = product_in_parts<true, true>(
-                d, s.x.op, n, H, T,
+            rp = product_in_parts<kPanelsMN, kPanelsMN>(
+                d, xm, n, H, T,
                 DwEpi{dw_float ? nullptr : (uint16_t *)dw + v0 * stride_dw,
                       dw_float ? (float *)dw + v0 * stride_dw : nullptr, stride_dw, scale, dw_add != 0, vec_dw},
                 s.parts, stream);

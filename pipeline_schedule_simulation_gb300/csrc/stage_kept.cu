@@ -43,14 +43,14 @@ __global__ void __launch_bounds__(kThreads) k_pack(const uint16_t *x, int64_t st
 
 template <bool VEC, class I>
 __global__ void __launch_bounds__(kThreads) k_unpack(const int8_t *q, int64_t stride_q, const int8_t *e,
-                                                     int64_t stride_e, int64_t T, int64_t H, uint16_t *x,
-                                                     int64_t stride_x) {
+                                                     int64_t stride_e, int64_t T, int64_t H, uint16_t *x, int64_t ld,
+                                                     int64_t panel) {
     const I per = (I)((H + 7) / 8), u = (I)blockIdx.x * kThreads + threadIdx.x, g = u / per;
     const int64_t t = (int64_t)g * kRows, c = (int64_t)(u - g * per) * 8;
     if (t >= T) return;
     const int rows = (int)(T - t < kRows ? T - t : kRows), left = H - c > 8 ? 8 : (int)(H - c);
     const int8_t *pq = q + t * stride_q + c, *pe = e + t * stride_e + c / kBlock;
-    uint16_t *px = x + t * stride_x + c;
+    uint16_t *px = x + t * ld + c / kBlock * panel + c % kBlock;
     uint2 b[kRows];
     int ex[kRows];
 #pragma unroll
@@ -64,11 +64,12 @@ __global__ void __launch_bounds__(kThreads) k_unpack(const int8_t *q, int64_t st
         if (i < rows) {
             float v[8];
             unpack8(b[i], step_of(ex[i]), v);
-            store8_bf16<VEC>(px + i * stride_x, left, v);
+            store8_bf16<VEC>(px + i * ld, left, v);
         }
 }
 
 struct WgradEpi {
+    static constexpr bool kWhole = false;
     const float *add;
     float *dw;
     int64_t ld_add, ld;
@@ -94,20 +95,16 @@ bool bad_kept(const int8_t *q, int64_t sq, const int8_t *e, int64_t se, int64_t 
 }
 
 struct WgradSpace {
-    uint16_t *v;   // what the checkpoint stands for, rows of ld
-    uint16_t *dy;  // an aligned copy of dy, or null
+    uint16_t *v;   // what the checkpoint stands for, in panels
+    uint16_t *dy;  // an aligned copy of dy in panels, or null
     float *parts;
-    int64_t ld, ld_dy;
     size_t bytes;
 };
 WgradSpace wgrad_space(void *ws, const uint16_t *dy, int64_t stride_dy, int64_t T, int64_t N, int64_t H) {
     Carve c{static_cast<unsigned char *>(ws)};
     WgradSpace s;
-    s.ld = round_up(H, 8);
-    s.v = c.take<uint16_t>(T * s.ld);
-    const bool copy = !rows_aligned(dy, stride_dy, T, 2);
-    s.ld_dy = copy ? round_up(N, 8) : stride_dy;
-    s.dy = copy ? c.take<uint16_t>(T * s.ld_dy) : nullptr;
+    s.v = c.take<uint16_t>(T * round_up(H, 64));
+    s.dy = rows_aligned(dy, stride_dy, T, 2) ? nullptr : c.take<uint16_t>(T * round_up(N, 64));
     s.parts = c.take<float>(part_floats(N, H, T));
     s.bytes = c.used;
     return s;
@@ -116,11 +113,11 @@ WgradSpace wgrad_space(void *ws, const uint16_t *dy, int64_t stride_dy, int64_t 
 }  // namespace
 
 int launch_unpack(const int8_t *q, int64_t stride_q, const int8_t *e, int64_t stride_e, int64_t T, int64_t H,
-                  uint16_t *x, int64_t stride_x, cudaStream_t stream) {
+                  uint16_t *x, int64_t ld, int64_t panel, cudaStream_t stream) {
     const int64_t units = ceil_div(T, kRows) * ceil_div(H, 8), grid = ceil_div(units, kThreads);
-    const bool vec = rows_aligned(x, stride_x, T, 2) && kept_aligned(q, stride_q, T);
+    const bool vec = rows_aligned(x, ld, T, 2) && kept_aligned(q, stride_q, T);
     const auto go = [&](auto kernel) {
-        kernel<<<(unsigned)grid, kThreads, 0, stream>>>(q, stride_q, e, stride_e, T, H, x, stride_x);
+        kernel<<<(unsigned)grid, kThreads, 0, stream>>>(q, stride_q, e, stride_e, T, H, x, ld, panel);
     };
     if (units < kManyUnits) vec ? go(k_unpack<true, uint32_t>) : go(k_unpack<false, uint32_t>);
     else vec ? go(k_unpack<true, int64_t>) : go(k_unpack<false, int64_t>);
@@ -161,7 +158,7 @@ extern "C" int pp_stage_unpack(const int8_t *q, int64_t stride_q, const int8_t *
     if (rc != PP_OK) return rc;
     if (T == 0) return PP_OK;
     if (!x || ((uintptr_t)x & 1) || stride_x < H || bad_kept(q, stride_q, e, stride_e, H)) return PP_ERR_ARG;
-    return launch_unpack(q, stride_q, e, stride_e, T, H, x, stride_x, stream);
+    return launch_unpack(q, stride_q, e, stride_e, T, H, x, stride_x, kBlock, stream);
 }
 
 extern "C" size_t pp_stage_weight_grad_workspace(const uint16_t *dy, int64_t stride_dy, int64_t T, int64_t N,
@@ -191,10 +188,14 @@ extern "C" int pp_stage_weight_grad(const uint16_t *dy, int64_t stride_dy, const
     const WgradSpace s = wgrad_space(workspace, dy, stride_dy, T, N, H);
     if (!workspace || ((uintptr_t)workspace & (kStageAlign - 1)) || workspace_bytes < s.bytes) return PP_ERR_ARG;
     const bool copy = !rows_aligned(dy, stride_dy, T, 2);
-    int rp = launch_unpack(q, stride_q, e, stride_e, T, H, s.v, s.ld, stream);
-    if (rp == PP_OK && copy) rp = launch_copy_rows(dy, stride_dy, T, N, nullptr, 0, s.dy, s.ld_dy, stream);
+    int rp = launch_unpack(q, stride_q, e, stride_e, T, H, s.v, kBlock, T * kBlock, stream);
+    if (rp == PP_OK && copy) rp = launch_copy_rows(dy, stride_dy, T, N, nullptr, 0, s.dy, kBlock, T * kBlock, stream);
     if (rp != PP_OK) return rp;
     const bool vec = rows_aligned(dw, stride_dw, N, 4) && (!add || rows_aligned(add, stride_add, N, 4));
-    return product_in_parts<true, true>(Operand{copy ? s.dy : dy, s.ld_dy}, Operand{s.v, s.ld}, N, H, T,
-                                        WgradEpi{add, dw, stride_add, stride_dw, vec}, s.parts, stream);
+    const WgradEpi epi{add, dw, stride_add, stride_dw, vec};
+    const Matrix v = in_panels(s.v, T);
+    if (copy) return product_in_parts<kPanelsMN, kPanelsMN>(in_panels(s.dy, T), v, N, H, T, epi, s.parts, stream);
+    if (N % 64 == 0)
+        return product_in_parts<kPanelsMN, kPanelsMN>(in_rows(dy, stride_dy), v, N, H, T, epi, s.parts, stream);
+    return product_in_parts<kRowsMN, kPanelsMN>(in_rows(dy, stride_dy), v, N, H, T, epi, s.parts, stream);
 }

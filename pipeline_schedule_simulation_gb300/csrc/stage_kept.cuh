@@ -152,7 +152,8 @@ inline bool kept_aligned(const void *q, int64_t stride, int64_t rows) {
     return ((uintptr_t)q & 7) == 0 && (rows <= 1 || (stride & 7) == 0);
 }
 
+// As panels or rows: element (t, c) at x[t*ld + (c/64)*panel + c%64].
 int launch_unpack(const int8_t *q, int64_t stride_q, const int8_t *e, int64_t stride_e, int64_t T, int64_t H,
-                  uint16_t *x, int64_t stride_x, cudaStream_t stream);
+                  uint16_t *x, int64_t ld, int64_t panel, cudaStream_t stream);
 
 }  // namespace pps

@@ -7,13 +7,17 @@
 //   begin(row, m, part)  a row m of the tile starts (part: which part of K)
 //   chunk(row, m, n, cnt, v)  columns n .. n+cnt-1 (cnt <= 32) of row m
 //   end(row, m, tile)  the row's piece of column tile `tile` is done
+//   kWhole             the columns go on to the next multiple of 64, with cnt <= 0
+//                      past the last one
 // Each (row, column tile) is handed over by one thread, in column order.
 //
 // Persistent blocks, one to an SM: a warp loads 64-deep slices of A and B by
 // TMA into a ring of six, a thread issues the MMAs of a tile into one of two
 // TMEM accumulators, four warps take the other accumulator through the
 // epilogue.  Operands come K-major or MN-major as they lie in memory; both
-// forms use the 128-byte swizzle.
+// forms use the 128-byte swizzle.  What the library lays out itself lies in
+// panels of 64 columns (128 bytes), each panel's rows one after the other, so
+// that a box is one run of memory in either form.
 //
 // CG = 2: a pair of blocks shares a tile of 256 x 256: each holds half of A
 // and half of B, so that a slice costs each SM 32 KB of loads for 256 x 256 x
@@ -27,12 +31,33 @@
 
 namespace pps {
 
-// An operand: element (i, k) at p[i*ld + k] (K-major) or p[k*ld + i]
-// (MN-major), with rows aligned to 16 bytes (rows_aligned).
-struct Operand {
+// A matrix of bf16: element (row, col) at p[row*ld + (col/64)*panel + col%64].
+// Rows in memory: panel = 64 and ld their stride (aligned to 16 bytes); panels:
+// ld = 64 and panel their stride, the last panel's columns padded with zeros.
+struct Matrix {
     const uint16_t *p;
-    int64_t ld;
+    int64_t ld, panel;
 };
+inline Matrix in_rows(const uint16_t *p, int64_t ld) { return {p, ld, 64}; }
+inline Matrix in_panels(const uint16_t *p, int64_t rows) { return {p, 64, rows * 64}; }
+
+// How an operand lies: rows along k (K-major), rows along m or n (MN-major),
+// panels in either use.  MN-major rows whose columns are whole panels are
+// loaded as panels.
+enum Form { kRowsK, kRowsMN, kPanelsK, kPanelsMN };
+__host__ __device__ constexpr bool is_mn(Form f) { return f == kRowsMN || f == kPanelsMN; }
+
+// One stage's half of an operand: 128 of its rows (m or n) from i0, slice k.
+template <int CG, Form F>
+__device__ __forceinline__ void load_half(uint32_t to, const CUtensorMap *map, int i0, int k, uint32_t bar) {
+    if (F == kRowsK) tc::tma_load<CG>(to, map, k * 64, i0, 0, bar);
+    if (F == kPanelsK) tc::tma_load<CG>(to, map, 0, i0, k, bar);
+    if (F == kPanelsMN) tc::tma_load<CG>(to, map, 0, k * 64, i0 / 64, bar);
+    if (F == kRowsMN) {
+        tc::tma_load<CG>(to, map, i0, k * 64, 0, bar);
+        tc::tma_load<CG>(to + 8192, map, i0 + 64, k * 64, 0, bar);
+    }
+}
 
 constexpr int kTileK = 64, kHalf = 128;  // a block holds 128 rows of A and 128 of B
 constexpr int kStages = 6;
@@ -58,11 +83,12 @@ __device__ __forceinline__ void tile_at(const ProductShape &s, int64_t i, int &m
     n = r / rows;
 }
 
-template <class Epi, bool A_MN, bool B_MN, int CG>
+template <class Epi, Form FA, Form FB, int CG>
 __global__ void __launch_bounds__(kProductThreads, 1)
     k_product(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
               const ProductShape s, const Epi epi) {
     constexpr int kTileN = kHalf * CG;
+    constexpr bool A_MN = is_mn(FA), B_MN = is_mn(FB);
     constexpr uint32_t kCols = 2 * kTileN;  // TMEM columns: two accumulators
     extern __shared__ unsigned char raw[];
     __shared__ __align__(8) uint64_t bars[2 * kStages + 5];
@@ -118,18 +144,8 @@ __global__ void __launch_bounds__(kProductThreads, 1)
                     // a pair's loads all count on the first block's barrier
                     const uint32_t bar = CG == 2 ? tc::in_block(full + 8 * st, 0) : full + 8 * st;
                     if (rank == 0) tc::mbar_expect(full + 8 * st, CG * kBytesStage);
-                    if (A_MN) {
-                        tc::tma_load<CG>(a, &map_a, m0, k * kTileK, bar);
-                        tc::tma_load<CG>(a + 8192, &map_a, m0 + 64, k * kTileK, bar);
-                    } else {
-                        tc::tma_load<CG>(a, &map_a, k * kTileK, m0, bar);
-                    }
-                    if (B_MN) {
-                        tc::tma_load<CG>(b, &map_b, n0, k * kTileK, bar);
-                        tc::tma_load<CG>(b + 8192, &map_b, n0 + 64, k * kTileK, bar);
-                    } else {
-                        tc::tma_load<CG>(b, &map_b, k * kTileK, n0, bar);
-                    }
+                    load_half<CG, FA>(a, &map_a, m0, k, bar);
+                    load_half<CG, FB>(b, &map_b, n0, k, bar);
                 }
             }
             // after giving up: the copies still in flight land before the block ends
@@ -180,6 +196,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
         }
     } else if (warp >= 4) {
         const int quarter = warp - 4;
+        const int wide = Epi::kWhole ? (s.N + 63) & ~63 : s.N;
         int j = 0;
         for (int64_t t = first; t < tiles; t += step, ++j) {
             const int part = (int)(t % s.splits);
@@ -194,7 +211,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
             const bool ok = tc::mbar_wait(acc_full + 8 * buf, (uint32_t)(j >> 1) & 1, &stop, 4);
             if (!__all_sync(~0u, ok)) break;
             tc::fence_after();
-            for (int c = 0; c < kTileN && nt * kTileN + c < s.N; c += 32) {
+            for (int c = 0; c < kTileN && nt * kTileN + c < wide; c += 32) {
                 float v[32];
                 tc::tmem_load32(tmem + ((uint32_t)(quarter * 32) << 16) + buf * kTileN + c, v);
                 const int n = nt * kTileN + c, left = s.N - n;
@@ -218,9 +235,19 @@ __global__ void __launch_bounds__(kProductThreads, 1)
 
 // ---- host side
 
-// One map of a row-major matrix for boxes of box_rows x box_inner elements.
-int encode_map(CUtensorMap *map, const void *base, int64_t inner, int64_t rows, int64_t ld, int box_inner,
-               int box_rows);
+// The map of an operand of `rows` x `cols` as it lies in memory, for boxes of
+// box_rows x 64 x box_panels.
+int encode_map(CUtensorMap *map, const Matrix &m, int64_t rows, int64_t cols, bool panels, int box_rows,
+               int box_panels);
+
+// I: the operand's extent along m or n, K along k.
+template <Form F>
+int map_of(CUtensorMap *map, const Matrix &m, int64_t I, int64_t K) {
+    if (F == kRowsK) return encode_map(map, m, I, K, false, kHalf, 1);
+    if (F == kPanelsK) return encode_map(map, m, I, K, true, kHalf, 1);
+    if (F == kPanelsMN) return encode_map(map, m, K, I, true, 64, 2);
+    return encode_map(map, m, K, I, false, 64, 1);
+}
 
 // How a product is cut: pairs of blocks from the point on where lone blocks'
 // tiles would not all fit on the SMs at once, and K in parts where there are
@@ -242,14 +269,13 @@ inline ProductPlan plan_product(int64_t M, int64_t N, int64_t K) {
 
 // A product without parts of K, whatever the plan says of them: its column
 // tiles are plan_product()'s.
-template <bool A_MN, bool B_MN, class Epi>
-int launch_product(const Operand &A, const Operand &B, int64_t M, int64_t N, int64_t K, const Epi &epi,
+template <Form FA, Form FB, class Epi>
+int launch_product(const Matrix &A, const Matrix &B, int64_t M, int64_t N, int64_t K, const Epi &epi,
                    cudaStream_t stream, int splits = 1) {
     if (M <= 0 || N <= 0 || K <= 0) return PP_ERR_INTERNAL;
     CUtensorMap ma, mb;
-    int rc = A_MN ? encode_map(&ma, A.p, M, K, A.ld, 64, kTileK) : encode_map(&ma, A.p, K, M, A.ld, kTileK, kHalf);
-    if (rc == PP_OK)
-        rc = B_MN ? encode_map(&mb, B.p, N, K, B.ld, 64, kTileK) : encode_map(&mb, B.p, K, N, B.ld, kTileK, kHalf);
+    int rc = map_of<FA>(&ma, A, M, K);
+    if (rc == PP_OK) rc = map_of<FB>(&mb, B, N, K);
     if (rc != PP_OK) return rc;
     const ProductPlan p = plan_product(M, N, K);
     ProductShape s;
@@ -257,18 +283,18 @@ int launch_product(const Operand &A, const Operand &B, int64_t M, int64_t N, int
     s.mt = (int)p.mt, s.nt = (int)p.nt;
     s.splits = splits;
     s.k_blocks = (int)ceil_div(ceil_div(K, kTileK), splits);
-    s.group = s.mt < 16 / p.cg ? s.mt : 16 / p.cg;
+    s.group = s.mt < 16 ? s.mt : 16;
     const int64_t tiles = p.mt * p.nt * splits, most = sm_count() / p.cg;
     const unsigned grid = (unsigned)(tiles < most ? tiles : most) * p.cg;
     static std::atomic<uint64_t> ready[2];
     if (p.cg == 1) {
-        rc = allow_smem(k_product<Epi, A_MN, B_MN, 1>, kProductSmem, ready[0]);
+        rc = allow_smem(k_product<Epi, FA, FB, 1>, kProductSmem, ready[0]);
         if (rc != PP_OK) return rc;
-        k_product<Epi, A_MN, B_MN, 1><<<grid, kProductThreads, kProductSmem, stream>>>(ma, mb, s, epi);
+        k_product<Epi, FA, FB, 1><<<grid, kProductThreads, kProductSmem, stream>>>(ma, mb, s, epi);
         PPS_CUDA_TRY(cudaGetLastError());
         return PP_OK;
     }
-    rc = allow_smem(k_product<Epi, A_MN, B_MN, 2>, kProductSmem, ready[1]);
+    rc = allow_smem(k_product<Epi, FA, FB, 2>, kProductSmem, ready[1]);
     if (rc != PP_OK) return rc;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid), cfg.blockDim = dim3(kProductThreads), cfg.dynamicSmemBytes = kProductSmem;
@@ -277,7 +303,7 @@ int launch_product(const Operand &A, const Operand &B, int64_t M, int64_t N, int
     pair.id = cudaLaunchAttributeClusterDimension;
     pair.val.clusterDim.x = 2, pair.val.clusterDim.y = 1, pair.val.clusterDim.z = 1;
     cfg.attrs = &pair, cfg.numAttrs = 1;
-    PPS_CUDA_TRY(cudaLaunchKernelEx(&cfg, k_product<Epi, A_MN, B_MN, 2>, ma, mb, s, epi));
+    PPS_CUDA_TRY(cudaLaunchKernelEx(&cfg, k_product<Epi, FA, FB, 2>, ma, mb, s, epi));
     return PP_OK;
 }
 
@@ -286,6 +312,7 @@ int launch_product(const Operand &A, const Operand &B, int64_t M, int64_t N, int
 // them.
 namespace {
 struct PartEpi {
+    static constexpr bool kWhole = false;
     float *parts;
     int64_t M, ld;
     struct Row {
@@ -331,13 +358,13 @@ inline int64_t part_floats(int64_t M, int64_t N, int64_t K) {
 }
 
 // A product whose K is shared out where there are too few tiles for the SMs.
-template <bool A_MN, bool B_MN, class Epi>
-int product_in_parts(const Operand &A, const Operand &B, int64_t M, int64_t N, int64_t K, const Epi &epi, float *parts,
+template <Form FA, Form FB, class Epi>
+int product_in_parts(const Matrix &A, const Matrix &B, int64_t M, int64_t N, int64_t K, const Epi &epi, float *parts,
                      cudaStream_t stream) {
     const int splits = plan_product(M, N, K).splits;
-    if (splits == 1) return launch_product<A_MN, B_MN>(A, B, M, N, K, epi, stream);
+    if (splits == 1) return launch_product<FA, FB>(A, B, M, N, K, epi, stream);
     const int64_t ld = round_up(N, 32);
-    const int rc = launch_product<A_MN, B_MN>(A, B, M, N, K, PartEpi{parts, M, ld}, stream, splits);
+    const int rc = launch_product<FA, FB>(A, B, M, N, K, PartEpi{parts, M, ld}, stream, splits);
     if (rc != PP_OK) return rc;
     k_join_parts<Epi><<<(unsigned)ceil_div(M * (ld / 32), 128), 128, 0, stream>>>(parts, splits, M, N, ld, epi);
     PPS_CUDA_TRY(cudaGetLastError());
@@ -382,10 +409,10 @@ __device__ __forceinline__ void store_f32(float *p, int cnt, bool vec, const flo
     }
 }
 
-// A copy of rows at any stride and alignment into aligned ones (ld a multiple
-// of 8 elements), 0 past column H; with `target`, a row whose target is
+// A copy of rows at any stride and alignment as panels (or aligned rows), the
+// last panel's columns past H as zeros; with `target`, a row whose target is
 // outside 0..V-1 becomes 0.
 int launch_copy_rows(const uint16_t *x, int64_t stride, int64_t T, int64_t H, const int64_t *target, int64_t V,
-                     uint16_t *out, int64_t ld, cudaStream_t stream);
+                     uint16_t *out, int64_t ld, int64_t panel, cudaStream_t stream);
 
 }  // namespace pps

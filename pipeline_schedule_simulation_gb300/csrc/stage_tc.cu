@@ -3,6 +3,7 @@
 #include <mutex>
 #include <vector>
 
+#include "stage_kept.cuh"
 #include "stage_product.cuh"
 
 namespace pps {
@@ -39,15 +40,18 @@ int register_wait_reader(uint64_t (*reader)()) {
     return 0;
 }
 
-int encode_map(CUtensorMap *map, const void *base, int64_t inner, int64_t rows, int64_t ld, int box_inner,
-               int box_rows) {
+int encode_map(CUtensorMap *map, const Matrix &m, int64_t rows, int64_t cols, bool panels, int box_rows,
+               int box_panels) {
     const EncodeTiled fn = encoder();
     if (!fn) return PP_ERR_CUDA;
-    if (rows == 1) ld = round_up(inner, 8);  // there is no second row: any stride will do
-    const cuuint64_t dims[2] = {(cuuint64_t)inner, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)ld * 2};
-    const cuuint32_t box[2] = {(cuuint32_t)box_inner, (cuuint32_t)box_rows}, step[2] = {1, 1};
+    // a row's stride is of no account where there is one row
+    const int64_t ld = rows == 1 ? round_up(m.ld, 8) : m.ld;
+    const cuuint64_t dims[3] = {panels ? 64 : (cuuint64_t)cols, (cuuint64_t)rows,
+                                panels ? (cuuint64_t)ceil_div(cols, 64) : 1};
+    const cuuint64_t strides[2] = {(cuuint64_t)ld * 2, panels ? (cuuint64_t)m.panel * 2 : (cuuint64_t)ld * 2};
+    const cuuint32_t box[3] = {64, (cuuint32_t)box_rows, (cuuint32_t)box_panels}, step[3] = {1, 1, 1};
     const CUresult r =
-        fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(base), dims, strides, box, step,
+        fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<uint16_t *>(m.p), dims, strides, box, step,
            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? PP_OK : PP_ERR_CUDA;
@@ -71,23 +75,35 @@ int sm_count() {
 
 namespace {
 
+// A thread copies 8 columns of a row.
+template <bool VEC>
 __global__ void __launch_bounds__(256) k_copy_rows(const uint16_t *x, int64_t stride, int64_t T, int64_t H,
-                                                   const int64_t *target, int64_t V, uint16_t *out, int64_t ld) {
-    for (int64_t t = blockIdx.x; t < T; t += gridDim.x) {
+                                                   const int64_t *target, int64_t V, uint16_t *out, int64_t ld,
+                                                   int64_t panel) {
+    const int64_t per = (H + 63) / 64 * 8, units = T * per, step = (int64_t)gridDim.x * blockDim.x;
+    for (int64_t u = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; u < units; u += step) {
+        const int64_t t = u / per, c = (u - t * per) * 8, left = H - c;
         bool in = true;
         if (target) {
             const int64_t g = target[t];
             in = g >= 0 && g < V;
         }
-        for (int64_t h = threadIdx.x; h < ld; h += blockDim.x) out[t * ld + h] = in && h < H ? x[t * stride + h] : 0;
+        Raw8 r{};
+        if (in && left > 0) r = load8<VEC>(x + t * stride + c, left);
+        store8<true>(out + t * ld + c / 64 * panel + c % 64, 8, r);
     }
 }
 
 }  // namespace
 
 int launch_copy_rows(const uint16_t *x, int64_t stride, int64_t T, int64_t H, const int64_t *target, int64_t V,
-                     uint16_t *out, int64_t ld, cudaStream_t stream) {
-    k_copy_rows<<<(unsigned)(T < 152 * 32 ? T : 152 * 32), 256, 0, stream>>>(x, stride, T, H, target, V, out, ld);
+                     uint16_t *out, int64_t ld, int64_t panel, cudaStream_t stream) {
+    const int64_t blocks = ceil_div(T * ceil_div(H, 64) * 8, 256);
+    const unsigned grid = (unsigned)(blocks < 152 * 64 ? blocks : 152 * 64);
+    if (rows_aligned(x, stride, T, 2))
+        k_copy_rows<true><<<grid, 256, 0, stream>>>(x, stride, T, H, target, V, out, ld, panel);
+    else
+        k_copy_rows<false><<<grid, 256, 0, stream>>>(x, stride, T, H, target, V, out, ld, panel);
     PPS_CUDA_TRY(cudaGetLastError());
     return PP_OK;
 }

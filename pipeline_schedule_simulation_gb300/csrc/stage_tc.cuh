@@ -112,18 +112,18 @@ __device__ __forceinline__ void mbar_arrive_at(uint32_t cluster_bar) {
 
 // Loads one box; in a pair `bar` is a cluster address, in either block.
 template <int CG>
-__device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap *map, int x, int y, uint32_t bar) {
+__device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap *map, int x, int y, int z, uint32_t bar) {
     if (CG == 2)
         asm volatile(
-            "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, %3}], "
-            "[%4];" ::"r"(dst),
-            "l"(map), "r"(x), "r"(y), "r"(bar)
+            "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, %3, "
+            "%4}], [%5];" ::"r"(dst),
+            "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
             : "memory");
     else
         asm volatile(
-            "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
+            "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
                 dst),
-            "l"(map), "r"(x), "r"(y), "r"(bar)
+            "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
             : "memory");
 }
 // `bytes` consecutive bytes (both addresses and the size multiples of 16).
