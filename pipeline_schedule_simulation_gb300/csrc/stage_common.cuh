@@ -52,6 +52,27 @@ int allow_smem(K kernel, int bytes, std::atomic<uint64_t> &ready) {
     return PP_OK;
 }
 
+// A launch that may start while the kernel before it on the stream is still
+// running: the kernel calls after_previous() before it touches memory, which
+// waits until that one is done.  cluster: blocks that form a cluster.
+template <class... P, class... A>
+int launch_after(void (*kernel)(P...), int64_t grid, int threads, int smem, cudaStream_t stream, int cluster,
+                 const A &...args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)grid), cfg.blockDim = dim3(threads), cfg.dynamicSmemBytes = smem, cfg.stream = stream;
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = cluster, at[1].val.clusterDim.y = 1, at[1].val.clusterDim.z = 1;
+    cfg.attrs = at, cfg.numAttrs = cluster > 1 ? 2 : 1;
+    PPS_CUDA_TRY(cudaLaunchKernelEx(&cfg, kernel, args...));
+    return PP_OK;
+}
+__device__ __forceinline__ void after_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// Lets the kernel after this one take free places on the SMs and wait there.
+__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 __device__ __forceinline__ float bf16_to_f32(uint16_t b) { return __uint_as_float((uint32_t)b << 16); }
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
@@ -63,5 +84,18 @@ __device__ __forceinline__ uint32_t f32_to_bf16x2(float lo, float hi) {
 }
 
 constexpr float kLog2e = 1.4426950408889634f;
+
+// 2^x to 2 units in the last place; results below 2^-126 become 0.
+__device__ __forceinline__ float exp2_fast(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+// The same with results below 2^-126 (a gradient may consist of them).
+__device__ __forceinline__ float exp2_full(float x) {
+    float y;
+    asm("ex2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
 
 }  // namespace pps

@@ -22,14 +22,10 @@ constexpr float kNegInf = -__builtin_huge_valf();
 // that is infinite (so that inf - inf never appears).
 __device__ __forceinline__ float ref_of(float m) { return isinf(m) ? 0.f : m; }
 
-// Joins (m, s) with (m2, s2): sums of exponentials relative to ref_of(m).
-__device__ __forceinline__ void join_stats(float &m, float &s, float m2, float s2) {
-    const float mm = fmaxf(m, m2), r = ref_of(mm);
-    // an empty part (m = -inf, s = 0) adds nothing
-    const float a = s == 0.f ? 0.f : s * exp2f((ref_of(m) - r) * kLog2e);
-    const float b = s2 == 0.f ? 0.f : s2 * exp2f((ref_of(m2) - r) * kLog2e);
-    m = mm;
-    s = a + b;
+// A sum of exponentials relative to ref_of(m), taken relative to `r` (an empty
+// one stays empty).
+__device__ __forceinline__ float rebase(float s, float m, float r) {
+    return s == 0.f ? 0.f : s * exp2_fast((ref_of(m) - r) * kLog2e);
 }
 
 __device__ __forceinline__ bool inside(int64_t target, int64_t V) { return target >= 0 && target < V; }
@@ -38,7 +34,7 @@ struct StatsEpi {
     static constexpr bool kWhole = false;
     const int64_t *target;
     int64_t T, V;
-    float2 *part;   // [column tiles][T]: largest logit, sum of exponentials
+    float2 *part;   // [pieces][T]: largest logit, sum of exponentials
     float *picked;  // [T]: the target's logit
     struct Row {
         float m, s;
@@ -50,23 +46,33 @@ struct StatsEpi {
         r.target = target ? target[t] : -1;
     }
     __device__ __forceinline__ void chunk(Row &r, int64_t t, int64_t n, int cnt, const float (&v)[32]) const {
-        float m = kNegInf, s = 0.f;
+        float m = r.m;
+        if (cnt < 32) {
 #pragma unroll
-        for (int j = 0; j < 32; ++j)
-            if (j < cnt) m = fmaxf(m, v[j]);
+            for (int j = 0; j < 32; ++j) m = j < cnt ? fmaxf(m, v[j]) : m;
+        } else {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) m = fmaxf(m, v[j]);
+        }
         const float ref = ref_of(m);
+        float s[4] = {rebase(r.s, r.m, ref), 0.f, 0.f, 0.f};
+        if (cnt < 32) {
 #pragma unroll
-        for (int j = 0; j < 32; ++j)
-            if (j < cnt) s += exp2f((v[j] - ref) * kLog2e);
-        join_stats(r.m, r.s, m, s);
+            for (int j = 0; j < 32; ++j) s[j & 3] += j < cnt ? exp2_fast((v[j] - ref) * kLog2e) : 0.f;
+        } else {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) s[j & 3] += exp2_fast((v[j] - ref) * kLog2e);
+        }
+        r.m = m;
+        r.s = (s[0] + s[1]) + (s[2] + s[3]);
         if (r.target >= n && r.target < n + cnt) {
 #pragma unroll
             for (int j = 0; j < 32; ++j)
                 if (r.target == n + j) picked[t] = v[j];
         }
     }
-    __device__ __forceinline__ void end(Row &r, int64_t t, int64_t tile) const {
-        part[tile * T + t] = make_float2(r.m, r.s);
+    __device__ __forceinline__ void end(Row &r, int64_t t, int64_t piece) const {
+        part[piece * T + t] = make_float2(r.m, r.s);
     }
 };
 
@@ -92,10 +98,18 @@ struct GradEpi {
     __device__ __forceinline__ void chunk(Row &r, int64_t t, int64_t n, int cnt, const float (&v)[32]) const {
         float p[32];
 #pragma unroll
-        for (int j = 0; j < 32; ++j) {
-            p[j] = exp2f((v[j] - r.lse) * kLog2e);
-            if (n + j == r.at) p[j] -= 1.f;
-            p[j] = r.in && j < cnt ? p[j] * r.c : 0.f;
+        for (int j = 0; j < 32; ++j) p[j] = exp2_full((v[j] - r.lse) * kLog2e);
+        if (r.at >= n && r.at < n + 32) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+                if (n + j == r.at) p[j] -= 1.f;
+        }
+#pragma unroll
+        for (int j = 0; j < 32; ++j) p[j] *= r.c;
+        if (!r.in || cnt < 32) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+                if (!r.in || j >= cnt) p[j] = 0.f;
         }
         store_bf16(d + (n >> 6) * (T * 64) + t * 64 + (n & 63), 32, true, p);
     }
@@ -161,28 +175,49 @@ struct DwEpi {
     __device__ __forceinline__ void end(Row &, int64_t, int64_t) const {}
 };
 
-// One block of 32 tokens: 32 lanes along the tiles for each token.
-__global__ void __launch_bounds__(1024) k_head_join(const float2 *part, const float *picked, const int64_t *target,
-                                                    int64_t tiles, int64_t T, int64_t V, float *loss, float *lse) {
-    __shared__ float2 sh[32][33];
-    const int lane = threadIdx.x & 31, row = threadIdx.x >> 5;
-    const int64_t t = (int64_t)blockIdx.x * 32 + lane;
+// 8 tokens a block: 32 lanes along the pieces of each.  First the largest
+// logit, then the sums relative to it.
+__global__ void __launch_bounds__(256) k_head_join(const float2 *part, const float *picked, const int64_t *target,
+                                                   int64_t pieces, int64_t T, int64_t V, float *loss, float *lse) {
+    after_previous();
+    __shared__ float2 sh[8][33];
+    // 8 neighbouring tokens are read together; 32 runs of pieces for each
+    const int col = threadIdx.x & 7, run = threadIdx.x >> 3;
+    const int64_t t = (int64_t)blockIdx.x * 8 + col;
     float m = kNegInf, s = 0.f;
-    if (t < T)
-        for (int64_t i = row; i < tiles; i += 32) {
-            const float2 p = part[i * T + t];
-            join_stats(m, s, p.x, p.y);
-        }
-    sh[row][lane] = make_float2(m, s);
-    __syncthreads();
-    // token blockIdx*32 + row: its 32 parts across the warp, always in the same order
-    const int64_t u = (int64_t)blockIdx.x * 32 + row;
-    m = sh[lane][row].x;
-    s = sh[lane][row].y;
+    if (t < T) {
+        constexpr int kAhead = 8;
+        for (int64_t i = run; i < pieces; i += 32 * kAhead) {
+            float2 p[kAhead];
 #pragma unroll
-    for (int o = 16; o; o >>= 1) join_stats(m, s, __shfl_xor_sync(~0u, m, o), __shfl_xor_sync(~0u, s, o));
+            for (int j = 0; j < kAhead; ++j) {
+                const int64_t k = i + 32 * j;
+                p[j] = k < pieces ? part[k * T + t] : make_float2(kNegInf, 0.f);
+            }
+            float mm = m;
+#pragma unroll
+            for (int j = 0; j < kAhead; ++j) mm = fmaxf(mm, p[j].x);
+            const float ref = ref_of(mm);
+            s = rebase(s, m, ref);
+#pragma unroll
+            for (int j = 0; j < kAhead; ++j) s += rebase(p[j].y, p[j].x, ref);
+            m = mm;
+        }
+    }
+    sh[col][run] = make_float2(m, s);
+    __syncthreads();
+    const int lane = threadIdx.x & 31, row = threadIdx.x >> 5;
+    const int64_t u = (int64_t)blockIdx.x * 8 + row;
+    const float2 q = sh[row][lane];
+    m = q.x;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
+    const float ref = ref_of(m);
+    s = rebase(q.y, q.x, ref);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(~0u, s, o);
     if (lane == 0 && u < T) {
-        const float l = ref_of(m) + logf(s);
+        const float l = ref + logf(s);
         if (lse) lse[u] = l;
         if (loss) loss[u] = inside(target[u], V) ? l - picked[u] : 0.f;
     }
@@ -225,7 +260,7 @@ struct ForwardSpace {
     Aligned x, w;
     float2 *part;
     float *picked;
-    int64_t tiles;
+    ProductPlan plan;
     size_t bytes;
 };
 ForwardSpace forward_space(void *ws, const uint16_t *x, int64_t sx, const uint16_t *w, int64_t sw, int64_t T,
@@ -234,8 +269,8 @@ ForwardSpace forward_space(void *ws, const uint16_t *x, int64_t sx, const uint16
     ForwardSpace s;
     s.x = aligned(c, x, sx, T, H);
     s.w = aligned(c, w, sw, V, H);
-    s.tiles = plan_product(T, V, H).nt;
-    s.part = c.take<float2>(s.tiles * T);
+    s.plan = plan_product(T, V, H, false, false);
+    s.part = c.take<float2>(kPieces * s.plan.nt * T);
     s.picked = c.take<float>(T);
     s.bytes = c.used;
     return s;
@@ -295,12 +330,11 @@ extern "C" int pp_stage_head_forward(const uint16_t *x, int64_t stride_x, const 
     int rp = copy_if(s.x, x, stride_x, T, H, stream);
     if (rp == PP_OK) rp = copy_if(s.w, w, stride_w, V, H, stream);
     if (rp == PP_OK)
-        rp = launch_product<kRowsK, kRowsK>(s.x.at, s.w.at, T, V, H, StatsEpi{target, T, V, s.part, s.picked}, stream);
+        rp = launch_product<kRowsK, kRowsK>(s.x.at, s.w.at, T, V, H, StatsEpi{target, T, V, s.part, s.picked}, s.plan,
+                                            stream);
     if (rp != PP_OK) return rp;
-    k_head_join<<<(unsigned)ceil_div(T, 32), 1024, 0, stream>>>(s.part, s.picked, target, s.tiles, T, V, loss,
-                                                                lse);
-    PPS_CUDA_TRY(cudaGetLastError());
-    return PP_OK;
+    return launch_after(k_head_join, ceil_div(T, 8), 256, 0, stream, 1, (const float2 *)s.part, (const float *)s.picked,
+                        target, kPieces * s.plan.nt, T, V, loss, lse);
 }
 
 extern "C" size_t pp_stage_head_backward_workspace(const uint16_t *x, int64_t stride_x, const uint16_t *w,
@@ -335,7 +369,7 @@ extern "C" int pp_stage_head_backward(const uint16_t *x, int64_t stride_x, const
     for (int64_t v0 = 0; v0 < V && rp == PP_OK; v0 += s.piece) {
         const int64_t n = V - v0 < s.piece ? V - v0 : s.piece;
         const Matrix wp = in_rows(s.w.at.p + v0 * s.w.at.ld, s.w.at.ld);
-        rp = launch_product<kPanelsK, kRowsK>(xm, wp, T, n, H, GradEpi{target, lse, weight, T, V, v0, s.d}, stream);
+        rp = whole_product<kPanelsK, kRowsK>(xm, wp, T, n, H, GradEpi{target, lse, weight, T, V, v0, s.d}, stream);
         if (rp == PP_OK && dx) {
             const DxEpi epi{s.acc, dx, target, V, s.ld_acc, stride_dx, scale, v0 == 0, v0 + n == V, vec_dx};
             // the copy's rows are whole panels; so are w's own if H is

@@ -17,6 +17,8 @@ constexpr int64_t kManyUnits = 1ll << 31;  // from here on 64 bits
 template <bool VEC, class I>
 __global__ void __launch_bounds__(kThreads) k_pack(const uint16_t *x, int64_t stride_x, int64_t T, int64_t H, int8_t *q,
                                                    int64_t stride_q, int8_t *e, int64_t stride_e) {
+    let_next_start();
+    after_previous();
     const I per = (I)((H + kBlock - 1) / kBlock * 8), u = (I)blockIdx.x * kThreads + threadIdx.x, g = u / per;
     const int64_t t = (int64_t)g * kRows, c = (int64_t)(u - g * per) * 8;
     // threads past the last unit go on with nothing: whole warps shuffle
@@ -45,6 +47,8 @@ template <bool VEC, class I>
 __global__ void __launch_bounds__(kThreads) k_unpack(const int8_t *q, int64_t stride_q, const int8_t *e,
                                                      int64_t stride_e, int64_t T, int64_t H, uint16_t *x, int64_t ld,
                                                      int64_t panel) {
+    let_next_start();
+    after_previous();
     const I per = (I)((H + 7) / 8), u = (I)blockIdx.x * kThreads + threadIdx.x, g = u / per;
     const int64_t t = (int64_t)g * kRows, c = (int64_t)(u - g * per) * 8;
     if (t >= T) return;
@@ -116,13 +120,9 @@ int launch_unpack(const int8_t *q, int64_t stride_q, const int8_t *e, int64_t st
                   uint16_t *x, int64_t ld, int64_t panel, cudaStream_t stream) {
     const int64_t units = ceil_div(T, kRows) * ceil_div(H, 8), grid = ceil_div(units, kThreads);
     const bool vec = rows_aligned(x, ld, T, 2) && kept_aligned(q, stride_q, T);
-    const auto go = [&](auto kernel) {
-        kernel<<<(unsigned)grid, kThreads, 0, stream>>>(q, stride_q, e, stride_e, T, H, x, ld, panel);
-    };
-    if (units < kManyUnits) vec ? go(k_unpack<true, uint32_t>) : go(k_unpack<false, uint32_t>);
-    else vec ? go(k_unpack<true, int64_t>) : go(k_unpack<false, int64_t>);
-    PPS_CUDA_TRY(cudaGetLastError());
-    return PP_OK;
+    const auto kernel = units < kManyUnits ? (vec ? k_unpack<true, uint32_t> : k_unpack<false, uint32_t>)
+                                           : (vec ? k_unpack<true, int64_t> : k_unpack<false, int64_t>);
+    return launch_after(kernel, grid, kThreads, 0, stream, 1, q, stride_q, e, stride_e, T, H, x, ld, panel);
 }
 
 }  // namespace pps
@@ -143,13 +143,9 @@ extern "C" int pp_stage_pack(const uint16_t *x, int64_t stride_x, int64_t T, int
     if (!x || ((uintptr_t)x & 1) || stride_x < H || bad_kept(q, stride_q, e, stride_e, H)) return PP_ERR_ARG;
     const int64_t units = ceil_div(T, kRows) * ceil_div(H, kBlock) * 8, grid = ceil_div(units, kThreads);
     const bool vec = rows_aligned(x, stride_x, T, 2) && kept_aligned(q, stride_q, T);
-    const auto go = [&](auto kernel) {
-        kernel<<<(unsigned)grid, kThreads, 0, stream>>>(x, stride_x, T, H, q, stride_q, e, stride_e);
-    };
-    if (units < kManyUnits) vec ? go(k_pack<true, uint32_t>) : go(k_pack<false, uint32_t>);
-    else vec ? go(k_pack<true, int64_t>) : go(k_pack<false, int64_t>);
-    PPS_CUDA_TRY(cudaGetLastError());
-    return PP_OK;
+    const auto kernel = units < kManyUnits ? (vec ? k_pack<true, uint32_t> : k_pack<false, uint32_t>)
+                                           : (vec ? k_pack<true, int64_t> : k_pack<false, int64_t>);
+    return launch_after(kernel, grid, kThreads, 0, stream, 1, x, stride_x, T, H, q, stride_q, e, stride_e);
 }
 
 extern "C" int pp_stage_unpack(const int8_t *q, int64_t stride_q, const int8_t *e, int64_t stride_e, int64_t T,

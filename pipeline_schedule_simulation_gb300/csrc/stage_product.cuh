@@ -6,24 +6,26 @@
 //   typename Epi::Row  what a row keeps between its pieces
 //   begin(row, m, part)  a row m of the tile starts (part: which part of K)
 //   chunk(row, m, n, cnt, v)  columns n .. n+cnt-1 (cnt <= 32) of row m
-//   end(row, m, tile)  the row's piece of column tile `tile` is done
-//   kWhole             the columns go on to the next multiple of 64, with cnt <= 0
-//                      past the last one
-// Each (row, column tile) is handed over by one thread, in column order.
+//   end(row, m, piece)  the row's piece `piece` of the columns is done
+//   kWhole             runs of columns go on to the next multiple of 64, with
+//                      cnt <= 0 past the last one, and no run is cut by a tile's end
+// A row's part of a column tile is two pieces, the even and the odd runs of 32
+// columns; each piece is handed over by one thread, in column order.
 //
 // Persistent blocks, one to an SM: a warp loads 64-deep slices of A and B by
-// TMA into a ring of six, a thread issues the MMAs of a tile into one of two
-// TMEM accumulators, four warps take the other accumulator through the
-// epilogue.  Operands come K-major or MN-major as they lie in memory; both
-// forms use the 128-byte swizzle.  What the library lays out itself lies in
-// panels of 64 columns (128 bytes), each panel's rows one after the other, so
-// that a box is one run of memory in either form.
+// TMA into a ring, a thread issues the MMAs of a tile into one of two TMEM
+// accumulators, eight warps take the other accumulator through the epilogue.
+// Operands come K-major or MN-major as they lie in memory; both forms use the
+// 128-byte swizzle.  What the library lays out itself lies in panels of 64
+// columns (128 bytes), each panel's rows one after the other, so that a box is
+// one run of memory in either form.
 //
 // CG = 2: a pair of blocks shares a tile of 256 x 256: each holds half of A
-// and half of B, so that a slice costs each SM 32 KB of loads for 256 x 256 x
-// 64 products of the pair; a lone block needs 48 KB for half of that.
-// CG = 1: a block takes a tile of 128 x 128, with the same loads: for products
-// with so few tiles that more of them are worth more than fast ones.
+// and half of B, so that a slice costs each SM 32 KB of loads for its half of
+// 256 x 256 x 64 products.
+// CG = 1: a block takes a tile of 128 rows and 16 to 256 columns, chosen so
+// that the tiles fill the SMs: for products with few tiles, and for few rows,
+// where reading B is all that counts.
 #pragma once
 
 #include "stage_common.cuh"
@@ -47,26 +49,33 @@ inline Matrix in_panels(const uint16_t *p, int64_t rows) { return {p, 64, rows *
 enum Form { kRowsK, kRowsMN, kPanelsK, kPanelsMN };
 __host__ __device__ constexpr bool is_mn(Form f) { return f == kRowsMN || f == kPanelsMN; }
 
-// One stage's half of an operand: 128 of its rows (m or n) from i0, slice k.
+// One slice k of an operand's rows (m or n) from i0 on, as many as the map's box holds
+// (MN-major rows: `rows`, a multiple of 64, in boxes of 64).
 template <int CG, Form F>
-__device__ __forceinline__ void load_half(uint32_t to, const CUtensorMap *map, int i0, int k, uint32_t bar) {
+__device__ __forceinline__ void load_slice(uint32_t to, const CUtensorMap *map, int i0, int rows, int k, uint32_t bar) {
     if (F == kRowsK) tc::tma_load<CG>(to, map, k * 64, i0, 0, bar);
     if (F == kPanelsK) tc::tma_load<CG>(to, map, 0, i0, k, bar);
     if (F == kPanelsMN) tc::tma_load<CG>(to, map, 0, k * 64, i0 / 64, bar);
-    if (F == kRowsMN) {
-        tc::tma_load<CG>(to, map, i0, k * 64, 0, bar);
-        tc::tma_load<CG>(to + 8192, map, i0 + 64, k * 64, 0, bar);
-    }
+    if (F == kRowsMN)
+        for (int i = 0; i < rows; i += 64) tc::tma_load<CG>(to + i * 128, map, i0 + i, k * 64, 0, bar);
 }
 
-constexpr int kTileK = 64, kHalf = 128;  // a block holds 128 rows of A and 128 of B
-constexpr int kStages = 6;
-constexpr int kBytesHalf = kHalf * kTileK * 2, kBytesStage = 2 * kBytesHalf;
-constexpr int kProductSmem = kStages * kBytesStage + 1024;
-constexpr int kProductThreads = 256;
+constexpr int kTileK = 64, kHalf = 128;  // a block holds 128 rows of A
+constexpr int kBytesA = kHalf * kTileK * 2;
+constexpr int kRingBytes = 6 * 2 * kBytesA;  // 192 KB
+template <int CG>
+struct RingOf {
+    static constexpr int kRowsB = CG == 2 ? 128 : 256;  // most rows of B in a block
+    static constexpr int kStageBytes = kBytesA + kRowsB * kTileK * 2, kStages = kRingBytes / kStageBytes;
+};
+constexpr int kProductSmem = kRingBytes + 1024;
+constexpr int kEpilogueWarps = 8, kProductThreads = 128 + 32 * kEpilogueWarps;
+constexpr int kPieces = kEpilogueWarps / 4;  // pieces of a row's part of a tile
+constexpr int kAccStride = 256;  // TMEM columns of an accumulator
 
 struct ProductShape {
     int M, N, K;
+    int tile_n;    // columns of a tile
     int mt, nt;    // tiles
     int group;     // row tiles that are taken together
     int splits;    // parts of K
@@ -87,9 +96,8 @@ template <class Epi, Form FA, Form FB, int CG>
 __global__ void __launch_bounds__(kProductThreads, 1)
     k_product(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
               const ProductShape s, const Epi epi) {
-    constexpr int kTileN = kHalf * CG;
     constexpr bool A_MN = is_mn(FA), B_MN = is_mn(FB);
-    constexpr uint32_t kCols = 2 * kTileN;  // TMEM columns: two accumulators
+    constexpr int kStages = RingOf<CG>::kStages, kStageBytes = RingOf<CG>::kStageBytes;
     extern __shared__ unsigned char raw[];
     __shared__ __align__(8) uint64_t bars[2 * kStages + 5];
     __shared__ uint32_t tmem_at;
@@ -99,6 +107,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
     const uint32_t acc_full = empty + 8 * kStages, acc_empty = acc_full + 16, drained = acc_empty + 16;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = CG == 2 ? tc::cluster_rank() : 0;
+    const int rows_b = s.tile_n / CG;
     const int64_t tiles = (int64_t)s.mt * s.nt * s.splits, first = blockIdx.x / CG, step = gridDim.x / CG;
 
     if (threadIdx.x == 0) {
@@ -108,7 +117,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
         }
         for (int i = 0; i < 2; ++i) {
             tc::mbar_init(acc_full + 8 * i, 1);
-            tc::mbar_init(acc_empty + 8 * i, 4 * CG);
+            tc::mbar_init(acc_empty + 8 * i, kEpilogueWarps * CG);
         }
         tc::mbar_init(drained, 1);
         stop = 0;
@@ -116,12 +125,14 @@ __global__ void __launch_bounds__(kProductThreads, 1)
         tc::prefetch_map(&map_a);
         tc::prefetch_map(&map_b);
     }
-    if (warp == 2) tc::tmem_alloc<CG>(tc::smem_u32(&tmem_at), kCols);
+    if (warp == 2) tc::tmem_alloc<CG>(tc::smem_u32(&tmem_at), 2 * kAccStride);
     tc::fence_before();
     __syncthreads();
     if (CG == 2) tc::cluster_sync();  // the other block's barriers are ready
     tc::fence_after();
     const uint32_t tmem = tmem_at;
+    let_next_start();
+    after_previous();
     const int all_blocks = (s.K + kTileK - 1) / kTileK;
 
     if (warp == 0) {
@@ -132,7 +143,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
                 const int part = (int)(t % s.splits);
                 int m, n;
                 tile_at(s, t / s.splits, m, n);
-                const int m0 = (m * CG + (int)rank) * kHalf, n0 = (n * CG + (int)rank) * kHalf;
+                const int m0 = (m * CG + (int)rank) * kHalf, n0 = n * s.tile_n + (int)rank * rows_b;
                 const int k0 = part * s.k_blocks, k1 = min(k0 + s.k_blocks, all_blocks);
                 for (int k = k0; k < k1; ++k, ++it) {
                     const int st = (int)(it % kStages);
@@ -140,12 +151,12 @@ __global__ void __launch_bounds__(kProductThreads, 1)
                         ok = false;
                         break;
                     }
-                    const uint32_t a = ring + st * kBytesStage, b = a + kBytesHalf;
+                    const uint32_t a = ring + st * kStageBytes, b = a + kBytesA;
                     // a pair's loads all count on the first block's barrier
                     const uint32_t bar = CG == 2 ? tc::in_block(full + 8 * st, 0) : full + 8 * st;
-                    if (rank == 0) tc::mbar_expect(full + 8 * st, CG * kBytesStage);
-                    load_half<CG, FA>(a, &map_a, m0, k, bar);
-                    load_half<CG, FB>(b, &map_b, n0, k, bar);
+                    if (rank == 0) tc::mbar_expect(full + 8 * st, CG * (kBytesA + rows_b * kTileK * 2));
+                    load_slice<CG, FA>(a, &map_a, m0, kHalf, k, bar);
+                    load_slice<CG, FB>(b, &map_b, n0, rows_b, k, bar);
                 }
             }
             // after giving up: the copies still in flight land before the block ends
@@ -159,7 +170,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
         }
     } else if (warp == 1) {
         if (lane == 0 && rank == 0) {
-            constexpr uint32_t idesc = tc::instr_desc(kHalf * CG, kTileN, A_MN, B_MN);
+            const uint32_t idesc = tc::instr_desc(kHalf * CG, s.tile_n, A_MN, B_MN);
             // 16 k further: 32 bytes along a K-major row, two groups of 8 k in the MN-major form
             constexpr uint32_t step_a = A_MN ? 2048 : 32, step_b = B_MN ? 2048 : 32;
             int64_t it = 0;
@@ -181,10 +192,10 @@ __global__ void __launch_bounds__(kProductThreads, 1)
                         break;
                     }
                     tc::fence_after();
-                    const uint32_t a = ring + st * kBytesStage, b = a + kBytesHalf;
+                    const uint32_t a = ring + st * kStageBytes, b = a + kBytesA;
 #pragma unroll
                     for (int kk = 0; kk < kTileK / 16; ++kk)
-                        tc::mma<CG>(tmem + buf * kTileN, tc::smem_desc(a + kk * step_a, A_MN ? 8192 : 16, 1024),
+                        tc::mma<CG>(tmem + buf * kAccStride, tc::smem_desc(a + kk * step_a, A_MN ? 8192 : 16, 1024),
                                     tc::smem_desc(b + kk * step_b, B_MN ? 8192 : 16, 1024), idesc, k > k0 || kk > 0);
                     tc::mma_commit<CG>(empty + 8 * st);
                 }
@@ -195,7 +206,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
             tc::mbar_drain(drained, 0);
         }
     } else if (warp >= 4) {
-        const int quarter = warp - 4;
+        const int quarter = warp & 3, half = (warp - 4) >> 2;
         const int wide = Epi::kWhole ? (s.N + 63) & ~63 : s.N;
         int j = 0;
         for (int64_t t = first; t < tiles; t += step, ++j) {
@@ -204,6 +215,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
             tile_at(s, t / s.splits, mt, nt);
             const int buf = j & 1;
             const int64_t m = (int64_t)(mt * CG + (int)rank) * kHalf + quarter * 32 + lane;
+            const int n0 = nt * s.tile_n, n1 = min(n0 + s.tile_n, wide);
             const bool live = m < s.M;
             typename Epi::Row row;
             if (live) epi.begin(row, m, part);
@@ -211,11 +223,11 @@ __global__ void __launch_bounds__(kProductThreads, 1)
             const bool ok = tc::mbar_wait(acc_full + 8 * buf, (uint32_t)(j >> 1) & 1, &stop, 4);
             if (!__all_sync(~0u, ok)) break;
             tc::fence_after();
-            for (int c = 0; c < kTileN && nt * kTileN + c < wide; c += 32) {
+            const uint32_t acc = tmem + ((uint32_t)(quarter * 32) << 16) + buf * kAccStride;
+            for (int n = n0 + half * 32; n < n1; n += 32 * kPieces) {
                 float v[32];
-                tc::tmem_load32(tmem + ((uint32_t)(quarter * 32) << 16) + buf * kTileN + c, v);
-                const int n = nt * kTileN + c, left = s.N - n;
-                if (live) epi.chunk(row, m, n, left < 32 ? left : 32, v);
+                tc::tmem_load32(acc + (n - n0), v);
+                if (live) epi.chunk(row, m, n, min(min(32, n1 - n), s.N - n), v);
             }
             tc::fence_before();
             __syncwarp();
@@ -223,14 +235,14 @@ __global__ void __launch_bounds__(kProductThreads, 1)
                 if (CG == 2) tc::mbar_arrive_at(tc::in_block(acc_empty + 8 * buf, 0));
                 else tc::mbar_arrive(acc_empty + 8 * buf);
             }
-            if (live) epi.end(row, m, nt);
+            if (live) epi.end(row, m, kPieces * nt + half);
         }
     }
     tc::fence_before();
     __syncthreads();
     if (CG == 2) tc::cluster_sync();  // neither block ends while the other may still signal it
     tc::fence_after();
-    if (warp == 2) tc::tmem_free<CG>(tmem, kCols);
+    if (warp == 2) tc::tmem_free<CG>(tmem, 2 * kAccStride);
 }
 
 // ---- host side
@@ -240,71 +252,57 @@ __global__ void __launch_bounds__(kProductThreads, 1)
 int encode_map(CUtensorMap *map, const Matrix &m, int64_t rows, int64_t cols, bool panels, int box_rows,
                int box_panels);
 
-// I: the operand's extent along m or n, K along k.
+// I: the operand's extent along m or n, K along k; `rows` of I in a box.
 template <Form F>
-int map_of(CUtensorMap *map, const Matrix &m, int64_t I, int64_t K) {
-    if (F == kRowsK) return encode_map(map, m, I, K, false, kHalf, 1);
-    if (F == kPanelsK) return encode_map(map, m, I, K, true, kHalf, 1);
-    if (F == kPanelsMN) return encode_map(map, m, K, I, true, 64, 2);
+int map_of(CUtensorMap *map, const Matrix &m, int64_t I, int64_t K, int rows) {
+    if (F == kRowsK) return encode_map(map, m, I, K, false, rows, 1);
+    if (F == kPanelsK) return encode_map(map, m, I, K, true, rows, 1);
+    if (F == kPanelsMN) return encode_map(map, m, K, I, true, 64, rows / 64);
     return encode_map(map, m, K, I, false, 64, 1);
 }
 
-// How a product is cut: pairs of blocks from the point on where lone blocks'
-// tiles would not all fit on the SMs at once, and K in parts where there are
-// still fewer tiles than SMs (each part has at least 4 slices, none is empty).
+// How a product is cut.  A slice of 64 k costs a pair of blocks 512 cycles
+// (its 256 x 256 x 64 products), a lone block with n columns 256 + 2n (its
+// loads, 64 bytes a cycle); a tile costs some slices more for its start and
+// end, a part of K its sums written and read again.  The cheapest of: pairs;
+// lone blocks with as many columns as fill the SMs once, twice, ... (a
+// multiple of 16, of 64 where B is MN-major or the epilogue takes whole
+// columns); each whole, and with K in as many parts (of at least 4 slices) as
+// fill the SMs.
 struct ProductPlan {
-    int cg, splits;
+    int cg, splits, tile_n;
     int64_t mt, nt;
 };
-inline ProductPlan plan_product(int64_t M, int64_t N, int64_t K) {
-    const int64_t sms = sm_count(), blocks = ceil_div(K, kTileK);
-    ProductPlan p;
-    p.cg = M > kHalf && ceil_div(M, kHalf) * ceil_div(N, kHalf) > sms ? 2 : 1;
-    p.mt = ceil_div(M, kHalf * p.cg), p.nt = ceil_div(N, kHalf * p.cg);
-    int64_t s = sms / p.cg / (p.mt * p.nt > 0 ? p.mt * p.nt : 1);
-    if (s > blocks / 4) s = blocks / 4;
-    p.splits = s <= 1 ? 1 : (int)ceil_div(blocks, ceil_div(blocks, s));
-    return p;
-}
+ProductPlan plan_product(int64_t M, int64_t N, int64_t K, bool by_64, bool may_split);
 
-// A product without parts of K, whatever the plan says of them: its column
-// tiles are plan_product()'s.
 template <Form FA, Form FB, class Epi>
 int launch_product(const Matrix &A, const Matrix &B, int64_t M, int64_t N, int64_t K, const Epi &epi,
-                   cudaStream_t stream, int splits = 1) {
+                   const ProductPlan &p, cudaStream_t stream) {
     if (M <= 0 || N <= 0 || K <= 0) return PP_ERR_INTERNAL;
     CUtensorMap ma, mb;
-    int rc = map_of<FA>(&ma, A, M, K);
-    if (rc == PP_OK) rc = map_of<FB>(&mb, B, N, K);
+    int rc = map_of<FA>(&ma, A, M, K, kHalf);
+    if (rc == PP_OK) rc = map_of<FB>(&mb, B, N, K, p.tile_n / p.cg);
     if (rc != PP_OK) return rc;
-    const ProductPlan p = plan_product(M, N, K);
     ProductShape s;
     s.M = (int)M, s.N = (int)N, s.K = (int)K;
+    s.tile_n = p.tile_n;
     s.mt = (int)p.mt, s.nt = (int)p.nt;
-    s.splits = splits;
-    s.k_blocks = (int)ceil_div(ceil_div(K, kTileK), splits);
+    s.splits = p.splits;
+    s.k_blocks = (int)ceil_div(ceil_div(K, kTileK), p.splits);
     s.group = s.mt < 16 ? s.mt : 16;
-    const int64_t tiles = p.mt * p.nt * splits, most = sm_count() / p.cg;
-    const unsigned grid = (unsigned)(tiles < most ? tiles : most) * p.cg;
+    const int64_t tiles = p.mt * p.nt * p.splits, most = sm_count() / p.cg, grid = (tiles < most ? tiles : most) * p.cg;
     static std::atomic<uint64_t> ready[2];
-    if (p.cg == 1) {
-        rc = allow_smem(k_product<Epi, FA, FB, 1>, kProductSmem, ready[0]);
-        if (rc != PP_OK) return rc;
-        k_product<Epi, FA, FB, 1><<<grid, kProductThreads, kProductSmem, stream>>>(ma, mb, s, epi);
-        PPS_CUDA_TRY(cudaGetLastError());
-        return PP_OK;
-    }
-    rc = allow_smem(k_product<Epi, FA, FB, 2>, kProductSmem, ready[1]);
+    const auto kernel = p.cg == 1 ? k_product<Epi, FA, FB, 1> : k_product<Epi, FA, FB, 2>;
+    rc = allow_smem(kernel, kProductSmem, ready[p.cg - 1]);
     if (rc != PP_OK) return rc;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(grid), cfg.blockDim = dim3(kProductThreads), cfg.dynamicSmemBytes = kProductSmem;
-    cfg.stream = stream;
-    cudaLaunchAttribute pair;
-    pair.id = cudaLaunchAttributeClusterDimension;
-    pair.val.clusterDim.x = 2, pair.val.clusterDim.y = 1, pair.val.clusterDim.z = 1;
-    cfg.attrs = &pair, cfg.numAttrs = 1;
-    PPS_CUDA_TRY(cudaLaunchKernelEx(&cfg, k_product<Epi, FA, FB, 2>, ma, mb, s, epi));
-    return PP_OK;
+    return launch_after(kernel, grid, kProductThreads, kProductSmem, stream, p.cg, ma, mb, s, epi);
+}
+
+// A product that is not to be cut along K: its epilogue takes whole sums.
+template <Form FA, Form FB, class Epi>
+int whole_product(const Matrix &A, const Matrix &B, int64_t M, int64_t N, int64_t K, const Epi &epi,
+                  cudaStream_t stream) {
+    return launch_product<FA, FB>(A, B, M, N, K, epi, plan_product(M, N, K, is_mn(FB) || Epi::kWhole, false), stream);
 }
 
 // Parts of K: each part's sums apart, [part][M][ld].  Epilogues are local to
@@ -312,7 +310,7 @@ int launch_product(const Matrix &A, const Matrix &B, int64_t M, int64_t N, int64
 // them.
 namespace {
 struct PartEpi {
-    static constexpr bool kWhole = false;
+    static constexpr bool kWhole = true;
     float *parts;
     int64_t M, ld;
     struct Row {
@@ -320,7 +318,8 @@ struct PartEpi {
     };
     __device__ __forceinline__ void begin(Row &r, int64_t m, int part) const { r.p = parts + (part * M + m) * ld; }
     __device__ __forceinline__ void chunk(Row &r, int64_t, int64_t n, int cnt, const float (&v)[32]) const {
-        // ld is a multiple of 32: the columns past the last one are there to be written
+        // columns past the last one are there to be written, up to ld
+        if (n >= ld) return;
         float4 *p = reinterpret_cast<float4 *>(r.p + n);
 #pragma unroll
         for (int j = 0; j < 8; ++j) p[j] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
@@ -333,6 +332,8 @@ struct PartEpi {
 template <class Epi>
 __global__ void __launch_bounds__(128) k_join_parts(const float *parts, int splits, int64_t M, int64_t N, int64_t ld,
                                                     const Epi epi) {
+    let_next_start();
+    after_previous();
     const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x, per = ld / 32;
     const int64_t m = i / per, n = i % per * 32;
     if (m >= M || n >= N) return;
@@ -351,24 +352,24 @@ __global__ void __launch_bounds__(128) k_join_parts(const float *parts, int spli
     epi.end(row, m, 0);
 }
 
-// Floats of scratch memory that product_in_parts needs.
+// Floats of scratch memory that product_in_parts needs (B is MN-major there).
 inline int64_t part_floats(int64_t M, int64_t N, int64_t K) {
-    const int s = plan_product(M, N, K).splits;
+    const int s = plan_product(M, N, K, true, true).splits;
     return s > 1 ? s * M * round_up(N, 32) : 0;
 }
 
-// A product whose K is shared out where there are too few tiles for the SMs.
+// A product whose K is shared out where that is cheaper.
 template <Form FA, Form FB, class Epi>
 int product_in_parts(const Matrix &A, const Matrix &B, int64_t M, int64_t N, int64_t K, const Epi &epi, float *parts,
                      cudaStream_t stream) {
-    const int splits = plan_product(M, N, K).splits;
-    if (splits == 1) return launch_product<FA, FB>(A, B, M, N, K, epi, stream);
+    static_assert(is_mn(FB));
+    const ProductPlan p = plan_product(M, N, K, true, true);
+    if (p.splits == 1) return launch_product<FA, FB>(A, B, M, N, K, epi, p, stream);
     const int64_t ld = round_up(N, 32);
-    const int rc = launch_product<FA, FB>(A, B, M, N, K, PartEpi{parts, M, ld}, stream, splits);
+    const int rc = launch_product<FA, FB>(A, B, M, N, K, PartEpi{parts, M, ld}, p, stream);
     if (rc != PP_OK) return rc;
-    k_join_parts<Epi><<<(unsigned)ceil_div(M * (ld / 32), 128), 128, 0, stream>>>(parts, splits, M, N, ld, epi);
-    PPS_CUDA_TRY(cudaGetLastError());
-    return PP_OK;
+    return launch_after(k_join_parts<Epi>, ceil_div(M * (ld / 32), 128), 128, 0, stream, 1, parts, p.splits, M, N, ld,
+                        epi);
 }
 
 // 32 columns of a row as bf16, or added to / stored as 32-bit floats.

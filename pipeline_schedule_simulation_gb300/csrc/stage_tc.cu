@@ -57,6 +57,43 @@ int encode_map(CUtensorMap *map, const Matrix &m, int64_t rows, int64_t cols, bo
     return r == CUDA_SUCCESS ? PP_OK : PP_ERR_CUDA;
 }
 
+ProductPlan plan_product(int64_t M, int64_t N, int64_t K, bool by_64, bool may_split) {
+    const int64_t sms = sm_count(), blocks = ceil_div(K, kTileK);
+    const double start = 6;  // slices that a tile's start and end cost
+    // a slice's 512 cycles at about 1.8 GHz, in bytes of memory traffic
+    const double part_cost = 8. * (double)M * (double)N / 1.9e6;
+    ProductPlan best{};
+    double least = 0;
+    const auto consider = [&](int cg, int64_t tile_n) {
+        ProductPlan p;
+        p.cg = cg, p.tile_n = (int)tile_n;
+        p.mt = ceil_div(M, kHalf * cg), p.nt = ceil_div(N, tile_n);
+        const int64_t tiles = p.mt * p.nt, units = sms / cg;
+        const double slice = cg == 2 ? 1. : (256. + 2. * (double)tile_n) / 512.;
+        int64_t parts = may_split ? units / tiles : 1;
+        if (parts > blocks / 4) parts = blocks / 4;
+        for (int64_t s : {(int64_t)1, parts}) {
+            if (s < 1) continue;
+            s = ceil_div(blocks, ceil_div(blocks, s));  // no part is empty
+            const double cost = (double)ceil_div(tiles * s, units) * ((double)ceil_div(blocks, s) * slice + start) +
+                                (s > 1 ? (double)s * part_cost + start : 0.);
+            p.splits = (int)s;
+            if (best.cg == 0 || cost < least) best = p, least = cost;
+        }
+    };
+    if (M > kHalf) consider(2, 256);
+    const int64_t mt = ceil_div(M, kHalf), to = by_64 ? 64 : 16;
+    for (int64_t waves = 1; waves <= 4; ++waves) {
+        const int64_t columns = sms * waves / mt;  // column tiles that fill the SMs
+        if (columns < 1) continue;
+        const int64_t n = round_up(ceil_div(N, columns), to);
+        if (n <= 256) consider(1, n);
+    }
+    consider(1, 128);
+    consider(1, 256);
+    return best;
+}
+
 int sm_count() {
     static std::atomic<int> known[64];
     int dev = 0, n = 0;
@@ -80,6 +117,8 @@ template <bool VEC>
 __global__ void __launch_bounds__(256) k_copy_rows(const uint16_t *x, int64_t stride, int64_t T, int64_t H,
                                                    const int64_t *target, int64_t V, uint16_t *out, int64_t ld,
                                                    int64_t panel) {
+    let_next_start();
+    after_previous();
     const int64_t per = (H + 63) / 64 * 8, units = T * per, step = (int64_t)gridDim.x * blockDim.x;
     for (int64_t u = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; u < units; u += step) {
         const int64_t t = u / per, c = (u - t * per) * 8, left = H - c;
@@ -100,12 +139,8 @@ int launch_copy_rows(const uint16_t *x, int64_t stride, int64_t T, int64_t H, co
                      uint16_t *out, int64_t ld, int64_t panel, cudaStream_t stream) {
     const int64_t blocks = ceil_div(T * ceil_div(H, 64) * 8, 256);
     const unsigned grid = (unsigned)(blocks < 152 * 64 ? blocks : 152 * 64);
-    if (rows_aligned(x, stride, T, 2))
-        k_copy_rows<true><<<grid, 256, 0, stream>>>(x, stride, T, H, target, V, out, ld, panel);
-    else
-        k_copy_rows<false><<<grid, 256, 0, stream>>>(x, stride, T, H, target, V, out, ld, panel);
-    PPS_CUDA_TRY(cudaGetLastError());
-    return PP_OK;
+    return launch_after(rows_aligned(x, stride, T, 2) ? k_copy_rows<true> : k_copy_rows<false>, grid, 256, 0, stream, 1, x,
+                        stride, T, H, target, V, out, ld, panel);
 }
 
 }  // namespace pps
