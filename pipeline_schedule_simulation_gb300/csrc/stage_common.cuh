@@ -56,10 +56,10 @@ int allow_smem(K kernel, int bytes, std::atomic<uint64_t> &ready) {
 // running: the kernel calls after_previous() before it touches memory, which
 // waits until that one is done.  cluster: blocks that form a cluster.
 template <class... P, class... A>
-int launch_after(void (*kernel)(P...), int64_t grid, int threads, int smem, cudaStream_t stream, int cluster,
+int launch_after(void (*kernel)(P...), dim3 grid, int threads, int smem, cudaStream_t stream, int cluster,
                  const A &...args) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)grid), cfg.blockDim = dim3(threads), cfg.dynamicSmemBytes = smem, cfg.stream = stream;
+    cfg.gridDim = grid, cfg.blockDim = dim3(threads), cfg.dynamicSmemBytes = smem, cfg.stream = stream;
     cudaLaunchAttribute at[2];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;
@@ -68,6 +68,11 @@ int launch_after(void (*kernel)(P...), int64_t grid, int threads, int smem, cuda
     cfg.attrs = at, cfg.numAttrs = cluster > 1 ? 2 : 1;
     PPS_CUDA_TRY(cudaLaunchKernelEx(&cfg, kernel, args...));
     return PP_OK;
+}
+template <class... P, class... A>
+int launch_after(void (*kernel)(P...), int64_t grid, int threads, int smem, cudaStream_t stream, int cluster,
+                 const A &...args) {
+    return launch_after(kernel, dim3((unsigned)grid), threads, smem, stream, cluster, args...);
 }
 __device__ __forceinline__ void after_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 // Lets the kernel after this one take free places on the SMs and wait there.

@@ -56,6 +56,8 @@ struct JoinForward {
 template <int NT, int NV, bool VEC, bool KEEP>
 __global__ void __launch_bounds__(NT) k_join_forward(const JoinForward a) {
     __shared__ __align__(16) float sh[2][32];
+    let_next_start();
+    after_previous();
     const float inv_h = 1.f / (float)a.H;
     for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
         const uint16_t *g = a.gate ? a.gate + (a.rows_per_gate > 0 ? t / a.rows_per_gate : 0) * a.sg : nullptr;
@@ -126,6 +128,9 @@ __global__ void __launch_bounds__(NT) k_join_forward(const JoinForward a) {
     }
 }
 
+constexpr int kNarrow = 512;  // widths up to this: a warp to a row, kWarps rows a block at once
+constexpr int kWarps = 8;
+
 // Threads of a ring block for this width, two vectors of 8 columns each (one
 // up to 1024 columns); 0 where a row is too wide.
 int ring_threads(int64_t H) { return H <= 2048 ? 128 : H <= 4096 ? 256 : H <= 8192 ? 512 : 0; }
@@ -139,11 +144,12 @@ Items items_of(int64_t T, int64_t H, int64_t rows_per_gate) {
     Items it;
     it.rows_per_gate = rows_per_gate > 0 && rows_per_gate < T ? rows_per_gate : T;
     it.groups = ceil_div(T, it.rows_per_gate);
-    // one run of rows for each ring block that is resident, or one for each of
-    // two direct blocks on an SM
+    // one run of rows for each block that is resident on the GPU (two to an SM
+    // where rows are too wide for the ring)
     const int threads = ring_threads(H);
-    const int64_t want = (int64_t)sm_count() * (threads ? 512 / threads : 2);
+    const int64_t want = (int64_t)sm_count() * (H <= kNarrow ? (H <= 256 ? 4 : 2) : threads ? 512 / threads : 2);
     it.rows = ceil_div(T, want);
+    if (H <= kNarrow && it.rows < kWarps) it.rows = kWarps;
     if (it.rows > it.rows_per_gate) it.rows = it.rows_per_gate;
     it.per_group = ceil_div(it.rows_per_gate, it.rows);
     it.count = it.groups * it.per_group;
@@ -160,7 +166,8 @@ struct JoinBackward {
     int H;
     uint16_t *dx, *df;
     int64_t sdx, sdf;
-    float *part_pre, *part_post;  // [items][H]: sum dh n2, sum d n1
+    float *part_pre, *part_post;  // [items][ld]: sum dh n2, sum d n1
+    int64_t ld;
     Items it;
 };
 
@@ -183,6 +190,8 @@ __device__ __forceinline__ void load_saved(const uint16_t *p, int64_t s, const K
 template <int NT, int NV, bool VEC, bool PACKED>
 __global__ void __launch_bounds__(NT) k_join_backward(const JoinBackward a) {
     __shared__ __align__(16) float sh[2][32];
+    let_next_start();
+    after_previous();
     const float inv_h = 1.f / (float)a.H;
     const int64_t group = blockIdx.x / a.it.per_group, part = blockIdx.x % a.it.per_group;
     const int64_t first = group * a.it.rows_per_gate + part * a.it.rows;
@@ -256,9 +265,188 @@ __global__ void __launch_bounds__(NT) k_join_backward(const JoinBackward a) {
 #pragma unroll
         for (int j = 0; j < 8; ++j)
             if (c + j < a.H) {
-                a.part_pre[blockIdx.x * (int64_t)a.H + c + j] = sum_pre[i][j];
-                a.part_post[blockIdx.x * (int64_t)a.H + c + j] = sum_post[i][j];
+                a.part_pre[blockIdx.x * a.ld + c + j] = sum_pre[i][j];
+                a.part_post[blockIdx.x * a.ld + c + j] = sum_post[i][j];
             }
+    }
+}
+
+// ---- narrow rows: a warp to a row
+
+// H <= 256 * NV: sums need no other warp, and a block of 8 warps has 8 rows in
+// flight (a block of threads to a row would leave most of them idle).
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(~0u, v, o);
+    return v;
+}
+
+template <int NV, bool VEC, bool KEEP>
+__global__ void __launch_bounds__(32 * kWarps) k_join_forward_narrow(const JoinForward a) {
+    let_next_start();
+    after_previous();
+    const float inv_h = 1.f / (float)a.H;
+    const int lane = threadIdx.x & 31;
+    for (int64_t t = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5); t < a.T; t += (int64_t)gridDim.x * kWarps) {
+        const uint16_t *g = a.gate ? a.gate + (a.rows_per_gate > 0 ? t / a.rows_per_gate : 0) * a.sg : nullptr;
+        Raw8 fr[NV];
+        float y[NV][8], ss = 0.f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (i * 32 + lane) * 8, left = a.H - c, at = left > 0 ? c : 0;
+            fr[i] = load8<VEC>(a.f + t * a.sf + at, left);
+            load8_bf16<VEC>(a.x + t * a.sx + at, left, y[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            float f[8];
+            widen(fr[i], f);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) ss += f[j] * f[j];
+        }
+        const float r1 = rsqrtf(warp_sum(ss) * inv_h + a.eps);
+        ss = 0.f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (i * 32 + lane) * 8, left = a.H - c, at = left > 0 ? c : 0;
+            float w[8], f[8];
+            load8_bf16<VEC>(a.w_post + at, left, w);
+            if (g) {
+                load8_bf16<VEC>(g + at, left, f);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) w[j] *= f[j];
+            }
+            widen(fr[i], f);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                y[i][j] = a.alpha * y[i][j] + w[j] * (f[j] * r1);
+                ss += y[i][j] * y[i][j];
+            }
+            const Raw8 yr = narrow(y[i]);
+            if (left > 0) store8<VEC>(a.y + t * a.sy + c, left, yr);
+            if (KEEP) {
+                int ey, ef;
+                const uint2 by = pack8(yr, ey), bf = pack8(fr[i], ef);
+                if (left > 0) {
+                    store8_bytes<VEC>(a.ky.q + t * a.ky.sq + c, left, by);
+                    store8_bytes<VEC>(a.kf.q + t * a.kf.sq + c, left, bf);
+                    if ((lane & 7) == 0) {
+                        a.ky.e[t * a.ky.se + c / kBlock] = (int8_t)ey;
+                        a.kf.e[t * a.kf.se + c / kBlock] = (int8_t)ef;
+                    }
+                }
+            }
+        }
+        const float r2 = rsqrtf(warp_sum(ss) * inv_h + a.eps);
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (i * 32 + lane) * 8, left = a.H - c;
+            if (left > 0) {
+                float w[8];
+                load8_bf16<VEC>(a.w_pre + c, left, w);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) w[j] *= y[i][j] * r2;
+                store8_bf16<VEC>(a.h + t * a.sh + c, left, w);
+            }
+        }
+        if (lane == 0) {
+            a.rstd_post[t] = r1;
+            a.rstd_pre[t] = r2;
+        }
+    }
+}
+
+template <int NV, bool VEC, bool PACKED>
+__global__ void __launch_bounds__(32 * kWarps, NV == 1 ? 4 : 2) k_join_backward_narrow(const JoinBackward a) {
+    let_next_start();
+    after_previous();
+    __shared__ float sums[2][kWarps][NV * 256];
+    const float inv_h = 1.f / (float)a.H;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t group = blockIdx.x / a.it.per_group, part = blockIdx.x % a.it.per_group;
+    const int64_t first = group * a.it.rows_per_gate + part * a.it.rows;
+    int64_t last = min(first + a.it.rows, (group + 1) * a.it.rows_per_gate);
+    last = min(last, a.T);
+    float sum_pre[NV][8] = {}, sum_post[NV][8] = {};
+    for (int64_t t = first + warp; t < last; t += kWarps) {
+        const float r1 = a.rstd_post[t], r2 = a.rstd_pre[t];
+        Raw8 dr[NV], ur[NV];
+        float n2[NV][8], n1[NV][8], ss = 0.f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (i * 32 + lane) * 8, left = a.H - c, at = left > 0 ? c : 0;
+            dr[i] = load8<VEC>(a.dh + t * a.sdh + at, left);
+            ur[i] = a.dy ? load8<VEC>(a.dy + t * a.sdy + at, left) : Raw8{};
+            load_saved<VEC, PACKED>(a.y, a.sy, a.ky, t, c, left, n2[i]);
+            load_saved<VEC, PACKED>(a.f, a.sf, a.kf, t, c, left, n1[i]);
+        }
+        float d[NV][8];
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (i * 32 + lane) * 8, left = a.H - c, at = left > 0 ? c : 0;
+            float w[8];
+            widen(dr[i], d[i]);
+            load8_bf16<VEC>(a.w_pre + at, left, w);  // from the L1 cache: registers are what limits this kernel
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                n2[i][j] *= r2;
+                n1[i][j] *= r1;
+                sum_pre[i][j] += d[i][j] * n2[i][j];
+                d[i][j] *= w[j];
+                ss += d[i][j] * n2[i][j];
+            }
+        }
+        const float m2 = warp_sum(ss) * (inv_h * r2);
+        ss = 0.f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (i * 32 + lane) * 8, left = a.H - c, at = left > 0 ? c : 0;
+            float u[8], gw[8];
+            widen(ur[i], u);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                d[i][j] = fmaf(r2, d[i][j], fmaf(-m2, n2[i][j], u[j]));
+                u[j] = a.alpha * d[i][j];
+            }
+            if (left > 0) store8_bf16<VEC>(a.dx + t * a.sdx + c, left, u);
+            load8_bf16<VEC>(a.w_post + at, left, gw);
+            if (a.gate) {
+                load8_bf16<VEC>(a.gate + group * a.sg + at, left, u);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) gw[j] *= u[j];
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                sum_post[i][j] += d[i][j] * n1[i][j];
+                d[i][j] *= gw[j];
+                ss += d[i][j] * n1[i][j];
+            }
+        }
+        const float m1 = warp_sum(ss) * (inv_h * r1);
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (i * 32 + lane) * 8, left = a.H - c;
+            float u[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) u[j] = fmaf(r1, d[i][j], -m1 * n1[i][j]);
+            if (left > 0) store8_bf16<VEC>(a.df + t * a.sdf + c, left, u);
+        }
+    }
+    // the warps' sums, in the order of the warps
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            sums[0][warp][(i * 32 + lane) * 8 + j] = sum_pre[i][j];
+            sums[1][warp][(i * 32 + lane) * 8 + j] = sum_post[i][j];
+        }
+    __syncthreads();
+    for (int c = threadIdx.x; c < a.H; c += 32 * kWarps) {
+        float p = 0.f, q = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) p += sums[0][w][c], q += sums[1][w][c];
+        a.part_pre[blockIdx.x * a.ld + c] = p;
+        a.part_post[blockIdx.x * a.ld + c] = q;
     }
 }
 
@@ -298,6 +486,8 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_join_forward_ring(const JoinF
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ __align__(16) float sh[2][32];
     __shared__ int stop;
+    let_next_start();
+    after_previous();
     const uint32_t row_bytes = 2u * a.H;
     Ring<2> ring{tc::smem_u32(smem) + kRingHeader, tc::smem_u32(smem), 2 * row_bytes, stages,
                  {{(const unsigned char *)a.f, 2 * a.sf, row_bytes, 0}, {(const unsigned char *)a.x, 2 * a.sx, row_bytes, row_bytes}}};
@@ -414,6 +604,8 @@ __global__ void __launch_bounds__(NT, 512 / NT) k_join_backward_ring(const JoinB
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ __align__(16) float sh[2][32];
     __shared__ int stop;
+    let_next_start();
+    after_previous();
     const uint32_t wide = 2u * a.H, saved = PACKED ? (uint32_t)a.H : wide, at_dy = wide + 2 * saved;
     Ring<4> ring{tc::smem_u32(smem) + kRingHeader, tc::smem_u32(smem), at_dy + (a.dy ? wide : 0), stages,
                  {{(const unsigned char *)a.dh, 2 * a.sdh, wide, 0},
@@ -559,7 +751,7 @@ __global__ void __launch_bounds__(NT, 512 / NT) k_join_backward_ring(const JoinB
     for (int i = 0; i < NV; ++i) {
         const int c = (i * NT + (int)threadIdx.x) * 8;
         if (c < a.H) {
-            float *p = a.part_pre + blockIdx.x * (int64_t)a.H + c, *q = a.part_post + blockIdx.x * (int64_t)a.H + c;
+            float *p = a.part_pre + blockIdx.x * a.ld + c, *q = a.part_post + blockIdx.x * a.ld + c;
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 reinterpret_cast<float4 *>(p)[j] =
@@ -589,45 +781,41 @@ RingPlan ring_plan(int64_t H, int64_t stage_bytes, int threads_on_sm) {
 
 // Column sums of the items' parts, in a fixed order: blockIdx.y = 0 joins all
 // items (the part of the norm after the block weighted by its group's gate), the
-// others a gate group each.  8 quads of columns and 32 runs of items a block.
-template <bool VEC>
+// others a gate group each.  8 quads of columns and 32 runs of items a block,
+// each run four items at a time.
 __global__ void __launch_bounds__(256) k_join_columns(const float *part_pre, const float *part_post, Items it, int H,
-                                                      const uint16_t *w_post, const uint16_t *gate, int64_t sg,
-                                                      float *dw_post, float *dw_pre, float *dgate, int64_t sdg) {
+                                                      int64_t ld, const uint16_t *w_post, const uint16_t *gate,
+                                                      int64_t sg, float *dw_post, float *dw_pre, float *dgate,
+                                                      int64_t sdg) {
+    after_previous();
     __shared__ float s0[32][33], s1[32][33];
+    constexpr int kAhead = 4;
     const int quad = threadIdx.x & 7, row = threadIdx.x >> 3;
-    const int h = blockIdx.x * 32 + quad * 4;
+    const int h = blockIdx.x * 32 + quad * 4;  // rows of the parts are whole quads
     const bool all = blockIdx.y == 0;
-    const auto load4 = [&](const float *p, float (&v)[4]) {
-        if (VEC) {
-            const float4 q = *reinterpret_cast<const float4 *>(p);
-            v[0] = q.x, v[1] = q.y, v[2] = q.z, v[3] = q.w;
-        } else {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) v[j] = h + j < H ? p[j] : 0.f;
-        }
-    };
     for (int64_t g = all ? 0 : blockIdx.y - 1; g < (all ? 1 : it.groups); g += all ? 1 : gridDim.y - 1) {
         const int64_t from = all ? 0 : g * it.per_group, to = all ? it.count : (g + 1) * it.per_group;
         float a[4] = {}, b[4] = {};
         if (h < H) {
-#pragma unroll 4
-            for (int64_t i = from + row; i < to; i += 32) {
-                float p[4];
-                load4(part_post + i * H + h, p);
-                if (all) {
-                    float r[4];
-                    load4(part_pre + i * H + h, r);
+            for (int64_t i = from + row; i < to; i += 32 * kAhead) {
+                float4 p[kAhead], r[kAhead];
+                float u[kAhead][4];
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) a[j] += r[j];
-                    if (gate) {
-                        const uint16_t *gr = gate + i / it.per_group * sg + h;
+                for (int k = 0; k < kAhead; ++k) {
+                    const int64_t j = i + 32 * k;
+                    const bool in = j < to;
+                    p[k] = in ? *reinterpret_cast<const float4 *>(part_post + j * ld + h) : make_float4(0.f, 0.f, 0.f, 0.f);
+                    r[k] = in && all ? *reinterpret_cast<const float4 *>(part_pre + j * ld + h)
+                                     : make_float4(0.f, 0.f, 0.f, 0.f);
+                    const uint16_t *gr = gate + j / it.per_group * sg + h;
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) p[j] *= h + j < H ? bf16_to_f32(gr[j]) : 0.f;
-                    }
+                    for (int c = 0; c < 4; ++c) u[k][c] = in && all && gate && h + c < H ? bf16_to_f32(gr[c]) : 1.f;
                 }
 #pragma unroll
-                for (int j = 0; j < 4; ++j) b[j] += p[j];
+                for (int k = 0; k < kAhead; ++k) {
+                    a[0] += r[k].x, a[1] += r[k].y, a[2] += r[k].z, a[3] += r[k].w;
+                    b[0] += p[k].x * u[k][0], b[1] += p[k].y * u[k][1], b[2] += p[k].z * u[k][2], b[3] += p[k].w * u[k][3];
+                }
             }
         }
 #pragma unroll
@@ -656,30 +844,38 @@ __global__ void __launch_bounds__(256) k_join_columns(const float *part_pre, con
 }
 
 template <bool VEC, bool KEEP>
-void forward_by_width(const JoinForward &a, unsigned grid, cudaStream_t s) {
-    if (a.H <= 1024) k_join_forward<128, 1, VEC, KEEP><<<grid, 128, 0, s>>>(a);
-    else if (a.H <= 2048) k_join_forward<256, 1, VEC, KEEP><<<grid, 256, 0, s>>>(a);
-    else if (a.H <= 4096) k_join_forward<512, 1, VEC, KEEP><<<grid, 512, 0, s>>>(a);
-    else if (a.H <= 8192) k_join_forward<512, 2, VEC, KEEP><<<grid, 512, 0, s>>>(a);
-    else k_join_forward<1024, 2, VEC, KEEP><<<grid, 1024, 0, s>>>(a);
+int forward_by_width(const JoinForward &a, unsigned grid, cudaStream_t s) {
+    if (a.H <= kNarrow) {
+        const int64_t want = ceil_div(a.T, kWarps), most = (int64_t)sm_count() * 8;
+        const int64_t g = want < most ? want : most;
+        return a.H <= 256 ? launch_after(k_join_forward_narrow<1, VEC, KEEP>, g, 32 * kWarps, 0, s, 1, a)
+                          : launch_after(k_join_forward_narrow<2, VEC, KEEP>, g, 32 * kWarps, 0, s, 1, a);
+    }
+    if (a.H <= 1024) return launch_after(k_join_forward<128, 1, VEC, KEEP>, grid, 128, 0, s, 1, a);
+    if (a.H <= 2048) return launch_after(k_join_forward<256, 1, VEC, KEEP>, grid, 256, 0, s, 1, a);
+    if (a.H <= 4096) return launch_after(k_join_forward<512, 1, VEC, KEEP>, grid, 512, 0, s, 1, a);
+    if (a.H <= 8192) return launch_after(k_join_forward<512, 2, VEC, KEEP>, grid, 512, 0, s, 1, a);
+    return launch_after(k_join_forward<1024, 2, VEC, KEEP>, grid, 1024, 0, s, 1, a);
 }
 
 template <bool VEC, bool PACKED>
-void backward_by_width(const JoinBackward &a, cudaStream_t s) {
+int backward_by_width(const JoinBackward &a, cudaStream_t s) {
     const unsigned grid = (unsigned)a.it.count;
-    if (a.H <= 1024) k_join_backward<128, 1, VEC, PACKED><<<grid, 128, 0, s>>>(a);
-    else if (a.H <= 2048) k_join_backward<256, 1, VEC, PACKED><<<grid, 256, 0, s>>>(a);
-    else if (a.H <= 4096) k_join_backward<512, 1, VEC, PACKED><<<grid, 512, 0, s>>>(a);
-    else if (a.H <= 8192) k_join_backward<512, 2, VEC, PACKED><<<grid, 512, 0, s>>>(a);
-    else k_join_backward<1024, 2, VEC, PACKED><<<grid, 1024, 0, s>>>(a);
+    if (a.H <= kNarrow)
+        return a.H <= 256 ? launch_after(k_join_backward_narrow<1, VEC, PACKED>, grid, 32 * kWarps, 0, s, 1, a)
+                          : launch_after(k_join_backward_narrow<2, VEC, PACKED>, grid, 32 * kWarps, 0, s, 1, a);
+    if (a.H <= 1024) return launch_after(k_join_backward<128, 1, VEC, PACKED>, grid, 128, 0, s, 1, a);
+    if (a.H <= 2048) return launch_after(k_join_backward<256, 1, VEC, PACKED>, grid, 256, 0, s, 1, a);
+    if (a.H <= 4096) return launch_after(k_join_backward<512, 1, VEC, PACKED>, grid, 512, 0, s, 1, a);
+    if (a.H <= 8192) return launch_after(k_join_backward<512, 2, VEC, PACKED>, grid, 512, 0, s, 1, a);
+    return launch_after(k_join_backward<1024, 2, VEC, PACKED>, grid, 1024, 0, s, 1, a);
 }
 
 template <class K, class A>
 int launch_ring(K kernel, const A &a, const RingPlan &p, unsigned grid, std::atomic<uint64_t> &ready, cudaStream_t s) {
     const int rc = allow_smem(kernel, 226 * 1024, ready);
     if (rc != PP_OK) return rc;
-    kernel<<<grid, p.threads, p.smem, s>>>(a, p.stages);
-    return PP_OK;
+    return launch_after(kernel, grid, p.threads, (int)p.smem, s, 1, a, p.stages);
 }
 
 template <bool KEEP>
@@ -713,13 +909,15 @@ bool bad_kept(const Kept &k, int64_t H) { return !k.q || !k.e || k.sq < H || k.s
 
 struct BackSpace {
     float *pre, *post;
+    int64_t ld;
     size_t bytes;
 };
 BackSpace back_space(void *ws, const Items &it, int64_t H) {
     Carve c{static_cast<unsigned char *>(ws)};
     BackSpace s;
-    s.pre = c.take<float>(it.count * H);
-    s.post = c.take<float>(it.count * H);
+    s.ld = round_up(H, 8);
+    s.pre = c.take<float>(it.count * s.ld);
+    s.post = c.take<float>(it.count * s.ld);
     s.bytes = c.used;
     return s;
 }
@@ -754,17 +952,12 @@ extern "C" int pp_stage_join_forward(const uint16_t *x, int64_t stride_x, const 
                      (!keep || (kept_aligned(y_q, stride_yq, T) && kept_aligned(f_q, stride_fq, T)));
     // the ring pays from about two rows a block on
     const RingPlan p = ring_plan(H, 4 * H, 1024);
-    if (vec && p.threads && H % 8 == 0 && T >= 2 * (int64_t)sm_count() * p.blocks) {
-        const int rr = keep ? forward_ring<true>(a, p, stream) : forward_ring<false>(a, p, stream);
-        if (rr != PP_OK) return rr;
-        PPS_CUDA_TRY(cudaGetLastError());
-        return PP_OK;
+    if (vec && p.threads && H > kNarrow && H % 8 == 0 && T >= 2 * (int64_t)sm_count() * p.blocks) {
+        return keep ? forward_ring<true>(a, p, stream) : forward_ring<false>(a, p, stream);
     }
     const unsigned grid = (unsigned)(T < 152 * 16 ? T : 152 * 16);
-    if (vec) keep ? forward_by_width<true, true>(a, grid, stream) : forward_by_width<true, false>(a, grid, stream);
-    else keep ? forward_by_width<false, true>(a, grid, stream) : forward_by_width<false, false>(a, grid, stream);
-    PPS_CUDA_TRY(cudaGetLastError());
-    return PP_OK;
+    if (vec) return keep ? forward_by_width<true, true>(a, grid, stream) : forward_by_width<true, false>(a, grid, stream);
+    return keep ? forward_by_width<false, true>(a, grid, stream) : forward_by_width<false, false>(a, grid, stream);
 }
 
 extern "C" size_t pp_stage_join_backward_workspace(int64_t T, int64_t H, int64_t rows_per_gate) {
@@ -798,7 +991,7 @@ extern "C" int pp_stage_join_backward(const uint16_t *dh, int64_t stride_dh, con
     JoinBackward a{dh, dy, y, f, w_post, w_pre, gate, stride_dh, stride_dy, stride_y, stride_f, stride_gate,
                    Kept{const_cast<int8_t *>(y_q), const_cast<int8_t *>(y_e), stride_yq, stride_ye},
                    Kept{const_cast<int8_t *>(f_q), const_cast<int8_t *>(f_e), stride_fq, stride_fe},
-                   rstd_post, rstd_pre, alpha, T, (int)H, dx, df, stride_dx, stride_df, s.pre, s.post, it};
+                   rstd_post, rstd_pre, alpha, T, (int)H, dx, df, stride_dx, stride_df, s.pre, s.post, s.ld, it};
     if (bad_rows(dh, stride_dh, H) || (dy && bad_rows(dy, stride_dy, H)) || bad_rows(w_post, H, H) ||
         bad_rows(w_pre, H, H) || (gate && bad_rows(gate, stride_gate, H)) || bad_rows(dx, stride_dx, H) ||
         bad_rows(df, stride_df, H) || !rstd_post || !rstd_pre || ((uintptr_t)rstd_post & 3) ||
@@ -817,19 +1010,13 @@ extern "C" int pp_stage_join_backward(const uint16_t *dh, int64_t stride_dh, con
     // bulk copies take whole 16 bytes
     const bool whole = packed ? H % 16 == 0 && rows_aligned(y_q, stride_yq, T, 1) && rows_aligned(f_q, stride_fq, T, 1)
                               : H % 8 == 0;
-    if (vec && whole && p.threads && it.rows >= 2) {
-        const int rr = packed ? backward_ring<true>(a, p, stream) : backward_ring<false>(a, p, stream);
-        if (rr != PP_OK) return rr;
-    } else if (vec) packed ? backward_by_width<true, true>(a, stream) : backward_by_width<true, false>(a, stream);
-    else packed ? backward_by_width<false, true>(a, stream) : backward_by_width<false, false>(a, stream);
-    PPS_CUDA_TRY(cudaGetLastError());
+    int rr;
+    if (vec && whole && p.threads && H > kNarrow && it.rows >= 2)
+        rr = packed ? backward_ring<true>(a, p, stream) : backward_ring<false>(a, p, stream);
+    else if (vec) rr = packed ? backward_by_width<true, true>(a, stream) : backward_by_width<true, false>(a, stream);
+    else rr = packed ? backward_by_width<false, true>(a, stream) : backward_by_width<false, false>(a, stream);
+    if (rr != PP_OK) return rr;
     const dim3 grid((unsigned)ceil_div(H, 32), 1 + (gate ? (unsigned)(it.groups < 1024 ? it.groups : 1024) : 0));
-    if (H % 4 == 0)
-        k_join_columns<true><<<grid, 256, 0, stream>>>(s.pre, s.post, it, (int)H, w_post, gate, stride_gate, dw_post,
-                                                       dw_pre, dgate, stride_dgate);
-    else
-        k_join_columns<false><<<grid, 256, 0, stream>>>(s.pre, s.post, it, (int)H, w_post, gate, stride_gate, dw_post,
-                                                        dw_pre, dgate, stride_dgate);
-    PPS_CUDA_TRY(cudaGetLastError());
-    return PP_OK;
+    return launch_after(k_join_columns, grid, 256, 0, stream, 1, (const float *)s.pre, (const float *)s.post, it, (int)H,
+                        s.ld, w_post, gate, stride_gate, dw_post, dw_pre, dgate, stride_dgate);
 }

@@ -112,33 +112,37 @@ int sm_count() {
 
 namespace {
 
-// A thread copies 8 columns of a row.
+// A thread copies 8 columns of 4 rows.
+constexpr int kCopyRows = 4;
 template <bool VEC>
 __global__ void __launch_bounds__(256) k_copy_rows(const uint16_t *x, int64_t stride, int64_t T, int64_t H,
                                                    const int64_t *target, int64_t V, uint16_t *out, int64_t ld,
                                                    int64_t panel) {
     let_next_start();
     after_previous();
-    const int64_t per = (H + 63) / 64 * 8, units = T * per, step = (int64_t)gridDim.x * blockDim.x;
-    for (int64_t u = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; u < units; u += step) {
-        const int64_t t = u / per, c = (u - t * per) * 8, left = H - c;
-        bool in = true;
-        if (target) {
-            const int64_t g = target[t];
-            in = g >= 0 && g < V;
+    const int64_t per = (H + 63) / 64 * 8, u = (int64_t)blockIdx.x * blockDim.x + threadIdx.x, g = u / per;
+    const int64_t t = g * kCopyRows, c = (u - g * per) * 8, left = H - c;
+    Raw8 r[kCopyRows];
+#pragma unroll
+    for (int i = 0; i < kCopyRows; ++i) {
+        bool in = t + i < T && left > 0;
+        if (in && target) {
+            const int64_t v = target[t + i];
+            in = v >= 0 && v < V;
         }
-        Raw8 r{};
-        if (in && left > 0) r = load8<VEC>(x + t * stride + c, left);
-        store8<true>(out + t * ld + c / 64 * panel + c % 64, 8, r);
+        r[i] = Raw8{};
+        if (in) r[i] = load8<VEC>(x + (t + i) * stride + c, left);
     }
+#pragma unroll
+    for (int i = 0; i < kCopyRows; ++i)
+        if (t + i < T) store8<true>(out + (t + i) * ld + c / 64 * panel + c % 64, 8, r[i]);
 }
 
 }  // namespace
 
 int launch_copy_rows(const uint16_t *x, int64_t stride, int64_t T, int64_t H, const int64_t *target, int64_t V,
                      uint16_t *out, int64_t ld, int64_t panel, cudaStream_t stream) {
-    const int64_t blocks = ceil_div(T * ceil_div(H, 64) * 8, 256);
-    const unsigned grid = (unsigned)(blocks < 152 * 64 ? blocks : 152 * 64);
+    const int64_t grid = ceil_div(ceil_div(T, kCopyRows) * ceil_div(H, 64) * 8, 256);
     return launch_after(rows_aligned(x, stride, T, 2) ? k_copy_rows<true> : k_copy_rows<false>, grid, 256, 0, stream, 1, x,
                         stride, T, H, target, V, out, ld, panel);
 }
