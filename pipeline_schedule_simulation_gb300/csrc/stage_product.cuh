@@ -20,6 +20,15 @@
 // columns (128 bytes), each panel's rows one after the other, so that a box is
 // one run of memory in either form.
 //
+// The tensor cores add up in 32 bits but cut the sum off below its last bit at
+// every step, so a long sum shrinks, by about 6e-7 of itself in 1024 steps of k
+// where the terms have one sign and in proportion to that number (16384 steps
+// in a row: 2.5e-6 with K in five parts, 4e-6 for 4096 steps of one part).  A sum
+// is therefore taken in runs of 1024 k: each run goes to the other accumulator,
+// and the epilogue's threads, which hold the tile in registers, add the runs up
+// with rounding.  A run lasts 8192 cycles, taking it over less than a tenth of
+// that, beside the next run.
+//
 // CG = 2: a pair of blocks shares a tile of 256 x 256: each holds half of A
 // and half of B, so that a slice costs each SM 32 KB of loads for its half of
 // 256 x 256 x 64 products.
@@ -71,7 +80,12 @@ struct RingOf {
 constexpr int kProductSmem = kRingBytes + 1024;
 constexpr int kEpilogueWarps = 8, kProductThreads = 128 + 32 * kEpilogueWarps;
 constexpr int kPieces = kEpilogueWarps / 4;  // pieces of a row's part of a tile
+constexpr int kRuns = 256 / 32 / kPieces;    // runs of 32 columns in a piece
 constexpr int kAccStride = 256;  // TMEM columns of an accumulator
+constexpr int kRun = 32;         // slices (2048 k) that one accumulator adds up
+// Registers: the epilogue's 8 warps take what the first 4 can spare.
+constexpr int kLaunchRegs = 168, kFewRegs = 64, kManyRegs = 216;
+static_assert(128 * kFewRegs + 32 * kEpilogueWarps * kManyRegs <= kProductThreads * kLaunchRegs);
 
 struct ProductShape {
     int M, N, K;
@@ -84,13 +98,25 @@ struct ProductShape {
 
 // Tile number -> (row tile, column tile): `group` row tiles at a time run
 // through all column tiles, so that their slices of A stay in the L2 cache.
-__device__ __forceinline__ void tile_at(const ProductShape &s, int64_t i, int &m, int &n) {
-    const int64_t per = (int64_t)s.group * s.nt;
-    const int g = (int)(i / per), first = g * s.group;
-    const int rows = min(s.group, s.mt - first), r = (int)(i - g * per);
+__device__ __forceinline__ void tile_at(const ProductShape &s, uint32_t i, int &m, int &n) {
+    const uint32_t per = (uint32_t)s.group * s.nt, g = i / per;
+    const int first = (int)g * s.group, rows = min(s.group, s.mt - first), r = (int)(i - g * per);
     m = first + r % rows;
     n = r / rows;
 }
+
+// A place in a ring of N: the slot, and the parity of its current round.
+template <int N>
+struct Place {
+    int slot = 0;
+    uint32_t round = 0;
+    __device__ __forceinline__ void next() {
+        if (++slot == N) slot = 0, round ^= 1;
+    }
+    __device__ __forceinline__ void back() {
+        if (--slot < 0) slot = N - 1, round ^= 1;
+    }
+};
 
 template <class Epi, Form FA, Form FB, int CG>
 __global__ void __launch_bounds__(kProductThreads, 1)
@@ -108,7 +134,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = CG == 2 ? tc::cluster_rank() : 0;
     const int rows_b = s.tile_n / CG;
-    const int64_t tiles = (int64_t)s.mt * s.nt * s.splits, first = blockIdx.x / CG, step = gridDim.x / CG;
+    const uint32_t tiles = (uint32_t)s.mt * s.nt * s.splits, first = blockIdx.x / CG, step = gridDim.x / CG;
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < kStages; ++i) {
@@ -135,107 +161,139 @@ __global__ void __launch_bounds__(kProductThreads, 1)
     after_previous();
     const int all_blocks = (s.K + kTileK - 1) / kTileK;
 
-    if (warp == 0) {
-        if (lane == 0) {
-            int64_t it = 0;
-            bool ok = true;
-            for (int64_t t = first; t < tiles && ok; t += step) {
-                const int part = (int)(t % s.splits);
-                int m, n;
-                tile_at(s, t / s.splits, m, n);
-                const int m0 = (m * CG + (int)rank) * kHalf, n0 = n * s.tile_n + (int)rank * rows_b;
-                const int k0 = part * s.k_blocks, k1 = min(k0 + s.k_blocks, all_blocks);
-                for (int k = k0; k < k1; ++k, ++it) {
-                    const int st = (int)(it % kStages);
-                    if (!tc::mbar_wait(empty + 8 * st, (uint32_t)(it / kStages + 1) & 1, &stop, 1)) {
-                        ok = false;
-                        break;
+    if (warp < 4) {
+        tc::give_registers<kFewRegs>();
+        if (warp == 0) {
+            if (lane == 0) {
+                Place<kStages> at;
+                int loaded = 0;  // slots that have been filled, up to all of them
+                bool ok = true;
+                for (uint32_t t = first; t < tiles && ok; t += step) {
+                    const int part = (int)(t % s.splits);
+                    int m, n;
+                    tile_at(s, t / s.splits, m, n);
+                    const int m0 = (m * CG + (int)rank) * kHalf, n0 = n * s.tile_n + (int)rank * rows_b;
+                    const int k0 = part * s.k_blocks, k1 = min(k0 + s.k_blocks, all_blocks);
+                    for (int k = k0; k < k1; ++k, at.next()) {
+                        const int st = at.slot;
+                        if (!tc::mbar_wait(empty + 8 * st, at.round ^ 1, &stop, 1)) {
+                            ok = false;
+                            break;
+                        }
+                        const uint32_t a = ring + st * kStageBytes, b = a + kBytesA;
+                        // a pair's loads all count on the first block's barrier
+                        const uint32_t bar = CG == 2 ? tc::in_block(full + 8 * st, 0) : full + 8 * st;
+                        if (rank == 0) tc::mbar_expect(full + 8 * st, CG * (kBytesA + rows_b * kTileK * 2));
+                        load_slice<CG, FA>(a, &map_a, m0, kHalf, k, bar);
+                        load_slice<CG, FB>(b, &map_b, n0, rows_b, k, bar);
+                        if (loaded < kStages) ++loaded;
                     }
-                    const uint32_t a = ring + st * kStageBytes, b = a + kBytesA;
-                    // a pair's loads all count on the first block's barrier
-                    const uint32_t bar = CG == 2 ? tc::in_block(full + 8 * st, 0) : full + 8 * st;
-                    if (rank == 0) tc::mbar_expect(full + 8 * st, CG * (kBytesA + rows_b * kTileK * 2));
-                    load_slice<CG, FA>(a, &map_a, m0, kHalf, k, bar);
-                    load_slice<CG, FB>(b, &map_b, n0, rows_b, k, bar);
+                }
+                // after giving up: the copies still in flight land before the block ends
+                if (!ok) {
+                    if (rank == 0)
+                        for (; loaded > 0; --loaded) {
+                            at.back();
+                            tc::mbar_drain(full + 8 * at.slot, at.round);
+                        }
+                    else
+                        tc::let_land();
                 }
             }
-            // after giving up: the copies still in flight land before the block ends
-            if (!ok) {
-                if (rank == 0)
-                    for (int64_t j = it > kStages ? it - kStages : 0; j < it; ++j)
-                        tc::mbar_drain(full + 8 * (int)(j % kStages), (uint32_t)(j / kStages) & 1);
-                else
-                    tc::let_land();
-            }
-        }
-    } else if (warp == 1) {
-        if (lane == 0 && rank == 0) {
-            const uint32_t idesc = tc::instr_desc(kHalf * CG, s.tile_n, A_MN, B_MN);
-            // 16 k further: 32 bytes along a K-major row, two groups of 8 k in the MN-major form
-            constexpr uint32_t step_a = A_MN ? 2048 : 32, step_b = B_MN ? 2048 : 32;
-            int64_t it = 0;
-            int j = 0;
-            bool ok = true;
-            for (int64_t t = first; t < tiles && ok; t += step, ++j) {
-                const int part = (int)(t % s.splits);
-                const int k0 = part * s.k_blocks, k1 = min(k0 + s.k_blocks, all_blocks);
-                const int buf = j & 1;
-                if (!tc::mbar_wait(acc_empty + 8 * buf, (uint32_t)((j >> 1) + 1) & 1, &stop, 2)) {
-                    ok = false;
-                    break;
-                }
-                tc::fence_after();
-                for (int k = k0; k < k1; ++k, ++it) {
-                    const int st = (int)(it % kStages);
-                    if (!tc::mbar_wait(full + 8 * st, (uint32_t)(it / kStages) & 1, &stop, 3)) {
-                        ok = false;
-                        break;
-                    }
-                    tc::fence_after();
-                    const uint32_t a = ring + st * kStageBytes, b = a + kBytesA;
+        } else if (warp == 1) {
+            if (lane == 0 && rank == 0) {
+                const uint32_t idesc = tc::instr_desc(kHalf * CG, s.tile_n, A_MN, B_MN);
+                // 16 k further: 32 bytes along a K-major row, two groups of 8 k in the MN-major form
+                constexpr uint32_t step_a = A_MN ? 2048 : 32, step_b = B_MN ? 2048 : 32;
+                Place<kStages> at;
+                Place<2> run;
+                bool ok = true;
+                for (uint32_t t = first; t < tiles && ok; t += step) {
+                    const int part = (int)(t % s.splits);
+                    const int k0 = part * s.k_blocks, k1 = min(k0 + s.k_blocks, all_blocks);
+                    for (int r0 = k0; r0 < k1 && ok; r0 += kRun, run.next()) {
+                        const int buf = run.slot, r1 = min(r0 + kRun, k1);
+                        if (!tc::mbar_wait(acc_empty + 8 * buf, run.round ^ 1, &stop, 2)) {
+                            ok = false;
+                            break;
+                        }
+                        tc::fence_after();
+                        for (int k = r0; k < r1; ++k, at.next()) {
+                            const int st = at.slot;
+                            if (!tc::mbar_wait(full + 8 * st, at.round, &stop, 3)) {
+                                ok = false;
+                                break;
+                            }
+                            tc::fence_after();
+                            const uint32_t a = ring + st * kStageBytes, b = a + kBytesA;
 #pragma unroll
-                    for (int kk = 0; kk < kTileK / 16; ++kk)
-                        tc::mma<CG>(tmem + buf * kAccStride, tc::smem_desc(a + kk * step_a, A_MN ? 8192 : 16, 1024),
-                                    tc::smem_desc(b + kk * step_b, B_MN ? 8192 : 16, 1024), idesc, k > k0 || kk > 0);
-                    tc::mma_commit<CG>(empty + 8 * st);
+                            for (int kk = 0; kk < kTileK / 16; ++kk)
+                                tc::mma<CG>(tmem + buf * kAccStride, tc::smem_desc(a + kk * step_a, A_MN ? 8192 : 16, 1024),
+                                            tc::smem_desc(b + kk * step_b, B_MN ? 8192 : 16, 1024), idesc,
+                                            k > r0 || kk > 0);
+                            tc::mma_commit<CG>(empty + 8 * st);
+                        }
+                        if (ok) tc::mma_commit<CG>(acc_full + 8 * buf);
+                    }
                 }
-                if (ok) tc::mma_commit<CG>(acc_full + 8 * buf);
+                // the MMAs have finished before TMEM is given back
+                tc::mma_commit<CG>(drained);
+                tc::mbar_drain(drained, 0);
             }
-            // the MMAs have finished before TMEM is given back
-            tc::mma_commit<CG>(drained);
-            tc::mbar_drain(drained, 0);
         }
-    } else if (warp >= 4) {
+    } else {
+        tc::take_registers<kManyRegs>();
         const int quarter = warp & 3, half = (warp - 4) >> 2;
         const int wide = Epi::kWhole ? (s.N + 63) & ~63 : s.N;
-        int j = 0;
-        for (int64_t t = first; t < tiles; t += step, ++j) {
+        Place<2> run;
+        bool ok = true;
+        for (uint32_t t = first; t < tiles && ok; t += step) {
             const int part = (int)(t % s.splits);
             int mt, nt;
             tile_at(s, t / s.splits, mt, nt);
-            const int buf = j & 1;
             const int64_t m = (int64_t)(mt * CG + (int)rank) * kHalf + quarter * 32 + lane;
-            const int n0 = nt * s.tile_n, n1 = min(n0 + s.tile_n, wide);
+            const int first_n = nt * s.tile_n, n0 = first_n + half * 32, n1 = min(first_n + s.tile_n, wide);
+            const int k0 = part * s.k_blocks, k1 = min(k0 + s.k_blocks, all_blocks);
             const bool live = m < s.M;
             typename Epi::Row row;
             if (live) epi.begin(row, m, part);
-            // lanes give up one by one: the warp goes on together
-            const bool ok = tc::mbar_wait(acc_full + 8 * buf, (uint32_t)(j >> 1) & 1, &stop, 4);
-            if (!__all_sync(~0u, ok)) break;
-            tc::fence_after();
-            const uint32_t acc = tmem + ((uint32_t)(quarter * 32) << 16) + buf * kAccStride;
-            for (int n = n0 + half * 32; n < n1; n += 32 * kPieces) {
-                float v[32];
-                tc::tmem_load32(acc + (n - n0), v);
-                if (live) epi.chunk(row, m, n, min(min(32, n1 - n), s.N - n), v);
+            float sum[kRuns][32];
+            for (int r0 = k0; r0 < k1; r0 += kRun, run.next()) {
+                const int buf = run.slot;
+                // lanes give up one by one: the warp goes on together
+                ok = __all_sync(~0u, tc::mbar_wait(acc_full + 8 * buf, run.round, &stop, 4));
+                if (!ok) break;
+                tc::fence_after();
+                const uint32_t acc = tmem + ((uint32_t)(quarter * 32) << 16) + buf * kAccStride + half * 32;
+                const bool more = r0 > k0;
+#pragma unroll
+                for (int i = 0; i < kRuns; ++i)
+                    if (n0 + i * kPieces * 32 < n1) {
+                        if (more) {
+                            float v[32];
+                            tc::tmem_load32(acc + i * kPieces * 32, v);
+#pragma unroll
+                            for (int c = 0; c < 32; ++c) sum[i][c] += v[c];
+                        } else {
+                            tc::tmem_load32(acc + i * kPieces * 32, sum[i]);
+                        }
+                    }
+                tc::fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    if (CG == 2) tc::mbar_arrive_at(tc::in_block(acc_empty + 8 * buf, 0));
+                    else tc::mbar_arrive(acc_empty + 8 * buf);
+                }
             }
-            tc::fence_before();
+            if (ok && live) {
+#pragma unroll
+                for (int i = 0; i < kRuns; ++i) {
+                    const int n = n0 + i * kPieces * 32;
+                    if (n < n1) epi.chunk(row, m, n, min(min(32, n1 - n), s.N - n), sum[i]);
+                }
+                epi.end(row, m, kPieces * nt + half);
+            }
             __syncwarp();
-            if (lane == 0) {
-                if (CG == 2) tc::mbar_arrive_at(tc::in_block(acc_empty + 8 * buf, 0));
-                else tc::mbar_arrive(acc_empty + 8 * buf);
-            }
-            if (live) epi.end(row, m, kPieces * nt + half);
         }
     }
     tc::fence_before();
@@ -279,6 +337,7 @@ template <Form FA, Form FB, class Epi>
 int launch_product(const Matrix &A, const Matrix &B, int64_t M, int64_t N, int64_t K, const Epi &epi,
                    const ProductPlan &p, cudaStream_t stream) {
     if (M <= 0 || N <= 0 || K <= 0) return PP_ERR_INTERNAL;
+    if (p.mt * p.nt * p.splits > 0x7FFFFFFF) return PP_ERR_SIZE;  // tiles are counted in 32 bits
     CUtensorMap ma, mb;
     int rc = map_of<FA>(&ma, A, M, K, kHalf);
     if (rc == PP_OK) rc = map_of<FB>(&mb, B, N, K, p.tile_n / p.cg);
@@ -293,6 +352,12 @@ int launch_product(const Matrix &A, const Matrix &B, int64_t M, int64_t N, int64
     const int64_t tiles = p.mt * p.nt * p.splits, most = sm_count() / p.cg, grid = (tiles < most ? tiles : most) * p.cg;
     static std::atomic<uint64_t> ready[2];
     const auto kernel = p.cg == 1 ? k_product<Epi, FA, FB, 1> : k_product<Epi, FA, FB, 2>;
+    if (!ready[p.cg - 1].load(std::memory_order_relaxed)) {
+        // the epilogue's warps would wait forever for registers that the launch does not have
+        cudaFuncAttributes fa;
+        PPS_CUDA_TRY(cudaFuncGetAttributes(&fa, kernel));
+        if (fa.numRegs < kLaunchRegs) return PP_ERR_INTERNAL;
+    }
     rc = allow_smem(kernel, kProductSmem, ready[p.cg - 1]);
     if (rc != PP_OK) return rc;
     return launch_after(kernel, grid, kProductThreads, kProductSmem, stream, p.cg, ma, mb, s, epi);

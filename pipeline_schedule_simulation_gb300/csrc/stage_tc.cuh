@@ -175,6 +175,16 @@ __device__ __forceinline__ void tmem_load32(uint32_t addr, float (&v)[32]) {
     for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
 }
 
+// Register shares of a warpgroup, out of what the block was launched with.
+template <int N>
+__device__ __forceinline__ void give_registers() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void take_registers() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+
 // Shared-memory matrix descriptor: 128-byte swizzle, tiles of 64 bf16 (128
 // bytes) by 8 rows.  K-major: rows are 128 bytes of k, groups of 8 rows lie
 // `sbo` apart.  MN-major: rows are 128 bytes of m (or n), groups of 8 k lie
