@@ -31,7 +31,7 @@ __device__ __forceinline__ float rebase(float s, float m, float r) {
 __device__ __forceinline__ bool inside(int64_t target, int64_t V) { return target >= 0 && target < V; }
 
 struct StatsEpi {
-    static constexpr bool kWhole = false;
+    static constexpr bool kStore = false, kWhole = false;
     const int64_t *target;
     int64_t T, V;
     float2 *part;   // [pieces][T]: largest logit, sum of exponentials
@@ -40,7 +40,7 @@ struct StatsEpi {
         float m, s;
         int64_t target;
     };
-    __device__ __forceinline__ void begin(Row &r, int64_t t, int) const {
+    __device__ __forceinline__ void begin(Row &r, int64_t t) const {
         r.m = kNegInf;
         r.s = 0.f;
         r.target = target ? target[t] : -1;
@@ -51,8 +51,10 @@ struct StatsEpi {
 #pragma unroll
             for (int j = 0; j < 32; ++j) m = j < cnt ? fmaxf(m, v[j]) : m;
         } else {
+            float c[4] = {v[0], v[1], v[2], v[3]};
 #pragma unroll
-            for (int j = 0; j < 32; ++j) m = fmaxf(m, v[j]);
+            for (int j = 4; j < 32; ++j) c[j & 3] = fmaxf(c[j & 3], v[j]);
+            m = fmaxf(fmaxf(m, fmaxf(c[0], c[1])), fmaxf(c[2], c[3]));
         }
         const float ref = ref_of(m);
         float s[4] = {rebase(r.s, r.m, ref), 0.f, 0.f, 0.f};
@@ -78,7 +80,7 @@ struct StatsEpi {
 
 // d of one piece: columns v0 .. of the vocabulary, as bf16.
 struct GradEpi {
-    static constexpr bool kWhole = true;
+    static constexpr bool kStore = false, kWhole = true;
     const int64_t *target;
     const float *lse, *weight;
     int64_t T, V, v0;
@@ -88,7 +90,7 @@ struct GradEpi {
         int64_t at;  // the target's column counted from the piece's first
         bool in;
     };
-    __device__ __forceinline__ void begin(Row &r, int64_t t, int) const {
+    __device__ __forceinline__ void begin(Row &r, int64_t t) const {
         const int64_t g = target[t];
         r.in = inside(g, V);
         r.c = weight ? weight[t] : 1.f;
@@ -111,68 +113,93 @@ struct GradEpi {
             for (int j = 0; j < 32; ++j)
                 if (!r.in || j >= cnt) p[j] = 0.f;
         }
-        store_bf16(d + (n >> 6) * (T * 64) + t * 64 + (n & 63), 32, true, p);
+        store_bf16(d + (n >> 6) * (T * 64) + t * 64 + (n & 63), p);
     }
     __device__ __forceinline__ void end(Row &, int64_t, int64_t) const {}
 };
 
-// dx: pieces add up in 32 bits; the last one writes the result.
+// dx: pieces add up in 32 bits; the last one writes the result.  A row that is
+// left out is 0, whatever w holds.
 struct DxEpi {
-    static constexpr bool kWhole = false;
-    float *acc;  // [T][ld_acc]
+    static constexpr bool kStore = true, kWhole = false;
+    float *acc;  // [T][ld_acc], ld_acc a multiple of 4
     uint16_t *dx;
     const int64_t *target;
     int64_t V, ld_acc, ld;
     float scale;
     bool first, last, vec;
-    struct Row {
-        bool in;
-    };
-    __device__ __forceinline__ void begin(Row &r, int64_t t, int) const { r.in = inside(target[t], V); }
-    __device__ __forceinline__ void chunk(Row &r, int64_t t, int64_t n, int cnt, const float (&v)[32]) const {
+    __device__ __forceinline__ void run(int64_t t, int64_t n, const float (&v)[32], int) const {
         float s[32];
-        if (first) {
 #pragma unroll
-            for (int j = 0; j < 32; ++j) s[j] = v[j];
+        for (int j = 0; j < 32; ++j) s[j] = v[j];
+        if (!first) add_f32(s, acc + t * ld_acc + n);
+        if (last) {
+            const bool in = inside(target[t], V);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) s[j] = in ? s[j] * scale : 0.f;
+            store_bf16(dx + t * ld + n, s);
         } else {
-            load_f32(acc + t * ld_acc + n, cnt, true, s);
-#pragma unroll
-            for (int j = 0; j < 32; ++j) s[j] += v[j];
-        }
-        if (last) {  // a row that is left out is 0, whatever w holds
-#pragma unroll
-            for (int j = 0; j < 32; ++j) s[j] = r.in ? s[j] * scale : 0.f;
-            store_bf16(dx + t * ld + n, cnt, vec, s);
-        } else {
-            store_f32(acc + t * ld_acc + n, cnt, true, s);
+            store_f32(acc + t * ld_acc + n, s);
         }
     }
-    __device__ __forceinline__ void end(Row &, int64_t, int64_t) const {}
+    __device__ __forceinline__ void quad(int64_t t, int64_t n, int left, const float4 &v, int) const {
+        float4 s = v;
+        float4 *a = reinterpret_cast<float4 *>(acc + t * ld_acc + n);
+        if (!first) {
+            const float4 b = *a;
+            s.x += b.x, s.y += b.y, s.z += b.z, s.w += b.w;
+        }
+        if (last) {
+            const float c = scale;
+            s = inside(target[t], V) ? make_float4(s.x * c, s.y * c, s.z * c, s.w * c) : make_float4(0.f, 0.f, 0.f, 0.f);
+            store_quad(dx + t * ld + n, left, s);
+        } else {
+            *a = s;
+        }
+    }
+    __device__ __forceinline__ void one(int64_t t, int64_t n, float v, int) const {
+        float s = first ? v : acc[t * ld_acc + n] + v;
+        if (last) dx[t * ld + n] = inside(target[t], V) ? f32_to_bf16(s * scale) : 0;
+        else acc[t * ld_acc + n] = s;
+    }
 };
 
 struct DwEpi {
-    static constexpr bool kWhole = false;
+    static constexpr bool kStore = true, kWhole = false;
     uint16_t *dw16;  // one of the two
     float *dw32;
     int64_t ld;
     float scale;
     bool add, vec;
-    struct Row {};
-    __device__ __forceinline__ void begin(Row &, int64_t, int) const {}
-    __device__ __forceinline__ void chunk(Row &, int64_t m, int64_t n, int cnt, const float (&v)[32]) const {
+    __device__ __forceinline__ void run(int64_t m, int64_t n, const float (&v)[32], int) const {
         float s[32];
-        if (dw32 && add) {
-            load_f32(dw32 + m * ld + n, cnt, vec, s);
 #pragma unroll
-            for (int j = 0; j < 32; ++j) s[j] += v[j] * scale;
+        for (int j = 0; j < 32; ++j) s[j] = v[j] * scale;
+        if (dw16) {
+            store_bf16(dw16 + m * ld + n, s);
         } else {
-#pragma unroll
-            for (int j = 0; j < 32; ++j) s[j] = v[j] * scale;
+            if (add) add_f32(s, dw32 + m * ld + n);
+            store_f32(dw32 + m * ld + n, s);
         }
-        if (dw32) store_f32(dw32 + m * ld + n, cnt, vec, s);
-        else store_bf16(dw16 + m * ld + n, cnt, vec, s);
     }
-    __device__ __forceinline__ void end(Row &, int64_t, int64_t) const {}
+    __device__ __forceinline__ void quad(int64_t m, int64_t n, int left, const float4 &v, int) const {
+        float4 s = make_float4(v.x * scale, v.y * scale, v.z * scale, v.w * scale);
+        if (dw16) {
+            store_quad(dw16 + m * ld + n, left, s);
+            return;
+        }
+        float *p = dw32 + m * ld + n;
+        if (add) {
+            const float4 b = load_quad(p, left);
+            s.x += b.x, s.y += b.y, s.z += b.z, s.w += b.w;
+        }
+        store_quad(p, left, s);
+    }
+    __device__ __forceinline__ void one(int64_t m, int64_t n, float v, int) const {
+        const float s = v * scale;
+        if (dw16) dw16[m * ld + n] = f32_to_bf16(s);
+        else dw32[m * ld + n] = add ? dw32[m * ld + n] + s : s;
+    }
 };
 
 // 8 tokens a block: 32 lanes along the pieces of each.  First the largest
@@ -295,7 +322,7 @@ BackwardSpace backward_space(void *ws, const uint16_t *x, int64_t sx, const uint
     Carve c{static_cast<unsigned char *>(ws)};
     BackwardSpace s;
     s.piece = piece_of(T, V);
-    s.ld_acc = round_up(H, 32);
+    s.ld_acc = round_up(H, 4);
     s.w = aligned(c, w, sw, V, H, ceil_div(T, 256));
     s.x = c.take<uint16_t>(T * round_up(H, 64));
     s.d = c.take<uint16_t>(T * s.piece);

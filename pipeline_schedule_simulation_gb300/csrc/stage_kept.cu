@@ -73,25 +73,33 @@ __global__ void __launch_bounds__(kThreads) k_unpack(const int8_t *q, int64_t st
 }
 
 struct WgradEpi {
-    static constexpr bool kWhole = false;
+    static constexpr bool kStore = true, kWhole = false;
     const float *add;
     float *dw;
     int64_t ld_add, ld;
     bool vec;
-    struct Row {};
-    __device__ __forceinline__ void begin(Row &, int64_t, int) const {}
-    __device__ __forceinline__ void chunk(Row &, int64_t m, int64_t n, int cnt, const float (&v)[32]) const {
+    __device__ __forceinline__ void run(int64_t m, int64_t n, const float (&v)[32], int) const {
         if (add) {
             float s[32];
-            load_f32(add + m * ld_add + n, cnt, vec, s);
 #pragma unroll
-            for (int j = 0; j < 32; ++j) s[j] += v[j];
-            store_f32(dw + m * ld + n, cnt, vec, s);
+            for (int j = 0; j < 32; ++j) s[j] = v[j];
+            add_f32(s, add + m * ld_add + n);
+            store_f32(dw + m * ld + n, s);
         } else {
-            store_f32(dw + m * ld + n, cnt, vec, v);
+            store_f32(dw + m * ld + n, v);
         }
     }
-    __device__ __forceinline__ void end(Row &, int64_t, int64_t) const {}
+    __device__ __forceinline__ void quad(int64_t m, int64_t n, int left, const float4 &v, int) const {
+        float4 s = v;
+        if (add) {
+            const float4 b = load_quad(add + m * ld_add + n, left);
+            s.x += b.x, s.y += b.y, s.z += b.z, s.w += b.w;
+        }
+        store_quad(dw + m * ld + n, left, s);
+    }
+    __device__ __forceinline__ void one(int64_t m, int64_t n, float v, int) const {
+        dw[m * ld + n] = add ? add[m * ld_add + n] + v : v;
+    }
 };
 
 bool bad_kept(const int8_t *q, int64_t sq, const int8_t *e, int64_t se, int64_t H) {

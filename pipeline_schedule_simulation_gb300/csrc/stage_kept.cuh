@@ -95,17 +95,27 @@ __device__ __forceinline__ void unpack8(uint2 b, float step, float (&v)[8]) {
     }
 }
 
-// 8 consecutive elements at p, of which `left` exist (all 8 in the vector form).
+// 8 consecutive elements at p, of which `left` exist.  Unaligned ones are put
+// together from the aligned words that hold them: a word with a byte of the
+// row in it can be read whole, and no other is read.
 template <bool VEC>
 __device__ __forceinline__ Raw8 load8(const uint16_t *p, int64_t left) {
-    Raw8 r;
+    Raw8 r{};
     if (VEC && left >= 8) {
         const uint4 w = *reinterpret_cast<const uint4 *>(p);
         r.w[0] = w.x, r.w[1] = w.y, r.w[2] = w.z, r.w[3] = w.w;
-    } else {
+    } else if (left > 0) {
+        const uint32_t off = (uint32_t)((uintptr_t)p & 2) >> 1;  // halves before p in its word
+        const uint32_t *a = reinterpret_cast<const uint32_t *>(p - off);
+        const int n = left < 8 ? (int)left : 8;
+        uint32_t w[5];
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-            r.w[j] = (2 * j < left ? (uint32_t)p[2 * j] : 0u) | (2 * j + 1 < left ? (uint32_t)p[2 * j + 1] : 0u) << 16;
+        for (int j = 0; j < 5; ++j) w[j] = 2 * j < n + (int)off ? a[j] : 0u;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            r.w[j] = __funnelshift_r(w[j], w[j + 1], 16 * off);
+            if (2 * j + 1 >= n) r.w[j] &= 2 * j >= n ? 0u : 0xFFFFu;
+        }
     }
     return r;
 }
@@ -130,11 +140,19 @@ __device__ __forceinline__ void store8_bf16(uint16_t *p, int64_t left, const flo
 template <bool VEC>
 __device__ __forceinline__ uint2 load8_bytes(const int8_t *p, int64_t left) {
     if (VEC && left >= 8) return *reinterpret_cast<const uint2 *>(p);
-    uint32_t w[2] = {0, 0};
+    if (left <= 0) return make_uint2(0u, 0u);
+    const uint32_t off = (uint32_t)((uintptr_t)p & 3);
+    const uint32_t *a = reinterpret_cast<const uint32_t *>(p - off);
+    const int n = left < 8 ? (int)left : 8;
+    uint32_t w[3];
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-        if (j < left) w[j >> 2] |= (uint32_t)(uint8_t)p[j] << (8 * (j & 3));
-    return make_uint2(w[0], w[1]);
+    for (int j = 0; j < 3; ++j) w[j] = 4 * j < n + (int)off ? a[j] : 0u;
+    uint2 r = make_uint2(__funnelshift_r(w[0], w[1], 8 * off), __funnelshift_r(w[1], w[2], 8 * off));
+    if (n < 8) {
+        const uint64_t keep = (1ull << (8 * n)) - 1;
+        r.x &= (uint32_t)keep, r.y &= (uint32_t)(keep >> 32);
+    }
+    return r;
 }
 template <bool VEC>
 __device__ __forceinline__ void store8_bytes(int8_t *p, int64_t left, uint2 b) {

@@ -1,12 +1,18 @@
 // stage_product.cuh -- matrix products of the pipeline-stage operators on the
 // tensor cores.
 //
-// C[m][n] = sum_k A(m,k) B(n,k) over bf16 operands, summed in 32 bits in TMEM,
-// handed to an epilogue row by row instead of being stored:
-//   typename Epi::Row  what a row keeps between its pieces
-//   begin(row, m, part)  a row m of the tile starts (part: which part of K)
+// C[m][n] = sum_k A(m,k) B(n,k) over bf16 operands, summed in 32 bits in TMEM
+// and handed to an epilogue instead of being stored.  Epilogues that store C
+// (kStore), with columns in quads where `vec` says that rows are aligned and one
+// by one otherwise (part: which part of K):
+//   run(m, n, v, part)         columns n .. n+31 of row m
+//   quad(m, n, left, v, part)  columns n .. n+3, of which `left` exist
+//   one(m, n, v, part)         one column
+// The others get a row as a thread has it:
+//   typename Epi::Row  what a row keeps between its runs
+//   begin(row, m)      a row m of the tile starts
 //   chunk(row, m, n, cnt, v)  columns n .. n+cnt-1 (cnt <= 32) of row m
-//   end(row, m, piece)  the row's piece `piece` of the columns is done
+//   end(row, m, piece) the row's piece `piece` of the columns is done
 //   kWhole             runs of columns go on to the next multiple of 64, with
 //                      cnt <= 0 past the last one, and no run is cut by a tile's end
 // A row's part of a column tile is two pieces, the even and the odd runs of 32
@@ -77,10 +83,11 @@ struct RingOf {
     static constexpr int kRowsB = CG == 2 ? 128 : 256;  // most rows of B in a block
     static constexpr int kStageBytes = kBytesA + kRowsB * kTileK * 2, kStages = kRingBytes / kStageBytes;
 };
-constexpr int kProductSmem = kRingBytes + 1024;
 constexpr int kEpilogueWarps = 8, kProductThreads = 128 + 32 * kEpilogueWarps;
 constexpr int kPieces = kEpilogueWarps / 4;  // pieces of a row's part of a tile
 constexpr int kRuns = 256 / 32 / kPieces;    // runs of 32 columns in a piece
+constexpr int kTurnBytes = 32 * 32 * 4;  // a warp's run of columns, turned for storing
+constexpr int kProductSmem = kRingBytes + 1024 + kEpilogueWarps * kTurnBytes;
 constexpr int kAccStride = 256;  // TMEM columns of an accumulator
 constexpr int kRun = 32;         // slices (2048 k) that one accumulator adds up
 // Registers: the epilogue's 8 warps take what the first 4 can spare.
@@ -104,6 +111,98 @@ __device__ __forceinline__ void tile_at(const ProductShape &s, uint32_t i, int &
     m = first + r % rows;
     n = r / rows;
 }
+
+// Four columns of a row, of which `left` exist; aligned.
+__device__ __forceinline__ void store_quad(uint16_t *p, int left, const float4 &v) {
+    if (left >= 4) {
+        *reinterpret_cast<uint2 *>(p) = make_uint2(f32_to_bf16x2(v.x, v.y), f32_to_bf16x2(v.z, v.w));
+    } else {
+        p[0] = f32_to_bf16(v.x);
+        if (left > 1) p[1] = f32_to_bf16(v.y);
+        if (left > 2) p[2] = f32_to_bf16(v.z);
+    }
+}
+__device__ __forceinline__ void store_quad(float *p, int left, const float4 &v) {
+    if (left >= 4) {
+        *reinterpret_cast<float4 *>(p) = v;
+    } else {
+        p[0] = v.x;
+        if (left > 1) p[1] = v.y;
+        if (left > 2) p[2] = v.z;
+    }
+}
+__device__ __forceinline__ float4 load_quad(const float *p, int left) {
+    if (left >= 4) return *reinterpret_cast<const float4 *>(p);
+    return make_float4(p[0], left > 1 ? p[1] : 0.f, left > 2 ? p[2] : 0.f, 0.f);
+}
+
+// 32 columns of a row as bf16, aligned.
+__device__ __forceinline__ void store_bf16(uint16_t *p, const float (&v)[32]) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        reinterpret_cast<uint4 *>(p)[j] =
+            make_uint4(f32_to_bf16x2(v[8 * j], v[8 * j + 1]), f32_to_bf16x2(v[8 * j + 2], v[8 * j + 3]),
+                       f32_to_bf16x2(v[8 * j + 4], v[8 * j + 5]), f32_to_bf16x2(v[8 * j + 6], v[8 * j + 7]));
+}
+
+// 32 columns of a row in 32 bits, aligned.
+__device__ __forceinline__ void store_f32(float *p, const float (&v)[32]) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        reinterpret_cast<float4 *>(p)[j] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+}
+// The same added to what `to` holds, which is all loaded first.
+__device__ __forceinline__ void add_f32(float (&v)[32], const float *to) {
+    float4 b[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) b[j] = reinterpret_cast<const float4 *>(to)[j];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[4 * j] += b[j].x, v[4 * j + 1] += b[j].y, v[4 * j + 2] += b[j].z, v[4 * j + 3] += b[j].w;
+}
+
+// 32 rows x 32 columns, a row to a lane.  Aligned rows are stored by their lanes,
+// everything that they are added to loaded first (turning them into whole
+// lines as below made the weight gradient of 8192^3 757 us instead of 712).  Others
+// are turned through the warp's shared memory, so that the lanes' narrow
+// stores lie side by side.
+template <class Epi>
+__device__ __forceinline__ void store_run(const Epi &epi, float4 *turn, int lane, int64_t m0, int64_t M, int n, int end,
+                                          int part, const float (&v)[32]) {
+    if (epi.vec) {
+        const int64_t m = m0 + lane;
+        if (m >= M) return;
+        if (end - n >= 32) {
+            epi.run(m, n, v, part);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int left = end - (n + 4 * j);
+                if (left > 0)
+                    epi.quad(m, n + 4 * j, left, make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]), part);
+            }
+        }
+        return;
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        turn[lane * 8 + (j ^ (lane & 7))] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+    __syncwarp();
+    const float *one = reinterpret_cast<const float *>(turn);
+    for (int r = 0; r < 32 && m0 + r < M; ++r)
+        if (n + lane < end) epi.one(m0 + r, n + lane, one[r * 32 + ((lane >> 2) ^ (r & 7)) * 4 + (lane & 3)], part);
+    __syncwarp();
+}
+
+template <class Epi, bool STORE = Epi::kStore>
+struct RowType {
+    using type = int;
+};
+template <class Epi>
+struct RowType<Epi, false> {
+    using type = typename Epi::Row;
+};
+template <class Epi>
+using RowOf = typename RowType<Epi>::type;
 
 // A place in a ring of N: the slot, and the parity of its current round.
 template <int N>
@@ -255,8 +354,9 @@ __global__ void __launch_bounds__(kProductThreads, 1)
             const int first_n = nt * s.tile_n, n0 = first_n + half * 32, n1 = min(first_n + s.tile_n, wide);
             const int k0 = part * s.k_blocks, k1 = min(k0 + s.k_blocks, all_blocks);
             const bool live = m < s.M;
-            typename Epi::Row row;
-            if (live) epi.begin(row, m, part);
+            [[maybe_unused]] RowOf<Epi> row;
+            if constexpr (!Epi::kStore)
+                if (live) epi.begin(row, m);
             float sum[kRuns][32];
             for (int r0 = k0; r0 < k1; r0 += kRun, run.next()) {
                 const int buf = run.slot;
@@ -285,15 +385,29 @@ __global__ void __launch_bounds__(kProductThreads, 1)
                     else tc::mbar_arrive(acc_empty + 8 * buf);
                 }
             }
-            if (ok && live) {
+            if constexpr (Epi::kStore) {
+                if (ok) {
+                    float4 *turn = reinterpret_cast<float4 *>(raw + (ring - tc::smem_u32(raw)) + kRingBytes +
+                                                              (warp - 4) * kTurnBytes);
+                    const int64_t m_first = m - lane;
+                    const int end = min(n1, s.N);
 #pragma unroll
-                for (int i = 0; i < kRuns; ++i) {
-                    const int n = n0 + i * kPieces * 32;
-                    if (n < n1) epi.chunk(row, m, n, min(min(32, n1 - n), s.N - n), sum[i]);
+                    for (int i = 0; i < kRuns; ++i) {
+                        const int n = n0 + i * kPieces * 32;
+                        if (n < n1) store_run(epi, turn, lane, m_first, s.M, n, end, part, sum[i]);
+                    }
                 }
-                epi.end(row, m, kPieces * nt + half);
+            } else {
+                if (ok && live) {
+#pragma unroll
+                    for (int i = 0; i < kRuns; ++i) {
+                        const int n = n0 + i * kPieces * 32;
+                        if (n < n1) epi.chunk(row, m, n, min(min(32, n1 - n), s.N - n), sum[i]);
+                    }
+                    epi.end(row, m, kPieces * nt + half);
+                }
+                __syncwarp();
             }
-            __syncwarp();
         }
     }
     tc::fence_before();
@@ -367,7 +481,7 @@ int launch_product(const Matrix &A, const Matrix &B, int64_t M, int64_t N, int64
 template <Form FA, Form FB, class Epi>
 int whole_product(const Matrix &A, const Matrix &B, int64_t M, int64_t N, int64_t K, const Epi &epi,
                   cudaStream_t stream) {
-    return launch_product<FA, FB>(A, B, M, N, K, epi, plan_product(M, N, K, is_mn(FB) || Epi::kWhole, false), stream);
+    return launch_product<FA, FB>(A, B, M, N, K, epi, plan_product(M, N, K, true, false), stream);
 }
 
 // Parts of K: each part's sums apart, [part][M][ld].  Epilogues are local to
@@ -375,52 +489,64 @@ int whole_product(const Matrix &A, const Matrix &B, int64_t M, int64_t N, int64_
 // them.
 namespace {
 struct PartEpi {
-    static constexpr bool kWhole = true;
+    static constexpr bool kStore = true, kWhole = false;
+    static constexpr bool vec = true;
     float *parts;
-    int64_t M, ld;
-    struct Row {
-        float *p;
-    };
-    __device__ __forceinline__ void begin(Row &r, int64_t m, int part) const { r.p = parts + (part * M + m) * ld; }
-    __device__ __forceinline__ void chunk(Row &r, int64_t, int64_t n, int cnt, const float (&v)[32]) const {
-        // columns past the last one are there to be written, up to ld
-        if (n >= ld) return;
-        float4 *p = reinterpret_cast<float4 *>(r.p + n);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) p[j] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+    int64_t M, ld;  // ld is a multiple of 4: a quad may go past the last column
+    __device__ __forceinline__ void quad(int64_t m, int64_t n, int, const float4 &v, int part) const {
+        *reinterpret_cast<float4 *>(parts + (part * M + m) * ld + n) = v;
     }
-    __device__ __forceinline__ void end(Row &, int64_t, int64_t) const {}
+    __device__ __forceinline__ void run(int64_t m, int64_t n, const float (&v)[32], int part) const {
+        store_f32(parts + (part * M + m) * ld + n, v);
+    }
+    __device__ __forceinline__ void one(int64_t, int64_t, float, int) const {}
 };
 }  // namespace
 
-// Adds the parts up, always in the same order, and hands them to the epilogue.
+// Adds the parts up, always in the same order, and hands them to the epilogue:
+// 64 quads of columns a block, 4 threads to a quad.
 template <class Epi>
-__global__ void __launch_bounds__(128) k_join_parts(const float *parts, int splits, int64_t M, int64_t N, int64_t ld,
+__global__ void __launch_bounds__(256) k_join_parts(const float *parts, int splits, int64_t M, int64_t N, int64_t ld,
                                                     const Epi epi) {
     let_next_start();
     after_previous();
-    const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x, per = ld / 32;
-    const int64_t m = i / per, n = i % per * 32;
-    if (m >= M || n >= N) return;
-    float v[32] = {};
-    for (int s = 0; s < splits; ++s) {
-        const float4 *p = reinterpret_cast<const float4 *>(parts + (s * M + m) * ld + n);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const float4 q = p[j];
-            v[4 * j] += q.x, v[4 * j + 1] += q.y, v[4 * j + 2] += q.z, v[4 * j + 3] += q.w;
+    __shared__ float4 sh[4][64];
+    const int q = threadIdx.x & 63, run = threadIdx.x >> 6;
+    const int64_t i = (int64_t)blockIdx.x * 64 + q, per = ld / 4;
+    const int64_t m = i / per, n = (i - m * per) * 4;
+    const bool in = m < M && n < N;
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (in) {
+        const float4 *p = reinterpret_cast<const float4 *>(parts + m * ld + n);
+#pragma unroll 4
+        for (int s = run; s < splits; s += 4) {
+            const float4 x = p[s * (M * ld / 4)];
+            v.x += x.x, v.y += x.y, v.z += x.z, v.w += x.w;
         }
     }
-    typename Epi::Row row;
-    epi.begin(row, m, 0);
-    epi.chunk(row, m, n, N - n < 32 ? (int)(N - n) : 32, v);
-    epi.end(row, m, 0);
+    sh[run][q] = v;
+    __syncthreads();
+    if (run || !in) return;
+#pragma unroll
+    for (int r = 1; r < 4; ++r) {
+        const float4 x = sh[r][q];
+        v.x += x.x, v.y += x.y, v.z += x.z, v.w += x.w;
+    }
+    const int left = N - n < 4 ? (int)(N - n) : 4;
+    if (epi.vec) {
+        epi.quad(m, n, left, v, 0);
+    } else {
+        const float x[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (j < left) epi.one(m, n + j, x[j], 0);
+    }
 }
 
 // Floats of scratch memory that product_in_parts needs (B is MN-major there).
 inline int64_t part_floats(int64_t M, int64_t N, int64_t K) {
     const int s = plan_product(M, N, K, true, true).splits;
-    return s > 1 ? s * M * round_up(N, 32) : 0;
+    return s > 1 ? s * M * round_up(N, 4) : 0;
 }
 
 // A product whose K is shared out where that is cheaper.
@@ -430,49 +556,11 @@ int product_in_parts(const Matrix &A, const Matrix &B, int64_t M, int64_t N, int
     static_assert(is_mn(FB));
     const ProductPlan p = plan_product(M, N, K, true, true);
     if (p.splits == 1) return launch_product<FA, FB>(A, B, M, N, K, epi, p, stream);
-    const int64_t ld = round_up(N, 32);
+    const int64_t ld = round_up(N, 4);
     const int rc = launch_product<FA, FB>(A, B, M, N, K, PartEpi{parts, M, ld}, p, stream);
     if (rc != PP_OK) return rc;
-    return launch_after(k_join_parts<Epi>, ceil_div(M * (ld / 32), 128), 128, 0, stream, 1, parts, p.splits, M, N, ld,
-                        epi);
-}
-
-// 32 columns of a row as bf16, or added to / stored as 32-bit floats.
-__device__ __forceinline__ void store_bf16(uint16_t *p, int cnt, bool vec, const float (&v)[32]) {
-    if (vec && cnt == 32) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            reinterpret_cast<uint4 *>(p)[j] =
-                make_uint4(f32_to_bf16x2(v[8 * j], v[8 * j + 1]), f32_to_bf16x2(v[8 * j + 2], v[8 * j + 3]),
-                           f32_to_bf16x2(v[8 * j + 4], v[8 * j + 5]), f32_to_bf16x2(v[8 * j + 6], v[8 * j + 7]));
-    } else {
-#pragma unroll
-        for (int j = 0; j < 32; ++j)
-            if (j < cnt) p[j] = f32_to_bf16(v[j]);
-    }
-}
-__device__ __forceinline__ void load_f32(const float *p, int cnt, bool vec, float (&v)[32]) {
-    if (vec && cnt == 32) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const float4 q = reinterpret_cast<const float4 *>(p)[j];
-            v[4 * j] = q.x, v[4 * j + 1] = q.y, v[4 * j + 2] = q.z, v[4 * j + 3] = q.w;
-        }
-    } else {
-#pragma unroll
-        for (int j = 0; j < 32; ++j) v[j] = j < cnt ? p[j] : 0.f;
-    }
-}
-__device__ __forceinline__ void store_f32(float *p, int cnt, bool vec, const float (&v)[32]) {
-    if (vec && cnt == 32) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            reinterpret_cast<float4 *>(p)[j] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
-    } else {
-#pragma unroll
-        for (int j = 0; j < 32; ++j)
-            if (j < cnt) p[j] = v[j];
-    }
+    return launch_after(k_join_parts<Epi>, ceil_div(M * (ld / 4), 64), 256, 0, stream, 1, (const float *)parts, p.splits, M,
+                        N, ld, epi);
 }
 
 // A copy of rows at any stride and alignment as panels (or aligned rows), the
