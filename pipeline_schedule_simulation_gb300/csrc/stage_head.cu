@@ -37,48 +37,44 @@ struct StatsEpi {
     float2 *part;   // [pieces][T]: largest logit, sum of exponentials
     float *picked;  // [T]: the target's logit
     struct Row {
-        float m, s;
         int64_t target;
     };
-    __device__ __forceinline__ void begin(Row &r, int64_t t) const {
-        r.m = kNegInf;
-        r.s = 0.f;
-        r.target = target ? target[t] : -1;
-    }
-    __device__ __forceinline__ void chunk(Row &r, int64_t t, int64_t n, int cnt, const float (&v)[32]) const {
-        float m = r.m;
-        if (cnt < 32) {
+    __device__ __forceinline__ void begin(Row &r, int64_t t) const { r.target = target[t]; }
+    __device__ __forceinline__ void take(const Row &r, int64_t t, int n0, int end, int N, int piece,
+                                         float (&v)[kRuns][32]) const {
+        const int last = min(end, N);
+        float top = kNegInf, s = 0.f;
 #pragma unroll
-            for (int j = 0; j < 32; ++j) m = j < cnt ? fmaxf(m, v[j]) : m;
-        } else {
-            float c[4] = {v[0], v[1], v[2], v[3]};
+        for (int i = 0; i < kRuns; ++i) {
+            const int n = n0 + i * kPieces * 32, cnt = min(32, last - n);
+            if (cnt <= 0) break;
+            if (cnt < 32) {  // columns that do not exist add nothing
 #pragma unroll
-            for (int j = 4; j < 32; ++j) c[j & 3] = fmaxf(c[j & 3], v[j]);
-            m = fmaxf(fmaxf(m, fmaxf(c[0], c[1])), fmaxf(c[2], c[3]));
+                for (int j = 0; j < 32; ++j)
+                    if (j >= cnt) v[i][j] = kNegInf;
+            }
+            float m[4] = {v[i][0], v[i][1], v[i][2], v[i][3]};
+#pragma unroll
+            for (int j = 4; j < 32; ++j) m[j & 3] = fmaxf(m[j & 3], v[i][j]);
+            const float was = top;
+            top = fmaxf(fmaxf(top, fmaxf(m[0], m[1])), fmaxf(m[2], m[3]));
+            const float ref = ref_of(top);
+            float e[4] = {rebase(s, was, ref), 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int j = 0; j < 32; ++j) e[j & 3] += exp2_fast((v[i][j] - ref) * kLog2e);
+            s = (e[0] + e[1]) + (e[2] + e[3]);
+            const int64_t at = r.target - n;  // few rows have their target here
+            if (at >= 0 && at < cnt) {
+#pragma unroll
+                for (int j = 0; j < 32; ++j)
+                    if (at == j) picked[t] = v[i][j];
+            }
         }
-        const float ref = ref_of(m);
-        float s[4] = {rebase(r.s, r.m, ref), 0.f, 0.f, 0.f};
-        if (cnt < 32) {
-#pragma unroll
-            for (int j = 0; j < 32; ++j) s[j & 3] += j < cnt ? exp2_fast((v[j] - ref) * kLog2e) : 0.f;
-        } else {
-#pragma unroll
-            for (int j = 0; j < 32; ++j) s[j & 3] += exp2_fast((v[j] - ref) * kLog2e);
-        }
-        r.m = m;
-        r.s = (s[0] + s[1]) + (s[2] + s[3]);
-        if (r.target >= n && r.target < n + cnt) {
-#pragma unroll
-            for (int j = 0; j < 32; ++j)
-                if (r.target == n + j) picked[t] = v[j];
-        }
-    }
-    __device__ __forceinline__ void end(Row &r, int64_t t, int64_t piece) const {
-        part[piece * T + t] = make_float2(r.m, r.s);
+        part[(int64_t)piece * T + t] = make_float2(top, s);
     }
 };
 
-// d of one piece: columns v0 .. of the vocabulary, as bf16.
+// d of one piece of the vocabulary: columns v0 .., as bf16.
 struct GradEpi {
     static constexpr bool kStore = false, kWhole = true;
     const int64_t *target;
@@ -97,25 +93,29 @@ struct GradEpi {
         r.lse = lse[t];
         r.at = g - v0;
     }
-    __device__ __forceinline__ void chunk(Row &r, int64_t t, int64_t n, int cnt, const float (&v)[32]) const {
-        float p[32];
+    __device__ __forceinline__ void take(const Row &r, int64_t t, int n0, int end, int N, int, float (&v)[kRuns][32]) const {
 #pragma unroll
-        for (int j = 0; j < 32; ++j) p[j] = exp2_full((v[j] - r.lse) * kLog2e);
-        if (r.at >= n && r.at < n + 32) {
+        for (int i = 0; i < kRuns; ++i) {
+            const int n = n0 + i * kPieces * 32;
+            if (n >= end) break;
+            float p[32];
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
-                if (n + j == r.at) p[j] -= 1.f;
+            for (int j = 0; j < 32; ++j) p[j] = exp2_full((v[i][j] - r.lse) * kLog2e);
+            if (r.at >= n && r.at < n + 32) {
+#pragma unroll
+                for (int j = 0; j < 32; ++j)
+                    if (n + j == r.at) p[j] -= 1.f;
+            }
+#pragma unroll
+            for (int j = 0; j < 32; ++j) p[j] *= r.c;
+            if (!r.in || n + 32 > N) {
+#pragma unroll
+                for (int j = 0; j < 32; ++j)
+                    if (!r.in || n + j >= N) p[j] = 0.f;
+            }
+            store_bf16(d + (int64_t)(n >> 6) * (T * 64) + t * 64 + (n & 63), p);
         }
-#pragma unroll
-        for (int j = 0; j < 32; ++j) p[j] *= r.c;
-        if (!r.in || cnt < 32) {
-#pragma unroll
-            for (int j = 0; j < 32; ++j)
-                if (!r.in || j >= cnt) p[j] = 0.f;
-        }
-        store_bf16(d + (n >> 6) * (T * 64) + t * 64 + (n & 63), p);
     }
-    __device__ __forceinline__ void end(Row &, int64_t, int64_t) const {}
 };
 
 // dx: pieces add up in 32 bits; the last one writes the result.  A row that is

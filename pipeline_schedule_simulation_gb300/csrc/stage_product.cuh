@@ -8,15 +8,14 @@
 //   run(m, n, v, part)         columns n .. n+31 of row m
 //   quad(m, n, left, v, part)  columns n .. n+3, of which `left` exist
 //   one(m, n, v, part)         one column
-// The others get a row as a thread has it:
-//   typename Epi::Row  what a row keeps between its runs
-//   begin(row, m)      a row m of the tile starts
-//   chunk(row, m, n, cnt, v)  columns n .. n+cnt-1 (cnt <= 32) of row m
-//   end(row, m, piece) the row's piece `piece` of the columns is done
-//   kWhole             runs of columns go on to the next multiple of 64, with
-//                      cnt <= 0 past the last one, and no run is cut by a tile's end
-// A row's part of a column tile is two pieces, the even and the odd runs of 32
-// columns; each piece is handed over by one thread, in column order.
+// The others get a row as a thread has it.  A row's part of a column tile is two
+// pieces, the even and the odd runs of 32 columns:
+//   typename Epi::Row  what a row needs beside its sums
+//   begin(row, m)      loads that
+//   take(row, m, n0, end, N, piece, v)  one piece: run i is the columns from
+//                      n0 + 64 i on, below `end` and (what exists) N
+//   kWhole             runs go on to the next multiple of 64 past N, and none is
+//                      cut by a tile's end
 //
 // Persistent blocks, one to an SM: a warp loads 64-deep slices of A and B by
 // TMA into a ring, a thread issues the MMAs of a tile into one of two TMEM
@@ -346,6 +345,18 @@ __global__ void __launch_bounds__(kProductThreads, 1)
         const int wide = Epi::kWhole ? (s.N + 63) & ~63 : s.N;
         Place<2> run;
         bool ok = true;
+        // what a row needs beside its sums is loaded a tile ahead
+        [[maybe_unused]] RowOf<Epi> next{};
+        const auto begin_next = [&](uint32_t t) {
+            if constexpr (!Epi::kStore) {
+                if (t >= tiles) return;
+                int mt, nt;
+                tile_at(s, t / s.splits, mt, nt);
+                const int64_t m = (int64_t)(mt * CG + (int)rank) * kHalf + quarter * 32 + lane;
+                if (m < s.M) epi.begin(next, m);
+            }
+        };
+        begin_next(first);
         for (uint32_t t = first; t < tiles && ok; t += step) {
             const int part = (int)(t % s.splits);
             int mt, nt;
@@ -354,10 +365,8 @@ __global__ void __launch_bounds__(kProductThreads, 1)
             const int first_n = nt * s.tile_n, n0 = first_n + half * 32, n1 = min(first_n + s.tile_n, wide);
             const int k0 = part * s.k_blocks, k1 = min(k0 + s.k_blocks, all_blocks);
             const bool live = m < s.M;
-            [[maybe_unused]] RowOf<Epi> row;
-            if constexpr (!Epi::kStore)
-                if (live) epi.begin(row, m);
-            float sum[kRuns][32];
+            [[maybe_unused]] RowOf<Epi> row = next;
+            uint32_t sum[kRuns][32];  // floats, as the loads give them
             for (int r0 = k0; r0 < k1; r0 += kRun, run.next()) {
                 const int buf = run.slot;
                 // lanes give up one by one: the warp goes on together
@@ -365,19 +374,27 @@ __global__ void __launch_bounds__(kProductThreads, 1)
                 if (!ok) break;
                 tc::fence_after();
                 const uint32_t acc = tmem + ((uint32_t)(quarter * 32) << 16) + buf * kAccStride + half * 32;
-                const bool more = r0 > k0;
+                if (r0 > k0) {
 #pragma unroll
-                for (int i = 0; i < kRuns; ++i)
-                    if (n0 + i * kPieces * 32 < n1) {
-                        if (more) {
-                            float v[32];
+                    for (int i = 0; i < kRuns; ++i)
+                        if (n0 + i * kPieces * 32 < n1) {
+                            uint32_t v[32];
                             tc::tmem_load32(acc + i * kPieces * 32, v);
+                            tc::tmem_wait();
+                            tc::tmem_loaded(v);
 #pragma unroll
-                            for (int c = 0; c < 32; ++c) sum[i][c] += v[c];
-                        } else {
-                            tc::tmem_load32(acc + i * kPieces * 32, sum[i]);
+                            for (int c = 0; c < 32; ++c)
+                                sum[i][c] = __float_as_uint(__uint_as_float(sum[i][c]) + __uint_as_float(v[c]));
                         }
-                    }
+                } else {
+                    // nothing else is in these registers yet: all loads at once
+#pragma unroll
+                    for (int i = 0; i < kRuns; ++i)
+                        if (n0 + i * kPieces * 32 < n1) tc::tmem_load32(acc + i * kPieces * 32, sum[i]);
+                    tc::tmem_wait();
+#pragma unroll
+                    for (int i = 0; i < kRuns; ++i) tc::tmem_loaded(sum[i]);
+                }
                 tc::fence_before();
                 __syncwarp();
                 if (lane == 0) {
@@ -385,6 +402,11 @@ __global__ void __launch_bounds__(kProductThreads, 1)
                     else tc::mbar_arrive(acc_empty + 8 * buf);
                 }
             }
+            float v[kRuns][32];
+#pragma unroll
+            for (int i = 0; i < kRuns; ++i)
+#pragma unroll
+                for (int c = 0; c < 32; ++c) v[i][c] = __uint_as_float(sum[i][c]);
             if constexpr (Epi::kStore) {
                 if (ok) {
                     float4 *turn = reinterpret_cast<float4 *>(raw + (ring - tc::smem_u32(raw)) + kRingBytes +
@@ -394,18 +416,12 @@ __global__ void __launch_bounds__(kProductThreads, 1)
 #pragma unroll
                     for (int i = 0; i < kRuns; ++i) {
                         const int n = n0 + i * kPieces * 32;
-                        if (n < n1) store_run(epi, turn, lane, m_first, s.M, n, end, part, sum[i]);
+                        if (n < n1) store_run(epi, turn, lane, m_first, s.M, n, end, part, v[i]);
                     }
                 }
             } else {
-                if (ok && live) {
-#pragma unroll
-                    for (int i = 0; i < kRuns; ++i) {
-                        const int n = n0 + i * kPieces * 32;
-                        if (n < n1) epi.chunk(row, m, n, min(min(32, n1 - n), s.N - n), sum[i]);
-                    }
-                    epi.end(row, m, kPieces * nt + half);
-                }
+                begin_next(t + step);
+                if (ok && live) epi.take(row, m, n0, n1, s.N, kPieces * nt + half, v);
                 __syncwarp();
             }
         }
