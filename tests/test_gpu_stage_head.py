@@ -227,3 +227,24 @@ def test_refusals_on_the_gpu(S):
     with pytest.raises(S.PPSchedError):  # a workspace that is not aligned
         n = S.head_forward_workspace(x, w)
         S.head_forward(x, w, target, workspace=torch.empty(n + 1, dtype=torch.uint8, device="cuda")[1:])
+
+
+def test_in_a_graph_and_no_wait_ran_out(S):
+    """Captured calls give what direct ones give, again and again; and no wait inside the products ran out so far."""
+    x, w, target, weight = _inputs(500, 3000, 264, 18)
+    first = _both(S, x, w, target, weight=weight)
+    packed = S.pack(x)
+    grad = S.weight_grad(x, packed)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        again = S.head_forward(x, w, target)
+        again.update(S.head_backward(x, w, target, again["lse"], weight=weight))
+        grad2 = S.weight_grad(x, S.pack(x))
+    for _ in range(3):
+        for t in (*again.values(), grad2):
+            t.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(first[k], again[k]) for k in first) and torch.equal(grad, grad2)
+    assert S.wait_failure() == 0
