@@ -131,9 +131,9 @@ __global__ void __launch_bounds__(NT) k_join_forward(const JoinForward a) {
 constexpr int kNarrow = 512;  // widths up to this: a warp to a row, kWarps rows a block at once
 constexpr int kWarps = 8;
 
-// Threads of a ring block for this width, two vectors of 8 columns each (one
-// up to 1024 columns); 0 where a row is too wide.
-int ring_threads(int64_t H) { return H <= 2048 ? 128 : H <= 4096 ? 256 : H <= 8192 ? 512 : 0; }
+// Threads of a ring block for this width: two vectors of 8 columns each (one up
+// to 1024 columns), in whole warps; 0 where a row is too wide.
+int ring_threads(int64_t H) { return H > 8192 ? 0 : (int)round_up(ceil_div(H, H <= 1024 ? 8 : 16), 32); }
 
 // Rows are shared out in items: a run of rows of one gate group, so that an
 // item's column sums belong to one gate row.
@@ -450,7 +450,9 @@ __global__ void __launch_bounds__(32 * kWarps, NV == 1 ? 4 : 2) k_join_backward_
     }
 }
 
-// ---- rows through a ring
+// ---- rows through a ring.  FULL: the row's columns are all of the block's
+// vectors, and no vector's end is looked at (16384 x 8192 backward from
+// checkpoints: 216 us, 267 us with the looks).
 
 // Shared memory of one block: two mbarriers' worth of header, then the stages.
 constexpr int kRingHeader = 128, kMaxStages = 4;
@@ -481,11 +483,13 @@ __device__ __forceinline__ Raw8 ring_raw(const unsigned char *stage, uint32_t at
     return Raw8{{w.x, w.y, w.z, w.w}};
 }
 
-template <int NT, int NV, bool KEEP>
+template <int NT, int NV, bool KEEP, bool FULL>
 __global__ void __launch_bounds__(NT, 1024 / NT) k_join_forward_ring(const JoinForward a, const int stages) {
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ __align__(16) float sh[2][32];
     __shared__ int stop;
+    const int nt = blockDim.x;  // a whole number of warps, NT at most
+    if (threadIdx.x < 64) sh[threadIdx.x >> 5][threadIdx.x & 31] = 0.f;  // also for the warps that are not there
     let_next_start();
     after_previous();
     const uint32_t row_bytes = 2u * a.H;
@@ -515,11 +519,11 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_join_forward_ring(const JoinF
         float y[NV][8], ss = 0.f;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int c = (i * NT + (int)threadIdx.x) * 8;
+            const int c = (i * nt + (int)threadIdx.x) * 8;
             fr[i] = Raw8{};
 #pragma unroll
             for (int j = 0; j < 8; ++j) y[i][j] = 0.f;
-            if (c < a.H) {
+            if (FULL || c < a.H) {
                 fr[i] = ring_raw(stage, 0, c);
                 widen(ring_raw(stage, row_bytes, c), y[i]);
             }
@@ -537,19 +541,19 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_join_forward_ring(const JoinF
         if (KEEP) {
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
-                const int c = (i * NT + (int)threadIdx.x) * 8;
+                const int c = (i * nt + (int)threadIdx.x) * 8;
                 int e;
                 const uint2 b = pack8(fr[i], e);
-                if (c < a.H) {
-                    *reinterpret_cast<uint2 *>(qf + i * NT * 8) = b;
-                    if ((threadIdx.x & 7) == 0) ef[i * NT * 8 / kBlock] = (int8_t)e;
+                if (FULL || c < a.H) {
+                    *reinterpret_cast<uint2 *>(qf + i * nt * 8) = b;
+                    if ((threadIdx.x & 7) == 0) ef[i * nt * 8 / kBlock] = (int8_t)e;
                 }
             }
         }
         ss = 0.f;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int c = (i * NT + (int)threadIdx.x) * 8, at = c < a.H ? c : 0;
+            const int c = (i * nt + (int)threadIdx.x) * 8, at = FULL || c < a.H ? c : 0;
             float w[8], f[8];
             load8_bf16<true>(a.w_post + at, 8, w);
             if (g) {
@@ -564,26 +568,26 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_join_forward_ring(const JoinF
                 ss += y[i][j] * y[i][j];
             }
             const Raw8 yr = narrow(y[i]);
-            if (c < a.H) store8<true>(py + i * NT * 8, 8, yr);
+            if (FULL || c < a.H) store8<true>(py + i * nt * 8, 8, yr);
             if (KEEP) {
                 int e;
                 const uint2 b = pack8(yr, e);  // y as its next reader sees it
-                if (c < a.H) {
-                    *reinterpret_cast<uint2 *>(qy + i * NT * 8) = b;
-                    if ((threadIdx.x & 7) == 0) ey[i * NT * 8 / kBlock] = (int8_t)e;
+                if (FULL || c < a.H) {
+                    *reinterpret_cast<uint2 *>(qy + i * nt * 8) = b;
+                    if ((threadIdx.x & 7) == 0) ey[i * nt * 8 / kBlock] = (int8_t)e;
                 }
             }
         }
         const float r2 = rsqrtf(block_sum<NT>(ss, sh[1]) * inv_h + a.eps);
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int c = (i * NT + (int)threadIdx.x) * 8;
-            if (c < a.H) {
+            const int c = (i * nt + (int)threadIdx.x) * 8;
+            if (FULL || c < a.H) {
                 float w[8];
                 load8_bf16<true>(a.w_pre + c, 8, w);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) w[j] *= y[i][j] * r2;
-                store8_bf16<true>(ph + i * NT * 8, 8, w);
+                store8_bf16<true>(ph + i * nt * 8, 8, w);
             }
         }
         if (threadIdx.x == 0) {
@@ -599,11 +603,13 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_join_forward_ring(const JoinF
     }
 }
 
-template <int NT, int NV, bool PACKED>
+template <int NT, int NV, bool PACKED, bool FULL>
 __global__ void __launch_bounds__(NT, 512 / NT) k_join_backward_ring(const JoinBackward a, const int stages) {
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ __align__(16) float sh[2][32];
     __shared__ int stop;
+    const int nt = blockDim.x;  // a whole number of warps, NT at most
+    if (threadIdx.x < 64) sh[threadIdx.x >> 5][threadIdx.x & 31] = 0.f;  // also for the warps that are not there
     let_next_start();
     after_previous();
     const uint32_t wide = 2u * a.H, saved = PACKED ? (uint32_t)a.H : wide, at_dy = wide + 2 * saved;
@@ -630,7 +636,7 @@ __global__ void __launch_bounds__(NT, 512 / NT) k_join_backward_ring(const JoinB
     float gw[NV][8], sum_pre[NV][8] = {}, sum_post[NV][8] = {};
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        const int c = (i * NT + (int)threadIdx.x) * 8, left = a.H - c, at = left > 0 ? c : 0;
+        const int c = (i * nt + (int)threadIdx.x) * 8, left = FULL ? 8 : a.H - c, at = left > 0 ? c : 0;
         w_pre[i] = load8<true>(a.w_pre + at, left);
         load8_bf16<true>(a.w_post + at, left, gw[i]);
         if (a.gate) {
@@ -650,7 +656,7 @@ __global__ void __launch_bounds__(NT, 512 / NT) k_join_backward_ring(const JoinB
         if (PACKED) {
 #pragma unroll
             for (int i = 0; i < NV; ++i)
-                if (c0 + i * NT * 8 < a.H) ey[i] = py[i * NT * 8 / kBlock], ef[i] = pf[i * NT * 8 / kBlock];
+                if (FULL || c0 + i * nt * 8 < a.H) ey[i] = py[i * nt * 8 / kBlock], ef[i] = pf[i * nt * 8 / kBlock];
             py += a.ky.se, pf += a.kf.se;
         }
     };
@@ -682,10 +688,10 @@ __global__ void __launch_bounds__(NT, 512 / NT) k_join_backward_ring(const JoinB
         float n2[NV][8], d[NV][8], ss = 0.f;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int c = (i * NT + (int)threadIdx.x) * 8;
+            const int c = (i * nt + (int)threadIdx.x) * 8;
 #pragma unroll
             for (int j = 0; j < 8; ++j) n2[i][j] = d[i][j] = 0.f;
-            if (c < a.H) {
+            if (FULL || c < a.H) {
                 float w[8];
                 norm(wide, c, step_y[i], n2[i]);
                 widen(ring_raw(stage, 0, c), d[i]);
@@ -703,10 +709,10 @@ __global__ void __launch_bounds__(NT, 512 / NT) k_join_backward_ring(const JoinB
         ss = 0.f;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int c = (i * NT + (int)threadIdx.x) * 8;
+            const int c = (i * nt + (int)threadIdx.x) * 8;
 #pragma unroll
             for (int j = 0; j < 8; ++j) n1[i][j] = 0.f;
-            if (c < a.H) {
+            if (FULL || c < a.H) {
                 float u[8];
                 if (a.dy) {
                     widen(ring_raw(stage, at_dy, c), u);
@@ -718,7 +724,7 @@ __global__ void __launch_bounds__(NT, 512 / NT) k_join_backward_ring(const JoinB
                 }
 #pragma unroll
                 for (int j = 0; j < 8; ++j) u[j] = a.alpha * d[i][j];
-                store8_bf16<true>(px + i * NT * 8, 8, u);
+                store8_bf16<true>(px + i * nt * 8, 8, u);
                 norm(wide + saved, c, step_f[i], n1[i]);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
@@ -736,12 +742,12 @@ __global__ void __launch_bounds__(NT, 512 / NT) k_join_backward_ring(const JoinB
         }
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int c = (i * NT + (int)threadIdx.x) * 8;
-            if (c < a.H) {
+            const int c = (i * nt + (int)threadIdx.x) * 8;
+            if (FULL || c < a.H) {
                 float u[8];
 #pragma unroll
                 for (int j = 0; j < 8; ++j) u[j] = fmaf(r1, d[i][j], -m1 * n1[i][j]);
-                store8_bf16<true>(pd + i * NT * 8, 8, u);
+                store8_bf16<true>(pd + i * nt * 8, 8, u);
             }
         }
         px += a.sdx, pd += a.sdf;
@@ -749,8 +755,8 @@ __global__ void __launch_bounds__(NT, 512 / NT) k_join_backward_ring(const JoinB
     }
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        const int c = (i * NT + (int)threadIdx.x) * 8;
-        if (c < a.H) {
+        const int c = (i * nt + (int)threadIdx.x) * 8;
+        if (FULL || c < a.H) {
             float *p = a.part_pre + blockIdx.x * a.ld + c, *q = a.part_post + blockIdx.x * a.ld + c;
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
@@ -880,23 +886,41 @@ int launch_ring(K kernel, const A &a, const RingPlan &p, unsigned grid, std::ato
 
 template <bool KEEP>
 int forward_ring(const JoinForward &a, const RingPlan &p, cudaStream_t s) {
-    static std::atomic<uint64_t> ready[4];
+    static std::atomic<uint64_t> ready[8];
+    // 512 columns are a whole number of warps, whatever the vectors
     const int64_t most = (int64_t)sm_count() * p.blocks;
     const unsigned grid = (unsigned)(a.T < most ? a.T : most);
-    if (a.H <= 1024) return launch_ring(k_join_forward_ring<128, 1, KEEP>, a, p, grid, ready[0], s);
-    if (a.H <= 2048) return launch_ring(k_join_forward_ring<128, 2, KEEP>, a, p, grid, ready[1], s);
-    if (a.H <= 4096) return launch_ring(k_join_forward_ring<256, 2, KEEP>, a, p, grid, ready[2], s);
-    return launch_ring(k_join_forward_ring<512, 2, KEEP>, a, p, grid, ready[3], s);
+    const bool full = a.H % 512 == 0;
+    if (a.H <= 1024)
+        return full ? launch_ring(k_join_forward_ring<128, 1, KEEP, true>, a, p, grid, ready[0], s)
+                    : launch_ring(k_join_forward_ring<128, 1, KEEP, false>, a, p, grid, ready[1], s);
+    if (a.H <= 2048)
+        return full ? launch_ring(k_join_forward_ring<128, 2, KEEP, true>, a, p, grid, ready[2], s)
+                    : launch_ring(k_join_forward_ring<128, 2, KEEP, false>, a, p, grid, ready[3], s);
+    if (a.H <= 4096)
+        return full ? launch_ring(k_join_forward_ring<256, 2, KEEP, true>, a, p, grid, ready[4], s)
+                    : launch_ring(k_join_forward_ring<256, 2, KEEP, false>, a, p, grid, ready[5], s);
+    return full ? launch_ring(k_join_forward_ring<512, 2, KEEP, true>, a, p, grid, ready[6], s)
+                : launch_ring(k_join_forward_ring<512, 2, KEEP, false>, a, p, grid, ready[7], s);
 }
 
 template <bool PACKED>
 int backward_ring(const JoinBackward &a, const RingPlan &p, cudaStream_t s) {
-    static std::atomic<uint64_t> ready[4];
+    static std::atomic<uint64_t> ready[8];
+    // 512 columns are a whole number of warps, whatever the vectors
     const unsigned grid = (unsigned)a.it.count;
-    if (a.H <= 1024) return launch_ring(k_join_backward_ring<128, 1, PACKED>, a, p, grid, ready[0], s);
-    if (a.H <= 2048) return launch_ring(k_join_backward_ring<128, 2, PACKED>, a, p, grid, ready[1], s);
-    if (a.H <= 4096) return launch_ring(k_join_backward_ring<256, 2, PACKED>, a, p, grid, ready[2], s);
-    return launch_ring(k_join_backward_ring<512, 2, PACKED>, a, p, grid, ready[3], s);
+    const bool full = a.H % 512 == 0;
+    if (a.H <= 1024)
+        return full ? launch_ring(k_join_backward_ring<128, 1, PACKED, true>, a, p, grid, ready[0], s)
+                    : launch_ring(k_join_backward_ring<128, 1, PACKED, false>, a, p, grid, ready[1], s);
+    if (a.H <= 2048)
+        return full ? launch_ring(k_join_backward_ring<128, 2, PACKED, true>, a, p, grid, ready[2], s)
+                    : launch_ring(k_join_backward_ring<128, 2, PACKED, false>, a, p, grid, ready[3], s);
+    if (a.H <= 4096)
+        return full ? launch_ring(k_join_backward_ring<256, 2, PACKED, true>, a, p, grid, ready[4], s)
+                    : launch_ring(k_join_backward_ring<256, 2, PACKED, false>, a, p, grid, ready[5], s);
+    return full ? launch_ring(k_join_backward_ring<512, 2, PACKED, true>, a, p, grid, ready[6], s)
+                : launch_ring(k_join_backward_ring<512, 2, PACKED, false>, a, p, grid, ready[7], s);
 }
 
 int check_join(int64_t T, int64_t H) {

@@ -39,7 +39,7 @@ def _backward(S, a, y, f, r1, r2, alpha, dy=True, **kw):
 
 # widths on both sides of every variant's limit, and odd ones; groups 0: no gate
 CASES = [(1, 1, 1), (1, 64, 0), (3, 63, 3), (7, 1001, 1), (33, 1024, 2), (40, 1025, 5), (50, 2048, 1), (20, 2049, 4),
-         (17, 4096, 17), (19, 4097, 1), (31, 8192, 2), (9, 8193, 3), (5, 16384, 1), (2000, 72, 7), (513, 1000, 3)]
+         (17, 4096, 17), (19, 4097, 1), (31, 8192, 2), (9, 8193, 3), (5, 16384, 1), (400, 1536, 2), (700, 1360, 1), (350, 5120, 1), (2000, 72, 7), (513, 1000, 3)]
 
 
 @pytest.mark.parametrize("T,H,groups", CASES)
