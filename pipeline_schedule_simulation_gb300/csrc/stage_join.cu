@@ -483,6 +483,15 @@ __device__ __forceinline__ Raw8 ring_raw(const unsigned char *stage, uint32_t at
     return Raw8{{w.x, w.y, w.z, w.w}};
 }
 
+// A vector past the row's end (ok false) reads as zeros, without a branch: what
+// it would read is put aside, not skipped.
+__device__ __forceinline__ Raw8 ring_raw(const unsigned char *stage, uint32_t at, int c, bool ok) {
+    Raw8 r = ring_raw(stage, at, ok ? c : 0);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) r.w[j] = ok ? r.w[j] : 0u;
+    return r;
+}
+
 template <int NT, int NV, bool KEEP, bool FULL>
 __global__ void __launch_bounds__(NT, 1024 / NT) k_join_forward_ring(const JoinForward a, const int stages) {
     extern __shared__ __align__(128) unsigned char smem[];
@@ -520,13 +529,9 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_join_forward_ring(const JoinF
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = (i * nt + (int)threadIdx.x) * 8;
-            fr[i] = Raw8{};
-#pragma unroll
-            for (int j = 0; j < 8; ++j) y[i][j] = 0.f;
-            if (FULL || c < a.H) {
-                fr[i] = ring_raw(stage, 0, c);
-                widen(ring_raw(stage, row_bytes, c), y[i]);
-            }
+            const bool ok = FULL || c < a.H;
+            fr[i] = ring_raw(stage, 0, c, ok);
+            widen(ring_raw(stage, row_bytes, c, ok), y[i]);
             float f[8];
             widen(fr[i], f);
 #pragma unroll
@@ -676,11 +681,13 @@ __global__ void __launch_bounds__(NT, 512 / NT) k_join_backward_ring(const JoinB
         }
         if (t + 1 < last) ahead(t + 1);
         tc::mbar_wait(ring.bars + 8 * slot, parity, &stop, 6);
-        const auto norm = [&](uint32_t at, int c, float step, float (&n)[8]) {
+        const auto norm = [&](uint32_t at, int c, bool ok, float step, float (&n)[8]) {
             if (PACKED) {
-                unpack8(*reinterpret_cast<const uint2 *>(stage + at + c), step, n);
+                uint2 q = *reinterpret_cast<const uint2 *>(stage + at + (ok ? c : 0));
+                q.x = ok ? q.x : 0u, q.y = ok ? q.y : 0u;
+                unpack8(q, step, n);
             } else {
-                widen(ring_raw(stage, at, c), n);
+                widen(ring_raw(stage, at, c, ok), n);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) n[j] *= step;
             }
@@ -689,19 +696,16 @@ __global__ void __launch_bounds__(NT, 512 / NT) k_join_backward_ring(const JoinB
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = (i * nt + (int)threadIdx.x) * 8;
+            const bool ok = FULL || c < a.H;
+            float w[8];
+            norm(wide, c, ok, step_y[i], n2[i]);
+            widen(ring_raw(stage, 0, c, ok), d[i]);
+            widen(w_pre[i], w);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) n2[i][j] = d[i][j] = 0.f;
-            if (FULL || c < a.H) {
-                float w[8];
-                norm(wide, c, step_y[i], n2[i]);
-                widen(ring_raw(stage, 0, c), d[i]);
-                widen(w_pre[i], w);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    sum_pre[i][j] += d[i][j] * n2[i][j];
-                    d[i][j] *= w[j];
-                    ss += d[i][j] * n2[i][j];
-                }
+            for (int j = 0; j < 8; ++j) {
+                sum_pre[i][j] += d[i][j] * n2[i][j];
+                d[i][j] *= w[j];
+                ss += d[i][j] * n2[i][j];
             }
         }
         const float m2 = block_sum<NT>(ss, sh[0]) * (inv_h * r2);
@@ -710,28 +714,25 @@ __global__ void __launch_bounds__(NT, 512 / NT) k_join_backward_ring(const JoinB
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = (i * nt + (int)threadIdx.x) * 8;
+            const bool ok = FULL || c < a.H;
+            float u[8];
+            if (a.dy) {
+                widen(ring_raw(stage, at_dy, c, ok), u);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) n1[i][j] = 0.f;
-            if (FULL || c < a.H) {
-                float u[8];
-                if (a.dy) {
-                    widen(ring_raw(stage, at_dy, c), u);
+                for (int j = 0; j < 8; ++j) d[i][j] = fmaf(r2, d[i][j], fmaf(-m2, n2[i][j], u[j]));
+            } else {
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) d[i][j] = fmaf(r2, d[i][j], fmaf(-m2, n2[i][j], u[j]));
-                } else {
+                for (int j = 0; j < 8; ++j) d[i][j] = fmaf(r2, d[i][j], -m2 * n2[i][j]);
+            }
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) d[i][j] = fmaf(r2, d[i][j], -m2 * n2[i][j]);
-                }
+            for (int j = 0; j < 8; ++j) u[j] = a.alpha * d[i][j];
+            if (ok) store8_bf16<true>(px + i * nt * 8, 8, u);
+            norm(wide + saved, c, ok, step_f[i], n1[i]);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) u[j] = a.alpha * d[i][j];
-                store8_bf16<true>(px + i * nt * 8, 8, u);
-                norm(wide + saved, c, step_f[i], n1[i]);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    sum_post[i][j] += d[i][j] * n1[i][j];
-                    d[i][j] *= gw[i][j];
-                    ss += d[i][j] * n1[i][j];
-                }
+            for (int j = 0; j < 8; ++j) {
+                sum_post[i][j] += d[i][j] * n1[i][j];
+                d[i][j] *= gw[i][j];
+                ss += d[i][j] * n1[i][j];
             }
         }
         const float m1 = block_sum<NT>(ss, sh[1]) * (inv_h * r1);
