@@ -45,7 +45,8 @@
 extern "C" {
 #endif
 
-/* Limits (PP_ERR_SIZE beyond them). */
+/* Limits (PP_ERR_SIZE beyond them, and where a product would have more than
+ * 2^31 tiles). */
 #define PP_STAGE_MAX_ROWS (1 << 24)   /* T: tokens of one call */
 #define PP_STAGE_MAX_VOCAB (1 << 24)  /* V, and N of the weight gradient */
 #define PP_STAGE_MAX_WIDTH (1 << 16)  /* H of head and kept */
@@ -130,7 +131,8 @@ int pp_stage_join_forward(const uint16_t *x, int64_t stride_x, const uint16_t *f
  *   s  = d gate w_post                             df = rstd_post (s - n1 mean_h(s n1))   bf16
  *   dw_pre = sum_t dh n2     dw_post = sum_t d gate n1     dgate[g] = sum_{t of g} d n1 w_post   float
  * y and f come as bf16 (y, f given) or as checkpoints (y_q, y_e, f_q, f_e given):
- * one form for both.  dgate is NULL exactly where gate is. */
+ * one form for both.  dgate is NULL exactly where gate is; of it only the rows
+ * of gates that some token uses are written. */
 size_t pp_stage_join_backward_workspace(int64_t T, int64_t H, int64_t rows_per_gate);
 int pp_stage_join_backward(const uint16_t *dh, int64_t stride_dh, const uint16_t *dy, int64_t stride_dy,
                            const uint16_t *y, int64_t stride_y, const uint16_t *f, int64_t stride_f,

@@ -1,14 +1,26 @@
 // stage_head.cu -- softmax cross entropy of the last stage over a large
 // vocabulary, and its gradients, without keeping the logits.
 //
-// Forward.  l = x w^T is taken tile by tile; of each (token, vocabulary tile)
-// only the largest logit and the sum of exponentials relative to it leave the
-// product, and a second kernel joins the tiles of a token:
+// Forward.  l = x w^T is taken tile by tile; of each token's part of a
+// vocabulary tile (two pieces) only the largest logit and the sum of
+// exponentials relative to it leave the product, and a second kernel joins the
+// pieces of a token:
 //   m = max_i m_i,  s = sum_i s_i e^(m_i - m),  lse = m + log s.
 // Backward.  d = weight (softmax - onehot) is recomputed for a piece of the
 // vocabulary at a time, as bf16 in the workspace, and both gradients take
 // their product with it before the next piece:  dx += d w_piece,
-// dw_piece = d^T x.
+// dw_piece = d^T x.  So the step is four products of 2 T V H, a third more
+// than the gradients alone would need with the logits kept (4.3 GB in 32 bits
+// at 8192 x 131072).
+// d is rounded to bf16 before `scale` (and exact near -1 at a target, where the
+// gradient is largest): a tensor-core operand cannot be wider, and an error of
+// 2^-8 of each term at most is no more than the rounding of the results.
+//
+// The products bound both directions from a few hundred tokens on: 4096 tokens
+// on 131072 x 4096 take 2.52 ms (1750 TFLOP/s; a cuBLAS product alone holds
+// 1703 in a long loop on the same GPU, 1945 in a burst), the step of 8192 tokens
+// 20.8 ms (1690 TFLOP/s over its four products).  For a few tokens reading w
+// does: one token on 32000 x 2048 takes 31 us of the 19 that its 131 MB need.
 #include <algorithm>
 
 #include "stage_product.cuh"
