@@ -20,9 +20,10 @@
 // on 131072 x 4096 take 2.52 ms (1750 TFLOP/s; a cuBLAS product alone holds
 // 1703 in a long loop on the same GPU, 1945 in a burst), the step of 8192 tokens
 // 20.8 ms (1690 TFLOP/s over its four products).  For a few tokens reading w
-// does: one token on 32000 x 2048 takes 31 us of the 19 that its 131 MB need.
+// does: one token on 32000 x 2048 takes 29 us, its 131 MB alone 19 us.
 #include <algorithm>
 
+#include "stage_kept.cuh"
 #include "stage_product.cuh"
 
 namespace pps {
@@ -214,6 +215,104 @@ struct DwEpi {
     }
 };
 
+// ---- few tokens: w is read once, by the row
+
+// One or two tokens are two multiplications for every 2 bytes of w: a warp takes
+// 4 rows of w at a time straight from memory, the lanes 8 columns each, against
+// the tokens in shared memory as 32-bit floats, and keeps the tokens'
+// statistics over its run of the vocabulary; a block is one piece.  Rows need no
+// alignment (as a product, rows that TMA cannot load are copied first).  One
+// token on 131072 x 4096 takes 169 us, 94 % of the measured bandwidth (275 us
+// with rows of 4095), on 32000 x 2048 29 us with the join of the pieces, 34 us
+// as a product.  Four tokens are 313 us on 131072 x 4096 and 193 us as a product,
+// so the limit is two.
+constexpr int kFewTokens = 2, kFewFloats = 16384, kFewRows = 4, kFewWarps = 8, kFewBlocks = 4;
+
+template <int NT, bool VEC>
+__global__ void __launch_bounds__(32 * kFewWarps, kFewBlocks) k_head_few(const uint16_t *x, int64_t stride_x, const uint16_t *w,
+                                                            int64_t stride_w, const int64_t *target, int T, int64_t V,
+                                                            int H, int64_t rows, float2 *part, float *picked) {
+    extern __shared__ float4 xs[];  // [NT][2][chunks]: the two quads of each 8 columns apart
+    __shared__ float2 sh[kFewWarps][NT];
+    let_next_start();
+    after_previous();
+    const int chunks = (H + 7) / 8;
+    for (int i = threadIdx.x; i < NT * chunks; i += 32 * kFewWarps) {
+        const int t = i / chunks, c = i - t * chunks;
+        float v[8] = {};
+        if (t < T) load8_bf16<false>(x + t * stride_x + c * 8, H - c * 8, v);
+        xs[(2 * t) * chunks + c] = make_float4(v[0], v[1], v[2], v[3]);
+        xs[(2 * t + 1) * chunks + c] = make_float4(v[4], v[5], v[6], v[7]);
+    }
+    __syncthreads();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t first = ((int64_t)blockIdx.x * kFewWarps + warp) * rows, last = min(first + rows, V);
+    float m[NT], s[NT];
+    int64_t want[NT];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) m[t] = kNegInf, s[t] = 0.f, want[t] = t < T ? target[t] : -1;
+    for (int64_t v0 = first; v0 < last; v0 += kFewRows) {
+        const uint16_t *row[kFewRows];
+#pragma unroll
+        for (int r = 0; r < kFewRows; ++r) row[r] = w + min(v0 + r, last - 1) * stride_w;
+        float acc[kFewRows][NT] = {};
+#pragma unroll 2
+        for (int c = lane; c < chunks; c += 32) {
+            Raw8 q[kFewRows];
+#pragma unroll
+            for (int r = 0; r < kFewRows; ++r) q[r] = load8<VEC>(row[r] + c * 8, H - c * 8);
+            float4 a[NT], b[NT];
+#pragma unroll
+            for (int t = 0; t < NT; ++t) a[t] = xs[2 * t * chunks + c], b[t] = xs[(2 * t + 1) * chunks + c];
+#pragma unroll
+            for (int r = 0; r < kFewRows; ++r) {
+                float u[8];
+                widen(q[r], u);
+#pragma unroll
+                for (int t = 0; t < NT; ++t) {
+                    float z = acc[r][t];
+                    z = fmaf(u[0], a[t].x, z), z = fmaf(u[1], a[t].y, z), z = fmaf(u[2], a[t].z, z);
+                    z = fmaf(u[3], a[t].w, z), z = fmaf(u[4], b[t].x, z), z = fmaf(u[5], b[t].y, z);
+                    acc[r][t] = fmaf(u[7], b[t].w, fmaf(u[6], b[t].z, z));
+                }
+            }
+        }
+#pragma unroll
+        for (int r = 0; r < kFewRows; ++r) {
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+                float l = acc[r][t];
+#pragma unroll
+                for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(~0u, l, o);
+                if (v0 + r < last) {
+                    const float top = fmaxf(m[t], l), ref = ref_of(top);
+                    s[t] = rebase(s[t], m[t], ref) + exp2_fast((l - ref) * kLog2e);
+                    m[t] = top;
+                    if (lane == 0 && want[t] == v0 + r) picked[t] = l;
+                }
+            }
+        }
+    }
+    if (lane == 0) {
+#pragma unroll
+        for (int t = 0; t < NT; ++t) sh[warp][t] = make_float2(m[t], s[t]);
+    }
+    __syncthreads();
+    if (threadIdx.x < T) {  // the warps' parts, in the order of the warps
+        const int t = threadIdx.x;
+        float top = kNegInf, sum = 0.f;
+        for (int i = 0; i < kFewWarps; ++i) top = fmaxf(top, sh[i][t].x);
+        const float ref = ref_of(top);
+        for (int i = 0; i < kFewWarps; ++i) sum += rebase(sh[i][t].y, sh[i][t].x, ref);
+        part[(int64_t)blockIdx.x * T + t] = make_float2(top, sum);
+    }
+}
+
+bool few_tokens(int64_t T, int64_t H) { return T <= kFewTokens && T * round_up(H, 8) <= kFewFloats; }
+
+// Rows of w to a warp: all blocks are resident.
+int64_t few_rows(int64_t V) { return ceil_div(V, (int64_t)sm_count() * kFewBlocks * kFewWarps); }
+
 // 8 tokens a block: 32 lanes along the pieces of each.  First the largest
 // logit, then the sums relative to it.
 __global__ void __launch_bounds__(256) k_head_join(const float2 *part, const float *picked, const int64_t *target,
@@ -306,17 +405,25 @@ struct ForwardSpace {
     Aligned x, w;
     float2 *part;
     float *picked;
+    bool few;
     ProductPlan plan;
+    int64_t pieces;
     size_t bytes;
 };
 ForwardSpace forward_space(void *ws, const uint16_t *x, int64_t sx, const uint16_t *w, int64_t sw, int64_t T,
                            int64_t V, int64_t H) {
     Carve c{static_cast<unsigned char *>(ws)};
-    ForwardSpace s;
-    s.x = aligned(c, x, sx, T, H, ceil_div(V, 256));
-    s.w = aligned(c, w, sw, V, H, ceil_div(T, 256));
-    s.plan = plan_product(T, V, H, false, false);
-    s.part = c.take<float2>(kPieces * s.plan.nt * T);
+    ForwardSpace s{};
+    s.few = few_tokens(T, H);
+    if (s.few) {
+        s.pieces = ceil_div(V, few_rows(V) * kFewWarps);
+    } else {
+        s.x = aligned(c, x, sx, T, H, ceil_div(V, 256));
+        s.w = aligned(c, w, sw, V, H, ceil_div(T, 256));
+        s.plan = plan_product(T, V, H, false, false);
+        s.pieces = kPieces * s.plan.nt;
+    }
+    s.part = c.take<float2>(s.pieces * T);
     s.picked = c.take<float>(T);
     s.bytes = c.used;
     return s;
@@ -373,14 +480,26 @@ extern "C" int pp_stage_head_forward(const uint16_t *x, int64_t stride_x, const 
     if ((!loss && !lse) || ((uintptr_t)loss & 3) || ((uintptr_t)lse & 3)) return PP_ERR_ARG;
     const ForwardSpace s = forward_space(workspace, x, stride_x, w, stride_w, T, V, H);
     if (!workspace || ((uintptr_t)workspace & (kStageAlign - 1)) || workspace_bytes < s.bytes) return PP_ERR_ARG;
-    int rp = copy_if(s.x, x, stride_x, T, H, stream);
-    if (rp == PP_OK) rp = copy_if(s.w, w, stride_w, V, H, stream);
-    if (rp == PP_OK)
-        rp = launch_product<kRowsK, kRowsK>(s.x.at, s.w.at, T, V, H, StatsEpi{target, T, V, s.part, s.picked}, s.plan,
-                                            stream);
+    int rp = PP_OK;
+    if (s.few) {
+        const bool vec = rows_aligned(w, stride_w, V, 2);
+        const auto kernel = T == 1 ? (vec ? k_head_few<1, true> : k_head_few<1, false>)
+                                   : (vec ? k_head_few<2, true> : k_head_few<2, false>);
+        static std::atomic<uint64_t> ready[4];
+        rp = allow_smem(kernel, kFewFloats * 4, ready[2 * (T - 1) + vec]);
+        if (rp == PP_OK)
+            rp = launch_after(kernel, s.pieces, 32 * kFewWarps, (int)(T * ceil_div(H, 8) * 32), stream, 1, x, stride_x, w,
+                              stride_w, target, (int)T, V, (int)H, few_rows(V), s.part, s.picked);
+    } else {
+        rp = copy_if(s.x, x, stride_x, T, H, stream);
+        if (rp == PP_OK) rp = copy_if(s.w, w, stride_w, V, H, stream);
+        if (rp == PP_OK)
+            rp = launch_product<kRowsK, kRowsK>(s.x.at, s.w.at, T, V, H, StatsEpi{target, T, V, s.part, s.picked}, s.plan,
+                                                stream);
+    }
     if (rp != PP_OK) return rp;
     return launch_after(k_head_join, ceil_div(T, 8), 256, 0, stream, 1, (const float2 *)s.part, (const float *)s.picked,
-                        target, kPieces * s.plan.nt, T, V, loss, lse);
+                        target, s.pieces, T, V, loss, lse);
 }
 
 extern "C" size_t pp_stage_head_backward_workspace(const uint16_t *x, int64_t stride_x, const uint16_t *w,

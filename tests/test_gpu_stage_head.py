@@ -51,6 +51,21 @@ def test_loss_and_gradients(S, T, V, H, weighted):
     assert (got["loss"][target < 0] == 0).all() and (got["dx"][target < 0] == 0).all()
 
 
+@pytest.mark.parametrize("T", [1, 2, 3, 4, 5])
+@pytest.mark.parametrize("V,H,stride,offset", [(1, 8, 8, 0), (7, 4096, 4096, 0), (5000, 1001, 1001, 1), (40000, 264, 272, 8),
+                                               (9999, 4104, 4105, 3), (3000, 16384, 16384, 0)])
+def test_few_tokens(S, T, V, H, stride, offset):
+    """Both sides of the limit up to which w is read by the row: aligned and unaligned rows, more and fewer rows than
+    there are warps, widths on both sides of what shared memory holds."""
+    x, w, target, _ = _inputs(T, V, H, T + V + H, stride=stride, offset=offset)
+    if T > 2:
+        target[1] = -1
+    got = S.head_forward(x, w, target)
+    want = R.head(x, w, target)
+    for k in ("loss", "lse"):
+        R.check(got[k], want[k], k)
+
+
 @pytest.mark.parametrize("T,V,H,stride,offset", [(130, 300, 64, 64, 1), (130, 300, 64, 67, 0), (77, 515, 100, 104, 8),
                                                  (77, 515, 100, 133, 3)])
 def test_strides_and_offsets(S, T, V, H, stride, offset):
