@@ -141,37 +141,22 @@ struct DxEpi {
     int64_t V, ld_acc, ld;
     float scale;
     bool first, last, vec;
-    __device__ __forceinline__ void run(int64_t t, int64_t n, const float (&v)[32], int) const {
-        float s[32];
-#pragma unroll
-        for (int j = 0; j < 32; ++j) s[j] = v[j];
-        if (!first) add_f32(s, acc + t * ld_acc + n);
+    __device__ __forceinline__ void finish(int64_t t, int64_t n, float (&v)[32]) const {
+        if (!first) add_f32(v, acc + t * ld_acc + n);
         if (last) {
             const bool in = inside(target[t], V);
 #pragma unroll
-            for (int j = 0; j < 32; ++j) s[j] = in ? s[j] * scale : 0.f;
-            store_bf16(dx + t * ld + n, s);
-        } else {
-            store_f32(acc + t * ld_acc + n, s);
+            for (int j = 0; j < 32; ++j) v[j] = in ? v[j] * scale : 0.f;
         }
     }
-    __device__ __forceinline__ void quad(int64_t t, int64_t n, int left, const float4 &v, int) const {
-        float4 s = v;
-        float4 *a = reinterpret_cast<float4 *>(acc + t * ld_acc + n);
-        if (!first) {
-            const float4 b = *a;
-            s.x += b.x, s.y += b.y, s.z += b.z, s.w += b.w;
-        }
-        if (last) {
-            const float c = scale;
-            s = inside(target[t], V) ? make_float4(s.x * c, s.y * c, s.z * c, s.w * c) : make_float4(0.f, 0.f, 0.f, 0.f);
-            store_quad(dx + t * ld + n, left, s);
-        } else {
-            *a = s;
-        }
+    __device__ __forceinline__ bool narrow() const { return last; }
+    __device__ __forceinline__ void row(int64_t t, int64_t n, const float (&v)[32]) const { store_bf16(dx + t * ld + n, v); }
+    __device__ __forceinline__ void put(int64_t t, int64_t n, const float4 &v, int) const {
+        store_quad(acc + t * ld_acc + n, v);
     }
-    __device__ __forceinline__ void one(int64_t t, int64_t n, float v, int) const {
-        float s = first ? v : acc[t * ld_acc + n] + v;
+    __device__ __forceinline__ float with(int64_t t, int64_t n) const { return first ? 0.f : acc[t * ld_acc + n]; }
+    __device__ __forceinline__ void one(int64_t t, int64_t n, float v, float b, int) const {
+        const float s = v + b;
         if (last) dx[t * ld + n] = inside(target[t], V) ? f32_to_bf16(s * scale) : 0;
         else acc[t * ld_acc + n] = s;
     }
@@ -184,34 +169,19 @@ struct DwEpi {
     int64_t ld;
     float scale;
     bool add, vec;
-    __device__ __forceinline__ void run(int64_t m, int64_t n, const float (&v)[32], int) const {
-        float s[32];
+    __device__ __forceinline__ void finish(int64_t m, int64_t n, float (&v)[32]) const {
 #pragma unroll
-        for (int j = 0; j < 32; ++j) s[j] = v[j] * scale;
-        if (dw16) {
-            store_bf16(dw16 + m * ld + n, s);
-        } else {
-            if (add) add_f32(s, dw32 + m * ld + n);
-            store_f32(dw32 + m * ld + n, s);
-        }
+        for (int j = 0; j < 32; ++j) v[j] *= scale;
+        if (add) add_f32(v, dw32 + m * ld + n);
     }
-    __device__ __forceinline__ void quad(int64_t m, int64_t n, int left, const float4 &v, int) const {
-        float4 s = make_float4(v.x * scale, v.y * scale, v.z * scale, v.w * scale);
-        if (dw16) {
-            store_quad(dw16 + m * ld + n, left, s);
-            return;
-        }
-        float *p = dw32 + m * ld + n;
-        if (add) {
-            const float4 b = load_quad(p, left);
-            s.x += b.x, s.y += b.y, s.z += b.z, s.w += b.w;
-        }
-        store_quad(p, left, s);
-    }
-    __device__ __forceinline__ void one(int64_t m, int64_t n, float v, int) const {
-        const float s = v * scale;
+    __device__ __forceinline__ bool narrow() const { return dw16 != nullptr; }
+    __device__ __forceinline__ void row(int64_t m, int64_t n, const float (&v)[32]) const { store_bf16(dw16 + m * ld + n, v); }
+    __device__ __forceinline__ void put(int64_t m, int64_t n, const float4 &v, int) const { store_quad(dw32 + m * ld + n, v); }
+    __device__ __forceinline__ float with(int64_t m, int64_t n) const { return add ? dw32[m * ld + n] : 0.f; }
+    __device__ __forceinline__ void one(int64_t m, int64_t n, float v, float b, int) const {
+        const float s = v * scale + b;
         if (dw16) dw16[m * ld + n] = f32_to_bf16(s);
-        else dw32[m * ld + n] = add ? dw32[m * ld + n] + s : s;
+        else dw32[m * ld + n] = s;
     }
 };
 

@@ -5,7 +5,7 @@
 // 16384 x 8192 on one GB300 in 67 us and 73 us, 88 % and 81 % of the measured
 // copy rate.  The weight gradient dw = add + dy^T v is a tensor-core product
 // over the tokens; v is unpacked first into panels of the workspace (3 bytes
-// an element, 32 us of the 727 us that 8192^3 takes), exactly, since every
+// an element, 32 us of the 711-728 us that 8192^3 takes), exactly, since every
 // value of a checkpoint is a bf16 number.  Both operands lie with their tokens
 // apart (MN-major), which the MMA reads as they are.
 #include "stage_kept.cuh"
@@ -86,28 +86,14 @@ struct WgradEpi {
     float *dw;
     int64_t ld_add, ld;
     bool vec;
-    __device__ __forceinline__ void run(int64_t m, int64_t n, const float (&v)[32], int) const {
-        if (add) {
-            float s[32];
-#pragma unroll
-            for (int j = 0; j < 32; ++j) s[j] = v[j];
-            add_f32(s, add + m * ld_add + n);
-            store_f32(dw + m * ld + n, s);
-        } else {
-            store_f32(dw + m * ld + n, v);
-        }
+    __device__ __forceinline__ void finish(int64_t m, int64_t n, float (&v)[32]) const {
+        if (add) add_f32(v, add + m * ld_add + n);
     }
-    __device__ __forceinline__ void quad(int64_t m, int64_t n, int left, const float4 &v, int) const {
-        float4 s = v;
-        if (add) {
-            const float4 b = load_quad(add + m * ld_add + n, left);
-            s.x += b.x, s.y += b.y, s.z += b.z, s.w += b.w;
-        }
-        store_quad(dw + m * ld + n, left, s);
-    }
-    __device__ __forceinline__ void one(int64_t m, int64_t n, float v, int) const {
-        dw[m * ld + n] = add ? add[m * ld_add + n] + v : v;
-    }
+    __device__ __forceinline__ bool narrow() const { return false; }
+    __device__ __forceinline__ void row(int64_t, int64_t, const float (&)[32]) const {}
+    __device__ __forceinline__ void put(int64_t m, int64_t n, const float4 &v, int) const { store_quad(dw + m * ld + n, v); }
+    __device__ __forceinline__ float with(int64_t m, int64_t n) const { return add ? add[m * ld_add + n] : 0.f; }
+    __device__ __forceinline__ void one(int64_t m, int64_t n, float v, float b, int) const { dw[m * ld + n] = b + v; }
 };
 
 bool bad_kept(const int8_t *q, int64_t sq, const int8_t *e, int64_t se, int64_t H) {

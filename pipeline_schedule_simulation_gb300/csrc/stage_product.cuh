@@ -5,9 +5,12 @@
 // and handed to an epilogue instead of being stored.  Epilogues that store C
 // (kStore), with columns in quads where `vec` says that rows are aligned and one
 // by one otherwise (part: which part of K):
-//   run(m, n, v, part)         columns n .. n+31 of row m
-//   quad(m, n, left, v, part)  columns n .. n+3, of which `left` exist
-//   one(m, n, v, part)         one column
+//   finish(m, n, v)        columns n .. n+31 of row m: scaled, added, in place
+//   narrow()               whether rows are stored as bf16:
+//   row(m, n, v)           then 32 finished columns at once,
+//   put(m, n, v, part)     else four
+//   with(m, n)             what one column is added to
+//   one(m, n, v, b, part)  one column, from the sum and that to memory
 // The others get a row as a thread has it.  A row's part of a column tile is two
 // pieces, the even and the odd runs of 32 columns:
 //   typename Epi::Row  what a row needs beside its sums
@@ -111,29 +114,8 @@ __device__ __forceinline__ void tile_at(const ProductShape &s, uint32_t i, int &
     n = r / rows;
 }
 
-// Four columns of a row, of which `left` exist; aligned.
-__device__ __forceinline__ void store_quad(uint16_t *p, int left, const float4 &v) {
-    if (left >= 4) {
-        *reinterpret_cast<uint2 *>(p) = make_uint2(f32_to_bf16x2(v.x, v.y), f32_to_bf16x2(v.z, v.w));
-    } else {
-        p[0] = f32_to_bf16(v.x);
-        if (left > 1) p[1] = f32_to_bf16(v.y);
-        if (left > 2) p[2] = f32_to_bf16(v.z);
-    }
-}
-__device__ __forceinline__ void store_quad(float *p, int left, const float4 &v) {
-    if (left >= 4) {
-        *reinterpret_cast<float4 *>(p) = v;
-    } else {
-        p[0] = v.x;
-        if (left > 1) p[1] = v.y;
-        if (left > 2) p[2] = v.z;
-    }
-}
-__device__ __forceinline__ float4 load_quad(const float *p, int left) {
-    if (left >= 4) return *reinterpret_cast<const float4 *>(p);
-    return make_float4(p[0], left > 1 ? p[1] : 0.f, left > 2 ? p[2] : 0.f, 0.f);
-}
+// Four columns of a row, aligned.
+__device__ __forceinline__ void store_quad(float *p, const float4 &v) { *reinterpret_cast<float4 *>(p) = v; }
 
 // 32 columns of a row as bf16, aligned.
 __device__ __forceinline__ void store_bf16(uint16_t *p, const float (&v)[32]) {
@@ -144,13 +126,7 @@ __device__ __forceinline__ void store_bf16(uint16_t *p, const float (&v)[32]) {
                        f32_to_bf16x2(v[8 * j + 4], v[8 * j + 5]), f32_to_bf16x2(v[8 * j + 6], v[8 * j + 7]));
 }
 
-// 32 columns of a row in 32 bits, aligned.
-__device__ __forceinline__ void store_f32(float *p, const float (&v)[32]) {
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-        reinterpret_cast<float4 *>(p)[j] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
-}
-// The same added to what `to` holds, which is all loaded first.
+// 32 columns of a row, aligned, added to what `to` holds, all loaded first.
 __device__ __forceinline__ void add_f32(float (&v)[32], const float *to) {
     float4 b[8];
 #pragma unroll
@@ -159,36 +135,51 @@ __device__ __forceinline__ void add_f32(float (&v)[32], const float *to) {
     for (int j = 0; j < 8; ++j) v[4 * j] += b[j].x, v[4 * j + 1] += b[j].y, v[4 * j + 2] += b[j].z, v[4 * j + 3] += b[j].w;
 }
 
-// 32 rows x 32 columns, a row to a lane.  Aligned rows are stored by their lanes,
-// everything that they are added to loaded first (turning them into whole
-// lines as below made the weight gradient of 8192^3 757 us instead of 712).  Others
-// are turned through the warp's shared memory, so that the lanes' narrow
-// stores lie side by side.
+// 32 rows x 32 columns, a row to a lane.  Each lane finishes its row's values
+// (what they are added to comes in whole lines that way); then they are turned
+// through the warp's shared memory and stored along the rows, 4 rows at once,
+// where the lanes' own stores would be 16 bytes of 32 rows each: the weight
+// gradient of 512 tokens on 8192 x 8192 takes 84 us into new memory, 142 us by
+// the lanes.  (32 columns of bf16 are half a line either way; by the lanes they
+// are 16 bytes a store, turned 8: those stay with the lanes.)  Unaligned rows
+// are turned too, a column to a lane, 8 rows on their way at once.
 template <class Epi>
 __device__ __forceinline__ void store_run(const Epi &epi, float4 *turn, int lane, int64_t m0, int64_t M, int n, int end,
-                                          int part, const float (&v)[32]) {
-    if (epi.vec) {
-        const int64_t m = m0 + lane;
-        if (m >= M) return;
-        if (end - n >= 32) {
-            epi.run(m, n, v, part);
-        } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const int left = end - (n + 4 * j);
-                if (left > 0)
-                    epi.quad(m, n + 4 * j, left, make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]), part);
-            }
-        }
+                                          int part, float (&v)[32]) {
+    if (m0 >= M) return;
+    const bool whole = epi.vec && end - n >= 32;
+    if (whole && m0 + lane < M) epi.finish(m0 + lane, n, v);
+    if (whole && epi.narrow()) {
+        if (m0 + lane < M) epi.row(m0 + lane, n, v);
         return;
     }
 #pragma unroll
     for (int j = 0; j < 8; ++j)
         turn[lane * 8 + (j ^ (lane & 7))] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
     __syncwarp();
-    const float *one = reinterpret_cast<const float *>(turn);
-    for (int r = 0; r < 32 && m0 + r < M; ++r)
-        if (n + lane < end) epi.one(m0 + r, n + lane, one[r * 32 + ((lane >> 2) ^ (r & 7)) * 4 + (lane & 3)], part);
+    if (whole) {
+        const int at = lane & 7, row = lane >> 3;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const int r = 4 * k + row;
+            const float4 x = turn[r * 8 + (at ^ (r & 7))];
+            if (m0 + r < M) epi.put(m0 + r, n + 4 * at, x, part);
+        }
+    } else {
+        const float *one = reinterpret_cast<const float *>(turn);
+        const int rows = n + lane < end ? (M - m0 < 32 ? (int)(M - m0) : 32) : 0;
+        for (int r0 = 0; r0 < rows; r0 += 8) {
+            float b[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) b[k] = r0 + k < rows ? epi.with(m0 + r0 + k, n + lane) : 0.f;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const int r = r0 + k;
+                const float x = one[r * 32 + ((lane >> 2) ^ (r & 7)) * 4 + (lane & 3)];
+                if (r < rows) epi.one(m0 + r, n + lane, x, b[k], part);
+            }
+        }
+    }
     __syncwarp();
 }
 
@@ -508,14 +499,17 @@ struct PartEpi {
     static constexpr bool kStore = true, kWhole = false;
     static constexpr bool vec = true;
     float *parts;
-    int64_t M, ld;  // ld is a multiple of 4: a quad may go past the last column
-    __device__ __forceinline__ void quad(int64_t m, int64_t n, int, const float4 &v, int part) const {
+    int64_t M, ld;  // ld is a multiple of 4
+    __device__ __forceinline__ bool narrow() const { return false; }
+    __device__ __forceinline__ void finish(int64_t, int64_t, float (&)[32]) const {}
+    __device__ __forceinline__ void row(int64_t, int64_t, const float (&)[32]) const {}
+    __device__ __forceinline__ void put(int64_t m, int64_t n, const float4 &v, int part) const {
         *reinterpret_cast<float4 *>(parts + (part * M + m) * ld + n) = v;
     }
-    __device__ __forceinline__ void run(int64_t m, int64_t n, const float (&v)[32], int part) const {
-        store_f32(parts + (part * M + m) * ld + n, v);
+    __device__ __forceinline__ float with(int64_t, int64_t) const { return 0.f; }
+    __device__ __forceinline__ void one(int64_t m, int64_t n, float v, float, int part) const {
+        parts[(part * M + m) * ld + n] = v;
     }
-    __device__ __forceinline__ void one(int64_t, int64_t, float, int) const {}
 };
 }  // namespace
 
@@ -548,15 +542,10 @@ __global__ void __launch_bounds__(256) k_join_parts(const float *parts, int spli
         const float4 x = sh[r][q];
         v.x += x.x, v.y += x.y, v.z += x.z, v.w += x.w;
     }
-    const int left = N - n < 4 ? (int)(N - n) : 4;
-    if (epi.vec) {
-        epi.quad(m, n, left, v, 0);
-    } else {
-        const float x[4] = {v.x, v.y, v.z, v.w};
+    const float x[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-            if (j < left) epi.one(m, n + j, x[j], 0);
-    }
+    for (int j = 0; j < 4; ++j)
+        if (n + j < N) epi.one(m, n + j, x[j], epi.with(m, n + j), 0);
 }
 
 // Floats of scratch memory that product_in_parts needs (B is MN-major there).

@@ -91,7 +91,9 @@ def test_no_rows(S):
 @pytest.mark.parametrize("T,N,H", [(1, 1, 1), (1, 64, 64), (3, 70, 1001), (63, 128, 64), (65, 129, 65), (200, 1024, 1000),
                                    (128, 256, 256), (129, 257, 264), (1000, 40, 72), (4096, 64, 130), (511, 520, 511),
                                    # enough tiles for pairs of blocks
-                                   (100, 2000, 2010), (300, 1411, 2000), (65, 3000, 1025)])
+                                   (100, 2000, 2010), (300, 1411, 2000), (65, 3000, 1025),
+                                   # long sums: whole lines, parts of K
+                                   (2050, 2000, 1500), (2048, 1300, 2052), (5000, 136, 140)])
 @pytest.mark.parametrize("how", ["new", "add", "in place"])
 def test_weight_grad(S, T, N, H, how):
     g = R.generator(T + N + H)
