@@ -563,7 +563,9 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_join_forward_ring(const JoinF
         ss = 0.f;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int c = (i * nt + (int)threadIdx.x) * 8, at = FULL || c < a.H ? c : 0;
+            const int c = (i * nt + (int)threadIdx.x) * 8;
+            const bool ok = FULL || c < a.H;
+            const int at = ok ? c : 0;
             float w[8], f[8];
             load8_bf16<true>(a.w_post + at, 8, w);
             if (g) {
@@ -571,6 +573,9 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_join_forward_ring(const JoinF
 #pragma unroll
                 for (int j = 0; j < 8; ++j) w[j] *= f[j];
             }
+            // past the row's end column 0 was read: no weight, which an infinity or a NaN there would not be times 0
+#pragma unroll
+            for (int j = 0; j < 8; ++j) w[j] = ok ? w[j] : 0.f;
             widen(fr[i], f);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
@@ -578,11 +583,11 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_join_forward_ring(const JoinF
                 ss += y[i][j] * y[i][j];
             }
             const Raw8 yr = narrow(y[i]);
-            if (FULL || c < a.H) store8<true>(py + i * nt * 8, 8, yr);
+            if (ok) store8<true>(py + i * nt * 8, 8, yr);
             if (KEEP) {
                 int e;
                 const uint2 b = pack8(yr, e);  // y as its next reader sees it
-                if (FULL || c < a.H) {
+                if (ok) {
                     *reinterpret_cast<uint2 *>(qy + i * nt * 8) = b;
                     if ((threadIdx.x & 7) == 0) ey[i * nt * 8 / kBlock] = (int8_t)e;
                 }
