@@ -17,7 +17,7 @@
 #include <atomic>
 
 #include "stage_kept.cuh"
-#include "stage_tc.cuh"
+#include "stage_ring.cuh"
 
 namespace pps {
 namespace {
@@ -459,29 +459,8 @@ __global__ void __launch_bounds__(32 * kWarps, NV == 1 ? 4 : 2) k_join_backward_
 // vectors, and no vector's end is looked at (16384 x 8192 backward from
 // checkpoints: 216 us, 267 us with the looks).
 
-// Shared memory of one block: two mbarriers' worth of header, then the stages.
-constexpr int kRingHeader = 128, kMaxStages = 4;
-
-// The rows that one block takes, first, first + step, ... below last, each as
-// `parts` bulk copies into the ring's next stage.
-struct RowPart {
-    const unsigned char *p;
-    int64_t stride;  // bytes
-    uint32_t bytes, at;
-};
-template <int PARTS>
-struct Ring {
-    uint32_t base, bars, stage_bytes;
-    int stages;
-    RowPart part[PARTS];
-    __device__ __forceinline__ void load(int64_t row, int slot) const {  // one thread
-        const uint32_t bar = bars + 8 * slot, to = base + slot * stage_bytes;
-        tc::mbar_expect(bar, stage_bytes);
-#pragma unroll
-        for (int i = 0; i < PARTS; ++i)
-            if (part[i].bytes) tc::bulk_load(to + part[i].at, part[i].p + row * part[i].stride, part[i].bytes, bar);
-    }
-};
+// Shared memory of one block: a header with a barrier for each stage, then the stages.
+constexpr int kRingHeader = 128;
 
 __device__ __forceinline__ Raw8 ring_raw(const unsigned char *stage, uint32_t at, int c) {
     const uint4 w = *reinterpret_cast<const uint4 *>(stage + at + 2 * c);
@@ -501,7 +480,7 @@ template <int NT, int NV, bool KEEP, bool FULL>
 __global__ void __launch_bounds__(NT, 1024 / NT) k_join_forward_ring(const JoinForward a, const int stages) {
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ __align__(16) float sh[2][32];
-    __shared__ int stop;
+    __shared__ RingState state;
     const int nt = blockDim.x;  // a whole number of warps, NT at most
     if (threadIdx.x < 64) sh[threadIdx.x >> 5][threadIdx.x & 31] = 0.f;  // also for the warps that are not there
     let_next_start();
@@ -511,11 +490,9 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_join_forward_ring(const JoinF
                  {{(const unsigned char *)a.f, 2 * a.sf, row_bytes, 0}, {(const unsigned char *)a.x, 2 * a.sx, row_bytes, row_bytes}}};
     const float inv_h = 1.f / (float)a.H;
     if (threadIdx.x == 0) {
-        stop = 0;
-        for (int i = 0; i < stages; ++i) tc::mbar_init(ring.bars + 8 * i, 1);
-        tc::fence_barrier_init();
+        ring.init(&state);
         for (int i = 0; i < stages; ++i)
-            if (blockIdx.x + (int64_t)i * gridDim.x < a.T) ring.load(blockIdx.x + (int64_t)i * gridDim.x, i);
+            if (blockIdx.x + (int64_t)i * gridDim.x < a.T) ring.load(&state, blockIdx.x + (int64_t)i * gridDim.x, i, 0);
     }
     __syncthreads();
     int slot = 0;
@@ -527,8 +504,8 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_join_forward_ring(const JoinF
     for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
         const unsigned char *stage = smem + kRingHeader + slot * ring.stage_bytes;
         const uint16_t *g = a.gate ? a.gate + (a.rows_per_gate > 0 ? t / a.rows_per_gate : 0) * a.sg : nullptr;
-        // a wait that runs out is recorded; the block then goes through its rows without data
-        tc::mbar_wait(ring.bars + 8 * slot, parity, &stop, 5);
+        // a wait that runs out is recorded; the block then goes through its rows without data, and loads no more
+        tc::mbar_wait(ring.bars + 8 * slot, parity, &state.stop, 5);
         Raw8 fr[NV];
         float y[NV][8], ss = 0.f;
 #pragma unroll
@@ -544,10 +521,8 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_join_forward_ring(const JoinF
         }
         const float r1 = rsqrtf(block_sum<NT>(ss, sh[0]) * inv_h + a.eps);
         // every thread has read the stage
-        if (threadIdx.x == 0 && t + (int64_t)stages * gridDim.x < a.T) {
-            tc::fence_async();
-            ring.load(t + (int64_t)stages * gridDim.x, slot);
-        }
+        if (threadIdx.x == 0 && t + (int64_t)stages * gridDim.x < a.T)
+            ring.refill(&state, t + (int64_t)stages * gridDim.x, slot, parity);
         if (KEEP) {
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
@@ -616,13 +591,14 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_join_forward_ring(const JoinF
         }
         if (++slot == stages) slot = 0, parity ^= 1;
     }
+    if (threadIdx.x == 0) ring.finish(&state);
 }
 
 template <int NT, int NV, bool PACKED, bool FULL>
 __global__ void __launch_bounds__(NT, 512 / NT) k_join_backward_ring(const JoinBackward a, const int stages) {
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ __align__(16) float sh[2][32];
-    __shared__ int stop;
+    __shared__ RingState state;
     const int nt = blockDim.x;  // a whole number of warps, NT at most
     if (threadIdx.x < 64) sh[threadIdx.x >> 5][threadIdx.x & 31] = 0.f;  // also for the warps that are not there
     let_next_start();
@@ -640,11 +616,9 @@ __global__ void __launch_bounds__(NT, 512 / NT) k_join_backward_ring(const JoinB
     int64_t last = min(first + a.it.rows, (group + 1) * a.it.rows_per_gate);
     last = min(last, a.T);
     if (threadIdx.x == 0) {
-        stop = 0;
-        for (int i = 0; i < stages; ++i) tc::mbar_init(ring.bars + 8 * i, 1);
-        tc::fence_barrier_init();
+        ring.init(&state);
         for (int i = 0; i < stages; ++i)
-            if (first + i < last) ring.load(first + i, i);
+            if (first + i < last) ring.load(&state, first + i, i, 0);
     }
     // the weights of this thread's columns stay in registers: the item has one gate row
     Raw8 w_pre[NV];
@@ -690,7 +664,7 @@ __global__ void __launch_bounds__(NT, 512 / NT) k_join_backward_ring(const JoinB
             step_f[i] = PACKED ? step_of(ef[i]) * r1 : r1;
         }
         if (t + 1 < last) ahead(t + 1);
-        tc::mbar_wait(ring.bars + 8 * slot, parity, &stop, 6);
+        tc::mbar_wait(ring.bars + 8 * slot, parity, &state.stop, 6);
         const auto norm = [&](uint32_t at, int c, bool ok, float step, float (&n)[8]) {
             if (PACKED) {
                 uint2 q = *reinterpret_cast<const uint2 *>(stage + at + (ok ? c : 0));
@@ -747,10 +721,7 @@ __global__ void __launch_bounds__(NT, 512 / NT) k_join_backward_ring(const JoinB
         }
         const float m1 = block_sum<NT>(ss, sh[1]) * (inv_h * r1);
         // every thread has read the stage
-        if (threadIdx.x == 0 && t + stages < last) {
-            tc::fence_async();
-            ring.load(t + stages, slot);
-        }
+        if (threadIdx.x == 0 && t + stages < last) ring.refill(&state, t + stages, slot, parity);
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = (i * nt + (int)threadIdx.x) * 8;
@@ -764,6 +735,7 @@ __global__ void __launch_bounds__(NT, 512 / NT) k_join_backward_ring(const JoinB
         px += a.sdx, pd += a.sdf;
         if (++slot == stages) slot = 0, parity ^= 1;
     }
+    if (threadIdx.x == 0) ring.finish(&state);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         const int c = (i * nt + (int)threadIdx.x) * 8;

@@ -59,13 +59,14 @@ __device__ __forceinline__ unsigned long long now_ns() {
 
 // Waits for the phase of `parity`; false once the time limit has passed or
 // another role of the block has given up (*stop).
-__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int *stop, uint32_t role) {
+__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int *stop, uint32_t role,
+                                          unsigned long long limit = kWaitNs) {
     for (int i = 0; i < 64; ++i)
         if (mbar_try(bar, parity)) return true;
     const unsigned long long t0 = now_ns();
     while (!mbar_try(bar, parity)) {
         if (*stop) return false;
-        if (now_ns() - t0 > kWaitNs) {
+        if (now_ns() - t0 > limit) {
             *stop = 1;
             atomicCAS(&g_wait_failure, 0ull, 1ull << 63 | (unsigned long long)role << 32 | blockIdx.x);
             return false;
@@ -82,9 +83,9 @@ __device__ __forceinline__ void let_land() {
 
 // A bounded wait for something of the block's own that is still in flight
 // after it has given up.
-__device__ __forceinline__ void mbar_drain(uint32_t bar, uint32_t parity) {
+__device__ __forceinline__ void mbar_drain(uint32_t bar, uint32_t parity, unsigned long long limit = kWaitNs) {
     const unsigned long long t0 = now_ns();
-    while (!mbar_try(bar, parity) && now_ns() - t0 < kWaitNs) {
+    while (!mbar_try(bar, parity) && now_ns() - t0 < limit) {
     }
 }
 
