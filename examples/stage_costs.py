@@ -124,7 +124,9 @@ def run_1f1b(stage, inputs, targets, stages, device, scale):
             grads[mb] = timed("B", stage.backward, mb, scale)
             timed("W", stage.weights, mb)
         assert len(stage.held) <= int(peak[device])
-    torch.cuda.synchronize()
+    failed = S.wait_failure()  # waits for the device
+    if failed:
+        raise RuntimeError(f"a kernel gave up waiting (record {failed:#x}): the results are wrong")
     return losses, grads, {k: sorted(a.elapsed_time(b) for a, b in v)[len(v) // 2] for k, v in times.items()}
 
 

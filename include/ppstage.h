@@ -146,13 +146,17 @@ int pp_stage_join_backward(const uint16_t *dh, int64_t stride_dh, const uint16_t
                            void *workspace, size_t workspace_bytes, cudaStream_t stream);
 
 /* ---- waits --------------------------------------------------------------
- * The products' blocks wait for their own copies and matrix instructions with
- * a limit of two seconds.  A wait that runs out is recorded, its block gives up
- * (its outputs are then wrong) and the kernel ends.  *first_failure (HOST)
- * receives the first record since the previous call, 0 if there is none, and
- * the records are cleared: bit 63 set, the waiting role in bits 32..39 (1
- * loads, 2 and 3 matrix instructions, 4 results), the block below.
- * Synchronizes the device.  Errors: PP_ERR_ARG, PP_ERR_CUDA. */
+ * The blocks of the products and of the join's rings wait for their own copies
+ * and matrix instructions with a limit of two seconds.  A wait that runs out is
+ * recorded, its block gives up (the call's outputs are then wrong), lets what it
+ * has in flight land, with a limit again, and the kernel ends.  Calls are
+ * asynchronous and return PP_OK all the same: a program asks here once its work
+ * has run, before it relies on the results.  *first_failure (HOST) receives a
+ * record of the current device made since the previous call, 0 if there is none,
+ * and the records are cleared: bit 63 set, the waiting role in bits 32..39 (of a
+ * product: 1 loads, 2 and 3 matrix instructions, 4 results; of a ring: 5 forward,
+ * 6 backward), the block below.  Synchronizes the device.  Errors: PP_ERR_ARG;
+ * PP_ERR_CUDA, also where a record could not be read. */
 int pp_stage_wait_failure(uint64_t *first_failure);
 
 #ifdef __cplusplus

@@ -1,18 +1,15 @@
 // stage_tc.cu -- host side of the tensor-core products: tensor maps, and the
 // record of waits that ran out.
-#include <mutex>
-#include <vector>
-
 #include "stage_kept.cuh"
 #include "stage_product.cuh"
 
 namespace pps {
 namespace {
 
-std::mutex g_wait_mu;
-std::vector<uint64_t (*)()> &wait_readers() {
-    static std::vector<uint64_t (*)()> v;
-    return v;
+// Units register while the library is loaded, before or after this one.
+WaitRecords &wait_records() {
+    static WaitRecords r;
+    return r;
 }
 
 using EncodeTiled = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
@@ -34,9 +31,8 @@ EncodeTiled encoder() {
 
 }  // namespace
 
-int register_wait_reader(uint64_t (*reader)()) {
-    std::lock_guard<std::mutex> lk(g_wait_mu);
-    wait_readers().push_back(reader);
+int register_wait_reader(WaitReader *r) {
+    wait_records().add(r);
     return 0;
 }
 
@@ -147,17 +143,15 @@ int launch_copy_rows(const uint16_t *x, int64_t stride, int64_t T, int64_t H, co
                         stride, T, H, target, V, out, ld, panel);
 }
 
+static int take_waits(uint64_t *record) { return wait_records().take(record); }
+
 }  // namespace pps
 
 extern "C" int pp_stage_wait_failure(uint64_t *first_failure) {
     if (!first_failure) return PP_ERR_ARG;
-    uint64_t first = 0;
-    std::lock_guard<std::mutex> lk(pps::g_wait_mu);
+    *first_failure = 0;
     PPS_CUDA_TRY(cudaDeviceSynchronize());
-    for (uint64_t (*reader)() : pps::wait_readers()) {
-        const uint64_t w = reader();
-        if (!first) first = w;
-    }
-    *first_failure = first;
-    return PP_OK;
+    const int e = pps::take_waits(first_failure);
+    if (e) (void)cudaGetLastError();
+    return e ? PP_ERR_CUDA : PP_OK;
 }

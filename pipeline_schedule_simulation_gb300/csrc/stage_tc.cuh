@@ -7,22 +7,26 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include "stage_waits.h"
+
 namespace pps {
 
 // The first wait of the translation unit that ran out: bit 63 set, the waiting
 // role in bits 32..39, the block below.  Read by pp_stage_wait_failure.
 static __device__ unsigned long long g_wait_failure;
 
-int register_wait_reader(uint64_t (*reader)());
+int register_wait_reader(WaitReader *r);
 
-static uint64_t take_wait_failure() {
+static int take_wait_failure(uint64_t *word) {
     unsigned long long v = 0, zero = 0;
-    if (cudaMemcpyFromSymbol(&v, g_wait_failure, sizeof(v)) != cudaSuccess) return 0;
-    if (v) (void)cudaMemcpyToSymbol(g_wait_failure, &zero, sizeof(zero));
-    return v;
+    cudaError_t e = cudaMemcpyFromSymbol(&v, g_wait_failure, sizeof(v));
+    if (e == cudaSuccess && v) e = cudaMemcpyToSymbol(g_wait_failure, &zero, sizeof(zero));
+    *word = v;
+    return (int)e;
 }
 
-[[maybe_unused]] static const int g_wait_reader = register_wait_reader(take_wait_failure);
+static WaitReader g_wait_reader{take_wait_failure, nullptr};
+[[maybe_unused]] static const int g_wait_registered = register_wait_reader(&g_wait_reader);
 
 namespace tc {
 

@@ -436,7 +436,10 @@ def join_backward(dh, dy, y, f, rstd_post, rstd_pre, w_post, w_pre, gate=None, *
 
 
 def wait_failure():
-    """The first wait inside a product that ran out since the previous call (0: none); synchronizes the device."""
+    """A record of a wait that ran out on the current device since the previous call (0: none); synchronizes the device.
+
+    Calls return before their kernels have run, so they cannot tell: a block whose wait for its own copies or matrix
+    instructions runs out gives up, and the call's outputs are wrong.  Ask after a step, before its results are used."""
     word = ctypes.c_uint64()
     _check(LIB.pp_stage_wait_failure(ctypes.byref(word)), "pp_stage_wait_failure")
     return word.value

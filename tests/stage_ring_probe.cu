@@ -4,7 +4,7 @@
 #include "stage_ring.cuh"
 
 namespace pps {
-int register_wait_reader(decltype(&take_wait_failure)) { return 0; }
+int register_wait_reader(WaitReader *) { return 0; }
 
 constexpr int kThreads = 64, kStages = kMaxStages, kHeader = 128;
 
@@ -65,8 +65,5 @@ extern "C" int ring_probe(const uint32_t *in, int rows, int words, int held, uns
     k_probe<<<1, kThreads, kHeader + kStages * 4 * words>>>(in, rows, words, held, limit, out, issued, landed);
     const cudaError_t e = cudaDeviceSynchronize();
     if (e != cudaSuccess) return (int)e;
-    unsigned long long v = 0, zero = 0;
-    const cudaError_t r = cudaMemcpyFromSymbol(&v, g_wait_failure, sizeof(v));
-    *record = v;
-    return r != cudaSuccess ? (int)r : (int)cudaMemcpyToSymbol(g_wait_failure, &zero, sizeof(zero));
+    return take_wait_failure(record);
 }
