@@ -52,8 +52,8 @@ def build(force: bool = False, verbose: bool = False, extra=(), checked: bool = 
         extra = ["-DPPS_CHECKED", *extra]
     os.makedirs(build_dir, exist_ok=True)
     nvcc = _nvcc()
-    headers = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cuh", ".h"))]
-    headers.append(os.path.join(ROOT, "include", "ppsched.h"))
+    headers = [os.path.join(d, f) for d in (CSRC, os.path.join(ROOT, "include")) for f in os.listdir(d)
+               if f.endswith((".cuh", ".h"))]
     jobs = []
     objs = []
     for src in sources():
