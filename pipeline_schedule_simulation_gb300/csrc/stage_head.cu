@@ -280,8 +280,12 @@ __global__ void __launch_bounds__(32 * kFewWarps, kFewBlocks) k_head_few(const u
 
 bool few_tokens(int64_t T, int64_t H) { return T <= kFewTokens && T * round_up(H, 8) <= kFewFloats; }
 
-// Rows of w to a warp: all blocks are resident.
-int64_t few_rows(int64_t V) { return ceil_div(V, (int64_t)sm_count() * kFewBlocks * kFewWarps); }
+// Rows of w to a warp: all blocks run at once, as many to an SM as its 228 KB of
+// shared memory hold (with the block's own sums and what the SM takes for each).
+int64_t few_rows(int64_t T, int64_t V, int64_t H) {
+    const int64_t each = T * ceil_div(H, 8) * 32 + kFewWarps * kFewTokens * 8 + 1024, fit = 228 * 1024 / each;
+    return ceil_div(V, (int64_t)sm_count() * (fit < kFewBlocks ? fit : kFewBlocks) * kFewWarps);
+}
 
 // 8 tokens a block: 32 lanes along the pieces of each.  First the largest
 // logit, then the sums relative to it.
@@ -386,7 +390,7 @@ ForwardSpace forward_space(void *ws, const uint16_t *x, int64_t sx, const uint16
     ForwardSpace s{};
     s.few = few_tokens(T, H);
     if (s.few) {
-        s.pieces = ceil_div(V, few_rows(V) * kFewWarps);
+        s.pieces = ceil_div(V, few_rows(T, V, H) * kFewWarps);
     } else {
         s.x = aligned(c, x, sx, T, H, ceil_div(V, 256));
         s.w = aligned(c, w, sw, V, H, ceil_div(T, 256));
@@ -459,7 +463,7 @@ extern "C" int pp_stage_head_forward(const uint16_t *x, int64_t stride_x, const 
         rp = allow_smem(kernel, kFewFloats * 4, ready[2 * (T - 1) + vec]);
         if (rp == PP_OK)
             rp = launch_after(kernel, s.pieces, 32 * kFewWarps, (int)(T * ceil_div(H, 8) * 32), stream, 1, x, stride_x, w,
-                              stride_w, target, (int)T, V, (int)H, few_rows(V), s.part, s.picked);
+                              stride_w, target, (int)T, V, (int)H, few_rows(T, V, H), s.part, s.picked);
     } else {
         rp = copy_if(s.x, x, stride_x, T, H, stream);
         if (rp == PP_OK) rp = copy_if(s.w, w, stride_w, V, H, stream);
