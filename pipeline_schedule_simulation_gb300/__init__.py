@@ -6,11 +6,13 @@ order, every op's start/end tick by max-plus longest path, makespan, per-stage
 busy/idle ticks, the exact bubble fraction and the peak count of held
 activations, for thousands to millions of instances per call; plus GPU
 searches over contiguous layer-to-stage partitions (seeded, exhaustive, and
-interleaved layouts).
+interleaved layouts).  And the operators of one pipeline stage, whose time and
+held bytes are the costs: the last stage's loss over a large vocabulary,
+activation checkpoints in 8 bits, the join of a block to the residual stream.
 
 The compute runs in hand-written CUDA kernels behind the C ABI declared in
-``include/ppsched.h`` (``libppsched.so``); ``binding`` marshals arguments only.
-Importing this package does not load the library: ``binding`` does, and fails
-loudly if it has not been built.
+``include/ppsched.h`` and ``include/ppstage.h`` (``libppsched.so``); ``binding``
+and ``stage`` marshal arguments only.  Importing this package does not load the
+library: they do, and fail loudly if it has not been built.
 """
-__all__ = ["binding", "workloads", "sharding", "timeline"]
+__all__ = ["binding", "stage", "workloads", "sharding", "timeline"]

@@ -12,9 +12,12 @@
 // dw_piece = d^T x.  So the step is four products of 2 T V H, a third more
 // than the gradients alone would need with the logits kept (4.3 GB in 32 bits
 // at 8192 x 131072).
-// d is rounded to bf16 before `scale` (and exact near -1 at a target, where the
-// gradient is largest): a tensor-core operand cannot be wider, and an error of
-// 2^-8 of each term at most is no more than the rounding of the results.
+// d is rounded to bf16 before `scale`, by 2^-8 of each term at most: an operand
+// of these products is 16 bits wide, and d in two parts would take both of its
+// products twice.  The results carry that beside their own rounding: dx and dw
+// of weighted tokens are off by 2.4e-3 of their norm, where the rounding of the
+// results alone is 1.65e-3.  Without weights it is 1.7e-3 to 2e-3: the largest
+// term of a token, p - 1 at its target, is then near -1, a bf16 number.
 //
 // The products bound both directions from a few hundred tokens on: 4096 tokens
 // on 131072 x 4096 take 2.52 ms (1750 TFLOP/s; a cuBLAS product alone holds
@@ -336,7 +339,8 @@ __global__ void __launch_bounds__(256) k_head_join(const float2 *part, const flo
 }
 
 // Columns of the vocabulary per piece of the backward pass: d of one piece is
-// at most kPieceBytes.
+// at most kPieceBytes up to 2^20 tokens.  A piece has 256 columns at least, so
+// beyond them d takes 512 bytes a token (8.6 GB at 2^24).
 constexpr int64_t kPieceBytes = 512ll << 20;
 int64_t piece_of(int64_t T, int64_t V) {
     const int64_t cols = kPieceBytes / (2 * (T > 0 ? T : 1)) / 256 * 256;

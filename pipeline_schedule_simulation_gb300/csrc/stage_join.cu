@@ -962,7 +962,8 @@ extern "C" int pp_stage_join_forward(const uint16_t *x, int64_t stride_x, const 
     if (vec && p.threads && H > kNarrow && H % 8 == 0 && T >= 2 * (int64_t)sm_count() * p.blocks) {
         return keep ? forward_ring<true>(a, p, stream) : forward_ring<false>(a, p, stream);
     }
-    const unsigned grid = (unsigned)(T < 152 * 16 ? T : 152 * 16);
+    const int64_t most = (int64_t)sm_count() * 16;
+    const unsigned grid = (unsigned)(T < most ? T : most);
     if (vec) return keep ? forward_by_width<true, true>(a, grid, stream) : forward_by_width<true, false>(a, grid, stream);
     return keep ? forward_by_width<false, true>(a, grid, stream) : forward_by_width<false, false>(a, grid, stream);
 }

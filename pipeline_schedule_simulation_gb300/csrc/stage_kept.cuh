@@ -7,6 +7,9 @@
 // any other tie.  The error is at most half a step, a/128 at most.  A step that is a
 // power of two costs up to one bit against a / 127, and makes q 2^e a bf16
 // number: the backward pass multiplies exactly what was kept.
+// The step is 2^-126 at least, so that it is a normal number: where a < 2^-120
+// the error is still up to 2^-127, and a block whose a is no more than that is
+// held as zeros.
 #pragma once
 
 #include <cstring>

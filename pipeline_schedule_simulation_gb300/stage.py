@@ -13,8 +13,10 @@ any row stride.  Calls are asynchronous on ``stream`` (default: the current
 stream of the tensors' device).  Outputs and scratch memory that are not given
 are allocated for that stream, so nothing else may reuse them before the call
 has run; a caller that passes ``stream`` still orders its inputs before it.
-``workspace`` may be any CUDA uint8 tensor of at least the bytes that the
-matching *_workspace function gives.
+``workspace`` may be any CUDA uint8 tensor that starts on 256 bytes, of at least
+the bytes that the matching *_workspace function gives.  The forward and the
+backward pass are calls of their own: nothing is recorded for autograd, and
+results carry no gradient, whatever the inputs say.
 """
 from __future__ import annotations
 
