@@ -76,8 +76,10 @@ int pp_stage_head_forward(const uint16_t *x, int64_t stride_x, const uint16_t *w
  *   dw [V][H] = scale * d^T x         bf16, or float (dw_float = 1); with
  *               dw_add = 1 (float only) it is added to what dw holds
  * dx or dw may be NULL, not both (B and W as two calls).  d is taken piece by
- * piece of the vocabulary, rounded to bf16 before `scale` is applied.  A row of
- * x that is left out is not read into dw, whatever it holds. */
+ * piece of the vocabulary, rounded to bf16 before `scale` is applied; what the
+ * rounding leaves over at a token's target is added to dx, and to dw where up to
+ * eight tokens share the target, in 32 bits.  A row of x that is left out is not
+ * read into dw, whatever it holds. */
 size_t pp_stage_head_backward_workspace(const uint16_t *x, int64_t stride_x, const uint16_t *w, int64_t stride_w,
                                         int64_t T, int64_t V, int64_t H);
 int pp_stage_head_backward(const uint16_t *x, int64_t stride_x, const uint16_t *w, int64_t stride_w,

@@ -13,11 +13,13 @@
 // than the gradients alone would need with the logits kept (4.3 GB in 32 bits
 // at 8192 x 131072).
 // d is rounded to bf16 before `scale`, by 2^-8 of each term at most: an operand
-// of these products is 16 bits wide, and d in two parts would take both of its
-// products twice.  The results carry that beside their own rounding: dx and dw
-// of weighted tokens are off by 2.4e-3 of their norm, where the rounding of the
-// results alone is 1.65e-3.  Without weights it is 1.7e-3 to 2e-3: the largest
-// term of a token, p - 1 at its target, is then near -1, a bf16 number.
+// of these products is 16 bits wide.  The many small terms' errors average out,
+// but a token's term at its target, c (p - 1), is most of its gradient, and its
+// error alone would put dx and dw of weighted tokens off by 2.4e-3 of their norm
+// where the rounding of the results is 1.65e-3.  So what the rounding of that one
+// term leaves over is kept in 32 bits and added where the products' results are
+// finished: times the target's row of w to dx, times the token's row of x to the
+// target's row of dw.
 //
 // The products bound both directions from a few hundred tokens on: 4096 tokens
 // on 131072 x 4096 take 2.52 ms (1750 TFLOP/s; a cuBLAS product alone holds
@@ -90,6 +92,32 @@ struct StatsEpi {
     }
 };
 
+// What a finished result gains from what the rounding of d left over; a product
+// with an infinity or a NaN adds nothing (the rounded d has brought it already).
+__device__ __forceinline__ float rest_times(float rest, float x) {
+    const float c = rest * x;
+    return fabsf(c) <= 3.402823466e38f ? c : 0.f;
+}
+// The same for 8 columns of a row of bf16, aligned.
+__device__ __forceinline__ void add_rest(float (&b)[8], float rest, const uint16_t *row) {
+    const uint4 q = *reinterpret_cast<const uint4 *>(row);
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) b[2 * k] += rest_times(rest, bf16_lo(w[k])), b[2 * k + 1] += rest_times(rest, bf16_hi(w[k]));
+}
+
+// What the rounding leaves over is taken for nothing up to this share of the
+// term, a sixteenth of the results' own rounding: so it is for every token
+// without a weight whose target is improbable.
+constexpr float kNoRest = 0x1p-12f;
+
+// The other tokens of each target, as lists: head[v] is one, next[t] the one
+// after t, -1 none.  Their order is that in which the blocks of the gradient's
+// product run; what is taken from them does not depend on it.
+struct Lists {
+    int *head, *next;
+};
+
 // d of one piece of the vocabulary: columns v0 .., as bf16.
 struct GradEpi {
     static constexpr bool kStore = false, kWhole = true;
@@ -97,6 +125,8 @@ struct GradEpi {
     const float *lse, *weight;
     int64_t T, V, v0;
     uint16_t *d;  // in panels of T rows
+    float *rest;  // [T]: what the rounding leaves over at the target
+    Lists of;     // of the piece's columns; head null: not asked for
     struct Row {
         float lse, c;
         int64_t at;  // the target's column counted from the piece's first
@@ -110,6 +140,10 @@ struct GradEpi {
         r.at = g - v0;
     }
     __device__ __forceinline__ void take(const Row &r, int64_t t, int n0, int end, int N, int, float (&v)[kRuns][32]) const {
+        // whether the target is in one of these runs (past N it is the next piece's)
+        const int64_t off = r.at - n0;
+        const bool mine = r.in && off >= 0 && r.at < min(end, N) && (off & (kPieces * 32 - 1)) < 32;
+        float left = 0.f;
 #pragma unroll
         for (int i = 0; i < kRuns; ++i) {
             const int n = n0 + i * kPieces * 32;
@@ -117,13 +151,23 @@ struct GradEpi {
             float p[32];
 #pragma unroll
             for (int j = 0; j < 32; ++j) p[j] = exp2_full((v[i][j] - r.lse) * kLog2e);
-            if (r.at >= n && r.at < n + 32) {
+            const bool here = r.at >= n && r.at < n + 32;
+            if (here) {
 #pragma unroll
                 for (int j = 0; j < 32; ++j)
                     if (n + j == r.at) p[j] -= 1.f;
             }
 #pragma unroll
             for (int j = 0; j < 32; ++j) p[j] *= r.c;
+            if (here && mine) {
+                float x = 0.f;
+#pragma unroll
+                for (int j = 0; j < 32; ++j)
+                    if (n + j == r.at) x = p[j];
+                left = x - bf16_to_f32(f32_to_bf16(x));
+                // as good as exact, or an infinity or a NaN
+                if (!(fabsf(left) > kNoRest * fabsf(x) && fabsf(left) <= 1e38f)) left = 0.f;
+            }
             if (!r.in || n + 32 > N) {
 #pragma unroll
                 for (int j = 0; j < 32; ++j)
@@ -131,62 +175,210 @@ struct GradEpi {
             }
             store_bf16(d + (int64_t)(n >> 6) * (T * 64) + t * 64 + (n & 63), p);
         }
+        if (mine) rest[t] = left;
+        if (left != 0.f && of.head) of.next[t] = atomicExch(of.head + r.at, (int)t);
     }
 };
 
-// dx: pieces add up in 32 bits; the last one writes the result.  A row that is
-// left out is 0, whatever w holds.
+// dx: pieces add up in 32 bits; the last one adds what the rounding left over
+// and writes the result.  A row that is left out is 0, whatever w holds.
 struct DxEpi {
     static constexpr bool kStore = true, kWhole = false;
+    static constexpr Side kSide = kEveryRow;
     float *acc;  // [T][ld_acc], ld_acc a multiple of 4
     uint16_t *dx;
     const int64_t *target;
-    int64_t V, ld_acc, ld;
+    const float *rest;
+    const uint16_t *w;  // rows aligned to 16 bytes
+    int64_t V, ld_acc, ld, ld_w;
     float scale;
     bool first, last, vec;
-    __device__ __forceinline__ void finish(int64_t t, int64_t n, float (&v)[32]) const {
-        if (!first) add_f32(v, acc + t * ld_acc + n);
-        if (last) {
-            const bool in = inside(target[t], V);
+    struct Row {
+        int at;      // the target, -1 before the last piece and where the row is left out
+        float rest;  // at the target
+    };
+    __device__ __forceinline__ void begin(Row &r, int64_t t) const {
+        const int64_t g = target[t];
+        r.at = last && inside(g, V) ? (int)g : -1;
+        r.rest = r.at >= 0 ? rest[t] : 0.f;
+    }
+    __device__ __forceinline__ Row of_lane(const Row &r, int lane) const {
+        return {__shfl_sync(~0u, r.at, lane), __shfl_sync(~0u, r.rest, lane)};
+    }
+    __device__ __forceinline__ void finish(const Row &r, int64_t t, int64_t n, float (&v)[32]) const {
+        float b[4][8] = {};
+        if (!first) {
 #pragma unroll
-            for (int j = 0; j < 32; ++j) v[j] = in ? v[j] * scale : 0.f;
+            for (int j = 0; j < 8; ++j) {
+                const float4 q = reinterpret_cast<const float4 *>(acc + t * ld_acc + n)[j];
+                float *o = &b[j >> 1][4 * (j & 1)];
+                o[0] = q.x, o[1] = q.y, o[2] = q.z, o[3] = q.w;
+            }
         }
+        if (r.rest != 0.f) {
+            const uint16_t *row = w + r.at * ld_w + n;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) add_rest(b[j], r.rest, row + 8 * j);
+        }
+        const bool out = last && r.at < 0;
+        const float c = last ? scale : 1.f;
+#pragma unroll
+        for (int j = 0; j < 32; ++j) v[j] = out ? 0.f : (v[j] + b[j >> 3][j & 7]) * c;
     }
     __device__ __forceinline__ bool narrow() const { return last; }
-    __device__ __forceinline__ void row(int64_t t, int64_t n, const float (&v)[32]) const { store_bf16(dx + t * ld + n, v); }
+    __device__ __forceinline__ void row(const Row &, int64_t t, int64_t n, const float (&v)[32]) const {
+        store_bf16(dx + t * ld + n, v);
+    }
     __device__ __forceinline__ void put(int64_t t, int64_t n, const float4 &v, int) const {
         store_quad(acc + t * ld_acc + n, v);
     }
-    __device__ __forceinline__ float with(int64_t t, int64_t n) const { return first ? 0.f : acc[t * ld_acc + n]; }
-    __device__ __forceinline__ void one(int64_t t, int64_t n, float v, float b, int) const {
+    __device__ __forceinline__ float with(const Row &r, int64_t t, int64_t n) const {
+        const float x = r.rest != 0.f ? bf16_to_f32(w[r.at * ld_w + n]) : 0.f;
+        return (first ? 0.f : acc[t * ld_acc + n]) + rest_times(r.rest, x);
+    }
+    __device__ __forceinline__ void one(const Row &r, int64_t t, int64_t n, float v, float b, int) const {
         const float s = v + b;
-        if (last) dx[t * ld + n] = inside(target[t], V) ? f32_to_bf16(s * scale) : 0;
+        if (last) dx[t * ld + n] = r.at >= 0 ? f32_to_bf16(s * scale) : 0;
         else acc[t * ld_acc + n] = s;
     }
 };
 
+// dw.  A row with a list of tokens waits for what the rounding left over: as bf16
+// it is put aside in 32 bits and written by k_target_rows; in 32 bits it is added
+// to there.  (The walk along the list here would hold up a warp's other 31 rows:
+// 777 weighted tokens on 50257 x 1000 took 314 us that way, 264 us this way, and
+// 244 us without what is left over.)
 struct DwEpi {
     static constexpr bool kStore = true, kWhole = false;
+    static constexpr Side kSide = kSomeRows;
     uint16_t *dw16;  // one of the two
-    float *dw32;
-    int64_t ld;
+    float *dw32, *aside;
+    const int *head;  // of the piece's rows
+    int64_t ld, ld_aside;
     float scale;
-    bool add, vec;
-    __device__ __forceinline__ void finish(int64_t m, int64_t n, float (&v)[32]) const {
+    bool by_token, add, vec;
+    struct Row {
+        int aside;  // the row among those put aside, or -1
+    };
+    __device__ __forceinline__ void begin(Row &r, int64_t m) const {
+        const int t = dw16 ? head[m] : -1;
+        r.aside = t < 0 || by_token ? t : (int)m;
+    }
+    __device__ __forceinline__ bool apart(const Row &r) const { return r.aside >= 0; }
+    __device__ __forceinline__ Row of_lane(const Row &r, int lane) const { return {__shfl_sync(~0u, r.aside, lane)}; }
+    __device__ __forceinline__ void finish(const Row &r, int64_t m, int64_t n, float (&v)[32]) const {
+        const float c = r.aside < 0 ? scale : 1.f;
 #pragma unroll
-        for (int j = 0; j < 32; ++j) v[j] *= scale;
+        for (int j = 0; j < 32; ++j) v[j] *= c;
         if (add) add_f32(v, dw32 + m * ld + n);
     }
     __device__ __forceinline__ bool narrow() const { return dw16 != nullptr; }
-    __device__ __forceinline__ void row(int64_t m, int64_t n, const float (&v)[32]) const { store_bf16(dw16 + m * ld + n, v); }
+    __device__ __forceinline__ void row(const Row &r, int64_t m, int64_t n, const float (&v)[32]) const {
+        if (r.aside < 0) {
+            store_bf16(dw16 + m * ld + n, v);
+            return;
+        }
+        float *p = aside + r.aside * ld_aside + n;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) store_quad(p + 4 * j, make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]));
+    }
     __device__ __forceinline__ void put(int64_t m, int64_t n, const float4 &v, int) const { store_quad(dw32 + m * ld + n, v); }
-    __device__ __forceinline__ float with(int64_t m, int64_t n) const { return add ? dw32[m * ld + n] : 0.f; }
-    __device__ __forceinline__ void one(int64_t m, int64_t n, float v, float b, int) const {
-        const float s = v * scale + b;
-        if (dw16) dw16[m * ld + n] = f32_to_bf16(s);
-        else dw32[m * ld + n] = s;
+    __device__ __forceinline__ float with(const Row &, int64_t m, int64_t n) const { return add ? dw32[m * ld + n] : 0.f; }
+    __device__ __forceinline__ void one_apart(const Row &r, int64_t n, float v) const { aside[r.aside * ld_aside + n] = v; }
+    __device__ __forceinline__ void one(const Row &, int64_t m, int64_t n, float v, float b, int) const {
+        if (dw16) dw16[m * ld + n] = f32_to_bf16(v * scale);
+        else dw32[m * ld + n] = v * scale + b;
     }
 };
+
+// A block finishes 2048 columns of a row of dw that has a list: its tokens' rows
+// of x times what the rounding of d left over, added in the order of the tokens.
+// With more than kListed tokens nothing is added: so many errors average out, to
+// a third of one token's and less, and the walk stays short.  The kernel is a
+// chain of loads, so all that may be needed for a list of one token, as most are,
+// is on its way at once: 777 rows of 1000 take 4.7 us, 2048 of 2048 8 us.
+constexpr int kListed = 8, kTargetThreads = 256;
+struct TargetRows {
+    const int64_t *target;
+    const float *rest, *aside;
+    const uint16_t *x;  // in panels of T rows
+    Lists of;           // of the piece's rows
+    int64_t T, v0, n, H, ld, ld_aside;
+    uint16_t *dw16;
+    float *dw32, scale;
+    bool by_token, vec;
+};
+__global__ void __launch_bounds__(kTargetThreads) k_target_rows(const TargetRows a) {
+    let_next_start();
+    after_previous();
+    const int64_t row = blockIdx.x, c = ((int64_t)blockIdx.y * kTargetThreads + threadIdx.x) * 8;
+    if (c >= a.H) return;
+    // by token: one of a list's tokens is its head; else every row is looked at
+    const int first = a.by_token ? (int)row : a.of.head[row];
+    if (first < 0) return;
+    const int64_t v = a.by_token ? a.target[row] - a.v0 : row;
+    const uint16_t *x = a.x + (c >> 6) * (a.T * 64) + (c & 63);
+    const auto add = [&](float (&s)[8], float r, const uint4 &q) {
+        const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) s[2 * k] += rest_times(r, bf16_lo(w[k])), s[2 * k + 1] += rest_times(r, bf16_hi(w[k]));
+    };
+    const uint4 q = *reinterpret_cast<const uint4 *>(x + (int64_t)first * 64);
+    const float r = a.rest[first];
+    int u = a.of.next[first];
+    // rows put aside are whole quads: of 8 columns the second 4 may not be there
+    float4 p[2] = {};
+    if (a.dw16) {
+        const float *from = a.aside + row * a.ld_aside + c;
+        p[0] = *reinterpret_cast<const float4 *>(from);
+        if (c + 4 < a.H) p[1] = *reinterpret_cast<const float4 *>(from + 4);
+    }
+    if (a.by_token && (v < 0 || v >= a.n || a.of.head[v] != first)) return;
+    float s[8] = {};
+    if (u < 0) {
+        add(s, r, q);
+    } else {
+        int t[kListed] = {first};
+#pragma unroll
+        for (int i = 1; i < kListed; ++i) {
+            t[i] = 0x7FFFFFFF;
+            if (u >= 0) t[i] = u, u = a.of.next[u];
+        }
+        const bool more = u >= 0;
+#pragma unroll
+        for (int i = 1; i < kListed; ++i)
+#pragma unroll
+            for (int j = i; j > 0; --j) {
+                const int lo = min(t[j - 1], t[j]), hi = max(t[j - 1], t[j]);
+                t[j - 1] = lo, t[j] = hi;
+            }
+#pragma unroll
+        for (int i = 0; i < kListed; ++i)
+            if (!more && t[i] != 0x7FFFFFFF) add(s, a.rest[t[i]], *reinterpret_cast<const uint4 *>(x + (int64_t)t[i] * 64));
+    }
+    if (a.dw16) {
+        const float y[8] = {(p[0].x + s[0]) * a.scale, (p[0].y + s[1]) * a.scale, (p[0].z + s[2]) * a.scale,
+                            (p[0].w + s[3]) * a.scale, (p[1].x + s[4]) * a.scale, (p[1].y + s[5]) * a.scale,
+                            (p[1].z + s[6]) * a.scale, (p[1].w + s[7]) * a.scale};
+        if (a.vec) store8_bf16<true>(a.dw16 + v * a.ld + c, a.H - c, y);
+        else store8_bf16<false>(a.dw16 + v * a.ld + c, a.H - c, y);
+    } else {
+        float *o = a.dw32 + v * a.ld + c;
+        if (a.vec && c + 8 <= a.H) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                float4 &p = reinterpret_cast<float4 *>(o)[j];
+                const float4 w = p;
+                p = make_float4(fmaf(s[4 * j], a.scale, w.x), fmaf(s[4 * j + 1], a.scale, w.y),
+                                fmaf(s[4 * j + 2], a.scale, w.z), fmaf(s[4 * j + 3], a.scale, w.w));
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (c + j < a.H) o[j] = fmaf(s[j], a.scale, o[j]);
+        }
+    }
+}
 
 // ---- few tokens: w is read once, by the row
 
@@ -410,8 +602,9 @@ ForwardSpace forward_space(void *ws, const uint16_t *x, int64_t sx, const uint16
 struct BackwardSpace {
     Aligned w;
     uint16_t *x, *d;  // in panels: x with the rows that are left out at 0, d of one piece
-    float *acc, *parts;
-    int64_t piece, ld_acc;
+    float *acc, *parts, *rest, *aside;
+    Lists of;
+    int64_t piece, ld_acc;  // ld_acc: of the rows put aside too
     size_t bytes;
 };
 BackwardSpace backward_space(void *ws, const uint16_t *x, int64_t sx, const uint16_t *w, int64_t sw, int64_t T,
@@ -423,6 +616,9 @@ BackwardSpace backward_space(void *ws, const uint16_t *x, int64_t sx, const uint
     s.w = aligned(c, w, sw, V, H, ceil_div(T, 256));
     s.x = c.take<uint16_t>(T * round_up(H, 64));
     s.d = c.take<uint16_t>(T * s.piece);
+    s.rest = c.take<float>(T);
+    s.of = {c.take<int>(V), c.take<int>(T)};
+    s.aside = c.take<float>((s.piece < V ? std::min(T, s.piece) : std::min(T, V)) * s.ld_acc);
     s.acc = c.take<float>(s.piece < V ? T * s.ld_acc : 0);
     int64_t parts = 0;  // the last piece may be shorter than the others
     for (const int64_t n : {s.piece < V ? s.piece : V, V - (V - 1) / s.piece * s.piece}) {
@@ -435,7 +631,7 @@ BackwardSpace backward_space(void *ws, const uint16_t *x, int64_t sx, const uint
 }
 
 int copy_if(const Aligned &a, const uint16_t *p, int64_t stride, int64_t rows, int64_t H, cudaStream_t stream) {
-    return a.copy ? launch_copy_rows(p, stride, rows, H, nullptr, 0, a.copy, a.at.ld, 64, stream) : PP_OK;
+    return a.copy ? launch_copy_rows(p, stride, rows, H, nullptr, 0, nullptr, a.copy, a.at.ld, 64, stream) : PP_OK;
 }
 
 }  // namespace
@@ -505,27 +701,36 @@ extern "C" int pp_stage_head_backward(const uint16_t *x, int64_t stride_x, const
     }
     const BackwardSpace s = backward_space(workspace, x, stride_x, w, stride_w, T, V, H);
     if (!workspace || ((uintptr_t)workspace & (kStageAlign - 1)) || workspace_bytes < s.bytes) return PP_ERR_ARG;
-    int rp = launch_copy_rows(x, stride_x, T, H, target, V, s.x, 64, T * 64, stream);
+    // with dw every list is emptied
+    int rp = launch_copy_rows(x, stride_x, T, H, target, V, dw ? s.of.head : nullptr, s.x, 64, T * 64, stream);
     if (rp == PP_OK) rp = copy_if(s.w, w, stride_w, V, H, stream);
     const bool vec_dx = dx && rows_aligned(dx, stride_dx, T, 2), vec_dw = dw && rows_aligned(dw, stride_dw, V, dw_float ? 4 : 2);
     const Matrix xm = in_panels(s.x, T), d = in_panels(s.d, T);
     for (int64_t v0 = 0; v0 < V && rp == PP_OK; v0 += s.piece) {
         const int64_t n = V - v0 < s.piece ? V - v0 : s.piece;
         const Matrix wp = in_rows(s.w.at.p + v0 * s.w.at.ld, s.w.at.ld);
-        rp = whole_product<kPanelsK, kRowsK>(xm, wp, T, n, H, GradEpi{target, lse, weight, T, V, v0, s.d}, stream);
+        const Lists of{dw ? s.of.head + v0 : nullptr, s.of.next};
+        rp = whole_product<kPanelsK, kRowsK>(xm, wp, T, n, H, GradEpi{target, lse, weight, T, V, v0, s.d, s.rest, of}, stream);
         if (rp == PP_OK && dx) {
-            const DxEpi epi{s.acc, dx, target, V, s.ld_acc, stride_dx, scale, v0 == 0, v0 + n == V, vec_dx};
+            const DxEpi epi{s.acc, dx, target, s.rest, s.w.at.p, V, s.ld_acc, stride_dx, s.w.at.ld, scale, v0 == 0,
+                            v0 + n == V, vec_dx};
             // the copy's rows are whole panels; so are w's own if H is
             rp = s.w.copy || H % 64 == 0
                      ? product_in_parts<kPanelsK, kPanelsMN>(d, wp, T, H, n, epi, s.parts, stream)
                      : product_in_parts<kPanelsK, kRowsMN>(d, wp, T, H, n, epi, s.parts, stream);
         }
-        if (rp == PP_OK && dw)
-            rp = product_in_parts<kPanelsMN, kPanelsMN>(
-                d, xm, n, H, T,
-                DwEpi{dw_float ? nullptr : (uint16_t *)dw + v0 * stride_dw,
-                      dw_float ? (float *)dw + v0 * stride_dw : nullptr, stride_dw, scale, dw_add != 0, vec_dw},
-                s.parts, stream);
+        if (rp == PP_OK && dw) {
+            uint16_t *dw16 = dw_float ? nullptr : (uint16_t *)dw + v0 * stride_dw;
+            float *dw32 = dw_float ? (float *)dw + v0 * stride_dw : nullptr;
+            const bool by_token = T <= n;  // rows put aside: by their list's head, or all that the piece has
+            const DwEpi epi{dw16, dw32, s.aside, of.head, stride_dw, s.ld_acc, scale, by_token, dw_add != 0, vec_dw};
+            rp = product_in_parts<kPanelsMN, kPanelsMN>(d, xm, n, H, T, epi, s.parts, stream);
+            if (rp == PP_OK)
+                rp = launch_after(k_target_rows, dim3((unsigned)(by_token ? T : n), (unsigned)ceil_div(H, 8 * kTargetThreads)),
+                                  kTargetThreads, 0, stream, 1,
+                                  TargetRows{target, s.rest, s.aside, s.x, of, T, v0, n, H, stride_dw, s.ld_acc, dw16, dw32,
+                                             scale, by_token, vec_dw});
+        }
     }
     return rp;
 }

@@ -80,20 +80,20 @@ __global__ void __launch_bounds__(kThreads) k_unpack(const int8_t *q, int64_t st
         }
 }
 
-struct WgradEpi {
+struct WgradEpi : NoRow {
     static constexpr bool kStore = true, kWhole = false;
     const float *add;
     float *dw;
     int64_t ld_add, ld;
     bool vec;
-    __device__ __forceinline__ void finish(int64_t m, int64_t n, float (&v)[32]) const {
+    __device__ __forceinline__ void finish(const Row &, int64_t m, int64_t n, float (&v)[32]) const {
         if (add) add_f32(v, add + m * ld_add + n);
     }
     __device__ __forceinline__ bool narrow() const { return false; }
-    __device__ __forceinline__ void row(int64_t, int64_t, const float (&)[32]) const {}
+    __device__ __forceinline__ void row(const Row &, int64_t, int64_t, const float (&)[32]) const {}
     __device__ __forceinline__ void put(int64_t m, int64_t n, const float4 &v, int) const { store_quad(dw + m * ld + n, v); }
-    __device__ __forceinline__ float with(int64_t m, int64_t n) const { return add ? add[m * ld_add + n] : 0.f; }
-    __device__ __forceinline__ void one(int64_t m, int64_t n, float v, float b, int) const { dw[m * ld + n] = b + v; }
+    __device__ __forceinline__ float with(const Row &, int64_t m, int64_t n) const { return add ? add[m * ld_add + n] : 0.f; }
+    __device__ __forceinline__ void one(const Row &, int64_t m, int64_t n, float v, float b, int) const { dw[m * ld + n] = b + v; }
 };
 
 bool bad_kept(const int8_t *q, int64_t sq, const int8_t *e, int64_t se, int64_t H) {
@@ -187,10 +187,10 @@ extern "C" int pp_stage_weight_grad(const uint16_t *dy, int64_t stride_dy, const
     if (!workspace || ((uintptr_t)workspace & (kStageAlign - 1)) || workspace_bytes < s.bytes) return PP_ERR_ARG;
     const bool copy = !rows_aligned(dy, stride_dy, T, 2);
     int rp = launch_unpack(q, stride_q, e, stride_e, T, H, s.v, kBlock, T * kBlock, stream);
-    if (rp == PP_OK && copy) rp = launch_copy_rows(dy, stride_dy, T, N, nullptr, 0, s.dy, kBlock, T * kBlock, stream);
+    if (rp == PP_OK && copy) rp = launch_copy_rows(dy, stride_dy, T, N, nullptr, 0, nullptr, s.dy, kBlock, T * kBlock, stream);
     if (rp != PP_OK) return rp;
     const bool vec = rows_aligned(dw, stride_dw, N, 4) && (!add || rows_aligned(add, stride_add, N, 4));
-    const WgradEpi epi{add, dw, stride_add, stride_dw, vec};
+    const WgradEpi epi{{}, add, dw, stride_add, stride_dw, vec};
     const Matrix v = in_panels(s.v, T);
     if (copy) return product_in_parts<kPanelsMN, kPanelsMN>(in_panels(s.dy, T), v, N, H, T, epi, s.parts, stream);
     if (N % 64 == 0)

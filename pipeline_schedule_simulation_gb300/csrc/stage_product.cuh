@@ -5,16 +5,22 @@
 // and handed to an epilogue instead of being stored.  Epilogues that store C
 // (kStore), with columns in quads where `vec` says that rows are aligned and one
 // by one otherwise (part: which part of K):
-//   finish(m, n, v)        columns n .. n+31 of row m: scaled, added, in place
+//   finish(row, m, n, v)   columns n .. n+31 of row m: scaled, added, in place
 //   narrow()               whether rows are stored as bf16:
-//   row(m, n, v)           then 32 finished columns at once,
+//   row(row, m, n, v)      then 32 finished columns at once,
 //   put(m, n, v, part)     else four
-//   with(m, n)             what one column is added to
-//   one(m, n, v, b, part)  one column, from the sum and that to memory
+//   with(row, m, n)        what one column is added to
+//   one(row, m, n, v, b, part)  one column, from the sum and that to memory
 // The others get a row as a thread has it.  A row's part of a column tile is two
-// pieces, the even and the odd runs of 32 columns:
+// pieces, the even and the odd runs of 32 columns.  All of them:
 //   typename Epi::Row  what a row needs beside its sums
 //   begin(row, m)      loads that
+// and those that store C:
+//   kSide              which rows use that: kNoRow, kSomeRows, kEveryRow
+//   of_lane(row, lane) another lane's
+//   apart(row), one_apart(row, n, v)  (kSomeRows) those rows, and one column of
+//                      such a row in place of one()
+// and those that do not:
 //   take(row, m, n0, end, N, piece, v)  one piece: run i is the columns from
 //                      n0 + 64 i on, below `end` and (what exists) N
 //   kWhole             runs go on to the next multiple of 64 past N, and none is
@@ -136,6 +142,14 @@ __device__ __forceinline__ void add_f32(float (&v)[32], const float *to) {
     for (int j = 0; j < 8; ++j) v[4 * j] += b[j].x, v[4 * j + 1] += b[j].y, v[4 * j + 2] += b[j].z, v[4 * j + 3] += b[j].w;
 }
 
+// For epilogues that need nothing beside a row's sums.
+enum Side { kNoRow, kSomeRows, kEveryRow };
+struct NoRow {
+    static constexpr Side kSide = kNoRow;
+    struct Row {};
+    __device__ __forceinline__ void begin(Row &, int64_t) const {}
+};
+
 // 32 rows x 32 columns, a row to a lane.  Each lane finishes its row's values
 // (what they are added to comes in whole lines that way); then they are turned
 // through the warp's shared memory and stored along the rows, 4 rows at once,
@@ -145,13 +159,13 @@ __device__ __forceinline__ void add_f32(float (&v)[32], const float *to) {
 // are 16 bytes a store, turned 8: those stay with the lanes.)  Unaligned rows
 // are turned too, a column to a lane, 8 rows on their way at once.
 template <class Epi>
-__device__ __forceinline__ void store_run(const Epi &epi, float4 *turn, int lane, int64_t m0, int64_t M, int n, int end,
-                                          int part, float (&v)[32]) {
+__device__ __forceinline__ void store_run(const Epi &epi, const typename Epi::Row &side, float4 *turn, int lane, int64_t m0,
+                                          int64_t M, int n, int end, int part, float (&v)[32]) {
     if (m0 >= M) return;
     const bool whole = epi.vec && end - n >= 32;
-    if (whole && m0 + lane < M) epi.finish(m0 + lane, n, v);
+    if (whole && m0 + lane < M) epi.finish(side, m0 + lane, n, v);
     if (whole && epi.narrow()) {
-        if (m0 + lane < M) epi.row(m0 + lane, n, v);
+        if (m0 + lane < M) epi.row(side, m0 + lane, n, v);
         return;
     }
 #pragma unroll
@@ -169,31 +183,32 @@ __device__ __forceinline__ void store_run(const Epi &epi, float4 *turn, int lane
     } else {
         const float *one = reinterpret_cast<const float *>(turn);
         const int rows = n + lane < end ? (M - m0 < 32 ? (int)(M - m0) : 32) : 0;
-        for (int r0 = 0; r0 < rows; r0 += 8) {
+        const auto sum_of = [&](int r) { return one[r * 32 + ((lane >> 2) ^ (r & 7)) * 4 + (lane & 3)]; };
+        [[maybe_unused]] uint32_t apart = 0;
+        if constexpr (Epi::kSide == kSomeRows) apart = __ballot_sync(~0u, m0 + lane < M && epi.apart(side));
+        for (int r0 = 0; r0 < (Epi::kSide == kEveryRow ? 32 : rows); r0 += 8) {
+            [[maybe_unused]] typename Epi::Row of[8];
             float b[8];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) b[k] = r0 + k < rows ? epi.with(m0 + r0 + k, n + lane) : 0.f;
+            for (int k = 0; k < 8; ++k) {
+                if constexpr (Epi::kSide == kEveryRow) of[k] = epi.of_lane(side, r0 + k);
+                b[k] = r0 + k < rows ? epi.with(of[k], m0 + r0 + k, n + lane) : 0.f;
+            }
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
                 const int r = r0 + k;
-                const float x = one[r * 32 + ((lane >> 2) ^ (r & 7)) * 4 + (lane & 3)];
-                if (r < rows) epi.one(m0 + r, n + lane, x, b[k], part);
+                if (r < rows && !(apart >> r & 1)) epi.one(of[k], m0 + r, n + lane, sum_of(r), b[k], part);
             }
         }
+        if constexpr (Epi::kSide == kSomeRows)
+            for (; apart; apart &= apart - 1) {
+                const int r = __ffs(apart) - 1;
+                const typename Epi::Row its = epi.of_lane(side, r);
+                if (r < rows) epi.one_apart(its, n + lane, sum_of(r));
+            }
     }
     __syncwarp();
 }
-
-template <class Epi, bool STORE = Epi::kStore>
-struct RowType {
-    using type = int;
-};
-template <class Epi>
-struct RowType<Epi, false> {
-    using type = typename Epi::Row;
-};
-template <class Epi>
-using RowOf = typename RowType<Epi>::type;
 
 // A place in a ring of N: the slot, and the parity of its current round.
 template <int N>
@@ -337,27 +352,23 @@ __global__ void __launch_bounds__(kProductThreads, 1)
         const int wide = Epi::kWhole ? (s.N + 63) & ~63 : s.N;
         Place<2> run;
         bool ok = true;
-        // what a row needs beside its sums is loaded a tile ahead
-        [[maybe_unused]] RowOf<Epi> next{};
+        // a tile's place, and what a row needs beside its sums, are taken a tile ahead
+        typename Epi::Row next{};
+        int next_m = 0, next_n = 0;
         const auto begin_next = [&](uint32_t t) {
-            if constexpr (!Epi::kStore) {
-                if (t >= tiles) return;
-                int mt, nt;
-                tile_at(s, t / s.splits, mt, nt);
-                const int64_t m = (int64_t)(mt * CG + (int)rank) * kHalf + quarter * 32 + lane;
-                if (m < s.M) epi.begin(next, m);
-            }
+            if (t >= tiles) return;
+            tile_at(s, t / s.splits, next_m, next_n);
+            const int64_t m = (int64_t)(next_m * CG + (int)rank) * kHalf + quarter * 32 + lane;
+            if (m < s.M) epi.begin(next, m);
         };
         begin_next(first);
         for (uint32_t t = first; t < tiles && ok; t += step) {
-            const int part = (int)(t % s.splits);
-            int mt, nt;
-            tile_at(s, t / s.splits, mt, nt);
+            const int part = (int)(t % s.splits), mt = next_m, nt = next_n;
             const int64_t m = (int64_t)(mt * CG + (int)rank) * kHalf + quarter * 32 + lane;
             const int first_n = nt * s.tile_n, n0 = first_n + half * 32, n1 = min(first_n + s.tile_n, wide);
             const int k0 = part * s.k_blocks, k1 = min(k0 + s.k_blocks, all_blocks);
             const bool live = m < s.M;
-            [[maybe_unused]] RowOf<Epi> row = next;
+            const typename Epi::Row row = next;
             uint32_t sum[kRuns][32];  // floats, as the loads give them
             for (int r0 = k0; r0 < k1; r0 += kRun, run.next()) {
                 const int buf = run.slot;
@@ -399,6 +410,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
             for (int i = 0; i < kRuns; ++i)
 #pragma unroll
                 for (int c = 0; c < 32; ++c) v[i][c] = __uint_as_float(sum[i][c]);
+            begin_next(t + step);
             if constexpr (Epi::kStore) {
                 if (ok) {
                     float4 *turn = reinterpret_cast<float4 *>(raw + (ring - tc::smem_u32(raw)) + kRingBytes +
@@ -408,11 +420,10 @@ __global__ void __launch_bounds__(kProductThreads, 1)
 #pragma unroll
                     for (int i = 0; i < kRuns; ++i) {
                         const int n = n0 + i * kPieces * 32;
-                        if (n < n1) store_run(epi, turn, lane, m_first, s.M, n, end, part, v[i]);
+                        if (n < n1) store_run(epi, row, turn, lane, m_first, s.M, n, end, part, v[i]);
                     }
                 }
             } else {
-                begin_next(t + step);
                 if (ok && live) epi.take(row, m, n0, n1, s.N, kPieces * nt + half, v);
                 __syncwarp();
             }
@@ -496,19 +507,19 @@ int whole_product(const Matrix &A, const Matrix &B, int64_t M, int64_t N, int64_
 // their translation unit, and so are the kernels and attribute flags made from
 // them.
 namespace {
-struct PartEpi {
+struct PartEpi : NoRow {
     static constexpr bool kStore = true, kWhole = false;
     static constexpr bool vec = true;
     float *parts;
     int64_t M, ld;  // ld is a multiple of 4
     __device__ __forceinline__ bool narrow() const { return false; }
-    __device__ __forceinline__ void finish(int64_t, int64_t, float (&)[32]) const {}
-    __device__ __forceinline__ void row(int64_t, int64_t, const float (&)[32]) const {}
+    __device__ __forceinline__ void finish(const Row &, int64_t, int64_t, float (&)[32]) const {}
+    __device__ __forceinline__ void row(const Row &, int64_t, int64_t, const float (&)[32]) const {}
     __device__ __forceinline__ void put(int64_t m, int64_t n, const float4 &v, int part) const {
         *reinterpret_cast<float4 *>(parts + (part * M + m) * ld + n) = v;
     }
-    __device__ __forceinline__ float with(int64_t, int64_t) const { return 0.f; }
-    __device__ __forceinline__ void one(int64_t m, int64_t n, float v, float, int part) const {
+    __device__ __forceinline__ float with(const Row &, int64_t, int64_t) const { return 0.f; }
+    __device__ __forceinline__ void one(const Row &, int64_t m, int64_t n, float v, float, int part) const {
         parts[(part * M + m) * ld + n] = v;
     }
 };
@@ -527,6 +538,15 @@ __global__ void __launch_bounds__(256) k_join_parts(const float *parts, int spli
     const int64_t m = i / per, n = (i - m * per) * 4;
     const bool in = m < M && n < N;
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    // what the sums are added to is on its way beside the parts
+    typename Epi::Row row{};
+    float b[4] = {};
+    if (!run && in) {
+        epi.begin(row, m);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (n + j < N) b[j] = epi.with(row, m, n + j);
+    }
     if (in) {
         const float4 *p = reinterpret_cast<const float4 *>(parts + m * ld + n);
 #pragma unroll 4
@@ -546,7 +566,15 @@ __global__ void __launch_bounds__(256) k_join_parts(const float *parts, int spli
     const float x[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
     for (int j = 0; j < 4; ++j)
-        if (n + j < N) epi.one(m, n + j, x[j], epi.with(m, n + j), 0);
+        if (n + j < N) {
+            if constexpr (Epi::kSide == kSomeRows) {
+                if (epi.apart(row)) {
+                    epi.one_apart(row, n + j, x[j]);
+                    continue;
+                }
+            }
+            epi.one(row, m, n + j, x[j], b[j], 0);
+        }
 }
 
 // Floats of scratch memory that product_in_parts needs (B is MN-major there).
@@ -563,7 +591,7 @@ int product_in_parts(const Matrix &A, const Matrix &B, int64_t M, int64_t N, int
     const ProductPlan p = plan_product(M, N, K, true, true);
     if (p.splits == 1) return launch_product<FA, FB>(A, B, M, N, K, epi, p, stream);
     const int64_t ld = round_up(N, 4);
-    const int rc = launch_product<FA, FB>(A, B, M, N, K, PartEpi{parts, M, ld}, p, stream);
+    const int rc = launch_product<FA, FB>(A, B, M, N, K, PartEpi{{}, parts, M, ld}, p, stream);
     if (rc != PP_OK) return rc;
     return launch_after(k_join_parts<Epi>, ceil_div(M * (ld / 4), 64), 256, 0, stream, 1, (const float *)parts, p.splits, M,
                         N, ld, epi);
@@ -571,8 +599,8 @@ int product_in_parts(const Matrix &A, const Matrix &B, int64_t M, int64_t N, int
 
 // A copy of rows at any stride and alignment as panels (or aligned rows), the
 // last panel's columns past H as zeros; with `target`, a row whose target is
-// outside 0..V-1 becomes 0.
+// outside 0..V-1 becomes 0, and the V words from `clear` (null: none) become -1.
 int launch_copy_rows(const uint16_t *x, int64_t stride, int64_t T, int64_t H, const int64_t *target, int64_t V,
-                     uint16_t *out, int64_t ld, int64_t panel, cudaStream_t stream);
+                     int *clear, uint16_t *out, int64_t ld, int64_t panel, cudaStream_t stream);
 
 }  // namespace pps

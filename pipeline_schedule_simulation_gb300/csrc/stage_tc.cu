@@ -112,11 +112,13 @@ namespace {
 constexpr int kCopyRows = 4;
 template <bool VEC>
 __global__ void __launch_bounds__(256) k_copy_rows(const uint16_t *x, int64_t stride, int64_t T, int64_t H,
-                                                   const int64_t *target, int64_t V, uint16_t *out, int64_t ld,
-                                                   int64_t panel) {
+                                                   const int64_t *target, int64_t V, int *clear, uint16_t *out,
+                                                   int64_t ld, int64_t panel) {
     let_next_start();
     after_previous();
     const int64_t per = (H + 63) / 64 * 8, u = (int64_t)blockIdx.x * blockDim.x + threadIdx.x, g = u / per;
+    if (clear)
+        for (int64_t i = u; i < V; i += (int64_t)gridDim.x * blockDim.x) clear[i] = -1;
     const int64_t t = g * kCopyRows, c = (u - g * per) * 8, left = H - c;
     Raw8 r[kCopyRows];
 #pragma unroll
@@ -137,10 +139,10 @@ __global__ void __launch_bounds__(256) k_copy_rows(const uint16_t *x, int64_t st
 }  // namespace
 
 int launch_copy_rows(const uint16_t *x, int64_t stride, int64_t T, int64_t H, const int64_t *target, int64_t V,
-                     uint16_t *out, int64_t ld, int64_t panel, cudaStream_t stream) {
+                     int *clear, uint16_t *out, int64_t ld, int64_t panel, cudaStream_t stream) {
     const int64_t grid = ceil_div(ceil_div(T, kCopyRows) * ceil_div(H, 64) * 8, 256);
     return launch_after(rows_aligned(x, stride, T, 2) ? k_copy_rows<true> : k_copy_rows<false>, grid, 256, 0, stream, 1, x,
-                        stride, T, H, target, V, out, ld, panel);
+                        stride, T, H, target, V, clear, out, ld, panel);
 }
 
 static int take_waits(uint64_t *record) { return wait_records().take(record); }
