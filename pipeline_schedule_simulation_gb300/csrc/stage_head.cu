@@ -24,8 +24,8 @@
 // The products bound both directions from a few hundred tokens on: 4096 tokens
 // on 131072 x 4096 take 2.52 ms (1750 TFLOP/s; a cuBLAS product alone holds
 // 1703 in a long loop on the same GPU, 1945 in a burst), the step of 8192 tokens
-// 20.8 ms (1690 TFLOP/s over its four products).  For a few tokens reading w
-// does: one token on 32000 x 2048 takes 29 us, its 131 MB alone 19 us.
+// 21.0 ms (1680 TFLOP/s over its four products).  For a few tokens reading w
+// does: one token on 32000 x 2048 takes 28 us, its 131 MB alone 19 us.
 #include <algorithm>
 
 #include "stage_kept.cuh"
@@ -226,9 +226,7 @@ struct DxEpi {
         for (int j = 0; j < 32; ++j) v[j] = out ? 0.f : (v[j] + b[j >> 3][j & 7]) * c;
     }
     __device__ __forceinline__ bool narrow() const { return last; }
-    __device__ __forceinline__ void row(const Row &, int64_t t, int64_t n, const float (&v)[32]) const {
-        store_bf16(dx + t * ld + n, v);
-    }
+    __device__ __forceinline__ void row(int64_t t, int64_t n, const float (&v)[32]) const { store_bf16(dx + t * ld + n, v); }
     __device__ __forceinline__ void put(int64_t t, int64_t n, const float4 &v, int) const {
         store_quad(acc + t * ld_acc + n, v);
     }
@@ -244,10 +242,10 @@ struct DxEpi {
 };
 
 // dw.  A row with a list of tokens waits for what the rounding left over: as bf16
-// it is put aside in 32 bits and written by k_target_rows; in 32 bits it is added
-// to there.  (The walk along the list here would hold up a warp's other 31 rows:
-// 777 weighted tokens on 50257 x 1000 took 314 us that way, 264 us this way, and
-// 244 us without what is left over.)
+// it is also put aside in 32 bits, and written again by k_target_rows; in 32 bits
+// it is added to there.  (The walk along the list here would hold up a warp's
+// other 31 rows: the gradients of 777 weighted tokens on 50257 x 1000 took 314 us
+// that way, 258 us this way, and 244 us without what is left over.)
 struct DwEpi {
     static constexpr bool kStore = true, kWhole = false;
     static constexpr Side kSide = kSomeRows;
@@ -267,21 +265,17 @@ struct DwEpi {
     __device__ __forceinline__ bool apart(const Row &r) const { return r.aside >= 0; }
     __device__ __forceinline__ Row of_lane(const Row &r, int lane) const { return {__shfl_sync(~0u, r.aside, lane)}; }
     __device__ __forceinline__ void finish(const Row &r, int64_t m, int64_t n, float (&v)[32]) const {
-        const float c = r.aside < 0 ? scale : 1.f;
+        if (r.aside >= 0) {
+            float *p = aside + r.aside * ld_aside + n;
 #pragma unroll
-        for (int j = 0; j < 32; ++j) v[j] *= c;
+            for (int j = 0; j < 8; ++j) store_quad(p + 4 * j, make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]));
+        }
+#pragma unroll
+        for (int j = 0; j < 32; ++j) v[j] *= scale;
         if (add) add_f32(v, dw32 + m * ld + n);
     }
     __device__ __forceinline__ bool narrow() const { return dw16 != nullptr; }
-    __device__ __forceinline__ void row(const Row &r, int64_t m, int64_t n, const float (&v)[32]) const {
-        if (r.aside < 0) {
-            store_bf16(dw16 + m * ld + n, v);
-            return;
-        }
-        float *p = aside + r.aside * ld_aside + n;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) store_quad(p + 4 * j, make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]));
-    }
+    __device__ __forceinline__ void row(int64_t m, int64_t n, const float (&v)[32]) const { store_bf16(dw16 + m * ld + n, v); }
     __device__ __forceinline__ void put(int64_t m, int64_t n, const float4 &v, int) const { store_quad(dw32 + m * ld + n, v); }
     __device__ __forceinline__ float with(const Row &, int64_t m, int64_t n) const { return add ? dw32[m * ld + n] : 0.f; }
     __device__ __forceinline__ void one_apart(const Row &r, int64_t n, float v) const { aside[r.aside * ld_aside + n] = v; }
@@ -295,8 +289,8 @@ struct DwEpi {
 // of x times what the rounding of d left over, added in the order of the tokens.
 // With more than kListed tokens nothing is added: so many errors average out, to
 // a third of one token's and less, and the walk stays short.  The kernel is a
-// chain of loads, so all that may be needed for a list of one token, as most are,
-// is on its way at once: 777 rows of 1000 take 4.7 us, 2048 of 2048 8 us.
+// chain of loads, so all that a list of one token needs, as most are, is on its
+// way before it is known whether there are more: 777 rows of 1000 take 4.7 us, 2048 of 2048 8 us.
 constexpr int kListed = 8, kTargetThreads = 256;
 struct TargetRows {
     const int64_t *target;
@@ -314,9 +308,11 @@ __global__ void __launch_bounds__(kTargetThreads) k_target_rows(const TargetRows
     const int64_t row = blockIdx.x, c = ((int64_t)blockIdx.y * kTargetThreads + threadIdx.x) * 8;
     if (c >= a.H) return;
     // by token: one of a list's tokens is its head; else every row is looked at
-    const int first = a.by_token ? (int)row : a.of.head[row];
-    if (first < 0) return;
     const int64_t v = a.by_token ? a.target[row] - a.v0 : row;
+    const float r0 = a.by_token ? a.rest[row] : 0.f;
+    if (a.by_token && (v < 0 || v >= a.n || r0 == 0.f)) return;
+    const int head = a.of.head[v], first = a.by_token ? (int)row : head;
+    if (!a.by_token && head < 0) return;
     const uint16_t *x = a.x + (c >> 6) * (a.T * 64) + (c & 63);
     const auto add = [&](float (&s)[8], float r, const uint4 &q) {
         const uint32_t w[4] = {q.x, q.y, q.z, q.w};
@@ -324,7 +320,7 @@ __global__ void __launch_bounds__(kTargetThreads) k_target_rows(const TargetRows
         for (int k = 0; k < 4; ++k) s[2 * k] += rest_times(r, bf16_lo(w[k])), s[2 * k + 1] += rest_times(r, bf16_hi(w[k]));
     };
     const uint4 q = *reinterpret_cast<const uint4 *>(x + (int64_t)first * 64);
-    const float r = a.rest[first];
+    const float r = a.by_token ? r0 : a.rest[first];
     int u = a.of.next[first];
     // rows put aside are whole quads: of 8 columns the second 4 may not be there
     float4 p[2] = {};
@@ -333,7 +329,7 @@ __global__ void __launch_bounds__(kTargetThreads) k_target_rows(const TargetRows
         p[0] = *reinterpret_cast<const float4 *>(from);
         if (c + 4 < a.H) p[1] = *reinterpret_cast<const float4 *>(from + 4);
     }
-    if (a.by_token && (v < 0 || v >= a.n || a.of.head[v] != first)) return;
+    if (head != first) return;
     float s[8] = {};
     if (u < 0) {
         add(s, r, q);
@@ -387,8 +383,8 @@ __global__ void __launch_bounds__(kTargetThreads) k_target_rows(const TargetRows
 // the tokens in shared memory as 32-bit floats, and keeps the tokens'
 // statistics over its run of the vocabulary; a block is one piece.  Rows need no
 // alignment (as a product, rows that TMA cannot load are copied first).  One
-// token on 131072 x 4096 takes 169 us, 94 % of the measured bandwidth (275 us
-// with rows of 4095), on 32000 x 2048 29 us with the join of the pieces, 34 us
+// token on 131072 x 4096 takes 167 us, 94 % of the measured bandwidth (275 us
+// with rows of 4095), on 32000 x 2048 28 us with the join of the pieces, 34 us
 // as a product.  Four tokens are 313 us on 131072 x 4096 and 193 us as a product,
 // so the limit is two.
 constexpr int kFewTokens = 2, kFewFloats = 16384, kFewRows = 4, kFewWarps = 8, kFewBlocks = 4;

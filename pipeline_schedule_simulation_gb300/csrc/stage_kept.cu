@@ -90,7 +90,7 @@ struct WgradEpi : NoRow {
         if (add) add_f32(v, add + m * ld_add + n);
     }
     __device__ __forceinline__ bool narrow() const { return false; }
-    __device__ __forceinline__ void row(const Row &, int64_t, int64_t, const float (&)[32]) const {}
+    __device__ __forceinline__ void row(int64_t, int64_t, const float (&)[32]) const {}
     __device__ __forceinline__ void put(int64_t m, int64_t n, const float4 &v, int) const { store_quad(dw + m * ld + n, v); }
     __device__ __forceinline__ float with(const Row &, int64_t m, int64_t n) const { return add ? add[m * ld_add + n] : 0.f; }
     __device__ __forceinline__ void one(const Row &, int64_t m, int64_t n, float v, float b, int) const { dw[m * ld + n] = b + v; }

@@ -7,7 +7,7 @@
 // by one otherwise (part: which part of K):
 //   finish(row, m, n, v)   columns n .. n+31 of row m: scaled, added, in place
 //   narrow()               whether rows are stored as bf16:
-//   row(row, m, n, v)      then 32 finished columns at once,
+//   row(m, n, v)           then 32 finished columns at once,
 //   put(m, n, v, part)     else four
 //   with(row, m, n)        what one column is added to
 //   one(row, m, n, v, b, part)  one column, from the sum and that to memory
@@ -18,8 +18,8 @@
 // and those that store C:
 //   kSide              which rows use that: kNoRow, kSomeRows, kEveryRow
 //   of_lane(row, lane) another lane's
-//   apart(row), one_apart(row, n, v)  (kSomeRows) those rows, and one column of
-//                      such a row in place of one()
+//   apart(row), one_apart(row, n, v)  (kSomeRows) those rows, and what is done with
+//                      one column of such a row beside one()
 // and those that do not:
 //   take(row, m, n0, end, N, piece, v)  one piece: run i is the columns from
 //                      n0 + 64 i on, below `end` and (what exists) N
@@ -165,7 +165,7 @@ __device__ __forceinline__ void store_run(const Epi &epi, const typename Epi::Ro
     const bool whole = epi.vec && end - n >= 32;
     if (whole && m0 + lane < M) epi.finish(side, m0 + lane, n, v);
     if (whole && epi.narrow()) {
-        if (m0 + lane < M) epi.row(side, m0 + lane, n, v);
+        if (m0 + lane < M) epi.row(m0 + lane, n, v);
         return;
     }
 #pragma unroll
@@ -184,8 +184,6 @@ __device__ __forceinline__ void store_run(const Epi &epi, const typename Epi::Ro
         const float *one = reinterpret_cast<const float *>(turn);
         const int rows = n + lane < end ? (M - m0 < 32 ? (int)(M - m0) : 32) : 0;
         const auto sum_of = [&](int r) { return one[r * 32 + ((lane >> 2) ^ (r & 7)) * 4 + (lane & 3)]; };
-        [[maybe_unused]] uint32_t apart = 0;
-        if constexpr (Epi::kSide == kSomeRows) apart = __ballot_sync(~0u, m0 + lane < M && epi.apart(side));
         for (int r0 = 0; r0 < (Epi::kSide == kEveryRow ? 32 : rows); r0 += 8) {
             [[maybe_unused]] typename Epi::Row of[8];
             float b[8];
@@ -197,15 +195,18 @@ __device__ __forceinline__ void store_run(const Epi &epi, const typename Epi::Ro
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
                 const int r = r0 + k;
-                if (r < rows && !(apart >> r & 1)) epi.one(of[k], m0 + r, n + lane, sum_of(r), b[k], part);
+                const float x = sum_of(r);
+                if (r < rows) epi.one(of[k], m0 + r, n + lane, x, b[k], part);
             }
         }
-        if constexpr (Epi::kSide == kSomeRows)
+        if constexpr (Epi::kSide == kSomeRows) {
+            uint32_t apart = __ballot_sync(~0u, m0 + lane < M && epi.apart(side));
             for (; apart; apart &= apart - 1) {
                 const int r = __ffs(apart) - 1;
                 const typename Epi::Row its = epi.of_lane(side, r);
                 if (r < rows) epi.one_apart(its, n + lane, sum_of(r));
             }
+        }
     }
     __syncwarp();
 }
@@ -352,23 +353,30 @@ __global__ void __launch_bounds__(kProductThreads, 1)
         const int wide = Epi::kWhole ? (s.N + 63) & ~63 : s.N;
         Place<2> run;
         bool ok = true;
-        // a tile's place, and what a row needs beside its sums, are taken a tile ahead
+        // what a row needs beside its sums is loaded a tile ahead, or where results are stored (and the stores of the
+        // tile before are still on their way) before the wait for the sums
         typename Epi::Row next{};
-        int next_m = 0, next_n = 0;
         const auto begin_next = [&](uint32_t t) {
-            if (t >= tiles) return;
-            tile_at(s, t / s.splits, next_m, next_n);
-            const int64_t m = (int64_t)(next_m * CG + (int)rank) * kHalf + quarter * 32 + lane;
-            if (m < s.M) epi.begin(next, m);
+            if constexpr (!Epi::kStore) {
+                if (t >= tiles) return;
+                int mt, nt;
+                tile_at(s, t / s.splits, mt, nt);
+                const int64_t m = (int64_t)(mt * CG + (int)rank) * kHalf + quarter * 32 + lane;
+                if (m < s.M) epi.begin(next, m);
+            }
         };
         begin_next(first);
         for (uint32_t t = first; t < tiles && ok; t += step) {
-            const int part = (int)(t % s.splits), mt = next_m, nt = next_n;
+            const int part = (int)(t % s.splits);
+            int mt, nt;
+            tile_at(s, t / s.splits, mt, nt);
             const int64_t m = (int64_t)(mt * CG + (int)rank) * kHalf + quarter * 32 + lane;
             const int first_n = nt * s.tile_n, n0 = first_n + half * 32, n1 = min(first_n + s.tile_n, wide);
             const int k0 = part * s.k_blocks, k1 = min(k0 + s.k_blocks, all_blocks);
             const bool live = m < s.M;
-            const typename Epi::Row row = next;
+            typename Epi::Row row = next;
+            if constexpr (Epi::kStore)
+                if (live) epi.begin(row, m);
             uint32_t sum[kRuns][32];  // floats, as the loads give them
             for (int r0 = k0; r0 < k1; r0 += kRun, run.next()) {
                 const int buf = run.slot;
@@ -410,7 +418,6 @@ __global__ void __launch_bounds__(kProductThreads, 1)
             for (int i = 0; i < kRuns; ++i)
 #pragma unroll
                 for (int c = 0; c < 32; ++c) v[i][c] = __uint_as_float(sum[i][c]);
-            begin_next(t + step);
             if constexpr (Epi::kStore) {
                 if (ok) {
                     float4 *turn = reinterpret_cast<float4 *>(raw + (ring - tc::smem_u32(raw)) + kRingBytes +
@@ -424,6 +431,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
                     }
                 }
             } else {
+                begin_next(t + step);
                 if (ok && live) epi.take(row, m, n0, n1, s.N, kPieces * nt + half, v);
                 __syncwarp();
             }
@@ -514,7 +522,7 @@ struct PartEpi : NoRow {
     int64_t M, ld;  // ld is a multiple of 4
     __device__ __forceinline__ bool narrow() const { return false; }
     __device__ __forceinline__ void finish(const Row &, int64_t, int64_t, float (&)[32]) const {}
-    __device__ __forceinline__ void row(const Row &, int64_t, int64_t, const float (&)[32]) const {}
+    __device__ __forceinline__ void row(int64_t, int64_t, const float (&)[32]) const {}
     __device__ __forceinline__ void put(int64_t m, int64_t n, const float4 &v, int part) const {
         *reinterpret_cast<float4 *>(parts + (part * M + m) * ld + n) = v;
     }
@@ -567,12 +575,8 @@ __global__ void __launch_bounds__(256) k_join_parts(const float *parts, int spli
 #pragma unroll
     for (int j = 0; j < 4; ++j)
         if (n + j < N) {
-            if constexpr (Epi::kSide == kSomeRows) {
-                if (epi.apart(row)) {
-                    epi.one_apart(row, n + j, x[j]);
-                    continue;
-                }
-            }
+            if constexpr (Epi::kSide == kSomeRows)
+                if (epi.apart(row)) epi.one_apart(row, n + j, x[j]);
             epi.one(row, m, n + j, x[j], b[j], 0);
         }
 }
