@@ -10,10 +10,10 @@
 // shared memory that bulk copies keep filled, several rows ahead of the
 // arithmetic; few or unaligned rows are loaded directly, by as many blocks as
 // there are rows, and narrow rows (up to 512 columns) are taken by a warp each.
-// One GB300, 16384 x 8192: forward 166 us (6.5 TB/s, 95 % of the measured copy
-// rate), with both checkpoints 231 us (86 %; the packing's instructions issue in
-// two thirds of all cycles), backward from bf16 281 us (85 %), from checkpoints
-// 217-222 us (89 %).  16384 x 512 by warps: forward 13 us (75 %).
+// One GB300, 16384 x 8192: forward 168 us (6.4 TB/s, 94 % of the measured copy
+// rate), with both checkpoints 228 us (87 %; the packing's instructions issue in
+// two thirds of all cycles), backward from bf16 273 us (87 %), from checkpoints
+// 228 us (86 %), the column sums among them.  16384 x 512 by warps: forward 13 us (75 %).
 #include <atomic>
 
 #include "stage_kept.cuh"
