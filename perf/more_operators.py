@@ -368,13 +368,16 @@ def _exact_step(s):
     b1, b2 = BETAS
     t = int(s["step"]) + 1
 
+    def two_to(e):
+        return ((e.to(torch.int64) + 1023) << 52).view(f64)
+
     def held(moment, window):
         """What an 8-bit moment stands for."""
         codes, exps = moment
         n = codes.view(-1, BLOCK).to(torch.int64)
         size = n if window == 31 else n % 128
         place = size + 8 * (exps.to(torch.int64)[:, None] - window)
-        value = torch.ldexp(1 + (place % 8).to(f64) / 8, place // 8 - 127)
+        value = (1 + (place % 8).to(f64) / 8) * two_to(place // 8 - 127)
         value = torch.where(size == 0, torch.zeros_like(value), value)
         return (torch.where(n >= 128, -value, value) if window == 15 else value).view(-1)
 
@@ -382,11 +385,11 @@ def _exact_step(s):
         """x rounded to 4 significant bits, up with the probability of what is cut off, within the block's window."""
         x = x.view(-1, BLOCK)
         e = torch.frexp(x)[1] - 1
-        unit = torch.ldexp(torch.ones_like(x), e - 3)
+        unit = two_to(e - 3)
         size = torch.floor(x.abs() / unit + u.view(-1, BLOCK)) * unit
         top = x.abs().amax(1, keepdim=True)
-        unit = torch.ldexp(torch.ones_like(top), torch.frexp(top)[1] - 4)
-        least = torch.ldexp(torch.full_like(top, 1.125), torch.frexp(torch.ceil(top / unit) * unit)[1] - 1 - window)
+        unit = two_to(torch.frexp(top)[1] - 4)
+        least = 1.125 * two_to(torch.frexp(torch.ceil(top / unit) * unit)[1] - 1 - window)
         size = torch.where(size < least, least if window == 31 else torch.zeros_like(least), size)
         size = torch.where(x == 0, torch.zeros_like(size), size)
         return torch.where(x < 0, -size, size).view(-1)
@@ -404,7 +407,7 @@ def _exact_step(s):
     del g
     low, more = _draws(p.numel(), s["seed"], s["step"] + 1) if c["random"] else (None, None)
     if c["par"] == "bf16" and c["random"]:
-        unit = torch.ldexp(torch.ones_like(p), torch.frexp(p)[1] - 8)
+        unit = two_to(torch.frexp(p)[1] - 8)
         out["p"] = torch.where(p == 0, p, torch.sign(p) * torch.floor(p.abs() / unit + more / 65536) * unit)
     else:
         out["p"] = p
