@@ -8,11 +8,15 @@
  *          vocabulary, taken in pieces of the vocabulary so that the logits
  *          are never kept, with the gradients of the activations (B) and of
  *          the output matrix (W).
+ *   score  the last stage where it learns from log probabilities: those of given
+ *          tokens, the entropy and the likeliest alternatives, and the gradients.
  *   kept   activation checkpoints in 8 bits: what a microbatch holds between
  *          its F and its W, and the weight gradient taken from them.
  *   join   the end of one block and the start of the next: the norm after the
  *          block, its gate, the residual scale and sum, the norm before the
  *          next block; forward and backward.
+ *   step   what follows the flush: the norm of the gradients over all tensors of
+ *          the stage, and the AdamW step over them, its moments in 32 or in 8 bits.
  *
  * Conventions for every entry point (as in ppsched.h):
  *   - Arrays are caller-owned DEVICE memory; matrices are row-major with
@@ -51,6 +55,9 @@ extern "C" {
 #define PP_STAGE_MAX_VOCAB (1 << 24)  /* V, and N of the weight gradient */
 #define PP_STAGE_MAX_WIDTH (1 << 16)  /* H of head and kept */
 #define PP_STAGE_MAX_JOIN_WIDTH 16384 /* H of the join */
+#define PP_STAGE_MAX_TOP 32           /* alternatives of a token */
+#define PP_STAGE_MAX_TENSORS (1 << 20)       /* tensors of one step */
+#define PP_STAGE_MAX_ELEMENTS (1LL << 38)    /* elements of a tensor, and of the moments */
 
 /* Columns of a checkpoint that share one exponent. */
 #define PP_STAGE_BLOCK 64
@@ -87,6 +94,41 @@ int pp_stage_head_backward(const uint16_t *x, int64_t stride_x, const uint16_t *
                            int64_t T, int64_t V, int64_t H, uint16_t *dx, int64_t stride_dx,
                            void *dw, int64_t stride_dw, int dw_float, int dw_add,
                            void *workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/* ---- score --------------------------------------------------------------
+ * Of the same logits, with p = exp(l - lse):
+ *   logp[t]    = l[t][target[t]] - lse[t], and 0 for a token that is left out
+ *   entropy[t] = -sum_v p[t][v] (l[t][v] - lse[t])
+ *   top_index[t][i], top_logp[t][i], i < top: the columns of the `top` largest
+ *                logits in falling order, the lower column first among equal
+ *                ones, and their log probabilities
+ * lse, entropy and the alternatives are those of every token, left out or not.  A
+ * logit that is NaN comes behind all others; where fewer than `top` are numbers,
+ * the rest of the row is -1 and NaN.  An entropy without a finite value (no finite
+ * logit, or an infinite one) is NaN.  Any of logp, lse and entropy may be NULL, not
+ * all of them without alternatives; top = 0: top_logp and top_index are not used. */
+size_t pp_stage_score_forward_workspace(const uint16_t *x, int64_t stride_x, const uint16_t *w, int64_t stride_w,
+                                        int64_t T, int64_t V, int64_t H, int64_t top);
+int pp_stage_score_forward(const uint16_t *x, int64_t stride_x, const uint16_t *w, int64_t stride_w,
+                           const int64_t *target, int64_t T, int64_t V, int64_t H, int64_t top,
+                           float *logp, float *lse, float *entropy, float *top_logp, int64_t *top_index,
+                           void *workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/* Gradients of a loss that reaches the logits through logp and the entropy, given
+ * dlogp = dL/dlogp and dentropy = dL/dentropy (NULL: 0) of every token, and lse and
+ * entropy as pp_stage_score_forward returned them (entropy is read only where
+ * dentropy is given and not 0):
+ *   d[t][v] = dlogp[t] ([v == target[t]] - p) - dentropy[t] p (log p + entropy[t])
+ *   dx = d w,  dw = d^T x
+ * A token that is left out has no gradient, through its entropy neither.  dx, dw, the
+ * rounding of d and what is added for it: as for pp_stage_head_backward. */
+size_t pp_stage_score_backward_workspace(const uint16_t *x, int64_t stride_x, const uint16_t *w, int64_t stride_w,
+                                         int64_t T, int64_t V, int64_t H);
+int pp_stage_score_backward(const uint16_t *x, int64_t stride_x, const uint16_t *w, int64_t stride_w,
+                            const int64_t *target, const float *lse, const float *dlogp, const float *entropy,
+                            const float *dentropy, int64_t T, int64_t V, int64_t H, uint16_t *dx, int64_t stride_dx,
+                            void *dw, int64_t stride_dw, int dw_float, int dw_add,
+                            void *workspace, size_t workspace_bytes, cudaStream_t stream);
 
 /* ---- kept ---------------------------------------------------------------
  * The checkpoint of x [T][H] bf16: q [T][H] int8 and e [T][ceil(H/64)] int8.
@@ -146,6 +188,59 @@ int pp_stage_join_backward(const uint16_t *dh, int64_t stride_dh, const uint16_t
                            uint16_t *dx, int64_t stride_dx, uint16_t *df, int64_t stride_df,
                            float *dw_post, float *dw_pre, float *dgate, int64_t stride_dgate,
                            void *workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/* ---- step ---------------------------------------------------------------
+ * A tensor of the step.  The list is HOST memory, read before the call returns;
+ * what it points to is device memory.  Tensors are contiguous, of any length and
+ * element-aligned; 32-byte (float) and 16-byte (bf16) bases are faster. */
+typedef struct {
+    void *p;         /* parameters: float, or bf16 */
+    const void *g;   /* gradients: float, or bf16 */
+    uint16_t *copy;  /* of float parameters: where their bf16 copy is written, or NULL */
+    int64_t n;       /* elements */
+    int64_t at;      /* its first element among the moments: a multiple of PP_STAGE_BLOCK */
+    float decay;     /* weight decay */
+    uint8_t p_float, g_float;
+} pp_stage_tensor;
+
+/* norm = the root of the sum of the squares of all gradients (of each entry only g,
+ * n and g_float are looked at).  Squares are added in 32 bits within a thread and in
+ * 64 beyond: a gradient above 1.8e19 makes the norm infinite. */
+size_t pp_stage_grad_norm_workspace(const pp_stage_tensor *list, int64_t count);
+int pp_stage_grad_norm(const pp_stage_tensor *list, int64_t count, float *norm,
+                       void *workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/* One AdamW step, t = *step + 1 (a device word, written back: a captured call counts
+ * on as it is replayed):
+ *   c = max_norm / *norm where *norm > max_norm, else 1 (norm NULL: 1; a device float)
+ *   m = beta1 m + (1 - beta1) c g     v = beta2 v + (1 - beta2) (c g)^2
+ *   p = p (1 - lr decay) - lr / (1 - beta1^t) m / (sqrt(v / (1 - beta2^t)) + eps)
+ * lr is *lr_at (a device float) where that is given.  Where *norm is not a finite
+ * number nothing changes, *step neither.
+ *
+ * Moments: `held` elements of m and of v, those of a tensor from `at` on, 32-byte
+ * aligned; what lies between a tensor's end and the next multiple of PP_STAGE_BLOCK
+ * is written with zeros.  float, or (m_exp and v_exp given) 8 bits: a byte an
+ * element and one exponent for each PP_STAGE_BLOCK, e, as floats have it.  A byte's
+ * low bits c (m: 7, its 8th is the sign; v: 8) are 0 for 0 and else stand for the
+ * float whose bits are (c + 8 (e - w)) << 20, with w = 15 for m and 31 for v; e = 255:
+ * NaN.  e is the exponent of the block's largest magnitude rounded up to 4
+ * significant bits; magnitudes are rounded to 4 significant bits; an m below the
+ * window (2^-w of the block's largest binade) is held as 0, a v as the least that is
+ * not 0.
+ *
+ * random = 0: moments in 8 bits and bf16 parameters are rounded to nearest; 1: up
+ * with the probability of what is cut off, by bits that depend on seed, t and the
+ * element's place among the moments alone.  Copies are rounded to nearest.  Tensors
+ * must not overlap. */
+size_t pp_stage_adamw_workspace(void);
+int pp_stage_adamw(const pp_stage_tensor *list, int64_t count, void *m, void *v, uint8_t *m_exp, uint8_t *v_exp,
+                   int64_t held, int64_t *step, const float *lr_at, double lr, double beta1, double beta2, double eps,
+                   const float *norm, double max_norm, int random, uint64_t seed,
+                   void *workspace, size_t workspace_bytes, cudaStream_t stream);
+/* What moments in 8 bits stand for, as bf16 (exactly). */
+int pp_stage_adamw_moments(const uint8_t *m, const uint8_t *v, const uint8_t *m_exp, const uint8_t *v_exp, int64_t held,
+                           uint16_t *m_values, uint16_t *v_values, cudaStream_t stream);
 
 /* ---- waits --------------------------------------------------------------
  * The blocks of the products and of the join's rings wait for their own copies

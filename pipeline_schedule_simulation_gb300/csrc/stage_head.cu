@@ -28,25 +28,10 @@
 // does: one token on 32000 x 2048 takes 28 us, its 131 MB alone 19 us.
 #include <algorithm>
 
-#include "stage_kept.cuh"
-#include "stage_product.cuh"
+#include "stage_head.cuh"
 
 namespace pps {
 namespace {
-
-constexpr float kNegInf = -__builtin_huge_valf();
-
-// The reference point of a sum of exponentials: the largest logit, or 0 where
-// that is infinite (so that inf - inf never appears).
-__device__ __forceinline__ float ref_of(float m) { return isinf(m) ? 0.f : m; }
-
-// A sum of exponentials relative to ref_of(m), taken relative to `r` (an empty
-// one stays empty).
-__device__ __forceinline__ float rebase(float s, float m, float r) {
-    return s == 0.f ? 0.f : s * exp2_fast((ref_of(m) - r) * kLog2e);
-}
-
-__device__ __forceinline__ bool inside(int64_t target, int64_t V) { return target >= 0 && target < V; }
 
 struct StatsEpi {
     static constexpr bool kStore = false, kWhole = false;
@@ -118,7 +103,9 @@ struct Lists {
     int *head, *next;
 };
 
-// d of one piece of the vocabulary: columns v0 .., as bf16.
+// d of one piece of the vocabulary: columns v0 .., as bf16.  ENT: with what reaches
+// the logits through the entropy, so that d = c (p - onehot) + b p (log p + entropy).
+template <bool ENT>
 struct GradEpi {
     static constexpr bool kStore = false, kWhole = true;
     const int64_t *target;
@@ -127,8 +114,9 @@ struct GradEpi {
     uint16_t *d;  // in panels of T rows
     float *rest;  // [T]: what the rounding leaves over at the target
     Lists of;     // of the piece's columns; head null: not asked for
+    const float *entropy, *dentropy;  // [T], ENT only
     struct Row {
-        float lse, c;
+        float lse, c, b, sum;  // sum: c + b entropy
         int64_t at;  // the target's column counted from the piece's first
         bool in;
     };
@@ -138,6 +126,10 @@ struct GradEpi {
         r.c = weight ? weight[t] : 1.f;
         r.lse = lse[t];
         r.at = g - v0;
+        if constexpr (ENT) {
+            r.b = dentropy[t];
+            r.sum = r.b != 0.f ? fmaf(r.b, entropy[t], r.c) : r.c;  // a row without that gradient is not asked for its entropy
+        }
     }
     __device__ __forceinline__ void take(const Row &r, int64_t t, int n0, int end, int N, int, float (&v)[kRuns][32]) const {
         // whether the target is in one of these runs (past N it is the next piece's)
@@ -149,16 +141,29 @@ struct GradEpi {
             const int n = n0 + i * kPieces * 32;
             if (n >= end) break;
             float p[32];
-#pragma unroll
-            for (int j = 0; j < 32; ++j) p[j] = exp2_full((v[i][j] - r.lse) * kLog2e);
             const bool here = r.at >= n && r.at < n + 32;
-            if (here) {
+            if constexpr (ENT) {
 #pragma unroll
-                for (int j = 0; j < 32; ++j)
-                    if (n + j == r.at) p[j] -= 1.f;
+                for (int j = 0; j < 32; ++j) {
+                    const float l = v[i][j] - r.lse;
+                    p[j] = exp2_full(l * kLog2e) * fmaf(r.b, not_below(l, kNoLog), r.sum);
+                }
+                if (here) {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j)
+                        if (n + j == r.at) p[j] -= r.c;
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < 32; ++j) p[j] = exp2_full((v[i][j] - r.lse) * kLog2e);
+                if (here) {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j)
+                        if (n + j == r.at) p[j] -= 1.f;
+                }
+#pragma unroll
+                for (int j = 0; j < 32; ++j) p[j] *= r.c;
             }
-#pragma unroll
-            for (int j = 0; j < 32; ++j) p[j] *= r.c;
             if (here && mine) {
                 float x = 0.f;
 #pragma unroll
@@ -376,19 +381,8 @@ __global__ void __launch_bounds__(kTargetThreads) k_target_rows(const TargetRows
     }
 }
 
-// ---- few tokens: w is read once, by the row
-
-// One or two tokens are two multiplications for every 2 bytes of w: a warp takes
-// 4 rows of w at a time straight from memory, the lanes 8 columns each, against
-// the tokens in shared memory as 32-bit floats, and keeps the tokens'
-// statistics over its run of the vocabulary; a block is one piece.  Rows need no
-// alignment (as a product, rows that TMA cannot load are copied first).  One
-// token on 131072 x 4096 takes 167 us, 94 % of the measured bandwidth (275 us
-// with rows of 4095), on 32000 x 2048 28 us with the join of the pieces, 34 us
-// as a product.  Four tokens are 313 us on 131072 x 4096 and 193 us as a product,
-// so the limit is two.
-constexpr int kFewTokens = 2, kFewFloats = 16384, kFewRows = 4, kFewWarps = 8, kFewBlocks = 4;
-
+// ---- few tokens (few_logits): each warp keeps the statistics over its run of the
+// vocabulary, a block is one piece.
 template <int NT, bool VEC>
 __global__ void __launch_bounds__(32 * kFewWarps, kFewBlocks) k_head_few(const uint16_t *x, int64_t stride_x, const uint16_t *w,
                                                             int64_t stride_w, const int64_t *target, int T, int64_t V,
@@ -397,63 +391,19 @@ __global__ void __launch_bounds__(32 * kFewWarps, kFewBlocks) k_head_few(const u
     __shared__ float2 sh[kFewWarps][NT];
     let_next_start();
     after_previous();
-    const int chunks = (H + 7) / 8;
-    for (int i = threadIdx.x; i < NT * chunks; i += 32 * kFewWarps) {
-        const int t = i / chunks, c = i - t * chunks;
-        float v[8] = {};
-        if (t < T) load8_bf16<false>(x + t * stride_x + c * 8, H - c * 8, v);
-        xs[(2 * t) * chunks + c] = make_float4(v[0], v[1], v[2], v[3]);
-        xs[(2 * t + 1) * chunks + c] = make_float4(v[4], v[5], v[6], v[7]);
-    }
-    __syncthreads();
+    few_load<NT>(xs, x, stride_x, T, H);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t first = ((int64_t)blockIdx.x * kFewWarps + warp) * rows, last = min(first + rows, V);
     float m[NT], s[NT];
     int64_t want[NT];
 #pragma unroll
     for (int t = 0; t < NT; ++t) m[t] = kNegInf, s[t] = 0.f, want[t] = t < T ? target[t] : -1;
-    for (int64_t v0 = first; v0 < last; v0 += kFewRows) {
-        const uint16_t *row[kFewRows];
-#pragma unroll
-        for (int r = 0; r < kFewRows; ++r) row[r] = w + min(v0 + r, last - 1) * stride_w;
-        float acc[kFewRows][NT] = {};
-#pragma unroll 2
-        for (int c = lane; c < chunks; c += 32) {
-            Raw8 q[kFewRows];
-#pragma unroll
-            for (int r = 0; r < kFewRows; ++r) q[r] = load8<VEC>(row[r] + c * 8, H - c * 8);
-            float4 a[NT], b[NT];
-#pragma unroll
-            for (int t = 0; t < NT; ++t) a[t] = xs[2 * t * chunks + c], b[t] = xs[(2 * t + 1) * chunks + c];
-#pragma unroll
-            for (int r = 0; r < kFewRows; ++r) {
-                float u[8];
-                widen(q[r], u);
-#pragma unroll
-                for (int t = 0; t < NT; ++t) {
-                    float z = acc[r][t];
-                    z = fmaf(u[0], a[t].x, z), z = fmaf(u[1], a[t].y, z), z = fmaf(u[2], a[t].z, z);
-                    z = fmaf(u[3], a[t].w, z), z = fmaf(u[4], b[t].x, z), z = fmaf(u[5], b[t].y, z);
-                    acc[r][t] = fmaf(u[7], b[t].w, fmaf(u[6], b[t].z, z));
-                }
-            }
-        }
-#pragma unroll
-        for (int r = 0; r < kFewRows; ++r) {
-#pragma unroll
-            for (int t = 0; t < NT; ++t) {
-                float l = acc[r][t];
-#pragma unroll
-                for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(~0u, l, o);
-                if (v0 + r < last) {
-                    const float top = fmaxf(m[t], l), ref = ref_of(top);
-                    s[t] = rebase(s[t], m[t], ref) + exp2_fast((l - ref) * kLog2e);
-                    m[t] = top;
-                    if (lane == 0 && want[t] == v0 + r) picked[t] = l;
-                }
-            }
-        }
-    }
+    few_logits<NT, VEC>(xs, w, stride_w, H, first, last, [&](int t, int64_t v, float l) {
+        const float top = fmaxf(m[t], l), ref = ref_of(top);
+        s[t] = rebase(s[t], m[t], ref) + exp2_fast((l - ref) * kLog2e);
+        m[t] = top;
+        if (lane == 0 && want[t] == v) picked[t] = l;
+    });
     if (lane == 0) {
 #pragma unroll
         for (int t = 0; t < NT; ++t) sh[warp][t] = make_float2(m[t], s[t]);
@@ -467,15 +417,6 @@ __global__ void __launch_bounds__(32 * kFewWarps, kFewBlocks) k_head_few(const u
         for (int i = 0; i < kFewWarps; ++i) sum += rebase(sh[i][t].y, sh[i][t].x, ref);
         part[(int64_t)blockIdx.x * T + t] = make_float2(top, sum);
     }
-}
-
-bool few_tokens(int64_t T, int64_t H) { return T <= kFewTokens && T * round_up(H, 8) <= kFewFloats; }
-
-// Rows of w to a warp: all blocks run at once, as many to an SM as its 228 KB of
-// shared memory hold (with the block's own sums and what the SM takes for each).
-int64_t few_rows(int64_t T, int64_t V, int64_t H) {
-    const int64_t each = T * ceil_div(H, 8) * 32 + kFewWarps * kFewTokens * 8 + 1024, fit = 228 * 1024 / each;
-    return ceil_div(V, (int64_t)sm_count() * (fit < kFewBlocks ? fit : kFewBlocks) * kFewWarps);
 }
 
 // 8 tokens a block: 32 lanes along the pieces of each.  First the largest
@@ -539,34 +480,6 @@ int64_t piece_of(int64_t T, int64_t V) {
     return round_up(ceil_div(V, n), 256);
 }
 
-int check_head(const void *x, int64_t sx, const void *w, int64_t sw, const void *target, int64_t T, int64_t V,
-               int64_t H) {
-    if (T < 0 || V < 1 || H < 1) return PP_ERR_ARG;
-    if (T > PP_STAGE_MAX_ROWS || V > PP_STAGE_MAX_VOCAB || H > PP_STAGE_MAX_WIDTH) return PP_ERR_SIZE;
-    if (!w || ((uintptr_t)w & 1) || sw < H) return PP_ERR_ARG;
-    if (T > 0 && (!x || !target || ((uintptr_t)x & 1) || ((uintptr_t)target & 7) || sx < H)) return PP_ERR_ARG;
-    return PP_OK;
-}
-
-// An operand as the products read it: in place, or as a copy whose rows start on
-// 128 bytes.  Rows that TMA cannot load (not aligned to 16 bytes) are always
-// copied.  Rows that it can but that straddle 128-byte lines make the loads
-// slower; a copy costs 4 bytes an element and pays once enough row tiles of the
-// other operand pass over it: w 50257 x 1000 takes 25 us to copy, and the loss
-// of 777 tokens (4 row tiles) 94 us in place and 70 us from the copy.
-constexpr int64_t kCopyFrom = 8;
-struct Aligned {
-    uint16_t *copy;  // null: in place
-    Matrix at;
-};
-Aligned aligned(Carve &c, const uint16_t *p, int64_t stride, int64_t rows, int64_t H, int64_t passes) {
-    const bool lines = rows <= 1 || (((uintptr_t)p & 127) == 0 && stride % 64 == 0);
-    if (rows_aligned(p, stride, rows, 2) && (lines || passes < kCopyFrom)) return {nullptr, in_rows(p, stride)};
-    const int64_t ld = round_up(H, 64);
-    uint16_t *q = c.take<uint16_t>(rows * ld);
-    return {q, in_rows(q, ld)};
-}
-
 struct ForwardSpace {
     Aligned x, w;
     float2 *part;
@@ -582,7 +495,7 @@ ForwardSpace forward_space(void *ws, const uint16_t *x, int64_t sx, const uint16
     ForwardSpace s{};
     s.few = few_tokens(T, H);
     if (s.few) {
-        s.pieces = ceil_div(V, few_rows(T, V, H) * kFewWarps);
+        s.pieces = ceil_div(V, few_rows(T, V, H, kFewWarps * kFewTokens * 8) * kFewWarps);
     } else {
         s.x = aligned(c, x, sx, T, H, ceil_div(V, 256));
         s.w = aligned(c, w, sw, V, H, ceil_div(T, 256));
@@ -626,10 +539,6 @@ BackwardSpace backward_space(void *ws, const uint16_t *x, int64_t sx, const uint
     return s;
 }
 
-int copy_if(const Aligned &a, const uint16_t *p, int64_t stride, int64_t rows, int64_t H, cudaStream_t stream) {
-    return a.copy ? launch_copy_rows(p, stride, rows, H, nullptr, 0, nullptr, a.copy, a.at.ld, 64, stream) : PP_OK;
-}
-
 }  // namespace
 }  // namespace pps
 
@@ -659,7 +568,7 @@ extern "C" int pp_stage_head_forward(const uint16_t *x, int64_t stride_x, const 
         rp = allow_smem(kernel, kFewFloats * 4, ready[2 * (T - 1) + vec]);
         if (rp == PP_OK)
             rp = launch_after(kernel, s.pieces, 32 * kFewWarps, (int)(T * ceil_div(H, 8) * 32), stream, 1, x, stride_x, w,
-                              stride_w, target, (int)T, V, (int)H, few_rows(T, V, H), s.part, s.picked);
+                              stride_w, target, (int)T, V, (int)H, few_rows(T, V, H, kFewWarps * kFewTokens * 8), s.part, s.picked);
     } else {
         rp = copy_if(s.x, x, stride_x, T, H, stream);
         if (rp == PP_OK) rp = copy_if(s.w, w, stride_w, V, H, stream);
@@ -678,11 +587,11 @@ extern "C" size_t pp_stage_head_backward_workspace(const uint16_t *x, int64_t st
     return backward_space(nullptr, x, stride_x, w, stride_w, T, V, H).bytes;
 }
 
-extern "C" int pp_stage_head_backward(const uint16_t *x, int64_t stride_x, const uint16_t *w, int64_t stride_w,
-                                      const int64_t *target, const float *lse, const float *weight, float scale,
-                                      int64_t T, int64_t V, int64_t H, uint16_t *dx, int64_t stride_dx, void *dw,
-                                      int64_t stride_dw, int dw_float, int dw_add, void *workspace,
-                                      size_t workspace_bytes, cudaStream_t stream) {
+// entropy, dentropy: both null, or what GradEpi<true> reads.
+static int head_backward(const uint16_t *x, int64_t stride_x, const uint16_t *w, int64_t stride_w, const int64_t *target,
+                         const float *lse, const float *weight, const float *entropy, const float *dentropy, float scale,
+                         int64_t T, int64_t V, int64_t H, uint16_t *dx, int64_t stride_dx, void *dw, int64_t stride_dw,
+                         int dw_float, int dw_add, void *workspace, size_t workspace_bytes, cudaStream_t stream) {
     const int rc = check_head(x, stride_x, w, stride_w, target, T, V, H);
     if (rc != PP_OK) return rc;
     if (!dw && (T > 0 && !dx)) return PP_ERR_ARG;
@@ -706,7 +615,12 @@ extern "C" int pp_stage_head_backward(const uint16_t *x, int64_t stride_x, const
         const int64_t n = V - v0 < s.piece ? V - v0 : s.piece;
         const Matrix wp = in_rows(s.w.at.p + v0 * s.w.at.ld, s.w.at.ld);
         const Lists of{dw ? s.of.head + v0 : nullptr, s.of.next};
-        rp = whole_product<kPanelsK, kRowsK>(xm, wp, T, n, H, GradEpi{target, lse, weight, T, V, v0, s.d, s.rest, of}, stream);
+        rp = dentropy ? whole_product<kPanelsK, kRowsK>(
+                            xm, wp, T, n, H,
+                            GradEpi<true>{target, lse, weight, T, V, v0, s.d, s.rest, of, entropy, dentropy}, stream)
+                      : whole_product<kPanelsK, kRowsK>(
+                            xm, wp, T, n, H,
+                            GradEpi<false>{target, lse, weight, T, V, v0, s.d, s.rest, of, nullptr, nullptr}, stream);
         if (rp == PP_OK && dx) {
             const DxEpi epi{s.acc, dx, target, s.rest, s.w.at.p, V, s.ld_acc, stride_dx, s.w.at.ld, scale, v0 == 0,
                             v0 + n == V, vec_dx};
@@ -729,4 +643,29 @@ extern "C" int pp_stage_head_backward(const uint16_t *x, int64_t stride_x, const
         }
     }
     return rp;
+}
+
+extern "C" int pp_stage_head_backward(const uint16_t *x, int64_t stride_x, const uint16_t *w, int64_t stride_w,
+                                      const int64_t *target, const float *lse, const float *weight, float scale,
+                                      int64_t T, int64_t V, int64_t H, uint16_t *dx, int64_t stride_dx, void *dw,
+                                      int64_t stride_dw, int dw_float, int dw_add, void *workspace,
+                                      size_t workspace_bytes, cudaStream_t stream) {
+    return head_backward(x, stride_x, w, stride_w, target, lse, weight, nullptr, nullptr, scale, T, V, H, dx, stride_dx, dw,
+                         stride_dw, dw_float, dw_add, workspace, workspace_bytes, stream);
+}
+
+extern "C" size_t pp_stage_score_backward_workspace(const uint16_t *x, int64_t stride_x, const uint16_t *w,
+                                                    int64_t stride_w, int64_t T, int64_t V, int64_t H) {
+    return pp_stage_head_backward_workspace(x, stride_x, w, stride_w, T, V, H);
+}
+
+// logp is minus the loss: the loss's gradients, weighted with what reaches logp, and at the end minus that.
+extern "C" int pp_stage_score_backward(const uint16_t *x, int64_t stride_x, const uint16_t *w, int64_t stride_w,
+                                       const int64_t *target, const float *lse, const float *dlogp,
+                                       const float *entropy, const float *dentropy, int64_t T, int64_t V, int64_t H,
+                                       uint16_t *dx, int64_t stride_dx, void *dw, int64_t stride_dw, int dw_float,
+                                       int dw_add, void *workspace, size_t workspace_bytes, cudaStream_t stream) {
+    if (T > 0 && (!dlogp || (dentropy && !entropy) || ((uintptr_t)entropy & 3) || ((uintptr_t)dentropy & 3))) return PP_ERR_ARG;
+    return head_backward(x, stride_x, w, stride_w, target, lse, dlogp, entropy, dentropy, -1.f, T, V, H, dx, stride_dx, dw,
+                         stride_dw, dw_float, dw_add, workspace, workspace_bytes, stream);
 }

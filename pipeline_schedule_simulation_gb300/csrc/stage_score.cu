@@ -1,0 +1,534 @@
+// stage_score.cu -- log probabilities of given tokens over a large vocabulary,
+// with the entropy and the likeliest alternatives, without keeping the logits.
+// (Their gradients are those of the loss, stage_head.cu.)
+//
+// As in the loss, l = x w^T is taken tile by tile and of each token's part of a
+// tile (two pieces of up to 128 columns) only sums leave the product:
+//   m = max l,   s = sum 2^q,   u = sum q 2^q   with q = (l - m) log2 e
+// and, where alternatives are asked for, the logits that may be among the k
+// largest.  A second kernel joins the pieces of a token:
+//   lse = m + log s,   entropy = lse - sum p l = log s - u log 2 / s.
+// Both terms of the entropy are positive, so nothing cancels.
+//
+// Alternatives.  A thread holds its piece in registers and writes the logits that
+// reach a bound below which nothing can be among the token's k largest: k classes of pieces each keep the largest logit that any of
+// their pieces has had, and the least of these k is such a bound, since k
+// different logits reach it.  It rises as tiles finish; a thread reads it a tile
+// ahead, and an old bound only lets through more.  So the order in which blocks
+// run decides what is written, but not what is found.  Of 131072 columns a few
+// hundred are written for each token.
+#include <algorithm>
+
+#include "stage_head.cuh"
+
+namespace pps {
+namespace {
+
+constexpr float kNaN = __builtin_nanf("");
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr int kMaxTop = PP_STAGE_MAX_TOP;
+static_assert(kMaxTop <= 32);  // a lane to each
+
+// Largest logit, s and u of a piece, as above; relative to ref_of(m).
+struct Stats {
+    float m, s, u;
+};
+constexpr float kNoExp = -200.f;  // 2^q is 0 from there on; q itself may be infinite
+
+__device__ __forceinline__ Stats rebase(const Stats &a, float r) {
+    if (a.s == 0.f) return {a.m, 0.f, 0.f};
+    const float d = (ref_of(a.m) - r) * kLog2e, f = exp2_fast(d);
+    return {a.m, a.s * f, f == 0.f ? 0.f : f * fmaf(a.s, d, a.u)};
+}
+__device__ __forceinline__ Stats add(const Stats &a, const Stats &b) {
+    const float top = fmaxf(a.m, b.m), ref = ref_of(top);
+    const Stats x = rebase(a, ref), y = rebase(b, ref);
+    return {top, x.s + y.s, x.u + y.u};
+}
+
+// An alternative: its logit and its column.
+struct Found {
+    float l;
+    int n;
+};
+__device__ __forceinline__ bool before(const Found &a, const Found &b) { return a.l > b.l || (a.l == b.l && a.n < b.n); }
+
+// Floats as whole numbers of the same order, above 0 (which stands for no bound).
+__device__ __forceinline__ uint32_t ordered(float f) {
+    const uint32_t b = __float_as_uint(f);
+    return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+__device__ __forceinline__ float from_ordered(uint32_t u) {
+    return u == 0 ? kNegInf : __uint_as_float(u & 0x80000000u ? u & 0x7FFFFFFFu : ~u);
+}
+
+// What the pieces' alternatives are written to.
+struct Alternatives {
+    int k, slots;     // slots: of a piece, k or more
+    int64_t pieces;
+    uint8_t *count;   // [T][pieces]
+    Found *found;     // [T][pieces][slots]; of few tokens in order, else by column
+    uint32_t *least;  // [k][T]: the classes' largest logits, as ordered(); null for few tokens
+};
+
+template <bool TOP>
+struct ScoreEpi {
+    static constexpr bool kStore = false, kWhole = false;
+    const int64_t *target;
+    int64_t T, V;
+    Stats *part;    // [pieces][T]
+    float *picked;  // [T]: the target's logit
+    Alternatives alt;
+    struct Row {
+        int64_t target;
+        uint32_t least;
+    };
+    __device__ __forceinline__ void begin(Row &r, int64_t t) const {
+        r.target = target[t];
+        if constexpr (TOP) {
+            uint32_t a = ~0u;
+            for (int j = 0; j < alt.k; ++j) a = min(a, __ldcg(alt.least + j * T + t));
+            r.least = a;
+        }
+    }
+    __device__ __forceinline__ void take(const Row &r, int64_t t, int n0, int end, int N, int piece,
+                                         float (&v)[kRuns][32]) const {
+        const int last = min(end, N);
+        float run[kRuns];  // largest logits of the runs
+#pragma unroll
+        for (int i = 0; i < kRuns; ++i) {
+            const int cnt = last - (n0 + i * kPieces * 32);
+            run[i] = cnt >= 32 ? largest(v[i]) : largest_of(v[i], cnt);
+        }
+        if constexpr (TOP) take_out(r, t, n0, last, piece, run, v);
+        Stats a{kNegInf, 0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < kRuns; ++i) {
+            const int n = n0 + i * kPieces * 32, cnt = min(32, last - n);
+            if (cnt <= 0) break;
+            if (cnt < 32) {  // they add nothing
+#pragma unroll
+                for (int j = 0; j < 32; ++j)
+                    if (j >= cnt) v[i][j] = kNegInf;
+            }
+            const float top = fmaxf(a.m, run[i]), ref = ref_of(top);
+            const Stats b = rebase(a, ref);
+            float e[4] = {b.s, 0.f, 0.f, 0.f}, u[4] = {b.u, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+                const float q = not_below((v[i][j] - ref) * kLog2e, kNoExp), p = exp2_fast(q);
+                e[j & 3] += p;
+                u[j & 3] = fmaf(p, q, u[j & 3]);
+            }
+            a = {top, (e[0] + e[1]) + (e[2] + e[3]), (u[0] + u[1]) + (u[2] + u[3])};
+            const int64_t at = r.target - n;  // few rows have their target here
+            if (at >= 0 && at < cnt) {
+#pragma unroll
+                for (int j = 0; j < 32; ++j)
+                    if (at == j) picked[t] = v[i][j];
+            }
+        }
+        part[(int64_t)piece * T + t] = a;
+    }
+    static __device__ __forceinline__ float largest(const float (&v)[32]) {  // NaN only where all are
+        float m[4] = {v[0], v[1], v[2], v[3]};
+#pragma unroll
+        for (int j = 4; j < 32; ++j) m[j & 3] = fmaxf(m[j & 3], v[j]);
+        return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+    }
+    static __device__ __forceinline__ float largest_of(const float (&v)[32], int cnt) {  // of the first ones
+        float m = kNaN;
+#pragma unroll
+        for (int j = 0; j < 31; ++j) m = fmaxf(m, j < cnt ? v[j] : kNaN);
+        return m;
+    }
+    // The columns of a run that exist and reach a bound, as bits.
+    static __device__ __forceinline__ uint32_t reaching(float bound, const float (&v)[32], int cnt) {
+        uint32_t b[4] = {};
+#pragma unroll
+        for (int j = 0; j < 32; ++j) b[j & 3] |= v[j] >= bound ? 1u << j : 0u;
+        return ((b[0] | b[1]) | (b[2] | b[3])) & (cnt >= 32 ? ~0u : (1u << max(cnt, 0)) - 1);
+    }
+    static __device__ __forceinline__ int count(float bound, const float (&run)[kRuns], const float (&v)[kRuns][32], int left) {
+        int n = 0;
+#pragma unroll
+        for (int i = 0; i < kRuns; ++i)
+            if (run[i] >= bound) n += __popc(reaching(bound, v[i], left - i * kPieces * 32));
+        return n;
+    }
+    // What reaches the bound is written by ascending column.  Where that is more than there are slots, the bound is raised
+    // by bisection until it leaves k or a few more; among equals at such a bound the first columns are written.
+    __device__ __forceinline__ void take_out(const Row &r, int64_t t, int n0, int last, int piece, const float (&run)[kRuns],
+                                             const float (&v)[kRuns][32]) const {
+        const int64_t at = t * alt.pieces + piece;
+        const float least = from_ordered(r.least), top = fmaxf(fmaxf(run[0], run[1]), fmaxf(run[2], run[3]));
+        int c = 0;
+        if (top >= least) {
+            uint32_t lo = ordered(least), hi = ordered(top);
+            int n = count(least, run, v, last - n0), equals = kRuns * 32;
+            if (n > alt.slots) {
+                while (n > alt.slots && lo < hi) {
+                    const uint32_t mid = lo + (hi - lo + 1) / 2;
+                    const int q = count(from_ordered(mid), run, v, last - n0);
+                    if (q >= alt.k) lo = mid, n = q;
+                    else hi = mid - 1;
+                }
+                if (n > alt.slots) equals = alt.slots - count(from_ordered(lo + 1), run, v, last - n0);
+            }
+            const float bound = from_ordered(lo);
+            Found *to = alt.found + at * alt.slots;
+#pragma unroll
+            for (int i = 0; i < kRuns; ++i)
+                if (run[i] >= bound) {
+                    const int first = n0 + i * kPieces * 32;
+                    const uint32_t in = reaching(bound, v[i], last - first);
+#pragma unroll
+                    for (int j = 0; j < 32; ++j)
+                        if (in >> j & 1 && (v[i][j] > bound || --equals >= 0)) to[c++] = {v[i][j], first + j};
+                }
+        }
+        alt.count[at] = (uint8_t)c;
+        if (top > least) atomicMax(alt.least + (int64_t)(piece % alt.k) * T + t, ordered(top));
+    }
+};
+static_assert(kRuns == 4);
+
+// ---- few tokens (few_logits): a warp keeps its k largest in its lanes, in order;
+// a block is one piece.
+template <int NT, bool VEC, bool TOP>
+__global__ void __launch_bounds__(32 * kFewWarps, kFewBlocks)
+    k_score_few(const uint16_t *x, int64_t stride_x, const uint16_t *w, int64_t stride_w, const int64_t *target, int T,
+                int64_t V, int H, int64_t rows, Stats *part, float *picked, const Alternatives alt) {
+    extern __shared__ float4 xs[];
+    __shared__ Stats sh[kFewWarps][NT];
+    __shared__ Found tops[TOP ? NT : 1][TOP ? kFewWarps * 32 : 1];
+    __shared__ int counts[NT][kFewWarps];
+    let_next_start();
+    after_previous();
+    few_load<NT>(xs, x, stride_x, T, H);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t first = ((int64_t)blockIdx.x * kFewWarps + warp) * rows, last = min(first + rows, V);
+    Stats a[NT];
+    int64_t want[NT];
+    Found mine[NT];
+    float least[NT];  // the k-th of them
+    int have[NT];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+        a[t] = {kNegInf, 0.f, 0.f}, want[t] = t < T ? target[t] : -1;
+        mine[t] = {kNegInf, -1}, least[t] = kNegInf, have[t] = 0;
+    }
+    few_logits<NT, VEC>(xs, w, stride_w, H, first, last, [&](int t, int64_t v, float l) {
+        const float top = fmaxf(a[t].m, l), ref = ref_of(top);
+        const Stats b = rebase(a[t], ref);
+        const float q = not_below((l - ref) * kLog2e, kNoExp), p = exp2_fast(q);
+        a[t] = {top, b.s + p, fmaf(p, q, b.u)};
+        if (lane == 0 && want[t] == v) picked[t] = l;
+        if constexpr (TOP) {
+            // all lanes have the same l; columns ascend, so that an equal one goes behind
+            if (l > least[t] || (have[t] < alt.k && l == l)) {
+                const int to = __popc(__ballot_sync(~0u, lane < have[t] && mine[t].l >= l));
+                const float up = __shfl_up_sync(~0u, mine[t].l, 1);
+                const int un = __shfl_up_sync(~0u, mine[t].n, 1);
+                if (lane > to) mine[t] = {up, un};
+                if (lane == to) mine[t] = {l, (int)v};
+                have[t] = min(have[t] + 1, alt.k);
+                if (have[t] == alt.k) least[t] = __shfl_sync(~0u, mine[t].l, alt.k - 1);
+            }
+        }
+    });
+    if (lane == 0) {
+#pragma unroll
+        for (int t = 0; t < NT; ++t) sh[warp][t] = a[t], counts[t][warp] = have[t];
+    }
+    if constexpr (TOP) {
+#pragma unroll
+        for (int t = 0; t < NT; ++t) tops[t][warp * 32 + lane] = mine[t];
+    }
+    __syncthreads();
+    if (threadIdx.x < T) {  // the warps' parts, in the order of the warps
+        const int t = threadIdx.x;
+        Stats all = sh[0][t];
+        for (int i = 1; i < kFewWarps; ++i) all = add(all, sh[i][t]);
+        part[(int64_t)blockIdx.x * T + t] = all;
+    }
+    if constexpr (TOP) {
+        // each of the warps' alternatives finds its place among all of them
+        for (int t = 0; t < T; ++t) {
+            int total = 0;
+#pragma unroll
+            for (int i = 0; i < kFewWarps; ++i) total += counts[t][i];
+            const int64_t at = (int64_t)t * alt.pieces + blockIdx.x;
+            if (threadIdx.x == 0) alt.count[at] = (uint8_t)min(total, alt.k);
+            if (lane >= counts[t][warp]) continue;
+            const Found f = tops[t][warp * 32 + lane];
+            int place = 0;
+            for (int i = 0; i < kFewWarps; ++i)
+                for (int j = 0; j < counts[t][i]; ++j) place += before(tops[t][i * 32 + j], f);
+            if (place < alt.k) alt.found[at * alt.slots + place] = f;
+        }
+    }
+}
+
+// ---- the join: 8 tokens a block, 32 lanes along the pieces of each
+
+constexpr int kKept = 256;  // alternatives that a warp sorts at a time
+
+// Of the n entries a warp holds in shared memory the first k, in order.
+__device__ __forceinline__ int sort_kept(Found *kept, int n, int k, int lane) {
+    Found f[kKept / 32];
+    int place[kKept / 32];
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < kKept / 32; ++i) f[i] = kept[i * 32 + lane], place[i] = 0;
+    for (int j = 0; j < n; ++j) {
+        const Found g = kept[j];
+#pragma unroll
+        for (int i = 0; i < kKept / 32; ++i) place[i] += before(g, f[i]);
+    }
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < kKept / 32; ++i)
+        if (i * 32 + lane < n && place[i] < k) kept[place[i]] = f[i];
+    __syncwarp();
+    return min(n, k);
+}
+
+struct JoinArgs {
+    const Stats *part;
+    const float *picked;
+    const int64_t *target;
+    int64_t pieces, T, V;
+    float *logp, *lse, *entropy, *top_logp;
+    int64_t *top_index;
+};
+
+template <bool TOP>
+__global__ void __launch_bounds__(256) k_score_join(const JoinArgs a, const Alternatives alt) {
+    after_previous();
+    __shared__ Stats sh[8][33];
+    __shared__ Found keep[TOP ? 8 : 1][TOP ? kKept : 1];
+    // 8 neighbouring tokens are read together; 32 runs of pieces for each
+    const int col = threadIdx.x & 7, run = threadIdx.x >> 3;
+    const int64_t t = (int64_t)blockIdx.x * 8 + col;
+    Stats x{kNegInf, 0.f, 0.f};
+    if (t < a.T) {
+        constexpr int kAhead = 8;
+        for (int64_t i = run; i < a.pieces; i += 32 * kAhead) {
+            Stats p[kAhead];
+#pragma unroll
+            for (int j = 0; j < kAhead; ++j) {
+                const int64_t k = i + 32 * j;
+                p[j] = k < a.pieces ? a.part[k * a.T + t] : Stats{kNegInf, 0.f, 0.f};
+            }
+            float top = x.m;
+#pragma unroll
+            for (int j = 0; j < kAhead; ++j) top = fmaxf(top, p[j].m);
+            const float ref = ref_of(top);
+            x = rebase(x, ref);
+#pragma unroll
+            for (int j = 0; j < kAhead; ++j) {
+                const Stats y = rebase(p[j], ref);
+                x.s += y.s, x.u += y.u;
+            }
+            x.m = top;
+        }
+    }
+    sh[col][run] = x;
+    __syncthreads();
+    const int lane = threadIdx.x & 31, row = threadIdx.x >> 5;
+    const int64_t u = (int64_t)blockIdx.x * 8 + row;
+    x = sh[row][lane];
+    float m = x.m;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
+    const float ref = ref_of(m);
+    x = rebase(x, ref);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+        x.s += __shfl_xor_sync(~0u, x.s, o);
+        x.u += __shfl_xor_sync(~0u, x.u, o);
+    }
+    if (u >= a.T) return;
+    const float logs = logf(x.s), lse = ref + logs;
+    if (lane == 0) {
+        if (a.lse) a.lse[u] = lse;
+        if (a.entropy) a.entropy[u] = logs - x.u * kLn2 / x.s;
+        if (a.logp) a.logp[u] = inside(a.target[u], a.V) ? a.picked[u] - lse : 0.f;
+    }
+    if constexpr (TOP) {
+        const int k = alt.k, slots = alt.slots;
+        const uint8_t *count = alt.count + u * a.pieces;
+        const Found *found = alt.found + u * a.pieces * slots;
+        // k different logits reach the k-th largest of these; and the classes' bound
+        float best = kNegInf;
+        bool any = false;
+#pragma unroll 4
+        for (int64_t p = lane; p < a.pieces; p += 32)
+            if (count[p]) best = fmaxf(best, found[p * slots].l), any = true;
+        int place = 0;
+        for (int i = 0; i < 32; ++i) {
+            const float b = __shfl_sync(~0u, best, i);
+            place += __shfl_sync(~0u, (int)any, i) && (b > best || (b == best && i < lane));
+        }
+        const uint32_t kth = __ballot_sync(~0u, any && place == k - 1);
+        float least = kth ? __shfl_sync(~0u, best, __ffs(kth) - 1) : kNegInf;
+        if (alt.least)
+            least = fmaxf(least, from_ordered(__reduce_min_sync(~0u, lane < k ? alt.least[lane * a.T + u] : ~0u)));
+        Found *mine = keep[row];
+        int n = 0;
+        for (int64_t p0 = 0; p0 < a.pieces; p0 += 32) {
+            const int64_t p = p0 + lane;
+            int c = p < a.pieces ? count[p] : 0;
+            for (int e = 0; __any_sync(~0u, e < c); ++e) {
+                Found f{kNaN, 0};
+                if (e < c) f = found[p * slots + e];
+                const bool is = f.l >= least;
+                if (!is && !alt.least) c = 0;  // nor are those behind it
+                const uint32_t in = __ballot_sync(~0u, is);
+                if (is) mine[n + __popc(in & ((1u << lane) - 1))] = f;
+                n += __popc(in);
+                if (n > kKept - 32) {
+                    n = sort_kept(mine, n, k, lane);
+                    least = fmaxf(least, mine[k - 1].l);
+                }
+            }
+        }
+        n = sort_kept(mine, n, k, lane);
+        if (lane < k) {
+            // a row with fewer numbers than that has a NaN
+            a.top_logp[u * k + lane] = lane < n ? mine[lane].l - lse : kNaN;
+            a.top_index[u * k + lane] = lane < n ? mine[lane].n : -1;
+        }
+    }
+}
+
+__global__ void __launch_bounds__(256) k_no_bounds(uint32_t *least, int64_t n) {
+    let_next_start();
+    after_previous();
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (i < n) least[i] = 0;
+}
+
+// Bytes of a few-token block's own shared memory beside its tokens.
+int few_own(bool top) {
+    return kFewWarps * kFewTokens * ((int)sizeof(Stats) + 4) + (top ? kFewTokens * kFewWarps * 32 * (int)sizeof(Found) : 0);
+}
+
+// Tokens are taken so many at a time that what their pieces leave takes about
+// kLeftBytes (256 tokens at least): with 20 alternatives a piece leaves up to
+// 205 bytes of a token, which 131072 columns make 210 KB.
+constexpr int64_t kLeftBytes = 1ll << 30;
+constexpr int kMoreSlots = 4;
+
+struct ScoreSpace {
+    Aligned x, w;
+    Stats *part;
+    float *picked;
+    Alternatives alt;
+    bool few;
+    int64_t rows, each;  // rows of w to a warp of few tokens; tokens at a time
+    size_t bytes;
+};
+int64_t pieces_of(int64_t T, int64_t V, int64_t H) { return kPieces * plan_product(T, V, H, false, false).nt; }
+ScoreSpace score_space(void *ws, const uint16_t *x, int64_t sx, const uint16_t *w, int64_t sw, int64_t T, int64_t V,
+                       int64_t H, int k) {
+    Carve c{static_cast<unsigned char *>(ws)};
+    ScoreSpace s{};
+    s.few = few_tokens(T, H);
+    s.alt.k = k, s.alt.slots = s.few ? k : k + kMoreSlots;
+    s.each = T;
+    int64_t pieces;
+    if (s.few) {
+        s.rows = few_rows(T, V, H, few_own(k > 0));
+        pieces = ceil_div(V, s.rows * kFewWarps);
+    } else {
+        s.x = aligned(c, x, sx, T, H, ceil_div(V, 256));
+        s.w = aligned(c, w, sw, V, H, ceil_div(T, 256));
+        pieces = pieces_of(T, V, H);
+        const int64_t left = pieces * ((int64_t)sizeof(Stats) + (k ? 1 + s.alt.slots * (int64_t)sizeof(Found) : 0));
+        const int64_t most = std::max<int64_t>(kLeftBytes / left, 256);
+        if (T > most) {
+            s.each = std::min(T, round_up(ceil_div(T, ceil_div(T, most)), 256));
+            pieces = std::max(pieces_of(s.each, V, H), pieces_of((T - 1) % s.each + 1, V, H));
+        }
+    }
+    s.alt.pieces = pieces;  // the most
+    s.part = c.take<Stats>(pieces * s.each);
+    s.picked = c.take<float>(s.each);
+    if (k) {
+        s.alt.found = c.take<Found>(pieces * s.each * s.alt.slots);
+        s.alt.count = c.take<uint8_t>(pieces * s.each);
+        if (!s.few) s.alt.least = c.take<uint32_t>(k * s.each);
+    }
+    s.bytes = c.used;
+    return s;
+}
+
+template <bool TOP>
+int score(const ScoreSpace &s, const uint16_t *x, int64_t sx, const uint16_t *w, int64_t sw, const int64_t *target,
+          int64_t T, int64_t V, int64_t H, float *logp, float *lse, float *entropy, float *top_logp, int64_t *top_index,
+          cudaStream_t stream) {
+    const int k = s.alt.k;
+    int rc = PP_OK;
+    if (!s.few) {
+        rc = copy_if(s.x, x, sx, T, H, stream);
+        if (rc == PP_OK) rc = copy_if(s.w, w, sw, V, H, stream);
+    }
+    for (int64_t t0 = 0; t0 < T && rc == PP_OK; t0 += s.each) {
+        const int64_t n = std::min(s.each, T - t0);
+        Alternatives alt = s.alt;
+        if (s.few) {
+            const bool vec = rows_aligned(w, sw, V, 2);
+            const auto kernel = n == 1 ? (vec ? k_score_few<1, true, TOP> : k_score_few<1, false, TOP>)
+                                       : (vec ? k_score_few<2, true, TOP> : k_score_few<2, false, TOP>);
+            static std::atomic<uint64_t> ready[4];
+            rc = allow_smem(kernel, kFewFloats * 4, ready[2 * (n - 1) + vec]);
+            if (rc == PP_OK)
+                rc = launch_after(kernel, alt.pieces, 32 * kFewWarps, (int)(n * ceil_div(H, 8) * 32), stream, 1, x, sx, w, sw,
+                                  target, (int)n, V, (int)H, s.rows, s.part, s.picked, alt);
+        } else {
+            const ProductPlan plan = plan_product(n, V, H, false, false);
+            alt.pieces = kPieces * plan.nt;
+            if (TOP) rc = launch_after(k_no_bounds, ceil_div(n * k, 256), 256, 0, stream, 1, alt.least, n * k);
+            if (rc == PP_OK)
+                rc = launch_product<kRowsK, kRowsK>(in_rows(s.x.at.p + t0 * s.x.at.ld, s.x.at.ld), s.w.at, n, V, H,
+                                                    ScoreEpi<TOP>{target + t0, n, V, s.part, s.picked, alt}, plan, stream);
+        }
+        const auto from = [&](auto *p, int64_t each) { return p ? p + t0 * each : p; };
+        if (rc == PP_OK)
+            rc = launch_after(k_score_join<TOP>, ceil_div(n, 8), 256, 0, stream, 1,
+                              JoinArgs{s.part, s.picked, target + t0, alt.pieces, n, V, from(logp, 1), from(lse, 1),
+                                       from(entropy, 1), from(top_logp, k), from(top_index, k)},
+                              alt);
+    }
+    return rc;
+}
+
+}  // namespace
+}  // namespace pps
+
+using namespace pps;
+
+extern "C" size_t pp_stage_score_forward_workspace(const uint16_t *x, int64_t stride_x, const uint16_t *w,
+                                                   int64_t stride_w, int64_t T, int64_t V, int64_t H, int64_t top) {
+    if (T < 1 || V < 1 || H < 1 || top < 0 || top > kMaxTop) return 0;
+    return score_space(nullptr, x, stride_x, w, stride_w, T, V, H, (int)top).bytes;
+}
+
+extern "C" int pp_stage_score_forward(const uint16_t *x, int64_t stride_x, const uint16_t *w, int64_t stride_w,
+                                      const int64_t *target, int64_t T, int64_t V, int64_t H, int64_t top, float *logp,
+                                      float *lse, float *entropy, float *top_logp, int64_t *top_index, void *workspace,
+                                      size_t workspace_bytes, cudaStream_t stream) {
+    const int rc = check_head(x, stride_x, w, stride_w, target, T, V, H);
+    if (rc != PP_OK) return rc;
+    if (top < 0 || top > V) return PP_ERR_ARG;
+    if (top > kMaxTop) return PP_ERR_SIZE;
+    if (T == 0) return PP_OK;
+    if ((!logp && !lse && !entropy && !top) || (((uintptr_t)logp | (uintptr_t)lse | (uintptr_t)entropy) & 3)) return PP_ERR_ARG;
+    if (top && (!top_logp || !top_index || ((uintptr_t)top_logp & 3) || ((uintptr_t)top_index & 7))) return PP_ERR_ARG;
+    const ScoreSpace s = score_space(workspace, x, stride_x, w, stride_w, T, V, H, (int)top);
+    if (!workspace || ((uintptr_t)workspace & (kStageAlign - 1)) || workspace_bytes < s.bytes) return PP_ERR_ARG;
+    return (top ? score<true> : score<false>)(s, x, stride_x, w, stride_w, target, T, V, H, logp, lse, entropy, top_logp,
+                                              top_index, stream);
+}

@@ -1,0 +1,540 @@
+// stage_step.cu -- the AdamW step over all tensors of a stage in one launch,
+// moments in 32 or in 8 bits, and the norm of its gradients.
+//
+//   m = b1 m + (1 - b1) g      v = b2 v + (1 - b2) g^2      (g clipped before)
+//   p = p (1 - lr decay) - lr / (1 - b1^t) * m / (sqrt(v / (1 - b2^t)) + eps)
+// Every element is read and written once, so memory bounds it: 34 bytes an
+// element with 32-bit parameters, moments and gradients and a 16-bit copy, 18
+// with the moments in 8 bits.
+//
+// Moments in 8 bits.  64 consecutive elements share an exponent, and an element
+// keeps 4 significant bits and its exponent relative to the block's: m a sign and
+// 15 binades, v 31 binades (its root spans 15.5).  So a code is the number's
+// float bits from the 20th on, less those of the window's start: encoding and
+// decoding are an addition and a shift.  v matters by its ratio to m, so it is
+// never held as 0 unless it is: a v below the window is held at its start,
+// which makes a step smaller, never larger.  An average that changes by
+// 1 - b2 a step does not move in 4 bits rounded to nearest; with a seed a value
+// is rounded up with the probability of what is cut off, so that it moves as it
+// should on average.
+//
+// The random bits are a function of seed, step and place (random_key,
+// random_bits), so that a step can be taken again with the same result.
+#include <cmath>
+
+#include "stage_common.cuh"
+
+namespace pps {
+namespace {
+
+constexpr int kMoments = PP_STAGE_BLOCK;  // elements that share an exponent
+constexpr int kThreads = 256, kUnit = 8, kChunk = kThreads * kUnit;
+
+// What the steps of one call share, computed on the device: its first kernel
+// reads the step's number and the norm.
+struct StepNow {
+    float size, root, clip, lr;  // lr / (1 - b1^t), 1 / sqrt(1 - b2^t), the gradients' factor, lr
+    uint32_t key;                // of the random bits
+    int go;                      // 0: the norm is not a finite number, nothing is touched
+};
+
+__device__ __forceinline__ uint32_t mix(uint32_t x) {
+    x = (x ^ x >> 16) * 0x243F6A89u;
+    x = (x ^ x >> 15) * 0x85A308D3u;
+    return x ^ x >> 16;
+}
+__device__ __forceinline__ uint32_t random_key(uint64_t seed, int64_t step) {
+    return mix((uint32_t)step ^ mix((uint32_t)seed ^ mix((uint32_t)(seed >> 32))));
+}
+__device__ __forceinline__ uint32_t block_key(uint32_t key, uint32_t block) { return mix(block ^ key); }
+// 16 bits for m (the low ones) and 16 for v, of element i of a block.
+__device__ __forceinline__ uint32_t random_bits(uint32_t block_key, uint32_t i) {
+    uint32_t x = block_key + i * 0x9E3779B1u;
+    x = (x ^ x >> 15) * 0x13198A2Fu;
+    x = (x ^ x >> 12) * 0xA4093823u;
+    return x ^ x >> 15;
+}
+// 16 more, for the parameter.
+__device__ __forceinline__ uint32_t more_bits(uint32_t bits) { return bits * 0x299F31D1u >> 16; }
+
+constexpr int kWindowM = 15, kWindowV = 31, kBlockNaN = 255;
+constexpr uint32_t kNearest = 0x80000u;  // half of what is cut off
+
+// The block's exponent, from the bits of its largest magnitude: that of its next
+// larger number of 4 significant bits, so that no rounding leaves the window.
+__device__ __forceinline__ int moments_exp(uint32_t largest) {
+    if (largest >= 0x7F800000u) return kBlockNaN;
+    return min((int)((largest + 0xFFFFFu) >> 23), 254);
+}
+// What a magnitude's code starts to count from.
+__device__ __forceinline__ int window_of(int exp, int window) { return (exp - window) * 8; }
+__device__ __forceinline__ uint32_t encode(uint32_t magnitude, uint32_t r, int from, int least, int most) {
+    return (uint32_t)min(max((int)((magnitude + r) >> 20) - from, least), most);
+}
+__device__ __forceinline__ float decode(uint32_t code, int from) {
+    return code ? __uint_as_float((uint32_t)max((int)code + from, 0) << 20) : 0.f;
+}
+
+__device__ __forceinline__ float root(float x) {
+    float y;
+    asm("sqrt.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// 8 consecutive elements.
+template <bool VEC>
+__device__ __forceinline__ void load(const float *p, int n, float (&v)[8]) {
+    if (VEC) {
+        asm volatile("ld.global.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                     : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7])
+                     : "l"(p));
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = j < n ? p[j] : 0.f;
+    }
+}
+template <bool VEC>
+__device__ __forceinline__ void load(const uint16_t *p, int n, float (&v)[8]) {
+    if (VEC) {
+        const uint4 q = *reinterpret_cast<const uint4 *>(p);
+        const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[2 * j] = bf16_lo(w[j]), v[2 * j + 1] = bf16_hi(w[j]);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = j < n ? bf16_to_f32(p[j]) : 0.f;
+    }
+}
+template <bool VEC>
+__device__ __forceinline__ void store(float *p, int n, const float (&v)[8]) {
+    if (VEC) {
+        asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(v[0]), "f"(v[1]), "f"(v[2]),
+                     "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
+                     : "memory");
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (j < n) p[j] = v[j];
+    }
+}
+template <bool VEC>
+__device__ __forceinline__ void store(uint16_t *p, int n, const float (&v)[8]) {
+    if (VEC) {
+        *reinterpret_cast<uint4 *>(p) = make_uint4(f32_to_bf16x2(v[0], v[1]), f32_to_bf16x2(v[2], v[3]),
+                                                   f32_to_bf16x2(v[4], v[5]), f32_to_bf16x2(v[6], v[7]));
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (j < n) p[j] = f32_to_bf16(v[j]);
+    }
+}
+
+// A tensor of the step, as the kernels have it.
+struct Entry {
+    void *p;
+    const void *g;
+    uint16_t *copy;
+    int64_t n;
+    uint32_t at;     // its first block of moments
+    uint32_t first;  // its first chunk among the launch's
+    float decay;
+    int vec;  // p, g and copy may be read 8 elements at a time
+};
+// So many tensors to a launch: they are the kernel's parameters, 1.6 or 31 KB.
+constexpr int kFewEntries = 32, kManyEntries = 640;
+template <int N>
+struct Entries {
+    int count;
+    Entry e[N];
+};
+static_assert(sizeof(Entries<kManyEntries>) + 256 < 32764);
+
+template <int N>
+__device__ __forceinline__ const Entry &entry_of(const Entries<N> &t, uint32_t chunk) {
+    int lo = 0, hi = t.count;  // the last whose first chunk is no later
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) / 2;
+        if (t.e[mid].first <= chunk) lo = mid;
+        else hi = mid;
+    }
+    return t.e[lo];
+}
+
+struct Moments {
+    void *m, *v;
+    uint8_t *m_exp, *v_exp;  // null: 32 bits
+};
+struct Rates {
+    float b1, c1, b2, c2, eps;  // c1 = 1 - b1, c2 = 1 - b2
+    int random;
+};
+
+// 8 elements of one tensor, from element i on, of which n exist; held: whether
+// they have moments (whole blocks, past the tensor's end as well).  In 8 bits the
+// 8 lanes of an aligned group have one block, and all lanes of a warp are here.
+template <class P, class G, bool SMALL, bool VEC>
+__device__ __forceinline__ void step_unit(const Entry &e, int64_t i, int n, bool held, const Moments &mo, const Rates &r,
+                                          const StepNow &now) {
+    float p[8], g[8], m[8], v[8];
+    const int64_t at = (int64_t)e.at * kMoments + i;
+    const uint32_t block = e.at + (uint32_t)(i / kMoments);
+    load<VEC>(static_cast<const P *>(e.p) + i, n, p);
+    load<VEC>(static_cast<const G *>(e.g) + i, n, g);
+    if constexpr (SMALL) {
+        uint2 cm = make_uint2(0, 0), cv = make_uint2(0, 0);
+        int em = 0, ev = 0;
+        if (held) {
+            cm = *reinterpret_cast<const uint2 *>(static_cast<const uint8_t *>(mo.m) + at);
+            cv = *reinterpret_cast<const uint2 *>(static_cast<const uint8_t *>(mo.v) + at);
+            em = mo.m_exp[block], ev = mo.v_exp[block];
+        }
+        const int fm = window_of(em, kWindowM), fv = window_of(ev, kWindowV);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const uint32_t bm = (j < 4 ? cm.x : cm.y) >> (8 * (j & 3)) & 255, bv = (j < 4 ? cv.x : cv.y) >> (8 * (j & 3)) & 255;
+            m[j] = em == kBlockNaN ? __uint_as_float(0x7FC00000u)
+                                   : __uint_as_float(__float_as_uint(decode(bm & 127, fm)) | (bm & 128) << 24);
+            v[j] = ev == kBlockNaN ? __uint_as_float(0x7FC00000u) : decode(bv, fv);
+        }
+    } else {
+        load<true>(static_cast<const float *>(mo.m) + at, 8, m);
+        load<true>(static_cast<const float *>(mo.v) + at, 8, v);
+    }
+    const float shrink = -now.lr * e.decay;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        if (j >= n) g[j] = m[j] = v[j] = 0.f;  // nothing is kept past the tensor's end
+        const float x = __fmul_rn(g[j], now.clip);
+        m[j] = __fadd_rn(__fmul_rn(r.b1, m[j]), __fmul_rn(r.c1, x));
+        v[j] = __fadd_rn(__fmul_rn(r.b2, v[j]), __fmul_rn(r.c2, __fmul_rn(x, x)));
+        p[j] = fmaf(p[j], shrink, p[j]) - now.size * __fdividef(m[j], fmaf(root(v[j]), now.root, r.eps));
+    }
+    [[maybe_unused]] uint32_t bits[8];
+    constexpr bool kRound = sizeof(P) == 2;
+    if ((SMALL || kRound) && r.random) {
+        const uint32_t key = block_key(now.key, block);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) bits[j] = random_bits(key, (uint32_t)(i % kMoments) + j);
+    }
+    if constexpr (SMALL) {
+        uint32_t tm = 0, tv = 0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            tm = max(tm, __float_as_uint(m[j]) & 0x7FFFFFFFu);
+            tv = max(tv, __float_as_uint(v[j]) & 0x7FFFFFFFu);
+        }
+#pragma unroll
+        for (int o = 4; o; o >>= 1) {
+            tm = max(tm, __shfl_xor_sync(~0u, tm, o));
+            tv = max(tv, __shfl_xor_sync(~0u, tv, o));
+        }
+        const int em = moments_exp(tm), ev = moments_exp(tv), fm = window_of(em, kWindowM), fv = window_of(ev, kWindowV);
+        uint32_t wm[2] = {}, wv[2] = {};
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const uint32_t rm = r.random ? ((bits[j] & 0xFFFFu) << 4) + 8 : kNearest;
+            const uint32_t rv = r.random ? (bits[j] >> 16 << 4) + 8 : kNearest;
+            const uint32_t um = __float_as_uint(m[j]), uv = __float_as_uint(v[j]);
+            uint32_t a = encode(um & 0x7FFFFFFFu, rm, fm, 0, 127) | um >> 24 & 128;
+            uint32_t b = uv ? encode(uv, rv, fv, 1, 255) : 0;
+            if (um == 0x80000000u) a = 0;
+            wm[j >> 2] |= a << (8 * (j & 3)), wv[j >> 2] |= b << (8 * (j & 3));
+        }
+        if (em == kBlockNaN) wm[0] = wm[1] = 0;
+        if (ev == kBlockNaN) wv[0] = wv[1] = 0;
+        if (held) {
+            *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(mo.m) + at) = make_uint2(wm[0], wm[1]);
+            *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(mo.v) + at) = make_uint2(wv[0], wv[1]);
+            if (i % kMoments == 0) mo.m_exp[block] = (uint8_t)em, mo.v_exp[block] = (uint8_t)ev;
+        }
+    } else {
+        store<true>(static_cast<float *>(mo.m) + at, 8, m);
+        store<true>(static_cast<float *>(mo.v) + at, 8, v);
+    }
+    if (kRound && r.random) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            // up with the probability of what is cut off; an infinity or a NaN stays what it is
+            const uint32_t b = __float_as_uint(p[j]);
+            if ((b & 0x7F800000u) != 0x7F800000u) p[j] = __uint_as_float((b + more_bits(bits[j])) & 0xFFFF0000u);
+        }
+    }
+    store<VEC>(static_cast<P *>(e.p) + i, n, p);
+    if (e.copy) store<VEC>(e.copy + i, n, p);
+}
+
+template <class P, class G, bool SMALL, int N>
+__global__ void __launch_bounds__(kThreads) k_step(const __grid_constant__ Entries<N> t, const Moments mo, const Rates r,
+                                                   const StepNow *at) {
+    let_next_start();
+    const Entry &e = entry_of(t, blockIdx.x);
+    const int64_t i = (int64_t)(blockIdx.x - e.first) * kChunk + threadIdx.x * kUnit;
+    after_previous();
+    const StepNow now = *at;
+    if (!now.go) return;
+    const int n = i >= e.n ? 0 : e.n - i < kUnit ? (int)(e.n - i) : kUnit;
+    const bool held = i < (e.n + kMoments - 1) / kMoments * kMoments;
+    bool wide = e.vec && n == kUnit;
+    if constexpr (SMALL) wide = __all_sync(~0u, wide);  // a warp goes one way: its lanes shuffle
+    else if (!held) return;
+    if (wide) step_unit<P, G, SMALL, true>(e, i, n, held, mo, r, now);
+    else step_unit<P, G, SMALL, false>(e, i, n, held, mo, r, now);
+}
+
+// The step's number goes up, and all that depends on it is computed, in 64 bits.
+__global__ void k_step_begin(int64_t *step, const float *lr_at, double lr, double b1, double b2, const float *norm,
+                             double max_norm, uint64_t seed, StepNow *now) {
+    let_next_start();
+    after_previous();
+    const float nrm = norm ? *norm : 0.f;
+    const int64_t t = *step + 1;
+    const double rate = lr_at ? *lr_at : lr;
+    const double bias = threadIdx.x ? 1 / sqrt(1 - pow(b2, (double)t)) : rate / (1 - pow(b1, (double)t));
+    const double other = __shfl_down_sync(3u, bias, 1);
+    if (threadIdx.x) return;
+    StepNow s;
+    s.go = isfinite(nrm);
+    s.size = (float)bias, s.root = (float)other, s.lr = (float)rate;
+    s.clip = nrm > max_norm ? (float)(max_norm / nrm) : 1.f;
+    s.key = random_key(seed, t);
+    *now = s;
+    if (s.go) *step = t;
+}
+
+// ---- the norm: a block's sum of squares, then all blocks'
+
+constexpr int kNormThreads = 512;
+
+template <class G, int N>
+__global__ void __launch_bounds__(kNormThreads) k_norm(const __grid_constant__ Entries<N> t, int64_t chunk, double *part) {
+    __shared__ double sh[kNormThreads / 32];
+    let_next_start();
+    const Entry &e = entry_of(t, blockIdx.x);
+    const int64_t from = (int64_t)(blockIdx.x - e.first) * chunk, to = min(from + chunk, e.n);
+    const G *g = static_cast<const G *>(e.g);
+    after_previous();
+    constexpr int kEach = kNormThreads * kUnit;
+    float s[4] = {};
+    int64_t i = from + threadIdx.x * kUnit;
+    if (e.vec) {
+        for (; i + kUnit + kEach <= to; i += 2 * kEach) {
+            float a[8], b[8];
+            load<true>(g + i, 8, a);
+            load<true>(g + i + kEach, 8, b);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) s[j & 3] = fmaf(a[j], a[j], fmaf(b[j], b[j], s[j & 3]));
+        }
+    }
+    for (; i < to; i += kEach) {
+        float a[8];
+        load<false>(g + i, to - i < kUnit ? (int)(to - i) : kUnit, a);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) s[j & 3] = fmaf(a[j], a[j], s[j & 3]);
+    }
+    double x = (double)(s[0] + s[1]) + (double)(s[2] + s[3]);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(~0u, x, o);
+    if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = x;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        x = 0;
+        for (int k = 0; k < kNormThreads / 32; ++k) x += sh[k];
+        part[blockIdx.x] = x;
+    }
+}
+
+__global__ void __launch_bounds__(1024) k_norm_join(const double *part, int64_t n, float *norm) {
+    __shared__ double sh[32];
+    let_next_start();
+    after_previous();
+    double x = 0;
+    for (int64_t i = threadIdx.x; i < n; i += 1024) x += part[i];
+#pragma unroll
+    for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(~0u, x, o);
+    if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = x;
+    __syncthreads();
+    if (threadIdx.x >= 32) return;
+    x = sh[threadIdx.x];
+#pragma unroll
+    for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(~0u, x, o);
+    if (threadIdx.x == 0) *norm = (float)sqrt(x);
+}
+
+// What moments in 8 bits stand for, as bf16 (exactly): 8 elements of both a thread.
+__global__ void __launch_bounds__(kThreads) k_moments(const Moments mo, int64_t n, uint16_t *m, uint16_t *v) {
+    let_next_start();
+    after_previous();
+    const int64_t i = ((int64_t)blockIdx.x * kThreads + threadIdx.x) * kUnit;
+    if (i >= n) return;
+    const uint2 cm = *reinterpret_cast<const uint2 *>(static_cast<const uint8_t *>(mo.m) + i);
+    const uint2 cv = *reinterpret_cast<const uint2 *>(static_cast<const uint8_t *>(mo.v) + i);
+    const int em = mo.m_exp[i / kMoments], ev = mo.v_exp[i / kMoments];
+    const int fm = window_of(em, kWindowM), fv = window_of(ev, kWindowV);
+    uint32_t a[8], b[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const uint32_t bm = (j < 4 ? cm.x : cm.y) >> (8 * (j & 3)) & 255, bv = (j < 4 ? cv.x : cv.y) >> (8 * (j & 3)) & 255;
+        a[j] = em == kBlockNaN ? 0x7FC0u : __float_as_uint(decode(bm & 127, fm)) >> 16 | (bm & 128) << 8;
+        b[j] = ev == kBlockNaN ? 0x7FC0u : __float_as_uint(decode(bv, fv)) >> 16;
+    }
+    *reinterpret_cast<uint4 *>(m + i) = make_uint4(a[0] | a[1] << 16, a[2] | a[3] << 16, a[4] | a[5] << 16, a[6] | a[7] << 16);
+    *reinterpret_cast<uint4 *>(v + i) = make_uint4(b[0] | b[1] << 16, b[2] | b[3] << 16, b[4] | b[5] << 16, b[6] | b[7] << 16);
+}
+
+// ---- host side
+
+bool aligned_to(const void *p, uintptr_t bytes) { return ((uintptr_t)p & (bytes - 1)) == 0; }
+
+bool bad_tensor(const pp_stage_tensor &t, bool step) {
+    if (t.n < 0 || (t.p_float & ~1) || (t.g_float & ~1)) return true;
+    if (t.n == 0) return false;
+    if (!t.g || !aligned_to(t.g, t.g_float ? 4 : 2)) return true;
+    if (!step) return false;
+    return !t.p || !aligned_to(t.p, t.p_float ? 4 : 2) || (t.copy && (!t.p_float || !aligned_to(t.copy, 2))) || t.at < 0 ||
+           t.at % kMoments || !(std::fabs(t.decay) <= 3e38f);
+}
+
+// Hands the tensors that `want` picks to `launch(table, chunks)`, as many at a
+// time as a table holds; chunk: elements of a block.
+template <class Want, class Launch>
+int in_tables(const pp_stage_tensor *list, int64_t count, int64_t chunk, const Want &want, const Launch &launch) {
+    static thread_local Entries<kManyEntries> many;  // 31 KB
+    int64_t i = 0;
+    while (i < count) {
+        many.count = 0;
+        int64_t chunks = 0;
+        for (; i < count && many.count < kManyEntries; ++i) {
+            const pp_stage_tensor &t = list[i];
+            if (t.n == 0 || !want(t)) continue;
+            const int64_t c = ceil_div(t.n, chunk);
+            if (chunks + c > 0x7FFFFFFF) break;  // the rest in another launch
+            const bool vec = aligned_to(t.p, t.p_float ? 32 : 16) && aligned_to(t.g, t.g_float ? 32 : 16) && aligned_to(t.copy, 16);
+            many.e[many.count++] = {t.p, t.g, t.copy, t.n, (uint32_t)(t.at / kMoments), (uint32_t)chunks, t.decay, vec};
+            chunks += c;
+        }
+        if (many.count == 0) continue;
+        int rc;
+        if (many.count <= kFewEntries) {
+            Entries<kFewEntries> few;
+            few.count = many.count;
+            for (int j = 0; j < many.count; ++j) few.e[j] = many.e[j];
+            rc = launch(few, chunks);
+        } else {
+            rc = launch(many, chunks);
+        }
+        if (rc != PP_OK) return rc;
+    }
+    return PP_OK;
+}
+
+template <class P, class G, bool SMALL>
+int step_all(const pp_stage_tensor *list, int64_t count, const Moments &mo, const Rates &r, const StepNow *now,
+             cudaStream_t stream) {
+    return in_tables(
+        list, count, kChunk,
+        [](const pp_stage_tensor &t) { return t.p_float == (sizeof(P) == 4) && t.g_float == (sizeof(G) == 4); },
+        [&]<int N>(const Entries<N> &t, int64_t chunks) {
+            return launch_after(k_step<P, G, SMALL, N>, chunks, kThreads, 0, stream, 1, t, mo, r, now);
+        });
+}
+
+// Elements to a block of the norm: about 8 blocks to an SM, 16 K elements at least.
+int64_t norm_chunk(const pp_stage_tensor *list, int64_t count) {
+    int64_t n = 0;
+    for (int64_t i = 0; i < count; ++i) n += list[i].n;
+    return std::max<int64_t>(round_up(ceil_div(n, (int64_t)sm_count() * 8), 2 * kNormThreads * kUnit), 16384);
+}
+int64_t norm_blocks(const pp_stage_tensor *list, int64_t count) {
+    const int64_t chunk = norm_chunk(list, count);
+    int64_t n = 0;
+    for (int64_t i = 0; i < count; ++i) n += ceil_div(list[i].n, chunk);
+    return n;
+}
+
+bool bad_list(const pp_stage_tensor *list, int64_t count, bool step) {
+    if (count < 0 || (count > 0 && !list)) return true;
+    for (int64_t i = 0; i < count; ++i)
+        if (bad_tensor(list[i], step)) return true;
+    return false;
+}
+bool too_long(const pp_stage_tensor *list, int64_t count) {
+    for (int64_t i = 0; i < count; ++i)
+        if (list[i].n > PP_STAGE_MAX_ELEMENTS) return true;
+    return count > PP_STAGE_MAX_TENSORS;
+}
+
+}  // namespace
+}  // namespace pps
+
+using namespace pps;
+
+extern "C" size_t pp_stage_grad_norm_workspace(const pp_stage_tensor *list, int64_t count) {
+    if (bad_list(list, count, false) || too_long(list, count)) return 0;
+    return stage_align((size_t)norm_blocks(list, count) * sizeof(double));
+}
+
+extern "C" int pp_stage_grad_norm(const pp_stage_tensor *list, int64_t count, float *norm, void *workspace,
+                                  size_t workspace_bytes, cudaStream_t stream) {
+    if (bad_list(list, count, false) || !norm || !aligned_to(norm, 4)) return PP_ERR_ARG;
+    if (too_long(list, count)) return PP_ERR_SIZE;
+    const int64_t chunk = norm_chunk(list, count), blocks = norm_blocks(list, count);
+    if (blocks && (!workspace || !aligned_to(workspace, kStageAlign) || workspace_bytes < blocks * sizeof(double))) return PP_ERR_ARG;
+    double *part = static_cast<double *>(workspace);
+    const auto all = [&]<class G>(const G *) {
+        return in_tables(
+            list, count, chunk, [](const pp_stage_tensor &t) { return t.g_float == (sizeof(G) == 4); },
+            [&]<int N>(Entries<N> t, int64_t chunks) {
+                for (int i = 0; i < t.count; ++i) t.e[i].vec = aligned_to(t.e[i].g, sizeof(G) == 4 ? 32 : 16);
+                const int rc = launch_after(k_norm<G, N>, chunks, kNormThreads, 0, stream, 1, t, chunk, part);
+                part += chunks;
+                return rc;
+            });
+    };
+    int rc = all((const float *)nullptr);
+    if (rc == PP_OK) rc = all((const uint16_t *)nullptr);
+    if (rc == PP_OK)
+        rc = launch_after(k_norm_join, 1, 1024, 0, stream, 1, (const double *)workspace, blocks, norm);
+    return rc;
+}
+
+extern "C" size_t pp_stage_adamw_workspace(void) { return kStageAlign; }
+
+extern "C" int pp_stage_adamw(const pp_stage_tensor *list, int64_t count, void *m, void *v, uint8_t *m_exp, uint8_t *v_exp,
+                              int64_t held, int64_t *step, const float *lr_at, double lr, double beta1, double beta2,
+                              double eps, const float *norm, double max_norm, int random, uint64_t seed, void *workspace,
+                              size_t workspace_bytes, cudaStream_t stream) {
+    if (bad_list(list, count, true) || held < 0 || held % kMoments || !step || !aligned_to(step, 8)) return PP_ERR_ARG;
+    if (too_long(list, count) || held > PP_STAGE_MAX_ELEMENTS) return PP_ERR_SIZE;
+    if (!m != !v || !m_exp != !v_exp || (held > 0 && !m)) return PP_ERR_ARG;
+    if (!aligned_to(m, 32) || !aligned_to(v, 32)) return PP_ERR_ARG;
+    for (int64_t i = 0; i < count; ++i)
+        if (list[i].n && list[i].n > held - list[i].at) return PP_ERR_ARG;
+    if (!(beta1 >= 0 && beta1 < 1 && beta2 >= 0 && beta2 < 1 && eps >= 0 && eps <= 3e38)) return PP_ERR_ARG;
+    if (lr_at ? !aligned_to(lr_at, 4) : !(std::fabs(lr) <= 3e38)) return PP_ERR_ARG;
+    if (norm && (!aligned_to(norm, 4) || !(max_norm > 0))) return PP_ERR_ARG;
+    if (!workspace || !aligned_to(workspace, kStageAlign) || workspace_bytes < sizeof(StepNow)) return PP_ERR_ARG;
+    StepNow *now = static_cast<StepNow *>(workspace);
+    const Moments mo{m, v, m_exp, v_exp};
+    const Rates r{(float)beta1, (float)(1 - beta1), (float)beta2, (float)(1 - beta2), (float)eps, random != 0};
+    int rc = launch_after(k_step_begin, 1, 2, 0, stream, 1, step, lr_at, lr, beta1, beta2, norm, max_norm, seed, now);
+    const auto all = [&]<class P, class G>(const P *, const G *) {
+        if (rc != PP_OK) return;
+        rc = m_exp ? step_all<P, G, true>(list, count, mo, r, now, stream) : step_all<P, G, false>(list, count, mo, r, now, stream);
+    };
+    all((const float *)nullptr, (const float *)nullptr);
+    all((const float *)nullptr, (const uint16_t *)nullptr);
+    all((const uint16_t *)nullptr, (const float *)nullptr);
+    all((const uint16_t *)nullptr, (const uint16_t *)nullptr);
+    return rc;
+}
+
+extern "C" int pp_stage_adamw_moments(const uint8_t *m, const uint8_t *v, const uint8_t *m_exp, const uint8_t *v_exp,
+                                      int64_t held, uint16_t *m_values, uint16_t *v_values, cudaStream_t stream) {
+    if (held < 0 || held % kMoments) return PP_ERR_ARG;
+    if (held > PP_STAGE_MAX_ELEMENTS) return PP_ERR_SIZE;
+    if (held == 0) return PP_OK;
+    if (!m || !v || !m_exp || !v_exp || !m_values || !v_values) return PP_ERR_ARG;
+    if (!aligned_to(m, 8) || !aligned_to(v, 8) || !aligned_to(m_values, 16) || !aligned_to(v_values, 16)) return PP_ERR_ARG;
+    const Moments mo{(void *)m, (void *)v, (uint8_t *)m_exp, (uint8_t *)v_exp};
+    return launch_after(k_moments, ceil_div(held, kChunk), kThreads, 0, stream, 1, mo, held, m_values, v_values);
+}

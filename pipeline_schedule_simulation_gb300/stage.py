@@ -3,10 +3,14 @@ and marshalling only, every step of the computation runs in the library.
 
     head_forward, head_backward   the last stage's loss over a large vocabulary
                                   and its gradients, without kept logits
+    score_forward, score_backward log probabilities of given tokens, entropy and
+                                  likeliest alternatives, and their gradients
     pack, unpack, weight_grad     activation checkpoints in 8 bits and the
                                   weight gradient (the W op) taken from them
     join_forward, join_backward   the norm after a block, its gate, the residual
                                   scale and sum, the norm before the next block
+    grad_norm, AdamW              after the flush: the norm of the gradients and
+                                  the step over all tensors of the stage
 
 All tensors are CUDA tensors on one device; matrices have contiguous rows and
 any row stride.  Calls are asynchronous on ``stream`` (default: the current
@@ -21,29 +25,50 @@ results carry no gradient, whatever the inputs say.
 from __future__ import annotations
 
 import ctypes
+import math
 
 import torch
 
 from .binding import LIB, PP_OK, PPSchedError, _arg, _check, _reach
 
 EXPORTS = ("pp_stage_head_forward_workspace", "pp_stage_head_forward", "pp_stage_head_backward_workspace",
-           "pp_stage_head_backward", "pp_stage_pack", "pp_stage_unpack", "pp_stage_weight_grad_workspace",
+           "pp_stage_head_backward", "pp_stage_score_forward_workspace", "pp_stage_score_forward",
+           "pp_stage_score_backward_workspace", "pp_stage_score_backward", "pp_stage_pack", "pp_stage_unpack", "pp_stage_weight_grad_workspace",
            "pp_stage_weight_grad", "pp_stage_join_forward", "pp_stage_join_backward_workspace",
-           "pp_stage_join_backward", "pp_stage_wait_failure")
+           "pp_stage_join_backward", "pp_stage_grad_norm_workspace", "pp_stage_grad_norm", "pp_stage_adamw_workspace",
+           "pp_stage_adamw", "pp_stage_adamw_moments", "pp_stage_wait_failure")
 
-#: Columns of a checkpoint that share one exponent.
+#: Columns of a checkpoint, and elements of a moment in 8 bits, that share one exponent.
 BLOCK = 64
+#: Most alternatives of a token.
+MAX_TOP = 32
 #: Exponent of a checkpoint's block that holds an infinity or a NaN.
 NONFINITE = -128
 
 
+class _Tensors(ctypes.Structure):
+    """pp_stage_tensor"""
+    _fields_ = [("p", ctypes.c_void_p), ("g", ctypes.c_void_p), ("copy", ctypes.c_void_p), ("n", ctypes.c_int64),
+                ("at", ctypes.c_int64), ("decay", ctypes.c_float), ("p_float", ctypes.c_uint8), ("g_float", ctypes.c_uint8)]
+
+
 def _declare(lib):
     vp, i32, i64, f32, size = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_float, ctypes.c_size_t
+    f64, u64 = ctypes.c_double, ctypes.c_uint64
     m = [vp, i64]  # a matrix: pointer and row stride
     lib.pp_stage_head_forward_workspace.argtypes = [*m, *m, i64, i64, i64]
     lib.pp_stage_head_forward.argtypes = [*m, *m, vp, i64, i64, i64, vp, vp, vp, size, vp]
     lib.pp_stage_head_backward_workspace.argtypes = [*m, *m, i64, i64, i64]
     lib.pp_stage_head_backward.argtypes = [*m, *m, vp, vp, vp, f32, i64, i64, i64, *m, *m, i32, i32, vp, size, vp]
+    lib.pp_stage_score_forward_workspace.argtypes = [*m, *m, i64, i64, i64, i64]
+    lib.pp_stage_score_forward.argtypes = [*m, *m, vp, i64, i64, i64, i64, vp, vp, vp, vp, vp, vp, size, vp]
+    lib.pp_stage_score_backward_workspace.argtypes = [*m, *m, i64, i64, i64]
+    lib.pp_stage_score_backward.argtypes = [*m, *m, vp, vp, vp, vp, vp, i64, i64, i64, *m, *m, i32, i32, vp, size, vp]
+    lib.pp_stage_grad_norm_workspace.argtypes = [vp, i64]
+    lib.pp_stage_grad_norm.argtypes = [vp, i64, vp, vp, size, vp]
+    lib.pp_stage_adamw_workspace.argtypes = []
+    lib.pp_stage_adamw.argtypes = [vp, i64, vp, vp, vp, vp, i64, vp, vp, f64, f64, f64, f64, vp, f64, i32, u64, vp, size, vp]
+    lib.pp_stage_adamw_moments.argtypes = [vp, vp, vp, vp, i64, vp, vp, vp]
     lib.pp_stage_pack.argtypes = [*m, i64, i64, *m, *m, vp]
     lib.pp_stage_unpack.argtypes = [*m, *m, i64, i64, *m, vp]
     lib.pp_stage_weight_grad_workspace.argtypes = [*m, i64, i64, i64]
@@ -214,6 +239,20 @@ def head_forward(x, w, target, *, out=None, workspace=None, stream=None):
     return out
 
 
+def _gradients(out, outputs, add, T, V, H, device, dev):
+    """(pointer, stride) of dx and of dw, and whether dw is float."""
+    if not outputs or any(o not in ("dx", "dw") for o in outputs):
+        raise ValueError(f"outputs: expected some of 'dx' and 'dw', got {outputs!r}")
+    dx = _out_matrix(out, "dx", T, H, _BF16, device, dev) if "dx" in outputs else (None, 0)
+    dw, wide = (None, 0), False
+    if "dw" in outputs:
+        wide = isinstance(out.get("dw"), _Tensor) and out["dw"].dtype is _F32
+        if add and not wide:
+            raise ValueError("add: needs a float out['dw'] to add to")
+        dw = _out_matrix(out, "dw", V, H, _F32 if wide else _BF16, device, dev)
+    return dx, dw, wide
+
+
 def head_backward(x, w, target, lse, *, scale=1.0, weight=None, outputs=("dx", "dw"), add=False, out=None,
                   workspace=None, stream=None):
     """Gradients of sum_t scale * weight[t] * loss[t] (weight: float [T], default 1).
@@ -229,22 +268,95 @@ def head_backward(x, w, target, lse, *, scale=1.0, weight=None, outputs=("dx", "
     px, sx, pw, sw, T, V, H, pt = _head_inputs(x, w, target, dev)
     pl = _vector(lse, "lse", _F32, dev, T)
     pg = None if weight is None else _vector(weight, "weight", _F32, dev, T)
-    if not outputs or any(o not in ("dx", "dw") for o in outputs):
-        raise ValueError(f"outputs: expected some of 'dx' and 'dw', got {outputs!r}")
     out, device = dict(out) if out else {}, x.device
-    dx = _out_matrix(out, "dx", T, H, _BF16, device, dev) if "dx" in outputs else (None, 0)
-    dw, wide = (None, 0), False
-    if "dw" in outputs:
-        wide = isinstance(out.get("dw"), _Tensor) and out["dw"].dtype is _F32
-        if add and not wide:
-            raise ValueError("add: needs a float out['dw'] to add to")
-        dw = _out_matrix(out, "dw", V, H, _F32 if wide else _BF16, device, dev)
+    dx, dw, wide = _gradients(out, outputs, add, T, V, H, device, dev)
     need = LIB.pp_stage_head_backward_workspace(px, sx, pw, sw, T, V, H)
     _keep, ws, n = _scratch(workspace, need, device, dev)
     rc = LIB.pp_stage_head_backward(px, sx, pw, sw, pt, pl, pg, scale, T, V, H, *dx, *dw, wide, bool(add) and wide, ws, n,
                                     _raw_stream(dev))
     if rc != PP_OK:
         raise PPSchedError(rc, "pp_stage_head_backward")
+    return out
+
+
+def _top(top, V):
+    if isinstance(top, bool) or not isinstance(top, int) or not 0 <= top <= min(MAX_TOP, V):
+        raise ValueError(f"top: expected a whole number from 0 to {min(MAX_TOP, V)}, got {top!r}")
+    return top
+
+
+def score_forward_workspace(x, w, top=0):
+    """Bytes of scratch memory that score_forward needs for these matrices."""
+    px, sx, T, H = _matrix(x, "x", _BF16, _device(x))
+    pw, sw, V, _ = _matrix(w, "w", _BF16, _device(x), None, H)
+    return LIB.pp_stage_score_forward_workspace(px, sx, pw, sw, T, V, H, _top(top, V))
+
+
+def score_backward_workspace(x, w):
+    """Bytes of scratch memory that score_backward needs for these matrices."""
+    px, sx, T, H = _matrix(x, "x", _BF16, _device(x))
+    pw, sw, V, _ = _matrix(w, "w", _BF16, _device(x), None, H)
+    return LIB.pp_stage_score_backward_workspace(px, sx, pw, sw, T, V, H)
+
+
+def score_forward(x, w, target, *, top=0, out=None, workspace=None, stream=None):
+    """Log probabilities of the given tokens under the softmax of the logits x w^T, without keeping those.
+
+    x [T, H], w [V, H] bf16; target [T] int64, a token whose target is outside 0..V-1 is left out.  Returns logp [T]
+    (0 where left out), entropy [T] and lse [T]; float.  With `top` (up to 32) also top_index int64 [T, top], the
+    columns of the largest logits in falling order (the lower one first among equals), and top_logp float [T, top]."""
+    dev = _device(x)
+    ctx = _elsewhere(dev, stream)
+    if ctx is not None:
+        with ctx:
+            return score_forward(x, w, target, top=top, out=out, workspace=workspace)
+    px, sx, pw, sw, T, V, H, pt = _head_inputs(x, w, target, dev)
+    k = _top(top, V)
+    out, device = dict(out) if out else {}, x.device
+    logp = _out_vector(out, "logp", T, _F32, device, dev)
+    lse = _out_vector(out, "lse", T, _F32, device, dev)
+    entropy = _out_vector(out, "entropy", T, _F32, device, dev)
+    tops = [None, None]
+    if k:
+        for i, (name, dtype) in enumerate((("top_logp", _F32), ("top_index", _I64))):
+            tops[i], stride = _out_matrix(out, name, T, k, dtype, device, dev)
+            if stride != k:
+                raise ValueError(f"{name}: expected contiguous memory, got a row stride of {stride}")
+    need = LIB.pp_stage_score_forward_workspace(px, sx, pw, sw, T, V, H, k)
+    _keep, ws, n = _scratch(workspace, need, device, dev)
+    rc = LIB.pp_stage_score_forward(px, sx, pw, sw, pt, T, V, H, k, logp, lse, entropy, *tops, ws, n, _raw_stream(dev))
+    if rc != PP_OK:
+        raise PPSchedError(rc, "pp_stage_score_forward")
+    return out
+
+
+def score_backward(x, w, target, lse, dlogp, *, entropy=None, dentropy=None, outputs=("dx", "dw"), add=False, out=None,
+                   workspace=None, stream=None):
+    """Gradients of a loss that depends on score_forward's logp and entropy, from dlogp = dL/dlogp and, if given,
+    dentropy = dL/dentropy (float [T]; with it the entropy that score_forward returned).
+
+    Returns dx [T, H] bf16 and dw [V, H], or the one named in `outputs`; dw and `add` as in head_backward.  A token
+    that is left out has no gradient, through its entropy neither."""
+    dev = _device(x)
+    ctx = _elsewhere(dev, stream)
+    if ctx is not None:
+        with ctx:
+            return score_backward(x, w, target, lse, dlogp, entropy=entropy, dentropy=dentropy, outputs=outputs, add=add,
+                                  out=out, workspace=workspace)
+    px, sx, pw, sw, T, V, H, pt = _head_inputs(x, w, target, dev)
+    pl, pg = _vector(lse, "lse", _F32, dev, T), _vector(dlogp, "dlogp", _F32, dev, T)
+    if (entropy is None) != (dentropy is None):
+        raise ValueError("entropy and dentropy: expected both or neither")
+    pe, pd = (None, None) if entropy is None else (_vector(entropy, "entropy", _F32, dev, T),
+                                                   _vector(dentropy, "dentropy", _F32, dev, T))
+    out, device = dict(out) if out else {}, x.device
+    dx, dw, wide = _gradients(out, outputs, add, T, V, H, device, dev)
+    need = LIB.pp_stage_score_backward_workspace(px, sx, pw, sw, T, V, H)
+    _keep, ws, n = _scratch(workspace, need, device, dev)
+    rc = LIB.pp_stage_score_backward(px, sx, pw, sw, pt, pl, pg, pe, pd, T, V, H, *dx, *dw, wide, bool(add) and wide, ws, n,
+                                     _raw_stream(dev))
+    if rc != PP_OK:
+        raise PPSchedError(rc, "pp_stage_score_backward")
     return out
 
 
@@ -435,6 +547,198 @@ def join_backward(dh, dy, y, f, rstd_post, rstd_pre, w_post, w_pre, gate=None, *
     if rc != PP_OK:
         raise PPSchedError(rc, "pp_stage_join_backward")
     return out
+
+
+def _flat(t, name, dev, dtypes):
+    """Checks a tensor that is taken as one run of elements on CUDA device `dev`."""
+    if not isinstance(t, _Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
+    if t.get_device() != dev or dev < 0:
+        raise ValueError(f"{name}: expected a tensor on {f'cuda:{dev}' if dev >= 0 else 'a CUDA device'}, got {t.device}")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name}: expected {' or '.join(str(d) for d in dtypes)}, got {t.dtype}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: expected contiguous memory, got strides {t.stride()} for shape {tuple(t.shape)}")
+
+
+def _listed(tensors, name):
+    if isinstance(tensors, _Tensor) or not hasattr(tensors, "__iter__"):
+        raise TypeError(f"{name}: expected a list of tensors, got {type(tensors).__name__}")
+    return list(tensors)
+
+
+def grad_norm(grads, *, out=None, workspace=None, stream=None):
+    """The 2-norm of all gradients together, float [1] on their device: what AdamW.step clips by.
+
+    grads: float or bf16 tensors, contiguous, of any shapes.  A gradient above 1.8e19 makes it infinite."""
+    grads = _listed(grads, "grads")
+    dev = _device(grads[0]) if grads else _device(out)
+    ctx = _elsewhere(dev, stream)
+    if ctx is not None:
+        with ctx:
+            return grad_norm(grads, out=out, workspace=workspace)
+    table = (_Tensors * len(grads))()
+    for i, g in enumerate(grads):
+        _flat(g, f"grads[{i}]", dev, (_F32, _BF16))
+        e = table[i]
+        e.g, e.n, e.g_float = g.data_ptr(), g.numel(), g.dtype is _F32
+    if out is None:
+        if dev < 0:
+            raise ValueError("grads: expected at least one tensor, or an `out` on a CUDA device")
+        out = _empty(1, dtype=_F32, device=grads[0].device)
+    po = _vector(out, "out", _F32, dev, 1)
+    need = LIB.pp_stage_grad_norm_workspace(ctypes.addressof(table), len(grads))
+    _keep, ws, n = _scratch(workspace, need, out.device, dev)
+    rc = LIB.pp_stage_grad_norm(ctypes.addressof(table), len(grads), po, ws, n, _raw_stream(dev))
+    if rc != PP_OK:
+        raise PPSchedError(rc, "pp_stage_grad_norm")
+    return out
+
+
+class AdamW:
+    """The AdamW step over the tensors of a stage, in a few launches whatever their number.
+
+        m = beta1 m + (1 - beta1) g      v = beta2 v + (1 - beta2) g^2
+        p = p (1 - lr decay) - lr / (1 - beta1^t) m / (sqrt(v / (1 - beta2^t)) + eps)
+
+    params: contiguous float or bf16 tensors of any shapes, updated in place.  copies: for float parameters, a list of
+    bf16 tensors of the same shapes (or None for one that has none) that receive the new values.  weight_decay: a number,
+    or one for each parameter.
+
+    The moments are held in 32 bits or (bits=8) in 8: 64 consecutive elements share an exponent, each keeps 4 significant
+    bits; 2.03 bytes an element for both.  With a `seed` moments in 8 bits and bf16 parameters are rounded up with the
+    probability of what is cut off, by random bits that depend on the seed, the step and the element's place alone;
+    without one to nearest, which an average that changes by 1 - beta2 a step does not survive in 4 bits for long.
+
+    ``state`` has the flat tensors that a checkpoint keeps: "m", "v" (bits=8: and "m_exp", "v_exp"), each parameter's from
+    a multiple of 64 elements on, and "step", int64 [1], the steps taken.  Pass such a dict as ``state`` to go on from it
+    (the tensors are used, not copied).  The step's number is counted on the device: a captured step counts on at every
+    replay.  One step at a time: calls on several streams are the caller's to order."""
+
+    def __init__(self, params, *, bits=32, copies=None, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.0, seed=None,
+                 state=None):
+        params = _listed(params, "params")
+        if not params:
+            raise ValueError("params: expected at least one tensor")
+        if bits not in (8, 32):
+            raise ValueError(f"bits: expected 8 or 32, got {bits!r}")
+        b1, b2 = (float(b) for b in betas)
+        if not (0 <= b1 < 1 and 0 <= b2 < 1):
+            raise ValueError(f"betas: expected two numbers from 0 to below 1, got {betas!r}")
+        if not 0 <= float(eps) < math.inf:
+            raise ValueError(f"eps: expected a number that is not negative, got {eps!r}")
+        if seed is not None and (isinstance(seed, bool) or not isinstance(seed, int) or not 0 <= seed < 1 << 64):
+            raise ValueError(f"seed: expected a whole number of 64 bits or None, got {seed!r}")
+        dev = _device(params[0])
+        copies = [None] * len(params) if copies is None else _listed(copies, "copies")
+        decay = [weight_decay] * len(params) if isinstance(weight_decay, (int, float)) else list(weight_decay)
+        for name, given in (("copies", copies), ("weight_decay", decay)):
+            if len(given) != len(params):
+                raise ValueError(f"{name}: expected {len(params)}, one for each parameter, got {len(given)}")
+        self.bits, self.betas, self.eps, self.seed = bits, (b1, b2), float(eps), seed
+        self.params, self.copies = tuple(params), tuple(copies)
+        self._dev = dev
+        self._table = (_Tensors * len(params))()
+        held = 0
+        for i, (p, c, d, e) in enumerate(zip(params, copies, decay, self._table)):
+            _flat(p, f"params[{i}]", dev, (_F32, _BF16))
+            if c is not None:
+                _flat(c, f"copies[{i}]", dev, (_BF16,))
+                if p.dtype is not _F32:
+                    raise TypeError(f"copies[{i}]: params[{i}] is bf16 itself")
+                if c.shape != p.shape:
+                    raise ValueError(f"copies[{i}]: expected shape {tuple(p.shape)}, got {tuple(c.shape)}")
+            if not math.isfinite(d):
+                raise ValueError(f"weight_decay: expected a finite number for params[{i}], got {d!r}")
+            e.p, e.copy = p.data_ptr(), None if c is None else c.data_ptr()
+            e.n, e.at, e.decay, e.p_float = p.numel(), held, d, p.dtype is _F32
+            held += (p.numel() + BLOCK - 1) // BLOCK * BLOCK
+        self._held, self._device = held, params[0].device
+        self._state = self._new_state() if state is None else self._given_state(state)
+        self._work = torch.empty(LIB.pp_stage_adamw_workspace(), dtype=_U8, device=self._device)
+
+    @property
+    def state(self):
+        """The tensors that a checkpoint keeps, by name."""
+        return dict(self._state)
+
+    def _layout(self):
+        small = self.bits == 8
+        names = {"m": (_U8 if small else _F32, self._held), "v": (_U8 if small else _F32, self._held),
+                 "step": (_I64, 1)}
+        if small:
+            names["m_exp"] = names["v_exp"] = (_U8, self._held // BLOCK)
+        return names
+
+    def _new_state(self):
+        return {k: torch.zeros(n, dtype=dtype, device=self._device) for k, (dtype, n) in self._layout().items()}
+
+    def _given_state(self, state):
+        layout = self._layout()
+        if set(state) != set(layout):
+            raise ValueError(f"state: expected {sorted(layout)}, got {sorted(state)}")
+        for k, (dtype, n) in layout.items():
+            _vector(state[k], f"state[{k!r}]", dtype, self._dev, n)
+            if k in "mv" and state[k].data_ptr() % 32:
+                raise ValueError(f"state[{k!r}]: expected memory that starts on 32 bytes")
+        return dict(state)
+
+    def step(self, grads, lr, *, norm=None, max_norm=None, stream=None):
+        """One step.  grads: float or bf16, of the parameters' shapes.  lr: a number, or a float [1] tensor on the device
+        that is read when the step runs.  With `norm` (of grad_norm) and `max_norm` the gradients are scaled by
+        max_norm / norm where the norm is larger; where it is not a finite number nothing changes, the step's number
+        neither."""
+        dev = self._dev
+        ctx = _elsewhere(dev, stream)
+        if ctx is not None:
+            with ctx:
+                return self.step(grads, lr, norm=norm, max_norm=max_norm)
+        if len(grads) != len(self.params):
+            raise ValueError(f"grads: expected {len(self.params)}, one for each parameter, got {len(grads)}")
+        for i, (e, p, g) in enumerate(zip(self._table, self.params, grads)):
+            if not (isinstance(g, _Tensor) and g.shape == p.shape):
+                _flat(g, f"grads[{i}]", dev, (_F32, _BF16))
+                raise ValueError(f"grads[{i}]: expected shape {tuple(p.shape)}, got {tuple(g.shape)}")
+            wide = g.dtype is _F32
+            if not (wide or g.dtype is _BF16) or g.get_device() != dev or not g.is_contiguous():
+                _flat(g, f"grads[{i}]", dev, (_F32, _BF16))
+            if p.data_ptr() != (e.p or 0):
+                raise ValueError(f"params[{i}]: its memory is not that which this step was made for")
+            e.g, e.g_float = g.data_ptr(), wide
+        lr_at = _vector(lr, "lr", _F32, dev, 1) if isinstance(lr, _Tensor) else None
+        rate = 0.0 if lr_at is not None else float(lr)
+        if not math.isfinite(rate):
+            raise ValueError(f"lr: expected a finite number, got {lr!r}")
+        if (norm is None) != (max_norm is None):
+            raise ValueError("norm and max_norm: expected both or neither")
+        if max_norm is not None and not 0 < max_norm < math.inf:
+            raise ValueError(f"max_norm: expected a number above 0, got {max_norm!r}")
+        pn = None if norm is None else _vector(norm, "norm", _F32, dev, 1)
+        s = self._state
+        small = self.bits == 8
+        rc = LIB.pp_stage_adamw(ctypes.addressof(self._table), len(self.params), s["m"].data_ptr(), s["v"].data_ptr(),
+                                s["m_exp"].data_ptr() if small else None, s["v_exp"].data_ptr() if small else None,
+                                self._held, s["step"].data_ptr(), lr_at, rate, *self.betas, self.eps, pn, max_norm or 1.0,
+                                self.seed is not None, self.seed or 0, self._work.data_ptr(), self._work.numel(),
+                                _raw_stream(dev))
+        if rc != PP_OK:
+            raise PPSchedError(rc, "pp_stage_adamw")
+
+    def moments(self, *, stream=None):
+        """(m, v) as numbers, flat as in ``state``: its float tensors themselves, or what the 8 bits stand for, as bf16."""
+        s, dev = self._state, self._dev
+        if self.bits == 32:
+            return s["m"], s["v"]
+        ctx = _elsewhere(dev, stream)
+        if ctx is not None:
+            with ctx:
+                return self.moments()
+        m, v = (torch.empty(self._held, dtype=_BF16, device=self._device) for _ in range(2))
+        rc = LIB.pp_stage_adamw_moments(s["m"].data_ptr(), s["v"].data_ptr(), s["m_exp"].data_ptr(), s["v_exp"].data_ptr(),
+                                        self._held, m.data_ptr(), v.data_ptr(), _raw_stream(dev))
+        if rc != PP_OK:
+            raise PPSchedError(rc, "pp_stage_adamw_moments")
+        return m, v
 
 
 def wait_failure():
