@@ -44,7 +44,7 @@ struct StatsEpi {
     };
     __device__ __forceinline__ void begin(Row &r, int64_t t) const { r.target = target[t]; }
     __device__ __forceinline__ void take(const Row &r, int64_t t, int n0, int end, int N, int piece,
-                                         float (&v)[kRuns][32]) const {
+                                         float (&v)[kRuns][32], float *) const {
         const int last = min(end, N);
         float top = kNegInf, s = 0.f;
 #pragma unroll
@@ -131,7 +131,8 @@ struct GradEpi {
             r.sum = r.b != 0.f ? fmaf(r.b, entropy[t], r.c) : r.c;  // a row without that gradient is not asked for its entropy
         }
     }
-    __device__ __forceinline__ void take(const Row &r, int64_t t, int n0, int end, int N, int, float (&v)[kRuns][32]) const {
+    __device__ __forceinline__ void take(const Row &r, int64_t t, int n0, int end, int N, int, float (&v)[kRuns][32],
+                                         float *) const {
         // whether the target is in one of these runs (past N it is the next piece's)
         const int64_t off = r.at - n0;
         const bool mine = r.in && off >= 0 && r.at < min(end, N) && (off & (kPieces * 32 - 1)) < 32;

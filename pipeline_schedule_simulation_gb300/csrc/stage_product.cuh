@@ -21,8 +21,9 @@
 //   apart(row), one_apart(row, n, v)  (kSomeRows) those rows, and what is done with
 //                      one column of such a row beside one()
 // and those that do not:
-//   take(row, m, n0, end, N, piece, v)  one piece: run i is the columns from
-//                      n0 + 64 i on, below `end` and (what exists) N
+//   take(row, m, n0, end, N, piece, v, own)  one piece: run i is the columns from
+//                      n0 + 64 i on, below `end` and (what exists) N; own: 32 floats
+//                      of shared memory of the lane's own, one every 32
 //   kWhole             runs go on to the next multiple of 64 past N, and none is
 //                      cut by a tile's end
 //
@@ -418,10 +419,9 @@ __global__ void __launch_bounds__(kProductThreads, 1)
             for (int i = 0; i < kRuns; ++i)
 #pragma unroll
                 for (int c = 0; c < 32; ++c) v[i][c] = __uint_as_float(sum[i][c]);
+            float4 *turn = reinterpret_cast<float4 *>(raw + (ring - tc::smem_u32(raw)) + kRingBytes + (warp - 4) * kTurnBytes);
             if constexpr (Epi::kStore) {
                 if (ok) {
-                    float4 *turn = reinterpret_cast<float4 *>(raw + (ring - tc::smem_u32(raw)) + kRingBytes +
-                                                              (warp - 4) * kTurnBytes);
                     const int64_t m_first = m - lane;
                     const int end = min(n1, s.N);
 #pragma unroll
@@ -432,7 +432,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
                 }
             } else {
                 begin_next(t + step);
-                if (ok && live) epi.take(row, m, n0, n1, s.N, kPieces * nt + half, v);
+                if (ok && live) epi.take(row, m, n0, n1, s.N, kPieces * nt + half, v, reinterpret_cast<float *>(turn) + lane);
                 __syncwarp();
             }
         }

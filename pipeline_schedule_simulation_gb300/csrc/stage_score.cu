@@ -11,12 +11,13 @@
 // Both terms of the entropy are positive, so nothing cancels.
 //
 // Alternatives.  A thread holds its piece in registers and writes the logits that
-// reach a bound below which nothing can be among the token's k largest: k classes of pieces each keep the largest logit that any of
-// their pieces has had, and the least of these k is such a bound, since k
-// different logits reach it.  It rises as tiles finish; a thread reads it a tile
-// ahead, and an old bound only lets through more.  So the order in which blocks
-// run decides what is written, but not what is found.  Of 131072 columns a few
-// hundred are written for each token.
+// reach a bound below which nothing can be among the token's k largest: k classes
+// of runs of 32 columns each keep the largest logit that any of their runs has
+// had, and the least of these k is such a bound, since k different logits reach
+// it.  It rises as tiles finish; a thread reads it a tile ahead, and an old bound
+// only lets through more.  So the order in which blocks run decides what is
+// written, but not what is found.  Of 131072 columns a few hundred are written
+// for each token.
 #include <algorithm>
 
 #include "stage_head.cuh"
@@ -85,14 +86,23 @@ struct ScoreEpi {
     };
     __device__ __forceinline__ void begin(Row &r, int64_t t) const {
         r.target = target[t];
-        if constexpr (TOP) {
-            uint32_t a = ~0u;
-            for (int j = 0; j < alt.k; ++j) a = min(a, __ldcg(alt.least + j * T + t));
-            r.least = a;
+        if constexpr (TOP) r.least = least_of(t);
+    }
+    __device__ __forceinline__ uint32_t least_of(int64_t t) const {
+        uint32_t a = ~0u;
+#pragma unroll
+        for (int j = 0; j < kMaxTop; j += 8) {
+            if (j >= alt.k) break;
+            uint32_t b[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) b[i] = j + i < alt.k ? __ldcg(alt.least + (j + i) * T + t) : ~0u;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) a = min(a, b[i]);
         }
+        return a;
     }
     __device__ __forceinline__ void take(const Row &r, int64_t t, int n0, int end, int N, int piece,
-                                         float (&v)[kRuns][32]) const {
+                                         float (&v)[kRuns][32], float *own) const {
         const int last = min(end, N);
         float run[kRuns];  // largest logits of the runs
 #pragma unroll
@@ -100,7 +110,7 @@ struct ScoreEpi {
             const int cnt = last - (n0 + i * kPieces * 32);
             run[i] = cnt >= 32 ? largest(v[i]) : largest_of(v[i], cnt);
         }
-        if constexpr (TOP) take_out(r, t, n0, last, piece, run, v);
+        if constexpr (TOP) take_out(r, t, n0, last, piece, run, v, own);
         Stats a{kNegInf, 0.f, 0.f};
 #pragma unroll
         for (int i = 0; i < kRuns; ++i) {
@@ -149,46 +159,71 @@ struct ScoreEpi {
         for (int j = 0; j < 32; ++j) b[j & 3] |= v[j] >= bound ? 1u << j : 0u;
         return ((b[0] | b[1]) | (b[2] | b[3])) & (cnt >= 32 ? ~0u : (1u << max(cnt, 0)) - 1);
     }
-    static __device__ __forceinline__ int count(float bound, const float (&run)[kRuns], const float (&v)[kRuns][32], int left) {
-        int n = 0;
-#pragma unroll
-        for (int i = 0; i < kRuns; ++i)
-            if (run[i] >= bound) n += __popc(reaching(bound, v[i], left - i * kPieces * 32));
-        return n;
-    }
     // What reaches the bound is written by ascending column.  Where that is more than there are slots, the bound is raised
     // by bisection until it leaves k or a few more; among equals at such a bound the first columns are written.
+    // A lane's run goes through its own shared memory, so that what is written is found by its number: a branch for each
+    // of 128 registers takes 80000 cycles a tile, most of them waiting for instructions.
     __device__ __forceinline__ void take_out(const Row &r, int64_t t, int n0, int last, int piece, const float (&run)[kRuns],
-                                             const float (&v)[kRuns][32]) const {
+                                             const float (&v)[kRuns][32], float *own) const {
         const int64_t at = t * alt.pieces + piece;
-        const float least = from_ordered(r.least), top = fmaxf(fmaxf(run[0], run[1]), fmaxf(run[2], run[3]));
+        const float top = fmaxf(fmaxf(run[0], run[1]), fmaxf(run[2], run[3]));
+        // no bound a tile ago: perhaps there is one by now
+        const float least = from_ordered(r.least ? r.least : least_of(t));
         int c = 0;
         if (top >= least) {
-            uint32_t lo = ordered(least), hi = ordered(top);
-            int n = count(least, run, v, last - n0), equals = kRuns * 32;
-            if (n > alt.slots) {
-                while (n > alt.slots && lo < hi) {
-                    const uint32_t mid = lo + (hi - lo + 1) / 2;
-                    const int q = count(from_ordered(mid), run, v, last - n0);
-                    if (q >= alt.k) lo = mid, n = q;
-                    else hi = mid - 1;
+            uint32_t lo = ordered(least), hi = max(ordered(top), lo), u = lo;  // (-0 is below 0)
+            uint32_t in[kRuns], equal[kRuns] = {};  // what is written; and what only for the first columns
+            int n = 0;
+            for (bool begun = false, done = false; !done;) {
+                const float bound = from_ordered(u);
+                uint32_t b[kRuns];
+                int q = 0;
+#pragma unroll
+                for (int i = 0; i < kRuns; ++i) {
+                    b[i] = reaching(bound, v[i], last - (n0 + i * kPieces * 32));
+                    q += __popc(b[i]);
                 }
-                if (n > alt.slots) equals = alt.slots - count(from_ordered(lo + 1), run, v, last - n0);
+                if (u > hi) {  // above the bound that leaves too many: these, and as many equals as there is room for
+#pragma unroll
+                    for (int i = 0; i < kRuns; ++i) equal[i] = in[i] & ~b[i], in[i] = b[i];
+                    n = q;
+                    break;
+                }
+                if (!begun || q >= alt.k) {
+                    lo = u, n = q;
+#pragma unroll
+                    for (int i = 0; i < kRuns; ++i) in[i] = b[i];
+                } else {
+                    hi = u - 1;
+                }
+                begun = true;
+                done = n <= alt.slots;
+                u = lo + (hi - lo + 1) / 2;
+                if (lo == hi) u = hi + 1;
             }
-            const float bound = from_ordered(lo);
             Found *to = alt.found + at * alt.slots;
+            int room = alt.slots - n;
+#pragma unroll
+            for (int i = 0; i < kRuns; ++i) {
+                if (equal[i]) {
+                    while (__popc(equal[i]) > room) equal[i] &= ~(0x80000000u >> __clz(equal[i]));
+                    room -= __popc(equal[i]);
+                    in[i] |= equal[i];
+                }
+                if (in[i]) {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) own[j * 32] = v[i][j];
+                    for (uint32_t b = in[i]; b; b &= b - 1) {
+                        const int j = __ffs(b) - 1;
+                        to[c++] = {own[j * 32], n0 + i * kPieces * 32 + j};
+                    }
+                }
+            }
 #pragma unroll
             for (int i = 0; i < kRuns; ++i)
-                if (run[i] >= bound) {
-                    const int first = n0 + i * kPieces * 32;
-                    const uint32_t in = reaching(bound, v[i], last - first);
-#pragma unroll
-                    for (int j = 0; j < 32; ++j)
-                        if (in >> j & 1 && (v[i][j] > bound || --equals >= 0)) to[c++] = {v[i][j], first + j};
-                }
+                if (run[i] > least) atomicMax(alt.least + (int64_t)((piece * kRuns + i) % alt.k) * T + t, ordered(run[i]));
         }
         alt.count[at] = (uint8_t)c;
-        if (top > least) atomicMax(alt.least + (int64_t)(piece % alt.k) * T + t, ordered(top));
     }
 };
 static_assert(kRuns == 4);
@@ -284,7 +319,8 @@ __device__ __forceinline__ int sort_kept(Found *kept, int n, int k, int lane) {
     for (int j = 0; j < n; ++j) {
         const Found g = kept[j];
 #pragma unroll
-        for (int i = 0; i < kKept / 32; ++i) place[i] += before(g, f[i]);
+        for (int i = 0; i < kKept / 32; ++i)
+            if (i * 32 < n) place[i] += before(g, f[i]);
     }
     __syncwarp();
 #pragma unroll
@@ -340,6 +376,7 @@ __global__ void __launch_bounds__(256) k_score_join(const JoinArgs a, const Alte
     const int64_t u = (int64_t)blockIdx.x * 8 + row;
     x = sh[row][lane];
     float m = x.m;
+    [[maybe_unused]] const float best = x.m;  // of the lane's pieces
 #pragma unroll
     for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
     const float ref = ref_of(m);
@@ -360,37 +397,38 @@ __global__ void __launch_bounds__(256) k_score_join(const JoinArgs a, const Alte
         const int k = alt.k, slots = alt.slots;
         const uint8_t *count = alt.count + u * a.pieces;
         const Found *found = alt.found + u * a.pieces * slots;
-        // k different logits reach the k-th largest of these; and the classes' bound
-        float best = kNegInf;
-        bool any = false;
-#pragma unroll 4
-        for (int64_t p = lane; p < a.pieces; p += 32)
-            if (count[p]) best = fmaxf(best, found[p * slots].l), any = true;
+        // k different logits reach the k-th of the lanes' largest; and the classes' bound
         int place = 0;
         for (int i = 0; i < 32; ++i) {
             const float b = __shfl_sync(~0u, best, i);
-            place += __shfl_sync(~0u, (int)any, i) && (b > best || (b == best && i < lane));
+            place += b > best || (b == best && i < lane);
         }
-        const uint32_t kth = __ballot_sync(~0u, any && place == k - 1);
-        float least = kth ? __shfl_sync(~0u, best, __ffs(kth) - 1) : kNegInf;
+        float least = __shfl_sync(~0u, best, __ffs(__ballot_sync(~0u, place == k - 1)) - 1);
         if (alt.least)
             least = fmaxf(least, from_ordered(__reduce_min_sync(~0u, lane < k ? alt.least[lane * a.T + u] : ~0u)));
         Found *mine = keep[row];
         int n = 0;
-        for (int64_t p0 = 0; p0 < a.pieces; p0 += 32) {
-            const int64_t p = p0 + lane;
-            int c = p < a.pieces ? count[p] : 0;
-            for (int e = 0; __any_sync(~0u, e < c); ++e) {
-                Found f{kNaN, 0};
-                if (e < c) f = found[p * slots + e];
-                const bool is = f.l >= least;
-                if (!is && !alt.least) c = 0;  // nor are those behind it
-                const uint32_t in = __ballot_sync(~0u, is);
-                if (is) mine[n + __popc(in & ((1u << lane) - 1))] = f;
-                n += __popc(in);
-                if (n > kKept - 32) {
-                    n = sort_kept(mine, n, k, lane);
-                    least = fmaxf(least, mine[k - 1].l);
+        constexpr int kAhead = 4;
+        for (int64_t p0 = 0; p0 < a.pieces; p0 += 32 * kAhead) {
+            int counts[kAhead];
+#pragma unroll
+            for (int h = 0; h < kAhead; ++h) counts[h] = p0 + 32 * h + lane < a.pieces ? count[p0 + 32 * h + lane] : 0;
+#pragma unroll
+            for (int h = 0; h < kAhead; ++h) {
+                const Found *from = found + (p0 + 32 * h + lane) * slots;
+                int c = counts[h];
+                for (int e = 0; __any_sync(~0u, e < c); ++e) {
+                    Found f{kNaN, 0};
+                    if (e < c) f = from[e];
+                    const bool is = f.l >= least;
+                    if (!is && !alt.least) c = 0;  // nor are those behind it
+                    const uint32_t in = __ballot_sync(~0u, is);
+                    if (is) mine[n + __popc(in & ((1u << lane) - 1))] = f;
+                    n += __popc(in);
+                    if (n > kKept - 32) {
+                        n = sort_kept(mine, n, k, lane);
+                        least = fmaxf(least, mine[k - 1].l);
+                    }
                 }
             }
         }
