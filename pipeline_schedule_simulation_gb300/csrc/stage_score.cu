@@ -65,10 +65,10 @@ __device__ __forceinline__ float from_ordered(uint32_t u) {
 
 // What the pieces' alternatives are written to.
 struct Alternatives {
-    int k, slots;     // slots: of a piece, k or more
+    int k, slots;     // slots: of a piece, k or more, even
     int64_t pieces;
     uint8_t *count;   // [T][pieces]
-    Found *found;     // [T][pieces][slots]; of few tokens in order, else by column
+    Found *found;     // [T][pieces][slots]
     uint32_t *least;  // [k][T]: the classes' largest logits, as ordered(); null for few tokens
 };
 
@@ -123,14 +123,16 @@ struct ScoreEpi {
             }
             const float top = fmaxf(a.m, run[i]), ref = ref_of(top);
             const Stats b = rebase(a, ref);
-            float e[4] = {b.s, 0.f, 0.f, 0.f}, u[4] = {b.u, 0.f, 0.f, 0.f};
+            float2 e[2] = {{b.s, 0.f}, {0.f, 0.f}}, u[2] = {{b.u, 0.f}, {0.f, 0.f}};
 #pragma unroll
-            for (int j = 0; j < 32; ++j) {
-                const float q = not_below((v[i][j] - ref) * kLog2e, kNoExp), p = exp2_fast(q);
-                e[j & 3] += p;
-                u[j & 3] = fmaf(p, q, u[j & 3]);
+            for (int j = 0; j < 32; j += 2) {
+                float2 q = __fmul2_rn(__fadd2_rn({v[i][j], v[i][j + 1]}, {-ref, -ref}), {kLog2e, kLog2e});
+                q = {not_below(q.x, kNoExp), not_below(q.y, kNoExp)};
+                const float2 p = {exp2_fast(q.x), exp2_fast(q.y)};
+                e[j >> 1 & 1] = __fadd2_rn(e[j >> 1 & 1], p);
+                u[j >> 1 & 1] = __ffma2_rn(p, q, u[j >> 1 & 1]);
             }
-            a = {top, (e[0] + e[1]) + (e[2] + e[3]), (u[0] + u[1]) + (u[2] + u[3])};
+            a = {top, (e[0].x + e[0].y) + (e[1].x + e[1].y), (u[0].x + u[0].y) + (u[1].x + u[1].y)};
             const int64_t at = r.target - n;  // few rows have their target here
             if (at >= 0 && at < cnt) {
 #pragma unroll
@@ -171,35 +173,47 @@ struct ScoreEpi {
         const float least = from_ordered(r.least ? r.least : least_of(t));
         int c = 0;
         if (top >= least) {
-            uint32_t lo = ordered(least), hi = max(ordered(top), lo), u = lo;  // (-0 is below 0)
+            constexpr int kAll = kRuns * 32;
+            uint32_t lo = ordered(least), hi = max(ordered(top), lo);  // (-0 is below 0)
             uint32_t in[kRuns], equal[kRuns] = {};  // what is written; and what only for the first columns
-            int n = 0;
-            for (bool begun = false, done = false; !done;) {
+            // without a bound the first guess is as far below the least of the runs' largest as that is below the largest
+            const float some = fminf(fminf(run[0], run[1]), fminf(run[2], run[3]));
+            float down = top - some;
+            int n = kAll + 1;  // what reaches lo; not known yet
+            for (int i = 0;; ++i) {
+                uint32_t u;
+                if (n > kAll) {
+                    u = least == kNegInf && i < 4 ? min(max(ordered(some - down), lo), hi) : lo;
+                    down *= 4;
+                } else if (lo == hi) {
+                    u = hi + 1;
+                } else {
+                    const float mid = 0.5f * (from_ordered(lo) + from_ordered(hi));
+                    u = i < 12 && isfinite(mid) ? min(max(ordered(mid), lo + 1), hi) : lo + (hi - lo + 1) / 2;
+                }
                 const float bound = from_ordered(u);
                 uint32_t b[kRuns];
                 int q = 0;
 #pragma unroll
-                for (int i = 0; i < kRuns; ++i) {
-                    b[i] = reaching(bound, v[i], last - (n0 + i * kPieces * 32));
-                    q += __popc(b[i]);
+                for (int r = 0; r < kRuns; ++r) {
+                    b[r] = 0;
+                    if (run[r] >= bound) b[r] = reaching(bound, v[r], last - (n0 + r * kPieces * 32));
+                    q += __popc(b[r]);
                 }
                 if (u > hi) {  // above the bound that leaves too many: these, and as many equals as there is room for
 #pragma unroll
-                    for (int i = 0; i < kRuns; ++i) equal[i] = in[i] & ~b[i], in[i] = b[i];
+                    for (int r = 0; r < kRuns; ++r) equal[r] = in[r] & ~b[r], in[r] = b[r];
                     n = q;
                     break;
                 }
-                if (!begun || q >= alt.k) {
+                if (u == lo || q >= alt.k) {
                     lo = u, n = q;
 #pragma unroll
-                    for (int i = 0; i < kRuns; ++i) in[i] = b[i];
+                    for (int r = 0; r < kRuns; ++r) in[r] = b[r];
+                    if (n <= alt.slots) break;
                 } else {
                     hi = u - 1;
                 }
-                begun = true;
-                done = n <= alt.slots;
-                u = lo + (hi - lo + 1) / 2;
-                if (lo == hi) u = hi + 1;
             }
             Found *to = alt.found + at * alt.slots;
             int room = alt.slots - n;
@@ -305,28 +319,40 @@ __global__ void __launch_bounds__(32 * kFewWarps, kFewBlocks)
     }
 }
 
-// ---- the join: 8 tokens a block, 32 lanes along the pieces of each
+// ---- the join
 
-constexpr int kKept = 256;  // alternatives that a warp sorts at a time
+// With many tokens a block takes 8, a warp's lanes the pieces of each; with few a
+// block takes one.  First the largest logit, then the sums relative to it, then of
+// the alternatives those that reach the k-th of the lanes' largest logits (as many
+// different logits do), a lane whose pieces have none left out.
+// The first gives 32 lanes to a token, the second 256: one token of 608 pieces
+// takes TIME_ONE us instead of TIME_EIGHT.
+constexpr int kJoinThreads = 256, kKept = 256;  // kKept: alternatives that are sorted at a time
 
-// Of the n entries a warp holds in shared memory the first k, in order.
-__device__ __forceinline__ int sort_kept(Found *kept, int n, int k, int lane) {
-    Found f[kKept / 32];
-    int place[kKept / 32];
-    __syncwarp();
+// Of the n entries in shared memory the first k, in order, by THREADS threads (a warp, or the block).
+template <int THREADS>
+__device__ __forceinline__ int sort_kept(Found *kept, int n, int k, int thread) {
+    constexpr int kEach = kKept / THREADS;
+    const auto sync = [] {
+        if (THREADS == 32) __syncwarp();
+        else __syncthreads();
+    };
+    Found f[kEach];
+    int place[kEach];
+    sync();
 #pragma unroll
-    for (int i = 0; i < kKept / 32; ++i) f[i] = kept[i * 32 + lane], place[i] = 0;
+    for (int i = 0; i < kEach; ++i) f[i] = kept[i * THREADS + thread], place[i] = 0;
     for (int j = 0; j < n; ++j) {
         const Found g = kept[j];
 #pragma unroll
-        for (int i = 0; i < kKept / 32; ++i)
-            if (i * 32 < n) place[i] += before(g, f[i]);
+        for (int i = 0; i < kEach; ++i)
+            if (i * THREADS < n) place[i] += before(g, f[i]);
     }
-    __syncwarp();
+    sync();
 #pragma unroll
-    for (int i = 0; i < kKept / 32; ++i)
-        if (i * 32 + lane < n && place[i] < k) kept[place[i]] = f[i];
-    __syncwarp();
+    for (int i = 0; i < kEach; ++i)
+        if (i * THREADS + thread < n && place[i] < k) kept[place[i]] = f[i];
+    sync();
     return min(n, k);
 }
 
@@ -339,22 +365,66 @@ struct JoinArgs {
     int64_t *top_index;
 };
 
-template <bool TOP>
-__global__ void __launch_bounds__(256) k_score_join(const JoinArgs a, const Alternatives alt) {
+// A warp collects and sorts the alternatives that reach `least` of one token's pieces; lanes with `skip` have none.
+__device__ __forceinline__ int collect(const Alternatives &alt, int64_t pieces, int64_t t, float least, bool skip, Found *mine,
+                                       int lane) {
+    const int k = alt.k, slots = alt.slots;
+    const uint8_t *count = alt.count + t * pieces;
+    const Found *found = alt.found + t * pieces * slots;
+    int n = 0;
+    constexpr int kAhead = 4;
+    for (int64_t p0 = 0; p0 < pieces; p0 += 32 * kAhead) {
+        int counts[kAhead];
+#pragma unroll
+        for (int h = 0; h < kAhead; ++h) counts[h] = !skip && p0 + 32 * h + lane < pieces ? count[p0 + 32 * h + lane] : 0;
+#pragma unroll
+        for (int h = 0; h < kAhead; ++h) {
+            const Found *from = found + (p0 + 32 * h + lane) * slots;
+            const int c = counts[h];
+            for (int e = 0; __any_sync(~0u, e < c); e += 2) {
+                // slots are even in number, so that two are 16 aligned bytes
+                Found f[2] = {{kNaN, 0}, {kNaN, 0}};
+                if (e < c) {
+                    const uint4 q = *reinterpret_cast<const uint4 *>(from + e);
+                    f[0] = {__uint_as_float(q.x), (int)q.y};
+                    if (e + 1 < c) f[1] = {__uint_as_float(q.z), (int)q.w};
+                }
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const bool is = f[i].l >= least;
+                    const uint32_t in = __ballot_sync(~0u, is);
+                    if (is) mine[n + __popc(in & ((1u << lane) - 1))] = f[i];
+                    n += __popc(in);
+                    if (n > kKept - 32) {
+                        n = sort_kept<32>(mine, n, k, lane);
+                        least = fmaxf(least, mine[k - 1].l);
+                    }
+                }
+            }
+        }
+    }
+    return sort_kept<32>(mine, n, k, lane);
+}
+
+template <bool TOP, int ROWS>
+__global__ void __launch_bounds__(kJoinThreads) k_score_join(const JoinArgs a, const Alternatives alt) {
+    constexpr int kGroups = kJoinThreads / ROWS;  // threads of a token
+    __shared__ Stats sh[ROWS][kGroups + 1];
+    __shared__ Found keep[TOP ? ROWS : 1][TOP ? kKept : 1];
+    __shared__ int kept;
+    let_next_start();
     after_previous();
-    __shared__ Stats sh[8][33];
-    __shared__ Found keep[TOP ? 8 : 1][TOP ? kKept : 1];
-    // 8 neighbouring tokens are read together; 32 runs of pieces for each
-    const int col = threadIdx.x & 7, run = threadIdx.x >> 3;
-    const int64_t t = (int64_t)blockIdx.x * 8 + col;
+    // neighbouring tokens are read together
+    const int col = threadIdx.x % ROWS, run = threadIdx.x / ROWS;
+    const int64_t t = (int64_t)blockIdx.x * ROWS + col;
     Stats x{kNegInf, 0.f, 0.f};
     if (t < a.T) {
-        constexpr int kAhead = 8;
-        for (int64_t i = run; i < a.pieces; i += 32 * kAhead) {
+        constexpr int kAhead = ROWS == 1 ? 4 : 8;
+        for (int64_t i = run; i < a.pieces; i += kGroups * kAhead) {
             Stats p[kAhead];
 #pragma unroll
             for (int j = 0; j < kAhead; ++j) {
-                const int64_t k = i + 32 * j;
+                const int64_t k = i + kGroups * j;
                 p[j] = k < a.pieces ? a.part[k * a.T + t] : Stats{kNegInf, 0.f, 0.f};
             }
             float top = x.m;
@@ -371,12 +441,16 @@ __global__ void __launch_bounds__(256) k_score_join(const JoinArgs a, const Alte
         }
     }
     sh[col][run] = x;
+    if (threadIdx.x == 0) kept = 0;
     __syncthreads();
-    const int lane = threadIdx.x & 31, row = threadIdx.x >> 5;
-    const int64_t u = (int64_t)blockIdx.x * 8 + row;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, row = ROWS == 1 ? 0 : warp;
+    const int64_t u = (int64_t)blockIdx.x * ROWS + row;
+    // a token's warp adds its parts up: lane i has those of threads i, i + 32, ...
     x = sh[row][lane];
+#pragma unroll
+    for (int i = 32; i < kGroups; i += 32) x = add(x, sh[row][i + lane]);
     float m = x.m;
-    [[maybe_unused]] const float best = x.m;  // of the lane's pieces
+    const float of_lane = m;
 #pragma unroll
     for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
     const float ref = ref_of(m);
@@ -388,51 +462,48 @@ __global__ void __launch_bounds__(256) k_score_join(const JoinArgs a, const Alte
     }
     if (u >= a.T) return;
     const float logs = logf(x.s), lse = ref + logs;
-    if (lane == 0) {
+    if (lane == 0 && (ROWS > 1 || warp == 0)) {
         if (a.lse) a.lse[u] = lse;
         if (a.entropy) a.entropy[u] = logs - x.u * kLn2 / x.s;
         if (a.logp) a.logp[u] = inside(a.target[u], a.V) ? a.picked[u] - lse : 0.f;
     }
     if constexpr (TOP) {
-        const int k = alt.k, slots = alt.slots;
-        const uint8_t *count = alt.count + u * a.pieces;
-        const Found *found = alt.found + u * a.pieces * slots;
-        // k different logits reach the k-th of the lanes' largest; and the classes' bound
-        int place = 0;
-        for (int i = 0; i < 32; ++i) {
-            const float b = __shfl_sync(~0u, best, i);
-            place += b > best || (b == best && i < lane);
-        }
-        float least = __shfl_sync(~0u, best, __ffs(__ballot_sync(~0u, place == k - 1)) - 1);
-        if (alt.least)
-            least = fmaxf(least, from_ordered(__reduce_min_sync(~0u, lane < k ? alt.least[lane * a.T + u] : ~0u)));
+        const int k = alt.k;
         Found *mine = keep[row];
-        int n = 0;
-        constexpr int kAhead = 4;
-        for (int64_t p0 = 0; p0 < a.pieces; p0 += 32 * kAhead) {
-            int counts[kAhead];
-#pragma unroll
-            for (int h = 0; h < kAhead; ++h) counts[h] = p0 + 32 * h + lane < a.pieces ? count[p0 + 32 * h + lane] : 0;
-#pragma unroll
-            for (int h = 0; h < kAhead; ++h) {
-                const Found *from = found + (p0 + 32 * h + lane) * slots;
-                int c = counts[h];
-                for (int e = 0; __any_sync(~0u, e < c); ++e) {
-                    Found f{kNaN, 0};
-                    if (e < c) f = from[e];
-                    const bool is = f.l >= least;
-                    if (!is && !alt.least) c = 0;  // nor are those behind it
-                    const uint32_t in = __ballot_sync(~0u, is);
-                    if (is) mine[n + __popc(in & ((1u << lane) - 1))] = f;
-                    n += __popc(in);
-                    if (n > kKept - 32) {
-                        n = sort_kept(mine, n, k, lane);
-                        least = fmaxf(least, mine[k - 1].l);
+        int n, place = 0;
+        // k different logits reach the k-th of the lanes' largest
+        for (int i = 0; i < 32; ++i) {
+            const float b = __shfl_sync(~0u, of_lane, i);
+            place += b > of_lane || (b == of_lane && i < lane);
+        }
+        float least = __shfl_sync(~0u, of_lane, __ffs(__ballot_sync(~0u, place == k - 1)) - 1);
+        if (ROWS > 1) {
+            if (alt.least)
+                least = fmaxf(least, from_ordered(__reduce_min_sync(~0u, lane < k ? alt.least[lane * a.T + u] : ~0u)));
+            n = collect(alt, a.pieces, u, least, !(of_lane >= least), mine, lane);
+        } else {
+            // the largest of this thread's pieces, which it looks through if any is large enough
+            if (sh[0][threadIdx.x].m >= least)
+                for (int64_t p = threadIdx.x; p < a.pieces; p += kGroups) {
+                    const int64_t at = u * a.pieces + p;
+                    const int c = alt.count[at];
+                    for (int e = 0; e < c; ++e) {
+                        const Found f = alt.found[at * alt.slots + e];
+                        if (f.l >= least) {
+                            const int to = atomicAdd(&kept, 1);
+                            if (to < kKept) mine[to] = f;
+                        }
                     }
                 }
+            __syncthreads();
+            n = kept;
+            if (n <= kKept) {
+                n = sort_kept<kJoinThreads>(mine, n, k, threadIdx.x);
+            } else if (warp == 0) {  // many equals
+                n = collect(alt, a.pieces, u, least, !(of_lane >= least), mine, lane);
             }
+            if (warp) return;
         }
-        n = sort_kept(mine, n, k, lane);
         if (lane < k) {
             // a row with fewer numbers than that has a NaN
             a.top_logp[u * k + lane] = lane < n ? mine[lane].l - lse : kNaN;
@@ -474,7 +545,7 @@ ScoreSpace score_space(void *ws, const uint16_t *x, int64_t sx, const uint16_t *
     Carve c{static_cast<unsigned char *>(ws)};
     ScoreSpace s{};
     s.few = few_tokens(T, H);
-    s.alt.k = k, s.alt.slots = s.few ? k : k + kMoreSlots;
+    s.alt.k = k, s.alt.slots = (s.few ? k : k + kMoreSlots) + 1 & ~1;
     s.each = T;
     int64_t pieces;
     if (s.few) {
@@ -534,8 +605,10 @@ int score(const ScoreSpace &s, const uint16_t *x, int64_t sx, const uint16_t *w,
                                                     ScoreEpi<TOP>{target + t0, n, V, s.part, s.picked, alt}, plan, stream);
         }
         const auto from = [&](auto *p, int64_t each) { return p ? p + t0 * each : p; };
+        const bool one = n <= 4 * (int64_t)sm_count();  // all blocks run at once
         if (rc == PP_OK)
-            rc = launch_after(k_score_join<TOP>, ceil_div(n, 8), 256, 0, stream, 1,
+            rc = launch_after(one ? k_score_join<TOP, 1> : k_score_join<TOP, 8>, one ? n : ceil_div(n, 8), kJoinThreads, 0,
+                              stream, 1,
                               JoinArgs{s.part, s.picked, target + t0, alt.pieces, n, V, from(logp, 1), from(lse, 1),
                                        from(entropy, 1), from(top_logp, k), from(top_index, k)},
                               alt);
