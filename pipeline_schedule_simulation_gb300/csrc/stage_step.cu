@@ -75,6 +75,39 @@ __device__ __forceinline__ float decode(uint32_t code, int from) {
     return code ? __uint_as_float((uint32_t)max((int)code + from, 0) << 20) : 0.f;
 }
 
+// Two at a time, in the halves of a word, where nothing leaves the window: a
+// number's upper 16 bits are 16 times its code counted from 0.  An element of
+// 10 bytes (all in 16 bits, moments in 8) leaves an SM some 55 instructions a
+// lane at the memory's rate, half of them at most whole-number ones.
+struct Window {
+    int exp, from;
+    // codes of a block are read two at a time unless it holds NaN or numbers below 2^-96 and the like
+    __device__ __forceinline__ bool reads(uint2 c, uint32_t sign) const {
+        return exp != kBlockNaN && (from >= 0 || ((c.x | c.y) & ~sign) == 0);
+    }
+    // and written, unless its largest is not finite, or as large or small as that
+    __device__ __forceinline__ bool writes() const { return from >= 0 && exp < 254; }
+};
+__device__ __forceinline__ Window window_of_block(int exp, int window) { return {exp, window_of(exp, window)}; }
+__device__ __forceinline__ uint32_t both(int x) { return (uint32_t)x * 0x10001u; }
+// The upper halves of two floats from two codes without sign.
+__device__ __forceinline__ uint32_t decode2(uint32_t codes, int from) {
+    return __vminu2(codes, 0x10001u) * (uint32_t)(from * 16) + codes * 16;
+}
+// Codes without sign from two magnitudes, rounded (r was added); `least` where they are less.
+__device__ __forceinline__ uint32_t encode2(uint32_t a, uint32_t b, int from, int least) {
+    const uint32_t t = __byte_perm(a, b, 0x7632) >> 4 & 0x0FFF0FFFu;
+    return __vmaxu2(t, both(from + least)) - both(from);
+}
+
+constexpr float kNaN = __builtin_nanf("");
+
+// The root is a normal number or 0 whatever x is, so what is below 2^-126 plays no part in the reciprocal.
+__device__ __forceinline__ float reciprocal(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
 __device__ __forceinline__ float root(float x) {
     float y;
     asm("sqrt.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -169,83 +202,137 @@ struct Rates {
     int random;
 };
 
+// 8 codes' numbers, a sign in bit 7 of each byte where SIGN.
+template <int WINDOW, bool SIGN>
+__device__ __forceinline__ void read_codes(uint2 c, int exp, float (&x)[8]) {
+    const Window w = window_of_block(exp, WINDOW);
+    constexpr uint32_t kSign = SIGN ? 0x80u : 0u;
+    if (w.reads(c, kSign * 0x01010101u)) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const uint32_t two = __byte_perm(j < 2 ? c.x : c.y, 0, j & 1 ? 0x4342 : 0x4140);
+            uint32_t h = decode2(SIGN ? two & 0x007F007Fu : two, w.from);
+            if (SIGN) h |= (two & 0x00800080u) << 8;
+            x[2 * j] = __uint_as_float(h << 16), x[2 * j + 1] = __uint_as_float(h & 0xFFFF0000u);
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const uint32_t b = (j < 4 ? c.x : c.y) >> (8 * (j & 3)) & 255;
+            x[j] = exp == kBlockNaN ? kNaN : __uint_as_float(__float_as_uint(decode(b & ~kSign & 255, w.from)) | (b & kSign) << 24);
+        }
+    }
+}
+// Codes of 8 numbers; largest: the bits of the block's largest magnitude, r: what is added before bits are cut off.
+template <int WINDOW, bool SIGN, class R>
+__device__ __forceinline__ uint2 write_codes(const float (&x)[8], uint32_t largest, int exp, const R &r) {
+    const Window w = window_of_block(exp, WINDOW);
+    constexpr int kLeast = SIGN ? 0 : 1, kMost = SIGN ? 127 : 255;
+    if (largest == 0 || exp == kBlockNaN) return make_uint2(0, 0);
+    uint32_t least = ~0u;  // a code of 0 stands for 0 alone where there is no sign
+    if (!SIGN) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) least = min(least, __float_as_uint(x[j]));
+    }
+    if (w.writes() && least) {
+        uint32_t h[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const uint32_t a = __float_as_uint(x[2 * j]), b = __float_as_uint(x[2 * j + 1]);
+            constexpr uint32_t kSize = SIGN ? 0x7FFFFFFFu : ~0u;
+            h[j] = encode2((a & kSize) + r(2 * j), (b & kSize) + r(2 * j + 1), w.from, kLeast);
+            if (SIGN) h[j] |= __byte_perm(a, b, 0x7632) >> 8 & 0x00800080u;
+        }
+        return make_uint2(__byte_perm(h[0], h[1], 0x6420), __byte_perm(h[2], h[3], 0x6420));
+    }
+    uint32_t c[2] = {};
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const uint32_t a = __float_as_uint(x[j]);
+        uint32_t b = 0;
+        if (SIGN || a) b = encode(SIGN ? a & 0x7FFFFFFFu : a, r(j), w.from, kLeast, kMost);
+        if (SIGN) b |= a >> 24 & 128;
+        c[j >> 2] |= b << (8 * (j & 3));
+    }
+    return make_uint2(c[0], c[1]);
+}
+// The bits of the largest magnitude, those of a NaN above all others, of the block that 8 lanes hold.
+__device__ __forceinline__ uint32_t largest_of_block(const float (&x)[8]) {
+    float a = fabsf(x[0]);
+#pragma unroll
+    for (int j = 1; j < 8; ++j) asm("max.NaN.f32 %0, %0, %1;" : "+f"(a) : "f"(fabsf(x[j])));
+    uint32_t b = __float_as_uint(a);
+#pragma unroll
+    for (int o = 4; o; o >>= 1) b = max(b, __shfl_xor_sync(~0u, b, o));
+    return b;
+}
+
 // 8 elements of one tensor, from element i on, of which n exist; held: whether
 // they have moments (whole blocks, past the tensor's end as well).  In 8 bits the
 // 8 lanes of an aligned group have one block, and all lanes of a warp are here.
 template <class P, class G, bool SMALL, bool VEC>
 __device__ __forceinline__ void step_unit(const Entry &e, int64_t i, int n, bool held, const Moments &mo, const Rates &r,
-                                          const StepNow &now) {
+                                          const StepNow *step) {
     float p[8], g[8], m[8], v[8];
     const int64_t at = (int64_t)e.at * kMoments + i;
     const uint32_t block = e.at + (uint32_t)(i / kMoments);
+    uint2 cm = make_uint2(0, 0), cv = make_uint2(0, 0);
+    int em = 0, ev = 0;
+    if (SMALL && held) {
+        cm = *reinterpret_cast<const uint2 *>(static_cast<const uint8_t *>(mo.m) + at);
+        cv = *reinterpret_cast<const uint2 *>(static_cast<const uint8_t *>(mo.v) + at);
+        em = mo.m_exp[block], ev = mo.v_exp[block];
+    }
     load<VEC>(static_cast<const P *>(e.p) + i, n, p);
     load<VEC>(static_cast<const G *>(e.g) + i, n, g);
+    const StepNow now = *step;
     if constexpr (SMALL) {
-        uint2 cm = make_uint2(0, 0), cv = make_uint2(0, 0);
-        int em = 0, ev = 0;
-        if (held) {
-            cm = *reinterpret_cast<const uint2 *>(static_cast<const uint8_t *>(mo.m) + at);
-            cv = *reinterpret_cast<const uint2 *>(static_cast<const uint8_t *>(mo.v) + at);
-            em = mo.m_exp[block], ev = mo.v_exp[block];
-        }
-        const int fm = window_of(em, kWindowM), fv = window_of(ev, kWindowV);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const uint32_t bm = (j < 4 ? cm.x : cm.y) >> (8 * (j & 3)) & 255, bv = (j < 4 ? cv.x : cv.y) >> (8 * (j & 3)) & 255;
-            m[j] = em == kBlockNaN ? __uint_as_float(0x7FC00000u)
-                                   : __uint_as_float(__float_as_uint(decode(bm & 127, fm)) | (bm & 128) << 24);
-            v[j] = ev == kBlockNaN ? __uint_as_float(0x7FC00000u) : decode(bv, fv);
-        }
+        read_codes<kWindowM, true>(cm, em, m);
+        read_codes<kWindowV, false>(cv, ev, v);
     } else {
         load<true>(static_cast<const float *>(mo.m) + at, 8, m);
         load<true>(static_cast<const float *>(mo.v) + at, 8, v);
     }
+    if (!now.go) return;
+    if (!VEC) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (j >= n) g[j] = m[j] = v[j] = 0.f;  // nothing is kept past the tensor's end
+    }
     const float shrink = -now.lr * e.decay;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        if (j >= n) g[j] = m[j] = v[j] = 0.f;  // nothing is kept past the tensor's end
-        const float x = __fmul_rn(g[j], now.clip);
-        m[j] = __fadd_rn(__fmul_rn(r.b1, m[j]), __fmul_rn(r.c1, x));
-        v[j] = __fadd_rn(__fmul_rn(r.b2, v[j]), __fmul_rn(r.c2, __fmul_rn(x, x)));
-        p[j] = fmaf(p[j], shrink, p[j]) - now.size * __fdividef(m[j], fmaf(root(v[j]), now.root, r.eps));
+    for (int j = 0; j < 8; j += 2) {
+        // products and sums rounded apart, as written above
+        const float2 x = __fmul2_rn({g[j], g[j + 1]}, {now.clip, now.clip});
+        const float2 a = __fadd2_rn(__fmul2_rn({r.b1, r.b1}, {m[j], m[j + 1]}), __fmul2_rn({r.c1, r.c1}, x));
+        const float2 b = __fadd2_rn(__fmul2_rn({r.b2, r.b2}, {v[j], v[j + 1]}), __fmul2_rn({r.c2, r.c2}, __fmul2_rn(x, x)));
+        const float2 den = __ffma2_rn({root(b.x), root(b.y)}, {now.root, now.root}, {r.eps, r.eps});
+        const float2 q = __fmul2_rn(a, {reciprocal(den.x), reciprocal(den.y)});
+        const float2 y = __ffma2_rn({p[j], p[j + 1]}, {shrink, shrink}, {p[j], p[j + 1]});
+        const float2 z = __ffma2_rn(q, {-now.size, -now.size}, y);
+        m[j] = a.x, m[j + 1] = a.y, v[j] = b.x, v[j + 1] = b.y, p[j] = z.x, p[j + 1] = z.y;
     }
-    [[maybe_unused]] uint32_t bits[8];
     constexpr bool kRound = sizeof(P) == 2;
+    [[maybe_unused]] uint32_t bits[8];
     if ((SMALL || kRound) && r.random) {
         const uint32_t key = block_key(now.key, block);
 #pragma unroll
         for (int j = 0; j < 8; ++j) bits[j] = random_bits(key, (uint32_t)(i % kMoments) + j);
     }
     if constexpr (SMALL) {
-        uint32_t tm = 0, tv = 0;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            tm = max(tm, __float_as_uint(m[j]) & 0x7FFFFFFFu);
-            tv = max(tv, __float_as_uint(v[j]) & 0x7FFFFFFFu);
+        const uint32_t tm = largest_of_block(m), tv = largest_of_block(v);
+        const int em1 = moments_exp(tm), ev1 = moments_exp(tv);
+        if (r.random) {
+            cm = write_codes<kWindowM, true>(m, tm, em1, [&](int j) { return (bits[j] << 4 & 0xFFFF0u) + 8; });
+            cv = write_codes<kWindowV, false>(v, tv, ev1, [&](int j) { return (bits[j] >> 12 & 0xFFFF0u) + 8; });
+        } else {
+            cm = write_codes<kWindowM, true>(m, tm, em1, [](int) { return kNearest; });
+            cv = write_codes<kWindowV, false>(v, tv, ev1, [](int) { return kNearest; });
         }
-#pragma unroll
-        for (int o = 4; o; o >>= 1) {
-            tm = max(tm, __shfl_xor_sync(~0u, tm, o));
-            tv = max(tv, __shfl_xor_sync(~0u, tv, o));
-        }
-        const int em = moments_exp(tm), ev = moments_exp(tv), fm = window_of(em, kWindowM), fv = window_of(ev, kWindowV);
-        uint32_t wm[2] = {}, wv[2] = {};
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const uint32_t rm = r.random ? ((bits[j] & 0xFFFFu) << 4) + 8 : kNearest;
-            const uint32_t rv = r.random ? (bits[j] >> 16 << 4) + 8 : kNearest;
-            const uint32_t um = __float_as_uint(m[j]), uv = __float_as_uint(v[j]);
-            uint32_t a = encode(um & 0x7FFFFFFFu, rm, fm, 0, 127) | um >> 24 & 128;
-            uint32_t b = uv ? encode(uv, rv, fv, 1, 255) : 0;
-            if (um == 0x80000000u) a = 0;
-            wm[j >> 2] |= a << (8 * (j & 3)), wv[j >> 2] |= b << (8 * (j & 3));
-        }
-        if (em == kBlockNaN) wm[0] = wm[1] = 0;
-        if (ev == kBlockNaN) wv[0] = wv[1] = 0;
         if (held) {
-            *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(mo.m) + at) = make_uint2(wm[0], wm[1]);
-            *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(mo.v) + at) = make_uint2(wv[0], wv[1]);
-            if (i % kMoments == 0) mo.m_exp[block] = (uint8_t)em, mo.v_exp[block] = (uint8_t)ev;
+            *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(mo.m) + at) = cm;
+            *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(mo.v) + at) = cv;
+            if (i % kMoments == 0) mo.m_exp[block] = (uint8_t)em1, mo.v_exp[block] = (uint8_t)ev1;
         }
     } else {
         store<true>(static_cast<float *>(mo.m) + at, 8, m);
@@ -255,8 +342,8 @@ __device__ __forceinline__ void step_unit(const Entry &e, int64_t i, int n, bool
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             // up with the probability of what is cut off; an infinity or a NaN stays what it is
-            const uint32_t b = __float_as_uint(p[j]);
-            if ((b & 0x7F800000u) != 0x7F800000u) p[j] = __uint_as_float((b + more_bits(bits[j])) & 0xFFFF0000u);
+            const uint32_t b = __float_as_uint(p[j]) + more_bits(bits[j]);
+            if (p[j] == p[j]) p[j] = __uint_as_float(b & 0xFFFF0000u);
         }
     }
     store<VEC>(static_cast<P *>(e.p) + i, n, p);
@@ -270,15 +357,13 @@ __global__ void __launch_bounds__(kThreads) k_step(const __grid_constant__ Entri
     const Entry &e = entry_of(t, blockIdx.x);
     const int64_t i = (int64_t)(blockIdx.x - e.first) * kChunk + threadIdx.x * kUnit;
     after_previous();
-    const StepNow now = *at;
-    if (!now.go) return;
     const int n = i >= e.n ? 0 : e.n - i < kUnit ? (int)(e.n - i) : kUnit;
     const bool held = i < (e.n + kMoments - 1) / kMoments * kMoments;
     bool wide = e.vec && n == kUnit;
     if constexpr (SMALL) wide = __all_sync(~0u, wide);  // a warp goes one way: its lanes shuffle
     else if (!held) return;
-    if (wide) step_unit<P, G, SMALL, true>(e, i, n, held, mo, r, now);
-    else step_unit<P, G, SMALL, false>(e, i, n, held, mo, r, now);
+    if (wide) step_unit<P, G, SMALL, true>(e, i, n, held, mo, r, at);
+    else step_unit<P, G, SMALL, false>(e, i, n, held, mo, r, at);
 }
 
 // The step's number goes up, and all that depends on it is computed, in 64 bits.
@@ -368,17 +453,11 @@ __global__ void __launch_bounds__(kThreads) k_moments(const Moments mo, int64_t 
     if (i >= n) return;
     const uint2 cm = *reinterpret_cast<const uint2 *>(static_cast<const uint8_t *>(mo.m) + i);
     const uint2 cv = *reinterpret_cast<const uint2 *>(static_cast<const uint8_t *>(mo.v) + i);
-    const int em = mo.m_exp[i / kMoments], ev = mo.v_exp[i / kMoments];
-    const int fm = window_of(em, kWindowM), fv = window_of(ev, kWindowV);
-    uint32_t a[8], b[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        const uint32_t bm = (j < 4 ? cm.x : cm.y) >> (8 * (j & 3)) & 255, bv = (j < 4 ? cv.x : cv.y) >> (8 * (j & 3)) & 255;
-        a[j] = em == kBlockNaN ? 0x7FC0u : __float_as_uint(decode(bm & 127, fm)) >> 16 | (bm & 128) << 8;
-        b[j] = ev == kBlockNaN ? 0x7FC0u : __float_as_uint(decode(bv, fv)) >> 16;
-    }
-    *reinterpret_cast<uint4 *>(m + i) = make_uint4(a[0] | a[1] << 16, a[2] | a[3] << 16, a[4] | a[5] << 16, a[6] | a[7] << 16);
-    *reinterpret_cast<uint4 *>(v + i) = make_uint4(b[0] | b[1] << 16, b[2] | b[3] << 16, b[4] | b[5] << 16, b[6] | b[7] << 16);
+    float x[8];
+    read_codes<kWindowM, true>(cm, mo.m_exp[i / kMoments], x);
+    store<true>(m + i, 8, x);
+    read_codes<kWindowV, false>(cv, mo.v_exp[i / kMoments], x);
+    store<true>(v + i, 8, x);
 }
 
 // ---- host side
