@@ -108,9 +108,11 @@ __device__ __forceinline__ float reciprocal(float x) {
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+template <bool NORMAL>
 __device__ __forceinline__ float root(float x) {
     float y;
-    asm("sqrt.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+    if (NORMAL) asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    else asm("sqrt.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
 
@@ -159,6 +161,21 @@ __device__ __forceinline__ void store(uint16_t *p, int n, const float (&v)[8]) {
 #pragma unroll
         for (int j = 0; j < 8; ++j)
             if (j < n) p[j] = f32_to_bf16(v[j]);
+    }
+}
+
+// The upper halves of 8 floats.
+template <bool VEC>
+__device__ __forceinline__ void store_cut(uint16_t *p, int n, const float (&v)[8]) {
+    uint32_t w[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) w[j] = __byte_perm(__float_as_uint(v[2 * j]), __float_as_uint(v[2 * j + 1]), 0x7632);
+    if (VEC) {
+        *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (j < n) p[j] = (uint16_t)(w[j >> 1] >> (16 * (j & 1)));
     }
 }
 
@@ -223,18 +240,14 @@ __device__ __forceinline__ void read_codes(uint2 c, int exp, float (&x)[8]) {
         }
     }
 }
-// Codes of 8 numbers; largest: the bits of the block's largest magnitude, r: what is added before bits are cut off.
+// Codes of 8 numbers; largest: the bits of the block's largest magnitude, r: what is added before bits are cut off;
+// zero: where there is no sign, whether some may be 0, which alone a code of 0 stands for.
 template <int WINDOW, bool SIGN, class R>
-__device__ __forceinline__ uint2 write_codes(const float (&x)[8], uint32_t largest, int exp, const R &r) {
+__device__ __forceinline__ uint2 write_codes(const float (&x)[8], uint32_t largest, int exp, bool zero, const R &r) {
     const Window w = window_of_block(exp, WINDOW);
     constexpr int kLeast = SIGN ? 0 : 1, kMost = SIGN ? 127 : 255;
     if (largest == 0 || exp == kBlockNaN) return make_uint2(0, 0);
-    uint32_t least = ~0u;  // a code of 0 stands for 0 alone where there is no sign
-    if (!SIGN) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) least = min(least, __float_as_uint(x[j]));
-    }
-    if (w.writes() && least) {
+    if (w.writes() && !zero) {
         uint32_t h[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -258,13 +271,21 @@ __device__ __forceinline__ uint2 write_codes(const float (&x)[8], uint32_t large
 }
 // The bits of the largest magnitude, those of a NaN above all others, of the block that 8 lanes hold.
 __device__ __forceinline__ uint32_t largest_of_block(const float (&x)[8]) {
-    float a = fabsf(x[0]);
+    float a = fabsf(x[7]);
 #pragma unroll
-    for (int j = 1; j < 8; ++j) asm("max.NaN.f32 %0, %0, %1;" : "+f"(a) : "f"(fabsf(x[j])));
+    for (int j = 0; j < 3; ++j)
+        asm("max.NaN.f32 %0, %0, %1, %2;" : "+f"(a) : "f"(fabsf(x[2 * j])), "f"(fabsf(x[2 * j + 1])));
+    asm("max.NaN.f32 %0, %0, %1;" : "+f"(a) : "f"(fabsf(x[6])));
     uint32_t b = __float_as_uint(a);
 #pragma unroll
     for (int o = 4; o; o >>= 1) b = max(b, __shfl_xor_sync(~0u, b, o));
     return b;
+}
+__device__ __forceinline__ float least_of(const float (&x)[8]) {
+    float a = x[7];
+#pragma unroll
+    for (int j = 0; j < 3; ++j) asm("min.f32 %0, %0, %1, %2;" : "+f"(a) : "f"(x[2 * j]), "f"(x[2 * j + 1]));
+    return fminf(a, x[6]);
 }
 
 // 8 elements of one tensor, from element i on, of which n exist; held: whether
@@ -299,18 +320,31 @@ __device__ __forceinline__ void step_unit(const Entry &e, int64_t i, int n, bool
         for (int j = 0; j < 8; ++j)
             if (j >= n) g[j] = m[j] = v[j] = 0.f;  // nothing is kept past the tensor's end
     }
-    const float shrink = -now.lr * e.decay;
 #pragma unroll
     for (int j = 0; j < 8; j += 2) {
         // products and sums rounded apart, as written above
         const float2 x = __fmul2_rn({g[j], g[j + 1]}, {now.clip, now.clip});
         const float2 a = __fadd2_rn(__fmul2_rn({r.b1, r.b1}, {m[j], m[j + 1]}), __fmul2_rn({r.c1, r.c1}, x));
         const float2 b = __fadd2_rn(__fmul2_rn({r.b2, r.b2}, {v[j], v[j + 1]}), __fmul2_rn({r.c2, r.c2}, __fmul2_rn(x, x)));
-        const float2 den = __ffma2_rn({root(b.x), root(b.y)}, {now.root, now.root}, {r.eps, r.eps});
-        const float2 q = __fmul2_rn(a, {reciprocal(den.x), reciprocal(den.y)});
+        m[j] = a.x, m[j + 1] = a.y, v[j] = b.x, v[j + 1] = b.y;
+    }
+    const bool tiny = !(least_of(v) >= 0x1p-126f);  // no normal numbers, or 0
+    float d[8];
+    if (tiny) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) d[j] = root<false>(v[j]);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) d[j] = root<true>(v[j]);
+    }
+    const float shrink = -now.lr * e.decay;
+#pragma unroll
+    for (int j = 0; j < 8; j += 2) {
+        const float2 den = __ffma2_rn({d[j], d[j + 1]}, {now.root, now.root}, {r.eps, r.eps});
+        const float2 q = __fmul2_rn({m[j], m[j + 1]}, {reciprocal(den.x), reciprocal(den.y)});
         const float2 y = __ffma2_rn({p[j], p[j + 1]}, {shrink, shrink}, {p[j], p[j + 1]});
         const float2 z = __ffma2_rn(q, {-now.size, -now.size}, y);
-        m[j] = a.x, m[j + 1] = a.y, v[j] = b.x, v[j + 1] = b.y, p[j] = z.x, p[j + 1] = z.y;
+        p[j] = z.x, p[j + 1] = z.y;
     }
     constexpr bool kRound = sizeof(P) == 2;
     [[maybe_unused]] uint32_t bits[8];
@@ -323,11 +357,11 @@ __device__ __forceinline__ void step_unit(const Entry &e, int64_t i, int n, bool
         const uint32_t tm = largest_of_block(m), tv = largest_of_block(v);
         const int em1 = moments_exp(tm), ev1 = moments_exp(tv);
         if (r.random) {
-            cm = write_codes<kWindowM, true>(m, tm, em1, [&](int j) { return (bits[j] << 4 & 0xFFFF0u) + 8; });
-            cv = write_codes<kWindowV, false>(v, tv, ev1, [&](int j) { return (bits[j] >> 12 & 0xFFFF0u) + 8; });
+            cm = write_codes<kWindowM, true>(m, tm, em1, false, [&](int j) { return (bits[j] << 4 & 0xFFFF0u) + 8; });
+            cv = write_codes<kWindowV, false>(v, tv, ev1, tiny, [&](int j) { return (bits[j] >> 12 & 0xFFFF0u) + 8; });
         } else {
-            cm = write_codes<kWindowM, true>(m, tm, em1, [](int) { return kNearest; });
-            cv = write_codes<kWindowV, false>(v, tv, ev1, [](int) { return kNearest; });
+            cm = write_codes<kWindowM, true>(m, tm, em1, false, [](int) { return kNearest; });
+            cv = write_codes<kWindowV, false>(v, tv, ev1, tiny, [](int) { return kNearest; });
         }
         if (held) {
             *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(mo.m) + at) = cm;
@@ -339,27 +373,31 @@ __device__ __forceinline__ void step_unit(const Entry &e, int64_t i, int n, bool
         store<true>(static_cast<float *>(mo.v) + at, 8, v);
     }
     if (kRound && r.random) {
+        // up with the probability of what is cut off; a NaN stays what it is (so does an infinity)
+        const float any = ((p[0] + p[1]) + (p[2] + p[3])) + ((p[4] + p[5]) + (p[6] + p[7]));
+        const bool check = any != any;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            // up with the probability of what is cut off; an infinity or a NaN stays what it is
             const uint32_t b = __float_as_uint(p[j]) + more_bits(bits[j]);
-            if (p[j] == p[j]) p[j] = __uint_as_float(b & 0xFFFF0000u);
+            if (!check || p[j] == p[j]) p[j] = __uint_as_float(b);
         }
+        store_cut<VEC>(static_cast<uint16_t *>(e.p) + i, n, p);
+        return;
     }
     store<VEC>(static_cast<P *>(e.p) + i, n, p);
     if (e.copy) store<VEC>(e.copy + i, n, p);
 }
 
 template <class P, class G, bool SMALL, int N>
-__global__ void __launch_bounds__(kThreads) k_step(const __grid_constant__ Entries<N> t, const Moments mo, const Rates r,
+__global__ void __launch_bounds__(kThreads, SMALL ? 4 : 3) k_step(const __grid_constant__ Entries<N> t, const Moments mo, const Rates r,
                                                    const StepNow *at) {
     let_next_start();
     const Entry &e = entry_of(t, blockIdx.x);
     const int64_t i = (int64_t)(blockIdx.x - e.first) * kChunk + threadIdx.x * kUnit;
-    after_previous();
     const int n = i >= e.n ? 0 : e.n - i < kUnit ? (int)(e.n - i) : kUnit;
     const bool held = i < (e.n + kMoments - 1) / kMoments * kMoments;
     bool wide = e.vec && n == kUnit;
+    after_previous();
     if constexpr (SMALL) wide = __all_sync(~0u, wide);  // a warp goes one way: its lanes shuffle
     else if (!held) return;
     if (wide) step_unit<P, G, SMALL, true>(e, i, n, held, mo, r, at);
@@ -615,5 +653,5 @@ extern "C" int pp_stage_adamw_moments(const uint8_t *m, const uint8_t *v, const 
     if (!m || !v || !m_exp || !v_exp || !m_values || !v_values) return PP_ERR_ARG;
     if (!aligned_to(m, 8) || !aligned_to(v, 8) || !aligned_to(m_values, 16) || !aligned_to(v_values, 16)) return PP_ERR_ARG;
     const Moments mo{(void *)m, (void *)v, (uint8_t *)m_exp, (uint8_t *)v_exp};
-    return launch_after(k_moments, ceil_div(held, kChunk), kThreads, 0, stream, 1, mo, held, m_values, v_values);
+    return launch_after(k_moments, ceil_div(held, kThreads * kUnit), kThreads, 0, stream, 1, mo, held, m_values, v_values);
 }
