@@ -56,9 +56,10 @@ __device__ __forceinline__ void few_load(float4 *xs, const uint16_t *x, int64_t 
     }
     __syncthreads();
 }
-// Logits of rows first .. last-1 of w, a warp's: take(t, v, l) in all its lanes, v ascending.
+// Products with rows first .. last-1 of w, a warp's, kFewRows at a time: take(v0, acc) with the lanes' parts of the sums
+// (rows from `last` on are copies of the last).
 template <int NT, bool VEC, class Take>
-__device__ __forceinline__ void few_logits(const float4 *xs, const uint16_t *w, int64_t stride_w, int H, int64_t first,
+__device__ __forceinline__ void few_dots(const float4 *xs, const uint16_t *w, int64_t stride_w, int H, int64_t first,
                                            int64_t last, const Take &take) {
     const int chunks = (H + 7) / 8, lane = threadIdx.x & 31;
     for (int64_t v0 = first; v0 < last; v0 += kFewRows) {
@@ -87,6 +88,14 @@ __device__ __forceinline__ void few_logits(const float4 *xs, const uint16_t *w, 
                 }
             }
         }
+        take(v0, acc);
+    }
+}
+// Logits of rows first .. last-1 of w: take(t, v, l) in all lanes, v ascending.
+template <int NT, bool VEC, class Take>
+__device__ __forceinline__ void few_logits(const float4 *xs, const uint16_t *w, int64_t stride_w, int H, int64_t first,
+                                           int64_t last, const Take &take) {
+    few_dots<NT, VEC>(xs, w, stride_w, H, first, last, [&](int64_t v0, const float (&acc)[kFewRows][NT]) {
 #pragma unroll
         for (int r = 0; r < kFewRows; ++r) {
 #pragma unroll
@@ -97,7 +106,7 @@ __device__ __forceinline__ void few_logits(const float4 *xs, const uint16_t *w, 
                 if (v0 + r < last) take(t, v0 + r, l);
             }
         }
-    }
+    });
 }
 
 inline bool few_tokens(int64_t T, int64_t H) { return T <= kFewTokens && T * round_up(H, 8) <= kFewFloats; }

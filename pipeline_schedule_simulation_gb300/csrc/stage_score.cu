@@ -242,79 +242,116 @@ struct ScoreEpi {
 };
 static_assert(kRuns == 4);
 
-// ---- few tokens (few_logits): a warp keeps its k largest in its lanes, in order;
-// a block is one piece.
+// ---- few tokens (few_dots): a block's logits go to shared memory, and when all are
+// there its threads take the statistics and each logit's place; a block is one
+// piece.  (With both in the loop over the rows of w, in all lanes, two tokens on
+// 131072 x 4096 with 8 alternatives took 211 us, 169 without those.)
+constexpr int kFewMost = 1024;  // rows of w to a block
+
+// Sums over the warp's lanes of M values; lane i ends with that of value first_of<M>(i).
+template <int M>
+__device__ __forceinline__ float sum_apart(const float (&v)[M], int lane) {
+    float x[M];
+#pragma unroll
+    for (int i = 0; i < M; ++i) x[i] = v[i];
+    int o = 16;
+#pragma unroll
+    for (int h = M / 2; h >= 1; h /= 2, o >>= 1) {
+        const bool upper = lane & o;
+#pragma unroll
+        for (int i = 0; i < h; ++i) {
+            const float give = upper ? x[i] : x[i + h], keep = upper ? x[i + h] : x[i];
+            x[i] = keep + __shfl_xor_sync(~0u, give, o);
+        }
+    }
+#pragma unroll
+    for (; o; o >>= 1) x[0] += __shfl_xor_sync(~0u, x[0], o);
+    return x[0];
+}
+
 template <int NT, bool VEC, bool TOP>
 __global__ void __launch_bounds__(32 * kFewWarps, kFewBlocks)
     k_score_few(const uint16_t *x, int64_t stride_x, const uint16_t *w, int64_t stride_w, const int64_t *target, int T,
                 int64_t V, int H, int64_t rows, Stats *part, float *picked, const Alternatives alt) {
     extern __shared__ float4 xs[];
-    __shared__ Stats sh[kFewWarps][NT];
-    __shared__ Found tops[TOP ? NT : 1][TOP ? kFewWarps * 32 : 1];
-    __shared__ int counts[NT][kFewWarps];
+    __shared__ float4 quads[NT][kFewMost / 4];
+    __shared__ float tops[NT][kFewWarps];
+    __shared__ float2 sums[NT][kFewWarps];
     let_next_start();
     after_previous();
     few_load<NT>(xs, x, stride_x, T, H);
+    constexpr int kThreads = 32 * kFewWarps, M = kFewRows * NT;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t first = ((int64_t)blockIdx.x * kFewWarps + warp) * rows, last = min(first + rows, V);
-    Stats a[NT];
-    int64_t want[NT];
-    Found mine[NT];
-    float least[NT];  // the k-th of them
-    int have[NT];
+    const int64_t first = (int64_t)blockIdx.x * kFewWarps * rows, from = first + warp * rows;
+    const int all = (int)min(V - first, kFewWarps * rows);
+    const auto l = [&](int t) { return reinterpret_cast<float *>(quads[t]); };
+    few_dots<NT, VEC>(xs, w, stride_w, H, from, min(from + rows, V), [&](int64_t v0, const float (&acc)[kFewRows][NT]) {
+        float v[M];
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
-        a[t] = {kNegInf, 0.f, 0.f}, want[t] = t < T ? target[t] : -1;
-        mine[t] = {kNegInf, -1}, least[t] = kNegInf, have[t] = 0;
-    }
-    few_logits<NT, VEC>(xs, w, stride_w, H, first, last, [&](int t, int64_t v, float l) {
-        const float top = fmaxf(a[t].m, l), ref = ref_of(top);
-        const Stats b = rebase(a[t], ref);
-        const float q = not_below((l - ref) * kLog2e, kNoExp), p = exp2_fast(q);
-        a[t] = {top, b.s + p, fmaf(p, q, b.u)};
-        if (lane == 0 && want[t] == v) picked[t] = l;
-        if constexpr (TOP) {
-            // all lanes have the same l; columns ascend, so that an equal one goes behind
-            if (l > least[t] || (have[t] < alt.k && l == l)) {
-                const int to = __popc(__ballot_sync(~0u, lane < have[t] && mine[t].l >= l));
-                const float up = __shfl_up_sync(~0u, mine[t].l, 1);
-                const int un = __shfl_up_sync(~0u, mine[t].n, 1);
-                if (lane > to) mine[t] = {up, un};
-                if (lane == to) mine[t] = {l, (int)v};
-                have[t] = min(have[t] + 1, alt.k);
-                if (have[t] == alt.k) least[t] = __shfl_sync(~0u, mine[t].l, alt.k - 1);
-            }
-        }
+        for (int i = 0; i < M; ++i) v[i] = acc[i / NT][i % NT];
+        const float sum = sum_apart<M>(v, lane);
+        const int i = lane / (32 / M), r = i / NT, t = i % NT;  // M runs of lanes have a value each
+        if (lane % (32 / M) == 0 && v0 + r < from + rows && v0 + r < V) l(t)[v0 - first + r] = sum;
     });
-    if (lane == 0) {
+    if (threadIdx.x < 4 && all + threadIdx.x < kFewMost) {  // whole quads are read: no comparison finds NaN
 #pragma unroll
-        for (int t = 0; t < NT; ++t) sh[warp][t] = a[t], counts[t][warp] = have[t];
-    }
-    if constexpr (TOP) {
-#pragma unroll
-        for (int t = 0; t < NT; ++t) tops[t][warp * 32 + lane] = mine[t];
+        for (int t = 0; t < NT; ++t) l(t)[all + threadIdx.x] = kNaN;
     }
     __syncthreads();
-    if (threadIdx.x < T) {  // the warps' parts, in the order of the warps
-        const int t = threadIdx.x;
-        Stats all = sh[0][t];
-        for (int i = 1; i < kFewWarps; ++i) all = add(all, sh[i][t]);
-        part[(int64_t)blockIdx.x * T + t] = all;
+    float m[NT];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+        m[t] = kNegInf;
+        for (int i = threadIdx.x; i < all; i += kThreads) m[t] = fmaxf(m[t], l(t)[i]);
+#pragma unroll
+        for (int o = 16; o; o >>= 1) m[t] = fmaxf(m[t], __shfl_xor_sync(~0u, m[t], o));
+        if (lane == 0) tops[t][warp] = m[t];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+#pragma unroll
+        for (int i = 0; i < kFewWarps; ++i) m[t] = fmaxf(m[t], tops[t][i]);
+        const float ref = ref_of(m[t]);
+        const int64_t at = t < T ? target[t] - first : -1;
+        float s = 0.f, u = 0.f;
+        for (int i = threadIdx.x; i < all; i += kThreads) {
+            const float q = not_below((l(t)[i] - ref) * kLog2e, kNoExp), p = exp2_fast(q);
+            s += p, u = fmaf(p, q, u);
+            if (i == at) picked[t] = l(t)[i];
+        }
+#pragma unroll
+        for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(~0u, s, o), u += __shfl_xor_sync(~0u, u, o);
+        if (lane == 0) sums[t][warp] = make_float2(s, u);
+    }
+    __syncthreads();
+    if (threadIdx.x < T) {
+        Stats a{m[0], 0.f, 0.f};
+#pragma unroll
+        for (int t = 1; t < NT; ++t)
+            if (threadIdx.x == t) a.m = m[t];
+        for (int i = 0; i < kFewWarps; ++i) a.s += sums[threadIdx.x][i].x, a.u += sums[threadIdx.x][i].y;
+        part[(int64_t)blockIdx.x * T + threadIdx.x] = a;
     }
     if constexpr (TOP) {
-        // each of the warps' alternatives finds its place among all of them
         for (int t = 0; t < T; ++t) {
-            int total = 0;
-#pragma unroll
-            for (int i = 0; i < kFewWarps; ++i) total += counts[t][i];
             const int64_t at = (int64_t)t * alt.pieces + blockIdx.x;
-            if (threadIdx.x == 0) alt.count[at] = (uint8_t)min(total, alt.k);
-            if (lane >= counts[t][warp]) continue;
-            const Found f = tops[t][warp * 32 + lane];
-            int place = 0;
-            for (int i = 0; i < kFewWarps; ++i)
-                for (int j = 0; j < counts[t][i]; ++j) place += before(tops[t][i * 32 + j], f);
-            if (place < alt.k) alt.found[at * alt.slots + place] = f;
+            const float *mine = reinterpret_cast<const float *>(quads[t]);
+            int numbers = 0;
+            for (int i0 = 0; i0 < all; i0 += kThreads) {
+                const int i = i0 + threadIdx.x;
+                const float f = i < all ? mine[i] : kNaN;
+                numbers += __syncthreads_count(f == f);
+                if (f != f) continue;
+                int place = 0;
+                for (int j = 0; j < all; j += 4) {
+                    const float4 g = quads[t][j / 4];
+                    place += (g.x > f || (g.x == f && j < i)) + (g.y > f || (g.y == f && j + 1 < i)) +
+                             (g.z > f || (g.z == f && j + 2 < i)) + (g.w > f || (g.w == f && j + 3 < i));
+                }
+                if (place < alt.k) alt.found[at * alt.slots + place] = {f, (int)first + i};
+            }
+            if (threadIdx.x == 0) alt.count[at] = (uint8_t)min(numbers, alt.k);
         }
     }
 }
@@ -377,18 +414,19 @@ __device__ __forceinline__ int collect(const Alternatives &alt, int64_t pieces, 
         int counts[kAhead];
 #pragma unroll
         for (int h = 0; h < kAhead; ++h) counts[h] = !skip && p0 + 32 * h + lane < pieces ? count[p0 + 32 * h + lane] : 0;
+        // slots are even in number, so that two are 16 aligned bytes
+        uint4 ahead[kAhead];
+#pragma unroll
+        for (int h = 0; h < kAhead; ++h)
+            if (counts[h] > 0) ahead[h] = *reinterpret_cast<const uint4 *>(found + (p0 + 32 * h + lane) * slots);
 #pragma unroll
         for (int h = 0; h < kAhead; ++h) {
             const Found *from = found + (p0 + 32 * h + lane) * slots;
             const int c = counts[h];
+            uint4 q = ahead[h];
             for (int e = 0; __any_sync(~0u, e < c); e += 2) {
-                // slots are even in number, so that two are 16 aligned bytes
-                Found f[2] = {{kNaN, 0}, {kNaN, 0}};
-                if (e < c) {
-                    const uint4 q = *reinterpret_cast<const uint4 *>(from + e);
-                    f[0] = {__uint_as_float(q.x), (int)q.y};
-                    if (e + 1 < c) f[1] = {__uint_as_float(q.z), (int)q.w};
-                }
+                if (e > 0 && e < c) q = *reinterpret_cast<const uint4 *>(from + e);
+                const Found f[2] = {{e < c ? __uint_as_float(q.x) : kNaN, (int)q.y}, {e + 1 < c ? __uint_as_float(q.z) : kNaN, (int)q.w}};
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     const bool is = f[i].l >= least;
@@ -414,6 +452,15 @@ __global__ void __launch_bounds__(kJoinThreads) k_score_join(const JoinArgs a, c
     __shared__ int kept;
     let_next_start();
     after_previous();
+    constexpr int kCounts = TOP && ROWS == 1 ? 4 : 1;
+    [[maybe_unused]] int counts[kCounts] = {};  // of the first pieces of one token's thread, on their way already
+    if constexpr (TOP && ROWS == 1) {
+#pragma unroll
+        for (int j = 0; j < kCounts; ++j) {
+            const int p = threadIdx.x + j * kGroups;
+            if (p < a.pieces) counts[j] = alt.count[blockIdx.x * a.pieces + p];
+        }
+    }
     // neighbouring tokens are read together
     const int col = threadIdx.x % ROWS, run = threadIdx.x / ROWS;
     const int64_t t = (int64_t)blockIdx.x * ROWS + col;
@@ -483,18 +530,25 @@ __global__ void __launch_bounds__(kJoinThreads) k_score_join(const JoinArgs a, c
             n = collect(alt, a.pieces, u, least, !(of_lane >= least), mine, lane);
         } else {
             // the largest of this thread's pieces, which it looks through if any is large enough
-            if (sh[0][threadIdx.x].m >= least)
-                for (int64_t p = threadIdx.x; p < a.pieces; p += kGroups) {
-                    const int64_t at = u * a.pieces + p;
-                    const int c = alt.count[at];
-                    for (int e = 0; e < c; ++e) {
-                        const Found f = alt.found[at * alt.slots + e];
-                        if (f.l >= least) {
+            const auto look = [&](int64_t p, int c) {
+                const Found *from = alt.found + (u * a.pieces + p) * alt.slots;
+                for (int e = 0; e < c; e += 2) {
+                    const uint4 q = *reinterpret_cast<const uint4 *>(from + e);
+                    const Found f[2] = {{__uint_as_float(q.x), (int)q.y}, {__uint_as_float(q.z), (int)q.w}};
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+                        if (e + i < c && f[i].l >= least) {
                             const int to = atomicAdd(&kept, 1);
-                            if (to < kKept) mine[to] = f;
+                            if (to < kKept) mine[to] = f[i];
                         }
-                    }
+                    if (!alt.least && f[0].l < least) break;  // in order
                 }
+            };
+            if (sh[0][threadIdx.x].m >= least) {
+#pragma unroll
+                for (int j = 0; j < kCounts; ++j) look(threadIdx.x + j * kGroups, counts[j]);
+                for (int64_t p = threadIdx.x + kCounts * kGroups; p < a.pieces; p += kGroups) look(p, alt.count[u * a.pieces + p]);
+            }
             __syncthreads();
             n = kept;
             if (n <= kKept) {
@@ -519,9 +573,9 @@ __global__ void __launch_bounds__(256) k_no_bounds(uint32_t *least, int64_t n) {
     if (i < n) least[i] = 0;
 }
 
-// Bytes of a few-token block's own shared memory beside its tokens.
-int few_own(bool top) {
-    return kFewWarps * kFewTokens * ((int)sizeof(Stats) + 4) + (top ? kFewTokens * kFewWarps * 32 * (int)sizeof(Found) : 0);
+// Rows of w to a warp of few tokens.
+int64_t score_rows(int64_t T, int64_t V, int64_t H) {
+    return std::min<int64_t>(few_rows(T, V, H, T * (kFewMost * 4 + kFewWarps * 12)), kFewMost / kFewWarps);
 }
 
 // Tokens are taken so many at a time that what their pieces leave takes about
@@ -549,7 +603,7 @@ ScoreSpace score_space(void *ws, const uint16_t *x, int64_t sx, const uint16_t *
     s.each = T;
     int64_t pieces;
     if (s.few) {
-        s.rows = few_rows(T, V, H, few_own(k > 0));
+        s.rows = score_rows(T, V, H);
         pieces = ceil_div(V, s.rows * kFewWarps);
     } else {
         s.x = aligned(c, x, sx, T, H, ceil_div(V, 256));
