@@ -204,15 +204,17 @@ typedef struct {
 } pp_stage_tensor;
 
 /* norm = the root of the sum of the squares of all gradients (of each entry only g,
- * n and g_float are looked at).  Squares are added in 32 bits within a thread and in
- * 64 beyond: a gradient above 1.8e19 makes the norm infinite. */
+ * n and g_float are looked at), rounded once; wide (NULL: not wanted) is the same
+ * before that.  Squares beyond the range of 32 bits, of gradients above 1.8e19, make
+ * the norm infinite. */
 size_t pp_stage_grad_norm_workspace(const pp_stage_tensor *list, int64_t count);
-int pp_stage_grad_norm(const pp_stage_tensor *list, int64_t count, float *norm,
+int pp_stage_grad_norm(const pp_stage_tensor *list, int64_t count, float *norm, double *wide,
                        void *workspace, size_t workspace_bytes, cudaStream_t stream);
 
 /* One AdamW step, t = *step + 1 (a device word, written back: a captured call counts
  * on as it is replayed):
- *   c = max_norm / *norm where *norm > max_norm, else 1 (norm NULL: 1; a device float)
+ *   c = max_norm / *norm where *norm > max_norm, else 1 (norm NULL: 1; a device float,
+ *       and *wide, if given, in its place where it rounds to that)
  *   m = beta1 m + (1 - beta1) c g     v = beta2 v + (1 - beta2) (c g)^2
  *   p = p (1 - lr decay) - lr / (1 - beta1^t) m / (sqrt(v / (1 - beta2^t)) + eps)
  * lr is *lr_at (a device float) where that is given.  Where *norm is not a finite
@@ -236,7 +238,7 @@ int pp_stage_grad_norm(const pp_stage_tensor *list, int64_t count, float *norm,
 size_t pp_stage_adamw_workspace(void);
 int pp_stage_adamw(const pp_stage_tensor *list, int64_t count, void *m, void *v, uint8_t *m_exp, uint8_t *v_exp,
                    int64_t held, int64_t *step, const float *lr_at, double lr, double beta1, double beta2, double eps,
-                   const float *norm, double max_norm, int random, uint64_t seed,
+                   const float *norm, const double *wide, double max_norm, int random, uint64_t seed,
                    void *workspace, size_t workspace_bytes, cudaStream_t stream);
 /* What moments in 8 bits stand for, as bf16 (exactly). */
 int pp_stage_adamw_moments(const uint8_t *m, const uint8_t *v, const uint8_t *m_exp, const uint8_t *v_exp, int64_t held,

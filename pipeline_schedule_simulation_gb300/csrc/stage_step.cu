@@ -406,10 +406,12 @@ __global__ void __launch_bounds__(kThreads, SMALL ? 4 : 3) k_step(const __grid_c
 
 // The step's number goes up, and all that depends on it is computed, in 64 bits.
 __global__ void k_step_begin(int64_t *step, const float *lr_at, double lr, double b1, double b2, const float *norm,
-                             double max_norm, uint64_t seed, StepNow *now) {
+                             const double *wide, double max_norm, uint64_t seed, StepNow *now) {
     let_next_start();
     after_previous();
     const float nrm = norm ? *norm : 0.f;
+    // the norm before it was rounded, if it is still that
+    const double full = norm && wide && (float)*wide == nrm ? *wide : nrm;
     const int64_t t = *step + 1;
     const double rate = lr_at ? *lr_at : lr;
     const double bias = threadIdx.x ? 1 / sqrt(1 - pow(b2, (double)t)) : rate / (1 - pow(b1, (double)t));
@@ -418,7 +420,7 @@ __global__ void k_step_begin(int64_t *step, const float *lr_at, double lr, doubl
     StepNow s;
     s.go = isfinite(nrm);
     s.size = (float)bias, s.root = (float)other, s.lr = (float)rate;
-    s.clip = nrm > max_norm ? (float)(max_norm / nrm) : 1.f;
+    s.clip = full > max_norm ? (float)(max_norm / full) : 1.f;
     s.key = random_key(seed, t);
     *now = s;
     if (s.go) *step = t;
@@ -427,6 +429,25 @@ __global__ void k_step_begin(int64_t *step, const float *lr_at, double lr, doubl
 // ---- the norm: a block's sum of squares, then all blocks'
 
 constexpr int kNormThreads = 512;
+
+// Two sums of squares in 32 bits that keep what each addition and each square
+// cuts off: as good as 64 bits, which the GPU adds at a fiftieth of the rate.
+// (The factor of a clip is then the same however the sum was shared out, and with
+// it what moments in 8 bits are rounded to.)
+struct Squares {
+    float2 s = {0.f, 0.f}, low = {0.f, 0.f};
+    __device__ __forceinline__ void add(float2 x) {
+        const float2 p = __fmul2_rn(x, x), e = __ffma2_rn(x, x, minus(p));  // x^2 = p + e
+        const float2 t = __fadd2_rn(s, p), z = __fadd2_rn(t, minus(s));
+        low = __fadd2_rn(low, __fadd2_rn(__fadd2_rn(__fadd2_rn(s, minus(__fadd2_rn(t, minus(z)))), __fadd2_rn(p, minus(z))), e));
+        s = t;
+    }
+    static __device__ __forceinline__ float2 minus(float2 x) { return {-x.x, -x.y}; }
+    __device__ __forceinline__ double total() const {
+        // beyond the range the rest is no number
+        return ((double)s.x + (double)s.y) + (isfinite(s.x) && isfinite(s.y) ? (double)low.x + (double)low.y : 0.);
+    }
+};
 
 template <class G, int N>
 __global__ void __launch_bounds__(kNormThreads) k_norm(const __grid_constant__ Entries<N> t, int64_t chunk, double *part) {
@@ -437,7 +458,7 @@ __global__ void __launch_bounds__(kNormThreads) k_norm(const __grid_constant__ E
     const G *g = static_cast<const G *>(e.g);
     after_previous();
     constexpr int kEach = kNormThreads * kUnit;
-    float s[4] = {};
+    Squares s[2];
     int64_t i = from + threadIdx.x * kUnit;
     if (e.vec) {
         for (; i + kUnit + kEach <= to; i += 2 * kEach) {
@@ -445,16 +466,16 @@ __global__ void __launch_bounds__(kNormThreads) k_norm(const __grid_constant__ E
             load<true>(g + i, 8, a);
             load<true>(g + i + kEach, 8, b);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) s[j & 3] = fmaf(a[j], a[j], fmaf(b[j], b[j], s[j & 3]));
+            for (int j = 0; j < 8; j += 2) s[0].add({a[j], a[j + 1]}), s[1].add({b[j], b[j + 1]});
         }
     }
     for (; i < to; i += kEach) {
         float a[8];
         load<false>(g + i, to - i < kUnit ? (int)(to - i) : kUnit, a);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) s[j & 3] = fmaf(a[j], a[j], s[j & 3]);
+        for (int j = 0; j < 8; j += 4) s[0].add({a[j], a[j + 1]}), s[1].add({a[j + 2], a[j + 3]});
     }
-    double x = (double)(s[0] + s[1]) + (double)(s[2] + s[3]);
+    double x = s[0].total() + s[1].total();
 #pragma unroll
     for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(~0u, x, o);
     if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = x;
@@ -466,7 +487,7 @@ __global__ void __launch_bounds__(kNormThreads) k_norm(const __grid_constant__ E
     }
 }
 
-__global__ void __launch_bounds__(1024) k_norm_join(const double *part, int64_t n, float *norm) {
+__global__ void __launch_bounds__(1024) k_norm_join(const double *part, int64_t n, float *norm, double *wide) {
     __shared__ double sh[32];
     let_next_start();
     after_previous();
@@ -480,7 +501,10 @@ __global__ void __launch_bounds__(1024) k_norm_join(const double *part, int64_t 
     x = sh[threadIdx.x];
 #pragma unroll
     for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(~0u, x, o);
-    if (threadIdx.x == 0) *norm = (float)sqrt(x);
+    if (threadIdx.x) return;
+    x = sqrt(x);
+    *norm = (float)x;
+    if (wide) *wide = x;
 }
 
 // What moments in 8 bits stand for, as bf16 (exactly): 8 elements of both a thread.
@@ -590,9 +614,9 @@ extern "C" size_t pp_stage_grad_norm_workspace(const pp_stage_tensor *list, int6
     return stage_align((size_t)norm_blocks(list, count) * sizeof(double));
 }
 
-extern "C" int pp_stage_grad_norm(const pp_stage_tensor *list, int64_t count, float *norm, void *workspace,
-                                  size_t workspace_bytes, cudaStream_t stream) {
-    if (bad_list(list, count, false) || !norm || !aligned_to(norm, 4)) return PP_ERR_ARG;
+extern "C" int pp_stage_grad_norm(const pp_stage_tensor *list, int64_t count, float *norm, double *wide,
+                                  void *workspace, size_t workspace_bytes, cudaStream_t stream) {
+    if (bad_list(list, count, false) || !norm || !aligned_to(norm, 4) || !aligned_to(wide, 8)) return PP_ERR_ARG;
     if (too_long(list, count)) return PP_ERR_SIZE;
     const int64_t chunk = norm_chunk(list, count), blocks = norm_blocks(list, count);
     if (blocks && (!workspace || !aligned_to(workspace, kStageAlign) || workspace_bytes < blocks * sizeof(double))) return PP_ERR_ARG;
@@ -610,7 +634,7 @@ extern "C" int pp_stage_grad_norm(const pp_stage_tensor *list, int64_t count, fl
     int rc = all((const float *)nullptr);
     if (rc == PP_OK) rc = all((const uint16_t *)nullptr);
     if (rc == PP_OK)
-        rc = launch_after(k_norm_join, 1, 1024, 0, stream, 1, (const double *)workspace, blocks, norm);
+        rc = launch_after(k_norm_join, 1, 1024, 0, stream, 1, (const double *)workspace, blocks, norm, wide);
     return rc;
 }
 
@@ -618,7 +642,7 @@ extern "C" size_t pp_stage_adamw_workspace(void) { return kStageAlign; }
 
 extern "C" int pp_stage_adamw(const pp_stage_tensor *list, int64_t count, void *m, void *v, uint8_t *m_exp, uint8_t *v_exp,
                               int64_t held, int64_t *step, const float *lr_at, double lr, double beta1, double beta2,
-                              double eps, const float *norm, double max_norm, int random, uint64_t seed, void *workspace,
+                              double eps, const float *norm, const double *wide, double max_norm, int random, uint64_t seed, void *workspace,
                               size_t workspace_bytes, cudaStream_t stream) {
     if (bad_list(list, count, true) || held < 0 || held % kMoments || !step || !aligned_to(step, 8)) return PP_ERR_ARG;
     if (too_long(list, count) || held > PP_STAGE_MAX_ELEMENTS) return PP_ERR_SIZE;
@@ -628,12 +652,12 @@ extern "C" int pp_stage_adamw(const pp_stage_tensor *list, int64_t count, void *
         if (list[i].n && list[i].n > held - list[i].at) return PP_ERR_ARG;
     if (!(beta1 >= 0 && beta1 < 1 && beta2 >= 0 && beta2 < 1 && eps >= 0 && eps <= 3e38)) return PP_ERR_ARG;
     if (lr_at ? !aligned_to(lr_at, 4) : !(std::fabs(lr) <= 3e38)) return PP_ERR_ARG;
-    if (norm && (!aligned_to(norm, 4) || !(max_norm > 0))) return PP_ERR_ARG;
+    if (norm && (!aligned_to(norm, 4) || !aligned_to(wide, 8) || !(max_norm > 0))) return PP_ERR_ARG;
     if (!workspace || !aligned_to(workspace, kStageAlign) || workspace_bytes < sizeof(StepNow)) return PP_ERR_ARG;
     StepNow *now = static_cast<StepNow *>(workspace);
     const Moments mo{m, v, m_exp, v_exp};
     const Rates r{(float)beta1, (float)(1 - beta1), (float)beta2, (float)(1 - beta2), (float)eps, random != 0};
-    int rc = launch_after(k_step_begin, 1, 2, 0, stream, 1, step, lr_at, lr, beta1, beta2, norm, max_norm, seed, now);
+    int rc = launch_after(k_step_begin, 1, 2, 0, stream, 1, step, lr_at, lr, beta1, beta2, norm, wide, max_norm, seed, now);
     const auto all = [&]<class P, class G>(const P *, const G *) {
         if (rc != PP_OK) return;
         rc = m_exp ? step_all<P, G, true>(list, count, mo, r, now, stream) : step_all<P, G, false>(list, count, mo, r, now, stream);

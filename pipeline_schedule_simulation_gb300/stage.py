@@ -65,9 +65,9 @@ def _declare(lib):
     lib.pp_stage_score_backward_workspace.argtypes = [*m, *m, i64, i64, i64]
     lib.pp_stage_score_backward.argtypes = [*m, *m, vp, vp, vp, vp, vp, i64, i64, i64, *m, *m, i32, i32, vp, size, vp]
     lib.pp_stage_grad_norm_workspace.argtypes = [vp, i64]
-    lib.pp_stage_grad_norm.argtypes = [vp, i64, vp, vp, size, vp]
+    lib.pp_stage_grad_norm.argtypes = [vp, i64, vp, vp, vp, size, vp]
     lib.pp_stage_adamw_workspace.argtypes = []
-    lib.pp_stage_adamw.argtypes = [vp, i64, vp, vp, vp, vp, i64, vp, vp, f64, f64, f64, f64, vp, f64, i32, u64, vp, size, vp]
+    lib.pp_stage_adamw.argtypes = [vp, i64, vp, vp, vp, vp, i64, vp, vp, f64, f64, f64, f64, vp, vp, f64, i32, u64, vp, size, vp]
     lib.pp_stage_adamw_moments.argtypes = [vp, vp, vp, vp, i64, vp, vp, vp]
     lib.pp_stage_pack.argtypes = [*m, i64, i64, *m, *m, vp]
     lib.pp_stage_unpack.argtypes = [*m, *m, i64, i64, *m, vp]
@@ -570,7 +570,8 @@ def _listed(tensors, name):
 def grad_norm(grads, *, out=None, workspace=None, stream=None):
     """The 2-norm of all gradients together, float [1] on their device: what AdamW.step clips by.
 
-    grads: float or bf16 tensors, contiguous, of any shapes.  A gradient above 1.8e19 makes it infinite."""
+    grads: float or bf16 tensors, contiguous, of any shapes.  A gradient above 1.8e19 makes it infinite.  The tensor
+    also carries the norm before its rounding, which the step clips by as long as it rounds to what the tensor holds."""
     grads = _listed(grads, "grads")
     dev = _device(grads[0]) if grads else _device(out)
     ctx = _elsewhere(dev, stream)
@@ -587,9 +588,10 @@ def grad_norm(grads, *, out=None, workspace=None, stream=None):
             raise ValueError("grads: expected at least one tensor, or an `out` on a CUDA device")
         out = _empty(1, dtype=_F32, device=grads[0].device)
     po = _vector(out, "out", _F32, dev, 1)
+    wide = out._wide = torch.empty(1, dtype=torch.float64, device=out.device)
     need = LIB.pp_stage_grad_norm_workspace(ctypes.addressof(table), len(grads))
     _keep, ws, n = _scratch(workspace, need, out.device, dev)
-    rc = LIB.pp_stage_grad_norm(ctypes.addressof(table), len(grads), po, ws, n, _raw_stream(dev))
+    rc = LIB.pp_stage_grad_norm(ctypes.addressof(table), len(grads), po, wide.data_ptr(), ws, n, _raw_stream(dev))
     if rc != PP_OK:
         raise PPSchedError(rc, "pp_stage_grad_norm")
     return out
@@ -714,11 +716,12 @@ class AdamW:
         if max_norm is not None and not 0 < max_norm < math.inf:
             raise ValueError(f"max_norm: expected a number above 0, got {max_norm!r}")
         pn = None if norm is None else _vector(norm, "norm", _F32, dev, 1)
+        wide = getattr(norm, "_wide", None)
         s = self._state
         small = self.bits == 8
         rc = LIB.pp_stage_adamw(ctypes.addressof(self._table), len(self.params), s["m"].data_ptr(), s["v"].data_ptr(),
                                 s["m_exp"].data_ptr() if small else None, s["v_exp"].data_ptr() if small else None,
-                                self._held, s["step"].data_ptr(), lr_at, rate, *self.betas, self.eps, pn, max_norm or 1.0,
+                                self._held, s["step"].data_ptr(), lr_at, rate, *self.betas, self.eps, pn, None if wide is None else wide.data_ptr(), max_norm or 1.0,
                                 self.seed is not None, self.seed or 0, self._work.data_ptr(), self._work.numel(),
                                 _raw_stream(dev))
         if rc != PP_OK:

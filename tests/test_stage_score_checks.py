@@ -60,10 +60,10 @@ def _list(*entries):
 
 
 def adamw(*entries, count=None, lst=True, m=P, v=P, me=None, ve=None, held=128, step=P, lr_at=None, lr=1e-3, b1=0.9, b2=0.99,
-          eps=1e-8, norm=None, most=1.0, ws=P, n=256):
+          eps=1e-8, norm=None, wide=None, most=1.0, ws=P, n=256):
     t = _list(*(entries or ({}, {"at": 64})))
     return L.pp_stage_adamw(ctypes.addressof(t) if lst else None, len(t) if count is None else count, m, v, me, ve, held, step,
-                            lr_at, lr, b1, b2, eps, norm, most, 0, 0, ws, n, None)
+                            lr_at, lr, b1, b2, eps, norm, wide, most, 0, 0, ws, n, None)
 
 
 def test_step():
@@ -71,7 +71,7 @@ def test_step():
     for bad in (dict(lst=False), dict(count=-1), dict(m=None), dict(v=None), dict(me=P), dict(ve=P), dict(held=-64), dict(held=100),
                 dict(held=64), dict(m=P + 16), dict(v=P + 4), dict(step=None), dict(step=P + 4), dict(lr_at=P + 2), dict(lr=nan),
                 dict(lr=float("inf")), dict(b1=1.0), dict(b1=-0.1), dict(b2=nan), dict(eps=-1.0), dict(eps=nan), dict(norm=P + 1),
-                dict(norm=P, most=0.0), dict(norm=P, most=nan), dict(ws=None), dict(ws=P + 16), dict(n=8)):
+                dict(norm=P, most=0.0), dict(norm=P, wide=P + 4), dict(norm=P, most=nan), dict(ws=None), dict(ws=P + 16), dict(n=8)):
         assert adamw(**bad) == B.PP_ERR_ARG, bad
     for bad in (dict(n=-1), dict(p=None), dict(g=None), dict(p=P + 2), dict(g=P + 2), dict(p_float=0, p=P + 1), dict(g_float=2),
                 dict(p_float=255), dict(copy=P + 1), dict(copy=P, p_float=0), dict(at=-64), dict(at=32), dict(at=128), dict(n=129),
@@ -82,10 +82,10 @@ def test_step():
 
 
 def test_norm_and_moments():
-    def norm(*entries, count=None, out=P, ws=P, n=1 << 20):
+    def norm(*entries, count=None, out=P, wide=None, ws=P, n=1 << 20):
         t = _list(*entries)
-        return L.pp_stage_grad_norm(ctypes.addressof(t), len(t) if count is None else count, out, ws, n, None)
-    for bad in (dict(out=None), dict(out=P + 2), dict(count=-1), dict(ws=None), dict(ws=P + 8), dict(n=4)):
+        return L.pp_stage_grad_norm(ctypes.addressof(t), len(t) if count is None else count, out, wide, ws, n, None)
+    for bad in (dict(out=None), dict(out=P + 2), dict(wide=P + 4), dict(count=-1), dict(ws=None), dict(ws=P + 8), dict(n=4)):
         assert norm({}, **bad) == B.PP_ERR_ARG, bad
     for bad in (dict(n=-1), dict(g=None), dict(g=P + 2), dict(g_float=7)):
         assert norm(bad) == B.PP_ERR_ARG, bad
