@@ -322,11 +322,13 @@ __device__ __forceinline__ void step_unit(const Entry &e, int64_t i, int n, bool
     }
 #pragma unroll
     for (int j = 0; j < 8; j += 2) {
-        // products and sums rounded apart, as written above
+        // Products and sums are rounded apart, as written above, so that the 8 bits are the same whatever computes them:
+        // single sums, for a sum of a pair would be made one with its product.
         const float2 x = __fmul2_rn({g[j], g[j + 1]}, {now.clip, now.clip});
-        const float2 a = __fadd2_rn(__fmul2_rn({r.b1, r.b1}, {m[j], m[j + 1]}), __fmul2_rn({r.c1, r.c1}, x));
-        const float2 b = __fadd2_rn(__fmul2_rn({r.b2, r.b2}, {v[j], v[j + 1]}), __fmul2_rn({r.c2, r.c2}, __fmul2_rn(x, x)));
-        m[j] = a.x, m[j + 1] = a.y, v[j] = b.x, v[j + 1] = b.y;
+        const float2 a = __fmul2_rn({r.b1, r.b1}, {m[j], m[j + 1]}), c = __fmul2_rn({r.c1, r.c1}, x);
+        const float2 b = __fmul2_rn({r.b2, r.b2}, {v[j], v[j + 1]}), d = __fmul2_rn({r.c2, r.c2}, __fmul2_rn(x, x));
+        m[j] = __fadd_rn(a.x, c.x), m[j + 1] = __fadd_rn(a.y, c.y);
+        v[j] = __fadd_rn(b.x, d.x), v[j + 1] = __fadd_rn(b.y, d.y);
     }
     const bool tiny = !(least_of(v) >= 0x1p-126f);  // no normal numbers, or 0
     float d[8];
@@ -430,16 +432,15 @@ __global__ void k_step_begin(int64_t *step, const float *lr_at, double lr, doubl
 
 constexpr int kNormThreads = 512;
 
-// Two sums of squares in 32 bits that keep what each addition and each square
-// cuts off: as good as 64 bits, which the GPU adds at a fiftieth of the rate.
-// (The factor of a clip is then the same however the sum was shared out, and with
-// it what moments in 8 bits are rounded to.)
+// Two sums of squares in 32 bits that keep what each addition cuts off: as good
+// as 64 bits, which the GPU adds at a fiftieth of the rate.  (The factor of a clip
+// is then the same however the sum was shared out, and with it what moments in 8
+// bits are rounded to.)
 struct Squares {
     float2 s = {0.f, 0.f}, low = {0.f, 0.f};
     __device__ __forceinline__ void add(float2 x) {
-        const float2 p = __fmul2_rn(x, x), e = __ffma2_rn(x, x, minus(p));  // x^2 = p + e
-        const float2 t = __fadd2_rn(s, p), z = __fadd2_rn(t, minus(s));
-        low = __fadd2_rn(low, __fadd2_rn(__fadd2_rn(__fadd2_rn(s, minus(__fadd2_rn(t, minus(z)))), __fadd2_rn(p, minus(z))), e));
+        const float2 t = __ffma2_rn(x, x, s), z = __fadd2_rn(t, minus(s));  // z: x^2 as far as t has it
+        low = __fadd2_rn(low, __fadd2_rn(__fadd2_rn(s, minus(__fadd2_rn(t, minus(z)))), __ffma2_rn(x, x, minus(z))));
         s = t;
     }
     static __device__ __forceinline__ float2 minus(float2 x) { return {-x.x, -x.y}; }
