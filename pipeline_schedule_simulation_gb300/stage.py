@@ -24,8 +24,10 @@ results carry no gradient, whatever the inputs say.
 """
 from __future__ import annotations
 
+import array
 import ctypes
 import math
+import struct
 
 import torch
 
@@ -47,9 +49,14 @@ NONFINITE = -128
 
 
 class _Tensors(ctypes.Structure):
-    """pp_stage_tensor"""
+    """pp_stage_tensor.  Lists of them are built as 64-bit words, six to an entry: setting fields one by one is most of
+    the time that a call over a few hundred tensors takes."""
     _fields_ = [("p", ctypes.c_void_p), ("g", ctypes.c_void_p), ("copy", ctypes.c_void_p), ("n", ctypes.c_int64),
                 ("at", ctypes.c_int64), ("decay", ctypes.c_float), ("p_float", ctypes.c_uint8), ("g_float", ctypes.c_uint8)]
+
+
+_WORDS, _P_FLOAT, _G_FLOAT = 6, 1 << 32, 1 << 40  # words of an entry; bits of its last
+assert ctypes.sizeof(_Tensors) == 8 * _WORDS and _Tensors.g_float.offset == 8 * _WORDS - 3
 
 
 def _declare(lib):
@@ -578,20 +585,23 @@ def grad_norm(grads, *, out=None, workspace=None, stream=None):
     if ctx is not None:
         with ctx:
             return grad_norm(grads, out=out, workspace=workspace)
-    table = (_Tensors * len(grads))()
+    words = []
     for i, g in enumerate(grads):
-        _flat(g, f"grads[{i}]", dev, (_F32, _BF16))
-        e = table[i]
-        e.g, e.n, e.g_float = g.data_ptr(), g.numel(), g.dtype is _F32
+        if not (isinstance(g, _Tensor) and ((wide := g.dtype is _F32) or g.dtype is _BF16) and g.get_device() == dev >= 0
+                and g.is_contiguous()):
+            _flat(g, f"grads[{i}]", dev, (_F32, _BF16))
+        words += (0, g.data_ptr(), 0, g.numel(), 0, _G_FLOAT if wide else 0)
+    table = array.array("Q", words)
+    at = table.buffer_info()[0]
     if out is None:
         if dev < 0:
             raise ValueError("grads: expected at least one tensor, or an `out` on a CUDA device")
         out = _empty(1, dtype=_F32, device=grads[0].device)
     po = _vector(out, "out", _F32, dev, 1)
     wide = out._wide = torch.empty(1, dtype=torch.float64, device=out.device)
-    need = LIB.pp_stage_grad_norm_workspace(ctypes.addressof(table), len(grads))
+    need = LIB.pp_stage_grad_norm_workspace(at, len(grads))
     _keep, ws, n = _scratch(workspace, need, out.device, dev)
-    rc = LIB.pp_stage_grad_norm(ctypes.addressof(table), len(grads), po, wide.data_ptr(), ws, n, _raw_stream(dev))
+    rc = LIB.pp_stage_grad_norm(at, len(grads), po, wide.data_ptr(), ws, n, _raw_stream(dev))
     if rc != PP_OK:
         raise PPSchedError(rc, "pp_stage_grad_norm")
     return out
@@ -640,9 +650,9 @@ class AdamW:
         self.bits, self.betas, self.eps, self.seed = bits, (b1, b2), float(eps), seed
         self.params, self.copies = tuple(params), tuple(copies)
         self._dev = dev
-        self._table = (_Tensors * len(params))()
+        words = []
         held = 0
-        for i, (p, c, d, e) in enumerate(zip(params, copies, decay, self._table)):
+        for i, (p, c, d) in enumerate(zip(params, copies, decay)):
             _flat(p, f"params[{i}]", dev, (_F32, _BF16))
             if c is not None:
                 _flat(c, f"copies[{i}]", dev, (_BF16,))
@@ -652,9 +662,11 @@ class AdamW:
                     raise ValueError(f"copies[{i}]: expected shape {tuple(p.shape)}, got {tuple(c.shape)}")
             if not math.isfinite(d):
                 raise ValueError(f"weight_decay: expected a finite number for params[{i}], got {d!r}")
-            e.p, e.copy = p.data_ptr(), None if c is None else c.data_ptr()
-            e.n, e.at, e.decay, e.p_float = p.numel(), held, d, p.dtype is _F32
+            bits_of_d = int.from_bytes(struct.pack("<f", d), "little")
+            words += (p.data_ptr(), 0, 0 if c is None else c.data_ptr(), p.numel(), held,
+                      bits_of_d + (_P_FLOAT if p.dtype is _F32 else 0))
             held += (p.numel() + BLOCK - 1) // BLOCK * BLOCK
+        self._table = array.array("Q", words)
         self._held, self._device = held, params[0].device
         self._state = self._new_state() if state is None else self._given_state(state)
         self._work = torch.empty(LIB.pp_stage_adamw_workspace(), dtype=_U8, device=self._device)
@@ -697,16 +709,19 @@ class AdamW:
                 return self.step(grads, lr, norm=norm, max_norm=max_norm)
         if len(grads) != len(self.params):
             raise ValueError(f"grads: expected {len(self.params)}, one for each parameter, got {len(grads)}")
-        for i, (e, p, g) in enumerate(zip(self._table, self.params, grads)):
-            if not (isinstance(g, _Tensor) and g.shape == p.shape):
+        table, at = self._table, 0
+        for p, g in zip(self.params, grads):
+            if not (isinstance(g, _Tensor) and g.shape == p.shape and ((wide := g.dtype is _F32) or g.dtype is _BF16)
+                    and g.get_device() == dev and g.is_contiguous()):
+                i = at // _WORDS
                 _flat(g, f"grads[{i}]", dev, (_F32, _BF16))
                 raise ValueError(f"grads[{i}]: expected shape {tuple(p.shape)}, got {tuple(g.shape)}")
-            wide = g.dtype is _F32
-            if not (wide or g.dtype is _BF16) or g.get_device() != dev or not g.is_contiguous():
-                _flat(g, f"grads[{i}]", dev, (_F32, _BF16))
-            if p.data_ptr() != (e.p or 0):
-                raise ValueError(f"params[{i}]: its memory is not that which this step was made for")
-            e.g, e.g_float = g.data_ptr(), wide
+            if p.data_ptr() != table[at]:
+                raise ValueError(f"params[{at // _WORDS}]: its memory is not that which this step was made for")
+            table[at + 1] = g.data_ptr()
+            flags = table[at + 5]
+            table[at + 5] = flags | _G_FLOAT if wide else flags & ~_G_FLOAT
+            at += _WORDS
         lr_at = _vector(lr, "lr", _F32, dev, 1) if isinstance(lr, _Tensor) else None
         rate = 0.0 if lr_at is not None else float(lr)
         if not math.isfinite(rate):
@@ -719,7 +734,7 @@ class AdamW:
         wide = getattr(norm, "_wide", None)
         s = self._state
         small = self.bits == 8
-        rc = LIB.pp_stage_adamw(ctypes.addressof(self._table), len(self.params), s["m"].data_ptr(), s["v"].data_ptr(),
+        rc = LIB.pp_stage_adamw(table.buffer_info()[0], len(self.params), s["m"].data_ptr(), s["v"].data_ptr(),
                                 s["m_exp"].data_ptr() if small else None, s["v_exp"].data_ptr() if small else None,
                                 self._held, s["step"].data_ptr(), lr_at, rate, *self.betas, self.eps, pn, None if wide is None else wide.data_ptr(), max_norm or 1.0,
                                 self.seed is not None, self.seed or 0, self._work.data_ptr(), self._work.numel(),
