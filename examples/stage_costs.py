@@ -12,7 +12,11 @@ between its F and its W kept in 8 bits:
     W   the gradients of the matrices, added to the microbatches' sums, from the
         checkpointed inputs
 
-F, B and W are timed; the times, as ticks, are then the costs of a P-stage
+and after the flush the AdamW step over all of the stage's tensors, clipped by
+the norm of the gradients: parameters in 32 bits with the 16-bit copies that F
+and B run on, moments in 8 bits.
+
+F, B, W and the step are timed; the times of F, B and W, as ticks, are then the costs of a P-stage
 pipeline of such stages that the schedule evaluator compares under GPipe, 1F1B
 and the Zero Bubble schedules, next to the bytes that 1F1B's peak of held
 microbatches takes in 8 bits and in bf16.
@@ -56,6 +60,11 @@ class LastStage:
         self.out = (torch.randn(vocab, width, generator=gen, device="cuda") * width ** -0.5).to(torch.bfloat16)
         self.out_sum = torch.zeros(vocab, width, device="cuda")
         self.held = {}
+        copies = [t for b in self.blocks for t in (b.matrix, b.w_post, b.w_pre, b.gate)] + [self.out]
+        self.sums = [t for b in self.blocks for t in b.sums.values()] + [self.out_sum]
+        decay = [0.1 if c.shape[0] > 1 and c.dim() == 2 else 0.0 for c in copies]  # the matrices'
+        self.adamw = S.AdamW([c.float() for c in copies], bits=8, copies=copies, betas=(0.9, 0.95), weight_decay=decay,
+                             seed=seed)
 
     def forward(self, mb, x, h, target):
         """F: x is the residual stream and h the normed input that the stage before sends.  Returns the tokens' losses."""
@@ -94,6 +103,13 @@ class LastStage:
             S.weight_grad(k["df"], k["h"], add=b.sums["matrix"], out=b.sums["matrix"])
         S.head_backward(S.unpack(keep["h"]), self.out, keep["target"], keep["lse"], scale=keep["scale"], outputs=("dw",),
                         add=True, out={"dw": self.out_sum})
+
+    def step(self, lr, max_norm=1.0):
+        """The step on the microbatches' sums, which are 0 again after it; returns the gradients' norm."""
+        norm = S.grad_norm(self.sums)
+        self.adamw.step(self.sums, lr, norm=norm, max_norm=max_norm)
+        torch._foreach_zero_(self.sums)
+        return norm
 
     def held_bytes(self, mb):
         """Bytes of the activations that a microbatch keeps after its F: in 8 bits, and as they would be in bf16."""
@@ -163,10 +179,18 @@ def main(argv=None):
     targets = [torch.randint(0, a.vocab, (a.tokens,), generator=gen, device="cuda") for _ in inputs]
     scale = 1 / (a.tokens * a.microbatches)
     run_1f1b(stage, inputs, targets, a.stages, 0, scale)  # the first run builds plans and loads kernels
+    stage.step(0.0)
     losses, _, ms = run_1f1b(stage, inputs, targets, a.stages, 0, scale)
+    start, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+    start.record()
+    norm = stage.step(1e-3)
+    end.record()
+    end.synchronize()
     print(f"stage of {a.blocks} blocks of width {a.width} and a head of {a.vocab}: {a.tokens} tokens take "
           + ", ".join(f"{k} {v * 1e3:.0f} us" for k, v in ms.items())
           + f"; mean loss {torch.stack(losses).mean().item():.4f}")
+    print(f"the step over {sum(t.numel() for t in stage.sums) / 1e6:.1f} million elements takes "
+          f"{start.elapsed_time(end) * 1e3:.0f} us, norm of the gradients {norm.item():.4f}")
     stage.forward(0, *inputs[0], targets[0])
     eight, sixteen = stage.held_bytes(0)
     stage.held.clear()

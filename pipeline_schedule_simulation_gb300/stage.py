@@ -613,7 +613,7 @@ class AdamW:
         m = beta1 m + (1 - beta1) g      v = beta2 v + (1 - beta2) g^2
         p = p (1 - lr decay) - lr / (1 - beta1^t) m / (sqrt(v / (1 - beta2^t)) + eps)
 
-    params: contiguous float or bf16 tensors of any shapes, updated in place.  copies: for float parameters, a list of
+    params: contiguous float or bf16 tensors of any shapes, updated in place, none overlapping another.  copies: for float parameters, a list of
     bf16 tensors of the same shapes (or None for one that has none) that receive the new values.  weight_decay: a number,
     or one for each parameter.
 
@@ -660,12 +660,17 @@ class AdamW:
                     raise TypeError(f"copies[{i}]: params[{i}] is bf16 itself")
                 if c.shape != p.shape:
                     raise ValueError(f"copies[{i}]: expected shape {tuple(p.shape)}, got {tuple(c.shape)}")
-            if not math.isfinite(d):
+            if not abs(d) <= 3e38:
                 raise ValueError(f"weight_decay: expected a finite number for params[{i}], got {d!r}")
             bits_of_d = int.from_bytes(struct.pack("<f", d), "little")
             words += (p.data_ptr(), 0, 0 if c is None else c.data_ptr(), p.numel(), held,
                       bits_of_d + (_P_FLOAT if p.dtype is _F32 else 0))
             held += (p.numel() + BLOCK - 1) // BLOCK * BLOCK
+        spans = sorted((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size(), name)
+                       for name, ts in (("params", params), ("copies", copies)) for t in ts if t is not None and t.numel())
+        for (_, end, one), (start, _, other) in zip(spans, spans[1:]):
+            if start < end:
+                raise ValueError(f"{one} and {other}: two of them overlap")
         self._table = array.array("Q", words)
         self._held, self._device = held, params[0].device
         self._state = self._new_state() if state is None else self._given_state(state)

@@ -396,6 +396,11 @@ def test_refusals(S):
             S.AdamW([z(4), z(8)], **kw)
     with pytest.raises(TypeError):
         S.AdamW([z(4, d=BF16)], copies=[z(4, d=BF16)])
+    p = z(8)
+    for twice in ([p, p], [p[:5], p[4:]], [z(8), p[2:3], z(4), p]):
+        with pytest.raises(ValueError, match="overlap"):
+            S.AdamW(twice)
+    S.AdamW([p[:5], p[5:], p[5:5]])
     opt = S.AdamW([z(4), z(2, 3)])
     for args, kw, kind in ((([z(4)], 1.0), {}, ValueError), (([z(4), z(6)], 1.0), {}, ValueError),
                            (([z(4), z(2, 3, d=torch.float16)], 1.0), {}, TypeError), (([z(4), z(3, 2).t()], 1.0), {}, ValueError),
