@@ -94,10 +94,11 @@ __device__ __forceinline__ uint32_t both(int x) { return (uint32_t)x * 0x10001u;
 __device__ __forceinline__ uint32_t decode2(uint32_t codes, int from) {
     return __vminu2(codes, 0x10001u) * (uint32_t)(from * 16) + codes * 16;
 }
-// Codes without sign from two magnitudes, rounded (r was added); `least` where they are less.
+// Codes from two numbers, r added to their bits; `least` where they are less.  (A sum does not reach the sign.)
+template <bool SIGN>
 __device__ __forceinline__ uint32_t encode2(uint32_t a, uint32_t b, int from, int least) {
-    const uint32_t t = __byte_perm(a, b, 0x7632) >> 4 & 0x0FFF0FFFu;
-    return __vmaxu2(t, both(from + least)) - both(from);
+    const uint32_t h = __byte_perm(a, b, 0x7632), t = __vmaxu2(h >> 4 & 0x07FF07FFu, both(from + least)) - both(from);
+    return SIGN ? t | (h >> 8 & 0x00800080u) : t;
 }
 
 constexpr float kNaN = __builtin_nanf("");
@@ -279,9 +280,7 @@ __device__ __forceinline__ uint2 write_codes(const float (&x)[8], uint32_t large
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const uint32_t a = __float_as_uint(x[2 * j]), b = __float_as_uint(x[2 * j + 1]);
-            constexpr uint32_t kSize = SIGN ? 0x7FFFFFFFu : ~0u;
-            h[j] = encode2((a & kSize) + r(2 * j), (b & kSize) + r(2 * j + 1), w.from, kLeast);
-            if (SIGN) h[j] |= __byte_perm(a, b, 0x7632) >> 8 & 0x00800080u;
+            h[j] = encode2<SIGN>(a + r(2 * j), b + r(2 * j + 1), w.from, kLeast);
         }
         return make_uint2(__byte_perm(h[0], h[1], 0x6420), __byte_perm(h[2], h[3], 0x6420));
     }
