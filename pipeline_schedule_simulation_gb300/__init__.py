@@ -7,8 +7,10 @@ busy/idle ticks, the exact bubble fraction and the peak count of held
 activations, for thousands to millions of instances per call; plus GPU
 searches over contiguous layer-to-stage partitions (seeded, exhaustive, and
 interleaved layouts).  And the operators of one pipeline stage, whose time and
-held bytes are the costs: the last stage's loss over a large vocabulary,
-activation checkpoints in 8 bits, the join of a block to the residual stream.
+held bytes are the costs: the last stage's loss over a large vocabulary, log
+probabilities of given tokens with entropy and alternatives, activation
+checkpoints in 8 bits, the join of a block to the residual stream, and the AdamW
+step after the flush.
 
 The compute runs in hand-written CUDA kernels behind the C ABI declared in
 ``include/ppsched.h`` and ``include/ppstage.h`` (``libppsched.so``); ``binding``

@@ -3,9 +3,14 @@
 //
 //   m = b1 m + (1 - b1) g      v = b2 v + (1 - b2) g^2      (g clipped before)
 //   p = p (1 - lr decay) - lr / (1 - b1^t) * m / (sqrt(v / (1 - b2^t)) + eps)
-// Every element is read and written once, so memory bounds it: 34 bytes an
-// element with 32-bit parameters, moments and gradients and a 16-bit copy, 18
-// with the moments in 8 bits.
+// Every element is read and written once, so memory bounds it: 30 bytes an
+// element with 32-bit parameters, moments and gradients and a 16-bit copy, 18 with
+// the moments in 8 bits.  571 million elements take 2.40 ms and 1.44 ms, both 105 %
+// of the measured copy rate (reads outweigh writes).  All in 16 bits with moments
+// in 8 it is 10 bytes an element, and whole-number arithmetic (some 35 of 70
+// instructions) bounds it: 1.34 ms rounded at random, 63 %; 90 million elements in
+// 161 tensors 233 us at random and 191 to nearest (70 %).  The norm takes 319 us of
+// 32-bit gradients (105 %), 183 us of 16-bit ones (92 %).
 //
 // Moments in 8 bits.  64 consecutive elements share an exponent, and an element
 // keeps 4 significant bits and its exponent relative to the block's: m a sign and
