@@ -78,7 +78,7 @@ struct Alternatives {
     int k, slots;     // slots: of a piece, k or more, even
     int64_t pieces;
     uint8_t *count;   // [T][pieces]
-    Found *found;     // [T][pieces][slots]
+    Found *found;     // [T][pieces][slots]; a piece's largest first
     uint32_t *least;  // [k][T]: the classes' largest logits, as ordered(); null for few tokens
 };
 
@@ -171,7 +171,7 @@ struct ScoreEpi {
         for (int j = 0; j < 32; ++j) b[j & 3] |= v[j] >= bound ? 1u << j : 0u;
         return ((b[0] | b[1]) | (b[2] | b[3])) & (cnt >= 32 ? ~0u : (1u << max(cnt, 0)) - 1);
     }
-    // What reaches the bound is written by ascending column.  Where that is more than there are slots, the bound is raised
+    // What reaches the bound is written.  Where that is more than there are slots, the bound is raised
     // by bisection until it leaves k or a few more; among equals at such a bound the first columns are written.
     // A lane's run goes through its own shared memory, so that what is written is found by its number: a branch for each
     // of 128 registers takes 80000 cycles a tile, most of them waiting for instructions.
@@ -225,8 +225,11 @@ struct ScoreEpi {
                     hi = u - 1;
                 }
             }
+            // the largest comes first, so that the join may leave the others unread
             Found *to = alt.found + at * alt.slots;
             int room = alt.slots - n;
+            bool led = false;
+            c = 1;
 #pragma unroll
             for (int i = 0; i < kRuns; ++i) {
                 if (equal[i]) {
@@ -239,7 +242,11 @@ struct ScoreEpi {
                     for (int j = 0; j < 32; ++j) own[j * 32] = v[i][j];
                     for (uint32_t b = in[i]; b; b &= b - 1) {
                         const int j = __ffs(b) - 1;
-                        to[c++] = {own[j * 32], n0 + i * kPieces * 32 + j};
+                        const Found f{own[j * 32], n0 + i * kPieces * 32 + j};
+                        const bool first = !led && f.l == top;
+                        to[first ? 0 : c] = f;
+                        if (first) led = true;
+                        else ++c;
                     }
                 }
             }
@@ -433,8 +440,8 @@ __device__ __forceinline__ int collect(const Alternatives &alt, int64_t pieces, 
 #pragma unroll
         for (int h = 0; h < kAhead; ++h) {
             const Found *from = found + (p0 + 32 * h + lane) * slots;
-            const int c = counts[h];
             uint4 q = ahead[h];
+            const int c = counts[h] > 0 && __uint_as_float(q.x) >= least ? counts[h] : 0;
             for (int e = 0; __any_sync(~0u, e < c); e += 2) {
                 if (e > 0 && e < c) q = *reinterpret_cast<const uint4 *>(from + e);
                 const Found f[2] = {{e < c ? __uint_as_float(q.x) : kNaN, (int)q.y}, {e + 1 < c ? __uint_as_float(q.z) : kNaN, (int)q.w}};
@@ -552,7 +559,7 @@ __global__ void __launch_bounds__(kJoinThreads) k_score_join(const JoinArgs a, c
                             const int to = atomicAdd(&kept, 1);
                             if (to < kKept) mine[to] = f[i];
                         }
-                    if (!alt.least && f[0].l < least) break;  // in order
+                    if (f[0].l < least && (e == 0 || !alt.least)) break;  // (those of few tokens are in order)
                 }
             };
             if (sh[0][threadIdx.x].m >= least) {

@@ -7,9 +7,9 @@
 // element with 32-bit parameters, moments and gradients and a 16-bit copy, 18 with
 // the moments in 8 bits.  571 million elements take 2.40 ms and 1.44 ms, both 105 %
 // of the measured copy rate (reads outweigh writes).  All in 16 bits with moments
-// in 8 it is 10 bytes an element, and whole-number arithmetic (some 35 of 70
-// instructions) bounds it: 1.34 ms rounded at random, 63 %; 90 million elements in
-// 161 tensors 233 us at random and 191 to nearest (70 %).  The norm takes 319 us of
+// in 8 it is 10 bytes an element, and its 70 instructions bound it, half of them
+// whole-number ones (issue slots 88 % busy): 1.31 ms rounded at random, 64 %; 90
+// million elements in 161 tensors 229 us at random and 191 to nearest (70 %).  The norm takes 319 us of
 // 32-bit gradients (105 %), 183 us of 16-bit ones (92 %).
 //
 // Moments in 8 bits.  64 consecutive elements share an exponent, and an element
@@ -426,13 +426,13 @@ __device__ __forceinline__ void prefetch(const void *p, uint32_t bytes) {
 }
 
 // Moments in 8 bits leave few bytes in flight: a block brings what another will
-// read so many chunks later into the L2 cache (about half the blocks that run at
-// once; 571 million elements with 32-bit parameters 1.43 ms, 1.53 without, 1.75
+// read so many chunks later into the L2 cache, two thirds of the blocks that run
+// at once (571 million elements with 32-bit parameters 1.43 ms, 1.53 without, 1.75
 // with four times as many).  32-bit moments fill the memory's queues by
 // themselves (2.40 ms, 2.45 with it).
 constexpr int64_t kAhead = 400;
 template <class P, class G, bool SMALL, int N>
-__global__ void __launch_bounds__(kThreads, SMALL ? 5 : 3) k_step(const __grid_constant__ Entries<N> t, const Moments mo, const Rates r,
+__global__ void __launch_bounds__(kThreads, SMALL ? 4 : 3) k_step(const __grid_constant__ Entries<N> t, const Moments mo, const Rates r,
                                                    const StepNow *at) {
     let_next_start();
     const Entry &e = entry_of(t, blockIdx.x);
@@ -454,6 +454,14 @@ __global__ void __launch_bounds__(kThreads, SMALL ? 5 : 3) k_step(const __grid_c
     else step_unit<P, G, SMALL, false>(e, i, n, held, mo, r, at);
 }
 
+// b^t by squaring: off by t roundings at most, and nearly 0 where those are many.
+__device__ __forceinline__ double power(double b, int64_t t) {
+    double y = 1;
+    for (; t > 0; t >>= 1, b *= b)
+        if (t & 1) y *= b;
+    return y;
+}
+
 // The step's number goes up, and all that depends on it is computed, in 64 bits.
 __global__ void k_step_begin(int64_t *step, const float *lr_at, double lr, double b1, double b2, const float *norm,
                              const double *wide, double max_norm, uint64_t seed, StepNow *now) {
@@ -464,7 +472,7 @@ __global__ void k_step_begin(int64_t *step, const float *lr_at, double lr, doubl
     const double full = norm && wide && (float)*wide == nrm ? *wide : nrm;
     const int64_t t = *step + 1;
     const double rate = lr_at ? *lr_at : lr;
-    const double bias = threadIdx.x ? 1 / sqrt(1 - pow(b2, (double)t)) : rate / (1 - pow(b1, (double)t));
+    const double rest = 1 - power(threadIdx.x ? b2 : b1, t), bias = threadIdx.x ? 1 / sqrt(rest) : rate / rest;
     const double other = __shfl_down_sync(3u, bias, 1);
     if (threadIdx.x) return;
     StepNow s;
