@@ -666,14 +666,15 @@ class AdamW:
             words += (p.data_ptr(), 0, 0 if c is None else c.data_ptr(), p.numel(), held,
                       bits_of_d + (_P_FLOAT if p.dtype is _F32 else 0))
             held += (p.numel() + BLOCK - 1) // BLOCK * BLOCK
-        spans = sorted((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size(), name)
-                       for name, ts in (("params", params), ("copies", copies)) for t in ts if t is not None and t.numel())
-        for (_, end, one), (start, _, other) in zip(spans, spans[1:]):
-            if start < end:
-                raise ValueError(f"{one} and {other}: two of them overlap")
         self._table = array.array("Q", words)
         self._held, self._device = held, params[0].device
         self._state = self._new_state() if state is None else self._given_state(state)
+        named = [("params", p) for p in params] + [("copies", c) for c in copies] + [("state", t) for t in self._state.values()]
+        spans = sorted((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size(), name) for name, t in named
+                       if t is not None and t.numel())
+        for (_, end, one), (start, _, other) in zip(spans, spans[1:]):
+            if start < end:
+                raise ValueError(f"{one} and {other}: two of their tensors overlap")
         self._work = torch.empty(LIB.pp_stage_adamw_workspace(), dtype=_U8, device=self._device)
 
     @property

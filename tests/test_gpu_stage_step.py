@@ -401,6 +401,10 @@ def test_refusals(S):
         with pytest.raises(ValueError, match="overlap"):
             S.AdamW(twice)
     S.AdamW([p[:5], p[5:], p[5:5]])
+    m, step = z(64), z(1, d=torch.int64)
+    for state in ({"m": m, "v": m, "step": step}, {"m": m, "v": z(64), "step": m[:2].view(torch.int64)}):
+        with pytest.raises(ValueError, match="overlap"):
+            S.AdamW([p], state=state)
     opt = S.AdamW([z(4), z(2, 3)])
     for args, kw, kind in ((([z(4)], 1.0), {}, ValueError), (([z(4), z(6)], 1.0), {}, ValueError),
                            (([z(4), z(2, 3, d=torch.float16)], 1.0), {}, TypeError), (([z(4), z(3, 2).t()], 1.0), {}, ValueError),
