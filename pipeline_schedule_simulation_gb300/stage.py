@@ -27,6 +27,7 @@ from __future__ import annotations
 import array
 import ctypes
 import math
+import operator
 import struct
 
 import torch
@@ -95,6 +96,8 @@ _declare(LIB)
 
 _BF16, _F32, _I64, _I8, _U8 = torch.bfloat16, torch.float32, torch.int64, torch.int8, torch.uint8
 _Tensor, _empty = torch.Tensor, torch.empty
+_data_ptr, _get_device, _is_contiguous, _numel = _Tensor.data_ptr, _Tensor.get_device, _Tensor.is_contiguous, _Tensor.numel
+_dtype, _shape = operator.attrgetter("dtype"), operator.attrgetter("shape")
 # the handle of a device's current stream and the current device, without the objects around them: a small call
 # is mostly its host path
 _raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
@@ -574,6 +577,24 @@ def _listed(tensors, name):
     return list(tensors)
 
 
+def _accessors(tensors, name, dev):
+    """(pointers, types) of tensors that are float or bf16, contiguous and on CUDA device `dev`.  Attribute by attribute:
+    PyTorch's accessors are most of what a call over hundreds of tensors costs, and the loops around them are not."""
+    if not tensors:
+        return [], []
+    try:
+        ptrs, types = list(map(_data_ptr, tensors)), list(map(_dtype, tensors))
+        fine = (dev >= 0 and types.count(_F32) + types.count(_BF16) == len(ptrs) and all(map(_is_contiguous, tensors))
+                and list(map(_get_device, tensors)).count(dev) == len(ptrs))
+    except (TypeError, AttributeError, RuntimeError):
+        fine = False
+    if not fine:
+        for i, t in enumerate(tensors):
+            _flat(t, f"{name}[{i}]", dev, (_F32, _BF16))
+        raise ValueError(f"{name}: tensors without plain memory")
+    return ptrs, types
+
+
 def grad_norm(grads, *, out=None, workspace=None, stream=None):
     """The 2-norm of all gradients together, float [1] on their device: what AdamW.step clips by.
 
@@ -585,13 +606,11 @@ def grad_norm(grads, *, out=None, workspace=None, stream=None):
     if ctx is not None:
         with ctx:
             return grad_norm(grads, out=out, workspace=workspace)
-    words = []
-    for i, g in enumerate(grads):
-        if not (isinstance(g, _Tensor) and ((wide := g.dtype is _F32) or g.dtype is _BF16) and g.get_device() == dev >= 0
-                and g.is_contiguous()):
-            _flat(g, f"grads[{i}]", dev, (_F32, _BF16))
-        words += (0, g.data_ptr(), 0, g.numel(), 0, _G_FLOAT if wide else 0)
-    table = array.array("Q", words)
+    ptrs, types = _accessors(grads, "grads", dev)
+    table = array.array("Q", bytes(8 * _WORDS * len(ptrs)))
+    table[1::_WORDS] = array.array("Q", ptrs)
+    table[3::_WORDS] = array.array("Q", map(_numel, grads))
+    table[5::_WORDS] = array.array("Q", (_G_FLOAT if t is _F32 else 0 for t in types))
     at = table.buffer_info()[0]
     if out is None:
         if dev < 0:
@@ -667,6 +686,8 @@ class AdamW:
                       bits_of_d + (_P_FLOAT if p.dtype is _F32 else 0))
             held += (p.numel() + BLOCK - 1) // BLOCK * BLOCK
         self._table = array.array("Q", words)
+        self._shapes, self._ptrs = [p.shape for p in params], [p.data_ptr() for p in params]
+        self._flags, self._types = self._table[5::_WORDS], None  # of the gradients that the table was filled with last
         self._held, self._device = held, params[0].device
         self._state = self._new_state() if state is None else self._given_state(state)
         named = [("params", p) for p in params] + [("copies", c) for c in copies] + [("state", t) for t in self._state.values()]
@@ -715,19 +736,18 @@ class AdamW:
                 return self.step(grads, lr, norm=norm, max_norm=max_norm)
         if len(grads) != len(self.params):
             raise ValueError(f"grads: expected {len(self.params)}, one for each parameter, got {len(grads)}")
-        table, at = self._table, 0
-        for p, g in zip(self.params, grads):
-            if not (isinstance(g, _Tensor) and g.shape == p.shape and ((wide := g.dtype is _F32) or g.dtype is _BF16)
-                    and g.get_device() == dev and g.is_contiguous()):
-                i = at // _WORDS
-                _flat(g, f"grads[{i}]", dev, (_F32, _BF16))
-                raise ValueError(f"grads[{i}]: expected shape {tuple(p.shape)}, got {tuple(g.shape)}")
-            if p.data_ptr() != table[at]:
-                raise ValueError(f"params[{at // _WORDS}]: its memory is not that which this step was made for")
-            table[at + 1] = g.data_ptr()
-            flags = table[at + 5]
-            table[at + 5] = flags | _G_FLOAT if wide else flags & ~_G_FLOAT
-            at += _WORDS
+        grads = list(grads)
+        ptrs, types = _accessors(grads, "grads", dev)
+        if list(map(_shape, grads)) != self._shapes:
+            i = next(i for i, (g, s) in enumerate(zip(grads, self._shapes)) if g.shape != s)
+            raise ValueError(f"grads[{i}]: expected shape {tuple(self._shapes[i])}, got {tuple(grads[i].shape)}")
+        if list(map(_data_ptr, self.params)) != self._ptrs:
+            raise ValueError("params: their memory is not that which this step was made for")
+        table = self._table
+        table[1::_WORDS] = array.array("Q", ptrs)
+        if types != self._types:
+            self._types = types
+            table[5::_WORDS] = array.array("Q", (f | _G_FLOAT if t is _F32 else f for f, t in zip(self._flags, types)))
         lr_at = _vector(lr, "lr", _F32, dev, 1) if isinstance(lr, _Tensor) else None
         rate = 0.0 if lr_at is not None else float(lr)
         if not math.isfinite(rate):
