@@ -27,8 +27,9 @@
 // 131072 x 4096 187 us, 172 without alternatives.  333 tokens on 50257 x 1000 with
 // 5 take 66 us, of which the product's loads 37: 3 row tiles, whose blocks each
 // load 48 KB for 128 x 256 x 64 products.  Short rows leave the tiles' ends in
-// sight: 8192 tokens on 131072 x 512 take 0.87 ms, 1.57 with 5 alternatives.
+// sight: 8192 tokens on 131072 x 512 take 0.87 ms, 1.44 with 5 alternatives.
 #include <algorithm>
+#include <cmath>
 
 #include "stage_head.cuh"
 
@@ -76,11 +77,17 @@ __device__ __forceinline__ float from_ordered(uint32_t u) {
 // What the pieces' alternatives are written to.
 struct Alternatives {
     int k, slots;     // slots: of a piece, k or more, even
+    float guess;      // how far below the largest of 128 the k-th lies, in distances of the runs' largest (of normal numbers)
     int64_t pieces;
     uint8_t *count;   // [T][pieces]
     Found *found;     // [T][pieces][slots]; a piece's largest first
-    uint32_t *least;  // [k][T]: the classes' largest logits, as ordered(); null for few tokens
+    uint32_t *least;  // [k + 1][T]: the classes' largest logits, as ordered(), and the bound; null for few tokens
 };
+
+// The bound is taken from the classes in a token's first pieces, and then in the pieces of every kEvery-th column
+// tile; the others read it as a word, a tile ahead (8192 tokens on 131072 x 512 with 5 alternatives 1.53 ms with the
+// classes read in every tile, 1.50 like this).
+constexpr int kYoung = 16, kEvery = 8;
 
 template <bool TOP>
 struct ScoreEpi {
@@ -96,7 +103,7 @@ struct ScoreEpi {
     };
     __device__ __forceinline__ void begin(Row &r, int64_t t) const {
         r.target = target[t];
-        if constexpr (TOP) r.least = least_of(t);
+        if constexpr (TOP) r.least = __ldcg(alt.least + (int64_t)alt.k * T + t);
     }
     __device__ __forceinline__ uint32_t least_of(int64_t t) const {
         uint32_t a = ~0u;
@@ -179,22 +186,25 @@ struct ScoreEpi {
                                              const float (&v)[kRuns][32], float *own) const {
         const int64_t at = t * alt.pieces + piece;
         const float top = fmaxf(fmaxf(run[0], run[1]), fmaxf(run[2], run[3]));
-        // no bound a tile ago: perhaps there is one by now
-        const float least = from_ordered(r.least ? r.least : least_of(t));
+        uint32_t low = r.least;
+        if (low == 0 || piece < kYoung || piece / kPieces % kEvery == 0) {
+            low = max(low, least_of(t));
+            if (low > r.least) atomicMax(alt.least + (int64_t)alt.k * T + t, low);
+        }
+        const float least = from_ordered(low);
         int c = 0;
         if (top >= least) {
             constexpr int kAll = kRuns * 32;
             uint32_t lo = ordered(least), hi = max(ordered(top), lo);  // (-0 is below 0)
             uint32_t in[kRuns], equal[kRuns] = {};  // what is written; and what only for the first columns
-            // without a bound the first guess is as far below the least of the runs' largest as that is below the largest
-            const float some = fminf(fminf(run[0], run[1]), fminf(run[2], run[3]));
-            float down = top - some;
+            // without a bound the first guess goes by how far the runs' largest lie apart
+            float down = alt.guess * (top - fminf(fminf(run[0], run[1]), fminf(run[2], run[3])));
             int n = kAll + 1;  // what reaches lo; not known yet
             for (int i = 0;; ++i) {
                 uint32_t u;
                 if (n > kAll) {
-                    u = least == kNegInf && i < 4 ? min(max(ordered(some - down), lo), hi) : lo;
-                    down *= 4;
+                    u = least == kNegInf && i < 4 ? min(max(ordered(top - down), lo), hi) : lo;
+                    down *= 2;
                 } else if (lo == hi) {
                     u = hi + 1;
                 } else {
@@ -238,11 +248,14 @@ struct ScoreEpi {
                     in[i] |= equal[i];
                 }
                 if (in[i]) {
+                    const bool more = in[i] & (in[i] - 1);  // one alone is the run's largest
+                    if (more) {
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) own[j * 32] = v[i][j];
+                        for (int j = 0; j < 32; ++j) own[j * 32] = v[i][j];
+                    }
                     for (uint32_t b = in[i]; b; b &= b - 1) {
                         const int j = __ffs(b) - 1;
-                        const Found f{own[j * 32], n0 + i * kPieces * 32 + j};
+                        const Found f{more ? own[j * 32] : run[i], n0 + i * kPieces * 32 + j};
                         const bool first = !led && f.l == top;
                         to[first ? 0 : c] = f;
                         if (first) led = true;
@@ -617,7 +630,8 @@ ScoreSpace score_space(void *ws, const uint16_t *x, int64_t sx, const uint16_t *
     Carve c{static_cast<unsigned char *>(ws)};
     ScoreSpace s{};
     s.few = few_tokens(T, H);
-    s.alt.k = k, s.alt.slots = (s.few ? k : k + kMoreSlots) + 1 & ~1;
+    s.alt.k = k, s.alt.slots = ((s.few ? k : k + kMoreSlots) + 1) & ~1;
+    s.alt.guess = 0.5f + 0.32f * std::sqrt((float)k);
     s.each = T;
     int64_t pieces;
     if (s.few) {
@@ -640,7 +654,7 @@ ScoreSpace score_space(void *ws, const uint16_t *x, int64_t sx, const uint16_t *
     if (k) {
         s.alt.found = c.take<Found>(pieces * s.each * s.alt.slots);
         s.alt.count = c.take<uint8_t>(pieces * s.each);
-        if (!s.few) s.alt.least = c.take<uint32_t>(k * s.each);
+        if (!s.few) s.alt.least = c.take<uint32_t>((k + 1) * s.each);
     }
     s.bytes = c.used;
     return s;
@@ -671,7 +685,7 @@ int score(const ScoreSpace &s, const uint16_t *x, int64_t sx, const uint16_t *w,
         } else {
             const ProductPlan plan = plan_product(n, V, H, false, false);
             alt.pieces = kPieces * plan.nt;
-            if (TOP) rc = launch_after(k_no_bounds, ceil_div(n * k, 256), 256, 0, stream, 1, alt.least, n * k);
+            if (TOP) rc = launch_after(k_no_bounds, ceil_div(n * (k + 1), 256), 256, 0, stream, 1, alt.least, n * (k + 1));
             if (rc == PP_OK)
                 rc = launch_product<kRowsK, kRowsK>(in_rows(s.x.at.p + t0 * s.x.at.ld, s.x.at.ld), s.w.at, n, V, H,
                                                     ScoreEpi<TOP>{target + t0, n, V, s.part, s.picked, alt}, plan, stream);
