@@ -280,7 +280,7 @@ static_assert(kRuns == 4);
 // 131072 x 4096 with 8 alternatives took 211 us, 169 without those.)
 constexpr int kFewMost = 1024;  // rows of w to a block
 
-// Sums over the warp's lanes of M values; lane i ends with that of value first_of<M>(i).
+// Sums over the warp's lanes of M values; lane i ends with that of value i / (32 / M).
 template <int M>
 __device__ __forceinline__ float sum_apart(const float (&v)[M], int lane) {
     float x[M];
