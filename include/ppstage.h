@@ -226,7 +226,7 @@ int pp_stage_grad_norm(const pp_stage_tensor *list, int64_t count, float *norm, 
  * element and one exponent for each PP_STAGE_BLOCK, e, as floats have it.  A byte's
  * low bits c (m: 7, its 8th is the sign; v: 8) are 0 for 0 and else stand for the
  * float whose bits are (c + 8 (e - w)) << 20, with w = 15 for m and 31 for v; e = 255:
- * NaN.  e is the exponent of the block's largest magnitude rounded up to 4
+ * a block with an infinity or a NaN, which stands for NaN.  Else e is the exponent of the block's largest magnitude rounded up to 4
  * significant bits; magnitudes are rounded to 4 significant bits; an m below the
  * window (2^-w of the block's largest binade) is held as 0, a v as the least that is
  * not 0.

@@ -22,7 +22,7 @@
 //
 // The product bounds it from a few hundred tokens on: 2048 tokens on 131072 x 4096
 // take 1.12 ms (1960 TFLOP/s, the measured burst rate of a library product), 4096
-// with 20 alternatives 2.33 ms (1890; the join of their pieces 0.09 ms of it).
+// with 20 alternatives 2.31 ms (1905; the join of their pieces 0.07 ms of it).
 // One token on 32000 x 2048 with 8 takes 32 us, its 131 MB alone 19; two on
 // 131072 x 4096 187 us, 172 without alternatives.  333 tokens on 50257 x 1000 with
 // 5 take 66 us, of which the product's loads 37: 3 row tiles, whose blocks each

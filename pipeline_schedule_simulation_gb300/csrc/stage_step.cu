@@ -592,11 +592,17 @@ bool bad_tensor(const pp_stage_tensor &t, bool step) {
            t.at % kMoments || !(std::fabs(t.decay) <= 3e38f);
 }
 
+// 31 KB, one for all instances below.
+Entries<kManyEntries> &table_of_thread() {
+    static thread_local Entries<kManyEntries> t;
+    return t;
+}
+
 // Hands the tensors that `want` picks to `launch(table, chunks)`, as many at a
 // time as a table holds; chunk: elements of a block.
 template <class Want, class Launch>
 int in_tables(const pp_stage_tensor *list, int64_t count, int64_t chunk, const Want &want, const Launch &launch) {
-    static thread_local Entries<kManyEntries> many;  // 31 KB
+    Entries<kManyEntries> &many = table_of_thread();
     int64_t i = 0;
     while (i < count) {
         many.count = 0;

@@ -637,7 +637,8 @@ class AdamW:
     or one for each parameter.
 
     The moments are held in 32 bits or (bits=8) in 8: 64 consecutive elements share an exponent, each keeps 4 significant
-    bits; 2.03 bytes an element for both.  With a `seed` moments in 8 bits and bf16 parameters are rounded up with the
+    bits; 2.03 bytes an element for both.  A block of a moment that is not finite any more (a gradient whose square is
+    beyond 32 bits) is NaN from then on; clip by a norm, which such a gradient makes infinite.  With a `seed` moments in 8 bits and bf16 parameters are rounded up with the
     probability of what is cut off, by random bits that depend on the seed, the step and the element's place alone;
     without one to nearest, which an average that changes by 1 - beta2 a step does not survive in 4 bits for long.
 

@@ -335,3 +335,43 @@ def test_stream_graph_and_other_thread_of_work(S):
     for k in again:
         assert torch.equal(again[k], want[0][k]), k
     assert S.wait_failure() == 0
+
+
+def test_two_captured_calls_share_their_workspace(S):
+    """Replayed in turn: each call clears what it needs of the workspace."""
+    a, b = _grid_inputs(600, 5000, 64, 18), _grid_inputs(40, 9000, 128, 19)
+    want = [S.score_forward(*q, top=7) for q in (a, b)]
+    ws = torch.full((max(S.score_forward_workspace(*q[:2], 7) for q in (a, b)),), 255, dtype=torch.uint8, device="cuda")
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graphs, got = [], []
+    for q in (a, b):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=side):
+            got.append(S.score_forward(*q, top=7, workspace=ws))
+        graphs.append(g)
+    for i in (0, 1, 0, 0, 1):
+        for t in got[i].values():
+            t.zero_()
+        graphs[i].replay()
+        torch.cuda.synchronize()
+        for k in want[i]:
+            assert torch.equal(got[i][k], want[i][k]), k
+
+
+def test_refusals(S):
+    x, w, t = _grid_inputs(4, 20, 8, 20)
+    f = torch.zeros(4, device="cuda")
+    for top in (-1, 21, 33, 1.0, True, None):
+        with pytest.raises(ValueError, match="top"):
+            S.score_forward(x, w, t, top=top)
+    wide = torch.zeros(4, 6, device="cuda")
+    for kw, kind in ((dict(top=3, out={"top_logp": wide[:, :3]}), ValueError), (dict(out={"logp": f[:3]}), ValueError),
+                     (dict(top=3, out={"top_index": wide[:, :3].contiguous()}), TypeError), (dict(workspace=t), TypeError)):
+        with pytest.raises((kind, ValueError)):
+            S.score_forward(x, w, t, **kw)
+    with pytest.raises(ValueError):
+        S.score_forward(x, w[:, :4], t)
+    for kw in (dict(entropy=f), dict(dentropy=f), dict(entropy=f, dentropy=f[:3]), dict(outputs=("dy",)), dict(add=True)):
+        with pytest.raises(ValueError):
+            S.score_backward(x, w, t, f, f, **kw)
