@@ -426,6 +426,9 @@ __device__ __forceinline__ int sort_kept(Found *kept, int n, int k, int thread) 
     return min(n, k);
 }
 
+// How many alternatives a piece has; no more than its slots, should its block have given up and written nothing.
+__device__ __forceinline__ int count_of(const Alternatives &alt, int64_t at) { return min((int)alt.count[at], alt.slots); }
+
 struct JoinArgs {
     const Stats *part;
     const float *picked;
@@ -439,14 +442,13 @@ struct JoinArgs {
 __device__ __forceinline__ int collect(const Alternatives &alt, int64_t pieces, int64_t t, float least, bool skip, Found *mine,
                                        int lane) {
     const int k = alt.k, slots = alt.slots;
-    const uint8_t *count = alt.count + t * pieces;
     const Found *found = alt.found + t * pieces * slots;
     int n = 0;
     constexpr int kAhead = 4;
     for (int64_t p0 = 0; p0 < pieces; p0 += 32 * kAhead) {
         int counts[kAhead];
 #pragma unroll
-        for (int h = 0; h < kAhead; ++h) counts[h] = !skip && p0 + 32 * h + lane < pieces ? count[p0 + 32 * h + lane] : 0;
+        for (int h = 0; h < kAhead; ++h) counts[h] = !skip && p0 + 32 * h + lane < pieces ? count_of(alt, t * pieces + p0 + 32 * h + lane) : 0;
         // slots are even in number, so that two are 16 aligned bytes
         uint4 ahead[kAhead];
 #pragma unroll
@@ -491,7 +493,7 @@ __global__ void __launch_bounds__(kJoinThreads) k_score_join(const JoinArgs a, c
 #pragma unroll
         for (int j = 0; j < kCounts; ++j) {
             const int p = threadIdx.x + j * kGroups;
-            if (p < a.pieces) counts[j] = alt.count[blockIdx.x * a.pieces + p];
+            if (p < a.pieces) counts[j] = count_of(alt, blockIdx.x * a.pieces + p);
         }
     }
     // neighbouring tokens are read together
@@ -580,7 +582,7 @@ __global__ void __launch_bounds__(kJoinThreads) k_score_join(const JoinArgs a, c
             if (sh[0][threadIdx.x].m >= least) {
 #pragma unroll
                 for (int j = 0; j < kCounts; ++j) look(threadIdx.x + j * kGroups, counts[j]);
-                for (int64_t p = threadIdx.x + kCounts * kGroups; p < a.pieces; p += kGroups) look(p, alt.count[u * a.pieces + p]);
+                for (int64_t p = threadIdx.x + kCounts * kGroups; p < a.pieces; p += kGroups) look(p, count_of(alt, u * a.pieces + p));
             }
             __syncthreads();
             n = kept;
