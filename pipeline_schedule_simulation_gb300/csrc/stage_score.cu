@@ -65,9 +65,10 @@ struct Found {
 };
 __device__ __forceinline__ bool before(const Found &a, const Found &b) { return a.l > b.l || (a.l == b.l && a.n < b.n); }
 
-// Floats as whole numbers of the same order, above 0 (which stands for no bound).
+// Floats as whole numbers of the same order, above 0 (which stands for no bound).  -0 is taken as 0: no float that is
+// larger follows it, and the search below goes by a number's successor being above it.
 __device__ __forceinline__ uint32_t ordered(float f) {
-    const uint32_t b = __float_as_uint(f);
+    const uint32_t b = __float_as_uint(f + 0.f);
     return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
 __device__ __forceinline__ float from_ordered(uint32_t u) {
@@ -197,7 +198,7 @@ struct ScoreEpi {
         int c = 0;
         if (top >= least) {
             constexpr int kAll = kRuns * 32;
-            uint32_t lo = ordered(least), hi = max(ordered(top), lo);  // (-0 is below 0)
+            uint32_t lo = ordered(least), hi = max(ordered(top), lo);
             uint32_t in[kRuns], equal[kRuns] = {};  // what is written; and what only for the first columns
             // without a bound the first guess goes by how far the runs' largest lie apart
             float down = alt.guess * (top - fminf(fminf(run[0], run[1]), fminf(run[2], run[3])));
@@ -222,7 +223,9 @@ struct ScoreEpi {
                     if (run[r] >= bound) b[r] = reaching(bound, v[r], last - (n0 + r * kPieces * 32));
                     q += __popc(b[r]);
                 }
-                if (u > hi) {  // above the bound that leaves too many: these, and as many equals as there is room for
+                // Above the bound that leaves too many: these, and as many equals as there is room for.  They are fewer
+                // than k (at hi + 1, none or what a larger bound was tried for), so that all written have a slot.
+                if (u > hi) {
 #pragma unroll
                     for (int r = 0; r < kRuns; ++r) equal[r] = in[r] & ~b[r], in[r] = b[r];
                     n = q;

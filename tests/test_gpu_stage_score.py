@@ -89,6 +89,31 @@ def test_equal_logits_come_by_column(S, T, V, k):
     _check(S.score_forward(x, w, t, top=k), want, ["logp", "lse", "entropy", "top_logp", "top_index"])
 
 
+@pytest.mark.parametrize("T,V,H", [(2, 700, 64), (3, 300, 64), (40, 20000, 64), (130, 700, 2048)])
+@pytest.mark.parametrize("k", [1, 5, 32])
+def test_logits_of_minus_zero(S, T, V, H, k):
+    """Logits that are 0, of either sign, alone or above negative ones: equal, so the first columns, each piece's within
+    its places, and the rows beside them as they were."""
+    x, w, t = _grid_inputs(T, V, H, 31)
+    clean = S.score_forward(x, w, t, top=k)
+    first = torch.arange(k, device="cuda")
+    x = x.clone()
+    for sign in (0.0, -0.0):
+        x[::2] = sign  # every other row
+        for rows in (-w.abs(), w.abs(), w):
+            r = S.score_forward(x, rows, t, top=k)
+            assert (r["top_index"][::2] == first).all()
+            R.check(r["top_logp"][::2], (torch.full_like(r["top_logp"][::2], -math.log(V)).double(), torch.tensor(1e-4, device="cuda")))
+        for n in clean:
+            assert torch.equal(r[n][1::2], clean[n][1::2]), n
+    # -0 as the largest logit: products of positive numbers with -0, and some that are negative
+    y = torch.ones(T, H, dtype=torch.bfloat16, device="cuda")
+    rows = torch.full((V, H), -0.0, dtype=torch.bfloat16, device="cuda")
+    rows[::3, 0] = -1.0
+    want = Q.score(y, rows, t, k, exact=True)
+    _check(S.score_forward(y, rows, t, top=k), want, ["logp", "lse", "entropy", "top_logp", "top_index"])
+
+
 @pytest.mark.parametrize("T", [1, 70])
 def test_rising_and_falling_logits(S, T):
     """Logits that rise along the vocabulary, so that every tile beats the one before it; and that fall."""
