@@ -120,8 +120,11 @@ int pp_stage_score_forward(const uint16_t *x, int64_t stride_x, const uint16_t *
  * dentropy is given and not 0):
  *   d[t][v] = dlogp[t] ([v == target[t]] - p) - dentropy[t] p (log p + entropy[t])
  *   dx = d w,  dw = d^T x
- * A token that is left out has no gradient, through its entropy neither.  dx, dw, the
- * rounding of d and what is added for it: as for pp_stage_head_backward. */
+ * A token that is left out has no gradient, through its entropy neither.  dx and dw
+ * as for pp_stage_head_backward, d too: bf16, and the target's term alone keeps what
+ * its rounding leaves over.  Every other term is off by up to 2^-8 of itself (an
+ * accumulating float dw as well): where a row is peaked on a column that is not its
+ * target, that is a rounding of the gradient to bf16 beside the result's own. */
 size_t pp_stage_score_backward_workspace(const uint16_t *x, int64_t stride_x, const uint16_t *w, int64_t stride_w,
                                          int64_t T, int64_t V, int64_t H);
 int pp_stage_score_backward(const uint16_t *x, int64_t stride_x, const uint16_t *w, int64_t stride_w,

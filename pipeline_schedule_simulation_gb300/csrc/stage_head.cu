@@ -20,6 +20,13 @@
 // term leaves over is kept in 32 bits and added where the products' results are
 // finished: times the target's row of w to dx, times the token's row of x to the
 // target's row of dw.
+// Scores (GradEpi<true>, and a policy gradient through GradEpi<false>) take the
+// same d and the same addition, but the argument is the loss's: on a peaked row the
+// likeliest other column, or an entropy's terms, may be as large as the target's and
+// stay rounded.  Logits six units wide put dx and dw off by 0.8e-3 of their norm before
+// the results' own rounding (1.65e-3), 1.85e-3 with it; a row whose gradient is one
+// such term by 1.65e-3, 2.3e-3 with it.  Two parts of 16 bits would hold d to 2^-16
+// and take six products in place of four, forward included.
 //
 // The products bound both directions from a few hundred tokens on: 4096 tokens
 // on 131072 x 4096 take 2.52 ms (1750 TFLOP/s; a cuBLAS product alone holds
@@ -103,8 +110,9 @@ struct Lists {
     int *head, *next;
 };
 
-// d of one piece of the vocabulary: columns v0 .., as bf16.  ENT: with what reaches
-// the logits through the entropy, so that d = c (p - onehot) + b p (log p + entropy).
+// d of one piece of the vocabulary: columns v0 .., as bf16 (why, and what it costs:
+// above).  ENT: with what reaches the logits through the entropy, so that
+// d = c (p - onehot) + b p (log p + entropy).
 template <bool ENT>
 struct GradEpi {
     static constexpr bool kStore = false, kWhole = true;

@@ -346,7 +346,9 @@ def score_backward(x, w, target, lse, dlogp, *, entropy=None, dentropy=None, out
     dentropy = dL/dentropy (float [T]; with it the entropy that score_forward returned).
 
     Returns dx [T, H] bf16 and dw [V, H], or the one named in `outputs`; dw and `add` as in head_backward.  A token
-    that is left out has no gradient, through its entropy neither."""
+    that is left out has no gradient, through its entropy neither.  The logits' gradient is held in bf16 between the
+    products, each term off by up to 2^-8 of itself, but for the target's, whose rest is added in 32 bits: a float dw
+    has 32 bits of the sums, not of the terms."""
     dev = _device(x)
     ctx = _elsewhere(dev, stream)
     if ctx is not None:
