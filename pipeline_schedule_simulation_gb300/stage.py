@@ -647,7 +647,8 @@ class AdamW:
     ``state`` has the flat tensors that a checkpoint keeps: "m", "v" (bits=8: and "m_exp", "v_exp"), each parameter's from
     a multiple of 64 elements on, and "step", int64 [1], the steps taken.  Pass such a dict as ``state`` to go on from it
     (the tensors are used, not copied).  The step's number is counted on the device: a captured step counts on at every
-    replay.  One step at a time: calls on several streams are the caller's to order."""
+    replay.  One step at a time: calls on several streams are the caller's to order, and so are the tensors (``state``
+    among them) that a step on another stream still works on when they are let go."""
 
     def __init__(self, params, *, bits=32, copies=None, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.0, seed=None,
                  state=None):
@@ -699,7 +700,6 @@ class AdamW:
         for (_, end, one), (start, _, other) in zip(spans, spans[1:]):
             if start < end:
                 raise ValueError(f"{one} and {other}: two of their tensors overlap")
-        self._work = torch.empty(LIB.pp_stage_adamw_workspace(), dtype=_U8, device=self._device)
 
     @property
     def state(self):
@@ -763,11 +763,11 @@ class AdamW:
         wide = getattr(norm, "_wide", None)
         s = self._state
         small = self.bits == 8
+        _keep, ws, n = _scratch(None, LIB.pp_stage_adamw_workspace(), self._device, dev)
         rc = LIB.pp_stage_adamw(table.buffer_info()[0], len(self.params), s["m"].data_ptr(), s["v"].data_ptr(),
                                 s["m_exp"].data_ptr() if small else None, s["v_exp"].data_ptr() if small else None,
                                 self._held, s["step"].data_ptr(), lr_at, rate, *self.betas, self.eps, pn, None if wide is None else wide.data_ptr(), max_norm or 1.0,
-                                self.seed is not None, self.seed or 0, self._work.data_ptr(), self._work.numel(),
-                                _raw_stream(dev))
+                                self.seed is not None, self.seed or 0, ws, n, _raw_stream(dev))
         if rc != PP_OK:
             raise PPSchedError(rc, "pp_stage_adamw")
 

@@ -338,6 +338,26 @@ def test_other_stream_and_current_device(S):
     assert torch.equal(m, plain.opt.moments()[0])
 
 
+@pytest.mark.parametrize("bits", [8, 32])
+def test_scratch_belongs_to_the_steps_stream(S, bits):
+    """A step on another stream, waiting there when its optimizer goes: nothing is written into memory that the first
+    stream has been given since."""
+    many, plain = Many(S, F32, F32, bits, seed=1), Many(S, F32, F32, bits, seed=1)
+    plain.opt.step(plain.grads, 1e-2)
+    state = many.opt.state
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(100_000_000)  # 50 ms or so
+    many.opt.step(many.grads, 1e-2, stream=side)
+    many.opt = None
+    given = [torch.full((256,), 255, dtype=torch.uint8, device="cuda") for _ in range(2000)]
+    torch.cuda.synchronize()
+    assert all((t == 255).all() for t in given)
+    for a, b in zip(many.params + list(state.values()), plain.params + list(plain.opt.state.values())):
+        assert torch.equal(a, b)
+
+
 @pytest.mark.parametrize("n", [0, 1, 4095, 16384, 16385, 3 << 20, 40_000_003])
 @pytest.mark.parametrize("dtype", [F32, BF16])
 @pytest.mark.parametrize("offset", [0, 1])
