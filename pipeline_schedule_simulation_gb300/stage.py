@@ -690,10 +690,13 @@ class AdamW:
                       bits_of_d + (_P_FLOAT if p.dtype is _F32 else 0))
             held += (p.numel() + BLOCK - 1) // BLOCK * BLOCK
         self._table = array.array("Q", words)
-        self._shapes, self._ptrs = [p.shape for p in params], [p.data_ptr() for p in params]
+        self._shapes = [p.shape for p in params]
         self._flags, self._types = self._table[5::_WORDS], None  # of the gradients that the table was filled with last
         self._held, self._device = held, params[0].device
         self._state = self._new_state() if state is None else self._given_state(state)
+        # a step goes by the pointers and lengths that these had here
+        self._written = [t for t in (*params, *copies, *self._state.values()) if t is not None]
+        self._ptrs = list(map(_data_ptr, self._written))
         named = [("params", p) for p in params] + [("copies", c) for c in copies] + [("state", t) for t in self._state.values()]
         spans = sorted((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size(), name) for name, t in named
                        if t is not None and t.numel())
@@ -727,6 +730,10 @@ class AdamW:
                 raise ValueError(f"state[{k!r}]: expected memory that starts on 32 bytes")
         return dict(state)
 
+    def _check_memory(self):
+        if list(map(_data_ptr, self._written)) != self._ptrs:
+            raise ValueError("params, copies, state: their memory is not that which this step was made for")
+
     def step(self, grads, lr, *, norm=None, max_norm=None, stream=None):
         """One step.  grads: float or bf16, of the parameters' shapes.  lr: a number, or a float [1] tensor on the device
         that is read when the step runs.  With `norm` (of grad_norm) and `max_norm` the gradients are scaled by
@@ -744,8 +751,7 @@ class AdamW:
         if list(map(_shape, grads)) != self._shapes:
             i = next(i for i, (g, s) in enumerate(zip(grads, self._shapes)) if g.shape != s)
             raise ValueError(f"grads[{i}]: expected shape {tuple(self._shapes[i])}, got {tuple(grads[i].shape)}")
-        if list(map(_data_ptr, self.params)) != self._ptrs:
-            raise ValueError("params: their memory is not that which this step was made for")
+        self._check_memory()
         table = self._table
         table[1::_WORDS] = array.array("Q", ptrs)
         if types != self._types:
@@ -780,6 +786,7 @@ class AdamW:
         if ctx is not None:
             with ctx:
                 return self.moments()
+        self._check_memory()
         m, v = (torch.empty(self._held, dtype=_BF16, device=self._device) for _ in range(2))
         rc = LIB.pp_stage_adamw_moments(s["m"].data_ptr(), s["v"].data_ptr(), s["m_exp"].data_ptr(), s["v_exp"].data_ptr(),
                                         self._held, m.data_ptr(), v.data_ptr(), _raw_stream(dev))

@@ -443,3 +443,26 @@ def test_refusals(S):
     for grads, kind in (([], ValueError), ([z(4).cpu()], ValueError), ([z(4), z(4, d=torch.int64)], TypeError), (z(4), TypeError)):
         with pytest.raises(kind):
             S.grad_norm(grads)
+
+
+def test_a_copy_or_a_state_that_moved_is_refused(S):
+    """A copy's values would go to where it used to be, moments to a tensor that may be too short."""
+    z = lambda *s, d=F32: torch.ones(*s, dtype=d, device="cuda")  # noqa: E731
+    params, copies = [z(4), z(2, 3), z(5)], [z(4, d=BF16), None, z(5, d=BF16)]
+    opt = S.AdamW(params, copies=copies, bits=8)
+    opt.step([z(4), z(2, 3), z(5)], 0.5)
+    old = copies[2]
+    was = copies[2].data
+    old.data = z(5, d=BF16)
+    with pytest.raises(ValueError, match="memory"):
+        opt.step([z(4), z(2, 3), z(5)], 0.5)
+    assert int(opt.state["step"]) == 1
+    old.data = was
+    m = opt.state["m"]
+    was, m.data = m.data, z(64, d=torch.uint8)
+    for call in (lambda: opt.step([z(4), z(2, 3), z(5)], 0.5), opt.moments):
+        with pytest.raises(ValueError, match="memory"):
+            call()
+    m.data = was
+    opt.step([z(4), z(2, 3), z(5)], 0.5)
+    assert torch.equal(copies[2], params[2].to(BF16)) and torch.equal(copies[0], params[0].to(BF16))
