@@ -597,11 +597,24 @@ def _accessors(tensors, name, dev):
     return ptrs, types
 
 
+def _wide_at(norm, dev):
+    """Pointer of what a norm was before its rounding, None where the tensor has none.  Memory of its own is recorded on
+    the current stream, since nobody else knows of it."""
+    wide = getattr(norm, "_wide", None)
+    if wide is None or wide.get_device() != dev:
+        return None
+    at = wide.data_ptr()
+    if norm.data_ptr() != at + 8:
+        wide.record_stream(torch.cuda.current_stream(dev))
+    return at
+
+
 def grad_norm(grads, *, out=None, workspace=None, stream=None):
     """The 2-norm of all gradients together, float [1] on their device: what AdamW.step clips by.
 
     grads: float or bf16 tensors, contiguous, of any shapes.  A gradient above 1.8e19 makes it infinite.  The tensor
-    also carries the norm before its rounding, which the step clips by as long as it rounds to what the tensor holds."""
+    also carries the norm before its rounding, which the step clips by as long as it rounds to what the tensor holds.
+    An `out` keeps the one that it was given first, so that a captured step goes on reading what a later call writes."""
     grads = _listed(grads, "grads")
     dev = _device(grads[0]) if grads else _device(out)
     ctx = _elsewhere(dev, stream)
@@ -617,12 +630,17 @@ def grad_norm(grads, *, out=None, workspace=None, stream=None):
     if out is None:
         if dev < 0:
             raise ValueError("grads: expected at least one tensor, or an `out` on a CUDA device")
-        out = _empty(1, dtype=_F32, device=grads[0].device)
+        # both in one piece of memory: who holds the norm, or records it on another stream, has the other number too
+        both = _empty(2, dtype=torch.float64, device=grads[0].device)
+        out = both.view(_F32)[2:3]
+        out._wide = both[:1]
     po = _vector(out, "out", _F32, dev, 1)
-    wide = out._wide = torch.empty(1, dtype=torch.float64, device=out.device)
+    if not _wide_at(out, dev):
+        out._wide = _empty(1, dtype=torch.float64, device=out.device)
+    wide = _wide_at(out, dev)
     need = LIB.pp_stage_grad_norm_workspace(at, len(grads))
     _keep, ws, n = _scratch(workspace, need, out.device, dev)
-    rc = LIB.pp_stage_grad_norm(at, len(grads), po, wide.data_ptr(), ws, n, _raw_stream(dev))
+    rc = LIB.pp_stage_grad_norm(at, len(grads), po, wide, ws, n, _raw_stream(dev))
     if rc != PP_OK:
         raise PPSchedError(rc, "pp_stage_grad_norm")
     return out
@@ -766,13 +784,13 @@ class AdamW:
         if max_norm is not None and not 0 < max_norm < math.inf:
             raise ValueError(f"max_norm: expected a number above 0, got {max_norm!r}")
         pn = None if norm is None else _vector(norm, "norm", _F32, dev, 1)
-        wide = getattr(norm, "_wide", None)
+        wide = None if norm is None else _wide_at(norm, dev)
         s = self._state
         small = self.bits == 8
         _keep, ws, n = _scratch(None, LIB.pp_stage_adamw_workspace(), self._device, dev)
         rc = LIB.pp_stage_adamw(table.buffer_info()[0], len(self.params), s["m"].data_ptr(), s["v"].data_ptr(),
                                 s["m_exp"].data_ptr() if small else None, s["v_exp"].data_ptr() if small else None,
-                                self._held, s["step"].data_ptr(), lr_at, rate, *self.betas, self.eps, pn, None if wide is None else wide.data_ptr(), max_norm or 1.0,
+                                self._held, s["step"].data_ptr(), lr_at, rate, *self.betas, self.eps, pn, wide, max_norm or 1.0,
                                 self.seed is not None, self.seed or 0, ws, n, _raw_stream(dev))
         if rc != PP_OK:
             raise PPSchedError(rc, "pp_stage_adamw")

@@ -324,6 +324,38 @@ def test_captured_steps_count_on(S):
             assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("given", [False, True])
+def test_a_captured_step_follows_a_norm_that_is_computed_outside(S, given):
+    """Only the step is captured; before each replay grad_norm writes the same tensor, and what it was before its
+    rounding where the step reads it: all as in calls one by one, to the last bit."""
+    def make():
+        return Many(S, F32, F32, 8, copied=True, seed=77)
+
+    one, two = make(), make()
+    norm = S.grad_norm(two.grads, out=torch.empty(1, device="cuda") if given else None)
+    wide = norm._wide
+    at = wide.data_ptr()
+    # the norm's own memory holds both, a caller's tensor has another for it
+    assert (wide.untyped_storage().data_ptr() == norm.untyped_storage().data_ptr()) != given
+    del wide
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        two.opt.step(two.grads, 1e-2, norm=norm, max_norm=0.05)
+    for i in range(4):
+        for m in (one, two):
+            m.grads[11].mul_(1.37)
+        assert S.grad_norm(two.grads, out=norm) is norm and norm._wide.data_ptr() == at
+        torch.cuda.empty_cache()
+        graph.replay()
+        one.opt.step(one.grads, 1e-2, norm=S.grad_norm(one.grads), max_norm=0.05)
+        torch.cuda.synchronize()
+        for a, b in zip([b for b, *_ in one.buffers] + list(one.opt.state.values()),
+                        [b for b, *_ in two.buffers] + list(two.opt.state.values())):
+            assert torch.equal(a, b)
+
+
 def test_other_stream_and_current_device(S):
     many, plain = Many(S, F32, F32, 8, seed=1), Many(S, F32, F32, 8, seed=1)
     side = torch.cuda.Stream()
