@@ -209,7 +209,7 @@ typedef struct {
 /* norm = the root of the sum of the squares of all gradients (of each entry only g,
  * n and g_float are looked at), rounded once; wide (NULL: not wanted) is the same
  * before that.  Squares beyond the range of 32 bits, of gradients above 1.8e19, make
- * the norm infinite. */
+ * the norm infinite; small gradients count in full, subnormal ones too. */
 size_t pp_stage_grad_norm_workspace(const pp_stage_tensor *list, int64_t count);
 int pp_stage_grad_norm(const pp_stage_tensor *list, int64_t count, float *norm, double *wide,
                        void *workspace, size_t workspace_bytes, cudaStream_t stream);

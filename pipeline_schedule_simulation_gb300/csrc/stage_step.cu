@@ -9,8 +9,8 @@
 // of the measured copy rate (reads outweigh writes).  All in 16 bits with moments
 // in 8 it is 10 bytes an element, and its 70 instructions bound it, half of them
 // whole-number ones (issue slots 88 % busy): 1.31 ms rounded at random, 64 %; 90
-// million elements in 161 tensors 229 us at random and 191 to nearest (70 %).  The norm takes 319 us of
-// 32-bit gradients (105 %), 183 us of 16-bit ones (92 %).
+// million elements in 161 tensors 229 us at random and 191 to nearest (70 %).  The norm takes 324 us of
+// 32-bit gradients (104 %), 185 us of 16-bit ones (91 %).
 //
 // Moments in 8 bits.  64 consecutive elements share an exponent, and an element
 // keeps 4 significant bits and its exponent relative to the block's: m a sign and
@@ -506,42 +506,61 @@ struct Squares {
     }
 };
 
-template <class G, int N>
-__global__ void __launch_bounds__(kNormThreads) k_norm(const __grid_constant__ Entries<N> t, int64_t chunk, double *part) {
-    __shared__ double sh[kNormThreads / 32];
-    let_next_start();
-    const Entry &e = entry_of(t, blockIdx.x);
-    const int64_t from = (int64_t)(blockIdx.x - e.first) * chunk, to = min(from + chunk, e.n);
-    const G *g = static_cast<const G *>(e.g);
-    after_previous();
+// The sum of a thread's squares, of elements i on below `to`; SCALED: of 2^90 times the elements.
+template <bool SCALED, class G>
+__device__ __forceinline__ double squares_of(const G *g, int64_t i, int64_t to, bool vec) {
     constexpr int kEach = kNormThreads * kUnit;
+    const auto pair = [](float a, float b) { return SCALED ? mul2({a, b}, {0x1p90f, 0x1p90f}) : make_float2(a, b); };
     Squares s[2];
-    int64_t i = from + threadIdx.x * kUnit;
-    if (e.vec) {
+    if (vec) {
         for (; i + kUnit + kEach <= to; i += 2 * kEach) {
             float a[8], b[8];
             load<true>(g + i, 8, a);
             load<true>(g + i + kEach, 8, b);
 #pragma unroll
-            for (int j = 0; j < 8; j += 2) s[0].add({a[j], a[j + 1]}), s[1].add({b[j], b[j + 1]});
+            for (int j = 0; j < 8; j += 2) s[0].add(pair(a[j], a[j + 1])), s[1].add(pair(b[j], b[j + 1]));
         }
     }
     for (; i < to; i += kEach) {
         float a[8];
         load<false>(g + i, to - i < kUnit ? (int)(to - i) : kUnit, a);
 #pragma unroll
-        for (int j = 0; j < 8; j += 4) s[0].add({a[j], a[j + 1]}), s[1].add({a[j + 2], a[j + 3]});
+        for (int j = 0; j < 8; j += 4) s[0].add(pair(a[j], a[j + 1])), s[1].add(pair(a[j + 2], a[j + 3]));
     }
-    double x = s[0].total() + s[1].total();
+    return s[0].total() + s[1].total();
+}
+
+// A block's sum, in thread 0.
+__device__ __forceinline__ double sum_of_block(double x, double (&sh)[kNormThreads / 32]) {
 #pragma unroll
     for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(~0u, x, o);
     if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = x;
     __syncthreads();
-    if (threadIdx.x == 0) {
-        x = 0;
+    x = 0;
+    if (threadIdx.x == 0)
         for (int k = 0; k < kNormThreads / 32; ++k) x += sh[k];
-        part[blockIdx.x] = x;
-    }
+    return x;
+}
+
+// A square below 2^-126 loses bits, of a gradient below 2^-75 all: each 2^-147 at most with its rest, nothing beside a
+// block's sum of 2^-70.  A block that has less takes its elements, all below 2^-35 then, once more, 2^90 times as large:
+// subnormal ones become normal, and no sum exceeds 2^110.  571 million float gradients take 324 us, 322 without this; a
+// block whose gradients are all 0 reads them twice (all of them 626 us).  To look for bits that are not 0 on the way
+// spares that, but takes 5 % more of every call (337 us).
+constexpr double kSmallSum = 0x1p-70;
+
+template <class G, int N>
+__global__ void __launch_bounds__(kNormThreads) k_norm(const __grid_constant__ Entries<N> t, int64_t chunk, double *part) {
+    __shared__ double sh[kNormThreads / 32], again[kNormThreads / 32];
+    let_next_start();
+    const Entry &e = entry_of(t, blockIdx.x);
+    const int64_t from = (int64_t)(blockIdx.x - e.first) * chunk, to = min(from + chunk, e.n);
+    const G *g = static_cast<const G *>(e.g);
+    after_previous();
+    const int64_t i = from + threadIdx.x * kUnit;
+    double x = sum_of_block(squares_of<false>(g, i, to, e.vec), sh);
+    if (__syncthreads_or(threadIdx.x == 0 && x < kSmallSum)) x = sum_of_block(squares_of<true>(g, i, to, e.vec) * 0x1p-180, again);
+    if (threadIdx.x == 0) part[blockIdx.x] = x;
 }
 
 __global__ void __launch_bounds__(1024) k_norm_join(const double *part, int64_t n, float *norm, double *wide) {

@@ -406,6 +406,28 @@ def test_norm(S, n, dtype, offset):
         assert S.grad_norm(grads, out=out, workspace=ws) is out and torch.equal(out, got)
 
 
+@pytest.mark.parametrize("n", [1, 9, 5000, 3 << 20])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("scale", [1e-10, 1e-18, 1e-21, 1e-25, 1e-38, 1e-40])
+@pytest.mark.parametrize("offset", [0, 1])
+def test_norm_of_small_gradients(S, n, dtype, scale, offset):
+    """Gradients whose squares are subnormal in 32 bits, or nothing: rounded once, as large ones are (the norm itself may
+    be subnormal: half its step then).  Alone, and with a tensor, an element and a run of elements that are larger."""
+    g = R.generator(n)
+    x = _random(g, n, dtype, scale, offset)[1]
+    assert n == 1 or (x != 0).any()  # (bf16's least number is 9.2e-41: one element of 1e-40 may be 0)
+    y, z = x.clone(), x.clone()
+    y[n // 2] = scale * 1000
+    z[:n // 3] *= 1024
+    for grads in ([x], [y], [z], [x, x[:0], y, z], [x, torch.full((3,), scale * 64, device="cuda")], [x, torch.zeros(70000, device="cuda")]):
+        want = sum(q.double().square().sum() for q in grads) ** 0.5
+        got = S.grad_norm(grads)
+        assert abs(got.double() - want) <= 2.0 ** -24 * 1.001 * want + 2.0 ** -150
+        assert abs(got._wide - want) <= 2.0 ** -40 * want
+    ones = torch.ones(1, device="cuda")
+    assert float(S.grad_norm([x, ones])) == float((1 + x.double().square().sum()).sqrt().float())
+
+
 def test_norm_of_many_tensors(S):
     g = R.generator(8)
     grads = [torch.randn(int(n), generator=g, device="cuda").to(F32 if i % 3 else BF16)
