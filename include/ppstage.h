@@ -220,7 +220,8 @@ int pp_stage_grad_norm(const pp_stage_tensor *list, int64_t count, float *norm, 
  *       and *wide, if given, in its place where it rounds to that)
  *   m = beta1 m + (1 - beta1) c g     v = beta2 v + (1 - beta2) (c g)^2
  *   p = p (1 - lr decay) - lr / (1 - beta1^t) m / (sqrt(v / (1 - beta2^t)) + eps)
- * lr is *lr_at (a device float) where that is given.  Where *norm is not a finite
+ * eps is 0 or at least 2^-126, a normal number in 32 bits (with 0, an element whose
+ * moments are both 0 is 0 / 0).  lr is *lr_at (a device float) where that is given.  Where *norm is not a finite
  * number nothing changes, *step neither.
  *
  * Moments: `held` elements of m and of v, those of a tensor from `at` on, 32-byte

@@ -122,7 +122,8 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
     return of_pair(y);
 }
 
-// The root is a normal number or 0 whatever x is, so what is below 2^-126 plays no part in the reciprocal.
+// The root is a normal number or 0 whatever x is, and so is eps (checked), so what is below 2^-126 plays no part in the
+// reciprocal.
 __device__ __forceinline__ float reciprocal(float x) {
     float y;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -734,7 +735,7 @@ extern "C" int pp_stage_adamw(const pp_stage_tensor *list, int64_t count, void *
     if (!aligned_to(m, 32) || !aligned_to(v, 32)) return PP_ERR_ARG;
     for (int64_t i = 0; i < count; ++i)
         if (list[i].n && list[i].n > held - list[i].at) return PP_ERR_ARG;
-    if (!(beta1 >= 0 && beta1 < 1 && beta2 >= 0 && beta2 < 1 && eps >= 0 && eps <= 3e38)) return PP_ERR_ARG;
+    if (!(beta1 >= 0 && beta1 < 1 && beta2 >= 0 && beta2 < 1 && (eps == 0 || (eps >= 0x1p-126 && eps <= 3e38)))) return PP_ERR_ARG;
     if (lr_at ? !aligned_to(lr_at, 4) : !(std::fabs(lr) <= 3e38)) return PP_ERR_ARG;
     if (norm && (!aligned_to(norm, 4) || !aligned_to(wide, 8) || !(max_norm > 0))) return PP_ERR_ARG;
     if (!workspace || !aligned_to(workspace, kStageAlign) || workspace_bytes < sizeof(StepNow)) return PP_ERR_ARG;

@@ -678,8 +678,8 @@ class AdamW:
         b1, b2 = (float(b) for b in betas)
         if not (0 <= b1 < 1 and 0 <= b2 < 1):
             raise ValueError(f"betas: expected two numbers from 0 to below 1, got {betas!r}")
-        if not 0 <= float(eps) < math.inf:
-            raise ValueError(f"eps: expected a number that is not negative, got {eps!r}")
+        if float(eps) != 0 and not 2.0 ** -126 <= float(eps) <= 3e38:
+            raise ValueError(f"eps: expected 0 or a normal number of 32 bits above it, got {eps!r}")
         if seed is not None and (isinstance(seed, bool) or not isinstance(seed, int) or not 0 <= seed < 1 << 64):
             raise ValueError(f"seed: expected a whole number of 64 bits or None, got {seed!r}")
         dev = _device(params[0])

@@ -520,3 +520,18 @@ def test_a_copy_or_a_state_that_moved_is_refused(S):
     m.data = was
     opt.step([z(4), z(2, 3), z(5)], 0.5)
     assert torch.equal(copies[2], params[2].to(BF16)) and torch.equal(copies[0], params[0].to(BF16))
+
+
+@pytest.mark.parametrize("bits", [8, 32])
+def test_the_least_eps(S, bits):
+    """Moments of 0 make no step with any eps that is taken; smaller ones than 2^-126 are refused."""
+    p = torch.ones(100, device="cuda")
+    g = torch.zeros(100, device="cuda")
+    S.AdamW([p], bits=bits, eps=2.0 ** -126).step([g], 1e-2)
+    assert (p == 1).all()
+    g[5] = 2.0
+    S.AdamW([p], bits=bits, eps=2.0 ** -126).step([g], 0.25)  # m / sqrt(v) is 1
+    assert abs(float(p[5]) - 0.75) <= 2 ** -19 and (p[:5] == 1).all() and (p[6:] == 1).all()
+    for eps in (1e-40, 1e-46, 1e-300, 3.1e38, math.inf, math.nan):
+        with pytest.raises(ValueError, match="eps"):
+            S.AdamW([p], bits=bits, eps=eps)

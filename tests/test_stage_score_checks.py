@@ -81,6 +81,12 @@ def test_step():
     assert adamw(held=(1 << 38) + 64) == B.PP_ERR_SIZE
 
 
+@pytest.mark.parametrize("eps", [1e-300, 1e-46, 1e-40, 2.0 ** -126 * (1 - 2 ** -53), 3.1e38])
+def test_an_eps_that_is_no_normal_number(eps):
+    """The step's reciprocal takes what is below 2^-126 as 0: with both moments 0 it would make NaN of 0 / eps."""
+    assert adamw(eps=eps) == B.PP_ERR_ARG
+
+
 def test_norm_and_moments():
     def norm(*entries, count=None, out=P, wide=None, ws=P, n=1 << 20):
         t = _list(*entries)
