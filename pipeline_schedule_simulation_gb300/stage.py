@@ -715,6 +715,7 @@ class AdamW:
         # a step goes by the pointers and lengths that these had here
         self._written = [t for t in (*params, *copies, *self._state.values()) if t is not None]
         self._ptrs = list(map(_data_ptr, self._written))
+        self._updated = [t for t in (*params, *copies) if t is not None]
         named = [("params", p) for p in params] + [("copies", c) for c in copies] + [("state", t) for t in self._state.values()]
         spans = sorted((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size(), name) for name, t in named
                        if t is not None and t.numel())
@@ -794,6 +795,8 @@ class AdamW:
                                 self.seed is not None, self.seed or 0, ws, n, _raw_stream(dev))
         if rc != PP_OK:
             raise PPSchedError(rc, "pp_stage_adamw")
+        # what autograd saved of them before is not what a backward pass would find now
+        torch.autograd.graph.increment_version(self._updated)
 
     def moments(self, *, stream=None):
         """(m, v) as numbers, flat as in ``state``: its float tensors themselves, or what the 8 bits stand for, as bf16."""

@@ -535,3 +535,24 @@ def test_the_least_eps(S, bits):
     for eps in (1e-40, 1e-46, 1e-300, 3.1e38, math.inf, math.nan):
         with pytest.raises(ValueError, match="eps"):
             S.AdamW([p], bits=bits, eps=eps)
+
+
+def test_autograd_notices_a_step(S):
+    """What was saved for a backward pass before a step is refused after it, as after an optimizer of PyTorch's."""
+    master, grad = torch.ones(8, 8, device="cuda"), torch.ones(8, 8, device="cuda")
+    copy = torch.ones(8, 8, dtype=BF16, device="cuda")
+    opt = S.AdamW([master], copies=[copy])
+    for saved in (master, copy):
+        x = torch.ones(2, 8, dtype=saved.dtype, device="cuda", requires_grad=True)
+        y = (x @ saved).sum()
+        opt.step([grad], 1e-2)
+        with pytest.raises(RuntimeError, match="inplace"):
+            y.backward()
+        (x @ saved).sum().backward()  # a new pass sees the new values
+        want = saved.double().sum(1)  # a sum of 8 equal numbers: 7 additions, 2^-24 of it each at most, and bf16's rounding
+        assert ((x.grad.double() - want).abs() <= (7 * 2.0 ** -24 + (Q.U16 if saved is copy else 0)) * want).all()
+    # parameters that were made in inference mode have no version; a captured step bumps it once
+    with torch.inference_mode():
+        p = torch.ones(4, device="cuda")
+    S.AdamW([p]).step([torch.ones(4, device="cuda")], 0.5)
+    assert torch.allclose(p, torch.full_like(p, 0.5), atol=1e-5)
