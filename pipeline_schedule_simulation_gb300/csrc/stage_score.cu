@@ -397,9 +397,15 @@ __global__ void __launch_bounds__(32 * kFewWarps, kFewBlocks)
 // block takes one.  First the largest logit, then the sums relative to it, then of
 // the alternatives those that reach the k-th of the lanes' largest logits (as many
 // different logits do), a lane whose pieces have none left out.
-// The first gives 32 lanes to a token, the second 256: one token with 8
-// alternatives in 608 pieces takes 43 us altogether with the second and 51 with the
-// first.  From 4 tokens to an SM on the second's blocks do not run at once.
+// The first gives 32 lanes to a token, the second 256.  With alternatives (80
+// registers: three such blocks to an SM) a token is so much to look through that
+// the second stays ahead beyond the blocks that run at once.  Whole calls on
+// 32000 x 256 with 5 and with 20, a block to a token against 8 tokens a block: one
+// token 11.3 / 16.9 and 13.6 / 45.5 us, 456 41.6 / 48.3 and 56 / 76, 608 (four to an
+// SM) 54.9 / 54.8 and 73 / 85, 900 71 / 69 and 89 / 96, 2048 127 / 109 and 162 / 142.
+// Without alternatives a token is two sums: one 7.8 / 8.7 us, 3 10.4 / 10.7, 64
+// 14.8 / 11.1 (on 131072 x 64 3 tokens 18.2 / 19.5, 4 19.8 / 19.5, 16 32.4 / 20.6).
+constexpr int kOneToSM = 4, kOneAlone = 3;  // up to so many tokens a block each: to an SM with alternatives, in all without
 constexpr int kJoinThreads = 256, kKept = 256;  // kKept: alternatives that are sorted at a time
 
 // Of the n entries in shared memory the first k, in order, by THREADS threads (a warp, or the block).
@@ -700,7 +706,7 @@ int score(const ScoreSpace &s, const uint16_t *x, int64_t sx, const uint16_t *w,
                                                     ScoreEpi<TOP>{target + t0, n, V, s.part, s.picked, alt}, plan, stream);
         }
         const auto from = [&](auto *p, int64_t each) { return p ? p + t0 * each : p; };
-        const bool one = n <= 4 * (int64_t)sm_count();  // all blocks run at once
+        const bool one = n <= (TOP ? kOneToSM * (int64_t)sm_count() : kOneAlone);
         if (rc == PP_OK)
             rc = launch_after(one ? k_score_join<TOP, 1> : k_score_join<TOP, 8>, one ? n : ceil_div(n, 8), kJoinThreads, 0,
                               stream, 1,

@@ -56,6 +56,17 @@ def test_forward(S, T, V, H, k):
     assert (got["logp"][target < 0] == 0).all()
 
 
+@pytest.mark.parametrize("k", [0, 1, 6])
+def test_both_joins(S, k):
+    """Around the numbers of tokens from which a block joins the pieces of eight: to the last bit the same alternatives,
+    and each token's numbers as in a call of its own kind."""
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    x, w, t = _grid_inputs(4 * sms + 9, 2000, 64, 41)
+    for T in (2, 3, 4, 5, 3 * sms, 3 * sms + 1, 4 * sms, 4 * sms + 1, 4 * sms + 9):
+        got, want = S.score_forward(x[:T], w, t[:T], top=k), Q.score(x[:T], w, t[:T], k, exact=True)
+        _check(got, want, want)
+
+
 @pytest.mark.parametrize("T,V,H", [(2, 3000, 512), (200, 3000, 512)])
 def test_forward_off_the_grid(S, T, V, H):
     """Logits that are rounded: an alternative's own logit is no further below the true one of its rank than they are off."""
