@@ -56,6 +56,16 @@ def test_forward(S, T, V, H, k):
     assert (got["logp"][target < 0] == 0).all()
 
 
+@pytest.mark.parametrize("T", [3, 4, 8, 16, 37, 64, 128])
+@pytest.mark.parametrize("V,H", [(32000, 128), (50257, 72)])
+@pytest.mark.parametrize("k", [0, 8, 20, 32])
+def test_a_batch_of_single_tokens(S, T, V, H, k):
+    """One token of each sequence against a vocabulary of tens of thousands."""
+    x, w, target = _grid_inputs(T, V, H, T + k)
+    want = Q.score(x, w, target, k, exact=True)
+    _check(S.score_forward(x, w, target, top=k), want, want)
+
+
 @pytest.mark.parametrize("k", [0, 1, 6])
 def test_both_joins(S, k):
     """Around the numbers of tokens from which a block joins the pieces of eight: to the last bit the same alternatives,
