@@ -36,8 +36,8 @@ from .binding import LIB, PP_OK, PPSchedError, _arg, _check, _reach
 
 EXPORTS = ("pp_stage_head_forward_workspace", "pp_stage_head_forward", "pp_stage_head_backward_workspace",
            "pp_stage_head_backward", "pp_stage_score_forward_workspace", "pp_stage_score_forward",
-           "pp_stage_score_backward_workspace", "pp_stage_score_backward", "pp_stage_pack", "pp_stage_unpack", "pp_stage_weight_grad_workspace",
-           "pp_stage_weight_grad", "pp_stage_join_forward", "pp_stage_join_backward_workspace",
+           "pp_stage_score_backward_workspace", "pp_stage_score_backward", "pp_stage_pack", "pp_stage_unpack",
+           "pp_stage_weight_grad_workspace", "pp_stage_weight_grad", "pp_stage_join_forward", "pp_stage_join_backward_workspace",
            "pp_stage_join_backward", "pp_stage_grad_norm_workspace", "pp_stage_grad_norm", "pp_stage_adamw_workspace",
            "pp_stage_adamw", "pp_stage_adamw_moments", "pp_stage_wait_failure")
 
@@ -92,6 +92,7 @@ def _declare(lib):
 
 
 _declare(LIB)
+_STEP_BYTES = LIB.pp_stage_adamw_workspace()
 
 
 _BF16, _F32, _I64, _I8, _U8 = torch.bfloat16, torch.float32, torch.int64, torch.int8, torch.uint8
@@ -101,6 +102,7 @@ _dtype, _shape = operator.attrgetter("dtype"), operator.attrgetter("shape")
 # the handle of a device's current stream and the current device, without the objects around them: a small call
 # is mostly its host path
 _raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+_capturing = torch._C._cuda_isCurrentStreamCapturing
 
 
 class Packed:
@@ -598,15 +600,14 @@ def _accessors(tensors, name, dev):
 
 
 def _wide_at(norm, dev):
-    """Pointer of what a norm was before its rounding, None where the tensor has none.  Memory of its own is recorded on
-    the current stream, since nobody else knows of it."""
+    """Pointer of what a norm was before its rounding, None where the tensor has none.  Who records the norm on another
+    stream does not know of it, so every stream that uses it is recorded here."""
     wide = getattr(norm, "_wide", None)
     if wide is None or wide.get_device() != dev:
         return None
-    at = wide.data_ptr()
-    if norm.data_ptr() != at + 8:
+    if wide._made_on != _raw_stream(dev):
         wide.record_stream(torch.cuda.current_stream(dev))
-    return at
+    return wide.data_ptr()
 
 
 def grad_norm(grads, *, out=None, workspace=None, stream=None):
@@ -630,14 +631,13 @@ def grad_norm(grads, *, out=None, workspace=None, stream=None):
     if out is None:
         if dev < 0:
             raise ValueError("grads: expected at least one tensor, or an `out` on a CUDA device")
-        # both in one piece of memory: who holds the norm, or records it on another stream, has the other number too
-        both = _empty(2, dtype=torch.float64, device=grads[0].device)
-        out = both.view(_F32)[2:3]
-        out._wide = both[:1]
+        out = _empty(1, dtype=_F32, device=grads[0].device)
     po = _vector(out, "out", _F32, dev, 1)
-    if not _wide_at(out, dev):
-        out._wide = _empty(1, dtype=torch.float64, device=out.device)
     wide = _wide_at(out, dev)
+    if wide is None:
+        out._wide = t = _empty(1, dtype=torch.float64, device=out.device)
+        t._made_on = _raw_stream(dev)
+        wide = t.data_ptr()
     need = LIB.pp_stage_grad_norm_workspace(at, len(grads))
     _keep, ws, n = _scratch(workspace, need, out.device, dev)
     rc = LIB.pp_stage_grad_norm(at, len(grads), po, wide, ws, n, _raw_stream(dev))
@@ -652,15 +652,17 @@ class AdamW:
         m = beta1 m + (1 - beta1) g      v = beta2 v + (1 - beta2) g^2
         p = p (1 - lr decay) - lr / (1 - beta1^t) m / (sqrt(v / (1 - beta2^t)) + eps)
 
-    params: contiguous float or bf16 tensors of any shapes, updated in place, none overlapping another.  copies: for float parameters, a list of
-    bf16 tensors of the same shapes (or None for one that has none) that receive the new values.  weight_decay: a number,
-    or one for each parameter.
+    params: contiguous float or bf16 tensors of any shapes, updated in place, none overlapping another, nor a gradient.
+    copies: for float parameters, a list of bf16 tensors of the same shapes (or None for one that has none) that receive
+    the new values.  weight_decay: a number, or one for each parameter.  eps: 0 (an element whose moments are both 0 is
+    then 0 / 0), or 2**-126 and more.  All these keep the memory that they have here: a step refuses others.
 
     The moments are held in 32 bits or (bits=8) in 8: 64 consecutive elements share an exponent, each keeps 4 significant
     bits; 2.03 bytes an element for both.  A block of a moment that is not finite any more (a gradient whose square is
-    beyond 32 bits) is NaN from then on; clip by a norm, which such a gradient makes infinite.  With a `seed` moments in 8 bits and bf16 parameters are rounded up with the
-    probability of what is cut off, by random bits that depend on the seed, the step and the element's place alone;
-    without one to nearest, which an average that changes by 1 - beta2 a step does not survive in 4 bits for long.
+    beyond 32 bits) is NaN from then on; clip by a norm, which such a gradient makes infinite.  With a `seed` moments in
+    8 bits and bf16 parameters are rounded up with the probability of what is cut off, by random bits that depend on the
+    seed, the step and the element's place alone; without one to nearest, which an average that changes by 1 - beta2 a
+    step does not survive in 4 bits for long.
 
     ``state`` has the flat tensors that a checkpoint keeps: "m", "v" (bits=8: and "m_exp", "v_exp"), each parameter's from
     a multiple of 64 elements on, and "step", int64 [1], the steps taken.  Pass such a dict as ``state`` to go on from it
@@ -716,7 +718,10 @@ class AdamW:
         self._written = [t for t in (*params, *copies, *self._state.values()) if t is not None]
         self._ptrs = list(map(_data_ptr, self._written))
         self._updated = [t for t in (*params, *copies) if t is not None]
-        named = [("params", p) for p in params] + [("copies", c) for c in copies] + [("state", t) for t in self._state.values()]
+        with torch.cuda.device(dev):
+            self._work, self._work_on = _empty(_STEP_BYTES, dtype=_U8, device=self._device), _raw_stream(dev)
+        named = ([("params", p) for p in params] + [("copies", c) for c in copies]
+                 + [("state", t) for t in self._state.values()])
         spans = sorted((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size(), name) for name, t in named
                        if t is not None and t.numel())
         for (_, end, one), (start, _, other) in zip(spans, spans[1:]):
@@ -788,11 +793,16 @@ class AdamW:
         wide = None if norm is None else _wide_at(norm, dev)
         s = self._state
         small = self.bits == 8
-        _keep, ws, n = _scratch(None, LIB.pp_stage_adamw_workspace(), self._device, dev)
+        # its own scratch memory only where that was allocated: another stream's step has its own, and a captured one
+        # the graph's (allocating at every step takes 5 us of a small one's 20)
+        ws = self._work
+        if _raw_stream(dev) != self._work_on or _capturing():
+            ws = _empty(_STEP_BYTES, dtype=_U8, device=self._device)
         rc = LIB.pp_stage_adamw(table.buffer_info()[0], len(self.params), s["m"].data_ptr(), s["v"].data_ptr(),
                                 s["m_exp"].data_ptr() if small else None, s["v_exp"].data_ptr() if small else None,
-                                self._held, s["step"].data_ptr(), lr_at, rate, *self.betas, self.eps, pn, wide, max_norm or 1.0,
-                                self.seed is not None, self.seed or 0, ws, n, _raw_stream(dev))
+                                self._held, s["step"].data_ptr(), lr_at, rate, *self.betas, self.eps, pn, wide,
+                                max_norm or 1.0, self.seed is not None, self.seed or 0, ws.data_ptr(), _STEP_BYTES,
+                                _raw_stream(dev))
         if rc != PP_OK:
             raise PPSchedError(rc, "pp_stage_adamw")
         # what autograd saved of them before is not what a backward pass would find now

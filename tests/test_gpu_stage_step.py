@@ -335,8 +335,6 @@ def test_a_captured_step_follows_a_norm_that_is_computed_outside(S, given):
     norm = S.grad_norm(two.grads, out=torch.empty(1, device="cuda") if given else None)
     wide = norm._wide
     at = wide.data_ptr()
-    # the norm's own memory holds both, a caller's tensor has another for it
-    assert (wide.untyped_storage().data_ptr() == norm.untyped_storage().data_ptr()) != given
     del wide
     side = torch.cuda.Stream()
     side.wait_stream(torch.cuda.current_stream())
@@ -384,6 +382,25 @@ def test_scratch_belongs_to_the_steps_stream(S, bits):
     many.opt.step(many.grads, 1e-2, stream=side)
     many.opt = None
     given = [torch.full((256,), 255, dtype=torch.uint8, device="cuda") for _ in range(2000)]
+    torch.cuda.synchronize()
+    assert all((t == 255).all() for t in given)
+    for a, b in zip(many.params + list(state.values()), plain.params + list(plain.opt.state.values())):
+        assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("bits", [8, 32])
+def test_a_captured_step_outlives_its_optimizer(S, bits):
+    """The graph writes into the tensors that its owner keeps, and into nothing that the allocator has given away."""
+    many, plain = Many(S, F32, F32, bits, seed=1), Many(S, F32, F32, bits, seed=1)
+    state = many.opt.state
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        many.opt.step(many.grads, 1e-2)
+    many.opt = None
+    given = [torch.full((256,), 255, dtype=torch.uint8, device="cuda") for _ in range(2000)]
+    for _ in range(3):
+        graph.replay()
+        plain.opt.step(plain.grads, 1e-2)
     torch.cuda.synchronize()
     assert all((t == 255).all() for t in given)
     for a, b in zip(many.params + list(state.values()), plain.params + list(plain.opt.state.values())):
