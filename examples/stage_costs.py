@@ -16,10 +16,10 @@ and after the flush the AdamW step over all of the stage's tensors, clipped by
 the norm of the gradients: parameters in 32 bits with the 16-bit copies that F
 and B run on, moments in 8 bits.
 
-F, B, W and the step are timed; the times of F, B and W, as ticks, are then the costs of a P-stage
-pipeline of such stages that the schedule evaluator compares under GPipe, 1F1B
-and the Zero Bubble schedules, next to the bytes that 1F1B's peak of held
-microbatches takes in 8 bits and in bf16.
+F, B, W and the step are timed; the times of F, B and W, as ticks, are then the
+costs of a P-stage pipeline of such stages that the schedule evaluator compares
+under GPipe, 1F1B and the Zero Bubble schedules, next to the bytes that 1F1B's
+peak of held microbatches takes in 8 bits and in bf16.
 
     python examples/stage_costs.py [--tokens 2048 --width 2048 --vocab 32000 --blocks 2 --stages 8 --microbatches 16]
 """

@@ -221,8 +221,8 @@ int pp_stage_grad_norm(const pp_stage_tensor *list, int64_t count, float *norm, 
  *   m = beta1 m + (1 - beta1) c g     v = beta2 v + (1 - beta2) (c g)^2
  *   p = p (1 - lr decay) - lr / (1 - beta1^t) m / (sqrt(v / (1 - beta2^t)) + eps)
  * eps is 0 or at least 2^-126, a normal number in 32 bits (with 0, an element whose
- * moments are both 0 is 0 / 0).  lr is *lr_at (a device float) where that is given.  Where *norm is not a finite
- * number nothing changes, *step neither.
+ * moments are both 0 is 0 / 0).  lr is *lr_at (a device float) where that is given.
+ * Where *norm is not a finite number nothing changes, *step neither.
  *
  * Moments: `held` elements of m and of v, those of a tensor from `at` on, 32-byte
  * aligned; what lies between a tensor's end and the next multiple of PP_STAGE_BLOCK
@@ -230,15 +230,15 @@ int pp_stage_grad_norm(const pp_stage_tensor *list, int64_t count, float *norm, 
  * element and one exponent for each PP_STAGE_BLOCK, e, as floats have it.  A byte's
  * low bits c (m: 7, its 8th is the sign; v: 8) are 0 for 0 and else stand for the
  * float whose bits are (c + 8 (e - w)) << 20, with w = 15 for m and 31 for v; e = 255:
- * a block with an infinity or a NaN, which stands for NaN.  Else e is the exponent of the block's largest magnitude rounded up to 4
- * significant bits; magnitudes are rounded to 4 significant bits; an m below the
- * window (2^-w of the block's largest binade) is held as 0, a v as the least that is
- * not 0.
+ * a block with an infinity or a NaN, which stands for NaN.  Else e is the exponent of
+ * the block's largest magnitude rounded up to 4 significant bits; magnitudes are
+ * rounded to 4 significant bits; an m below the window (2^-w of the block's largest
+ * binade) is held as 0, a v as the least that is not 0.
  *
  * random = 0: moments in 8 bits and bf16 parameters are rounded to nearest; 1: up
  * with the probability of what is cut off, by bits that depend on seed, t and the
  * element's place among the moments alone.  Copies are rounded to nearest.  Tensors
- * must not overlap. */
+ * must not overlap, gradients what is written neither. */
 size_t pp_stage_adamw_workspace(void);
 int pp_stage_adamw(const pp_stage_tensor *list, int64_t count, void *m, void *v, uint8_t *m_exp, uint8_t *v_exp,
                    int64_t held, int64_t *step, const float *lr_at, double lr, double beta1, double beta2, double eps,

@@ -5,12 +5,13 @@
 //   p = p (1 - lr decay) - lr / (1 - b1^t) * m / (sqrt(v / (1 - b2^t)) + eps)
 // Every element is read and written once, so memory bounds it: 30 bytes an
 // element with 32-bit parameters, moments and gradients and a 16-bit copy, 18 with
-// the moments in 8 bits.  571 million elements take 2.40 ms and 1.44 ms, both 105 %
-// of the measured copy rate (reads outweigh writes).  All in 16 bits with moments
+// the moments in 8 bits.  571 million elements take 2.42 ms and 1.45 ms, both 105 %
+// of the measured copy rate (reads outweigh writes), 16-bit parameters and
+// gradients with moments in 32 bits 1.77 ms, the same.  All in 16 bits with moments
 // in 8 it is 10 bytes an element, and its 70 instructions bound it, half of them
-// whole-number ones (issue slots 88 % busy): 1.31 ms rounded at random, 64 %; 90
-// million elements in 161 tensors 229 us at random and 191 to nearest (70 %).  The norm takes 324 us of
-// 32-bit gradients (104 %), 185 us of 16-bit ones (91 %).
+// whole-number ones (issue slots 85 % busy): 1.33 ms rounded at random, 63 %; 90
+// million elements in 161 tensors 229 us at random and 191 to nearest (70 %).  The
+// norm takes 324 us of 32-bit gradients (104 %), 185 us of 16-bit ones (91 %).
 //
 // Moments in 8 bits.  64 consecutive elements share an exponent, and an element
 // keeps 4 significant bits and its exponent relative to the block's: m a sign and
