@@ -85,6 +85,7 @@ struct Alternatives {
     uint32_t *least;  // [k + 1][T]: the classes' largest logits, as ordered(), and the bound; null where all tiles run at
                       // once (a call of 90 tokens on 3600 x 512 with 5 alternatives 28 us, 32 with it)
     bool sorted;      // pieces' alternatives are in order
+    bool narrow;      // every second piece is empty
 };
 
 // The bound is taken from the classes in a token's first pieces, and then in the pieces of every kEvery-th column
@@ -406,12 +407,23 @@ __global__ void __launch_bounds__(32 * kFewWarps, kFewBlocks)
 // Without alternatives a token is two sums: one 7.8 / 8.7 us, 3 10.4 / 10.7, 64
 // 14.8 / 11.1 (on 131072 x 64 3 tokens 18.2 / 19.5, 4 19.8 / 19.5, 16 32.4 / 20.6).
 constexpr int kOneToSM = 4, kOneAlone = 3;  // up to so many tokens a block each: to an SM with alternatives, in all without
-constexpr int kJoinThreads = 256, kKept = 256;  // kKept: alternatives that are sorted at a time
+constexpr int kJoinThreads = 256;
 
-// Of the n entries in shared memory the first k, in order, by THREADS threads (a warp, or the block).
-template <int THREADS>
+// The i-th of a lane's pieces: every 32nd, or both of every 32nd tile where a tile's second piece is empty (tiles of up
+// to 32 columns): half of the lanes would have nothing else, and no k largest logits to take a bound from (16 tokens on
+// 3000 x 64 with 20 alternatives 149 us by that, 22 like this; both of each tile always: 900 tokens 127 us, 43).
+__device__ __forceinline__ int piece_of_lane(bool narrow, int lane, int i) {
+    return narrow ? 64 * (i >> 1) + 2 * lane + (i & 1) : 32 * i + lane;
+}
+
+// Alternatives that a warp sorts at a time, and a block: all that pass the bound, but for many equals (with as many
+// alternatives as lanes some hundred do).
+constexpr int kKept = 256, kKeptOfBlock = 512;
+
+// Of the n entries in shared memory, MOST at most, the first k, in order, by THREADS threads (a warp, or the block).
+template <int THREADS, int MOST>
 __device__ __forceinline__ int sort_kept(Found *kept, int n, int k, int thread) {
-    constexpr int kEach = kKept / THREADS;
+    constexpr int kEach = MOST / THREADS;
     const auto sync = [] {
         if (THREADS == 32) __syncwarp();
         else __syncthreads();
@@ -457,15 +469,19 @@ __device__ __forceinline__ int collect(const Alternatives &alt, int64_t pieces, 
     for (int64_t p0 = 0; p0 < pieces; p0 += 32 * kAhead) {
         int counts[kAhead];
 #pragma unroll
-        for (int h = 0; h < kAhead; ++h) counts[h] = !skip && p0 + 32 * h + lane < pieces ? count_of(alt, t * pieces + p0 + 32 * h + lane) : 0;
+        for (int h = 0; h < kAhead; ++h) {
+            const int64_t p = p0 + piece_of_lane(alt.narrow, lane, h);
+            counts[h] = !skip && p < pieces ? count_of(alt, t * pieces + p) : 0;
+        }
         // slots are even in number, so that two are 16 aligned bytes
         uint4 ahead[kAhead];
 #pragma unroll
         for (int h = 0; h < kAhead; ++h)
-            if (counts[h] > 0) ahead[h] = *reinterpret_cast<const uint4 *>(found + (p0 + 32 * h + lane) * slots);
+            if (counts[h] > 0)
+                ahead[h] = *reinterpret_cast<const uint4 *>(found + (p0 + piece_of_lane(alt.narrow, lane, h)) * slots);
 #pragma unroll
         for (int h = 0; h < kAhead; ++h) {
-            const Found *from = found + (p0 + 32 * h + lane) * slots;
+            const Found *from = found + (p0 + piece_of_lane(alt.narrow, lane, h)) * slots;
             uint4 q = ahead[h];
             const int c = counts[h] > 0 && __uint_as_float(q.x) >= least ? counts[h] : 0;
             for (int e = 0; __any_sync(~0u, e < c); e += 2) {
@@ -478,22 +494,24 @@ __device__ __forceinline__ int collect(const Alternatives &alt, int64_t pieces, 
                     if (is) mine[n + __popc(in & ((1u << lane) - 1))] = f[i];
                     n += __popc(in);
                     if (n > kKept - 32) {
-                        n = sort_kept<32>(mine, n, k, lane);
+                        n = sort_kept<32, kKept>(mine, n, k, lane);
                         least = fmaxf(least, mine[k - 1].l);
                     }
                 }
             }
         }
     }
-    return sort_kept<32>(mine, n, k, lane);
+    return sort_kept<32, kKept>(mine, n, k, lane);
 }
 
 template <bool TOP, int ROWS>
-__global__ void __launch_bounds__(kJoinThreads) k_score_join(const JoinArgs a, const Alternatives alt) {
+__global__ void __launch_bounds__(kJoinThreads, TOP ? 3 : 4) k_score_join(const JoinArgs a, const Alternatives alt) {
     constexpr int kGroups = kJoinThreads / ROWS;  // threads of a token
     __shared__ Stats sh[ROWS][kGroups + 1];
-    __shared__ Found keep[TOP ? ROWS : 1][TOP ? kKept : 1];
+    constexpr int kMost = ROWS == 1 ? kKeptOfBlock : kKept;
+    __shared__ Found keep[TOP ? ROWS : 1][TOP ? kMost : 1];
     __shared__ int kept;
+    const bool narrow = TOP && alt.narrow;
     let_next_start();
     after_previous();
     constexpr int kCounts = TOP && ROWS == 1 ? 4 : 1;
@@ -510,12 +528,13 @@ __global__ void __launch_bounds__(kJoinThreads) k_score_join(const JoinArgs a, c
     const int64_t t = (int64_t)blockIdx.x * ROWS + col;
     Stats x{kNegInf, 0.f, 0.f};
     if (t < a.T) {
+        // of one token, a thread's pieces are those of every 256th place; of eight, a lane's
         constexpr int kAhead = ROWS == 1 ? 4 : 8;
-        for (int64_t i = run; i < a.pieces; i += kGroups * kAhead) {
+        for (int64_t i = 0; i < a.pieces; i += kGroups * kAhead) {
             Stats p[kAhead];
 #pragma unroll
             for (int j = 0; j < kAhead; ++j) {
-                const int64_t k = i + kGroups * j;
+                const int64_t k = i + (ROWS == 1 ? run + kGroups * j : piece_of_lane(narrow, run, j));
                 p[j] = k < a.pieces ? a.part[k * a.T + t] : Stats{kNegInf, 0.f, 0.f};
             }
             float top = x.m;
@@ -536,10 +555,10 @@ __global__ void __launch_bounds__(kJoinThreads) k_score_join(const JoinArgs a, c
     __syncthreads();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, row = ROWS == 1 ? 0 : warp;
     const int64_t u = (int64_t)blockIdx.x * ROWS + row;
-    // a token's warp adds its parts up: lane i has those of threads i, i + 32, ...
-    x = sh[row][lane];
+    // a token's warp adds its parts up
+    x = sh[row][ROWS == 1 ? piece_of_lane(narrow, lane, 0) : lane];
 #pragma unroll
-    for (int i = 32; i < kGroups; i += 32) x = add(x, sh[row][i + lane]);
+    for (int i = 1; i < kGroups / 32; ++i) x = add(x, sh[row][piece_of_lane(narrow, lane, i)]);
     float m = x.m;
     const float of_lane = m;
 #pragma unroll
@@ -583,7 +602,7 @@ __global__ void __launch_bounds__(kJoinThreads) k_score_join(const JoinArgs a, c
                     for (int i = 0; i < 2; ++i)
                         if (e + i < c && f[i].l >= least) {
                             const int to = atomicAdd(&kept, 1);
-                            if (to < kKept) mine[to] = f[i];
+                            if (to < kMost) mine[to] = f[i];
                         }
                     if (f[0].l < least && (e == 0 || alt.sorted)) break;
                 }
@@ -595,8 +614,8 @@ __global__ void __launch_bounds__(kJoinThreads) k_score_join(const JoinArgs a, c
             }
             __syncthreads();
             n = kept;
-            if (n <= kKept) {
-                n = sort_kept<kJoinThreads>(mine, n, k, threadIdx.x);
+            if (n <= kMost) {
+                n = sort_kept<kJoinThreads, kMost>(mine, n, k, threadIdx.x);
             } else if (warp == 0) {  // many equals
                 n = collect(alt, a.pieces, u, least, !(of_lane >= least), mine, lane);
             }
@@ -699,6 +718,7 @@ int score(const ScoreSpace &s, const uint16_t *x, int64_t sx, const uint16_t *w,
         } else {
             const ProductPlan plan = plan_product(n, V, H, false, false);
             alt.pieces = kPieces * plan.nt;
+            alt.narrow = plan.tile_n <= 32;
             if (plan.mt * plan.nt * plan.cg <= sm_count()) alt.least = nullptr;
             if (TOP && alt.least) rc = launch_after(k_no_bounds, ceil_div(n * (k + 1), 256), 256, 0, stream, 1, alt.least, n * (k + 1));
             if (rc == PP_OK)

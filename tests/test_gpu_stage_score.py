@@ -66,6 +66,17 @@ def test_a_batch_of_single_tokens(S, T, V, H, k):
     _check(S.score_forward(x, w, target, top=k), want, want)
 
 
+@pytest.mark.parametrize("T", [3, 16, 130, 700])
+@pytest.mark.parametrize("V", [47, 300, 511, 1000, 2433, 3000, 4865])
+@pytest.mark.parametrize("k", [16, 17, 20, 32])
+def test_tiles_of_few_columns(S, T, V, k):
+    """Tiles whose second pieces are empty, fewer pieces than alternatives, more alternatives than are sorted at a time:
+    the same by which lane looks at which piece."""
+    x, w, target = _grid_inputs(T, V, 64, T + V)
+    want = Q.score(x, w, target, k, exact=True)
+    _check(S.score_forward(x, w, target, top=k), want, want)
+
+
 @pytest.mark.parametrize("k", [0, 1, 6])
 def test_both_joins(S, k):
     """Around the numbers of tokens from which a block joins the pieces of eight: to the last bit the same alternatives,
